@@ -326,6 +326,161 @@ per_status per_nleaves(const per_buffer *h, uint64_t *out);
 per_status per_rank_order_noalloc(const float *d_raw, uint32_t n, uint32_t *d_order,
                                   uint32_t *d_status, void *stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * The learner's and the actor's operators beside the buffer: a loss per sampled row whose values
+ * are the next priorities (distillation from a teacher's top logits), the recurrence of a
+ * sequence model with its gradient, and the verification of drafted tokens by an actor.
+ * They need no handle and keep nothing between calls: the caller owns every array, no call
+ * allocates, and each enqueues one kernel on `stream`.  A failed call's message is
+ * per_last_op_error(), on the calling thread.  Strides count elements; the innermost axis of
+ * every array is contiguous.  Input strides may be any value (0 repeats a row for all); rows of an
+ * output must not overlap.  Pointers need the alignment of their element type only; rows whose
+ * start and stride are multiples of 16 bytes move in 16-byte pieces.  Where d_status is given, a
+ * call sets PER_DEVFLAG_* bits in it (it never clears them).
+ * ------------------------------------------------------------------------------------------- */
+
+/* per_last_op_error -- a description of the last failure of an operator on this thread ("" if none).
+ * The string stays valid until the next failure on the thread. */
+const char *per_last_op_error(void);
+
+/* Element types of the operators' arrays.  Sums, normalisers, states and losses are float. */
+enum { PER_TYPE_F32 = 0, PER_TYPE_F16 = 1, PER_TYPE_BF16 = 2 };
+
+enum { PER_DISTILL_IDX64 = 1u };   /* per_distill_shape.flags: d_idx is int64, else int32 */
+
+typedef struct {
+    uint64_t rows;         /* N, 0 .. 2^31 - 1 (0 is a no-op) */
+    uint32_t vocab;        /* V, 1 .. 2^18 */
+    uint32_t top;          /* K, entries a teacher row has, 1 .. 1024 */
+    uint32_t type;         /* PER_TYPE_* of the logits and of their gradient */
+    uint32_t top_type;     /* PER_TYPE_* of the teacher's logits */
+    int64_t stride_logits, stride_top, stride_idx, stride_grad;   /* between rows */
+    float temperature;     /* tau, > 0 */
+    uint32_t flags;        /* PER_DISTILL_* */
+} per_distill_shape;
+
+/*
+ * per_distill_forward -- the loss of each row of student logits x against a teacher's top K
+ * logits t at the places idx.  With lse_n = tau log sum_j exp(x_nj / tau) (over all V),
+ * p_nj = exp((x_nj - lse_n) / tau) and q_nk = exp((t_nk - L_n) / tau):
+ *     loss_n = tau^2 sum_k q_nk (log q_nk - log p_n,idx_nk).
+ * L_n is the same soft maximum of the row's own teacher entries (their q sum to 1) or, where
+ * d_teacher_lse is given, d_teacher_lse[n]: the teacher's over its whole vocabulary (q then sums to
+ * the share that the top K hold).  An entry with idx < 0 is left out, whatever its t; one with
+ * idx >= V is left out and sets PER_DEVFLAG_BAD_INDEX.  Entries that name one place several times
+ * each count.  A row with no entry of q > 0, or whose logits are all -inf, has nothing to learn from:
+ * its loss and its gradient are 0.  A q > 0 where x is -inf gives a loss of +inf; NaN in x
+ * or in a kept t gives NaN in its row.  The loss is not weighted: it is the row's next TD error
+ * (per_update_priorities).
+ *   d_logits [N x V], d_top [N x K], d_idx [N x K], d_teacher_lse [N] float or NULL,
+ *   d_loss [N] float, d_lse [N] float (NULL to skip).
+ * per_distill_backward -- its gradient from the saved d_lse, for row factors s (d_scale [N] float;
+ * NULL: 1), an importance weight over the batch's size or what an outer gradient brings:
+ *     grad_nj = s_n tau (S_n p_nj - sum over k with idx_nk = j of q_nk),  S_n = sum_k q_nk.
+ * per_distill_step -- loss, lse and gradient in one pass over the logits (read once, gradient
+ * written once; a row stays in the shared memory of up to 8 CTAs).
+ * d_grad may be d_logits itself (same stride): the gradient then takes the logits' place.
+ * The gradient is rounded once to its type.  Results do not depend on the launch's order.
+ */
+per_status per_distill_forward(const per_distill_shape *shape, const void *d_logits, const void *d_top,
+                               const void *d_idx, const float *d_teacher_lse, float *d_loss,
+                               float *d_lse, uint32_t *d_status, void *stream);
+per_status per_distill_backward(const per_distill_shape *shape, const void *d_logits, const void *d_top,
+                                const void *d_idx, const float *d_teacher_lse, const float *d_lse,
+                                const float *d_scale, void *d_grad, uint32_t *d_status, void *stream);
+per_status per_distill_step(const per_distill_shape *shape, const void *d_logits, const void *d_top,
+                            const void *d_idx, const float *d_teacher_lse, const float *d_scale,
+                            float *d_loss, float *d_lse, void *d_grad, uint32_t *d_status,
+                            void *stream);
+
+enum { PER_VERIFY_TOKENS64 = 1u };   /* per_verify_shape.flags: d_tokens is int64, else int32 */
+
+typedef struct {
+    uint32_t batch;        /* B, 0 .. 2^20 (0 is a no-op) */
+    uint32_t drafts;       /* D, drafted tokens a sequence has at most, 0 .. 1024 */
+    uint32_t vocab;        /* V, 1 .. 2^18 */
+    uint32_t type;         /* PER_TYPE_* of the probabilities */
+    int64_t stride_p[2], stride_q[2];      /* between sequences, between positions */
+    int64_t stride_tokens, stride_u;       /* between sequences */
+    uint32_t flags;        /* PER_VERIFY_* */
+    uint32_t reserved;     /* 0 */
+} per_verify_shape;
+
+/*
+ * per_verify_draft -- verify drafted tokens against the target's probabilities so that what is
+ * emitted follows the target's distribution.  Sequence b drafted m = d_lens[b] tokens (clamped to
+ * 0 .. D; D where d_lens is NULL).  Token i is accepted when every one before it was and
+ *     u_i q_i(token_i) < p_i(token_i)      (the product rounded to binary32),
+ * with p_i row i of d_p, q_i row i of d_q, or q = 1 where d_q is NULL (a draft that was certain of its
+ * token).  With n the number accepted, one more token is drawn: after a refusal (n < m) from the
+ * masses max(p_n(j) - q_n(j), 0) (binary32; with d_q NULL p_n without token_n), else from p_m.  The draw is exact
+ * in integers, so it does not depend on any order of summation: a mass counts floor(2^40 mass)
+ * units (NaN and negative 0, above 1 as 1), M is their sum, and with U = floor(2^31 u) (u =
+ * d_sample_u[b], held to 0 <= U < 2^31; NaN: 0) the token is the first j whose inclusive sum exceeds
+ * floor(U M / 2^31).  M = 0 draws from p_n instead; if that holds nothing either, the token is -1.
+ * D = 0 draws one token from each row of p.  A drafted token outside [0, V) has p = q = 0: it is
+ * refused, and if the verification reaches it PER_DEVFLAG_BAD_INDEX is set.
+ *   d_p [B x (D + 1) x V], d_q [B x D x V] or NULL, d_tokens [B x D], d_lens [B] int32 or NULL,
+ *   d_accept_u [B x D] float, d_sample_u [B] float, d_accepted [B] int32 (n),
+ *   d_out [B x (D + 1)] int32 (contiguous): the accepted tokens, the drawn one, then -1,
+ *   d_accept_p [B x D] float (contiguous) or NULL: min(1, p_i / q_i) of every drafted token (1 where
+ *   q_i <= p_i), 0 past m and for a token outside [0, V): what a buffer of drafts can take as its
+ *   rows' priorities.
+ */
+per_status per_verify_draft(const per_verify_shape *shape, const void *d_p, const void *d_q,
+                            const void *d_tokens, const int32_t *d_lens, const float *d_accept_u,
+                            const float *d_sample_u, int32_t *d_accepted, int32_t *d_out,
+                            float *d_accept_p, uint32_t *d_status, void *stream);
+
+/* per_scan_shape.flags */
+enum {
+    PER_SCAN_SIGMOID = 1u,   /* a is a gate before its sigmoid; without it a is the decay itself */
+    PER_SCAN_REVERSE = 2u    /* time runs from the last step to the first */
+};
+
+typedef struct {
+    uint64_t steps;        /* T, 0 .. 2^31 - 1 */
+    uint32_t batch;        /* B */
+    uint32_t channels;     /* C; B C < 2^31 */
+    uint32_t type;         /* PER_TYPE_* of a, x, h and their gradients */
+    uint32_t flags;        /* PER_SCAN_* */
+    int64_t stride_a[2], stride_x[2], stride_h[2];       /* between sequences, between steps */
+    int64_t stride_gh[2], stride_ga[2], stride_gx[2];    /* the gradients' (per_scan_backward) */
+    int64_t stride_resets[2];
+} per_scan_shape;
+
+/*
+ * per_scan_forward -- the gated linear recurrence over T steps, channel by channel:
+ *     h_t = a_t h_{t-1} + x_t                        (decays given), or
+ *     h_t = f_t h_{t-1} + (1 - f_t) x_t, f = 1 / (1 + exp(-a))      (PER_SCAN_SIGMOID).
+ * h_{-1} is d_h0 (NULL: 0).  A step with d_resets[b, t] != 0 starts an episode: the state that comes into it counts
+ * as 0, whatever it holds.  A weight of exactly 0 likewise drops what it multiplies, infinities and NaN
+ * too (a gate of -inf drops the state, of +inf the input: padding can hold anything).  The
+ * state is kept in binary32; h is rounded to its type where it is stored.  Long sequences are
+ * split over time where the channels alone do not fill the GPU; the joints multiply the decays of
+ * a stretch, whose product must stay finite in binary32 (decays of magnitude at most 1 always
+ * do).  PER_SCAN_REVERSE runs t = T-1 .. 0 (discounted returns: a = gamma, x = reward, a reset at each
+ * episode's last step).
+ *   d_a, d_x [B x T x C], d_h0 [B x C] float or NULL, d_resets [B x T] uint8 or NULL,
+ *   d_h [B x T x C], d_last [B x C] float (NULL to skip): the state after the last step; it may be
+ *   d_h0 itself.  T = 1 is the step of a model that is being served.  T = 0 copies h0 to last.
+ * per_scan_backward -- its gradients for d_gh (of h) and d_glast (of last; NULL: 0), reading the h that the
+ * forward call stored.  With w_t the weight of h_{t-1} (0 at a reset) and g_t = gh_t + w_{t+1} g_{t+1}:
+ *     ga_t = g_t h_{t-1}, gx_t = g_t                                       (decays given), or
+ *     ga_t = g_t (h_{t-1} - x_t) f_t (1 - f_t), gx_t = g_t (1 - f_t)       (PER_SCAN_SIGMOID),
+ *     gh0 = w_0 g_0.       (h_{t-1} counts as 0 at a reset.)
+ *   d_x may be NULL where decays are given.  d_ga, d_gx [B x T x C] and d_gh0 [B x C] float, each may be
+ *   NULL to skip.
+ * Outputs must not overlap inputs except where said.
+ */
+per_status per_scan_forward(const per_scan_shape *shape, const void *d_a, const void *d_x,
+                            const float *d_h0, const uint8_t *d_resets, void *d_h, float *d_last,
+                            void *stream);
+per_status per_scan_backward(const per_scan_shape *shape, const void *d_a, const void *d_x,
+                             const void *d_h, const float *d_h0, const uint8_t *d_resets,
+                             const void *d_gh, const float *d_glast, void *d_ga, void *d_gx,
+                             float *d_gh0, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

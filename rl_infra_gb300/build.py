@@ -14,7 +14,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libgbper.so")
-SOURCES = ["per_api.cu", "k_tree.cu", "k_sample.cu", "k_rank.cu", "k_flat.cu"]
+SOURCES = ["per_api.cu", "k_tree.cu", "k_sample.cu", "k_rank.cu", "k_flat.cu",
+           "ops_api.cu", "k_distill.cu", "k_verify.cu", "k_scan.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

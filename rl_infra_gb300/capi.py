@@ -51,7 +51,15 @@ _STATE_DTYPE = {
 # every symbol include/gbper.h declares
 EXPORTS = ("per_create", "per_destroy", "per_add", "per_sample", "per_update_priorities",
            "per_total", "per_min", "per_size", "per_status_device", "per_last_error",
-           "per_read_state", "per_nleaves", "per_rank_order_noalloc", "per_rank_refresh")
+           "per_read_state", "per_nleaves", "per_rank_order_noalloc", "per_rank_refresh",
+           "per_distill_forward", "per_distill_backward", "per_distill_step", "per_verify_draft",
+           "per_scan_forward", "per_scan_backward", "per_last_op_error")
+
+# element types, flags and shapes of the learner's and the actor's operators
+PER_TYPE_F32, PER_TYPE_F16, PER_TYPE_BF16 = 0, 1, 2
+PER_DISTILL_IDX64 = 1
+PER_VERIFY_TOKENS64 = 1
+PER_SCAN_SIGMOID, PER_SCAN_REVERSE = 1, 2
 
 
 class per_config(ctypes.Structure):
@@ -59,6 +67,27 @@ class per_config(ctypes.Structure):
                 ("row_stride_out", ctypes.c_uint32), ("seed", ctypes.c_uint64),
                 ("flags", ctypes.c_uint32), ("rebuild_batch", ctypes.c_uint32),
                 ("element_batch", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+class per_distill_shape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_uint64), ("vocab", ctypes.c_uint32), ("top", ctypes.c_uint32),
+                ("type", ctypes.c_uint32), ("top_type", ctypes.c_uint32),
+                ("stride_logits", ctypes.c_int64), ("stride_top", ctypes.c_int64),
+                ("stride_idx", ctypes.c_int64), ("stride_grad", ctypes.c_int64),
+                ("temperature", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+class per_verify_shape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_uint32), ("drafts", ctypes.c_uint32), ("vocab", ctypes.c_uint32),
+                ("type", ctypes.c_uint32), ("stride_p", ctypes.c_int64 * 2),
+                ("stride_q", ctypes.c_int64 * 2), ("stride_tokens", ctypes.c_int64),
+                ("stride_u", ctypes.c_int64), ("flags", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+class per_scan_shape(ctypes.Structure):
+    _fields_ = [("steps", ctypes.c_uint64), ("batch", ctypes.c_uint32), ("channels", ctypes.c_uint32),
+                ("type", ctypes.c_uint32), ("flags", ctypes.c_uint32)] + [
+        ("stride_" + n, ctypes.c_int64 * 2) for n in ("a", "x", "h", "gh", "ga", "gx", "resets")]
 
 
 class PerError(RuntimeError):
@@ -117,6 +146,21 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         L.per_rank_refresh.argtypes = [vp, vp]
         L.per_rank_refresh.restype = st
         L.per_rank_order_noalloc.restype = st
+        # the shapes are passed as the structures' bytes or as a pointer to one (see ops.py)
+        L.per_distill_forward.argtypes = [vp] * 9
+        L.per_distill_forward.restype = st
+        L.per_distill_backward.argtypes = [vp] * 10
+        L.per_distill_backward.restype = st
+        L.per_distill_step.argtypes = [vp] * 11
+        L.per_distill_step.restype = st
+        L.per_verify_draft.argtypes = [vp] * 12
+        L.per_verify_draft.restype = st
+        L.per_scan_forward.argtypes = [vp] * 8
+        L.per_scan_forward.restype = st
+        L.per_scan_backward.argtypes = [vp] * 12
+        L.per_scan_backward.restype = st
+        L.per_last_op_error.argtypes = []
+        L.per_last_op_error.restype = ctypes.c_char_p
         _lib = L
         return L
 
@@ -198,6 +242,42 @@ def per_rank_order_noalloc(d_raw, n, d_order, d_status, stream):
     """Slot order by raw priority, descending, without any device allocation (n <= 2^18);
     d_status (a device uint32, or None) receives the device's PER_DEVFLAG_* bits."""
     return load().per_rank_order_noalloc(d_raw, n, d_order, d_status, stream)
+
+
+def per_last_op_error():
+    return load().per_last_op_error().decode()
+
+
+def per_distill_forward(shape, d_logits, d_top, d_idx, d_teacher_lse, d_loss, d_lse, d_status, stream):
+    return load().per_distill_forward(shape, d_logits, d_top, d_idx, d_teacher_lse, d_loss, d_lse,
+                                      d_status, stream)
+
+
+def per_distill_backward(shape, d_logits, d_top, d_idx, d_teacher_lse, d_lse, d_scale, d_grad, d_status,
+                         stream):
+    return load().per_distill_backward(shape, d_logits, d_top, d_idx, d_teacher_lse, d_lse, d_scale,
+                                       d_grad, d_status, stream)
+
+
+def per_distill_step(shape, d_logits, d_top, d_idx, d_teacher_lse, d_scale, d_loss, d_lse, d_grad,
+                     d_status, stream):
+    return load().per_distill_step(shape, d_logits, d_top, d_idx, d_teacher_lse, d_scale, d_loss,
+                                   d_lse, d_grad, d_status, stream)
+
+
+def per_verify_draft(shape, d_p, d_q, d_tokens, d_lens, d_accept_u, d_sample_u, d_accepted, d_out,
+                     d_accept_p, d_status, stream):
+    return load().per_verify_draft(shape, d_p, d_q, d_tokens, d_lens, d_accept_u, d_sample_u,
+                                   d_accepted, d_out, d_accept_p, d_status, stream)
+
+
+def per_scan_forward(shape, d_a, d_x, d_h0, d_resets, d_h, d_last, stream):
+    return load().per_scan_forward(shape, d_a, d_x, d_h0, d_resets, d_h, d_last, stream)
+
+
+def per_scan_backward(shape, d_a, d_x, d_h, d_h0, d_resets, d_gh, d_glast, d_ga, d_gx, d_gh0, stream):
+    return load().per_scan_backward(shape, d_a, d_x, d_h, d_h0, d_resets, d_gh, d_glast, d_ga, d_gx,
+                                    d_gh0, stream)
 
 
 # -- torch-facing convenience ---------------------------------------------------------------
