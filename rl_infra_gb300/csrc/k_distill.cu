@@ -1,170 +1,409 @@
 // k_distill.cu -- the loss of a student's logits against a teacher's top logits, and its gradient.
-// One CTA takes one row: the teacher's entries are normalised in shared memory, the row's soft
-// maximum is one pass with a running maximum and sum, the gradient a second pass.
+//
+// Mathematics.  With c = log2(e) / tau, a row's soft maximum is lse = m + tau ln s, m = max x, s =
+// sum 2^((x - m) c); (m, s) of two stretches join by rescaling each s to the larger m, so one pass
+// over a row suffices, split over threads, warps and CTAs, joined in a fixed order.  The differences
+// are taken before they are scaled: x - m is exact where it matters and logits of the type's lowest
+// value do not overflow.  -inf contributes 0; NaN and +inf make s NaN.
+//   loss = tau sum_k q_k ((t_k - L) - (x_k - lse)),  grad_j = s_n tau (S p_j - q_j).
+// Sums and normalisers are binary32; the gradient is rounded once.
+//
+// Work.  A row is split over a cluster of 1 to 8 CTAs.  Each CTA's loader warps read their part of the
+// row once, keep the running (m, s) and, where the gradient is wanted in the same pass, put the raw
+// part into shared memory; the CTAs exchange (m, s) through distributed shared memory (one hardware
+// barrier), then turn their part of shared memory into the gradient.  Every access to memory is 16 bytes
+// on a 16-byte boundary but for a row's ends: a row that starts elsewhere (an odd vocabulary) is
+// shifted into place between neighbouring lanes, so a row is summed in the same order, and gives the same
+// bits, wherever it lies.  So the step reads the logits once and writes the gradient once, which
+// is its bound (HBM).  One more warp of each CTA handles the teacher's entries meanwhile; their q is
+// taken off the gradient by a second write to those places after the CTA's barrier.
 #include "ops_internal.cuh"
+
+#include <algorithm>
+#include <mutex>
 
 namespace gbper {
 
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kMaxTop = 1024;
+constexpr int kMaxCluster = 8;
+#ifndef DW
+#define DW 8
+#endif
+#ifndef DM
+#define DM 3
+#endif
+#ifndef DP
+#define DP 64
+#endif
+constexpr int kMaxWarps = DW;    // loader warps of a CTA at most
+constexpr int kUnroll = 4;       // 16-byte loads a loader thread has in flight
 constexpr float kInf = __builtin_huge_valf();
 
-// (m, s) of two stretches: the maximum and the sum of 2^((x - maximum) c)
-__device__ __forceinline__ void join(float &m, float &s, float m2, float s2, float c)
+struct RowSum {
+    float m, s;
+};
+
+__device__ __forceinline__ float finite_or_zero(float m) { return m == -kInf ? 0.0f : m; }
+
+__device__ __forceinline__ RowSum join(RowSum a, RowSum b, float c)
 {
-    const float mm = fmaxf(m, m2);
-    if (mm == -kInf) return;   // both empty (NaN never raises a maximum: it stays in the sum)
-    s = (m == -kInf ? s : s * exp2f((m - mm) * c)) + (m2 == -kInf ? s2 : s2 * exp2f((m2 - mm) * c));
-    m = mm;
+    RowSum r;
+    r.m = fmaxf(a.m, b.m);
+    const float e = finite_or_zero(r.m);
+    r.s = a.s * ex2((a.m - e) * c) + b.s * ex2((b.m - e) * c);
+    return r;
 }
 
-__device__ __forceinline__ float block_sum(float v, float *red)
-{
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = red[0];
-    for (int w = 1; w < kThreads / 32; ++w) v += red[w];
-    return v;
-}
+// P consecutive elements of a row from element j on (j + P is the next lane's j; the whole warp calls), of
+// which those in [lo, hi) may be read; the others give -inf.  p + j need not be on a 16-byte
+// boundary: the blocks on boundaries are read, and joined with the next lane's.
+template <typename T, typename Load>
+struct Pieces {
+    static constexpr int P = Pack<T>::N;
+    const T *p;
+    long long lo, hi;
+    Load load;
+    unsigned off;   // bytes from the boundary at or before p + j
+    uint4 a[kUnroll], b[kUnroll];
 
-__device__ __forceinline__ float block_max(float v, float *red)
-{
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = red[0];
-    for (int w = 1; w < kThreads / 32; ++w) v = fmaxf(v, red[w]);
-    return v;
-}
+    __device__ __forceinline__ Pieces(const T *p_, long long lo_, long long hi_, long long j, Load load_)
+        : p(p_), lo(lo_), hi(hi_), load(load_), off((unsigned)(reinterpret_cast<uintptr_t>(p_ + j) & 15u))
+    {
+    }
+    __device__ __forceinline__ bool whole(long long j) const { return j >= lo && j + P <= hi; }
+    __device__ __forceinline__ void request(int i, long long j)
+    {
+        const long long first = j - off / (unsigned)sizeof(T);
+        a[i] = b[i] = make_uint4(0, 0, 0, 0);
+        if (whole(first)) a[i] = load(p + first);
+        if (off && (threadIdx.x & 31) == 31 && whole(first + P)) b[i] = load(p + first + P);
+    }
+    __device__ __forceinline__ Pack<T> get(int i, long long j)
+    {
+        Pack<T> r;
+        r.raw = a[i];
+        const long long first = j - off / (unsigned)sizeof(T);
+        if (off) {
+            const uint4 n = make_uint4(__shfl_down_sync(0xffffffffu, a[i].x, 1), __shfl_down_sync(0xffffffffu, a[i].y, 1),
+                                       __shfl_down_sync(0xffffffffu, a[i].z, 1), __shfl_down_sync(0xffffffffu, a[i].w, 1));
+            r.raw = shift_bytes(a[i], (threadIdx.x & 31) == 31 ? b[i] : n, off);
+        }
+        if (!(whole(first) && (!off || whole(first + P)))) {
+            float f[P];
+#pragma unroll
+            for (int e = 0; e < P; ++e) f[e] = j + e >= lo && j + e < hi ? to_f32(p[j + e]) : -kInf;
+            r.pack(f);   // exact: the values came from T
+        }
+        return r;
+    }
+};
+
+struct FromGlobal {
+    __device__ __forceinline__ uint4 operator()(const void *p) const { return load_stream(p); }
+};
+struct FromShared {
+    __device__ __forceinline__ uint4 operator()(const void *p) const { return *static_cast<const uint4 *>(p); }
+};
+
+// Shared memory of a CTA: the part of the row (step only), then the teacher's entries.
+struct Shared {
+    RowSum cluster[kMaxCluster];
+    RowSum warp[kMaxWarps];
+    float S, L;
+    int some, repeated;
+};
+
+__device__ __forceinline__ unsigned hash_place(int at, unsigned mask) { return ((unsigned)at * 2654435761u >> 12) & mask; }
 
 template <typename T, int PART>
-__global__ void __launch_bounds__(kThreads) k_distill(DistillArgs a)
+__global__ void __launch_bounds__((kMaxWarps + 1) * 32, DM) k_distill(DistillArgs a, unsigned csize, unsigned per_cta,
+                                                                  unsigned hash_size)
 {
-    __shared__ float q[kMaxTop], d[kMaxTop], xk[kMaxTop];
-    __shared__ int at[kMaxTop];
-    __shared__ float red[2 * (kThreads / 32)];
-    const long long row = blockIdx.x;
-    const T *x = static_cast<const T *>(a.x) + row * a.sx;
-    const int t = threadIdx.x, K = a.k;
+    constexpr int P = Pack<T>::N;
+    extern __shared__ __align__(16) unsigned char dyn[];
+    __shared__ Shared sh;
+    uint4 *part = reinterpret_cast<uint4 *>(dyn);                       // [per_cta] (step)
+    float *q = reinterpret_cast<float *>(dyn + (PART == kDistillStep ? (size_t)per_cta * 16 : 0));   // [K]
+    float *d = q + a.k;                                                 // [K] t - L
+    float *xk = d + a.k;                                                // [K] the student's logits there
+    int *at = reinterpret_cast<int *>(xk + a.k);                        // [K] place, -1: left out
+    int *table = at + a.k;                                              // [hash_size]
+    const int K = (int)a.k;
+    const unsigned rank = blockIdx.x % csize;   // also the CTA's rank in its cluster, where there is one
+    const long long row = blockIdx.x / csize;
     const float c = kLog2e / a.tau;
-    // the teacher's row: q, log q as a difference, the student's logits at its places
-    float tm = -kInf;
-    for (int k = t; k < K; k += kThreads) {
-        long long i = load_index(a.idx, row * a.si + k, a.idx64);
-        if (i >= (long long)a.vocab) {
-            if (a.status) atomicOr(a.status, PER_DEVFLAG_BAD_INDEX);
-            i = -1;
-        }
-        if (i < 0) i = -1;
-        at[k] = (int)i;
-        d[k] = i < 0 ? -kInf : load_typed(a.top, row * a.st + k, a.top_type);
-        xk[k] = i < 0 ? 0.0f : to_f32(x[i]);
-        tm = fmaxf(tm, d[k]);
-    }
-    tm = block_max(tm, red);
-    float L;
-    if (a.teacher_lse) {
-        L = a.teacher_lse[row];
-    } else {
-        float s = 0.0f;
-        for (int k = t; k < K; k += kThreads)
-            if (at[k] >= 0 && tm != -kInf) s += exp2f((d[k] - tm) * c);
-            else if (at[k] >= 0) s += d[k] == d[k] ? 0.0f : d[k];
-        s = block_sum(s, red);
-        L = tm + a.tau * logf(s);
-        if (tm == -kInf) L = s == s ? 0.0f : s;
-    }
-    float S = 0.0f;
-    for (int k = t; k < K; k += kThreads) {
-        d[k] -= L;
-        q[k] = at[k] >= 0 ? exp2f(d[k] * c) : 0.0f;
-        S += q[k];
-    }
-    S = block_sum(S, red);
-    const bool some = !(S == 0.0f);
-    float m = -kInf, s = 0.0f;
-    float lse;
-    if (PART != kDistillBackward) {
-        for (unsigned j = t; j < a.vocab; j += kThreads) {
-            const float v = to_f32(x[j]);
-            if (v > m) {
-                s *= exp2f((m - v) * c);
-                m = v;
+    const int loaders = (int)blockDim.x - 32, t = (int)threadIdx.x, lane = t & 31;
+    pdl_wait();
+    pdl_release();
+    if (csize > 1 && PART != kDistillBackward) cluster_arrive_relaxed();   // this CTA has started
+
+    const T *x = static_cast<const T *>(a.x) + row * a.sx;
+    // the row in pieces of P elements; this CTA takes pieces [v0, v1), which are elements [j0, j1)
+    const unsigned pieces = (a.vocab + P - 1) / P;
+    const unsigned v0 = min(rank * per_cta, pieces), v1 = min(v0 + per_cta, pieces);
+    const int j0 = (int)(v0 * P), j1 = (int)min(v1 * P, a.vocab);
+
+    RowSum own{-kInf, 0.0f};
+    if (t >= loaders) {
+        // ---- the teacher's entries -----------------------------------------------------------
+        if (PART != kDistillForward)
+            for (unsigned i = lane; i < hash_size; i += 32) table[i] = -1;
+        float tm = -kInf;
+        for (int k = lane; k < K; k += 32) {
+            long long i = load_index(a.idx, row * a.si + k, a.idx64);
+            float v = load_typed(a.top, row * a.st + k, a.top_type);
+            if (i >= (long long)a.vocab) {
+                if (a.status && rank == 0) atomicOr(a.status, PER_DEVFLAG_BAD_INDEX);
+                i = -1;
             }
-            if (m != -kInf) s += exp2f((v - m) * c);
-            else if (!(v == v)) s = v;
+            if (i < 0) {
+                i = -1;
+                v = -kInf;
+            }
+            at[k] = (int)i;
+            d[k] = v;
+            // the loss needs every entry's logit (first CTA), the gradient those of its own part
+            const bool mine = i >= j0 && i < j1;
+            xk[k] = i >= 0 && (PART == kDistillBackward ? mine : PART == kDistillStep ? rank == 0 || mine : rank == 0)
+                        ? to_f32(x[i]) : 0.0f;
+            tm = fmaxf(tm, v);
+        }
+        for (int o = 16; o; o >>= 1) tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, o));
+        float L;
+        if (a.teacher_lse) {
+            L = a.teacher_lse[row];
+        } else {
+            const float e = finite_or_zero(tm);
+            float s = 0.0f;
+            for (int k = lane; k < K; k += 32) s += ex2((d[k] - e) * c);
+            for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            L = s == 0.0f ? 0.0f : e + a.tau * logf(s);
+        }
+        float S = 0.0f;
+        for (int k = lane; k < K; k += 32) {
+            const float v = d[k] - L, w = at[k] >= 0 ? ex2(v * c) : 0.0f;
+            d[k] = v;
+            q[k] = w;
+            S += w;
+        }
+        for (int o = 16; o; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
+        int repeated = 0;
+        if (PART != kDistillForward) {
+            // does a place stand twice among the entries?  open addressing, at most half full
+            __syncwarp();
+            for (int k = lane; k < K; k += 32) {
+                const int p = at[k];
+                if (p < 0) continue;
+                for (unsigned h = hash_place(p, hash_size - 1);; h = (h + 1) & (hash_size - 1)) {
+                    const int was = atomicCAS(&table[h], -1, p);
+                    if (was == p) repeated = 1;
+                    if (was == -1 || was == p) break;
+                }
+            }
+            repeated = __any_sync(0xffffffffu, repeated);
+        }
+        if (lane == 0) {
+            sh.S = S;
+            sh.some = !(S == 0.0f);
+            sh.repeated = repeated;
+        }
+    } else if (PART != kDistillBackward) {
+        // ---- this CTA's part of the row --------------------------------------------------------
+        // (the last piece of the part may need the block behind it)
+        Pieces<T, FromGlobal> in(x, 0, min((int)a.vocab, j1 + P), 0, FromGlobal());
+        for (unsigned v = v0 + (t & ~31); v < v1; v += loaders * kUnroll) {
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i) in.request(i, (long long)(v + i * loaders + lane) * P);
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i) {
+                const unsigned w = v + i * loaders + lane;
+                const Pack<T> piece = in.get(i, (long long)w * P);
+                if (w >= v1) continue;
+                if (PART == kDistillStep) part[w - v0] = piece.raw;
+                float f[P], m = own.m;
+                piece.unpack(f);
+#pragma unroll
+                for (int e = 0; e < P; ++e) m = fmaxf(m, f[e]);
+                const float ref = finite_or_zero(m);
+                float s = own.s * ex2((own.m - ref) * c);
+#pragma unroll
+                for (int e = 0; e < P; ++e) s += ex2((f[e] - ref) * c);
+                own.m = m;
+                own.s = s;
+            }
         }
         for (int o = 16; o; o >>= 1) {
-            const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-            join(m, s, m2, s2, c);
+            RowSum other{__shfl_xor_sync(0xffffffffu, own.m, o), __shfl_xor_sync(0xffffffffu, own.s, o)};
+            // the lower lane's stretch first, so that both lanes get the same bits
+            own = (lane & o) ? join(other, own, c) : join(own, other, c);
         }
-        __syncthreads();
-        if ((t & 31) == 0) {
-            red[2 * (t >> 5)] = m;
-            red[2 * (t >> 5) + 1] = s;
+        if (lane == 0) sh.warp[t >> 5] = own;
+    }
+    __syncthreads();
+    float lse;
+    RowSum all{-kInf, 0.0f};
+    if (PART != kDistillBackward) {
+        for (int w = 0; w < loaders / 32; ++w) all = join(all, sh.warp[w], c);
+        if (csize > 1) {
+            cluster_wait_acquire();   // every CTA of the row has started
+            if (t < (int)csize) {
+                const unsigned to = cluster_smem_addr(&sh.cluster[rank], t);
+                st_cluster_f32(to, all.m);
+                st_cluster_f32(to + 4, all.s);
+            }
+            cluster_sync_all();
+            all = sh.cluster[0];
+            for (unsigned r = 1; r < csize; ++r) all = join(all, sh.cluster[r], c);
         }
-        __syncthreads();
-        m = red[0];
-        s = red[1];
-        for (int w = 1; w < kThreads / 32; ++w) join(m, s, red[2 * w], red[2 * w + 1], c);
-        lse = m == -kInf ? (s == s ? -kInf : s) : m + a.tau * logf(s);
-        float loss = 0.0f;
-        for (int k = t; k < K; k += kThreads)
-            if (q[k] != 0.0f) loss += q[k] * (d[k] - (xk[k] - lse));
-        loss = a.tau * block_sum(loss, red);
-        if (t == 0) {
-            a.loss[row] = some && lse != -kInf ? loss : 0.0f;
-            if (a.lse) a.lse[row] = lse;
+        lse = all.s == 0.0f ? -kInf : finite_or_zero(all.m) + a.tau * logf(all.s);
+        if (rank == 0 && t >= loaders) {
+            float loss = 0.0f;
+            for (int k = lane; k < K; k += 32)
+                if (q[k] != 0.0f) loss += q[k] * (d[k] - (xk[k] - lse));
+            for (int o = 16; o; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
+            if (lane == 0) {
+                a.loss[row] = sh.some && lse != -kInf ? a.tau * loss : 0.0f;
+                if (a.lse) a.lse[row] = lse;
+            }
         }
     } else {
         lse = a.lse[row];
     }
     if (PART == kDistillForward) return;
+
+    // ---- the gradient of this CTA's part --------------------------------------------------------
+    const bool live = sh.some && lse != -kInf;
     const float g = (a.scale ? a.scale[row] : 1.0f) * a.tau;
-    const bool live = some && lse != -kInf;
+    // from lse in the step too: it gives the same bits as the forward and the backward call
+    const float f0 = live ? g * sh.S : 0.0f;
     T *out = static_cast<T *>(a.grad) + row * a.sg;
-    __syncthreads();
-    for (unsigned j = t; j < a.vocab; j += kThreads) {
-        const float p = exp2f((to_f32(x[j]) - lse) * c);
-        out[j] = from_f32<T>(live ? g * (S * p) : 0.0f);
-    }
-    __syncthreads();
-    if (!live) return;
-    for (int k = t; k < K; k += kThreads) {
-        if (at[k] < 0) continue;
-        bool first = true;
-        float sum = 0.0f;
-        for (int i = 0; i < K; ++i)
-            if (at[i] == at[k]) {
-                if (i < k) first = false;
-                sum += q[i];
+    // pieces of the output's own 16-byte boundaries; those that another CTA or row shares are written
+    // element by element
+    const int misg = (int)(reinterpret_cast<uintptr_t>(out) % 16 / sizeof(T));
+    if (t < loaders && j0 < j1) {
+        const int o0 = (j0 + misg) / P, o1 = (j1 - 1 + misg) / P + 1;
+        auto write = [&](auto &in) {
+            for (int v = o0 + (t & ~31); v < o1; v += loaders * kUnroll) {
+#pragma unroll
+                for (int i = 0; i < kUnroll; ++i) in.request(i, (long long)(v + i * loaders + lane) * P - misg);
+#pragma unroll
+                for (int i = 0; i < kUnroll; ++i) {
+                    const long long j = (long long)(v + i * loaders + lane) * P - misg;
+                    Pack<T> piece = in.get(i, j);
+                    if (j >= j1) continue;
+                    float f[P];
+                    piece.unpack(f);
+#pragma unroll
+                    for (int e = 0; e < P; ++e) f[e] = live ? f0 * ex2((f[e] - lse) * c) : 0.0f;
+                    if (j >= j0 && j + P <= j1) {
+                        piece.pack(f);
+                        *reinterpret_cast<uint4 *>(out + j) = piece.raw;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < P; ++e)
+                            if (j + e >= j0 && j + e < j1) out[j + e] = from_f32<T>(f[e]);
+                    }
+                }
             }
-        if (first) out[at[k]] = from_f32<T>(g * (S * exp2f((xk[k] - lse) * c) - sum));
+        };
+        if (PART == kDistillStep) {
+            Pieces<T, FromShared> in(reinterpret_cast<const T *>(part) - j0, j0, j1, (long long)o0 * P - misg, FromShared());
+            write(in);
+        } else {
+            // in place, another CTA may be writing its part: nothing outside [j0, j1) is read
+            Pieces<T, FromGlobal> in(x, j0, j1, (long long)o0 * P - misg, FromGlobal());
+            write(in);
+        }
+    }
+    if (!live) return;
+    __syncthreads();   // the places of the entries below are written
+    for (int k = t; k < K; k += (int)blockDim.x) {
+        const int p = at[k];
+        if (p < j0 || p >= j1) continue;   // left out, or another CTA's
+        float sum = q[k];
+        if (sh.repeated) {   // entries that name one place: the first of them takes all, in their order
+            bool first = true;
+            sum = 0.0f;
+            for (int i = 0; i < K; ++i)
+                if (at[i] == p) {
+                    first = first && i >= k;
+                    sum += q[i];
+                }
+            if (!first) continue;
+        }
+        out[p] = from_f32<T>(f0 * ex2((xk[k] - lse) * c) - g * sum);
     }
 }
 
+// The largest dynamic shared memory a launch may ask for, set once per device.
+constexpr size_t kMaxPart = 160 * 1024;
+constexpr size_t kMaxDyn = kMaxPart + kMaxTop * 16 + 2 * kMaxTop * 4;
+
 template <typename T>
-cudaError_t launch_t(DistillPart part, const DistillArgs &a, cudaStream_t st)
+cudaError_t attributes()
 {
-    const unsigned grid = (unsigned)a.rows;
-    if (part == kDistillForward) k_distill<T, kDistillForward><<<grid, kThreads, 0, st>>>(a);
-    else if (part == kDistillBackward) k_distill<T, kDistillBackward><<<grid, kThreads, 0, st>>>(a);
-    else k_distill<T, kDistillStep><<<grid, kThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    cudaError_t e = cudaFuncSetAttribute(k_distill<T, kDistillForward>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxDyn);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k_distill<T, kDistillBackward>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxDyn);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k_distill<T, kDistillStep>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxDyn);
+    return e;
+}
+
+cudaError_t init_once(int device)
+{
+    static std::mutex mu;
+    static bool done[64] = {};
+    std::lock_guard<std::mutex> lock(mu);
+    if (done[device]) return cudaSuccess;
+    cudaError_t e = attributes<float>();
+    if (e == cudaSuccess) e = attributes<__half>();
+    if (e == cudaSuccess) e = attributes<__nv_bfloat16>();
+    if (e == cudaSuccess) done[device] = true;
+    return e;
+}
+
+template <typename T>
+cudaError_t launch_t(DistillPart part, const DistillArgs &a, const DeviceInfo &dev, cudaStream_t st)
+{
+    constexpr unsigned P = 16 / sizeof(T);
+    const unsigned pieces = (a.vocab + P - 1) / P;
+    // CTAs for a row: enough that its part takes at most 64 KB of shared memory (three CTAs an SM, so
+    // that one writes while others read), and that few rows still fill the SMs
+    unsigned csize = 1;
+    while (csize < kMaxCluster && (pieces + csize - 1) / csize * 16 > DP * 1024) csize *= 2;
+    while (csize < kMaxCluster && a.rows * csize < 2ull * dev.sms && pieces / csize > 512) csize *= 2;
+    const unsigned per_cta = (pieces + csize - 1) / csize;
+    if (a.rows * csize > 0x7fffffffull) return cudaErrorInvalidConfiguration;
+    unsigned warps = 1;
+    while (warps < (unsigned)kMaxWarps && warps * 32 * kUnroll < per_cta) warps *= 2;
+    unsigned hash_size = 0;
+    if (part != kDistillForward) {
+        hash_size = 32;
+        while (hash_size < 2 * a.k) hash_size *= 2;
+    }
+    const size_t smem = (part == kDistillStep ? (size_t)per_cta * 16 : 0) + (size_t)a.k * 16 + (size_t)hash_size * 4;
+    const unsigned grid = (unsigned)(a.rows * csize), block = (warps + 1) * 32;
+    if (part == kDistillForward)
+        return launch_clusters(k_distill<T, kDistillForward>, grid, block, csize, smem, st, a, csize, per_cta, hash_size);
+    if (part == kDistillBackward)
+        return launch_clusters(k_distill<T, kDistillBackward>, grid, block, 1, smem, st, a, csize, per_cta, hash_size);
+    return launch_clusters(k_distill<T, kDistillStep>, grid, block, csize, smem, st, a, csize, per_cta, hash_size);
 }
 
 }  // namespace
 
 cudaError_t launch_distill(int type, DistillPart part, const DistillArgs &a, cudaStream_t st)
 {
-    if (type == PER_TYPE_F32) return launch_t<float>(part, a, st);
-    if (type == PER_TYPE_F16) return launch_t<__half>(part, a, st);
-    return launch_t<__nv_bfloat16>(part, a, st);
+    DeviceInfo dev;
+    cudaError_t e = device_info(&dev);
+    if (e == cudaSuccess) e = init_once(dev.device);
+    if (e != cudaSuccess) return e;
+    if (type == PER_TYPE_F32) return launch_t<float>(part, a, dev, st);
+    if (type == PER_TYPE_F16) return launch_t<__half>(part, a, dev, st);
+    return launch_t<__nv_bfloat16>(part, a, dev, st);
 }
 
 }  // namespace gbper

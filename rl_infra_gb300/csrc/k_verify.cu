@@ -1,14 +1,30 @@
-// k_verify.cu -- verification of drafted tokens.  One CTA takes one sequence: the accept tests, the
-// total of the masses of the row it stops at (integers, so the order of summation does not
-// matter), and the first place whose inclusive sum passes the mark.
+// k_verify.cu -- verification of drafted tokens against the target's probabilities.
+//
+// Mathematics.  Token i passes when u_i q_i < p_i; the first that does not (or the end of the draft)
+// fixes the row n, whose masses max(p - q, 0) (or p) are drawn from by their inclusive sum.  A mass
+// counts in whole units of 2^-40: the sum of up to 2^18 of them fits in 64 bits and is the same in any
+// order, so the draw can be split over CTAs and warps and still be one number, exactly.  The mark
+// floor(U M / 2^31) with U < 2^31 is below M, and is taken in two 64-bit products.
+//
+// Work.  Two rows of V are all that has to be read (HBM bounds large batches; a chain of dependent loads
+// bounds small ones: token, its probabilities, the rows, the place).  A sequence takes a cluster of
+// 1 to 8 CTAs; each runs the accept tests for itself (a handful of loads, instead of a barrier), sums its
+// part of the row, 16 bytes a load, and exchanges the sum through distributed shared memory (one
+// hardware barrier).  The one warp whose stretch holds the mark reads its stretch again, from
+// cache, and walks it with warp prefix sums.
 #include "ops_internal.cuh"
+
+#include <algorithm>
 
 namespace gbper {
 
 namespace {
 
-constexpr int kThreads = 256;
 typedef unsigned long long u64;
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxCluster = 8;
+constexpr int kUnroll = 4;   // 16-byte loads of each row that a lane has in flight
 
 // a mass in units of 2^-40: NaN and negative 0, above 1 as 1
 __device__ __forceinline__ u64 units(float r)
@@ -16,106 +32,233 @@ __device__ __forceinline__ u64 units(float r)
     return r > 0.0f ? (u64)(fminf(r, 1.0f) * 1099511627776.0f) : 0ull;
 }
 
-template <typename T>
-__device__ __forceinline__ u64 mass(const T *p, const T *q, long long without, unsigned j)
+// 16 bytes at any address that is a multiple of 2: two aligned loads, shifted together.  The caller makes
+// sure that both lie inside the row.
+__device__ __forceinline__ uint4 load_across(const unsigned char *p)
 {
-    const float v = to_f32(p[j]);
-    if (q) return units(v - to_f32(q[j]));
-    return (long long)j == without ? 0ull : units(v);
+    const unsigned off = (unsigned)(reinterpret_cast<uintptr_t>(p) & 15u);
+    const uint4 *a = reinterpret_cast<const uint4 *>(p - off);
+    const uint4 lo = __ldg(a);
+    if (off == 0) return lo;
+    const uint4 hi = __ldg(a + 1);
+    return shift_bytes(lo, hi, off);
 }
 
-__device__ __forceinline__ u64 block_total(u64 v, u64 *red)
+// The row that is drawn from, in 16-byte pieces of p from the boundary at or before its start.
+template <typename T>
+struct Row {
+    static constexpr int P = Pack<T>::N;
+    const T *p, *q;         // q null: nothing is taken off
+    long long without;      // a place that counts 0, or -1
+    unsigned vocab, mis;
+
+    // the values of p and q (0 without a q) of one piece; places outside the row give 0
+    __device__ __forceinline__ void load(unsigned w, Pack<T> &a, Pack<T> &b) const
+    {
+        const long long j = (long long)w * P - mis;
+        const bool inside = j >= 0 && j + P <= (long long)vocab;
+        // the pieces around q's stretch must lie inside q's row too
+        const bool margin = j >= P && j + 2 * P <= (long long)vocab;
+        b.raw = make_uint4(0, 0, 0, 0);
+        if (inside && (!q || margin)) {
+            a.raw = __ldg(reinterpret_cast<const uint4 *>(p + j));
+            if (q) b.raw = load_across(reinterpret_cast<const unsigned char *>(q + j));
+        } else {
+            float f[P], g[P];
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+                const bool in = j + e >= 0 && j + e < (long long)vocab;
+                f[e] = in ? to_f32(p[j + e]) : 0.0f;
+                g[e] = in && q ? to_f32(q[j + e]) : 0.0f;
+            }
+            a.pack(f);   // exact: the values came from T
+            b.pack(g);
+        }
+    }
+
+    __device__ __forceinline__ u64 mass(unsigned w, int e, float f, float g) const
+    {
+        return (long long)w * P - mis + e == without ? 0ull : units(q ? f - g : f);
+    }
+
+    // the sum over one piece
+    __device__ __forceinline__ u64 sum(unsigned w, const Pack<T> &a, const Pack<T> &b) const
+    {
+        float f[P], g[P];
+        a.unpack(f);
+        b.unpack(g);
+        u64 s = 0;
+#pragma unroll
+        for (int e = 0; e < P; ++e) s += mass(w, e, f[e], g[e]);
+        return s;
+    }
+};
+
+__device__ __forceinline__ u64 warp_sum(u64 v)
 {
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0;
-    for (int w = 0; w < kThreads / 32; ++w) v += red[w];
     return v;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_verify(VerifyArgs a)
+__global__ void __launch_bounds__(kThreads) k_verify(VerifyArgs a, unsigned csize, unsigned per_cta)
 {
-    __shared__ u64 red[kThreads / 32], sums[kThreads];
-    __shared__ int s_n, s_token;
-    const long long b = blockIdx.x;
-    const int t = threadIdx.x, D = a.drafts;
+    constexpr int P = Pack<T>::N;
+    __shared__ u64 warp_total[kWarps], cluster_total[2][kMaxCluster];
+    __shared__ int s_n;
+    const unsigned rank = blockIdx.x % csize;
+    const long long b = blockIdx.x / csize;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, D = (int)a.drafts;
+    if (t == 0) s_n = D;
+    pdl_wait();
+    pdl_release();
+    if (csize > 1) cluster_arrive_relaxed();   // this CTA has started
     const T *p = static_cast<const T *>(a.p) + b * a.sp[0];
     const T *q = a.q ? static_cast<const T *>(a.q) + b * a.sq[0] : nullptr;
-    int m = a.lens ? a.lens[b] : D;
-    m = max(0, min(m, D));
-    if (t == 0) {
-        s_n = m;
-        s_token = -1;
-    }
+    const int m = a.lens ? max(0, min(a.lens[b], D)) : D;
+    const float us = a.us[b];
     __syncthreads();
     for (int i = t; i < D; i += kThreads) {
         const long long tok = load_index(a.tokens, b * a.stok + i, a.tok64);
+        const float u = a.u[b * a.su + i];
         const bool in = tok >= 0 && tok < (long long)a.vocab;
         const float pt = in ? to_f32(p[i * a.sp[1] + tok]) : 0.0f;
         const float qt = !in ? 0.0f : q ? to_f32(q[i * a.sq[1] + tok]) : 1.0f;
-        if (a.accept_p) a.accept_p[b * D + i] = i >= m || !in ? 0.0f : pt < qt ? pt / qt : 1.0f;
-        if (i < m && !(in && __fmul_rn(a.u[b * a.su + i], qt) < pt)) atomicMin(&s_n, i);
+        if (a.accept_p && rank == 0) a.accept_p[b * D + i] = i >= m || !in ? 0.0f : pt < qt ? pt / qt : 1.0f;
+        if (i < m && !(in && __fmul_rn(u, qt) < pt)) atomicMin(&s_n, i);
     }
     __syncthreads();
-    const int n = s_n;
-    const T *pr = p + n * a.sp[1];
-    const T *qr = nullptr;
-    long long without = -1;
+    const int n = min(s_n, m);
+
+    Row<T> row;
+    row.p = p + n * a.sp[1];
+    row.q = nullptr;
+    row.without = -1;
+    row.vocab = a.vocab;
+    row.mis = (unsigned)(reinterpret_cast<uintptr_t>(row.p) % 16 / sizeof(T));
     if (n < m) {
         const long long tok = load_index(a.tokens, b * a.stok + n, a.tok64);
         if (tok < 0 || tok >= (long long)a.vocab) {
-            if (t == 0 && a.status) atomicOr(a.status, PER_DEVFLAG_BAD_INDEX);
-        } else {
-            without = tok;
+            if (t == 0 && rank == 0 && a.status) atomicOr(a.status, PER_DEVFLAG_BAD_INDEX);
+        } else if (!q) {
+            row.without = tok;
         }
-        if (q) qr = q + n * a.sq[1];
+        if (q) row.q = q + n * a.sq[1];
     }
-    const unsigned per = (a.vocab + kThreads - 1) / kThreads;
-    const unsigned j0 = min(a.vocab, t * per), j1 = min(a.vocab, j0 + per);
-    for (int pass = 0; pass < 2; ++pass) {
+    if (rank == 0) {
+        if (t == 0) a.accepted[b] = n;
+        for (int i = t; i <= D; i += kThreads)
+            if (i != n) a.out[b * (D + 1) + i] = i < n ? (int)load_index(a.tokens, b * a.stok + i, a.tok64) : -1;
+    }
+
+    const unsigned pieces = (row.mis + a.vocab + P - 1) / P;
+    const unsigned v1 = min(pieces, (rank + 1) * per_cta);
+    const unsigned per_warp = (per_cta + kWarps - 1) / kWarps;
+    const unsigned w0 = min(rank * per_cta + warp * per_warp, v1), w1 = min(w0 + per_warp, v1);
+    for (int attempt = 0; attempt < 2; ++attempt) {
         u64 own = 0;
-        for (unsigned j = j0; j < j1; ++j) own += mass(pr, qr, without, j);
-        const u64 total = block_total(own, red);
-        if (total == 0) {   // the target's own row
-            qr = nullptr;
-            without = -1;
-            continue;
+        for (unsigned w = w0 + lane; w < w1; w += 32 * kUnroll) {
+            Pack<T> x[kUnroll], y[kUnroll];
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i)
+                if (w + 32 * i < w1) row.load(w + 32 * i, x[i], y[i]);
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i)
+                if (w + 32 * i < w1) own += row.sum(w + 32 * i, x[i], y[i]);
         }
-        float u = a.us[b];
-        const u64 U = u > 0.0f ? min((u64)(fminf(u, 1.0f) * 2147483648.0f), 0x7fffffffull) : 0ull;
-        const u64 mark = U * (total >> 31) + ((U * (total & 0x7fffffffull)) >> 31);
-        sums[t] = own;
+        own = warp_sum(own);
+        if (lane == 0) warp_total[warp] = own;
         __syncthreads();
-        u64 before = 0;
-        for (int i = 0; i < t; ++i) before += sums[i];
-        if (before <= mark && mark < before + own) {
-            for (unsigned j = j0; j < j1; ++j) {
-                before += mass(pr, qr, without, j);
-                if (before > mark) {
-                    s_token = (int)j;
-                    break;
-                }
+        u64 mine = 0, before = 0;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            const u64 v = warp_total[i];
+            mine += v;
+            before += i < warp ? v : 0;
+        }
+        u64 total = mine;
+        if (csize > 1) {
+            if (attempt == 0) cluster_wait_acquire();   // every CTA of the sequence has started
+            if (t < (int)csize) {
+                const unsigned to = cluster_smem_addr(&cluster_total[attempt][rank], t);
+                st_cluster_u32(to, (unsigned)mine);
+                st_cluster_u32(to + 4, (unsigned)(mine >> 32));
+            }
+            cluster_sync_all();
+            total = 0;
+            for (unsigned r = 0; r < csize; ++r) {
+                const u64 v = cluster_total[attempt][r];
+                total += v;
+                before += r < rank ? v : 0;
             }
         }
-        __syncthreads();
-        break;
+        if (total == 0) {
+            if (attempt == 0 && (row.q || row.without >= 0)) {   // the target's own row
+                row.q = nullptr;
+                row.without = -1;
+                __syncthreads();   // warp_total is read
+                continue;
+            }
+            if (rank == 0 && t == 0) a.out[b * (D + 1) + n] = -1;
+            return;
+        }
+        const u64 U = us > 0.0f ? min((u64)(fminf(us, 1.0f) * 2147483648.0f), 0x7fffffffull) : 0ull;
+        const u64 mark = U * (total >> 31) + ((U * (total & 0x7fffffffull)) >> 31);
+        if (mark < before || mark >= before + own) return;   // another warp's stretch
+        for (unsigned w = w0; w < w1; w += 32 * kUnroll) {
+            Pack<T> x[kUnroll], y[kUnroll];
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i)
+                if (w + 32 * i + lane < w1) row.load(w + 32 * i + lane, x[i], y[i]);
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i) {
+                const unsigned at = w + 32 * i + lane;
+                const u64 s = at < w1 ? row.sum(at, x[i], y[i]) : 0;
+                u64 incl = s;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const u64 v = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += v;
+                }
+                if (mark < before + incl && mark >= before + incl - s) {
+                    float f[P], g[P];
+                    x[i].unpack(f);
+                    y[i].unpack(g);
+                    u64 c = before + incl - s;
+                    int e = 0;
+#pragma unroll
+                    for (int k = 0; k < P; ++k) {
+                        c += row.mass(at, k, f[k], g[k]);
+                        if (c <= mark) e = k + 1;
+                    }
+                    a.out[b * (D + 1) + n] = (int)((long long)at * P - row.mis + e);
+                }
+                before += __shfl_sync(0xffffffffu, incl, 31);
+            }
+            if (mark < before) return;
+        }
+        return;
     }
-    if (t == 0) a.accepted[b] = n;
-    for (int i = t; i <= D; i += kThreads)
-        a.out[b * (D + 1) + i] = i < n ? (int)load_index(a.tokens, b * a.stok + i, a.tok64) : i == n ? s_token : -1;
+}
+
+template <typename T>
+cudaError_t launch_t(const VerifyArgs &a, cudaStream_t st)
+{
+    constexpr unsigned P = 16 / sizeof(T);
+    const unsigned pieces = (a.vocab + P - 1) / P + 1;   // a row that starts off a boundary has one more
+    // CTAs for a sequence: at least 512 pieces each (16 a lane of one warp); more, smaller CTAs also even out
+    // the load over the SMs where there are many sequences
+    unsigned csize = 1;
+    while (csize < kMaxCluster && pieces / csize > 1024) csize *= 2;
+    return launch_clusters(k_verify<T>, a.batch * csize, kThreads, csize, 0, st, a, csize, (pieces + csize - 1) / csize);
 }
 
 }  // namespace
 
 cudaError_t launch_verify(int type, const VerifyArgs &a, cudaStream_t st)
 {
-    if (type == PER_TYPE_F32) k_verify<float><<<a.batch, kThreads, 0, st>>>(a);
-    else if (type == PER_TYPE_F16) k_verify<__half><<<a.batch, kThreads, 0, st>>>(a);
-    else k_verify<__nv_bfloat16><<<a.batch, kThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    if (type == PER_TYPE_F32) return launch_t<float>(a, st);
+    if (type == PER_TYPE_F16) return launch_t<__half>(a, st);
+    return launch_t<__nv_bfloat16>(a, st);
 }
 
 }  // namespace gbper

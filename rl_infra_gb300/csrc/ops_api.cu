@@ -2,6 +2,7 @@
 // Nothing is kept between calls.
 #include "ops_internal.cuh"
 
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 
@@ -125,6 +126,25 @@ void set_axis(P **p, const void *src, const int64_t stride[2], long long dst[2],
 }
 
 }  // namespace
+
+namespace gbper {
+
+cudaError_t device_info(DeviceInfo *out)
+{
+    static std::atomic<int> sms[64];   // zero: not asked yet
+    cudaError_t e = cudaGetDevice(&out->device);
+    if (e != cudaSuccess) return e;
+    if (out->device < 0 || out->device >= 64) return cudaErrorInvalidDevice;
+    out->sms = sms[out->device].load(std::memory_order_relaxed);
+    if (out->sms == 0) {
+        e = cudaDeviceGetAttribute(&out->sms, cudaDevAttrMultiProcessorCount, out->device);
+        if (e != cudaSuccess) return e;
+        sms[out->device].store(out->sms, std::memory_order_relaxed);
+    }
+    return cudaSuccess;
+}
+
+}  // namespace gbper
 
 extern "C" {
 

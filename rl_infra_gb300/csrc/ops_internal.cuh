@@ -78,6 +78,136 @@ __device__ __forceinline__ long long load_index(const void *p, long long i, int 
     return wide ? static_cast<const long long *>(p)[i] : (long long)static_cast<const int *>(p)[i];
 }
 
+// 2^x by the special-function unit (2 ulp; a result below 2^-126 is 0)
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 16 bytes of T in registers
+template <typename T>
+struct Pack {
+    static constexpr int N = 16 / (int)sizeof(T);
+    uint4 raw;
+    __device__ __forceinline__ void unpack(float *f) const;
+    __device__ __forceinline__ void pack(const float *f);
+};
+
+template <>
+__device__ __forceinline__ void Pack<float>::unpack(float *f) const
+{
+    f[0] = __uint_as_float(raw.x);
+    f[1] = __uint_as_float(raw.y);
+    f[2] = __uint_as_float(raw.z);
+    f[3] = __uint_as_float(raw.w);
+}
+template <>
+__device__ __forceinline__ void Pack<float>::pack(const float *f)
+{
+    raw = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+template <>
+__device__ __forceinline__ void Pack<__nv_bfloat16>::unpack(float *f) const
+{
+    const unsigned w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {   // a bfloat16 is the upper half of a binary32
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+template <>
+__device__ __forceinline__ void Pack<__nv_bfloat16>::pack(const float *f)
+{
+    unsigned w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const unsigned *>(&h);
+    }
+    raw = make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <>
+__device__ __forceinline__ void Pack<__half>::unpack(float *f) const
+{
+    const unsigned w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+        f[2 * i] = v.x;
+        f[2 * i + 1] = v.y;
+    }
+}
+template <>
+__device__ __forceinline__ void Pack<__half>::pack(const float *f)
+{
+    unsigned w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const unsigned *>(&h);
+    }
+    raw = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 16 bytes that nobody reads again soon
+__device__ __forceinline__ uint4 load_stream(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+// The 16 bytes that begin `off` bytes (a multiple of 2 below 16, the same for the whole warp) into the 32
+// bytes of lo and hi.
+__device__ __forceinline__ uint4 shift_bytes(uint4 lo, uint4 hi, unsigned off)
+{
+    unsigned w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    if (off & 8u) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (off & 4u) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    const unsigned bits = (off & 3u) * 8;
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                      __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+
+// A launch whose grid is made of clusters of `cluster` CTAs (1: none) and which may begin while the kernel
+// before it in the stream finishes (pdl_wait).
+template <typename... KArgs, typename... Args>
+cudaError_t launch_clusters(void (*kernel)(KArgs...), unsigned grid, unsigned block, unsigned cluster, size_t smem,
+                            cudaStream_t st, Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+// SMs of the current device, and whether a launch on it must first set its kernels' attributes.
+struct DeviceInfo {
+    int device, sms;
+};
+cudaError_t device_info(DeviceInfo *out);   // ops_api.cu
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
