@@ -5,31 +5,83 @@
 // a long sequence can be cut: every stretch is run once from 0 for its (A, H), the joints are
 // scanned, and each stretch is run again from the state that really comes in, which needs no
 // stored prefixes and rounds like the plain recurrence.  The gradient is the same recurrence in
-// the other direction: with c_t = w_t g_t, g_t = gh_t + c_{t+1}, so c_t = w_t c_{t+1} + w_t gh_t.
+// the other direction: with c_t = w_t g_t, g_t = gh_t + c_{t+1}, so c_t = w_t (gh_t + c_{t+1}).
 // A weight of exactly 0 (a reset, a closed gate) drops what comes in whatever it holds, so it is a
 // select, not a product; a product of weights that merely underflows is held at the smallest number,
 // so that an infinite state is not dropped by it.  All of it is binary32.
 //
 // Work.  HBM bounds every case of some size (forward: two arrays read, one written; gradient: four or
-// three read, two written).  A CTA takes a tile of CT channels and a stretch of steps; a thread takes VEC
-// neighbouring channels (16 bytes) and R consecutive steps, so the rows of a tile are read in whole
-// 128-byte lines; the threads' (A, H) are scanned by shuffles in a warp and by one thread a channel over the
-// warps.  Where the channels alone do not fill the SMs, a cluster of up to 16 CTAs takes the same
-// channels over consecutive stretches and exchanges the stretches' (A, H) through distributed shared
-// memory, one hardware barrier a round.  The next rounds' rows arrive meanwhile: each thread
-// copies what it will itself read (cp.async), so the copies need no barrier.
+// three read, two written).  A warp takes a strip of 16 channels and works through time by itself, in
+// tiles of 64 steps, without a barrier: its lanes copy the tile's rows 16 bytes a copy (cp.async) some
+// tiles ahead into a ring in shared memory, and read it the other way round: a lane takes two neighbouring
+// channels and 16 consecutive steps, so only the (A, H) of four groups of lanes are left to be scanned by
+// shuffles (with 16 bytes of channels a lane and 4 steps the scan took three times the
+// recurrence's instructions).  Up to four warps side by side make a CTA.  Where the channels alone do not
+// fill the SMs, a cluster of up to 16 CTAs takes the same channels over consecutive tiles: each warp
+// sends its tile's (A, H) to its partners in the other CTAs by asynchronous stores into their shared
+// memory, which count down a barrier there (no fence, so output stores in flight are not waited
+// for), and only then finishes the tile before: the exchange runs beside the next tile's first pass.
 #include "ops_internal.cuh"
 
 #include <algorithm>
+#include <cstring>
 #include <mutex>
+#include <type_traits>
 
 namespace gbper {
 
 namespace {
 
 constexpr int kMaxCluster = 16;
-constexpr int kMaxWarps = 8;
+constexpr int kWarps = 4;     // of a CTA at most, side by side over the channels
+constexpr int kStrip = 16;    // channels of a warp
+constexpr int kGroups = 4;    // groups of 8 lanes, one after the other in time
+constexpr float kInf = __builtin_huge_valf();
 constexpr unsigned kFull = 0xffffffffu;
+
+// ---- pairs of binary32, two to an instruction -------------------------------------------------
+struct F2 {
+    float x, y;
+};
+__device__ __forceinline__ unsigned long long bits2(F2 v)
+{
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+    return r;
+}
+__device__ __forceinline__ F2 from_bits2(unsigned long long b)
+{
+    F2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(b));
+    return v;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b)
+{
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return from_bits2(r);
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b)
+{
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return from_bits2(r);
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+    return from_bits2(r);
+}
+__device__ __forceinline__ float &at(F2 &v, int i) { return i ? v.y : v.x; }
+__device__ __forceinline__ float at(const F2 &v, int i) { return i ? v.y : v.x; }
+
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 struct Gate {
     float w, v;   // the state's weight f and the input's 1 - f
@@ -40,29 +92,677 @@ template <bool SIG>
 __device__ __forceinline__ Gate gate(float a)
 {
     if (!SIG) return {a, 1.0f};
-    const float e = ex2(a * -kLog2e);
-    float f;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(1.0f + e));
+    const float e = ex2(a * -kLog2e), f = rcp(1.0f + e);
     return {f, f == 0.0f ? 1.0f : e * f};
+}
+
+// the same of two gates that are not 0
+__device__ __forceinline__ void gates(F2 a, F2 &w, F2 &v)
+{
+    const F2 x = a * F2{-kLog2e, -kLog2e};
+    const F2 e{ex2(x.x), ex2(x.y)};
+    const F2 d = e + F2{1.0f, 1.0f};
+    w = {rcp(d.x), rcp(d.y)};
+    v = e * w;
 }
 
 // w h + more, a weight of 0 dropping whatever h holds
 __device__ __forceinline__ float weigh(float w, float h, float more) { return w == 0.0f ? more : fmaf(w, h, more); }
 
-// the product of two weights, 0 only if one of them is
-__device__ __forceinline__ float chain(float a, float b)
-{
-    const float p = a * b;
-    return p == 0.0f && a != 0.0f && b != 0.0f ? 1.4e-45f : p;
-}
-
+// A stretch of steps.  A is NaN where the stretch drops what comes in (a weight of exactly 0 in it), and is
+// never 0: a product that underflows is held at the smallest number, so that an infinite state times it
+// stays infinite.  (A weight of NaN makes H NaN too.)
 struct Stretch {
     float A, H;
 };
 
+__device__ __forceinline__ float nonzero(float a) { return a == 0.0f ? 1.4e-45f : a; }
+
+__device__ __forceinline__ float apply(Stretch s, float h)
+{
+    const float r = fmaf(s.A, h, s.H);
+    return s.A == s.A ? r : s.H;
+}
+
 __device__ __forceinline__ Stretch join(Stretch first, Stretch then)
 {
-    return {chain(first.A, then.A), weigh(then.A, first.H, then.H)};
+    return {nonzero(first.A * then.A), apply(then, first.H)};
+}
+
+__device__ __forceinline__ Stretch shfl_up(Stretch s, int o)
+{
+    return {__shfl_up_sync(kFull, s.A, o), __shfl_up_sync(kFull, s.H, o)};
+}
+__device__ __forceinline__ Stretch shfl(Stretch s, int lane)
+{
+    return {__shfl_sync(kFull, s.A, lane), __shfl_sync(kFull, s.H, lane)};
+}
+
+// ---- the ring ------------------------------------------------------------------------------
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *smem, const void *global)
+{
+    const unsigned s = (unsigned)__cvta_generic_to_shared(smem);
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(global) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(s), "l"(global) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+template <typename T>
+__device__ __forceinline__ F2 unpack2(const T *p);
+template <> __device__ __forceinline__ F2 unpack2<float>(const float *p)
+{
+    const float2 v = *reinterpret_cast<const float2 *>(p);
+    return {v.x, v.y};
+}
+template <> __device__ __forceinline__ F2 unpack2<__nv_bfloat16>(const __nv_bfloat16 *p)
+{
+    const unsigned w = *reinterpret_cast<const unsigned *>(p);
+    return {__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)};
+}
+template <> __device__ __forceinline__ F2 unpack2<__half>(const __half *p)
+{
+    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(p));
+    return {v.x, v.y};
+}
+
+// stores two channels where `wide` says that both exist and lie on a boundary of the pair
+template <typename T>
+__device__ __forceinline__ void store2(T *p, F2 v, bool wide, bool second)
+{
+    if (wide) {
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<float2 *>(p) = make_float2(v.x, v.y);
+        } else if constexpr (std::is_same<T, __half>::value) {
+            *reinterpret_cast<__half2 *>(p) = __floats2half2_rn(v.x, v.y);
+        } else {
+            *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v.x, v.y);
+        }
+    } else {
+        p[0] = from_f32<T>(v.x);
+        if (second) p[1] = from_f32<T>(v.y);
+    }
+}
+
+// A warp's tiles of NA arrays in shared memory, ST of them.  A group's 16 rows lie together, with a pad
+// between groups that puts the four groups of a read into different banks.
+template <typename T, int N, int NA, int ST, bool WIDE>
+struct Ring {
+    static constexpr int ROW = kStrip * (int)sizeof(T);
+    static constexpr int GROUP = N * ROW + ROW;
+    static constexpr int SLOT = kGroups * GROUP;
+    static constexpr int BYTES = ST * NA * SLOT;       // of a warp
+    unsigned char *mem;
+
+    __device__ __forceinline__ unsigned char *slot(int tile, int array) const { return mem + (tile % ST * NA + array) * SLOT; }
+
+    // requests rows [t0, t0 + (kGroups * N)) of an array, of which those below `steps` exist; p: the strip's first
+    // channel, of which `channels` exist
+    __device__ __forceinline__ void request(int tile, int array, const T *p, long long stride, long long t0, long long steps, int channels) const
+    {
+        const int lane = threadIdx.x & 31;
+        unsigned char *to = slot(tile, array);
+        constexpr int PIECE = WIDE ? 16 : (int)sizeof(T), PER = ROW / PIECE, ROWS = 32 / PER;
+        const int c = lane % PER * (PIECE / (int)sizeof(T)), r0 = lane / PER;
+        if (c >= channels) return;
+        const long long left = steps - t0 - r0;
+        const T *from = p + c + (t0 + r0) * stride;
+#pragma unroll
+        for (int i = 0; i < (kGroups * N) / ROWS; ++i) {
+            const int r = i * ROWS;   // + r0
+            if (r < left) {
+                unsigned char *at = to + (r + r0) / N * GROUP + (r + r0) % N * ROW + lane % PER * PIECE;
+                if constexpr (PIECE >= 4) copy_async<PIECE>(at, from);
+                else *reinterpret_cast<T *>(at) = *from;   // too small for an asynchronous copy
+            }
+            from += (long long)ROWS * stride;
+        }
+    }
+    // this lane's two channels of its step i
+    __device__ __forceinline__ F2 read(int tile, int array, int i) const
+    {
+        const int lane = threadIdx.x & 31;
+        return unpack2<T>(reinterpret_cast<const T *>(slot(tile, array) + lane / 8 * GROUP + i * ROW) + lane % 8 * 2);
+    }
+};
+
+// ---- the partners of a cluster ------------------------------------------------------------
+
+__device__ __forceinline__ unsigned smem_u32(const void *p) { return (unsigned)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void mbar_init(unsigned bar)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(unsigned bar, unsigned bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// Waits for the phase of the given parity to end; false when it has not after a bounded number of tries.
+__device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned parity)
+{
+    for (int tries = 0; tries < 1 << 22; ++tries) {
+        unsigned ok;
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+        if (ok) return true;
+    }
+    return false;
+}
+// copies 128 bytes of this CTA's shared memory to a CTA of the cluster, counted by a barrier there
+__device__ __forceinline__ void send_128(unsigned to, unsigned from, unsigned bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], 128, [%2];"
+                 ::"r"(to), "r"(from), "r"(bar) : "memory");
+}
+__device__ __forceinline__ unsigned in_cta(unsigned addr, unsigned rank)
+{
+    unsigned r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+// Rounds whose exchanges have places of their own.  A partner sends round k + 4 after finishing round k + 2,
+// so after this warp sent round k + 2, so after this warp finished round k: nothing is overwritten unread
+// (nor is what this warp sent in round k before its copies are done).
+constexpr int kDepth = 4;
+
+// A warp's tiles, joined over its groups, its cluster and time.
+template <bool CLUSTER>
+struct Joints {
+    struct Shared {
+        unsigned long long bar[kDepth];
+        uint4 own[kDepth][8];   // what is sent: two channels' (A, H) each
+        uint4 slots[1];         // [kDepth][csize][8]: what has come
+    };
+    Shared *sh;
+    unsigned csize, rank;
+    F2 state;   // what comes into the tile of the cluster's first CTA, alike in all groups
+    bool lost = false;
+
+    static __host__ __device__ size_t bytes(unsigned csize) { return CLUSTER ? kDepth * (8 + 128 + 128 * (size_t)csize) : 0; }
+
+    // mem: warps x bytes(csize); the whole cluster calls
+    __device__ __forceinline__ void begin(unsigned char *mem, unsigned csize_, unsigned rank_)
+    {
+        csize = csize_;
+        rank = rank_;
+        if (!CLUSTER) return;
+        sh = reinterpret_cast<Shared *>(mem + (threadIdx.x >> 5) * bytes(csize));
+        if ((threadIdx.x & 31) == 0) {
+            for (int i = 0; i < kDepth; ++i) mbar_init(smem_u32(&sh->bar[i]));
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            for (int i = 0; i < kDepth; ++i) mbar_expect(smem_u32(&sh->bar[i]), csize * 128);
+        }
+        cluster_sync_all();   // every CTA's barriers are ready (and every CTA has read the first state)
+    }
+
+    // nothing of this CTA is read any more when the whole cluster has finished every round
+    __device__ __forceinline__ void end() const
+    {
+        if (CLUSTER) cluster_sync_all();
+    }
+
+    // own: this lane's stretch, by channel.  Leaves the stretch of the groups before in `before` and that of the
+    // warp in `all`, and sends it out.
+    __device__ __forceinline__ void first(int round, const Stretch (&own)[2], Stretch (&before)[2], Stretch (&all)[2])
+    {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            Stretch incl = own[c];
+#pragma unroll
+            for (int o = 8; o < 32; o <<= 1) {
+                const Stretch b = shfl_up(incl, o);
+                if (lane >= o) incl = join(b, incl);
+            }
+            before[c] = shfl_up(incl, 8);
+            all[c] = shfl(incl, 24 + lane % 8);
+        }
+        if (CLUSTER) {
+            const unsigned place = round % kDepth;
+            if (lane < 8)
+                sh->own[place][lane] = make_uint4(__float_as_uint(all[0].A), __float_as_uint(all[0].H),
+                                                  __float_as_uint(all[1].A), __float_as_uint(all[1].H));
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane < csize)   // one message a partner: a barrier takes its counts one after the other
+                send_128(in_cta(smem_u32(sh->slots + (place * csize + rank) * 8), lane), smem_u32(sh->own[place]),
+                         in_cta(smem_u32(&sh->bar[place]), lane));
+        }
+    }
+
+    // the state that comes into this lane's steps; moves `state` on
+    __device__ __forceinline__ F2 second(int round, const Stretch (&before)[2], const Stretch (&all)[2])
+    {
+        const int lane = threadIdx.x & 31;
+        F2 in = state;
+        if (!CLUSTER) {
+            state = {apply(all[0], in.x), apply(all[1], in.y)};
+        } else {
+            const unsigned place = round % kDepth, bar = smem_u32(&sh->bar[place]);
+            if (!lost) lost = !mbar_wait(bar, round / kDepth & 1);
+            if (__any_sync(kFull, lost)) {   // never seen: the states say so
+                lost = true;
+                in = state = {__int_as_float(0x7fffffff), __int_as_float(0x7fffffff)};
+            } else {
+                if (lane == 0) mbar_expect(bar, csize * 128);   // for the round that uses it next
+                // a group of lanes takes a run of the cluster's CTAs
+                const unsigned run = (csize + 3) / 4, part = lane / 8;
+                const uint4 *slots = sh->slots + place * csize * 8 + lane % 8;
+                Stretch sum[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}}, mine[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}};
+#pragma unroll 4
+                for (unsigned i = 0; i < run; ++i) {
+                    const unsigned r = part * run + i;
+                    if (r >= csize) break;
+                    const uint4 v = slots[r * 8];
+                    if (r == rank) {
+                        mine[0] = sum[0];
+                        mine[1] = sum[1];
+                    }
+                    sum[0] = join(sum[0], {__uint_as_float(v.x), __uint_as_float(v.y)});
+                    sum[1] = join(sum[1], {__uint_as_float(v.z), __uint_as_float(v.w)});
+                }
+                F2 s = state, start = state;
+#pragma unroll
+                for (unsigned p = 0; p < 4; ++p) {
+                    if (p == part) start = s;
+                    const Stretch r0 = shfl(sum[0], p * 8 + lane % 8), r1 = shfl(sum[1], p * 8 + lane % 8);
+                    s = {apply(r0, s.x), apply(r1, s.y)};
+                }
+                state = s;
+                start = {apply(mine[0], start.x), apply(mine[1], start.y)};
+                const unsigned from = rank / run * 8 + lane % 8;
+                in = {__shfl_sync(kFull, start.x, from), __shfl_sync(kFull, start.y, from)};
+            }
+        }
+        return lane >= 8 ? F2{apply(before[0], in.x), apply(before[1], in.y)} : in;
+    }
+};
+
+// Where a warp and a lane stand.
+template <int N>   // steps of a lane in a tile
+struct Place {
+    unsigned rank;
+    int c0, channels, ch;    // the strip's first channel, how many of its channels exist, this lane's first
+    long long b, span, t0;   // sequence, steps a cluster takes a round, this warp's first step
+    int rounds, off;         // off: this lane's first step in a tile
+    bool live, second;       // this lane's first and second channel exist
+    __device__ __forceinline__ Place(const ScanArgs &s, unsigned ctiles, unsigned csize)
+    {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+        rank = blockIdx.x % csize;
+        const unsigned id = blockIdx.x / csize;
+        b = id / ctiles;
+        c0 = (int)(id % ctiles * warps + warp) * kStrip;
+        channels = max(0, min(kStrip, (int)s.channels - c0));
+        ch = c0 + lane % 8 * 2;
+        live = ch < (int)s.channels;
+        second = ch + 1 < (int)s.channels;
+        span = (long long)(kGroups * N) * csize;
+        t0 = (long long)rank * (kGroups * N);
+        off = lane / 8 * N;
+        rounds = (int)((s.steps + span - 1) / span);
+    }
+};
+
+// The resets of this lane's steps in the warp's tile from step t0 on, bit by bit.
+template <int N>
+__device__ __forceinline__ unsigned reset_bits(const ScanArgs &s, long long b, long long t0)
+{
+    if (!s.resets) return 0;
+    const int lane = threadIdx.x & 31;
+    const uint8_t *p = s.resets + b * s.sr[0] + (t0 + lane) * s.sr[1];
+    const bool lo = t0 + lane < s.steps && *p != 0;
+    const bool hi = N == 16 && t0 + 32 + lane < s.steps && p[32 * s.sr[1]] != 0;
+    const unsigned a = __ballot_sync(kFull, lo), c = __ballot_sync(kFull, hi);
+    const int first = lane / 8 * N;   // of the tile's steps
+    return (first < 32 ? a : c) >> (first & 31) & ((1u << N) - 1u);
+}
+
+template <int N>
+__device__ __forceinline__ F2 first_state(const float *p, const ScanArgs &s, const Place<N> &me)
+{
+    const long long i = me.b * s.channels + me.ch;
+    return {p && me.live ? p[i] : 0.0f, p && me.second ? p[i + 1] : 0.0f};
+}
+
+template <int N>
+__device__ __forceinline__ void last_state(float *p, F2 v, const ScanArgs &s, const Place<N> &me)
+{
+    if (!p || me.rank != 0 || (threadIdx.x & 31) >= 8) return;
+    const long long i = me.b * s.channels + me.ch;
+    if (me.live) p[i] = v.x;
+    if (me.second) p[i + 1] = v.y;
+}
+
+// A tile between its two passes.
+template <int N>
+struct Held {
+    F2 w[N], v[N];
+    Stretch before[2], all[2];
+    unsigned resets;
+    bool plain, any;   // any: a lane of the warp has resets
+};
+
+// The stretches of a lane's two channels from its products and sums.  False where the lane has to go the
+// careful way.  A channel that does not exist passes its state on.
+template <int N>
+__device__ __forceinline__ bool settle(Stretch (&own)[2], F2 A, F2 H, unsigned resets, const Place<N> &me, bool whole)
+{
+    bool plain = whole || !me.live;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const bool exists = c ? me.second : me.live;
+        if (exists) plain = plain && at(A, c) != 0.0f && fabsf(at(H, c)) < kInf;
+        own[c] = exists ? Stretch{resets ? __int_as_float(0x7fffffff) : at(A, c), at(H, c)} : Stretch{1.0f, 0.0f};
+    }
+    return plain;
+}
+
+// Each pass is first written with products and sums alone: w h + v, and a reset's state of 0 by a select
+// where a warp has any.  That is right unless a weight is 0 (then the product A is, or may be) or a dropped
+// input is not finite (then H is not), or not every step exists; those lanes go the careful way.
+template <typename T, int N, bool SIG, bool WIDE, bool CLUSTER, int ST>
+__global__ void __launch_bounds__(kWarps * 32) k_scan_fwd(ScanArgs s, unsigned ctiles, unsigned csize)
+{
+    extern __shared__ __align__(16) unsigned char dyn[];
+    typedef Ring<T, N, 2, ST, WIDE> R;
+    const Place<N> me(s, ctiles, csize);
+    const R ring{dyn + (threadIdx.x >> 5) * R::BYTES};
+    Joints<CLUSTER> joints;
+    pdl_wait();
+    pdl_release();
+    const T *a = static_cast<const T *>(s.a) + me.b * s.sa[0] + me.c0;
+    const T *x = static_cast<const T *>(s.x) + me.b * s.sx[0] + me.c0;
+    T *out = static_cast<T *>(s.out_h) + me.b * s.sh[0] + me.ch;
+    auto request = [&](int k) {
+        ring.request(k, 0, a, s.sa[1], me.t0 + k * me.span, s.steps, me.channels);
+        ring.request(k, 1, x, s.sx[1], me.t0 + k * me.span, s.steps, me.channels);
+        copies_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < ST - 1; ++k) request(k);
+    unsigned resets = reset_bits<N>(s, me.b, me.t0);
+    joints.state = first_state(s.h0, s, me);
+    joints.begin(dyn + (blockDim.x >> 5) * R::BYTES, csize, me.rank);
+    const bool both = WIDE && me.second;
+
+    auto first = [&](int k, Held<N> &h) {
+        const long long t = me.t0 + k * me.span + me.off;
+        copies_wait<ST - 2>();
+        __syncwarp();
+        h.resets = resets;
+        F2 A{1.0f, 1.0f}, H{0.0f, 0.0f};
+        auto run = [&](auto any) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                h.w[i] = ring.read(k, 0, i);
+                h.v[i] = ring.read(k, 1, i);
+                if (SIG) {
+                    F2 c;
+                    gates(h.w[i], h.w[i], c);
+                    h.v[i] = h.v[i] * c;
+                }
+                if (any.value && resets >> i & 1u) H = {0.0f, 0.0f};
+                H = fma2(h.w[i], H, h.v[i]);
+                A = A * h.w[i];
+            }
+        };
+        h.any = __any_sync(kFull, resets != 0);
+        if (h.any) run(std::true_type());
+        else run(std::false_type());
+        Stretch own[2];
+        h.plain = settle(own, A, H, resets, me, t + N <= s.steps);
+        if (!h.plain) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                own[c] = {1.0f, 0.0f};
+                bool drop = false;
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const bool valid = (c ? me.second : me.live) && t + i < s.steps;
+                    float w = 1.0f, v = 0.0f;   // past the end the state stays
+                    if (valid) {
+                        const F2 ra = ring.read(k, 0, i), rx = ring.read(k, 1, i);
+                        const Gate g = gate<SIG>(at(ra, c));
+                        v = SIG ? weigh(g.v, at(rx, c), 0.0f) : at(rx, c);
+                        w = resets >> i & 1u ? 0.0f : g.w;
+                    }
+                    at(h.w[i], c) = w;
+                    at(h.v[i], c) = v;
+                    drop = drop || w == 0.0f;
+                    own[c].H = weigh(w, own[c].H, v);
+                    own[c].A *= w;
+                }
+                own[c].A = drop ? __int_as_float(0x7fffffff) : nonzero(own[c].A);
+            }
+        }
+        joints.first(k, own, h.before, h.all);   // (its shuffles also say that every lane has read the tile)
+        __syncwarp();
+        request(k + ST - 1);
+        resets = reset_bits<N>(s, me.b, t - me.off + me.span);
+    };
+    auto second = [&](int k, const Held<N> &h) {
+        const long long t = me.t0 + k * me.span + me.off;
+        F2 st = joints.second(k, h.before, h.all);
+        T *o = out + t * s.sh[1];
+        if (h.plain) {
+            auto run = [&](auto any) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    if (any.value && h.resets >> i & 1u) st = {0.0f, 0.0f};
+                    st = fma2(h.w[i], st, h.v[i]);
+                    if (me.live) store2(o, st, both, me.second);
+                    o += s.sh[1];
+                }
+            };
+            if (h.any) run(std::true_type());
+            else run(std::false_type());
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                st = {weigh(h.w[i].x, st.x, h.v[i].x), weigh(h.w[i].y, st.y, h.v[i].y)};
+                if (me.live && t + i < s.steps) store2(o, st, both, me.second);
+                o += s.sh[1];
+            }
+        }
+    };
+    if constexpr (CLUSTER) {
+        Held<N> h0, h1;
+        first(0, h0);
+        for (int k = 1; k < me.rounds; k += 2) {
+            first(k, h1);
+            second(k - 1, h0);
+            if (k + 1 < me.rounds) {
+                first(k + 1, h0);
+                second(k, h1);
+            }
+        }
+        if (me.rounds & 1) second(me.rounds - 1, h0);
+        else second(me.rounds - 1, h1);
+    } else {
+        Held<N> h;
+        for (int k = 0; k < me.rounds; ++k) {
+            first(k, h);
+            second(k, h);
+        }
+    }
+    joints.end();
+    last_state(s.last, joints.state, s, me);
+}
+
+// The gradient, on arrays turned so that step 0 is the last one forward; s.h is shifted by one step, so
+// that row t holds the state before that step (row steps - 1 is h0).
+template <typename T, int N, bool SIG, bool WIDE, bool CLUSTER, int ST>
+__global__ void __launch_bounds__(kWarps * 32) k_scan_bwd(ScanArgs s, unsigned ctiles, unsigned csize)
+{
+    extern __shared__ __align__(16) unsigned char dyn[];
+    constexpr int NA = SIG ? 4 : 3;
+    constexpr int AHEAD = CLUSTER ? ST - 2 : ST - 1;   // the tile before is still read
+    typedef Ring<T, N, NA, ST, WIDE> R;
+    const Place<N> me(s, ctiles, csize);
+    const R ring{dyn + (threadIdx.x >> 5) * R::BYTES};
+    Joints<CLUSTER> joints;
+    pdl_wait();
+    pdl_release();
+    const T *a = static_cast<const T *>(s.a) + me.b * s.sa[0] + me.c0;
+    const T *gh = static_cast<const T *>(s.gh) + me.b * s.sgh[0] + me.c0;
+    const T *h = static_cast<const T *>(s.h) + me.b * s.sh[0] + me.c0;
+    const T *x = SIG ? static_cast<const T *>(s.x) + me.b * s.sx[0] + me.c0 : nullptr;
+    T *ga = s.ga ? static_cast<T *>(s.ga) + me.b * s.sga[0] + me.ch : nullptr;
+    T *gx = s.gx ? static_cast<T *>(s.gx) + me.b * s.sgx[0] + me.ch : nullptr;
+    auto request = [&](int k) {
+        const long long t = me.t0 + k * me.span;
+        ring.request(k, 0, a, s.sa[1], t, s.steps, me.channels);
+        ring.request(k, 1, gh, s.sgh[1], t, s.steps, me.channels);
+        ring.request(k, 2, h, s.sh[1], t, s.steps - 1, me.channels);
+        if (SIG) ring.request(k, 3, x, s.sx[1], t, s.steps, me.channels);
+        copies_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) request(k);
+    unsigned resets = reset_bits<N>(s, me.b, me.t0);
+    joints.state = first_state(s.glast, s, me);
+    joints.begin(dyn + (blockDim.x >> 5) * R::BYTES, csize, me.rank);
+    const bool both = WIDE && me.second;
+
+    auto first = [&](int k, Held<N> &d) {
+        const long long t = me.t0 + k * me.span + me.off;
+        copies_wait<AHEAD - 1>();
+        __syncwarp();
+        d.resets = resets;
+        F2 A{1.0f, 1.0f}, H{0.0f, 0.0f};
+        auto run = [&](auto any) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                d.w[i] = ring.read(k, 0, i);
+                if (SIG) gates(d.w[i], d.w[i], d.v[i]);
+                H = d.w[i] * (H + ring.read(k, 1, i));
+                if (any.value && resets >> i & 1u) H = {0.0f, 0.0f};
+                A = A * d.w[i];
+            }
+        };
+        d.any = __any_sync(kFull, resets != 0);
+        if (d.any) run(std::true_type());
+        else run(std::false_type());
+        Stretch own[2];
+        d.plain = settle(own, A, H, resets, me, t + N < s.steps);   // (row steps - 1 reads h0)
+        if (!d.plain) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                own[c] = {1.0f, 0.0f};
+                bool drop = false;
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    if (!((c ? me.second : me.live) && t + i < s.steps)) continue;
+                    const F2 ra = ring.read(k, 0, i), rg = ring.read(k, 1, i);
+                    const float w = resets >> i & 1u ? 0.0f : gate<SIG>(at(ra, c)).w;
+                    drop = drop || w == 0.0f;
+                    own[c].H = weigh(w, own[c].H + at(rg, c), 0.0f);
+                    own[c].A *= w;
+                }
+                own[c].A = drop ? __int_as_float(0x7fffffff) : nonzero(own[c].A);
+            }
+        }
+        joints.first(k, own, d.before, d.all);
+        resets = reset_bits<N>(s, me.b, t - me.off + me.span);
+    };
+    auto second = [&](int k, const Held<N> &d) {
+        const long long t = me.t0 + k * me.span + me.off;
+        F2 c = joints.second(k, d.before, d.all);
+        T *oa = ga + t * s.sga[1], *ox = gx + t * s.sgx[1];
+        if (d.plain) {
+            auto run = [&](auto any) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const bool reset = any.value && (d.resets >> i & 1u);
+                    const F2 g = ring.read(k, 1, i) + c;
+                    F2 before = ring.read(k, 2, i), da, dx;
+                    if (reset) before = {0.0f, 0.0f};
+                    if (SIG) {
+                        const F2 in_x = ring.read(k, 3, i);
+                        da = g * fma2(in_x, F2{-1.0f, -1.0f}, before) * (d.w[i] * d.v[i]);
+                        dx = g * d.v[i];
+                        if (d.v[i].x == 0.0f) da.x = dx.x = 0.0f;
+                        if (d.v[i].y == 0.0f) da.y = dx.y = 0.0f;
+                    } else {
+                        da = g * before;
+                        dx = g;
+                        if (reset) da = {0.0f, 0.0f};
+                    }
+                    c = d.w[i] * g;
+                    if (reset) c = {0.0f, 0.0f};
+                    if (ga && me.live) store2(oa, da, both, me.second);
+                    if (gx && me.live) store2(ox, dx, both, me.second);
+                    oa += s.sga[1];
+                    ox += s.sgx[1];
+                }
+            };
+            if (d.any) run(std::true_type());
+            else run(std::false_type());
+        } else {
+            const F2 h0 = first_state(s.h0, s, me);
+#pragma unroll 1
+            for (int i = 0; i < N; ++i) {
+                if (!(me.live && t + i < s.steps)) break;
+                const bool reset = d.resets >> i & 1u;
+                const F2 rw = ring.read(k, 0, i), rg = ring.read(k, 1, i);
+                const F2 rb = t + i == s.steps - 1 ? h0 : ring.read(k, 2, i);
+                const F2 rx = SIG ? ring.read(k, 3, i) : F2{0.0f, 0.0f};
+                F2 da, dx;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const Gate f = gate<SIG>(at(rw, e));
+                    const float g = at(rg, e) + at(c, e), before = reset ? 0.0f : at(rb, e);
+                    if (SIG) {
+                        const float slope = f.w * f.v;
+                        at(da, e) = slope == 0.0f ? 0.0f : g * (before - at(rx, e)) * slope;
+                        at(dx, e) = weigh(f.v, g, 0.0f);
+                    } else {
+                        at(da, e) = reset ? 0.0f : g * before;
+                        at(dx, e) = g;
+                    }
+                    at(c, e) = weigh(reset ? 0.0f : f.w, g, 0.0f);
+                }
+                if (ga) store2(oa, da, both, me.second);
+                if (gx) store2(ox, dx, both, me.second);
+                oa += s.sga[1];
+                ox += s.sgx[1];
+            }
+        }
+        __syncwarp();   // every lane has read the tile
+        request(k + ST - 1);
+    };
+    if constexpr (CLUSTER) {
+        Held<N> h0, h1;
+        request(AHEAD);   // the first tile's predecessor's place is free
+        first(0, h0);
+        for (int k = 1; k < me.rounds; k += 2) {
+            first(k, h1);
+            second(k - 1, h0);
+            if (k + 1 < me.rounds) {
+                first(k + 1, h0);
+                second(k, h1);
+            }
+        }
+        if (me.rounds & 1) second(me.rounds - 1, h0);
+        else second(me.rounds - 1, h1);
+    } else {
+        Held<N> d;
+        for (int k = 0; k < me.rounds; ++k) {
+            first(k, d);
+            second(k, d);
+        }
+    }
+    joints.end();
+    last_state(s.gh0, joints.state, s, me);
 }
 
 // VEC values of T as they are in memory
@@ -97,386 +797,6 @@ struct Cell {
         }
     }
 };
-
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void *smem, const void *global)
-{
-    const unsigned s = (unsigned)__cvta_generic_to_shared(smem);
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(global) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(s), "l"(global) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-// A thread's rows of NA arrays for the rounds ahead.  Values of 4 bytes and more are copied to a ring of
-// ST rounds in shared memory, each thread reading only what it copied; single values of 2 bytes, which
-// cp.async cannot copy, are held in registers one round ahead.
-template <typename T, int VEC, int R, int NA, int ST>
-struct Rows {
-    typedef Cell<T, VEC> C;
-    typedef typename C::Raw Raw;
-    static constexpr int BYTES = VEC * (int)sizeof(T);
-    static constexpr bool ASYNC = BYTES >= 4;
-    static constexpr int AHEAD = ASYNC ? ST - 1 : 1;   // rounds requested before they are used
-    Raw *ring;                      // [ST][NA][R][threads]
-    Raw now[ASYNC ? 1 : NA][ASYNC ? 1 : R], next[ASYNC ? 1 : NA][ASYNC ? 1 : R];
-
-    __device__ __forceinline__ Raw *slot(int round, int array, int i) const
-    {
-        return ring + (((round % ST) * NA + array) * R + i) * blockDim.x + threadIdx.x;
-    }
-    // requests rows [t0, t0 + R) of one array for `round`
-    __device__ __forceinline__ void request(int round, int array, const T *p, long long stride, long long t0, long long steps, bool live)
-    {
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            if (!live || t0 + i >= steps) continue;
-            const Raw *from = reinterpret_cast<const Raw *>(p + (t0 + i) * stride);
-            if constexpr (ASYNC) copy_async<BYTES>(slot(round, array, i), from);
-            else next[array][i] = *from;
-        }
-    }
-    __device__ __forceinline__ void requested() const
-    {
-        if constexpr (ASYNC) copies_commit();
-    }
-    // makes `round` readable
-    __device__ __forceinline__ void arrive()
-    {
-        if constexpr (ASYNC) {
-            copies_wait<ST - 2>();
-        } else {
-#pragma unroll
-            for (int a = 0; a < NA; ++a)
-#pragma unroll
-                for (int i = 0; i < R; ++i) now[a][i] = next[a][i];
-        }
-    }
-    __device__ __forceinline__ void read(int round, int array, int i, float *f) const
-    {
-        if constexpr (ASYNC) C::unpack(*slot(round, array, i), f);
-        else C::unpack(now[array][i], f);
-    }
-};
-
-// The scan of the threads' stretches over one round of a CTA (and its cluster).
-template <int VEC, int LC>
-struct Joints {
-    static constexpr int CT = VEC * LC, RW = 32 / LC;
-    Stretch *totals;   // [warps][CT]
-    float *carry;      // [warps][CT] the state that comes into each warp's stretch
-    float *state;      // [CT] the state that comes into the round
-    Stretch *cluster;  // [2][csize][CT]
-    unsigned csize, rank;
-
-    static __host__ __device__ size_t bytes(int warps, unsigned csize)
-    {
-        return (size_t)CT * (warps * 12 + 4 + (csize > 1 ? 16 * csize : 0));
-    }
-    __device__ __forceinline__ Joints(unsigned char *mem, unsigned csize_, unsigned rank_) : csize(csize_), rank(rank_)
-    {
-        const int warps = blockDim.x >> 5;
-        totals = reinterpret_cast<Stretch *>(mem);
-        cluster = totals + warps * CT;
-        carry = reinterpret_cast<float *>(cluster + (csize > 1 ? 2 * csize * CT : 0));
-        state = carry + warps * CT;
-    }
-    // own: this thread's stretch, by channel; h receives the state that comes into it
-    __device__ __forceinline__ void scan(int round, const Stretch *own, float *h)
-    {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lc = lane % LC, warps = blockDim.x >> 5;
-        Stretch incl[VEC], excl[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            incl[e] = own[e];
-            excl[e] = {1.0f, 0.0f};
-        }
-        if constexpr (RW > 1) {
-#pragma unroll
-            for (int o = LC; o < 32; o <<= 1)
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const Stretch before{__shfl_up_sync(kFull, incl[e].A, o), __shfl_up_sync(kFull, incl[e].H, o)};
-                    if (lane >= o) incl[e] = join(before, incl[e]);
-                }
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const Stretch before{__shfl_up_sync(kFull, incl[e].A, LC), __shfl_up_sync(kFull, incl[e].H, LC)};
-                if (lane >= LC) excl[e] = before;
-            }
-        }
-        if (lane >= 32 - LC) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) totals[warp * CT + lc * VEC + e] = incl[e];
-        }
-        __syncthreads();
-        if (csize > 1) {
-            Stretch *slot = cluster + (round & 1) * csize * CT;
-            for (int ch = threadIdx.x; ch < CT; ch += blockDim.x) {
-                Stretch all = totals[ch];
-                for (int w = 1; w < warps; ++w) all = join(all, totals[w * CT + ch]);
-                for (unsigned r = 0; r < csize; ++r) {
-                    const unsigned to = cluster_smem_addr(slot + rank * CT + ch, r);
-                    st_cluster_f32(to, all.A);
-                    st_cluster_f32(to + 4, all.H);
-                }
-            }
-            cluster_sync_all();
-            for (int ch = threadIdx.x; ch < CT; ch += blockDim.x) {
-                float c = state[ch], in = 0.0f;
-                for (unsigned r = 0; r < csize; ++r) {
-                    if (r == rank) in = c;
-                    c = weigh(slot[r * CT + ch].A, c, slot[r * CT + ch].H);
-                }
-                state[ch] = c;
-                for (int w = 0; w < warps; ++w) {
-                    carry[w * CT + ch] = in;
-                    in = weigh(totals[w * CT + ch].A, in, totals[w * CT + ch].H);
-                }
-            }
-        } else {
-            for (int ch = threadIdx.x; ch < CT; ch += blockDim.x) {
-                float c = state[ch];
-                for (int w = 0; w < warps; ++w) {
-                    carry[w * CT + ch] = c;
-                    c = weigh(totals[w * CT + ch].A, c, totals[w * CT + ch].H);
-                }
-                state[ch] = c;
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) h[e] = weigh(excl[e].A, carry[warp * CT + lc * VEC + e], excl[e].H);
-    }
-};
-
-// Where a CTA and a thread stand.
-template <int VEC, int LC, int R>
-struct Place {
-    static constexpr int CT = VEC * LC, RW = 32 / LC;
-    unsigned rank;
-    long long b, tile, span, row0;   // sequence, steps a CTA takes a round, a cluster takes, this thread's first
-    unsigned c0, ch;                 // the tile's first channel and this thread's
-    int rounds;
-    bool live;
-    __device__ __forceinline__ Place(const ScanArgs &s, unsigned ctiles, unsigned csize)
-    {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        rank = blockIdx.x % csize;
-        const unsigned id = blockIdx.x / csize;
-        b = id / ctiles;
-        c0 = id % ctiles * CT;
-        ch = c0 + lane % LC * VEC;
-        live = ch < s.channels;
-        tile = (long long)(blockDim.x >> 5) * RW * R;
-        span = tile * csize;
-        row0 = rank * tile + (warp * RW + lane / LC) * R;
-        rounds = (int)((s.steps + span - 1) / span);
-    }
-};
-
-template <int R>
-__device__ __forceinline__ unsigned reset_bits(const ScanArgs &s, long long b, long long t0)
-{
-    unsigned bits = 0;
-    if (s.resets) {
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-            if (t0 + i < s.steps && s.resets[b * s.sr[0] + (t0 + i) * s.sr[1]]) bits |= 1u << i;
-    }
-    return bits;
-}
-
-template <typename T, bool SIG, int VEC, int LC, int R, int ST>
-__global__ void __launch_bounds__(kMaxWarps * 32) k_scan_fwd(ScanArgs s, unsigned ctiles, unsigned csize)
-{
-    extern __shared__ __align__(16) unsigned char dyn[];
-    typedef Rows<T, VEC, R, 2, ST> In;
-    typedef Joints<VEC, LC> J;
-    const Place<VEC, LC, R> me(s, ctiles, csize);
-    In in;
-    in.ring = reinterpret_cast<typename In::Raw *>(dyn);
-    J joints(dyn + (In::ASYNC ? (size_t)ST * 2 * R * In::BYTES * blockDim.x : 0), csize, me.rank);
-    pdl_wait();
-    pdl_release();
-    const T *a = static_cast<const T *>(s.a) + me.b * s.sa[0] + me.ch;
-    const T *x = static_cast<const T *>(s.x) + me.b * s.sx[0] + me.ch;
-    T *out = static_cast<T *>(s.out_h) + me.b * s.sh[0] + me.ch;
-#pragma unroll
-    for (int k = 0; k < In::AHEAD; ++k) {
-        in.request(k, 0, a, s.sa[1], me.row0 + k * me.span, s.steps, me.live);
-        in.request(k, 1, x, s.sx[1], me.row0 + k * me.span, s.steps, me.live);
-        in.requested();
-    }
-    unsigned resets = reset_bits<R>(s, me.b, me.row0);
-    for (unsigned ch = threadIdx.x; ch < (unsigned)J::CT; ch += blockDim.x)
-        joints.state[ch] = s.h0 && me.c0 + ch < s.channels ? s.h0[me.b * s.channels + me.c0 + ch] : 0.0f;
-    if (csize > 1) cluster_sync_all();   // every CTA of the cluster has started (and has read h0)
-    for (int k = 0; k < me.rounds; ++k) {
-        const long long t0 = me.row0 + k * me.span;
-        in.arrive();
-        float w[R][VEC], v[R][VEC];
-        Stretch own[VEC];
-        unsigned zero[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            own[e] = {1.0f, 0.0f};
-            zero[e] = 0;
-        }
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            in.read(k, 0, i, w[i]);
-            in.read(k, 1, i, v[i]);
-            const bool valid = me.live && t0 + i < s.steps, reset = resets >> i & 1u;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const Gate g = gate<SIG>(w[i][e]);
-                if (SIG) v[i][e] = weigh(g.v, v[i][e], 0.0f);
-                w[i][e] = reset ? 0.0f : g.w;
-                if (!valid) {   // past the end: the state stays
-                    w[i][e] = 1.0f;
-                    v[i][e] = 0.0f;
-                }
-                zero[e] |= w[i][e] == 0.0f;
-                own[e].H = weigh(w[i][e], own[e].H, v[i][e]);
-                own[e].A *= w[i][e];
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-            if (own[e].A == 0.0f && !zero[e]) own[e].A = 1.4e-45f;
-        if (In::ASYNC || k + 1 < me.rounds) {
-            const long long ahead = t0 + In::AHEAD * me.span;
-            in.request(k + In::AHEAD, 0, a, s.sa[1], ahead, s.steps, me.live);
-            in.request(k + In::AHEAD, 1, x, s.sx[1], ahead, s.steps, me.live);
-            in.requested();
-        }
-        resets = reset_bits<R>(s, me.b, t0 + me.span);
-        float h[VEC];
-        joints.scan(k, own, h);
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) h[e] = weigh(w[i][e], h[e], v[i][e]);
-            if (me.live && t0 + i < s.steps) Cell<T, VEC>::store(out + (t0 + i) * s.sh[1], h);
-        }
-    }
-    if (s.last && me.rank == 0)
-        for (unsigned ch = threadIdx.x; ch < (unsigned)J::CT && me.c0 + ch < s.channels; ch += blockDim.x)
-            s.last[me.b * s.channels + me.c0 + ch] = joints.state[ch];
-}
-
-// The gradient, on arrays turned so that step 0 is the last one forward; s.h is shifted by one step, so
-// that row t holds the state before that step (row steps - 1 is h0).
-template <typename T, bool SIG, int VEC, int LC, int R, int ST>
-__global__ void __launch_bounds__(kMaxWarps * 32) k_scan_bwd(ScanArgs s, unsigned ctiles, unsigned csize)
-{
-    extern __shared__ __align__(16) unsigned char dyn[];
-    constexpr int NA = SIG ? 4 : 3;
-    typedef Rows<T, VEC, R, NA, ST> In;
-    typedef Joints<VEC, LC> J;
-    const Place<VEC, LC, R> me(s, ctiles, csize);
-    In in;
-    in.ring = reinterpret_cast<typename In::Raw *>(dyn);
-    J joints(dyn + (In::ASYNC ? (size_t)ST * NA * R * In::BYTES * blockDim.x : 0), csize, me.rank);
-    pdl_wait();
-    pdl_release();
-    const T *a = static_cast<const T *>(s.a) + me.b * s.sa[0] + me.ch;
-    const T *gh = static_cast<const T *>(s.gh) + me.b * s.sgh[0] + me.ch;
-    const T *h = static_cast<const T *>(s.h) + me.b * s.sh[0] + me.ch;
-    const T *x = SIG ? static_cast<const T *>(s.x) + me.b * s.sx[0] + me.ch : nullptr;
-    T *ga = s.ga ? static_cast<T *>(s.ga) + me.b * s.sga[0] + me.ch : nullptr;
-    T *gx = s.gx ? static_cast<T *>(s.gx) + me.b * s.sgx[0] + me.ch : nullptr;
-    auto request = [&](int k, long long t0) {
-        in.request(k, 0, a, s.sa[1], t0, s.steps, me.live);
-        in.request(k, 1, gh, s.sgh[1], t0, s.steps, me.live);
-        in.request(k, 2, h, s.sh[1], t0, s.steps - 1, me.live);
-        if (SIG) in.request(k, 3, x, s.sx[1], t0, s.steps, me.live);
-        in.requested();
-    };
-#pragma unroll
-    for (int k = 0; k < In::AHEAD; ++k) request(k, me.row0 + k * me.span);
-    unsigned resets = reset_bits<R>(s, me.b, me.row0);
-    for (unsigned ch = threadIdx.x; ch < (unsigned)J::CT; ch += blockDim.x)
-        joints.state[ch] = s.glast && me.c0 + ch < s.channels ? s.glast[me.b * s.channels + me.c0 + ch] : 0.0f;
-    if (csize > 1) cluster_sync_all();
-    for (int k = 0; k < me.rounds; ++k) {
-        const long long t0 = me.row0 + k * me.span;
-        in.arrive();
-        if (!In::ASYNC && k + 1 < me.rounds) request(k + 1, t0 + me.span);
-        const unsigned next_resets = reset_bits<R>(s, me.b, t0 + me.span);
-        Stretch own[VEC];
-        unsigned zero[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            own[e] = {1.0f, 0.0f};
-            zero[e] = 0;
-        }
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            float w[VEC], g[VEC];
-            in.read(k, 0, i, w);
-            in.read(k, 1, i, g);
-            const bool valid = me.live && t0 + i < s.steps, reset = resets >> i & 1u;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                float f = reset ? 0.0f : gate<SIG>(w[e]).w;
-                float in_c = weigh(f, g[e], 0.0f);
-                if (!valid) {
-                    f = 1.0f;
-                    in_c = 0.0f;
-                }
-                zero[e] |= f == 0.0f;
-                own[e].H = weigh(f, own[e].H, in_c);
-                own[e].A *= f;
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-            if (own[e].A == 0.0f && !zero[e]) own[e].A = 1.4e-45f;
-        float c[VEC];
-        joints.scan(k, own, c);
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const bool valid = me.live && t0 + i < s.steps, reset = resets >> i & 1u;
-            if (!valid) continue;
-            float w[VEC], g[VEC], before[VEC], in_x[VEC], da[VEC], dx[VEC];
-            in.read(k, 0, i, w);
-            in.read(k, 1, i, g);
-            in.read(k, 2, i, before);
-            if (SIG) in.read(k, 3, i, in_x);
-            if (t0 + i == s.steps - 1) {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) before[e] = s.h0 ? s.h0[me.b * s.channels + me.ch + e] : 0.0f;
-            }
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const Gate f = gate<SIG>(w[e]);
-                const float gt = g[e] + c[e];
-                const float bt = reset ? 0.0f : before[e];
-                if (SIG) {
-                    const float slope = f.w * f.v;
-                    da[e] = slope == 0.0f ? 0.0f : gt * (bt - in_x[e]) * slope;
-                    dx[e] = weigh(f.v, gt, 0.0f);
-                } else {
-                    da[e] = reset ? 0.0f : gt * bt;
-                    dx[e] = gt;
-                }
-                c[e] = weigh(reset ? 0.0f : f.w, gt, 0.0f);
-            }
-            if (ga) Cell<T, VEC>::store(ga + (t0 + i) * s.sga[1], da);
-            if (gx) Cell<T, VEC>::store(gx + (t0 + i) * s.sgx[1], dx);
-        }
-        resets = next_resets;
-        if (In::ASYNC) request(k + In::AHEAD, t0 + In::AHEAD * me.span);
-    }
-    if (s.gh0 && me.rank == 0)
-        for (unsigned ch = threadIdx.x; ch < (unsigned)J::CT && me.c0 + ch < s.channels; ch += blockDim.x)
-            s.gh0[me.b * s.channels + me.c0 + ch] = joints.state[ch];
-}
 
 // A few steps: one thread takes VEC channels through all of them.
 template <typename T, bool SIG, int VEC>
@@ -523,34 +843,21 @@ __global__ void __launch_bounds__(128) k_scan_few(ScanArgs s)
 #ifndef BST
 #define BST 3
 #endif
-#ifndef FR16
-#define FR16 4
+#ifndef BCL
+#define BCL 0
 #endif
-#ifndef BR16
-#define BR16 2
+#ifndef FN32
+#define FN32 8
 #endif
-#ifndef FR32
-#define FR32 4
-#endif
-#ifndef BR32
-#define BR32 2
+#ifndef BN32
+#define BN32 8
 #endif
 #ifndef FILL
-#define FILL 2
+#define FILL 8
 #endif
 #ifndef MAXCL
 #define MAXCL 16
 #endif
-
-// The tiles: 16 bytes a thread where the arrays allow it, else one value.
-template <typename T, bool WIDE>
-struct Tile;
-template <> struct Tile<float, true> { static constexpr int VEC = 4, LC = 8, FR = FR32, BR = BR32; };
-template <> struct Tile<__half, true> { static constexpr int VEC = 8, LC = 8, FR = FR16, BR = BR16; };
-template <> struct Tile<__nv_bfloat16, true> { static constexpr int VEC = 8, LC = 8, FR = FR16, BR = BR16; };
-template <> struct Tile<float, false> { static constexpr int VEC = 1, LC = 32, FR = 16, BR = 8; };
-template <> struct Tile<__half, false> { static constexpr int VEC = 1, LC = 32, FR = 16, BR = 8; };
-template <> struct Tile<__nv_bfloat16, false> { static constexpr int VEC = 1, LC = 32, FR = 16, BR = 8; };
 
 template <typename K>
 cudaError_t allow(K kernel, int smem)
@@ -560,39 +867,45 @@ cudaError_t allow(K kernel, int smem)
     return e;
 }
 
-template <typename T, bool SIG, bool WIDE, bool BACK>
-cudaError_t launch_tiles(const ScanArgs &a, const DeviceInfo &dev, cudaStream_t st)
+template <typename T, bool SIG, bool WIDE, bool BACK, bool CLUSTER>
+cudaError_t launch_tiles(const ScanArgs &a, unsigned warps, unsigned csize, const DeviceInfo &dev, cudaStream_t st)
 {
-    typedef Tile<T, WIDE> S;
-    constexpr int R = BACK ? S::BR : S::FR, NA = BACK ? (SIG ? 4 : 3) : 2, ST = BACK ? BST : FST;
-    constexpr int BYTES = S::VEC * (int)sizeof(T), CT = S::VEC * S::LC, RW = 32 / S::LC;
+    constexpr int NA = BACK ? (SIG ? 4 : 3) : 2, ST = BACK ? BST + BCL * CLUSTER : FST;
+    constexpr int N = sizeof(T) == 4 ? (BACK ? BN32 : FN32) : 16;
     auto kernel = [] {
-        if constexpr (BACK) return k_scan_bwd<T, SIG, S::VEC, S::LC, R, ST>;
-        else return k_scan_fwd<T, SIG, S::VEC, S::LC, R, ST>;
+        if constexpr (BACK) return k_scan_bwd<T, N, SIG, WIDE, CLUSTER, ST>;
+        else return k_scan_fwd<T, N, SIG, WIDE, CLUSTER, ST>;
     }();
-    auto smem_of = [](int warps, unsigned csize) {
-        return (BYTES >= 4 ? (size_t)ST * NA * R * BYTES * warps * 32 : 0) + Joints<S::VEC, S::LC>::bytes(warps, csize);
-    };
+    auto smem_of = [](unsigned w, unsigned cs) { return w * (Ring<T, N, NA, ST, WIDE>::BYTES + Joints<CLUSTER>::bytes(cs)); };
     {
         static std::mutex mu;
         static bool done[64] = {};
         std::lock_guard<std::mutex> lock(mu);
         if (!done[dev.device]) {
-            const cudaError_t e = allow(kernel, (int)smem_of(kMaxWarps, kMaxCluster));
+            const cudaError_t e = allow(kernel, (int)smem_of(kWarps, kMaxCluster));
             if (e != cudaSuccess) return e;
             done[dev.device] = true;
         }
     }
-    const unsigned ctiles = (a.channels + CT - 1) / CT;
-    const unsigned long long tiles = (unsigned long long)ctiles * a.batch;
-    // warps: no more than the steps need; then CTAs over time until the SMs are filled, as long as each
-    // has a stretch of its own
-    int warps = 1;
-    while (warps < kMaxWarps && (long long)warps * RW * R < a.steps) warps *= 2;
+    const unsigned ctiles = (a.channels + kStrip * warps - 1) / (kStrip * warps);
+    const unsigned long long grid = (unsigned long long)ctiles * a.batch * csize;
+    if (grid > 0x7fffffffull) return cudaErrorInvalidConfiguration;
+    return launch_clusters(kernel, (unsigned)grid, warps * 32, csize, smem_of(warps, csize), st, a, ctiles, csize);
+}
+
+template <typename T, bool SIG, bool WIDE, bool BACK>
+cudaError_t launch_any(const ScanArgs &a, const DeviceInfo &dev, cudaStream_t st)
+{
+    constexpr int TILE = kGroups * (sizeof(T) == 4 ? (BACK ? BN32 : FN32) : 16);
+    const unsigned strips = (a.channels + kStrip - 1) / kStrip;
+    const unsigned warps = strips >= 4 ? 4 : strips >= 2 ? 2 : 1;
+    // CTAs over time until there are FILL warps an SM, as long as each has a tile
     unsigned csize = 1;
-    while (csize < MAXCL && tiles * csize < (unsigned)FILL * dev.sms && (long long)warps * RW * R * csize < a.steps) csize *= 2;
-    if (tiles * csize > 0x7fffffffull) return cudaErrorInvalidConfiguration;
-    return launch_clusters(kernel, (unsigned)(tiles * csize), warps * 32, csize, smem_of(warps, csize), st, a, ctiles, csize);
+    while (csize < MAXCL && (unsigned long long)strips * a.batch * csize < (unsigned)FILL * dev.sms &&
+           (long long)TILE * csize < a.steps)
+        csize *= 2;
+    return csize > 1 ? launch_tiles<T, SIG, WIDE, BACK, true>(a, warps, csize, dev, st)
+                     : launch_tiles<T, SIG, WIDE, BACK, false>(a, warps, 1, dev, st);
 }
 
 bool aligned16(const void *p, const long long st[2], const ScanArgs &a, unsigned e)
@@ -613,7 +926,7 @@ cudaError_t fwd_t(const ScanArgs &a, const DeviceInfo &dev, cudaStream_t st)
         if (wide) return launch_clusters(k_scan_few<T, SIG, (int)P>, grid, 128, 1, 0, st, a);
         return launch_clusters(k_scan_few<T, SIG, 1>, grid, 128, 1, 0, st, a);
     }
-    return wide ? launch_tiles<T, SIG, true, false>(a, dev, st) : launch_tiles<T, SIG, false, false>(a, dev, st);
+    return wide ? launch_any<T, SIG, true, false>(a, dev, st) : launch_any<T, SIG, false, false>(a, dev, st);
 }
 
 template <typename T, bool SIG>
@@ -623,7 +936,7 @@ cudaError_t bwd_t(const ScanArgs &a, const DeviceInfo &dev, cudaStream_t st)
     const bool wide = a.channels % P == 0 && aligned16(a.a, a.sa, a, e) && aligned16(a.x, a.sx, a, e) &&
                       aligned16(a.h, a.sh, a, e) && aligned16(a.gh, a.sgh, a, e) && aligned16(a.ga, a.sga, a, e) &&
                       aligned16(a.gx, a.sgx, a, e);
-    return wide ? launch_tiles<T, SIG, true, true>(a, dev, st) : launch_tiles<T, SIG, false, true>(a, dev, st);
+    return wide ? launch_any<T, SIG, true, true>(a, dev, st) : launch_any<T, SIG, false, true>(a, dev, st);
 }
 
 // What a pass of no steps leaves: the state that came in.

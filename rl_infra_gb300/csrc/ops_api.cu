@@ -29,7 +29,9 @@ per_status refuse(const char *where, const char *what) { return fail(PER_ERR_INV
 
 per_status done(cudaError_t e, const char *where)
 {
-    return e == cudaSuccess ? PER_OK : fail(PER_ERR_CUDA, where, cudaGetErrorString(e));
+    if (e == cudaSuccess) return PER_OK;
+    cudaGetLastError();   // a refused launch is this call's error, not the next call's
+    return fail(PER_ERR_CUDA, where, cudaGetErrorString(e));
 }
 
 // An output's rows must not overlap: each stride covers what lies inside it.
