@@ -11,16 +11,17 @@
 // so that an infinite state is not dropped by it.  All of it is binary32.
 //
 // Work.  HBM bounds every case of some size (forward: two arrays read, one written; gradient: four or
-// three read, two written).  A warp takes a strip of 16 channels and works through time by itself, in
-// tiles of 64 steps, without a barrier: its lanes copy the tile's rows 16 bytes a copy (cp.async) some
-// tiles ahead into a ring in shared memory, and read it the other way round: a lane takes two neighbouring
-// channels and 16 consecutive steps, so only the (A, H) of four groups of lanes are left to be scanned by
-// shuffles (with 16 bytes of channels a lane and 4 steps the scan took three times the
-// recurrence's instructions).  Up to four warps side by side make a CTA.  Where the channels alone do not
-// fill the SMs, a cluster of up to 16 CTAs takes the same channels over consecutive tiles: each warp
-// sends its tile's (A, H) to its partners in the other CTAs by asynchronous stores into their shared
-// memory, which count down a barrier there (no fence, so output stores in flight are not waited
-// for), and only then finishes the tile before: the exchange runs beside the next tile's first pass.
+// three read, two written).  A warp takes a strip of 16 channels and works through time in tiles of 4 x N
+// steps: its lanes copy the tile's rows 16 bytes a copy (cp.async) some tiles ahead into a ring in shared
+// memory, and read it the other way round: a lane takes two neighbouring channels and N consecutive
+// steps, sweeps them once from 0 for its (A, H) and, when the state that comes in is known, once more for
+// the outputs, so only the joints of four groups of lanes are left to be scanned by shuffles.  Where there
+// are strips enough, nothing else is needed: no barrier.  Else several warps of a CTA take consecutive tiles
+// of a strip (one CTA barrier a round), and then a cluster of up to 16 CTAs: each CTA sends its round's
+// (A, H) to the others by asynchronous stores into their shared memory, which count down a barrier there
+// (no fence, so output stores in flight are not waited for), and only then finishes the round before:
+// the exchange runs beside the next round's first sweep.  (A remote store takes about 8 cycles of the
+// receiver: with one warp's stretch a message, 16 CTAs to 16, the exchange took 3.6 us a round.)
 #include "ops_internal.cuh"
 
 #include <algorithm>
@@ -33,7 +34,7 @@ namespace gbper {
 namespace {
 
 constexpr int kMaxCluster = 16;
-constexpr int kWarps = 4;     // of a CTA at most, side by side over the channels
+constexpr int kWarps = 8;     // of a CTA at most: strips side by side, times tiles one after the other
 constexpr int kStrip = 16;    // channels of a warp
 constexpr int kGroups = 4;    // groups of 8 lanes, one after the other in time
 constexpr float kInf = __builtin_huge_valf();
@@ -243,23 +244,26 @@ __device__ __forceinline__ void mbar_expect(unsigned bar, unsigned bytes)
 {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-// Waits for the phase of the given parity to end; false when it has not after a bounded number of tries.
+// Waits for the phase of the given parity to end; false when it has not after about two seconds.
 __device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned parity)
 {
-    for (int tries = 0; tries < 1 << 22; ++tries) {
+    unsigned long long began = 0, now;
+    for (int tries = 0; tries < 1 << 26; ++tries) {
         unsigned ok;
         asm volatile("{\n\t.reg .pred p;\n\t"
                      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
                      "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
         if (ok) return true;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+        if (tries == 0) began = now;
+        else if (now - began > 2000000000ull) return false;
     }
     return false;
 }
-// copies 128 bytes of this CTA's shared memory to a CTA of the cluster, counted by a barrier there
-__device__ __forceinline__ void send_128(unsigned to, unsigned from, unsigned bar)
+__device__ __forceinline__ void store_async(unsigned to, uint4 v, unsigned bar)
 {
-    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], 128, [%2];"
-                 ::"r"(to), "r"(from), "r"(bar) : "memory");
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];"
+                 ::"r"(to), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(bar) : "memory");
 }
 __device__ __forceinline__ unsigned in_cta(unsigned addr, unsigned rank)
 {
@@ -268,49 +272,58 @@ __device__ __forceinline__ unsigned in_cta(unsigned addr, unsigned rank)
     return r;
 }
 
-// Rounds whose exchanges have places of their own.  A partner sends round k + 4 after finishing round k + 2,
-// so after this warp sent round k + 2, so after this warp finished round k: nothing is overwritten unread
-// (nor is what this warp sent in round k before its copies are done).
+// Rounds whose joints have places of their own.  A CTA sends round k + 4 after finishing round k + 2, so
+// after this CTA sent round k + 2, so after this CTA finished round k: nothing is overwritten unread.
 constexpr int kDepth = 4;
 
-// A warp's tiles, joined over its groups, its cluster and time.
+__device__ __forceinline__ uint4 packed(const Stretch (&s)[2])
+{
+    return make_uint4(__float_as_uint(s[0].A), __float_as_uint(s[0].H), __float_as_uint(s[1].A), __float_as_uint(s[1].H));
+}
+__device__ __forceinline__ void unpacked(uint4 v, Stretch (&s)[2])
+{
+    s[0] = {__uint_as_float(v.x), __uint_as_float(v.y)};
+    s[1] = {__uint_as_float(v.z), __uint_as_float(v.w)};
+}
+
+// A strip's tiles, joined over a warp's groups, the CTA's warps (`times` tiles of one strip one after the
+// other), its cluster and the rounds.
 template <bool CLUSTER>
 struct Joints {
-    struct Shared {
-        unsigned long long bar[kDepth];
-        uint4 own[kDepth][8];   // what is sent: two channels' (A, H) each
-        uint4 slots[1];         // [kDepth][csize][8]: what has come
-    };
-    Shared *sh;
+    uint4 *tiles;               // [kDepth][times][8] of the strip: two channels' (A, H) of each tile
+    uint4 *slots;               // [kDepth][csize][8] of the strip: of each CTA
+    unsigned long long *bar;    // [kDepth] of the strip
     unsigned csize, rank;
-    F2 state;   // what comes into the tile of the cluster's first CTA, alike in all groups
+    int times, time;            // tiles of a strip in a round of the CTA, and which is this warp's
+    F2 state;                   // what comes into the round, alike in all groups and warps of the strip
     bool lost = false;
 
-    static __host__ __device__ size_t bytes(unsigned csize) { return CLUSTER ? kDepth * (8 + 128 + 128 * (size_t)csize) : 0; }
+    static __host__ __device__ size_t bytes(int times, unsigned csize)   // of a strip
+    {
+        return (times > 1 || CLUSTER ? kDepth * 128 * (size_t)times : 0) + (CLUSTER ? kDepth * (8 + 128 * (size_t)csize) : 0);
+    }
 
-    // mem: warps x bytes(csize); the whole cluster calls
-    __device__ __forceinline__ void begin(unsigned char *mem, unsigned csize_, unsigned rank_)
+    // mem: strips x bytes(times, csize); the whole cluster calls
+    __device__ __forceinline__ void begin(unsigned char *mem, int strip, int times_, int time_, unsigned csize_, unsigned rank_)
     {
         csize = csize_;
         rank = rank_;
+        times = times_;
+        time = time_;
+        tiles = reinterpret_cast<uint4 *>(mem + strip * bytes(times, csize));
         if (!CLUSTER) return;
-        sh = reinterpret_cast<Shared *>(mem + (threadIdx.x >> 5) * bytes(csize));
-        if ((threadIdx.x & 31) == 0) {
-            for (int i = 0; i < kDepth; ++i) mbar_init(smem_u32(&sh->bar[i]));
+        slots = tiles + kDepth * times * 8;
+        bar = reinterpret_cast<unsigned long long *>(slots + kDepth * csize * 8);
+        if (time == 0 && (threadIdx.x & 31) == 0) {
+            for (int i = 0; i < kDepth; ++i) mbar_init(smem_u32(&bar[i]));
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-            for (int i = 0; i < kDepth; ++i) mbar_expect(smem_u32(&sh->bar[i]), csize * 128);
+            for (int i = 0; i < kDepth; ++i) mbar_expect(smem_u32(&bar[i]), csize * 128);
         }
         cluster_sync_all();   // every CTA's barriers are ready (and every CTA has read the first state)
     }
 
-    // nothing of this CTA is read any more when the whole cluster has finished every round
-    __device__ __forceinline__ void end() const
-    {
-        if (CLUSTER) cluster_sync_all();
-    }
-
     // own: this lane's stretch, by channel.  Leaves the stretch of the groups before in `before` and that of the
-    // warp in `all`, and sends it out.
+    // warp in `all`, and makes it known.
     __device__ __forceinline__ void first(int round, const Stretch (&own)[2], Stretch (&before)[2], Stretch (&all)[2])
     {
         const int lane = threadIdx.x & 31;
@@ -325,16 +338,21 @@ struct Joints {
             before[c] = shfl_up(incl, 8);
             all[c] = shfl(incl, 24 + lane % 8);
         }
-        if (CLUSTER) {
-            const unsigned place = round % kDepth;
-            if (lane < 8)
-                sh->own[place][lane] = make_uint4(__float_as_uint(all[0].A), __float_as_uint(all[0].H),
-                                                  __float_as_uint(all[1].A), __float_as_uint(all[1].H));
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane < csize)   // one message a partner: a barrier takes its counts one after the other
-                send_128(in_cta(smem_u32(sh->slots + (place * csize + rank) * 8), lane), smem_u32(sh->own[place]),
-                         in_cta(smem_u32(&sh->bar[place]), lane));
+        if (times == 1 && !CLUSTER) return;
+        const unsigned place = round % kDepth;
+        uint4 *mine = tiles + place * times * 8 + lane % 8;
+        if (lane < 8) mine[time * 8] = packed(all);
+        __syncthreads();
+        if (CLUSTER && time == times - 1) {   // the CTA's stretch, to four CTAs at a time
+            Stretch sum[2], next[2];
+            unpacked(mine[0], sum);
+            for (int i = 1; i < times; ++i) {
+                unpacked(mine[i * 8], next);
+                sum[0] = join(sum[0], next[0]);
+                sum[1] = join(sum[1], next[1]);
+            }
+            const unsigned to = smem_u32(slots + (place * csize + rank) * 8 + lane % 8), b = smem_u32(&bar[place]);
+            for (unsigned r = lane / 8; r < csize; r += 4) store_async(in_cta(to, r), packed(sum), in_cta(b, r));
         }
     }
 
@@ -343,46 +361,64 @@ struct Joints {
     {
         const int lane = threadIdx.x & 31;
         F2 in = state;
-        if (!CLUSTER) {
+        if (times == 1 && !CLUSTER) {
             state = {apply(all[0], in.x), apply(all[1], in.y)};
         } else {
-            const unsigned place = round % kDepth, bar = smem_u32(&sh->bar[place]);
-            if (!lost) lost = !mbar_wait(bar, round / kDepth & 1);
-            if (__any_sync(kFull, lost)) {   // never seen: the states say so
-                lost = true;
-                in = state = {__int_as_float(0x7fffffff), __int_as_float(0x7fffffff)};
-            } else {
-                if (lane == 0) mbar_expect(bar, csize * 128);   // for the round that uses it next
-                // a group of lanes takes a run of the cluster's CTAs
-                const unsigned run = (csize + 3) / 4, part = lane / 8;
-                const uint4 *slots = sh->slots + place * csize * 8 + lane % 8;
-                Stretch sum[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}}, mine[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}};
+            const unsigned place = round % kDepth;
+            if (CLUSTER) {
+                const unsigned b = smem_u32(&bar[place]);
+                if (!lost) lost = !mbar_wait(b, round / kDepth & 1);
+                if (__any_sync(kFull, lost)) {   // never seen: the states say so
+                    lost = true;
+                    in = state = {__int_as_float(0x7fffffff), __int_as_float(0x7fffffff)};
+                } else {
+                    if (lane == 0 && time == 0) mbar_expect(b, csize * 128);   // for the round that uses it next
+                    // a group of lanes takes a run of the cluster's CTAs
+                    const unsigned run = (csize + 3) / 4, part = lane / 8;
+                    const uint4 *from = slots + place * csize * 8 + lane % 8;
+                    Stretch sum[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}}, mine[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}}, next[2];
 #pragma unroll 4
-                for (unsigned i = 0; i < run; ++i) {
-                    const unsigned r = part * run + i;
-                    if (r >= csize) break;
-                    const uint4 v = slots[r * 8];
-                    if (r == rank) {
-                        mine[0] = sum[0];
-                        mine[1] = sum[1];
+                    for (unsigned i = 0; i < run; ++i) {
+                        const unsigned r = part * run + i;
+                        if (r >= csize) break;
+                        if (r == rank) {
+                            mine[0] = sum[0];
+                            mine[1] = sum[1];
+                        }
+                        unpacked(from[r * 8], next);
+                        sum[0] = join(sum[0], next[0]);
+                        sum[1] = join(sum[1], next[1]);
                     }
-                    sum[0] = join(sum[0], {__uint_as_float(v.x), __uint_as_float(v.y)});
-                    sum[1] = join(sum[1], {__uint_as_float(v.z), __uint_as_float(v.w)});
-                }
-                F2 s = state, start = state;
+                    F2 s = state, start = state;
 #pragma unroll
-                for (unsigned p = 0; p < 4; ++p) {
-                    if (p == part) start = s;
-                    const Stretch r0 = shfl(sum[0], p * 8 + lane % 8), r1 = shfl(sum[1], p * 8 + lane % 8);
-                    s = {apply(r0, s.x), apply(r1, s.y)};
+                    for (unsigned p = 0; p < 4; ++p) {
+                        if (p == part) start = s;
+                        const Stretch r0 = shfl(sum[0], p * 8 + lane % 8), r1 = shfl(sum[1], p * 8 + lane % 8);
+                        s = {apply(r0, s.x), apply(r1, s.y)};
+                    }
+                    state = s;
+                    start = {apply(mine[0], start.x), apply(mine[1], start.y)};
+                    const unsigned lane0 = rank / run * 8 + lane % 8;
+                    in = {__shfl_sync(kFull, start.x, lane0), __shfl_sync(kFull, start.y, lane0)};
                 }
-                state = s;
-                start = {apply(mine[0], start.x), apply(mine[1], start.y)};
-                const unsigned from = rank / run * 8 + lane % 8;
-                in = {__shfl_sync(kFull, start.x, from), __shfl_sync(kFull, start.y, from)};
             }
+            F2 s = in;
+            const uint4 *mine = tiles + place * times * 8 + lane % 8;
+            for (int i = 0; i < times; ++i) {
+                if (i == time) in = s;
+                Stretch next[2];
+                unpacked(mine[i * 8], next);
+                s = {apply(next[0], s.x), apply(next[1], s.y)};
+            }
+            if (!CLUSTER) state = s;
         }
         return lane >= 8 ? F2{apply(before[0], in.x), apply(before[1], in.y)} : in;
+    }
+
+    // nothing of this CTA is read or written any more when the whole cluster has finished every round
+    __device__ __forceinline__ void end() const
+    {
+        if (CLUSTER) cluster_sync_all();
     }
 };
 
@@ -390,23 +426,26 @@ struct Joints {
 template <int N>   // steps of a lane in a tile
 struct Place {
     unsigned rank;
+    int strip, time;         // which of the CTA's strips, which of its tiles
     int c0, channels, ch;    // the strip's first channel, how many of its channels exist, this lane's first
     long long b, span, t0;   // sequence, steps a cluster takes a round, this warp's first step
     int rounds, off;         // off: this lane's first step in a tile
     bool live, second;       // this lane's first and second channel exist
-    __device__ __forceinline__ Place(const ScanArgs &s, unsigned ctiles, unsigned csize)
+    __device__ __forceinline__ Place(const ScanArgs &s, unsigned ctiles, unsigned csize, int times)
     {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, strips = (int)(blockDim.x >> 5) / times;
+        strip = warp % strips;
+        time = warp / strips;
         rank = blockIdx.x % csize;
         const unsigned id = blockIdx.x / csize;
         b = id / ctiles;
-        c0 = (int)(id % ctiles * warps + warp) * kStrip;
+        c0 = (int)(id % ctiles * strips + strip) * kStrip;
         channels = max(0, min(kStrip, (int)s.channels - c0));
         ch = c0 + lane % 8 * 2;
         live = ch < (int)s.channels;
         second = ch + 1 < (int)s.channels;
-        span = (long long)(kGroups * N) * csize;
-        t0 = (long long)rank * (kGroups * N);
+        span = (long long)(kGroups * N) * csize * times;
+        t0 = (long long)((int)rank * times + time) * (kGroups * N);
         off = lane / 8 * N;
         rounds = (int)((s.steps + span - 1) / span);
     }
@@ -420,7 +459,7 @@ __device__ __forceinline__ unsigned reset_bits(const ScanArgs &s, long long b, l
     const int lane = threadIdx.x & 31;
     const uint8_t *p = s.resets + b * s.sr[0] + (t0 + lane) * s.sr[1];
     const bool lo = t0 + lane < s.steps && *p != 0;
-    const bool hi = N == 16 && t0 + 32 + lane < s.steps && p[32 * s.sr[1]] != 0;
+    const bool hi = kGroups * N > 32 && t0 + 32 + lane < s.steps && p[32 * s.sr[1]] != 0;
     const unsigned a = __ballot_sync(kFull, lo), c = __ballot_sync(kFull, hi);
     const int first = lane / 8 * N;   // of the tile's steps
     return (first < 32 ? a : c) >> (first & 31) & ((1u << N) - 1u);
@@ -442,10 +481,8 @@ __device__ __forceinline__ void last_state(float *p, F2 v, const ScanArgs &s, co
     if (me.second) p[i + 1] = v.y;
 }
 
-// A tile between its two passes.
-template <int N>
+// A tile between its two sweeps.
 struct Held {
-    F2 w[N], v[N];
     Stretch before[2], all[2];
     unsigned resets;
     bool plain, any;   // any: a lane of the warp has resets
@@ -466,15 +503,16 @@ __device__ __forceinline__ bool settle(Stretch (&own)[2], F2 A, F2 H, unsigned r
     return plain;
 }
 
-// Each pass is first written with products and sums alone: w h + v, and a reset's state of 0 by a select
+// Each sweep is first written with products and sums alone: w h + v, and a reset's state of 0 by a select
 // where a warp has any.  That is right unless a weight is 0 (then the product A is, or may be) or a dropped
 // input is not finite (then H is not), or not every step exists; those lanes go the careful way.
 template <typename T, int N, bool SIG, bool WIDE, bool CLUSTER, int ST>
-__global__ void __launch_bounds__(kWarps * 32) k_scan_fwd(ScanArgs s, unsigned ctiles, unsigned csize)
+__global__ void __launch_bounds__(kWarps * 32, 2) k_scan_fwd(ScanArgs s, unsigned ctiles, unsigned csize, int times)
 {
     extern __shared__ __align__(16) unsigned char dyn[];
+    constexpr int AHEAD = CLUSTER ? ST - 2 : ST - 1;   // with a cluster the tile before is still read
     typedef Ring<T, N, 2, ST, WIDE> R;
-    const Place<N> me(s, ctiles, csize);
+    const Place<N> me(s, ctiles, csize, times);
     const R ring{dyn + (threadIdx.x >> 5) * R::BYTES};
     Joints<CLUSTER> joints;
     pdl_wait();
@@ -488,31 +526,31 @@ __global__ void __launch_bounds__(kWarps * 32) k_scan_fwd(ScanArgs s, unsigned c
         copies_commit();
     };
 #pragma unroll
-    for (int k = 0; k < ST - 1; ++k) request(k);
+    for (int k = 0; k < AHEAD; ++k) request(k);
     unsigned resets = reset_bits<N>(s, me.b, me.t0);
     joints.state = first_state(s.h0, s, me);
-    joints.begin(dyn + (blockDim.x >> 5) * R::BYTES, csize, me.rank);
+    joints.begin(dyn + (blockDim.x >> 5) * R::BYTES, me.strip, times, me.time, csize, me.rank);
     const bool both = WIDE && me.second;
 
-    auto first = [&](int k, Held<N> &h) {
+    auto first = [&](int k, Held &h) {
         const long long t = me.t0 + k * me.span + me.off;
-        copies_wait<ST - 2>();
+        copies_wait<CLUSTER ? AHEAD - 1 : AHEAD>();
         __syncwarp();
+        if (CLUSTER) request(k + AHEAD);   // (the place was last read before this warp's last shuffles)
         h.resets = resets;
         F2 A{1.0f, 1.0f}, H{0.0f, 0.0f};
         auto run = [&](auto any) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                h.w[i] = ring.read(k, 0, i);
-                h.v[i] = ring.read(k, 1, i);
+                F2 w = ring.read(k, 0, i), v = ring.read(k, 1, i);
                 if (SIG) {
                     F2 c;
-                    gates(h.w[i], h.w[i], c);
-                    h.v[i] = h.v[i] * c;
+                    gates(w, w, c);
+                    v = v * c;
                 }
                 if (any.value && resets >> i & 1u) H = {0.0f, 0.0f};
-                H = fma2(h.w[i], H, h.v[i]);
-                A = A * h.w[i];
+                H = fma2(w, H, v);
+                A = A * w;
             }
         };
         h.any = __any_sync(kFull, resets != 0);
@@ -525,31 +563,22 @@ __global__ void __launch_bounds__(kWarps * 32) k_scan_fwd(ScanArgs s, unsigned c
             for (int c = 0; c < 2; ++c) {
                 own[c] = {1.0f, 0.0f};
                 bool drop = false;
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < N; ++i) {
-                    const bool valid = (c ? me.second : me.live) && t + i < s.steps;
-                    float w = 1.0f, v = 0.0f;   // past the end the state stays
-                    if (valid) {
-                        const F2 ra = ring.read(k, 0, i), rx = ring.read(k, 1, i);
-                        const Gate g = gate<SIG>(at(ra, c));
-                        v = SIG ? weigh(g.v, at(rx, c), 0.0f) : at(rx, c);
-                        w = resets >> i & 1u ? 0.0f : g.w;
-                    }
-                    at(h.w[i], c) = w;
-                    at(h.v[i], c) = v;
+                    if (!((c ? me.second : me.live) && t + i < s.steps)) break;   // past the end the state stays
+                    const Gate g = gate<SIG>(at(ring.read(k, 0, i), c));
+                    const float x1 = at(ring.read(k, 1, i), c), w = resets >> i & 1u ? 0.0f : g.w;
                     drop = drop || w == 0.0f;
-                    own[c].H = weigh(w, own[c].H, v);
+                    own[c].H = weigh(w, own[c].H, SIG ? weigh(g.v, x1, 0.0f) : x1);
                     own[c].A *= w;
                 }
                 own[c].A = drop ? __int_as_float(0x7fffffff) : nonzero(own[c].A);
             }
         }
-        joints.first(k, own, h.before, h.all);   // (its shuffles also say that every lane has read the tile)
-        __syncwarp();
-        request(k + ST - 1);
+        joints.first(k, own, h.before, h.all);
         resets = reset_bits<N>(s, me.b, t - me.off + me.span);
     };
-    auto second = [&](int k, const Held<N> &h) {
+    auto second = [&](int k, const Held &h) {
         const long long t = me.t0 + k * me.span + me.off;
         F2 st = joints.second(k, h.before, h.all);
         T *o = out + t * s.sh[1];
@@ -557,8 +586,14 @@ __global__ void __launch_bounds__(kWarps * 32) k_scan_fwd(ScanArgs s, unsigned c
             auto run = [&](auto any) {
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
+                    F2 w = ring.read(k, 0, i), v = ring.read(k, 1, i);
+                    if (SIG) {
+                        F2 c;
+                        gates(w, w, c);
+                        v = v * c;
+                    }
                     if (any.value && h.resets >> i & 1u) st = {0.0f, 0.0f};
-                    st = fma2(h.w[i], st, h.v[i]);
+                    st = fma2(w, st, v);
                     if (me.live) store2(o, st, both, me.second);
                     o += s.sh[1];
                 }
@@ -566,16 +601,26 @@ __global__ void __launch_bounds__(kWarps * 32) k_scan_fwd(ScanArgs s, unsigned c
             if (h.any) run(std::true_type());
             else run(std::false_type());
         } else {
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < N; ++i) {
-                st = {weigh(h.w[i].x, st.x, h.v[i].x), weigh(h.w[i].y, st.y, h.v[i].y)};
-                if (me.live && t + i < s.steps) store2(o, st, both, me.second);
+                if (!(me.live && t + i < s.steps)) break;
+                const F2 ra = ring.read(k, 0, i), rx = ring.read(k, 1, i);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const Gate g = gate<SIG>(at(ra, c));
+                    at(st, c) = weigh(h.resets >> i & 1u ? 0.0f : g.w, at(st, c), SIG ? weigh(g.v, at(rx, c), 0.0f) : at(rx, c));
+                }
+                store2(o, st, both, me.second);
                 o += s.sh[1];
             }
         }
+        if (!CLUSTER) {
+            __syncwarp();   // every lane has read the tile
+            request(k + ST);
+        }
     };
     if constexpr (CLUSTER) {
-        Held<N> h0, h1;
+        Held h0, h1;
         first(0, h0);
         for (int k = 1; k < me.rounds; k += 2) {
             first(k, h1);
@@ -588,26 +633,27 @@ __global__ void __launch_bounds__(kWarps * 32) k_scan_fwd(ScanArgs s, unsigned c
         if (me.rounds & 1) second(me.rounds - 1, h0);
         else second(me.rounds - 1, h1);
     } else {
-        Held<N> h;
+        Held h;
+        request(ST - 1);
         for (int k = 0; k < me.rounds; ++k) {
             first(k, h);
             second(k, h);
         }
     }
     joints.end();
-    last_state(s.last, joints.state, s, me);
+    if (me.time == 0) last_state(s.last, joints.state, s, me);
 }
 
 // The gradient, on arrays turned so that step 0 is the last one forward; s.h is shifted by one step, so
 // that row t holds the state before that step (row steps - 1 is h0).
 template <typename T, int N, bool SIG, bool WIDE, bool CLUSTER, int ST>
-__global__ void __launch_bounds__(kWarps * 32) k_scan_bwd(ScanArgs s, unsigned ctiles, unsigned csize)
+__global__ void __launch_bounds__(kWarps * 32, 2) k_scan_bwd(ScanArgs s, unsigned ctiles, unsigned csize, int times)
 {
     extern __shared__ __align__(16) unsigned char dyn[];
     constexpr int NA = SIG ? 4 : 3;
-    constexpr int AHEAD = CLUSTER ? ST - 2 : ST - 1;   // the tile before is still read
+    constexpr int AHEAD = CLUSTER ? ST - 2 : ST - 1;
     typedef Ring<T, N, NA, ST, WIDE> R;
-    const Place<N> me(s, ctiles, csize);
+    const Place<N> me(s, ctiles, csize, times);
     const R ring{dyn + (threadIdx.x >> 5) * R::BYTES};
     Joints<CLUSTER> joints;
     pdl_wait();
@@ -630,23 +676,24 @@ __global__ void __launch_bounds__(kWarps * 32) k_scan_bwd(ScanArgs s, unsigned c
     for (int k = 0; k < AHEAD; ++k) request(k);
     unsigned resets = reset_bits<N>(s, me.b, me.t0);
     joints.state = first_state(s.glast, s, me);
-    joints.begin(dyn + (blockDim.x >> 5) * R::BYTES, csize, me.rank);
+    joints.begin(dyn + (blockDim.x >> 5) * R::BYTES, me.strip, times, me.time, csize, me.rank);
     const bool both = WIDE && me.second;
 
-    auto first = [&](int k, Held<N> &d) {
+    auto first = [&](int k, Held &d) {
         const long long t = me.t0 + k * me.span + me.off;
-        copies_wait<AHEAD - 1>();
+        copies_wait<CLUSTER ? AHEAD - 1 : AHEAD>();
         __syncwarp();
+        if (CLUSTER) request(k + AHEAD);
         d.resets = resets;
         F2 A{1.0f, 1.0f}, H{0.0f, 0.0f};
         auto run = [&](auto any) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                d.w[i] = ring.read(k, 0, i);
-                if (SIG) gates(d.w[i], d.w[i], d.v[i]);
-                H = d.w[i] * (H + ring.read(k, 1, i));
+                F2 w = ring.read(k, 0, i), v;
+                if (SIG) gates(w, w, v);
+                H = w * (H + ring.read(k, 1, i));
                 if (any.value && resets >> i & 1u) H = {0.0f, 0.0f};
-                A = A * d.w[i];
+                A = A * w;
             }
         };
         d.any = __any_sync(kFull, resets != 0);
@@ -659,13 +706,12 @@ __global__ void __launch_bounds__(kWarps * 32) k_scan_bwd(ScanArgs s, unsigned c
             for (int c = 0; c < 2; ++c) {
                 own[c] = {1.0f, 0.0f};
                 bool drop = false;
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < N; ++i) {
-                    if (!((c ? me.second : me.live) && t + i < s.steps)) continue;
-                    const F2 ra = ring.read(k, 0, i), rg = ring.read(k, 1, i);
-                    const float w = resets >> i & 1u ? 0.0f : gate<SIG>(at(ra, c)).w;
+                    if (!((c ? me.second : me.live) && t + i < s.steps)) break;
+                    const float w = resets >> i & 1u ? 0.0f : gate<SIG>(at(ring.read(k, 0, i), c)).w;
                     drop = drop || w == 0.0f;
-                    own[c].H = weigh(w, own[c].H + at(rg, c), 0.0f);
+                    own[c].H = weigh(w, own[c].H + at(ring.read(k, 1, i), c), 0.0f);
                     own[c].A *= w;
                 }
                 own[c].A = drop ? __int_as_float(0x7fffffff) : nonzero(own[c].A);
@@ -674,7 +720,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_scan_bwd(ScanArgs s, unsigned c
         joints.first(k, own, d.before, d.all);
         resets = reset_bits<N>(s, me.b, t - me.off + me.span);
     };
-    auto second = [&](int k, const Held<N> &d) {
+    auto second = [&](int k, const Held &d) {
         const long long t = me.t0 + k * me.span + me.off;
         F2 c = joints.second(k, d.before, d.all);
         T *oa = ga + t * s.sga[1], *ox = gx + t * s.sgx[1];
@@ -684,20 +730,21 @@ __global__ void __launch_bounds__(kWarps * 32) k_scan_bwd(ScanArgs s, unsigned c
                 for (int i = 0; i < N; ++i) {
                     const bool reset = any.value && (d.resets >> i & 1u);
                     const F2 g = ring.read(k, 1, i) + c;
-                    F2 before = ring.read(k, 2, i), da, dx;
+                    F2 w = ring.read(k, 0, i), before = ring.read(k, 2, i), da, dx;
                     if (reset) before = {0.0f, 0.0f};
                     if (SIG) {
-                        const F2 in_x = ring.read(k, 3, i);
-                        da = g * fma2(in_x, F2{-1.0f, -1.0f}, before) * (d.w[i] * d.v[i]);
-                        dx = g * d.v[i];
-                        if (d.v[i].x == 0.0f) da.x = dx.x = 0.0f;
-                        if (d.v[i].y == 0.0f) da.y = dx.y = 0.0f;
+                        F2 v;
+                        gates(w, w, v);
+                        da = g * fma2(ring.read(k, 3, i), F2{-1.0f, -1.0f}, before) * (w * v);
+                        dx = g * v;
+                        if (v.x == 0.0f) da.x = dx.x = 0.0f;
+                        if (v.y == 0.0f) da.y = dx.y = 0.0f;
                     } else {
                         da = g * before;
                         dx = g;
                         if (reset) da = {0.0f, 0.0f};
                     }
-                    c = d.w[i] * g;
+                    c = w * g;
                     if (reset) c = {0.0f, 0.0f};
                     if (ga && me.live) store2(oa, da, both, me.second);
                     if (gx && me.live) store2(ox, dx, both, me.second);
@@ -737,12 +784,13 @@ __global__ void __launch_bounds__(kWarps * 32) k_scan_bwd(ScanArgs s, unsigned c
                 ox += s.sgx[1];
             }
         }
-        __syncwarp();   // every lane has read the tile
-        request(k + ST - 1);
+        if (!CLUSTER) {
+            __syncwarp();   // every lane has read the tile
+            request(k + ST);
+        }
     };
     if constexpr (CLUSTER) {
-        Held<N> h0, h1;
-        request(AHEAD);   // the first tile's predecessor's place is free
+        Held h0, h1;
         first(0, h0);
         for (int k = 1; k < me.rounds; k += 2) {
             first(k, h1);
@@ -755,14 +803,15 @@ __global__ void __launch_bounds__(kWarps * 32) k_scan_bwd(ScanArgs s, unsigned c
         if (me.rounds & 1) second(me.rounds - 1, h0);
         else second(me.rounds - 1, h1);
     } else {
-        Held<N> d;
+        Held d;
+        request(ST - 1);
         for (int k = 0; k < me.rounds; ++k) {
             first(k, d);
             second(k, d);
         }
     }
     joints.end();
-    last_state(s.gh0, joints.state, s, me);
+    if (me.time == 0) last_state(s.gh0, joints.state, s, me);
 }
 
 // VEC values of T as they are in memory
@@ -838,13 +887,16 @@ __global__ void __launch_bounds__(128) k_scan_few(ScanArgs s)
 // ---- launches --------------------------------------------------------------------------------
 
 #ifndef FST
-#define FST 3
+#define FST 2
 #endif
 #ifndef BST
-#define BST 3
+#define BST 2
 #endif
-#ifndef BCL
-#define BCL 0
+#ifndef FN16
+#define FN16 16
+#endif
+#ifndef BN16
+#define BN16 16
 #endif
 #ifndef FN32
 #define FN32 8
@@ -858,6 +910,12 @@ __global__ void __launch_bounds__(128) k_scan_few(ScanArgs s)
 #ifndef MAXCL
 #define MAXCL 16
 #endif
+#ifndef MAXTW
+#define MAXTW 4
+#endif
+#ifndef CTAW
+#define CTAW 4
+#endif
 
 template <typename K>
 cudaError_t allow(K kernel, int smem)
@@ -867,45 +925,53 @@ cudaError_t allow(K kernel, int smem)
     return e;
 }
 
+template <typename T, bool BACK>
+constexpr int lane_steps() { return sizeof(T) == 4 ? (BACK ? BN32 : FN32) : (BACK ? BN16 : FN16); }
+
 template <typename T, bool SIG, bool WIDE, bool BACK, bool CLUSTER>
-cudaError_t launch_tiles(const ScanArgs &a, unsigned warps, unsigned csize, const DeviceInfo &dev, cudaStream_t st)
+cudaError_t launch_tiles(const ScanArgs &a, int strips, int times, unsigned csize, const DeviceInfo &dev, cudaStream_t st)
 {
-    constexpr int NA = BACK ? (SIG ? 4 : 3) : 2, ST = BACK ? BST + BCL * CLUSTER : FST;
-    constexpr int N = sizeof(T) == 4 ? (BACK ? BN32 : FN32) : 16;
+    constexpr int NA = BACK ? (SIG ? 4 : 3) : 2, ST = CLUSTER ? (BACK ? 3 : 4) : BACK ? BST : FST;
+    constexpr int N = lane_steps<T, BACK>();
     auto kernel = [] {
         if constexpr (BACK) return k_scan_bwd<T, N, SIG, WIDE, CLUSTER, ST>;
         else return k_scan_fwd<T, N, SIG, WIDE, CLUSTER, ST>;
     }();
-    auto smem_of = [](unsigned w, unsigned cs) { return w * (Ring<T, N, NA, ST, WIDE>::BYTES + Joints<CLUSTER>::bytes(cs)); };
+    auto smem_of = [](int sw, int tw, unsigned cs) {
+        return sw * (tw * (size_t)Ring<T, N, NA, ST, WIDE>::BYTES + Joints<CLUSTER>::bytes(tw, cs));
+    };
     {
         static std::mutex mu;
         static bool done[64] = {};
         std::lock_guard<std::mutex> lock(mu);
         if (!done[dev.device]) {
-            const cudaError_t e = allow(kernel, (int)smem_of(kWarps, kMaxCluster));
+            const cudaError_t e = allow(kernel, 227 * 1024);
             if (e != cudaSuccess) return e;
             done[dev.device] = true;
         }
     }
-    const unsigned ctiles = (a.channels + kStrip * warps - 1) / (kStrip * warps);
+    const unsigned ctiles = (a.channels + kStrip * strips - 1) / (kStrip * strips);
     const unsigned long long grid = (unsigned long long)ctiles * a.batch * csize;
     if (grid > 0x7fffffffull) return cudaErrorInvalidConfiguration;
-    return launch_clusters(kernel, (unsigned)grid, warps * 32, csize, smem_of(warps, csize), st, a, ctiles, csize);
+    return launch_clusters(kernel, (unsigned)grid, strips * times * 32, csize, smem_of(strips, times, csize), st, a, ctiles, csize,
+                           times);
 }
 
 template <typename T, bool SIG, bool WIDE, bool BACK>
 cudaError_t launch_any(const ScanArgs &a, const DeviceInfo &dev, cudaStream_t st)
 {
-    constexpr int TILE = kGroups * (sizeof(T) == 4 ? (BACK ? BN32 : FN32) : 16);
-    const unsigned strips = (a.channels + kStrip - 1) / kStrip;
-    const unsigned warps = strips >= 4 ? 4 : strips >= 2 ? 2 : 1;
-    // CTAs over time until there are FILL warps an SM, as long as each has a tile
+    constexpr int TILE = kGroups * lane_steps<T, BACK>();
+    const unsigned per_row = (a.channels + kStrip - 1) / kStrip;
+    const unsigned long long all = (unsigned long long)per_row * a.batch, want = (unsigned long long)FILL * dev.sms;
+    // warps over time, then CTAs over time, until there are FILL warps an SM, as long as each has a tile
+    int times = 1;
+    while (times < (BACK ? 4 : MAXTW) && all * times < want && (long long)TILE * times < a.steps) times *= 2;
+    int strips = 1;
+    while (strips < 4 && strips * times < (BACK ? 4 : CTAW) && (unsigned)strips < per_row) strips *= 2;
     unsigned csize = 1;
-    while (csize < MAXCL && (unsigned long long)strips * a.batch * csize < (unsigned)FILL * dev.sms &&
-           (long long)TILE * csize < a.steps)
-        csize *= 2;
-    return csize > 1 ? launch_tiles<T, SIG, WIDE, BACK, true>(a, warps, csize, dev, st)
-                     : launch_tiles<T, SIG, WIDE, BACK, false>(a, warps, 1, dev, st);
+    while (csize < MAXCL && all * times * csize < want && (long long)TILE * times * csize < a.steps) csize *= 2;
+    return csize > 1 ? launch_tiles<T, SIG, WIDE, BACK, true>(a, strips, times, csize, dev, st)
+                     : launch_tiles<T, SIG, WIDE, BACK, false>(a, strips, times, 1, dev, st);
 }
 
 bool aligned16(const void *p, const long long st[2], const ScanArgs &a, unsigned e)
