@@ -20,7 +20,9 @@
 #include "ops_internal.cuh"
 
 #include <algorithm>
+#include <cstring>
 #include <mutex>
+#include <type_traits>
 
 namespace gbper {
 
@@ -56,6 +58,74 @@ __device__ __forceinline__ RowSum join(RowSum a, RowSum b, float c)
     return r;
 }
 
+// A thread's running maximum and sums of two lanes of pairs, rescaled where the maximum rises.
+template <typename T>
+struct Running {
+    static constexpr int P = Pack<T>::N;
+    float m = -kInf;
+    F2 s0 = {0.0f, 0.0f}, s1 = {0.0f, 0.0f};
+
+    // the largest of a batch (NaN never raises it: it stays in the sums)
+    static __device__ __forceinline__ float largest(const Pack<T> (&in)[kUnroll])
+    {
+        if constexpr (sizeof(T) == 2) {   // pairs, in their own type
+            typedef typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type Two;
+            Two r;
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i) {
+                const unsigned w[4] = {in[i].raw.x, in[i].raw.y, in[i].raw.z, in[i].raw.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    Two v;
+                    memcpy(&v, &w[k], 4);
+                    r = i + k ? __hmax2(r, v) : v;
+                }
+            }
+            const float a = to_f32(r.x), b = to_f32(r.y);
+            return fmaxf(fmaxf(a, b), -kInf);   // (both NaN)
+        } else {
+            float r = -kInf;
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i) {
+                float f[P];
+                in[i].unpack(f);
+#pragma unroll
+                for (int e = 0; e < P; ++e) r = fmaxf(r, f[e]);
+            }
+            return r;
+        }
+    }
+    __device__ __forceinline__ void add(const Pack<T> (&in)[kUnroll], float c)
+    {
+        const float b = largest(in);
+        if (b > m) {
+            const float k = ex2((m - b) * c);   // 0 at first
+            s0 = s0 * F2{k, k};
+            s1 = s1 * F2{k, k};
+            m = b;
+        }
+        const float r = -finite_or_zero(m);
+        const F2 ref{r, r}, cc{c, c};
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            float f[P];
+            in[i].unpack(f);
+#pragma unroll
+            for (int e = 0; e < P; e += 2) {
+                const F2 x = (F2{f[e], f[e + 1]} + ref) * cc;
+                const F2 v{ex2(x.x), ex2(x.y)};
+                if (e & 2) s1 = s1 + v;
+                else s0 = s0 + v;
+            }
+        }
+    }
+    __device__ __forceinline__ RowSum sum() const
+    {
+        const F2 s = s0 + s1;
+        return {m, s.x + s.y};
+    }
+};
+
 // P consecutive elements of a row from element j on (j + P is the next lane's j; the whole warp calls), of
 // which those in [lo, hi) may be read; the others give -inf.  p + j need not be on a 16-byte
 // boundary: the blocks on boundaries are read, and joined with the next lane's.
@@ -63,39 +133,71 @@ template <typename T, typename Load>
 struct Pieces {
     static constexpr int P = Pack<T>::N;
     const T *p;
-    long long lo, hi;
+    int lo, hi;
     Load load;
     unsigned off;   // bytes from the boundary at or before p + j
     uint4 a[kUnroll], b[kUnroll];
 
-    __device__ __forceinline__ Pieces(const T *p_, long long lo_, long long hi_, long long j, Load load_)
+    __device__ __forceinline__ Pieces(const T *p_, int lo_, int hi_, int j, Load load_)
         : p(p_), lo(lo_), hi(hi_), load(load_), off((unsigned)(reinterpret_cast<uintptr_t>(p_ + j) & 15u))
     {
     }
-    __device__ __forceinline__ bool whole(long long j) const { return j >= lo && j + P <= hi; }
-    __device__ __forceinline__ void request(int i, long long j)
+    __device__ __forceinline__ int before() const { return (int)(off / (unsigned)sizeof(T)); }
+    __device__ __forceinline__ bool whole(int j) const { return j >= lo && j + P <= hi; }
+    // every block that the pieces from element `first` to element `last` need may be read
+    __device__ __forceinline__ bool whole_blocks(int first, int last) const
     {
-        const long long first = j - off / (unsigned)sizeof(T);
+        return first - before() >= lo && last - before() + (off ? 2 * P : P) <= hi;
+    }
+    __device__ __forceinline__ void request(int i, int j)
+    {
+        const int first = j - before();
         a[i] = b[i] = make_uint4(0, 0, 0, 0);
         if (whole(first)) a[i] = load(p + first);
         if (off && (threadIdx.x & 31) == 31 && whole(first + P)) b[i] = load(p + first + P);
     }
-    __device__ __forceinline__ Pack<T> get(int i, long long j)
+    // pieces w, w + step, ... of P elements counted from p (whole_blocks)
+    __device__ __forceinline__ void request_all(int w, int step, int shift = 0)
+    {
+        const unsigned char *from = reinterpret_cast<const unsigned char *>(p + shift) - off + (long long)w * 16;
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) a[i] = load(from + i * step * 16);
+        if (off && (threadIdx.x & 31) == 31) {
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i) b[i] = load(from + i * step * 16 + 16);
+        }
+    }
+    // the whole warp calls
+    __device__ __forceinline__ Pack<T> shifted(int i) const
     {
         Pack<T> r;
         r.raw = a[i];
-        const long long first = j - off / (unsigned)sizeof(T);
         if (off) {
             const uint4 n = make_uint4(__shfl_down_sync(0xffffffffu, a[i].x, 1), __shfl_down_sync(0xffffffffu, a[i].y, 1),
                                        __shfl_down_sync(0xffffffffu, a[i].z, 1), __shfl_down_sync(0xffffffffu, a[i].w, 1));
             r.raw = shift_bytes(a[i], (threadIdx.x & 31) == 31 ? b[i] : n, off);
         }
+        return r;
+    }
+    __device__ __forceinline__ Pack<T> get(int i, int j) const
+    {
+        Pack<T> r = shifted(i);
+        const int first = j - before();
         if (!(whole(first) && (!off || whole(first + P)))) {
             float f[P];
 #pragma unroll
             for (int e = 0; e < P; ++e) f[e] = j + e >= lo && j + e < hi ? to_f32(p[j + e]) : -kInf;
             r.pack(f);   // exact: the values came from T
         }
+        return r;
+    }
+    static __device__ __forceinline__ Pack<T> nothing()
+    {
+        float f[P];
+#pragma unroll
+        for (int e = 0; e < P; ++e) f[e] = -kInf;
+        Pack<T> r;
+        r.pack(f);
         return r;
     }
 };
@@ -211,29 +313,33 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, DM) k_distill(DistillArg
         }
     } else if (PART != kDistillBackward) {
         // ---- this CTA's part of the row --------------------------------------------------------
-        // (the last piece of the part may need the block behind it)
-        Pieces<T, FromGlobal> in(x, 0, min((int)a.vocab, j1 + P), 0, FromGlobal());
+        const int hi = min((int)a.vocab, j1 + P);   // (the last piece of the part may need the block behind it)
+        Pieces<T, FromGlobal> from(x, 0, hi, 0, FromGlobal());
+        Running<T> run;
         for (unsigned v = v0 + (t & ~31); v < v1; v += loaders * kUnroll) {
+            Pack<T> in[kUnroll];
+            const unsigned last = v + (kUnroll - 1) * loaders + 31;
+            if (last < v1 && from.whole_blocks((int)(v * P), (int)(last * P))) {
+                from.request_all(v + lane, loaders);
 #pragma unroll
-            for (int i = 0; i < kUnroll; ++i) in.request(i, (long long)(v + i * loaders + lane) * P);
+                for (int i = 0; i < kUnroll; ++i) {
+                    in[i] = from.shifted(i);
+                    if (PART == kDistillStep) part[v + i * loaders + lane - v0] = in[i].raw;
+                }
+            } else {
 #pragma unroll
-            for (int i = 0; i < kUnroll; ++i) {
-                const unsigned w = v + i * loaders + lane;
-                const Pack<T> piece = in.get(i, (long long)w * P);
-                if (w >= v1) continue;
-                if (PART == kDistillStep) part[w - v0] = piece.raw;
-                float f[P], m = own.m;
-                piece.unpack(f);
+                for (int i = 0; i < kUnroll; ++i) from.request(i, (int)((v + i * loaders + lane) * P));
 #pragma unroll
-                for (int e = 0; e < P; ++e) m = fmaxf(m, f[e]);
-                const float ref = finite_or_zero(m);
-                float s = own.s * ex2((own.m - ref) * c);
-#pragma unroll
-                for (int e = 0; e < P; ++e) s += ex2((f[e] - ref) * c);
-                own.m = m;
-                own.s = s;
+                for (int i = 0; i < kUnroll; ++i) {
+                    const unsigned w = v + i * loaders + lane;
+                    in[i] = from.get(i, (int)(w * P));
+                    if (w >= v1) in[i] = from.nothing();
+                    else if (PART == kDistillStep) part[w - v0] = in[i].raw;
+                }
             }
+            run.add(in, c);
         }
+        own = run.sum();
         for (int o = 16; o; o >>= 1) {
             RowSum other{__shfl_xor_sync(0xffffffffu, own.m, o), __shfl_xor_sync(0xffffffffu, own.s, o)};
             // the lower lane's stretch first, so that both lanes get the same bits
@@ -284,22 +390,42 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, DM) k_distill(DistillArg
     const int misg = (int)(reinterpret_cast<uintptr_t>(out) % 16 / sizeof(T));
     if (t < loaders && j0 < j1) {
         const int o0 = (j0 + misg) / P, o1 = (j1 - 1 + misg) / P + 1;
-        auto write = [&](auto &in) {
+        const F2 ref{-lse, -lse}, cc{c, c}, ff{f0, f0};
+        auto write = [&](auto &from) {
             for (int v = o0 + (t & ~31); v < o1; v += loaders * kUnroll) {
+                Pack<T> in[kUnroll];
+                const int last = v + (kUnroll - 1) * loaders + 31;
+                const bool fast = v * P - misg >= j0 && (last + 1) * P - misg <= j1 &&
+                                  from.whole_blocks(v * P - misg, last * P - misg);
+                if (fast) {
+                    from.request_all(v + lane, loaders, -misg);
 #pragma unroll
-                for (int i = 0; i < kUnroll; ++i) in.request(i, (long long)(v + i * loaders + lane) * P - misg);
+                    for (int i = 0; i < kUnroll; ++i) in[i] = from.shifted(i);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kUnroll; ++i) from.request(i, (v + i * loaders + lane) * P - misg);
+#pragma unroll
+                    for (int i = 0; i < kUnroll; ++i) in[i] = from.get(i, (v + i * loaders + lane) * P - misg);
+                }
 #pragma unroll
                 for (int i = 0; i < kUnroll; ++i) {
-                    const long long j = (long long)(v + i * loaders + lane) * P - misg;
-                    Pack<T> piece = in.get(i, j);
-                    if (j >= j1) continue;
+                    const int j = (v + i * loaders + lane) * P - misg;
                     float f[P];
-                    piece.unpack(f);
+                    in[i].unpack(f);
 #pragma unroll
-                    for (int e = 0; e < P; ++e) f[e] = live ? f0 * ex2((f[e] - lse) * c) : 0.0f;
-                    if (j >= j0 && j + P <= j1) {
-                        piece.pack(f);
-                        *reinterpret_cast<uint4 *>(out + j) = piece.raw;
+                    for (int e = 0; e < P; e += 2) {
+                        const F2 x = (F2{f[e], f[e + 1]} + ref) * cc;
+                        const F2 y = F2{ex2(x.x), ex2(x.y)} * ff;
+                        f[e] = y.x;
+                        f[e + 1] = y.y;
+                    }
+                    if (!live) {
+#pragma unroll
+                        for (int e = 0; e < P; ++e) f[e] = 0.0f;
+                    }
+                    if (fast || (j >= j0 && j + P <= j1)) {
+                        in[i].pack(f);
+                        *reinterpret_cast<uint4 *>(out + j) = in[i].raw;
                     } else {
 #pragma unroll
                         for (int e = 0; e < P; ++e)
@@ -309,12 +435,12 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, DM) k_distill(DistillArg
             }
         };
         if (PART == kDistillStep) {
-            Pieces<T, FromShared> in(reinterpret_cast<const T *>(part) - j0, j0, j1, (long long)o0 * P - misg, FromShared());
-            write(in);
+            Pieces<T, FromShared> from(reinterpret_cast<const T *>(part) - j0, j0, j1, o0 * P - misg, FromShared());
+            write(from);
         } else {
             // in place, another CTA may be writing its part: nothing outside [j0, j1) is read
-            Pieces<T, FromGlobal> in(x, j0, j1, (long long)o0 * P - misg, FromGlobal());
-            write(in);
+            Pieces<T, FromGlobal> from(x, j0, j1, o0 * P - misg, FromGlobal());
+            write(from);
         }
     }
     if (!live) return;

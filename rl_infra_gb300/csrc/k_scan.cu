@@ -25,8 +25,9 @@
 #include "ops_internal.cuh"
 
 #include <algorithm>
+#include <atomic>
+#include <cmath>
 #include <cstring>
-#include <mutex>
 #include <type_traits>
 
 namespace gbper {
@@ -39,43 +40,6 @@ constexpr int kStrip = 16;    // channels of a warp
 constexpr int kGroups = 4;    // groups of 8 lanes, one after the other in time
 constexpr float kInf = __builtin_huge_valf();
 constexpr unsigned kFull = 0xffffffffu;
-
-// ---- pairs of binary32, two to an instruction -------------------------------------------------
-struct F2 {
-    float x, y;
-};
-__device__ __forceinline__ unsigned long long bits2(F2 v)
-{
-    unsigned long long r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
-    return r;
-}
-__device__ __forceinline__ F2 from_bits2(unsigned long long b)
-{
-    F2 v;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(b));
-    return v;
-}
-__device__ __forceinline__ F2 operator*(F2 a, F2 b)
-{
-    unsigned long long r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
-    return from_bits2(r);
-}
-__device__ __forceinline__ F2 operator+(F2 a, F2 b)
-{
-    unsigned long long r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
-    return from_bits2(r);
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
-{
-    unsigned long long r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
-    return from_bits2(r);
-}
-__device__ __forceinline__ float &at(F2 &v, int i) { return i ? v.y : v.x; }
-__device__ __forceinline__ float at(const F2 &v, int i) { return i ? v.y : v.x; }
 
 __device__ __forceinline__ float rcp(float x)
 {
@@ -213,10 +177,11 @@ struct Ring {
         if (c >= channels) return;
         const long long left = steps - t0 - r0;
         const T *from = p + c + (t0 + r0) * stride;
+        const bool all = t0 + kGroups * N <= steps;
 #pragma unroll
         for (int i = 0; i < (kGroups * N) / ROWS; ++i) {
             const int r = i * ROWS;   // + r0
-            if (r < left) {
+            if (all || r < left) {
                 unsigned char *at = to + (r + r0) / N * GROUP + (r + r0) % N * ROW + lane % PER * PIECE;
                 if constexpr (PIECE >= 4) copy_async<PIECE>(at, from);
                 else *reinterpret_cast<T *>(at) = *from;   // too small for an asynchronous copy
@@ -723,8 +688,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_scan_bwd(ScanArgs s, unsigne
     auto second = [&](int k, const Held &d) {
         const long long t = me.t0 + k * me.span + me.off;
         F2 c = joints.second(k, d.before, d.all);
+        const F2 start = c;
         T *oa = ga + t * s.sga[1], *ox = gx + t * s.sgx[1];
-        if (d.plain) {
+        bool plain = d.plain;
+        if (plain) {
+            F2 check{0.0f, 0.0f};   // NaN once a gradient is not finite: a slope of 0 may have to drop it
             auto run = [&](auto any) {
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
@@ -737,8 +705,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_scan_bwd(ScanArgs s, unsigne
                         gates(w, w, v);
                         da = g * fma2(ring.read(k, 3, i), F2{-1.0f, -1.0f}, before) * (w * v);
                         dx = g * v;
-                        if (v.x == 0.0f) da.x = dx.x = 0.0f;
-                        if (v.y == 0.0f) da.y = dx.y = 0.0f;
+                        check = fma2(da, F2{0.0f, 0.0f}, check);
                     } else {
                         da = g * before;
                         dx = g;
@@ -754,8 +721,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_scan_bwd(ScanArgs s, unsigne
             };
             if (d.any) run(std::true_type());
             else run(std::false_type());
-        } else {
+            plain = !SIG || !me.live || (check.x == 0.0f && (check.y == 0.0f || !me.second));
+        }
+        if (!plain) {
             const F2 h0 = first_state(s.h0, s, me);
+            c = start;
+            oa = ga + t * s.sga[1];
+            ox = gx + t * s.sgx[1];
 #pragma unroll 1
             for (int i = 0; i < N; ++i) {
                 if (!(me.live && t + i < s.steps)) break;
@@ -904,74 +876,110 @@ __global__ void __launch_bounds__(128) k_scan_few(ScanArgs s)
 #ifndef BN32
 #define BN32 8
 #endif
-#ifndef FILL
-#define FILL 8
+#ifndef LATC
+#define LATC 2500
 #endif
 #ifndef MAXCL
 #define MAXCL 16
 #endif
-#ifndef MAXTW
-#define MAXTW 4
-#endif
-#ifndef CTAW
-#define CTAW 4
-#endif
-
-template <typename K>
-cudaError_t allow(K kernel, int smem)
-{
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    return e;
-}
-
 template <typename T, bool BACK>
 constexpr int lane_steps() { return sizeof(T) == 4 ? (BACK ? BN32 : FN32) : (BACK ? BN16 : FN16); }
 
+// How a pass is laid out: a CTA of `strips` x `times` warps, clusters of csize CTAs.
+struct Layout {
+    int strips, times;
+    unsigned csize;
+    unsigned warps() const { return (unsigned)(strips * times); }
+};
+
 template <typename T, bool SIG, bool WIDE, bool BACK, bool CLUSTER>
-cudaError_t launch_tiles(const ScanArgs &a, int strips, int times, unsigned csize, const DeviceInfo &dev, cudaStream_t st)
-{
-    constexpr int NA = BACK ? (SIG ? 4 : 3) : 2, ST = CLUSTER ? (BACK ? 3 : 4) : BACK ? BST : FST;
-    constexpr int N = lane_steps<T, BACK>();
-    auto kernel = [] {
+struct Launch {
+    static constexpr int NA = BACK ? (SIG ? 4 : 3) : 2, ST = CLUSTER ? (BACK ? 3 : 4) : BACK ? BST : FST;
+    static constexpr int N = lane_steps<T, BACK>(), TILE = kGroups * N;
+    static auto kernel()
+    {
         if constexpr (BACK) return k_scan_bwd<T, N, SIG, WIDE, CLUSTER, ST>;
         else return k_scan_fwd<T, N, SIG, WIDE, CLUSTER, ST>;
-    }();
-    auto smem_of = [](int sw, int tw, unsigned cs) {
-        return sw * (tw * (size_t)Ring<T, N, NA, ST, WIDE>::BYTES + Joints<CLUSTER>::bytes(tw, cs));
-    };
-    {
-        static std::mutex mu;
-        static bool done[64] = {};
-        std::lock_guard<std::mutex> lock(mu);
-        if (!done[dev.device]) {
-            const cudaError_t e = allow(kernel, 227 * 1024);
-            if (e != cudaSuccess) return e;
-            done[dev.device] = true;
-        }
     }
-    const unsigned ctiles = (a.channels + kStrip * strips - 1) / (kStrip * strips);
-    const unsigned long long grid = (unsigned long long)ctiles * a.batch * csize;
-    if (grid > 0x7fffffffull) return cudaErrorInvalidConfiguration;
-    return launch_clusters(kernel, (unsigned)grid, strips * times * 32, csize, smem_of(strips, times, csize), st, a, ctiles, csize,
-                           times);
-}
+    static size_t smem(const Layout &l)
+    {
+        return l.strips * (l.times * (size_t)Ring<T, N, NA, ST, WIDE>::BYTES + Joints<CLUSTER>::bytes(l.times, l.csize));
+    }
+    // CTAs that run at once: asked once for each layout and device (0: not asked yet)
+    static cudaError_t capacity(const Layout &l, const DeviceInfo &dev, int *ctas)
+    {
+        static std::atomic<int> known[64][3][3][5];
+        auto log2of = [](unsigned v) { return v >= 16 ? 4 : v >= 8 ? 3 : v >= 4 ? 2 : v >= 2 ? 1 : 0; };
+        std::atomic<int> &k = known[dev.device][log2of(l.strips)][log2of(l.times)][log2of(l.csize)];
+        *ctas = k.load(std::memory_order_relaxed);
+        if (*ctas) return cudaSuccess;
+        cudaError_t e = cudaFuncSetAttribute(kernel(), cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel(), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e == cudaSuccess && l.csize == 1) {
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, kernel(), l.warps() * 32, smem(l));
+            *ctas *= dev.sms;
+        } else if (e == cudaSuccess) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(l.csize);
+            cfg.blockDim = dim3(l.warps() * 32);
+            cfg.dynamicSmemBytes = smem(l);
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = l.csize;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(ctas, kernel(), &cfg);
+            *ctas *= (int)l.csize;
+        }
+        if (e == cudaSuccess && *ctas <= 0) e = cudaErrorInvalidConfiguration;
+        if (e == cudaSuccess) k.store(*ctas, std::memory_order_relaxed);
+        return e;
+    }
+    static cudaError_t run(const ScanArgs &a, const Layout &l, cudaStream_t st)
+    {
+        const unsigned ctiles = (a.channels + kStrip * l.strips - 1) / (kStrip * l.strips);
+        const unsigned long long grid = (unsigned long long)ctiles * a.batch * l.csize;
+        if (grid > 0x7fffffffull) return cudaErrorInvalidConfiguration;
+        return launch_clusters(kernel(), (unsigned)grid, l.warps() * 32, l.csize, smem(l), st, a, ctiles, l.csize, l.times);
+    }
+};
 
+// The layout that should finish first, by a model with both of its sides measured: a round of an SM takes
+// the time of its bytes at HBM's rate, or what one warp's round takes by itself, whichever is longer (0.8 us;
+// with a CTA barrier 1.0 us, with the exchange of a cluster LATC ns); CTAs beyond what fits at once
+// run after the others.
 template <typename T, bool SIG, bool WIDE, bool BACK>
 cudaError_t launch_any(const ScanArgs &a, const DeviceInfo &dev, cudaStream_t st)
 {
-    constexpr int TILE = kGroups * lane_steps<T, BACK>();
+    typedef Launch<T, SIG, WIDE, BACK, false> One;
+    typedef Launch<T, SIG, WIDE, BACK, true> Many;
     const unsigned per_row = (a.channels + kStrip - 1) / kStrip;
-    const unsigned long long all = (unsigned long long)per_row * a.batch, want = (unsigned long long)FILL * dev.sms;
-    // warps over time, then CTAs over time, until there are FILL warps an SM, as long as each has a tile
-    int times = 1;
-    while (times < (BACK ? 4 : MAXTW) && all * times < want && (long long)TILE * times < a.steps) times *= 2;
-    int strips = 1;
-    while (strips < 4 && strips * times < (BACK ? 4 : CTAW) && (unsigned)strips < per_row) strips *= 2;
-    unsigned csize = 1;
-    while (csize < MAXCL && all * times * csize < want && (long long)TILE * times * csize < a.steps) csize *= 2;
-    return csize > 1 ? launch_tiles<T, SIG, WIDE, BACK, true>(a, strips, times, csize, dev, st)
-                     : launch_tiles<T, SIG, WIDE, BACK, false>(a, strips, times, 1, dev, st);
+    const double warp_us = One::TILE * kStrip * sizeof(T) * (One::NA + (BACK ? 2 : 1)) / 44500.0;
+    Layout best{};
+    double least = 1e30;
+    for (int times = 1; times <= 4; times *= 2) {
+        for (unsigned csize = 1; csize <= (times == 4 ? (unsigned)MAXCL : 1u); csize *= 2) {
+            const long long span = (long long)One::TILE * times * csize;
+            if (times * csize > 1 && span / 2 >= a.steps) continue;   // some would have no tile
+            Layout l{1, times, csize};
+            while (l.strips * 2 * times <= 4 && (unsigned)l.strips < per_row) l.strips *= 2;
+            int fit = 0;
+            const cudaError_t e = csize > 1 ? Many::capacity(l, dev, &fit) : One::capacity(l, dev, &fit);
+            if (e != cudaSuccess) return e;
+            const double ctas = (double)((per_row + l.strips - 1) / l.strips) * a.batch * csize;
+            const double alone = csize > 1 ? LATC / 1000.0 : times > 1 ? 1.0 : 0.8;
+            const double full = std::floor(ctas / fit), rest = ctas - full * fit;
+            auto round = [&](double n) { return std::max(alone, n / dev.sms * l.warps() * warp_us); };
+            const double us = std::ceil((double)a.steps / span) * (full * round(fit) + (rest > 0 ? round(rest) : 0.0));
+            if (us < least) {
+                least = us;
+                best = l;
+            }
+        }
+    }
+    return best.csize > 1 ? Many::run(a, best, st) : One::run(a, best, st);
 }
 
 bool aligned16(const void *p, const long long st[2], const ScanArgs &a, unsigned e)

@@ -26,11 +26,29 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kMaxCluster = 8;
 constexpr int kUnroll = 4;   // 16-byte loads of each row that a lane has in flight
 
-// a mass in units of 2^-40: NaN and negative 0, above 1 as 1
-__device__ __forceinline__ u64 units(float r)
-{
-    return r > 0.0f ? (u64)(fminf(r, 1.0f) * 1099511627776.0f) : 0ull;
-}
+// Masses summed in units of 2^-40.  A mass r in [0, 1] is cut to hi 2^-20 + lo 2^-40 by two additions of
+// 2^23 that round toward zero, whose low mantissa bits are the two whole numbers; the additions' bit
+// patterns are summed as they are, and the pattern of 2^23 is taken off by the count.  (A conversion of a
+// binary32 to 64 bits runs on the binary64 pipe, which bound the kernel: 56 us against 31 for 128
+// sequences of 131072.)  Exact while a thread sums at most 2^12 masses.
+struct Units {
+    unsigned hi = 0, lo = 0;
+    // r = max(0, min(1, p - q)); NaN counts 0
+    __device__ __forceinline__ void add(float p, float q)
+    {
+        float r;
+        asm("sub.rn.sat.f32 %0, %1, %2;" : "=f"(r) : "f"(p), "f"(q));
+        const float a = __fmaf_rz(r, 1048576.0f, 8388608.0f);
+        const float rest = fmaf(r, 1048576.0f, 8388608.0f - a);   // exact
+        const float b = __fmaf_rz(rest, 1048576.0f, 8388608.0f);
+        hi += __float_as_uint(a);
+        lo += __float_as_uint(b);
+    }
+    __device__ __forceinline__ u64 total(unsigned n) const
+    {
+        return ((u64)(hi - n * 0x4b000000u) << 20) + (lo - n * 0x4b000000u);
+    }
+};
 
 // 16 bytes at any address that is a multiple of 2: two aligned loads, shifted together.  The caller makes
 // sure that both lie inside the row.
@@ -76,21 +94,25 @@ struct Row {
         }
     }
 
-    __device__ __forceinline__ u64 mass(unsigned w, int e, float f, float g) const
+    // p with the place that counts 0 taken out
+    __device__ __forceinline__ void unpack(unsigned w, const Pack<T> &a, float *f) const
     {
-        return (long long)w * P - mis + e == without ? 0ull : units(q ? f - g : f);
+        a.unpack(f);
+        const long long k = without - ((long long)w * P - mis);
+        if (without >= 0 && k >= 0 && k < P) {
+#pragma unroll
+            for (int e = 0; e < P; ++e)
+                if (e == k) f[e] = 0.0f;
+        }
     }
 
-    // the sum over one piece
-    __device__ __forceinline__ u64 sum(unsigned w, const Pack<T> &a, const Pack<T> &b) const
+    __device__ __forceinline__ void add(unsigned w, const Pack<T> &a, const Pack<T> &b, Units &s) const
     {
         float f[P], g[P];
-        a.unpack(f);
+        unpack(w, a, f);
         b.unpack(g);
-        u64 s = 0;
 #pragma unroll
-        for (int e = 0; e < P; ++e) s += mass(w, e, f[e], g[e]);
-        return s;
+        for (int e = 0; e < P; ++e) s.add(f[e], g[e]);
     }
 };
 
@@ -156,7 +178,8 @@ __global__ void __launch_bounds__(kThreads) k_verify(VerifyArgs a, unsigned csiz
     const unsigned per_warp = (per_cta + kWarps - 1) / kWarps;
     const unsigned w0 = min(rank * per_cta + warp * per_warp, v1), w1 = min(w0 + per_warp, v1);
     for (int attempt = 0; attempt < 2; ++attempt) {
-        u64 own = 0;
+        Units sum;
+        unsigned count = 0;   // a lane's masses: at most 2^18 / (8 CTAs x 8 warps x 32 lanes), and a piece more
         for (unsigned w = w0 + lane; w < w1; w += 32 * kUnroll) {
             Pack<T> x[kUnroll], y[kUnroll];
 #pragma unroll
@@ -164,9 +187,12 @@ __global__ void __launch_bounds__(kThreads) k_verify(VerifyArgs a, unsigned csiz
                 if (w + 32 * i < w1) row.load(w + 32 * i, x[i], y[i]);
 #pragma unroll
             for (int i = 0; i < kUnroll; ++i)
-                if (w + 32 * i < w1) own += row.sum(w + 32 * i, x[i], y[i]);
+                if (w + 32 * i < w1) {
+                    row.add(w + 32 * i, x[i], y[i], sum);
+                    count += P;
+                }
         }
-        own = warp_sum(own);
+        const u64 own = warp_sum(sum.total(count));
         if (lane == 0) warp_total[warp] = own;
         __syncthreads();
         u64 mine = 0, before = 0;
@@ -213,7 +239,9 @@ __global__ void __launch_bounds__(kThreads) k_verify(VerifyArgs a, unsigned csiz
 #pragma unroll
             for (int i = 0; i < kUnroll; ++i) {
                 const unsigned at = w + 32 * i + lane;
-                const u64 s = at < w1 ? row.sum(at, x[i], y[i]) : 0;
+                Units piece;
+                if (at < w1) row.add(at, x[i], y[i], piece);
+                const u64 s = at < w1 ? piece.total(P) : 0;
                 u64 incl = s;
                 for (int o = 1; o < 32; o <<= 1) {
                     const u64 v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -221,13 +249,15 @@ __global__ void __launch_bounds__(kThreads) k_verify(VerifyArgs a, unsigned csiz
                 }
                 if (mark < before + incl && mark >= before + incl - s) {
                     float f[P], g[P];
-                    x[i].unpack(f);
+                    row.unpack(at, x[i], f);
                     y[i].unpack(g);
                     u64 c = before + incl - s;
                     int e = 0;
 #pragma unroll
                     for (int k = 0; k < P; ++k) {
-                        c += row.mass(at, k, f[k], g[k]);
+                        Units one;
+                        one.add(f[k], g[k]);
+                        c += one.total(1);
                         if (c <= mark) e = k + 1;
                     }
                     a.out[b * (D + 1) + n] = (int)((long long)at * P - row.mis + e);

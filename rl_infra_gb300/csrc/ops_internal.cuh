@@ -86,6 +86,43 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// ---- pairs of binary32, two to an instruction -------------------------------------------------
+struct F2 {
+    float x, y;
+};
+__device__ __forceinline__ unsigned long long bits2(F2 v)
+{
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+    return r;
+}
+__device__ __forceinline__ F2 from_bits2(unsigned long long b)
+{
+    F2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(b));
+    return v;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b)
+{
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return from_bits2(r);
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b)
+{
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return from_bits2(r);
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+    return from_bits2(r);
+}
+__device__ __forceinline__ float &at(F2 &v, int i) { return i ? v.y : v.x; }
+__device__ __forceinline__ float at(const F2 &v, int i) { return i ? v.y : v.x; }
+
 // 16 bytes of T in registers
 template <typename T>
 struct Pack {
