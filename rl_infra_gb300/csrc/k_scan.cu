@@ -34,8 +34,39 @@ namespace gbper {
 
 namespace {
 
+#ifndef FST
+#define FST 2
+#endif
+#ifndef BST
+#define BST 2
+#endif
+#ifndef FN16
+#define FN16 8
+#endif
+#ifndef BN16
+#define BN16 8
+#endif
+#ifndef FN32
+#define FN32 8
+#endif
+#ifndef BN32
+#define BN32 8
+#endif
+#ifndef LATC
+#define LATC 2500
+#endif
+#ifndef MAXCL
+#define MAXCL 16
+#endif
+#ifndef FLB
+#define FLB 4
+#endif
+#ifndef BLB
+#define BLB 4
+#endif
+
 constexpr int kMaxCluster = 16;
-constexpr int kWarps = 8;     // of a CTA at most: strips side by side, times tiles one after the other
+constexpr int kWarps = 4;     // of a CTA at most: strips side by side, times tiles one after the other
 constexpr int kStrip = 16;    // channels of a warp
 constexpr int kGroups = 4;    // groups of 8 lanes, one after the other in time
 constexpr float kInf = __builtin_huge_valf();
@@ -136,21 +167,19 @@ template <> __device__ __forceinline__ F2 unpack2<__half>(const __half *p)
     return {v.x, v.y};
 }
 
-// stores two channels where `wide` says that both exist and lie on a boundary of the pair
-template <typename T>
-__device__ __forceinline__ void store2(T *p, F2 v, bool wide, bool second)
+// stores a lane's two channels; WIDE: both exist and lie on a boundary of the pair
+template <typename T, bool WIDE>
+__device__ __forceinline__ void store2(T *p, F2 v, bool second)
 {
-    if (wide) {
-        if constexpr (sizeof(T) == 4) {
-            *reinterpret_cast<float2 *>(p) = make_float2(v.x, v.y);
-        } else if constexpr (std::is_same<T, __half>::value) {
-            *reinterpret_cast<__half2 *>(p) = __floats2half2_rn(v.x, v.y);
-        } else {
-            *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v.x, v.y);
-        }
-    } else {
+    if constexpr (!WIDE) {
         p[0] = from_f32<T>(v.x);
         if (second) p[1] = from_f32<T>(v.y);
+    } else if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float2 *>(p) = make_float2(v.x, v.y);
+    } else if constexpr (std::is_same<T, __half>::value) {
+        *reinterpret_cast<__half2 *>(p) = __floats2half2_rn(v.x, v.y);
+    } else {
+        *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v.x, v.y);
     }
 }
 
@@ -177,23 +206,27 @@ struct Ring {
         if (c >= channels) return;
         const long long left = steps - t0 - r0;
         const T *from = p + c + (t0 + r0) * stride;
-        const bool all = t0 + kGroups * N <= steps;
+        auto copy = [&](int i) {
+            const int r = i * ROWS + r0;
+            unsigned char *at = to + r / N * GROUP + r % N * ROW + lane % PER * PIECE;
+            const T *src = from + i * (long long)ROWS * stride;
+            if constexpr (PIECE >= 4) copy_async<PIECE>(at, src);
+            else *reinterpret_cast<T *>(at) = *src;   // too small for an asynchronous copy
+        };
+        if (t0 + kGroups * N <= steps) {
 #pragma unroll
-        for (int i = 0; i < (kGroups * N) / ROWS; ++i) {
-            const int r = i * ROWS;   // + r0
-            if (all || r < left) {
-                unsigned char *at = to + (r + r0) / N * GROUP + (r + r0) % N * ROW + lane % PER * PIECE;
-                if constexpr (PIECE >= 4) copy_async<PIECE>(at, from);
-                else *reinterpret_cast<T *>(at) = *from;   // too small for an asynchronous copy
-            }
-            from += (long long)ROWS * stride;
+            for (int i = 0; i < (kGroups * N) / ROWS; ++i) copy(i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < (kGroups * N) / ROWS; ++i)
+                if (i * ROWS < left) copy(i);
         }
     }
     // this lane's two channels of its step i
     __device__ __forceinline__ F2 read(int tile, int array, int i) const
     {
         const int lane = threadIdx.x & 31;
-        return unpack2<T>(reinterpret_cast<const T *>(slot(tile, array) + lane / 8 * GROUP + i * ROW) + lane % 8 * 2);
+        return unpack2<T>(reinterpret_cast<const T *>(slot(tile, array) + (lane / 8 * GROUP + lane % 8 * 2 * (int)sizeof(T)) + i * ROW));
     }
 };
 
@@ -209,21 +242,29 @@ __device__ __forceinline__ void mbar_expect(unsigned bar, unsigned bytes)
 {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-// Waits for the phase of the given parity to end; false when it has not after about two seconds.
-__device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned parity)
+__device__ __forceinline__ bool mbar_try(unsigned bar, unsigned parity)
 {
-    unsigned long long began = 0, now;
-    for (int tries = 0; tries < 1 << 26; ++tries) {
-        unsigned ok;
-        asm volatile("{\n\t.reg .pred p;\n\t"
-                     "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-                     "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-        if (ok) return true;
+    unsigned ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+// Waits for the phase of the given parity to end; false when it has not after about two seconds.
+__device__ __noinline__ bool mbar_wait_long(unsigned bar, unsigned parity)
+{
+    unsigned long long began, now;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(began));
+    for (int tries = 0; tries < 1 << 24; ++tries) {
+        if (mbar_try(bar, parity)) return true;
         asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
-        if (tries == 0) began = now;
-        else if (now - began > 2000000000ull) return false;
+        if (now - began > 2000000000ull) return false;
     }
     return false;
+}
+__device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned parity)
+{
+    return mbar_try(bar, parity) || mbar_wait_long(bar, parity);
 }
 __device__ __forceinline__ void store_async(unsigned to, uint4 v, unsigned bar)
 {
@@ -287,21 +328,47 @@ struct Joints {
         cluster_sync_all();   // every CTA's barriers are ready (and every CTA has read the first state)
     }
 
-    // own: this lane's stretch, by channel.  Leaves the stretch of the groups before in `before` and that of the
-    // warp in `all`, and makes it known.
-    __device__ __forceinline__ void first(int round, const Stretch (&own)[2], Stretch (&before)[2], Stretch (&all)[2])
+    // A, H: this lane's stretch where it is plain (A not 0, H finite; `resets` drops what comes in), else `own`.
+    // Leaves the stretch of the groups before in `before` and that of the warp in `all`, and makes it known.
+    __device__ __forceinline__ void first(int round, bool plain, F2 A, F2 H, bool resets, const Stretch (&own)[2],
+                                          Stretch (&before)[2], Stretch (&all)[2])
     {
         const int lane = threadIdx.x & 31;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            Stretch incl = own[c];
+        if (__all_sync(kFull, plain)) {
+            // everything is finite: a drop is a product with 0, and which stretches drop is told by the resets
+            const unsigned drops = __ballot_sync(kFull, resets);
+            if (resets) A = {0.0f, 0.0f};
 #pragma unroll
             for (int o = 8; o < 32; o <<= 1) {
-                const Stretch b = shfl_up(incl, o);
-                if (lane >= o) incl = join(b, incl);
+                const F2 a{__shfl_up_sync(kFull, A.x, o), __shfl_up_sync(kFull, A.y, o)};
+                const F2 h{__shfl_up_sync(kFull, H.x, o), __shfl_up_sync(kFull, H.y, o)};
+                if (lane >= o) {
+                    H = fma2(A, h, H);
+                    A = A * a;
+                }
             }
-            before[c] = shfl_up(incl, 8);
-            all[c] = shfl(incl, 24 + lane % 8);
+            const bool earlier = (drops & ((1u << (lane & 24)) - 1u)) != 0u;
+            const float nan = __int_as_float(0x7fffffff);
+            const F2 ba{__shfl_up_sync(kFull, A.x, 8), __shfl_up_sync(kFull, A.y, 8)};
+            before[0] = {earlier ? nan : nonzero(ba.x), __shfl_up_sync(kFull, H.x, 8)};
+            before[1] = {earlier ? nan : nonzero(ba.y), __shfl_up_sync(kFull, H.y, 8)};
+            const int end = 24 + lane % 8;
+            const F2 aa{__shfl_sync(kFull, A.x, end), __shfl_sync(kFull, A.y, end)};
+            all[0] = {drops ? nan : nonzero(aa.x), __shfl_sync(kFull, H.x, end)};
+            all[1] = {drops ? nan : nonzero(aa.y), __shfl_sync(kFull, H.y, end)};
+        } else {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                Stretch incl = own[c];
+#pragma unroll
+                for (int o = 8; o < 32; o <<= 1) {
+                    const Stretch b = shfl_up(incl, o);
+                    if (lane >= o) incl = join(b, incl);
+                }
+                const Stretch b = shfl_up(incl, 8), e = shfl(incl, 24 + lane % 8);
+                before[c] = b;
+                all[c] = e;
+            }
         }
         if (times == 1 && !CLUSTER) return;
         const unsigned place = round % kDepth;
@@ -408,7 +475,7 @@ struct Place {
         channels = max(0, min(kStrip, (int)s.channels - c0));
         ch = c0 + lane % 8 * 2;
         live = ch < (int)s.channels;
-        second = ch + 1 < (int)s.channels;
+        second = ch + 1 < (int)s.channels;   // (with 16-byte pieces: where the first does)
         span = (long long)(kGroups * N) * csize * times;
         t0 = (long long)((int)rank * times + time) * (kGroups * N);
         off = lane / 8 * N;
@@ -447,35 +514,39 @@ __device__ __forceinline__ void last_state(float *p, F2 v, const ScanArgs &s, co
 }
 
 // A tile between its two sweeps.
+template <int N, int NV>
 struct Held {
+    F2 w[N], v[NV];
     Stretch before[2], all[2];
     unsigned resets;
     bool plain, any;   // any: a lane of the warp has resets
 };
 
-// The stretches of a lane's two channels from its products and sums.  False where the lane has to go the
-// careful way.  A channel that does not exist passes its state on.
+// Whether a lane's products and sums can be taken as they are.  A channel that does not exist passes its state
+// on.
 template <int N>
-__device__ __forceinline__ bool settle(Stretch (&own)[2], F2 A, F2 H, unsigned resets, const Place<N> &me, bool whole)
+__device__ __forceinline__ bool settle(F2 &A, F2 &H, const Place<N> &me, bool whole)
 {
-    bool plain = whole || !me.live;
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        const bool exists = c ? me.second : me.live;
-        if (exists) plain = plain && at(A, c) != 0.0f && fabsf(at(H, c)) < kInf;
-        own[c] = exists ? Stretch{resets ? __int_as_float(0x7fffffff) : at(A, c), at(H, c)} : Stretch{1.0f, 0.0f};
+    if (!me.second) {
+        A.y = 1.0f;
+        H.y = 0.0f;
+        if (!me.live) {
+            A.x = 1.0f;
+            H.x = 0.0f;
+            return true;
+        }
     }
-    return plain;
+    return whole && fminf(fabsf(A.x), fabsf(A.y)) > 0.0f && fabsf(H.x) < kInf && fabsf(H.y) < kInf;
 }
 
 // Each sweep is first written with products and sums alone: w h + v, and a reset's state of 0 by a select
 // where a warp has any.  That is right unless a weight is 0 (then the product A is, or may be) or a dropped
 // input is not finite (then H is not), or not every step exists; those lanes go the careful way.
 template <typename T, int N, bool SIG, bool WIDE, bool CLUSTER, int ST>
-__global__ void __launch_bounds__(kWarps * 32, 2) k_scan_fwd(ScanArgs s, unsigned ctiles, unsigned csize, int times)
+__global__ void __launch_bounds__(kWarps * 32, FLB) k_scan_fwd(ScanArgs s, unsigned ctiles, unsigned csize, int times)
 {
     extern __shared__ __align__(16) unsigned char dyn[];
-    constexpr int AHEAD = CLUSTER ? ST - 2 : ST - 1;   // with a cluster the tile before is still read
+    constexpr int AHEAD = ST - 1;   // a tile's place is free after its first sweep
     typedef Ring<T, N, 2, ST, WIDE> R;
     const Place<N> me(s, ctiles, csize, times);
     const R ring{dyn + (threadIdx.x >> 5) * R::BYTES};
@@ -491,115 +562,110 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_scan_fwd(ScanArgs s, unsigne
         copies_commit();
     };
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k) request(k);
+    for (int k = 0; k < ST; ++k) request(k);
     unsigned resets = reset_bits<N>(s, me.b, me.t0);
     joints.state = first_state(s.h0, s, me);
     joints.begin(dyn + (blockDim.x >> 5) * R::BYTES, me.strip, times, me.time, csize, me.rank);
-    const bool both = WIDE && me.second;
 
-    auto first = [&](int k, Held &h) {
+    typedef Held<N, N> Tile;
+    auto first = [&](int k, Tile &h) {
         const long long t = me.t0 + k * me.span + me.off;
-        copies_wait<CLUSTER ? AHEAD - 1 : AHEAD>();
+        copies_wait<AHEAD>();
         __syncwarp();
-        if (CLUSTER) request(k + AHEAD);   // (the place was last read before this warp's last shuffles)
         h.resets = resets;
         F2 A{1.0f, 1.0f}, H{0.0f, 0.0f};
         auto run = [&](auto any) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                F2 w = ring.read(k, 0, i), v = ring.read(k, 1, i);
+                h.w[i] = ring.read(k, 0, i);
+                h.v[i] = ring.read(k, 1, i);
                 if (SIG) {
                     F2 c;
-                    gates(w, w, c);
-                    v = v * c;
+                    gates(h.w[i], h.w[i], c);
+                    h.v[i] = h.v[i] * c;
                 }
                 if (any.value && resets >> i & 1u) H = {0.0f, 0.0f};
-                H = fma2(w, H, v);
-                A = A * w;
+                H = fma2(h.w[i], H, h.v[i]);
+                A = A * h.w[i];
             }
         };
         h.any = __any_sync(kFull, resets != 0);
         if (h.any) run(std::true_type());
         else run(std::false_type());
         Stretch own[2];
-        h.plain = settle(own, A, H, resets, me, t + N <= s.steps);
+        h.plain = settle(A, H, me, t + N <= s.steps);
         if (!h.plain) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 own[c] = {1.0f, 0.0f};
                 bool drop = false;
-#pragma unroll 1
+#pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    if (!((c ? me.second : me.live) && t + i < s.steps)) break;   // past the end the state stays
-                    const Gate g = gate<SIG>(at(ring.read(k, 0, i), c));
-                    const float x1 = at(ring.read(k, 1, i), c), w = resets >> i & 1u ? 0.0f : g.w;
+                    float w = 1.0f, v = 0.0f;   // past the end the state stays
+                    if ((c ? me.second : me.live) && t + i < s.steps) {
+                        const Gate g = gate<SIG>(at(ring.read(k, 0, i), c));
+                        v = at(ring.read(k, 1, i), c);
+                        v = SIG ? weigh(g.v, v, 0.0f) : v;
+                        w = resets >> i & 1u ? 0.0f : g.w;
+                    }
+                    at(h.w[i], c) = w;
+                    at(h.v[i], c) = v;
                     drop = drop || w == 0.0f;
-                    own[c].H = weigh(w, own[c].H, SIG ? weigh(g.v, x1, 0.0f) : x1);
+                    own[c].H = weigh(w, own[c].H, v);
                     own[c].A *= w;
                 }
                 own[c].A = drop ? __int_as_float(0x7fffffff) : nonzero(own[c].A);
             }
+        } else {
+            const float nan = __int_as_float(0x7fffffff);
+            own[0] = {resets && me.live ? nan : A.x, H.x};
+            own[1] = {resets && me.second ? nan : A.y, H.y};
         }
-        joints.first(k, own, h.before, h.all);
+        joints.first(k, h.plain, A, H, resets != 0, own, h.before, h.all);
+        __syncwarp();   // every lane has read the tile
+        request(k + ST);
         resets = reset_bits<N>(s, me.b, t - me.off + me.span);
     };
-    auto second = [&](int k, const Held &h) {
+    auto second = [&](int k, const Tile &h) {
         const long long t = me.t0 + k * me.span + me.off;
         F2 st = joints.second(k, h.before, h.all);
-        T *o = out + t * s.sh[1];
-        if (h.plain) {
+        const long long stride = s.sh[1];
+        T *o = out + t * stride;
+        if (!me.live) {
+            // nothing to store
+        } else if (h.plain) {
             auto run = [&](auto any) {
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    F2 w = ring.read(k, 0, i), v = ring.read(k, 1, i);
-                    if (SIG) {
-                        F2 c;
-                        gates(w, w, c);
-                        v = v * c;
-                    }
                     if (any.value && h.resets >> i & 1u) st = {0.0f, 0.0f};
-                    st = fma2(w, st, v);
-                    if (me.live) store2(o, st, both, me.second);
-                    o += s.sh[1];
+                    st = fma2(h.w[i], st, h.v[i]);
+                    store2<T, WIDE>(o + i * stride, st, me.second);
                 }
             };
             if (h.any) run(std::true_type());
             else run(std::false_type());
         } else {
-#pragma unroll 1
-            for (int i = 0; i < N; ++i) {
-                if (!(me.live && t + i < s.steps)) break;
-                const F2 ra = ring.read(k, 0, i), rx = ring.read(k, 1, i);
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const Gate g = gate<SIG>(at(ra, c));
-                    at(st, c) = weigh(h.resets >> i & 1u ? 0.0f : g.w, at(st, c), SIG ? weigh(g.v, at(rx, c), 0.0f) : at(rx, c));
-                }
-                store2(o, st, both, me.second);
+            for (int i = 0; i < N; ++i) {
+                st = {weigh(h.w[i].x, st.x, h.v[i].x), weigh(h.w[i].y, st.y, h.v[i].y)};
+                if (me.live && t + i < s.steps) store2<T, WIDE>(o, st, me.second);
                 o += s.sh[1];
             }
         }
-        if (!CLUSTER) {
-            __syncwarp();   // every lane has read the tile
-            request(k + ST);
-        }
     };
     if constexpr (CLUSTER) {
-        Held h0, h1;
-        first(0, h0);
-        for (int k = 1; k < me.rounds; k += 2) {
-            first(k, h1);
-            second(k - 1, h0);
-            if (k + 1 < me.rounds) {
-                first(k + 1, h0);
-                second(k, h1);
-            }
+        // (two copies of each sweep, no more: the code has to stay in the caches)
+        Tile h0, h1;
+        for (int k = 0;; k += 2) {
+            if (k < me.rounds) first(k, h0);
+            if (k > 0) second(k - 1, h1);
+            if (k >= me.rounds) break;
+            if (k + 1 < me.rounds) first(k + 1, h1);
+            second(k, h0);
+            if (k + 1 >= me.rounds) break;
         }
-        if (me.rounds & 1) second(me.rounds - 1, h0);
-        else second(me.rounds - 1, h1);
     } else {
-        Held h;
-        request(ST - 1);
+        Tile h;
         for (int k = 0; k < me.rounds; ++k) {
             first(k, h);
             second(k, h);
@@ -612,11 +678,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_scan_fwd(ScanArgs s, unsigne
 // The gradient, on arrays turned so that step 0 is the last one forward; s.h is shifted by one step, so
 // that row t holds the state before that step (row steps - 1 is h0).
 template <typename T, int N, bool SIG, bool WIDE, bool CLUSTER, int ST>
-__global__ void __launch_bounds__(kWarps * 32, 2) k_scan_bwd(ScanArgs s, unsigned ctiles, unsigned csize, int times)
+__global__ void __launch_bounds__(kWarps * 32, BLB) k_scan_bwd(ScanArgs s, unsigned ctiles, unsigned csize, int times)
 {
     extern __shared__ __align__(16) unsigned char dyn[];
     constexpr int NA = SIG ? 4 : 3;
-    constexpr int AHEAD = CLUSTER ? ST - 2 : ST - 1;
+    constexpr int AHEAD = CLUSTER ? ST - 2 : ST - 1;   // with a cluster the tile before is still read
     typedef Ring<T, N, NA, ST, WIDE> R;
     const Place<N> me(s, ctiles, csize, times);
     const R ring{dyn + (threadIdx.x >> 5) * R::BYTES};
@@ -642,30 +708,35 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_scan_bwd(ScanArgs s, unsigne
     unsigned resets = reset_bits<N>(s, me.b, me.t0);
     joints.state = first_state(s.glast, s, me);
     joints.begin(dyn + (blockDim.x >> 5) * R::BYTES, me.strip, times, me.time, csize, me.rank);
-    const bool both = WIDE && me.second;
 
-    auto first = [&](int k, Held &d) {
+    typedef Held<N, SIG ? N : 1> Tile;
+    auto first = [&](int k, Tile &d) {
         const long long t = me.t0 + k * me.span + me.off;
         copies_wait<CLUSTER ? AHEAD - 1 : AHEAD>();
         __syncwarp();
-        if (CLUSTER) request(k + AHEAD);
+        if (CLUSTER) request(k + AHEAD);   // (the place was last read before this warp's last shuffles)
         d.resets = resets;
         F2 A{1.0f, 1.0f}, H{0.0f, 0.0f};
         auto run = [&](auto any) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                F2 w = ring.read(k, 0, i), v;
-                if (SIG) gates(w, w, v);
-                H = w * (H + ring.read(k, 1, i));
+                d.w[i] = ring.read(k, 0, i);
+                if constexpr (SIG) gates(d.w[i], d.w[i], d.v[i]);
+                H = d.w[i] * (H + ring.read(k, 1, i));
                 if (any.value && resets >> i & 1u) H = {0.0f, 0.0f};
-                A = A * w;
+                A = A * d.w[i];
             }
         };
         d.any = __any_sync(kFull, resets != 0);
         if (d.any) run(std::true_type());
         else run(std::false_type());
         Stretch own[2];
-        d.plain = settle(own, A, H, resets, me, t + N < s.steps);   // (row steps - 1 reads h0)
+        d.plain = settle(A, H, me, t + N < s.steps);   // (row steps - 1 reads h0)
+        if (d.plain) {
+            const float nan = __int_as_float(0x7fffffff);
+            own[0] = {resets && me.live ? nan : A.x, H.x};
+            own[1] = {resets && me.second ? nan : A.y, H.y};
+        }
         if (!d.plain) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -682,52 +753,47 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_scan_bwd(ScanArgs s, unsigne
                 own[c].A = drop ? __int_as_float(0x7fffffff) : nonzero(own[c].A);
             }
         }
-        joints.first(k, own, d.before, d.all);
+        joints.first(k, d.plain, A, H, resets != 0, own, d.before, d.all);
         resets = reset_bits<N>(s, me.b, t - me.off + me.span);
     };
-    auto second = [&](int k, const Held &d) {
+    auto second = [&](int k, const Tile &d) {
         const long long t = me.t0 + k * me.span + me.off;
         F2 c = joints.second(k, d.before, d.all);
         const F2 start = c;
-        T *oa = ga + t * s.sga[1], *ox = gx + t * s.sgx[1];
-        bool plain = d.plain;
-        if (plain) {
+        const long long stride_a = s.sga[1], stride_x = s.sgx[1];
+        T *oa = ga + t * stride_a, *ox = gx + t * stride_x;
+        bool plain = d.plain || !me.live;
+        if (plain && me.live) {
             F2 check{0.0f, 0.0f};   // NaN once a gradient is not finite: a slope of 0 may have to drop it
             auto run = [&](auto any) {
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
                     const bool reset = any.value && (d.resets >> i & 1u);
                     const F2 g = ring.read(k, 1, i) + c;
-                    F2 w = ring.read(k, 0, i), before = ring.read(k, 2, i), da, dx;
+                    F2 before = ring.read(k, 2, i), da, dx;
                     if (reset) before = {0.0f, 0.0f};
-                    if (SIG) {
-                        F2 v;
-                        gates(w, w, v);
-                        da = g * fma2(ring.read(k, 3, i), F2{-1.0f, -1.0f}, before) * (w * v);
-                        dx = g * v;
+                    if constexpr (SIG) {
+                        da = g * fma2(ring.read(k, 3, i), F2{-1.0f, -1.0f}, before) * (d.w[i] * d.v[i]);
+                        dx = g * d.v[i];
                         check = fma2(da, F2{0.0f, 0.0f}, check);
                     } else {
                         da = g * before;
                         dx = g;
                         if (reset) da = {0.0f, 0.0f};
                     }
-                    c = w * g;
+                    c = d.w[i] * g;
                     if (reset) c = {0.0f, 0.0f};
-                    if (ga && me.live) store2(oa, da, both, me.second);
-                    if (gx && me.live) store2(ox, dx, both, me.second);
-                    oa += s.sga[1];
-                    ox += s.sgx[1];
+                    if (ga) store2<T, WIDE>(oa + i * stride_a, da, me.second);
+                    if (gx) store2<T, WIDE>(ox + i * stride_x, dx, me.second);
                 }
             };
             if (d.any) run(std::true_type());
             else run(std::false_type());
-            plain = !SIG || !me.live || (check.x == 0.0f && (check.y == 0.0f || !me.second));
+            plain = !SIG || (check.x == 0.0f && (check.y == 0.0f || !me.second));
         }
         if (!plain) {
             const F2 h0 = first_state(s.h0, s, me);
             c = start;
-            oa = ga + t * s.sga[1];
-            ox = gx + t * s.sgx[1];
 #pragma unroll 1
             for (int i = 0; i < N; ++i) {
                 if (!(me.live && t + i < s.steps)) break;
@@ -750,8 +816,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_scan_bwd(ScanArgs s, unsigne
                     }
                     at(c, e) = weigh(reset ? 0.0f : f.w, g, 0.0f);
                 }
-                if (ga) store2(oa, da, both, me.second);
-                if (gx) store2(ox, dx, both, me.second);
+                if (ga) store2<T, WIDE>(oa, da, me.second);
+                if (gx) store2<T, WIDE>(ox, dx, me.second);
                 oa += s.sga[1];
                 ox += s.sgx[1];
             }
@@ -762,20 +828,17 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_scan_bwd(ScanArgs s, unsigne
         }
     };
     if constexpr (CLUSTER) {
-        Held h0, h1;
-        first(0, h0);
-        for (int k = 1; k < me.rounds; k += 2) {
-            first(k, h1);
-            second(k - 1, h0);
-            if (k + 1 < me.rounds) {
-                first(k + 1, h0);
-                second(k, h1);
-            }
+        Tile h0, h1;
+        for (int k = 0;; k += 2) {
+            if (k < me.rounds) first(k, h0);
+            if (k > 0) second(k - 1, h1);
+            if (k >= me.rounds) break;
+            if (k + 1 < me.rounds) first(k + 1, h1);
+            second(k, h0);
+            if (k + 1 >= me.rounds) break;
         }
-        if (me.rounds & 1) second(me.rounds - 1, h0);
-        else second(me.rounds - 1, h1);
     } else {
-        Held d;
+        Tile d;
         request(ST - 1);
         for (int k = 0; k < me.rounds; ++k) {
             first(k, d);
@@ -858,30 +921,6 @@ __global__ void __launch_bounds__(128) k_scan_few(ScanArgs s)
 
 // ---- launches --------------------------------------------------------------------------------
 
-#ifndef FST
-#define FST 2
-#endif
-#ifndef BST
-#define BST 2
-#endif
-#ifndef FN16
-#define FN16 16
-#endif
-#ifndef BN16
-#define BN16 16
-#endif
-#ifndef FN32
-#define FN32 8
-#endif
-#ifndef BN32
-#define BN32 8
-#endif
-#ifndef LATC
-#define LATC 2500
-#endif
-#ifndef MAXCL
-#define MAXCL 16
-#endif
 template <typename T, bool BACK>
 constexpr int lane_steps() { return sizeof(T) == 4 ? (BACK ? BN32 : FN32) : (BACK ? BN16 : FN16); }
 
@@ -894,7 +933,7 @@ struct Layout {
 
 template <typename T, bool SIG, bool WIDE, bool BACK, bool CLUSTER>
 struct Launch {
-    static constexpr int NA = BACK ? (SIG ? 4 : 3) : 2, ST = CLUSTER ? (BACK ? 3 : 4) : BACK ? BST : FST;
+    static constexpr int NA = BACK ? (SIG ? 4 : 3) : 2, ST = BACK ? (CLUSTER ? BST + 1 : BST) : FST;
     static constexpr int N = lane_steps<T, BACK>(), TILE = kGroups * N;
     static auto kernel()
     {
