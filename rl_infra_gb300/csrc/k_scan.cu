@@ -58,6 +58,15 @@ namespace {
 #ifndef MAXCL
 #define MAXCL 16
 #endif
+#ifndef CN16
+#define CN16 16
+#endif
+#ifndef CN32
+#define CN32 8
+#endif
+#ifndef CST
+#define CST 3
+#endif
 #ifndef FLB
 #define FLB 4
 #endif
@@ -246,7 +255,7 @@ __device__ __forceinline__ bool mbar_try(unsigned bar, unsigned parity)
 {
     unsigned ok;
     asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
                  "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
@@ -405,33 +414,16 @@ struct Joints {
                     in = state = {__int_as_float(0x7fffffff), __int_as_float(0x7fffffff)};
                 } else {
                     if (lane == 0 && time == 0) mbar_expect(b, csize * 128);   // for the round that uses it next
-                    // a group of lanes takes a run of the cluster's CTAs
-                    const unsigned run = (csize + 3) / 4, part = lane / 8;
                     const uint4 *from = slots + place * csize * 8 + lane % 8;
-                    Stretch sum[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}}, mine[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}}, next[2];
+                    F2 s = state;
 #pragma unroll 4
-                    for (unsigned i = 0; i < run; ++i) {
-                        const unsigned r = part * run + i;
-                        if (r >= csize) break;
-                        if (r == rank) {
-                            mine[0] = sum[0];
-                            mine[1] = sum[1];
-                        }
+                    for (unsigned r = 0; r < csize; ++r) {
+                        if (r == rank) in = s;
+                        Stretch next[2];
                         unpacked(from[r * 8], next);
-                        sum[0] = join(sum[0], next[0]);
-                        sum[1] = join(sum[1], next[1]);
-                    }
-                    F2 s = state, start = state;
-#pragma unroll
-                    for (unsigned p = 0; p < 4; ++p) {
-                        if (p == part) start = s;
-                        const Stretch r0 = shfl(sum[0], p * 8 + lane % 8), r1 = shfl(sum[1], p * 8 + lane % 8);
-                        s = {apply(r0, s.x), apply(r1, s.y)};
+                        s = {apply(next[0], s.x), apply(next[1], s.y)};
                     }
                     state = s;
-                    start = {apply(mine[0], start.x), apply(mine[1], start.y)};
-                    const unsigned lane0 = rank / run * 8 + lane % 8;
-                    in = {__shfl_sync(kFull, start.x, lane0), __shfl_sync(kFull, start.y, lane0)};
                 }
             }
             F2 s = in;
@@ -546,7 +538,11 @@ template <typename T, int N, bool SIG, bool WIDE, bool CLUSTER, int ST>
 __global__ void __launch_bounds__(kWarps * 32, FLB) k_scan_fwd(ScanArgs s, unsigned ctiles, unsigned csize, int times)
 {
     extern __shared__ __align__(16) unsigned char dyn[];
-    constexpr int AHEAD = ST - 1;   // a tile's place is free after its first sweep
+    // Alone, a warp keeps a tile's weights and inputs in registers from one sweep to the next, and the tile's place
+    // is free after the first.  With a cluster two tiles are under way, which would take too many: the second
+    // sweep works them out again.
+    constexpr bool HOLD = !CLUSTER;
+    constexpr int AHEAD = CLUSTER ? ST - 2 : ST - 1;
     typedef Ring<T, N, 2, ST, WIDE> R;
     const Place<N> me(s, ctiles, csize, times);
     const R ring{dyn + (threadIdx.x >> 5) * R::BYTES};
@@ -562,31 +558,50 @@ __global__ void __launch_bounds__(kWarps * 32, FLB) k_scan_fwd(ScanArgs s, unsig
         copies_commit();
     };
 #pragma unroll
-    for (int k = 0; k < ST; ++k) request(k);
+    for (int k = 0; k < (CLUSTER ? AHEAD : ST); ++k) request(k);
     unsigned resets = reset_bits<N>(s, me.b, me.t0);
     joints.state = first_state(s.h0, s, me);
     joints.begin(dyn + (blockDim.x >> 5) * R::BYTES, me.strip, times, me.time, csize, me.rank);
 
-    typedef Held<N, N> Tile;
+    typedef Held<HOLD ? N : 1, HOLD ? N : 1> Tile;
+    auto weights = [&](int k, int i, F2 &w, F2 &v) {
+        w = ring.read(k, 0, i);
+        v = ring.read(k, 1, i);
+        if constexpr (SIG) {
+            F2 c;
+            gates(w, w, c);
+            v = v * c;
+        }
+    };
+    // the same with care; past the end the state stays
+    auto weights_of = [&](int k, int i, int c, bool valid, bool reset, float &w, float &v) {
+        w = 1.0f;
+        v = 0.0f;
+        if (!valid) return;
+        const Gate g = gate<SIG>(at(ring.read(k, 0, i), c));
+        v = at(ring.read(k, 1, i), c);
+        v = SIG ? weigh(g.v, v, 0.0f) : v;
+        w = reset ? 0.0f : g.w;
+    };
     auto first = [&](int k, Tile &h) {
         const long long t = me.t0 + k * me.span + me.off;
-        copies_wait<AHEAD>();
+        copies_wait<CLUSTER ? AHEAD - 1 : AHEAD>();
         __syncwarp();
+        if (CLUSTER) request(k + AHEAD);   // (the place was last read before this warp's last shuffles)
         h.resets = resets;
         F2 A{1.0f, 1.0f}, H{0.0f, 0.0f};
         auto run = [&](auto any) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                h.w[i] = ring.read(k, 0, i);
-                h.v[i] = ring.read(k, 1, i);
-                if (SIG) {
-                    F2 c;
-                    gates(h.w[i], h.w[i], c);
-                    h.v[i] = h.v[i] * c;
+                F2 w, v;
+                weights(k, i, w, v);
+                if constexpr (HOLD) {
+                    h.w[i] = w;
+                    h.v[i] = v;
                 }
                 if (any.value && resets >> i & 1u) H = {0.0f, 0.0f};
-                H = fma2(h.w[i], H, h.v[i]);
-                A = A * h.w[i];
+                H = fma2(w, H, v);
+                A = A * w;
             }
         };
         h.any = __any_sync(kFull, resets != 0);
@@ -599,17 +614,14 @@ __global__ void __launch_bounds__(kWarps * 32, FLB) k_scan_fwd(ScanArgs s, unsig
             for (int c = 0; c < 2; ++c) {
                 own[c] = {1.0f, 0.0f};
                 bool drop = false;
-#pragma unroll
+#pragma unroll HOLD ? N : 1
                 for (int i = 0; i < N; ++i) {
-                    float w = 1.0f, v = 0.0f;   // past the end the state stays
-                    if ((c ? me.second : me.live) && t + i < s.steps) {
-                        const Gate g = gate<SIG>(at(ring.read(k, 0, i), c));
-                        v = at(ring.read(k, 1, i), c);
-                        v = SIG ? weigh(g.v, v, 0.0f) : v;
-                        w = resets >> i & 1u ? 0.0f : g.w;
+                    float w, v;
+                    weights_of(k, i, c, (c ? me.second : me.live) && t + i < s.steps, resets >> i & 1u, w, v);
+                    if constexpr (HOLD) {
+                        at(h.w[i], c) = w;
+                        at(h.v[i], c) = v;
                     }
-                    at(h.w[i], c) = w;
-                    at(h.v[i], c) = v;
                     drop = drop || w == 0.0f;
                     own[c].H = weigh(w, own[c].H, v);
                     own[c].A *= w;
@@ -622,8 +634,10 @@ __global__ void __launch_bounds__(kWarps * 32, FLB) k_scan_fwd(ScanArgs s, unsig
             own[1] = {resets && me.second ? nan : A.y, H.y};
         }
         joints.first(k, h.plain, A, H, resets != 0, own, h.before, h.all);
-        __syncwarp();   // every lane has read the tile
-        request(k + ST);
+        if (!CLUSTER) {
+            __syncwarp();   // every lane has read the tile
+            request(k + ST);
+        }
         resets = reset_bits<N>(s, me.b, t - me.off + me.span);
     };
     auto second = [&](int k, const Tile &h) {
@@ -637,32 +651,44 @@ __global__ void __launch_bounds__(kWarps * 32, FLB) k_scan_fwd(ScanArgs s, unsig
             auto run = [&](auto any) {
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
+                    F2 w, v;
+                    if constexpr (HOLD) {
+                        w = h.w[i];
+                        v = h.v[i];
+                    } else {
+                        weights(k, i, w, v);
+                    }
                     if (any.value && h.resets >> i & 1u) st = {0.0f, 0.0f};
-                    st = fma2(h.w[i], st, h.v[i]);
+                    st = fma2(w, st, v);
                     store2<T, WIDE>(o + i * stride, st, me.second);
                 }
             };
             if (h.any) run(std::true_type());
             else run(std::false_type());
         } else {
-#pragma unroll
+#pragma unroll HOLD ? N : 1
             for (int i = 0; i < N; ++i) {
-                st = {weigh(h.w[i].x, st.x, h.v[i].x), weigh(h.w[i].y, st.y, h.v[i].y)};
-                if (me.live && t + i < s.steps) store2<T, WIDE>(o, st, me.second);
-                o += s.sh[1];
+                if (t + i >= s.steps) break;
+                F2 w, v;
+                if constexpr (HOLD) {
+                    w = h.w[i];
+                    v = h.v[i];
+                } else {
+                    weights_of(k, i, 0, true, h.resets >> i & 1u, w.x, v.x);
+                    weights_of(k, i, 1, me.second, h.resets >> i & 1u, w.y, v.y);
+                }
+                st = {weigh(w.x, st.x, v.x), weigh(w.y, st.y, v.y)};
+                store2<T, WIDE>(o + i * stride, st, me.second);
             }
         }
     };
     if constexpr (CLUSTER) {
-        // (two copies of each sweep, no more: the code has to stay in the caches)
-        Tile h0, h1;
-        for (int k = 0;; k += 2) {
-            if (k < me.rounds) first(k, h0);
-            if (k > 0) second(k - 1, h1);
-            if (k >= me.rounds) break;
-            if (k + 1 < me.rounds) first(k + 1, h1);
-            second(k, h0);
-            if (k + 1 >= me.rounds) break;
+        // (one copy of each sweep: the code has to stay in the caches)
+        Tile now{}, before{};
+        for (int k = 0; k <= me.rounds; ++k) {
+            if (k < me.rounds) first(k, now);
+            if (k > 0) second(k - 1, before);
+            before = now;
         }
     } else {
         Tile h;
@@ -682,6 +708,7 @@ __global__ void __launch_bounds__(kWarps * 32, BLB) k_scan_bwd(ScanArgs s, unsig
 {
     extern __shared__ __align__(16) unsigned char dyn[];
     constexpr int NA = SIG ? 4 : 3;
+    constexpr bool HOLD = !CLUSTER;
     constexpr int AHEAD = CLUSTER ? ST - 2 : ST - 1;   // with a cluster the tile before is still read
     typedef Ring<T, N, NA, ST, WIDE> R;
     const Place<N> me(s, ctiles, csize, times);
@@ -709,7 +736,7 @@ __global__ void __launch_bounds__(kWarps * 32, BLB) k_scan_bwd(ScanArgs s, unsig
     joints.state = first_state(s.glast, s, me);
     joints.begin(dyn + (blockDim.x >> 5) * R::BYTES, me.strip, times, me.time, csize, me.rank);
 
-    typedef Held<N, SIG ? N : 1> Tile;
+    typedef Held<HOLD ? N : 1, HOLD && SIG ? N : 1> Tile;
     auto first = [&](int k, Tile &d) {
         const long long t = me.t0 + k * me.span + me.off;
         copies_wait<CLUSTER ? AHEAD - 1 : AHEAD>();
@@ -720,11 +747,13 @@ __global__ void __launch_bounds__(kWarps * 32, BLB) k_scan_bwd(ScanArgs s, unsig
         auto run = [&](auto any) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                d.w[i] = ring.read(k, 0, i);
-                if constexpr (SIG) gates(d.w[i], d.w[i], d.v[i]);
-                H = d.w[i] * (H + ring.read(k, 1, i));
+                F2 w = ring.read(k, 0, i), v;
+                if constexpr (SIG) gates(w, w, v);
+                if constexpr (HOLD) d.w[i] = w;
+                if constexpr (HOLD && SIG) d.v[i] = v;
+                H = w * (H + ring.read(k, 1, i));
                 if (any.value && resets >> i & 1u) H = {0.0f, 0.0f};
-                A = A * d.w[i];
+                A = A * w;
             }
         };
         d.any = __any_sync(kFull, resets != 0);
@@ -770,18 +799,25 @@ __global__ void __launch_bounds__(kWarps * 32, BLB) k_scan_bwd(ScanArgs s, unsig
                 for (int i = 0; i < N; ++i) {
                     const bool reset = any.value && (d.resets >> i & 1u);
                     const F2 g = ring.read(k, 1, i) + c;
-                    F2 before = ring.read(k, 2, i), da, dx;
+                    F2 before = ring.read(k, 2, i), da, dx, w, v;
+                    if constexpr (HOLD) {
+                        w = d.w[i];
+                        if constexpr (SIG) v = d.v[i];
+                    } else {
+                        w = ring.read(k, 0, i);
+                        if constexpr (SIG) gates(w, w, v);
+                    }
                     if (reset) before = {0.0f, 0.0f};
                     if constexpr (SIG) {
-                        da = g * fma2(ring.read(k, 3, i), F2{-1.0f, -1.0f}, before) * (d.w[i] * d.v[i]);
-                        dx = g * d.v[i];
+                        da = g * fma2(ring.read(k, 3, i), F2{-1.0f, -1.0f}, before) * (w * v);
+                        dx = g * v;
                         check = fma2(da, F2{0.0f, 0.0f}, check);
                     } else {
                         da = g * before;
                         dx = g;
                         if (reset) da = {0.0f, 0.0f};
                     }
-                    c = d.w[i] * g;
+                    c = w * g;
                     if (reset) c = {0.0f, 0.0f};
                     if (ga) store2<T, WIDE>(oa + i * stride_a, da, me.second);
                     if (gx) store2<T, WIDE>(ox + i * stride_x, dx, me.second);
@@ -828,14 +864,11 @@ __global__ void __launch_bounds__(kWarps * 32, BLB) k_scan_bwd(ScanArgs s, unsig
         }
     };
     if constexpr (CLUSTER) {
-        Tile h0, h1;
-        for (int k = 0;; k += 2) {
-            if (k < me.rounds) first(k, h0);
-            if (k > 0) second(k - 1, h1);
-            if (k >= me.rounds) break;
-            if (k + 1 < me.rounds) first(k + 1, h1);
-            second(k, h0);
-            if (k + 1 >= me.rounds) break;
+        Tile now{}, before{};
+        for (int k = 0; k <= me.rounds; ++k) {
+            if (k < me.rounds) first(k, now);
+            if (k > 0) second(k - 1, before);
+            before = now;
         }
     } else {
         Tile d;
@@ -921,8 +954,8 @@ __global__ void __launch_bounds__(128) k_scan_few(ScanArgs s)
 
 // ---- launches --------------------------------------------------------------------------------
 
-template <typename T, bool BACK>
-constexpr int lane_steps() { return sizeof(T) == 4 ? (BACK ? BN32 : FN32) : (BACK ? BN16 : FN16); }
+template <typename T, bool BACK, bool CLUSTER>
+constexpr int lane_steps() { return CLUSTER ? (sizeof(T) == 4 ? CN32 : CN16) : sizeof(T) == 4 ? (BACK ? BN32 : FN32) : (BACK ? BN16 : FN16); }
 
 // How a pass is laid out: a CTA of `strips` x `times` warps, clusters of csize CTAs.
 struct Layout {
@@ -933,8 +966,8 @@ struct Layout {
 
 template <typename T, bool SIG, bool WIDE, bool BACK, bool CLUSTER>
 struct Launch {
-    static constexpr int NA = BACK ? (SIG ? 4 : 3) : 2, ST = BACK ? (CLUSTER ? BST + 1 : BST) : FST;
-    static constexpr int N = lane_steps<T, BACK>(), TILE = kGroups * N;
+    static constexpr int NA = BACK ? (SIG ? 4 : 3) : 2, ST = CLUSTER ? CST : BACK ? BST : FST;
+    static constexpr int N = lane_steps<T, BACK, CLUSTER>(), TILE = kGroups * N;
     static auto kernel()
     {
         if constexpr (BACK) return k_scan_bwd<T, N, SIG, WIDE, CLUSTER, ST>;
@@ -995,12 +1028,13 @@ cudaError_t launch_any(const ScanArgs &a, const DeviceInfo &dev, cudaStream_t st
     typedef Launch<T, SIG, WIDE, BACK, false> One;
     typedef Launch<T, SIG, WIDE, BACK, true> Many;
     const unsigned per_row = (a.channels + kStrip - 1) / kStrip;
-    const double warp_us = One::TILE * kStrip * sizeof(T) * (One::NA + (BACK ? 2 : 1)) / 44500.0;
+    constexpr double step_us = kStrip * sizeof(T) * (One::NA + (BACK ? 2 : 1)) / 44500.0;   // of a warp's strip
     Layout best{};
     double least = 1e30;
     for (int times = 1; times <= 4; times *= 2) {
         for (unsigned csize = 1; csize <= (times == 4 ? (unsigned)MAXCL : 1u); csize *= 2) {
-            const long long span = (long long)One::TILE * times * csize;
+            const int tile = csize > 1 ? Many::TILE : One::TILE;
+            const long long span = (long long)tile * times * csize;
             if (times * csize > 1 && span / 2 >= a.steps) continue;   // some would have no tile
             Layout l{1, times, csize};
             while (l.strips * 2 * times <= 4 && (unsigned)l.strips < per_row) l.strips *= 2;
@@ -1010,7 +1044,7 @@ cudaError_t launch_any(const ScanArgs &a, const DeviceInfo &dev, cudaStream_t st
             const double ctas = (double)((per_row + l.strips - 1) / l.strips) * a.batch * csize;
             const double alone = csize > 1 ? LATC / 1000.0 : times > 1 ? 1.0 : 0.8;
             const double full = std::floor(ctas / fit), rest = ctas - full * fit;
-            auto round = [&](double n) { return std::max(alone, n / dev.sms * l.warps() * warp_us); };
+            auto round = [&](double n) { return std::max(alone, n / dev.sms * l.warps() * tile * step_us); };
             const double us = std::ceil((double)a.steps / span) * (full * round(fit) + (rest > 0 ? round(rest) : 0.0));
             if (us < least) {
                 least = us;
