@@ -8,15 +8,16 @@
 //   loss = tau sum_k q_k ((t_k - L) - (x_k - lse)),  grad_j = s_n tau (S p_j - q_j).
 // Sums and normalisers are binary32; the gradient is rounded once.
 //
-// Work.  A row is split over a cluster of 1 to 8 CTAs.  Each CTA's loader warps read their part of the
-// row once, keep the running (m, s) and, where the gradient is wanted in the same pass, put the raw
-// part into shared memory; the CTAs exchange (m, s) through distributed shared memory (one hardware
-// barrier), then turn their part of shared memory into the gradient.  Every access to memory is 16 bytes
-// on a 16-byte boundary but for a row's ends: a row that starts elsewhere (an odd vocabulary) is
-// shifted into place between neighbouring lanes, so a row is summed in the same order, and gives the same
-// bits, wherever it lies.  So the step reads the logits once and writes the gradient once, which
-// is its bound (HBM).  One more warp of each CTA handles the teacher's entries meanwhile; their q is
-// taken off the gradient by a second write to those places after the CTA's barrier.
+// Work.  A row is split over a cluster of 1 to 8 CTAs.  Each CTA's loader warps copy their part of the
+// row into shared memory (cp.async, several batches ahead: as many bytes in flight as the part has),
+// keep the running (m, s) of what has arrived, exchange (m, s) with the row's other CTAs through
+// distributed shared memory (one hardware barrier), and turn the part into the gradient on its way
+// out.  So the step reads the logits once and writes the gradient once, which is its bound (HBM); three CTAs
+// an SM are in different phases.  One more warp of each CTA handles the teacher's entries meanwhile; their q
+// is taken off the gradient by a second write to those places after the CTA's barrier.  Every access to
+// memory is 16 bytes on a 16-byte boundary but for a row's ends: a row that starts elsewhere (an odd
+// vocabulary) is shifted into place between neighbouring lanes, so a row is summed in the same order, and
+// gives the same bits, wherever it lies.
 #include "ops_internal.cuh"
 
 #include <algorithm>
@@ -40,7 +41,11 @@ constexpr int kMaxCluster = 8;
 #define DP 64
 #endif
 constexpr int kMaxWarps = DW;    // loader warps of a CTA at most
-constexpr int kUnroll = 4;       // 16-byte loads a loader thread has in flight
+constexpr int kUnroll = 4;       // pieces of 16 bytes a loader thread takes at a time
+#ifndef DA
+#define DA 2
+#endif
+constexpr int kAhead = DA;        // batches of them that are requested before they are used
 constexpr float kInf = __builtin_huge_valf();
 
 struct RowSum {
@@ -56,6 +61,11 @@ __device__ __forceinline__ RowSum join(RowSum a, RowSum b, float c)
     const float e = finite_or_zero(r.m);
     r.s = a.s * ex2((a.m - e) * c) + b.s * ex2((b.m - e) * c);
     return r;
+}
+
+__device__ __forceinline__ void copy16(void *smem, const void *global)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(smem)), "l"(global) : "memory");
 }
 
 // A thread's running maximum and sums of two lanes of pairs, rescaled where the maximum rises.
@@ -181,14 +191,18 @@ struct Pieces {
     }
     __device__ __forceinline__ Pack<T> get(int i, int j) const
     {
-        Pack<T> r = shifted(i);
+        const Pack<T> r = shifted(i);
         const int first = j - before();
-        if (!(whole(first) && (!off || whole(first + P)))) {
-            float f[P];
+        return whole(first) && (!off || whole(first + P)) ? r : ragged(j);
+    }
+    // element by element
+    __device__ __forceinline__ Pack<T> ragged(int j) const
+    {
+        float f[P];
 #pragma unroll
-            for (int e = 0; e < P; ++e) f[e] = j + e >= lo && j + e < hi ? to_f32(p[j + e]) : -kInf;
-            r.pack(f);   // exact: the values came from T
-        }
+        for (int e = 0; e < P; ++e) f[e] = j + e >= lo && j + e < hi ? to_f32(p[j + e]) : -kInf;
+        Pack<T> r;
+        r.pack(f);   // exact: the values came from T
         return r;
     }
     static __device__ __forceinline__ Pack<T> nothing()
@@ -209,6 +223,16 @@ struct FromShared {
     __device__ __forceinline__ uint4 operator()(const void *p) const { return *static_cast<const uint4 *>(p); }
 };
 
+// The join of n stretches: the largest maximum first, then the rescaled sums in their order.
+__device__ __forceinline__ RowSum gather(const RowSum *p, int n, float c)
+{
+    RowSum r{-kInf, 0.0f};
+    for (int i = 0; i < n; ++i) r.m = fmaxf(r.m, p[i].m);
+    const float e = finite_or_zero(r.m);
+    for (int i = 0; i < n; ++i) r.s += p[i].s * ex2((p[i].m - e) * c);
+    return r;
+}
+
 // Shared memory of a CTA: the part of the row (step only), then the teacher's entries.
 struct Shared {
     RowSum cluster[kMaxCluster];
@@ -226,8 +250,8 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, DM) k_distill(DistillArg
     constexpr int P = Pack<T>::N;
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ Shared sh;
-    uint4 *part = reinterpret_cast<uint4 *>(dyn);                       // [per_cta] (step)
-    float *q = reinterpret_cast<float *>(dyn + (PART == kDistillStep ? (size_t)per_cta * 16 : 0));   // [K]
+    uint4 *part = reinterpret_cast<uint4 *>(dyn);                       // [per_cta]
+    float *q = reinterpret_cast<float *>(dyn + (size_t)per_cta * 16);   // [K]
     float *d = q + a.k;                                                 // [K] t - L
     float *xk = d + a.k;                                                // [K] the student's logits there
     int *at = reinterpret_cast<int *>(xk + a.k);                        // [K] place, -1: left out
@@ -266,10 +290,8 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, DM) k_distill(DistillArg
             }
             at[k] = (int)i;
             d[k] = v;
-            // the loss needs every entry's logit (first CTA), the gradient those of its own part
-            const bool mine = i >= j0 && i < j1;
-            xk[k] = i >= 0 && (PART == kDistillBackward ? mine : PART == kDistillStep ? rank == 0 || mine : rank == 0)
-                        ? to_f32(x[i]) : 0.0f;
+            // (the loss needs every entry's logit, the gradient those of the CTA's own part, which it holds)
+            if (PART != kDistillBackward && rank == 0) xk[k] = i >= 0 ? to_f32(x[i]) : 0.0f;
             tm = fmaxf(tm, v);
         }
         for (int o = 16; o; o >>= 1) tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, o));
@@ -311,57 +333,95 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, DM) k_distill(DistillArg
             sh.some = !(S == 0.0f);
             sh.repeated = repeated;
         }
-    } else if (PART != kDistillBackward) {
-        // ---- this CTA's part of the row --------------------------------------------------------
-        const int hi = min((int)a.vocab, j1 + P);   // (the last piece of the part may need the block behind it)
-        Pieces<T, FromGlobal> from(x, 0, hi, 0, FromGlobal());
+    } else {
+        // ---- this CTA's part of the row: pieces v + i loaders + lane of each batch ------------------
         Running<T> run;
-        for (unsigned v = v0 + (t & ~31); v < v1; v += loaders * kUnroll) {
-            Pack<T> in[kUnroll];
-            const unsigned last = v + (kUnroll - 1) * loaders + 31;
-            if (last < v1 && from.whole_blocks((int)(v * P), (int)(last * P))) {
-                from.request_all(v + lane, loaders);
-#pragma unroll
-                for (int i = 0; i < kUnroll; ++i) {
-                    in[i] = from.shifted(i);
-                    if (PART == kDistillStep) part[v + i * loaders + lane - v0] = in[i].raw;
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < kUnroll; ++i) from.request(i, (int)((v + i * loaders + lane) * P));
+        const unsigned base = v0 + (t & ~31), step = loaders * kUnroll;
+        Pieces<T, FromGlobal> from(x, 0, min((int)a.vocab, j1 + P), 0, FromGlobal());   // (the last may need the block behind it)
+        if (from.off == 0) {
+            auto request = [&](unsigned v) {
 #pragma unroll
                 for (int i = 0; i < kUnroll; ++i) {
                     const unsigned w = v + i * loaders + lane;
-                    in[i] = from.get(i, (int)(w * P));
-                    if (w >= v1) in[i] = from.nothing();
-                    else if (PART == kDistillStep) part[w - v0] = in[i].raw;
+                    if ((int)((w + 1) * P) <= j1) copy16(&part[w - v0], x + (size_t)w * P);
+                    else if (w < v1) part[w - v0] = from.ragged((int)(w * P)).raw;
                 }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            };
+#pragma unroll
+            for (int b = 0; b < kAhead; ++b) request(base + b * step);
+            for (unsigned v = base; v < v1; v += step) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+                if (PART != kDistillBackward) {
+                    Pack<T> in[kUnroll];
+                    if (v + (kUnroll - 1) * loaders + 31 < v1) {
+#pragma unroll
+                        for (int i = 0; i < kUnroll; ++i) in[i].raw = part[v + i * loaders + lane - v0];
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kUnroll; ++i) {
+                            const unsigned w = v + i * loaders + lane;
+                            if (w < v1) in[i].raw = part[w - v0];
+                            else in[i] = from.nothing();
+                        }
+                    }
+                    run.add(in, c);
+                }
+                request(v + kAhead * step);
             }
-            run.add(in, c);
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+        } else {
+            for (unsigned v = base; v < v1; v += step) {
+                Pack<T> in[kUnroll];
+                const unsigned last = v + (kUnroll - 1) * loaders + 31;
+                if (last < v1 && from.whole_blocks((int)(v * P), (int)(last * P))) {
+                    from.request_all(v + lane, loaders);
+#pragma unroll
+                    for (int i = 0; i < kUnroll; ++i) {
+                        in[i] = from.shifted(i);
+                        part[v + i * loaders + lane - v0] = in[i].raw;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kUnroll; ++i) from.request(i, (int)((v + i * loaders + lane) * P));
+#pragma unroll
+                    for (int i = 0; i < kUnroll; ++i) {
+                        const unsigned w = v + i * loaders + lane;
+                        in[i] = from.get(i, (int)(w * P));
+                        if (w >= v1) in[i] = from.nothing();
+                        else part[w - v0] = in[i].raw;
+                    }
+                }
+                if (PART != kDistillBackward) run.add(in, c);
+            }
         }
-        own = run.sum();
-        for (int o = 16; o; o >>= 1) {
-            RowSum other{__shfl_xor_sync(0xffffffffu, own.m, o), __shfl_xor_sync(0xffffffffu, own.s, o)};
-            // the lower lane's stretch first, so that both lanes get the same bits
-            own = (lane & o) ? join(other, own, c) : join(own, other, c);
+        if (PART != kDistillBackward) {
+            own = run.sum();
+            for (int o = 16; o; o >>= 1) {
+                RowSum other{__shfl_xor_sync(0xffffffffu, own.m, o), __shfl_xor_sync(0xffffffffu, own.s, o)};
+                // the lower lane's stretch first, so that both lanes get the same bits
+                own = (lane & o) ? join(other, own, c) : join(own, other, c);
+            }
+            if (lane == 0) sh.warp[t >> 5] = own;
         }
-        if (lane == 0) sh.warp[t >> 5] = own;
     }
     __syncthreads();
     float lse;
     RowSum all{-kInf, 0.0f};
     if (PART != kDistillBackward) {
-        for (int w = 0; w < loaders / 32; ++w) all = join(all, sh.warp[w], c);
-        if (csize > 1) {
+        const int warps = loaders / 32;
+        if (csize == 1) {
+            all = gather(sh.warp, warps, c);
+        } else {
             cluster_wait_acquire();   // every CTA of the row has started
             if (t < (int)csize) {
+                all = gather(sh.warp, warps, c);
                 const unsigned to = cluster_smem_addr(&sh.cluster[rank], t);
                 st_cluster_f32(to, all.m);
                 st_cluster_f32(to + 4, all.s);
             }
             cluster_sync_all();
-            all = sh.cluster[0];
-            for (unsigned r = 1; r < csize; ++r) all = join(all, sh.cluster[r], c);
+            all = gather(sh.cluster, (int)csize, c);
         }
         lse = all.s == 0.0f ? -kInf : finite_or_zero(all.m) + a.tau * logf(all.s);
         if (rank == 0 && t >= loaders) {
@@ -389,58 +449,69 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, DM) k_distill(DistillArg
     // element by element
     const int misg = (int)(reinterpret_cast<uintptr_t>(out) % 16 / sizeof(T));
     if (t < loaders && j0 < j1) {
-        const int o0 = (j0 + misg) / P, o1 = (j1 - 1 + misg) / P + 1;
+        const int o0 = (j0 + misg) / P, o1 = (j1 - 1 + misg) / P + 1, first = o0 + (t & ~31), step = loaders * kUnroll;
         const F2 ref{-lse, -lse}, cc{c, c}, ff{f0, f0};
-        auto write = [&](auto &from) {
-            for (int v = o0 + (t & ~31); v < o1; v += loaders * kUnroll) {
+        Pieces<T, FromShared> from(reinterpret_cast<const T *>(part) - j0, j0, j1, o0 * P - misg, FromShared());
+        auto turn = [&](Pack<T> &in) {
+            float f[P];
+            in.unpack(f);
+#pragma unroll
+            for (int e = 0; e < P; e += 2) {
+                const F2 x = (F2{f[e], f[e + 1]} + ref) * cc;
+                const F2 y = F2{ex2(x.x), ex2(x.y)} * ff;
+                f[e] = y.x;
+                f[e + 1] = y.y;
+            }
+            in.pack(f);
+        };
+        auto ragged = [&](int j, Pack<T> in) {   // the ends of the part
+            float f[P];
+            in.unpack(f);
+#pragma unroll
+            for (int e = 0; e < P; ++e)
+                if (j + e >= j0 && j + e < j1) out[j + e] = from_f32<T>(f[e]);   // exact
+        };
+        if (!live) {
+            for (int v = first; v < o1; v += loaders) {
+                const int j = (v + lane) * P - misg;
+                Pack<T> zero;
+                zero.raw = make_uint4(0, 0, 0, 0);
+                if (j >= j0 && j + P <= j1) *reinterpret_cast<uint4 *>(out + j) = zero.raw;
+                else ragged(j, zero);
+            }
+        } else {
+            for (int v = first; v < o1; v += step) {
                 Pack<T> in[kUnroll];
                 const int last = v + (kUnroll - 1) * loaders + 31;
-                const bool fast = v * P - misg >= j0 && (last + 1) * P - misg <= j1 &&
-                                  from.whole_blocks(v * P - misg, last * P - misg);
-                if (fast) {
-                    from.request_all(v + lane, loaders, -misg);
+                if (v * P - misg >= j0 && (last + 1) * P - misg <= j1 && from.whole_blocks(v * P - misg, last * P - misg)) {
+                    uint4 *to = reinterpret_cast<uint4 *>(out - misg) + v + lane;
+                    if (from.off == 0) {
+                        const uint4 *at = part + ((v + lane) - (j0 + misg) / P);
 #pragma unroll
-                    for (int i = 0; i < kUnroll; ++i) in[i] = from.shifted(i);
+                        for (int i = 0; i < kUnroll; ++i) in[i].raw = at[i * loaders];
+                    } else {
+                        from.request_all(v + lane, loaders, -misg);
+#pragma unroll
+                        for (int i = 0; i < kUnroll; ++i) in[i] = from.shifted(i);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kUnroll; ++i) {
+                        turn(in[i]);
+                        to[i * loaders] = in[i].raw;
+                    }
                 } else {
 #pragma unroll
                     for (int i = 0; i < kUnroll; ++i) from.request(i, (v + i * loaders + lane) * P - misg);
 #pragma unroll
-                    for (int i = 0; i < kUnroll; ++i) in[i] = from.get(i, (v + i * loaders + lane) * P - misg);
-                }
-#pragma unroll
-                for (int i = 0; i < kUnroll; ++i) {
-                    const int j = (v + i * loaders + lane) * P - misg;
-                    float f[P];
-                    in[i].unpack(f);
-#pragma unroll
-                    for (int e = 0; e < P; e += 2) {
-                        const F2 x = (F2{f[e], f[e + 1]} + ref) * cc;
-                        const F2 y = F2{ex2(x.x), ex2(x.y)} * ff;
-                        f[e] = y.x;
-                        f[e + 1] = y.y;
-                    }
-                    if (!live) {
-#pragma unroll
-                        for (int e = 0; e < P; ++e) f[e] = 0.0f;
-                    }
-                    if (fast || (j >= j0 && j + P <= j1)) {
-                        in[i].pack(f);
-                        *reinterpret_cast<uint4 *>(out + j) = in[i].raw;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < P; ++e)
-                            if (j + e >= j0 && j + e < j1) out[j + e] = from_f32<T>(f[e]);
+                    for (int i = 0; i < kUnroll; ++i) {
+                        const int j = (v + i * loaders + lane) * P - misg;
+                        in[i] = from.get(i, j);
+                        turn(in[i]);
+                        if (j >= j0 && j + P <= j1) *reinterpret_cast<uint4 *>(out + j) = in[i].raw;
+                        else ragged(j, in[i]);
                     }
                 }
             }
-        };
-        if (PART == kDistillStep) {
-            Pieces<T, FromShared> from(reinterpret_cast<const T *>(part) - j0, j0, j1, o0 * P - misg, FromShared());
-            write(from);
-        } else {
-            // in place, another CTA may be writing its part: nothing outside [j0, j1) is read
-            Pieces<T, FromGlobal> from(x, j0, j1, o0 * P - misg, FromGlobal());
-            write(from);
         }
     }
     if (!live) return;
@@ -459,7 +530,8 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, DM) k_distill(DistillArg
                 }
             if (!first) continue;
         }
-        out[p] = from_f32<T>(f0 * ex2((xk[k] - lse) * c) - g * sum);
+        const float v = to_f32(reinterpret_cast<const T *>(part)[p - j0]);
+        out[p] = from_f32<T>(f0 * ex2((v - lse) * c) - g * sum);
     }
 }
 
@@ -510,7 +582,7 @@ cudaError_t launch_t(DistillPart part, const DistillArgs &a, const DeviceInfo &d
         hash_size = 32;
         while (hash_size < 2 * a.k) hash_size *= 2;
     }
-    const size_t smem = (part == kDistillStep ? (size_t)per_cta * 16 : 0) + (size_t)a.k * 16 + (size_t)hash_size * 4;
+    const size_t smem = (size_t)per_cta * 16 + (size_t)a.k * 16 + (size_t)hash_size * 4;
     const unsigned grid = (unsigned)(a.rows * csize), block = (warps + 1) * 32;
     if (part == kDistillForward)
         return launch_clusters(k_distill<T, kDistillForward>, grid, block, csize, smem, st, a, csize, per_cta, hash_size);

@@ -23,6 +23,9 @@ namespace {
 typedef unsigned long long u64;
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
+#ifndef VF
+#define VF 8
+#endif
 constexpr int kMaxCluster = 8;
 constexpr int kUnroll = 4;   // 16-byte loads of each row that a lane has in flight
 
@@ -278,7 +281,7 @@ cudaError_t launch_t(const VerifyArgs &a, cudaStream_t st)
     // CTAs for a sequence: at least 512 pieces each (16 a lane of one warp); more, smaller CTAs also even out
     // the load over the SMs where there are many sequences
     unsigned csize = 1;
-    while (csize < kMaxCluster && pieces / csize > 1024) csize *= 2;
+    while (csize < kMaxCluster && pieces / csize > 1024 && (unsigned long long)a.batch * csize < VF * 152ull) csize *= 2;
     return launch_clusters(k_verify<T>, a.batch * csize, kThreads, csize, 0, st, a, csize, (pieces + csize - 1) / csize);
 }
 
