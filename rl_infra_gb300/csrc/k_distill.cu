@@ -339,12 +339,20 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, DM) k_distill(DistillArg
         const unsigned base = v0 + (t & ~31), step = loaders * kUnroll;
         Pieces<T, FromGlobal> from(x, 0, min((int)a.vocab, j1 + P), 0, FromGlobal());   // (the last may need the block behind it)
         if (from.off == 0) {
+            const unsigned inner = (kUnroll - 1) * loaders + 32;   // pieces from a warp's first to its last
             auto request = [&](unsigned v) {
+                if ((int)((v + inner) * P) <= j1) {
+                    uint4 *to = part + (v + lane - v0);
+                    const T *src = x + (size_t)(v + lane) * P;
 #pragma unroll
-                for (int i = 0; i < kUnroll; ++i) {
-                    const unsigned w = v + i * loaders + lane;
-                    if ((int)((w + 1) * P) <= j1) copy16(&part[w - v0], x + (size_t)w * P);
-                    else if (w < v1) part[w - v0] = from.ragged((int)(w * P)).raw;
+                    for (int i = 0; i < kUnroll; ++i) copy16(to + i * loaders, src + (size_t)(i * loaders) * P);
+                } else {
+#pragma unroll 1
+                    for (int i = 0; i < kUnroll; ++i) {
+                        const unsigned w = v + i * loaders + lane;
+                        if ((int)((w + 1) * P) <= j1) copy16(&part[w - v0], x + (size_t)w * P);
+                        else if (w < v1) part[w - v0] = from.ragged((int)(w * P)).raw;
+                    }
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
             };
@@ -354,18 +362,20 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, DM) k_distill(DistillArg
                 asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
                 if (PART != kDistillBackward) {
                     Pack<T> in[kUnroll];
-                    if (v + (kUnroll - 1) * loaders + 31 < v1) {
+                    if (v + inner <= v1) {
+                        const uint4 *at = part + (v + lane - v0);
 #pragma unroll
-                        for (int i = 0; i < kUnroll; ++i) in[i].raw = part[v + i * loaders + lane - v0];
+                        for (int i = 0; i < kUnroll; ++i) in[i].raw = at[i * loaders];
+                        run.add(in, c);
                     } else {
 #pragma unroll
                         for (int i = 0; i < kUnroll; ++i) {
                             const unsigned w = v + i * loaders + lane;
+                            in[i] = from.nothing();
                             if (w < v1) in[i].raw = part[w - v0];
-                            else in[i] = from.nothing();
                         }
+                        run.add(in, c);
                     }
-                    run.add(in, c);
                 }
                 request(v + kAhead * step);
             }
