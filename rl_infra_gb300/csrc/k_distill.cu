@@ -9,15 +9,16 @@
 // Sums and normalisers are binary32; the gradient is rounded once.
 //
 // Work.  A row is split over a cluster of 1 to 8 CTAs.  Each CTA's loader warps copy their part of the
-// row into shared memory (cp.async, several batches ahead: as many bytes in flight as the part has),
-// keep the running (m, s) of what has arrived, exchange (m, s) with the row's other CTAs through
+// row into shared memory (cp.async, batches ahead), keep the running (m, s) of what has arrived, exchange (m, s) with the row's other CTAs through
 // distributed shared memory (one hardware barrier), and turn the part into the gradient on its way
 // out.  So the step reads the logits once and writes the gradient once, which is its bound (HBM); three CTAs
 // an SM are in different phases.  One more warp of each CTA handles the teacher's entries meanwhile; their q
 // is taken off the gradient by a second write to those places after the CTA's barrier.  Every access to
-// memory is 16 bytes on a 16-byte boundary but for a row's ends: a row that starts elsewhere (an odd
-// vocabulary) is shifted into place between neighbouring lanes, so a row is summed in the same order, and
-// gives the same bits, wherever it lies.
+// memory is 16 bytes on a 16-byte boundary but for a row's ends; a row that starts elsewhere (an odd
+// vocabulary) keeps its place within the 16 bytes in shared memory and is shifted when it is read, so a row is
+// summed in the same order, and gives the same bits, wherever it lies.  (Clusters that stay for many rows and
+// load the next while they write this one were slower, 2.5 ms against 0.86 for 8192 rows of 131072: the
+// barrier between the CTAs then waits for the stores of the row before.)
 #include "ops_internal.cuh"
 
 #include <algorithm>
@@ -43,7 +44,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kMaxWarps = DW;    // loader warps of a CTA at most
 constexpr int kUnroll = 4;       // pieces of 16 bytes a loader thread takes at a time
 #ifndef DA
-#define DA 2
+#define DA 1
 #endif
 constexpr int kAhead = DA;        // batches of them that are requested before they are used
 constexpr float kInf = __builtin_huge_valf();
@@ -66,6 +67,30 @@ __device__ __forceinline__ RowSum join(RowSum a, RowSum b, float c)
 __device__ __forceinline__ void copy16(void *smem, const void *global)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(smem)), "l"(global) : "memory");
+}
+
+// what contributes nothing
+template <typename T>
+__device__ __forceinline__ Pack<T> nothing()
+{
+    float f[Pack<T>::N];
+#pragma unroll
+    for (int e = 0; e < Pack<T>::N; ++e) f[e] = -kInf;
+    Pack<T> r;
+    r.pack(f);
+    return r;
+}
+
+// the elements from j on that lie before `end`, element by element
+template <typename T>
+__device__ __forceinline__ Pack<T> ragged_end(const T *x, int j, int end)
+{
+    float f[Pack<T>::N];
+#pragma unroll
+    for (int e = 0; e < Pack<T>::N; ++e) f[e] = j + e < end ? to_f32(x[j + e]) : -kInf;
+    Pack<T> r;
+    r.pack(f);   // exact: the values came from T
+    return r;
 }
 
 // A thread's running maximum and sums of two lanes of pairs, rescaled where the maximum rises.
@@ -205,20 +230,8 @@ struct Pieces {
         r.pack(f);   // exact: the values came from T
         return r;
     }
-    static __device__ __forceinline__ Pack<T> nothing()
-    {
-        float f[P];
-#pragma unroll
-        for (int e = 0; e < P; ++e) f[e] = -kInf;
-        Pack<T> r;
-        r.pack(f);
-        return r;
-    }
 };
 
-struct FromGlobal {
-    __device__ __forceinline__ uint4 operator()(const void *p) const { return load_stream(p); }
-};
 struct FromShared {
     __device__ __forceinline__ uint4 operator()(const void *p) const { return *static_cast<const uint4 *>(p); }
 };
@@ -250,8 +263,8 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, DM) k_distill(DistillArg
     constexpr int P = Pack<T>::N;
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ Shared sh;
-    uint4 *part = reinterpret_cast<uint4 *>(dyn);                       // [per_cta]
-    float *q = reinterpret_cast<float *>(dyn + (size_t)per_cta * 16);   // [K]
+    uint4 *part = reinterpret_cast<uint4 *>(dyn);                             // [per_cta + 1]
+    float *q = reinterpret_cast<float *>(dyn + ((size_t)per_cta + 1) * 16);   // [K]
     float *d = q + a.k;                                                 // [K] t - L
     float *xk = d + a.k;                                                // [K] the student's logits there
     int *at = reinterpret_cast<int *>(xk + a.k);                        // [K] place, -1: left out
@@ -270,6 +283,10 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, DM) k_distill(DistillArg
     const unsigned pieces = (a.vocab + P - 1) / P;
     const unsigned v0 = min(rank * per_cta, pieces), v1 = min(v0 + per_cta, pieces);
     const int j0 = (int)(v0 * P), j1 = (int)min(v1 * P, a.vocab);
+
+    // element j of the part is cells[j]
+    const int mis = (int)(reinterpret_cast<uintptr_t>(x) % 16 / sizeof(T));
+    const T *cells = reinterpret_cast<const T *>(part) + mis - j0;
 
     RowSum own{-kInf, 0.0f};
     if (t >= loaders) {
@@ -337,9 +354,8 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, DM) k_distill(DistillArg
         // ---- this CTA's part of the row: pieces v + i loaders + lane of each batch ------------------
         Running<T> run;
         const unsigned base = v0 + (t & ~31), step = loaders * kUnroll;
-        Pieces<T, FromGlobal> from(x, 0, min((int)a.vocab, j1 + P), 0, FromGlobal());   // (the last may need the block behind it)
-        if (from.off == 0) {
-            const unsigned inner = (kUnroll - 1) * loaders + 32;   // pieces from a warp's first to its last
+        const unsigned inner = (kUnroll - 1) * loaders + 32;   // pieces from a warp's first to its last of a batch
+        if (mis == 0) {
             auto request = [&](unsigned v) {
                 if ((int)((v + inner) * P) <= j1) {
                     uint4 *to = part + (v + lane - v0);
@@ -351,7 +367,7 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, DM) k_distill(DistillArg
                     for (int i = 0; i < kUnroll; ++i) {
                         const unsigned w = v + i * loaders + lane;
                         if ((int)((w + 1) * P) <= j1) copy16(&part[w - v0], x + (size_t)w * P);
-                        else if (w < v1) part[w - v0] = from.ragged((int)(w * P)).raw;
+                        else if (w < v1) part[w - v0] = ragged_end(x, (int)(w * P), j1).raw;
                     }
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
@@ -371,7 +387,7 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, DM) k_distill(DistillArg
 #pragma unroll
                         for (int i = 0; i < kUnroll; ++i) {
                             const unsigned w = v + i * loaders + lane;
-                            in[i] = from.nothing();
+                            in[i] = nothing<T>();
                             if (w < v1) in[i].raw = part[w - v0];
                         }
                         run.add(in, c);
@@ -381,28 +397,41 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, DM) k_distill(DistillArg
             }
             asm volatile("cp.async.wait_group 0;" ::: "memory");
         } else {
-            for (unsigned v = base; v < v1; v += step) {
-                Pack<T> in[kUnroll];
-                const unsigned last = v + (kUnroll - 1) * loaders + 31;
-                if (last < v1 && from.whole_blocks((int)(v * P), (int)(last * P))) {
-                    from.request_all(v + lane, loaders);
-#pragma unroll
-                    for (int i = 0; i < kUnroll; ++i) {
-                        in[i] = from.shifted(i);
-                        part[v + i * loaders + lane - v0] = in[i].raw;
-                    }
+            // off a boundary: the blocks on boundaries that hold the part, each element as far from one as in
+            // memory; block w holds elements j0 - mis + w P and on.  Any thread's piece lies in two blocks, so
+            // all of them come first.
+            const T *src = x + (j0 - mis);
+            const int blocks = j0 < j1 ? (j1 - j0 + mis + P - 1) / P : 0;
+            const int lo = j0 == 0 ? 1 : 0, whole = min(blocks, ((int)a.vocab - j0 + mis) / P);   // the row's own
+            for (int w = t; w < blocks; w += loaders) {
+                if (w >= lo && w < whole) {
+                    copy16(&part[w], src + (size_t)w * P);
                 } else {
-#pragma unroll
-                    for (int i = 0; i < kUnroll; ++i) from.request(i, (int)((v + i * loaders + lane) * P));
-#pragma unroll
-                    for (int i = 0; i < kUnroll; ++i) {
-                        const unsigned w = v + i * loaders + lane;
-                        in[i] = from.get(i, (int)(w * P));
-                        if (w >= v1) in[i] = from.nothing();
-                        else part[w - v0] = in[i].raw;
+                    T *to = reinterpret_cast<T *>(&part[w]);
+#pragma unroll 1
+                    for (int e = 0; e < P; ++e) {
+                        const int j = j0 - mis + w * P + e;
+                        if (j >= j0 && j < j1) to[e] = x[j];
                     }
                 }
-                if (PART != kDistillBackward) run.add(in, c);
+            }
+            asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;\n\tbar.sync 1, %0;" ::"r"(loaders) : "memory");
+            if (PART != kDistillBackward) {
+                Pieces<T, FromShared> held(cells, j0, j1, j0, FromShared());
+                for (unsigned v = base; v < v1; v += step) {
+                    Pack<T> in[kUnroll];
+                    if ((int)((v + inner) * P) <= j1 && held.whole_blocks((int)(v * P), (int)((v + inner - 1) * P))) {
+                        held.request_all((int)v + lane, loaders);
+#pragma unroll
+                        for (int i = 0; i < kUnroll; ++i) in[i] = held.shifted(i);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kUnroll; ++i) held.request(i, (int)((v + i * loaders + lane) * P));
+#pragma unroll
+                        for (int i = 0; i < kUnroll; ++i) in[i] = held.get(i, (int)((v + i * loaders + lane) * P));
+                    }
+                    run.add(in, c);
+                }
             }
         }
         if (PART != kDistillBackward) {
@@ -461,7 +490,7 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, DM) k_distill(DistillArg
     if (t < loaders && j0 < j1) {
         const int o0 = (j0 + misg) / P, o1 = (j1 - 1 + misg) / P + 1, first = o0 + (t & ~31), step = loaders * kUnroll;
         const F2 ref{-lse, -lse}, cc{c, c}, ff{f0, f0};
-        Pieces<T, FromShared> from(reinterpret_cast<const T *>(part) - j0, j0, j1, o0 * P - misg, FromShared());
+        Pieces<T, FromShared> from(cells, j0, j1, o0 * P - misg, FromShared());
         auto turn = [&](Pack<T> &in) {
             float f[P];
             in.unpack(f);
@@ -496,7 +525,7 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, DM) k_distill(DistillArg
                 if (v * P - misg >= j0 && (last + 1) * P - misg <= j1 && from.whole_blocks(v * P - misg, last * P - misg)) {
                     uint4 *to = reinterpret_cast<uint4 *>(out - misg) + v + lane;
                     if (from.off == 0) {
-                        const uint4 *at = part + ((v + lane) - (j0 + misg) / P);
+                        const uint4 *at = reinterpret_cast<const uint4 *>(cells - misg) + v + lane;
 #pragma unroll
                         for (int i = 0; i < kUnroll; ++i) in[i].raw = at[i * loaders];
                     } else {
@@ -540,7 +569,7 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, DM) k_distill(DistillArg
                 }
             if (!first) continue;
         }
-        const float v = to_f32(reinterpret_cast<const T *>(part)[p - j0]);
+        const float v = to_f32(cells[p]);
         out[p] = from_f32<T>(f0 * ex2((v - lse) * c) - g * sum);
     }
 }
@@ -592,7 +621,7 @@ cudaError_t launch_t(DistillPart part, const DistillArgs &a, const DeviceInfo &d
         hash_size = 32;
         while (hash_size < 2 * a.k) hash_size *= 2;
     }
-    const size_t smem = (size_t)per_cta * 16 + (size_t)a.k * 16 + (size_t)hash_size * 4;
+    const size_t smem = ((size_t)per_cta + 1) * 16 + (size_t)a.k * 16 + (size_t)hash_size * 4;
     const unsigned grid = (unsigned)(a.rows * csize), block = (warps + 1) * 32;
     if (part == kDistillForward)
         return launch_clusters(k_distill<T, kDistillForward>, grid, block, csize, smem, st, a, csize, per_cta, hash_size);

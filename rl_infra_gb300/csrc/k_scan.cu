@@ -34,6 +34,9 @@ namespace gbper {
 
 namespace {
 
+#ifndef FEW
+#define FEW 4
+#endif
 #ifndef FST
 #define FST 2
 #endif
@@ -1067,7 +1070,7 @@ cudaError_t fwd_t(const ScanArgs &a, const DeviceInfo &dev, cudaStream_t st)
     constexpr unsigned e = sizeof(T), P = 16 / e;
     const bool wide = a.channels % P == 0 && aligned16(a.a, a.sa, a, e) && aligned16(a.x, a.sx, a, e) &&
                       aligned16(a.out_h, a.sh, a, e);
-    if (a.steps <= 4) {
+    if (a.steps <= FEW) {
         const unsigned long long threads = (unsigned long long)a.channels / (wide ? P : 1) * a.batch;
         const unsigned grid = (unsigned)((threads + 127) / 128);
         if (wide) return launch_clusters(k_scan_few<T, SIG, (int)P>, grid, 128, 1, 0, st, a);

@@ -49,11 +49,11 @@ def _arg(t, what, shape, dtype, dev):
     """Checks a tensor's place, type and shape; its innermost axis must be contiguous."""
     if not isinstance(t, torch.Tensor) or t.get_device() != dev:
         raise _bad(what, f"on cuda:{dev}", t)
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise _bad(what, f"of dtype {dtype}", t)
     if t.shape != shape:
         raise _bad(what, f"of shape {tuple(shape)}", t)
-    if shape[-1] > 1 and t.stride(-1) != 1:
+    if not t.is_contiguous() and shape[-1] > 1 and t.stride(-1) != 1:
         raise _bad(what, "contiguous in its last axis", t)
     return t.data_ptr()
 
@@ -113,11 +113,18 @@ class _On:
 
 
 def _elsewhere(stream, dev):
-    return stream is not None or dev != torch.cuda.current_device()
+    return stream is not None or dev != torch._C._cuda_getDevice()
 
 
-def _raw_stream(dev):
-    return torch._C._cuda_getCurrentRawStream(dev)
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+_lib = None
+
+
+def _library():
+    global _lib
+    if _lib is None:
+        _lib = capi.load()
+    return _lib
 
 
 def _check(status, name):
@@ -162,7 +169,7 @@ def distill_forward(logits, top_logits, top_idx, temperature=1.0, teacher_lse=No
             return distill_forward(logits, top_logits, top_idx, temperature, teacher_lse, out, status)
     loss = _given(out, "loss", (n,), torch.float32, dev, logits)
     lse = _given(out, "lse", (n,), torch.float32, dev, logits)
-    _check(capi.load().per_distill_forward(
+    _check(_library().per_distill_forward(
         _distill_shape(n, v, k, code, tcode, logits, top_logits, top_idx, v, temperature), logits.data_ptr(), tp,
         ip, lp, loss.data_ptr(), lse.data_ptr(), _status_ptr(status, dev), _raw_stream(dev)), "distill_forward")
     return {"loss": loss, "lse": lse}
@@ -182,7 +189,7 @@ def distill_backward(logits, top_logits, top_idx, lse, row_scale=None, temperatu
             return distill_backward(logits, top_logits, top_idx, lse, row_scale, temperature, teacher_lse, out,
                                     status)
     grad = _given(out, "grad", (n, v), logits.dtype, dev, logits)
-    _check(capi.load().per_distill_backward(
+    _check(_library().per_distill_backward(
         _distill_shape(n, v, k, code, tcode, logits, top_logits, top_idx, grad.stride(0), temperature),
         logits.data_ptr(), tp, ip, lp, ep, sp, grad.data_ptr(), _status_ptr(status, dev), _raw_stream(dev)),
         "distill_backward")
@@ -202,7 +209,7 @@ def distill_step(logits, top_logits, top_idx, row_scale=None, temperature=1.0, t
     loss = _given(out, "loss", (n,), torch.float32, dev, logits)
     lse = _given(out, "lse", (n,), torch.float32, dev, logits)
     grad = _given(out, "grad", (n, v), logits.dtype, dev, logits)
-    _check(capi.load().per_distill_step(
+    _check(_library().per_distill_step(
         _distill_shape(n, v, k, code, tcode, logits, top_logits, top_idx, grad.stride(0), temperature),
         logits.data_ptr(), tp, ip, lp, sp, loss.data_ptr(), lse.data_ptr(), grad.data_ptr(),
         _status_ptr(status, dev), _raw_stream(dev)), "distill_step")
@@ -266,7 +273,7 @@ def verify_draft(target_probs, draft_probs, draft_tokens, accept_u, sample_u, dr
         for name, t in got.items():
             if not t.is_contiguous():
                 raise _bad(name, "contiguous", t)
-    _check(capi.load().per_verify_draft(
+    _check(_library().per_verify_draft(
         _VERIFY.pack(b, d, v, code, target_probs.stride(0), target_probs.stride(1), q0, q1, draft_tokens.stride(0),
                      accept_u.stride(0), capi.PER_VERIFY_TOKENS64 if draft_tokens.dtype == torch.int64 else 0, 0),
         target_probs.data_ptr(), qp, tp, lp, up, sp, got["accepted"].data_ptr(), got["tokens"].data_ptr(),
@@ -317,7 +324,7 @@ def scan_forward(a, x, h0=None, resets=None, gate=GATE_DECAY, reverse=False, out
         _whole(last, "last", edge, torch.float32, dev)
     sa, sx, sh = a.stride(), x.stride(), h.stride()
     sr = resets.stride() if rp is not None else _NO_STRIDE
-    _check(capi.load().per_scan_forward(
+    _check(_library().per_scan_forward(
         _SCAN.pack(t, b, c, code, flags, sa[0], sa[1], sx[0], sx[1], sh[0], sh[1], 0, 0, 0, 0, 0, 0, sr[0], sr[1]),
         a.data_ptr(), xp, hp, rp, h.data_ptr(), last.data_ptr(), _raw_stream(dev)), "scan_forward")
     return {"h": h, "last": last}
@@ -341,7 +348,7 @@ def scan_step(a, x, state, resets=None, gate=GATE_DECAY, out=None, stream=None):
     new = _given(out, "state", a.shape, torch.float32, dev, a)
     if out is not None:
         _whole(new, "state", a.shape, torch.float32, dev)
-    _check(capi.load().per_scan_forward(
+    _check(_library().per_scan_forward(
         _SCAN.pack(1, b, c, code, flags, a.stride(0), 0, x.stride(0), 0, h.stride(0), 0, 0, 0, 0, 0, 0, 0,
                    resets.stride(0) if rp is not None else 0, 0),
         a.data_ptr(), xp, hp, rp, h.data_ptr(), new.data_ptr(), _raw_stream(dev)), "scan_step")
@@ -376,7 +383,7 @@ def scan_backward(a, x, h, grad_h, h0=None, resets=None, grad_last=None, gate=GA
         _whole(g0, "grad_h0", edge, torch.float32, dev)
     sa, sh, sg, sga, sgx = a.stride(), h.stride(), grad_h.stride(), ga.stride(), gx.stride()
     sr = resets.stride() if rp is not None else _NO_STRIDE
-    _check(capi.load().per_scan_backward(
+    _check(_library().per_scan_backward(
         _SCAN.pack(t, b, c, code, flags, sa[0], sa[1], sx[0], sx[1], sh[0], sh[1], sg[0], sg[1], sga[0], sga[1],
                    sgx[0], sgx[1], sr[0], sr[1]),
         a.data_ptr(), xp, yp, hp, rp, gp, lp, ga.data_ptr(), gx.data_ptr(), g0.data_ptr(), _raw_stream(dev)),
