@@ -34,48 +34,13 @@ namespace gbper {
 
 namespace {
 
-#ifndef FEW
-#define FEW 4
-#endif
-#ifndef FST
-#define FST 2
-#endif
-#ifndef BST
-#define BST 2
-#endif
-#ifndef FN16
-#define FN16 8
-#endif
-#ifndef BN16
-#define BN16 8
-#endif
-#ifndef FN32
-#define FN32 8
-#endif
-#ifndef BN32
-#define BN32 8
-#endif
-#ifndef LATC
-#define LATC 2500
-#endif
-#ifndef MAXCL
-#define MAXCL 16
-#endif
-#ifndef CN16
-#define CN16 16
-#endif
-#ifndef CN32
-#define CN32 8
-#endif
-#ifndef CST
-#define CST 3
-#endif
-#ifndef FLB
-#define FLB 4
-#endif
-#ifndef BLB
-#define BLB 4
-#endif
+// Steps of a lane in a tile and tiles in a ring, measured on 64 x 1024 x 1024 bf16 with sigmoid gates (forward,
+// gradient) and on one sequence of 65537 x 1024: 8 steps 83 and 183 us, 16 steps 99 and 199 (registers);
+// with a cluster, where the exchange is the larger part, 16 steps 141 us, 8 steps 149.  Rings of 2 tiles and
+// of 3 take the same time within 3%; in a cluster 3 (two under way, one arriving) 141 us, 4 165.
+constexpr int kLaneSteps = 8, kLaneStepsCluster16 = 16;
+constexpr int kRing = 2, kRingCluster = 3;
+constexpr int kCtasPerSm = 4;   // registers for 4 CTAs of 4 warps (128 each): 184 us against 248 at 3 and 332 at 5
 
 constexpr int kMaxCluster = 16;
 constexpr int kWarps = 4;     // of a CTA at most: strips side by side, times tiles one after the other
@@ -538,7 +503,7 @@ __device__ __forceinline__ bool settle(F2 &A, F2 &H, const Place<N> &me, bool wh
 // where a warp has any.  That is right unless a weight is 0 (then the product A is, or may be) or a dropped
 // input is not finite (then H is not), or not every step exists; those lanes go the careful way.
 template <typename T, int N, bool SIG, bool WIDE, bool CLUSTER, int ST>
-__global__ void __launch_bounds__(kWarps * 32, FLB) k_scan_fwd(ScanArgs s, unsigned ctiles, unsigned csize, int times)
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_fwd(ScanArgs s, unsigned ctiles, unsigned csize, int times)
 {
     extern __shared__ __align__(16) unsigned char dyn[];
     // Alone, a warp keeps a tile's weights and inputs in registers from one sweep to the next, and the tile's place
@@ -707,7 +672,7 @@ __global__ void __launch_bounds__(kWarps * 32, FLB) k_scan_fwd(ScanArgs s, unsig
 // The gradient, on arrays turned so that step 0 is the last one forward; s.h is shifted by one step, so
 // that row t holds the state before that step (row steps - 1 is h0).
 template <typename T, int N, bool SIG, bool WIDE, bool CLUSTER, int ST>
-__global__ void __launch_bounds__(kWarps * 32, BLB) k_scan_bwd(ScanArgs s, unsigned ctiles, unsigned csize, int times)
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_bwd(ScanArgs s, unsigned ctiles, unsigned csize, int times)
 {
     extern __shared__ __align__(16) unsigned char dyn[];
     constexpr int NA = SIG ? 4 : 3;
@@ -918,10 +883,16 @@ struct Cell {
     }
 };
 
-// A few steps: one thread takes VEC channels through all of them.
+// Many channels or few steps: one thread takes VEC channels through all steps, some rows requested ahead.  The
+// least instructions, and HBM's rate where the channels alone keep enough bytes in flight (512 x 64 x 4096
+// bf16 sigmoid: forward 94% of the copy rate).
+constexpr int kFewAhead = 8, kFewAheadBack = 4;
+
 template <typename T, bool SIG, int VEC>
 __global__ void __launch_bounds__(128) k_scan_few(ScanArgs s)
 {
+    typedef Cell<T, VEC> C;
+    typedef typename C::Raw Raw;
     const unsigned per = s.channels / VEC;
     const unsigned id = blockIdx.x * 128 + threadIdx.x;
     pdl_wait();
@@ -932,22 +903,33 @@ __global__ void __launch_bounds__(128) k_scan_few(ScanArgs s)
     const T *a = static_cast<const T *>(s.a) + b * s.sa[0] + ch;
     const T *x = static_cast<const T *>(s.x) + b * s.sx[0] + ch;
     T *out = static_cast<T *>(s.out_h) + b * s.sh[0] + ch;
-    typedef typename Cell<T, VEC>::Raw Raw;
+    const uint8_t *resets = s.resets ? s.resets + b * s.sr[0] : nullptr;
     float h[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) h[e] = s.h0 ? s.h0[b * s.channels + ch + e] : 0.0f;
-    for (long long t = 0; t < s.steps; ++t) {
-        float w[VEC], v[VEC];
-        const Raw ra = *reinterpret_cast<const Raw *>(a + t * s.sa[1]), rx = *reinterpret_cast<const Raw *>(x + t * s.sx[1]);
-        const bool reset = s.resets && s.resets[b * s.sr[0] + t * s.sr[1]];
-        Cell<T, VEC>::unpack(ra, w);
-        Cell<T, VEC>::unpack(rx, v);
+    for (long long t = 0; t < s.steps; t += kFewAhead) {
+        Raw ra[kFewAhead], rx[kFewAhead];
+        bool reset[kFewAhead];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const Gate g = gate<SIG>(w[e]);
-            h[e] = weigh(reset ? 0.0f : g.w, h[e], SIG ? weigh(g.v, v[e], 0.0f) : v[e]);
+        for (int i = 0; i < kFewAhead; ++i) {
+            if (t + i >= s.steps) continue;
+            ra[i] = *reinterpret_cast<const Raw *>(a + (t + i) * s.sa[1]);
+            rx[i] = *reinterpret_cast<const Raw *>(x + (t + i) * s.sx[1]);
+            reset[i] = resets && resets[(t + i) * s.sr[1]];
         }
-        Cell<T, VEC>::store(out + t * s.sh[1], h);
+#pragma unroll
+        for (int i = 0; i < kFewAhead; ++i) {
+            if (t + i >= s.steps) continue;
+            float w[VEC], v[VEC];
+            C::unpack(ra[i], w);
+            C::unpack(rx[i], v);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const Gate g = gate<SIG>(w[e]);
+                h[e] = weigh(reset[i] ? 0.0f : g.w, h[e], SIG ? weigh(g.v, v[e], 0.0f) : v[e]);
+            }
+            C::store(out + (t + i) * s.sh[1], h);
+        }
     }
     if (s.last) {
 #pragma unroll
@@ -955,10 +937,79 @@ __global__ void __launch_bounds__(128) k_scan_few(ScanArgs s)
     }
 }
 
-// ---- launches --------------------------------------------------------------------------------
+// The gradient of the same, on the turned arrays (as k_scan_bwd).
+template <typename T, bool SIG, int VEC>
+__global__ void __launch_bounds__(128) k_scan_few_bwd(ScanArgs s)
+{
+    typedef Cell<T, VEC> C;
+    typedef typename C::Raw Raw;
+    const unsigned per = s.channels / VEC;
+    const unsigned id = blockIdx.x * 128 + threadIdx.x;
+    pdl_wait();
+    pdl_release();
+    if (id >= per * s.batch) return;
+    const long long b = id / per;
+    const unsigned ch = id % per * VEC;
+    const T *a = static_cast<const T *>(s.a) + b * s.sa[0] + ch;
+    const T *gh = static_cast<const T *>(s.gh) + b * s.sgh[0] + ch;
+    const T *h = static_cast<const T *>(s.h) + b * s.sh[0] + ch;
+    const T *x = SIG ? static_cast<const T *>(s.x) + b * s.sx[0] + ch : nullptr;
+    T *ga = s.ga ? static_cast<T *>(s.ga) + b * s.sga[0] + ch : nullptr;
+    T *gx = s.gx ? static_cast<T *>(s.gx) + b * s.sgx[0] + ch : nullptr;
+    const uint8_t *resets = s.resets ? s.resets + b * s.sr[0] : nullptr;
+    float c[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) c[e] = s.glast ? s.glast[b * s.channels + ch + e] : 0.0f;
+    for (long long t = 0; t < s.steps; t += kFewAheadBack) {
+        Raw ra[kFewAheadBack], rg[kFewAheadBack], rh[kFewAheadBack], rx[SIG ? kFewAheadBack : 1];
+        bool reset[kFewAheadBack];
+#pragma unroll
+        for (int i = 0; i < kFewAheadBack; ++i) {
+            if (t + i >= s.steps) continue;
+            ra[i] = *reinterpret_cast<const Raw *>(a + (t + i) * s.sa[1]);
+            rg[i] = *reinterpret_cast<const Raw *>(gh + (t + i) * s.sgh[1]);
+            if (t + i < s.steps - 1) rh[i] = *reinterpret_cast<const Raw *>(h + (t + i) * s.sh[1]);
+            if constexpr (SIG) rx[i] = *reinterpret_cast<const Raw *>(x + (t + i) * s.sx[1]);
+            reset[i] = resets && resets[(t + i) * s.sr[1]];
+        }
+#pragma unroll
+        for (int i = 0; i < kFewAheadBack; ++i) {
+            if (t + i >= s.steps) continue;
+            float w[VEC], g[VEC], before[VEC], da[VEC], dx[VEC];
+            C::unpack(ra[i], w);
+            C::unpack(rg[i], g);
+            if constexpr (SIG) C::unpack(rx[i], dx);
+            if (t + i < s.steps - 1) {
+                C::unpack(rh[i], before);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) before[e] = s.h0 ? s.h0[b * s.channels + ch + e] : 0.0f;
+            }
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const Gate f = gate<SIG>(w[e]);
+                const float gt = g[e] + c[e], bt = reset[i] ? 0.0f : before[e];
+                if (SIG) {
+                    const float slope = f.w * f.v;
+                    da[e] = slope == 0.0f ? 0.0f : gt * (bt - dx[e]) * slope;
+                    dx[e] = weigh(f.v, gt, 0.0f);
+                } else {
+                    da[e] = reset[i] ? 0.0f : gt * bt;
+                    dx[e] = gt;
+                }
+                c[e] = weigh(reset[i] ? 0.0f : f.w, gt, 0.0f);
+            }
+            if (ga) C::store(ga + (t + i) * s.sga[1], da);
+            if (gx) C::store(gx + (t + i) * s.sgx[1], dx);
+        }
+    }
+    if (s.gh0) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) s.gh0[b * s.channels + ch + e] = c[e];
+    }
+}
 
-template <typename T, bool BACK, bool CLUSTER>
-constexpr int lane_steps() { return CLUSTER ? (sizeof(T) == 4 ? CN32 : CN16) : sizeof(T) == 4 ? (BACK ? BN32 : FN32) : (BACK ? BN16 : FN16); }
+// ---- launches --------------------------------------------------------------------------------
 
 // How a pass is laid out: a CTA of `strips` x `times` warps, clusters of csize CTAs.
 struct Layout {
@@ -969,8 +1020,8 @@ struct Layout {
 
 template <typename T, bool SIG, bool WIDE, bool BACK, bool CLUSTER>
 struct Launch {
-    static constexpr int NA = BACK ? (SIG ? 4 : 3) : 2, ST = CLUSTER ? CST : BACK ? BST : FST;
-    static constexpr int N = lane_steps<T, BACK, CLUSTER>(), TILE = kGroups * N;
+    static constexpr int NA = BACK ? (SIG ? 4 : 3) : 2, ST = CLUSTER ? kRingCluster : kRing;
+    static constexpr int N = CLUSTER && sizeof(T) == 2 ? kLaneStepsCluster16 : kLaneSteps, TILE = kGroups * N;
     static auto kernel()
     {
         if constexpr (BACK) return k_scan_bwd<T, N, SIG, WIDE, CLUSTER, ST>;
@@ -1021,10 +1072,13 @@ struct Launch {
     }
 };
 
-// The layout that should finish first, by a model with both of its sides measured: a round of an SM takes
-// the time of its bytes at HBM's rate, or what one warp's round takes by itself, whichever is longer (0.8 us;
-// with a CTA barrier 1.0 us, with the exchange of a cluster LATC ns); CTAs beyond what fits at once
-// run after the others.
+// What a pass is laid out as: the one that should finish first by a model whose constants are measured.
+// Tiles: a round of an SM takes the time of its bytes at HBM's rate (times `tile_cost`: 64 x 1024 x 1024 bf16
+// 80 us against 60, binary32 120 against 119, single values 333 against 118), or what one warp's round takes
+// by itself, whichever is longer (0.8 us, with a CTA barrier 1.0, with a cluster's exchange 2.5); CTAs beyond
+// what fits at once run after the others.  One thread a channel through all steps: `flat` us a step for
+// the latency of its rows and their bytes at HBM's rate (1 x 1024 x 256 bf16: 185 us, as tiles 5; 64 x 4 x 4096:
+// 3.6 us, as tiles 25).
 template <typename T, bool SIG, bool WIDE, bool BACK>
 cudaError_t launch_any(const ScanArgs &a, const DeviceInfo &dev, cudaStream_t st)
 {
@@ -1033,9 +1087,14 @@ cudaError_t launch_any(const ScanArgs &a, const DeviceInfo &dev, cudaStream_t st
     const unsigned per_row = (a.channels + kStrip - 1) / kStrip;
     constexpr double step_us = kStrip * sizeof(T) * (One::NA + (BACK ? 2 : 1)) / 44500.0;   // of a warp's strip
     Layout best{};
+    constexpr int P = WIDE ? 16 / (int)sizeof(T) : 1;
+    const double cells = (double)a.channels * a.batch;
+    constexpr double flat = WIDE ? (BACK ? 0.25 : 0.13) : (BACK ? 0.4 : 0.27);
+    constexpr double tile_cost = !WIDE ? 2.2 : sizeof(T) == 4 ? 1.05 : 1.35;
+    const double few = a.steps * (flat + cells * sizeof(T) * (One::NA + (BACK ? 2 : 1)) / 6.4e6);
     double least = 1e30;
     for (int times = 1; times <= 4; times *= 2) {
-        for (unsigned csize = 1; csize <= (times == 4 ? (unsigned)MAXCL : 1u); csize *= 2) {
+        for (unsigned csize = 1; csize <= (times == 4 ? (unsigned)kMaxCluster : 1u); csize *= 2) {
             const int tile = csize > 1 ? Many::TILE : One::TILE;
             const long long span = (long long)tile * times * csize;
             if (times * csize > 1 && span / 2 >= a.steps) continue;   // some would have no tile
@@ -1045,7 +1104,7 @@ cudaError_t launch_any(const ScanArgs &a, const DeviceInfo &dev, cudaStream_t st
             const cudaError_t e = csize > 1 ? Many::capacity(l, dev, &fit) : One::capacity(l, dev, &fit);
             if (e != cudaSuccess) return e;
             const double ctas = (double)((per_row + l.strips - 1) / l.strips) * a.batch * csize;
-            const double alone = csize > 1 ? LATC / 1000.0 : times > 1 ? 1.0 : 0.8;
+            const double alone = csize > 1 ? 2.5 : times > 1 ? 1.0 : 0.8;
             const double full = std::floor(ctas / fit), rest = ctas - full * fit;
             auto round = [&](double n) { return std::max(alone, n / dev.sms * l.warps() * tile * step_us); };
             const double us = std::ceil((double)a.steps / span) * (full * round(fit) + (rest > 0 ? round(rest) : 0.0));
@@ -1054,6 +1113,11 @@ cudaError_t launch_any(const ScanArgs &a, const DeviceInfo &dev, cudaStream_t st
                 best = l;
             }
         }
+    }
+    if (few <= least * tile_cost + 3.0) {
+        const unsigned grid = (unsigned)((unsigned long long)(a.channels / P) * a.batch + 127) / 128;
+        if constexpr (BACK) return launch_clusters(k_scan_few_bwd<T, SIG, P>, grid, 128, 1, 0, st, a);
+        else return launch_clusters(k_scan_few<T, SIG, P>, grid, 128, 1, 0, st, a);
     }
     return best.csize > 1 ? Many::run(a, best, st) : One::run(a, best, st);
 }
@@ -1070,12 +1134,6 @@ cudaError_t fwd_t(const ScanArgs &a, const DeviceInfo &dev, cudaStream_t st)
     constexpr unsigned e = sizeof(T), P = 16 / e;
     const bool wide = a.channels % P == 0 && aligned16(a.a, a.sa, a, e) && aligned16(a.x, a.sx, a, e) &&
                       aligned16(a.out_h, a.sh, a, e);
-    if (a.steps <= FEW) {
-        const unsigned long long threads = (unsigned long long)a.channels / (wide ? P : 1) * a.batch;
-        const unsigned grid = (unsigned)((threads + 127) / 128);
-        if (wide) return launch_clusters(k_scan_few<T, SIG, (int)P>, grid, 128, 1, 0, st, a);
-        return launch_clusters(k_scan_few<T, SIG, 1>, grid, 128, 1, 0, st, a);
-    }
     return wide ? launch_any<T, SIG, true, false>(a, dev, st) : launch_any<T, SIG, false, false>(a, dev, st);
 }
 

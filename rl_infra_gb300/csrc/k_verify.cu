@@ -23,9 +23,6 @@ namespace {
 typedef unsigned long long u64;
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-#ifndef VF
-#define VF 8
-#endif
 constexpr int kMaxCluster = 8;
 constexpr int kUnroll = 4;   // 16-byte loads of each row that a lane has in flight
 
@@ -126,7 +123,7 @@ __device__ __forceinline__ u64 warp_sum(u64 v)
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_verify(VerifyArgs a, unsigned csize, unsigned per_cta)
+__global__ void __launch_bounds__(kThreads, 4) k_verify(VerifyArgs a, unsigned csize, unsigned per_cta)
 {
     constexpr int P = Pack<T>::N;
     __shared__ u64 warp_total[kWarps], cluster_total[2][kMaxCluster];
@@ -182,7 +179,7 @@ __global__ void __launch_bounds__(kThreads) k_verify(VerifyArgs a, unsigned csiz
     const unsigned w0 = min(rank * per_cta + warp * per_warp, v1), w1 = min(w0 + per_warp, v1);
     for (int attempt = 0; attempt < 2; ++attempt) {
         Units sum;
-        unsigned count = 0;   // a lane's masses: at most 2^18 / (8 CTAs x 8 warps x 32 lanes), and a piece more
+        unsigned count = 0;   // a lane's masses: at most 2^18 / (8 warps x 32 lanes), and a piece more
         for (unsigned w = w0 + lane; w < w1; w += 32 * kUnroll) {
             Pack<T> x[kUnroll], y[kUnroll];
 #pragma unroll
@@ -274,14 +271,14 @@ __global__ void __launch_bounds__(kThreads) k_verify(VerifyArgs a, unsigned csiz
 }
 
 template <typename T>
-cudaError_t launch_t(const VerifyArgs &a, cudaStream_t st)
+cudaError_t launch_t(const VerifyArgs &a, const DeviceInfo &dev, cudaStream_t st)
 {
     constexpr unsigned P = 16 / sizeof(T);
     const unsigned pieces = (a.vocab + P - 1) / P + 1;   // a row that starts off a boundary has one more
-    // CTAs for a sequence: at least 512 pieces each (16 a lane of one warp); more, smaller CTAs also even out
-    // the load over the SMs where there are many sequences
+    // CTAs for a sequence: at least 512 pieces each (two a lane), and no more than 8 an SM in all: each runs the
+    // accept tests again (512 sequences of 131072: 4 CTAs a sequence 100 us, 8 103, 2 124)
     unsigned csize = 1;
-    while (csize < kMaxCluster && pieces / csize > 1024 && (unsigned long long)a.batch * csize < VF * 152ull) csize *= 2;
+    while (csize < kMaxCluster && pieces / csize > 1024 && (unsigned long long)a.batch * csize < 8ull * dev.sms) csize *= 2;
     return launch_clusters(k_verify<T>, a.batch * csize, kThreads, csize, 0, st, a, csize, (pieces + csize - 1) / csize);
 }
 
@@ -289,9 +286,12 @@ cudaError_t launch_t(const VerifyArgs &a, cudaStream_t st)
 
 cudaError_t launch_verify(int type, const VerifyArgs &a, cudaStream_t st)
 {
-    if (type == PER_TYPE_F32) return launch_t<float>(a, st);
-    if (type == PER_TYPE_F16) return launch_t<__half>(a, st);
-    return launch_t<__nv_bfloat16>(a, st);
+    DeviceInfo dev;
+    const cudaError_t e = device_info(&dev);
+    if (e != cudaSuccess) return e;
+    if (type == PER_TYPE_F32) return launch_t<float>(a, dev, st);
+    if (type == PER_TYPE_F16) return launch_t<__half>(a, dev, st);
+    return launch_t<__nv_bfloat16>(a, dev, st);
 }
 
 }  // namespace gbper
