@@ -331,7 +331,7 @@ per_status per_rank_order_noalloc(const float *d_raw, uint32_t n, uint32_t *d_or
  * are the next priorities (distillation from a teacher's top logits), the recurrence of a
  * sequence model with its gradient, and the verification of drafted tokens by an actor.
  * They need no handle and keep nothing between calls: the caller owns every array, no call
- * allocates, and each enqueues one kernel on `stream`.  A failed call's message is
+ * allocates, and each enqueues one kernel (or copy) on `stream`.  A failed call's message is
  * per_last_op_error(), on the calling thread.  Strides count elements; the innermost axis of
  * every array is contiguous.  Input strides may be any value (0 repeats a row for all); rows of an
  * output must not overlap.  Pointers need the alignment of their element type only; rows whose
@@ -459,7 +459,8 @@ typedef struct {
  * state is kept in binary32; h is rounded to its type where it is stored.  Long sequences are
  * split over time where the channels alone do not fill the GPU; the joints multiply the decays of
  * a stretch, whose product must stay finite in binary32 (decays of magnitude at most 1 always
- * do).  PER_SCAN_REVERSE runs t = T-1 .. 0 (discounted returns: a = gamma, x = reward, a reset at each
+ * do).  (The parts of a sequence wait for one another with a limit; one that ran out would leave NaN in
+ * the states.)  PER_SCAN_REVERSE runs t = T-1 .. 0 (discounted returns: a = gamma, x = reward, a reset at each
  * episode's last step).
  *   d_a, d_x [B x T x C], d_h0 [B x C] float or NULL, d_resets [B x T] uint8 or NULL,
  *   d_h [B x T x C], d_last [B x C] float (NULL to skip): the state after the last step; it may be

@@ -22,8 +22,8 @@
 #include "ops_internal.cuh"
 
 #include <algorithm>
+#include <atomic>
 #include <cstring>
-#include <mutex>
 #include <type_traits>
 
 namespace gbper {
@@ -151,22 +151,22 @@ struct Running {
     }
 };
 
-// P consecutive elements of a row from element j on (j + P is the next lane's j; the whole warp calls), of
-// which those in [lo, hi) may be read; the others give -inf.  p + j need not be on a 16-byte
+// P consecutive elements of a part in shared memory from element j on (j + P is the next lane's j; the whole
+// warp calls), of which those in [lo, hi) are there; the others give -inf.  p + j need not be on a 16-byte
 // boundary: the blocks on boundaries are read, and joined with the next lane's.
-template <typename T, typename Load>
+template <typename T>
 struct Pieces {
     static constexpr int P = Pack<T>::N;
     const T *p;
     int lo, hi;
-    Load load;
     unsigned off;   // bytes from the boundary at or before p + j
     uint4 a[kUnroll], b[kUnroll];
 
-    __device__ __forceinline__ Pieces(const T *p_, int lo_, int hi_, int j, Load load_)
-        : p(p_), lo(lo_), hi(hi_), load(load_), off((unsigned)(reinterpret_cast<uintptr_t>(p_ + j) & 15u))
+    __device__ __forceinline__ Pieces(const T *p_, int lo_, int hi_, int j)
+        : p(p_), lo(lo_), hi(hi_), off((unsigned)(reinterpret_cast<uintptr_t>(p_ + j) & 15u))
     {
     }
+    static __device__ __forceinline__ uint4 load(const void *p) { return *static_cast<const uint4 *>(p); }
     __device__ __forceinline__ int before() const { return (int)(off / (unsigned)sizeof(T)); }
     __device__ __forceinline__ bool whole(int j) const { return j >= lo && j + P <= hi; }
     // every block that the pieces from element `first` to element `last` need may be read
@@ -222,10 +222,6 @@ struct Pieces {
     }
 };
 
-struct FromShared {
-    __device__ __forceinline__ uint4 operator()(const void *p) const { return *static_cast<const uint4 *>(p); }
-};
-
 // The join of n stretches: the largest maximum first, then the rescaled sums in their order.
 __device__ __forceinline__ RowSum gather(const RowSum *p, int n, float c)
 {
@@ -236,11 +232,11 @@ __device__ __forceinline__ RowSum gather(const RowSum *p, int n, float c)
     return r;
 }
 
-// Shared memory of a CTA: the part of the row (step only), then the teacher's entries.
+// Static shared memory of a CTA (the dynamic part: the CTA's part of the row, then the teacher's entries).
 struct Shared {
     RowSum cluster[kMaxCluster];
     RowSum warp[kMaxWarps];
-    float S, L;
+    float S;
     int some, repeated;
 };
 
@@ -255,10 +251,10 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, kCtasPerSm) k_distill(Di
     __shared__ Shared sh;
     uint4 *part = reinterpret_cast<uint4 *>(dyn);                             // [per_cta + 1]
     float *q = reinterpret_cast<float *>(dyn + ((size_t)per_cta + 1) * 16);   // [K]
-    float *d = q + a.k;                                                 // [K] t - L
-    float *xk = d + a.k;                                                // [K] the student's logits there
-    int *at = reinterpret_cast<int *>(xk + a.k);                        // [K] place, -1: left out
-    int *table = at + a.k;                                              // [hash_size]
+    float *d = q + a.k;                                                       // [K] t - L
+    float *xk = d + a.k;                                                      // [K] the student's logits there
+    int *at = reinterpret_cast<int *>(xk + a.k);                              // [K] place, -1: left out
+    int *table = at + a.k;                                                    // [hash_size]
     const int K = (int)a.k;
     const unsigned rank = blockIdx.x % csize;   // also the CTA's rank in its cluster, where there is one
     const long long row = blockIdx.x / csize;
@@ -407,7 +403,7 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, kCtasPerSm) k_distill(Di
             }
             asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;\n\tbar.sync 1, %0;" ::"r"(loaders) : "memory");
             if (PART != kDistillBackward) {
-                Pieces<T, FromShared> held(cells, j0, j1, j0, FromShared());
+                Pieces<T> held(cells, j0, j1, j0);
                 for (unsigned v = base; v < v1; v += step) {
                     Pack<T> in[kUnroll];
                     if ((int)((v + inner) * P) <= j1 && held.whole_blocks((int)(v * P), (int)((v + inner - 1) * P))) {
@@ -480,7 +476,7 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, kCtasPerSm) k_distill(Di
     if (t < loaders && j0 < j1) {
         const int o0 = (j0 + misg) / P, o1 = (j1 - 1 + misg) / P + 1, first = o0 + (t & ~31), step = loaders * kUnroll;
         const F2 ref{-lse, -lse}, cc{c, c}, ff{f0, f0};
-        Pieces<T, FromShared> from(cells, j0, j1, o0 * P - misg, FromShared());
+        Pieces<T> from(cells, j0, j1, o0 * P - misg);
         auto turn = [&](Pack<T> &in) {
             float f[P];
             in.unpack(f);
@@ -581,14 +577,12 @@ cudaError_t attributes()
 
 cudaError_t init_once(int device)
 {
-    static std::mutex mu;
-    static bool done[64] = {};
-    std::lock_guard<std::mutex> lock(mu);
-    if (done[device]) return cudaSuccess;
+    static std::atomic<bool> done[64];   // (two threads may both set the attributes, to the same values)
+    if (done[device].load(std::memory_order_acquire)) return cudaSuccess;
     cudaError_t e = attributes<float>();
     if (e == cudaSuccess) e = attributes<__half>();
     if (e == cudaSuccess) e = attributes<__nv_bfloat16>();
-    if (e == cudaSuccess) done[device] = true;
+    if (e == cudaSuccess) done[device].store(true, std::memory_order_release);
     return e;
 }
 

@@ -189,15 +189,6 @@ __device__ __forceinline__ void Pack<__half>::pack(const float *f)
     raw = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// 16 bytes that nobody reads again soon
-__device__ __forceinline__ uint4 load_stream(const void *p)
-{
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
-}
-
 // The 16 bytes that begin `off` bytes (a multiple of 2 below 16, the same for the whole warp) into the 32
 // bytes of lo and hi.
 __device__ __forceinline__ uint4 shift_bytes(uint4 lo, uint4 hi, unsigned off)
@@ -239,13 +230,12 @@ cudaError_t launch_clusters(void (*kernel)(KArgs...), unsigned grid, unsigned bl
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
-// SMs of the current device, and whether a launch on it must first set its kernels' attributes.
+// The current device and its SMs.
 struct DeviceInfo {
     int device, sms;
 };
 cudaError_t device_info(DeviceInfo *out);   // ops_api.cu
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 }  // namespace gbper

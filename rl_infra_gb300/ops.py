@@ -116,7 +116,10 @@ def _elsewhere(stream, dev):
     return stream is not None or dev != torch._C._cuda_getDevice()
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+def _raw_stream(dev):
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
 _lib = None
 
 
