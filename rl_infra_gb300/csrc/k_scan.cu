@@ -443,18 +443,33 @@ struct Place {
     }
 };
 
-// The resets of this lane's steps in the warp's tile from step t0 on, bit by bit.
+// The resets of a warp's tile, a step or two a lane: requested a tile ahead, used as bits of a lane's own steps.
+struct Resets {
+    unsigned lo, hi;
+};
+
 template <int N>
-__device__ __forceinline__ unsigned reset_bits(const ScanArgs &s, long long b, long long t0)
+__device__ __forceinline__ Resets request_resets(const ScanArgs &s, long long b, long long t0)
 {
-    if (!s.resets) return 0;
+    Resets r{0, 0};
+    if (!s.resets) return r;
     const int lane = threadIdx.x & 31;
     const uint8_t *p = s.resets + b * s.sr[0] + (t0 + lane) * s.sr[1];
-    const bool lo = t0 + lane < s.steps && *p != 0;
-    const bool hi = kGroups * N > 32 && t0 + 32 + lane < s.steps && p[32 * s.sr[1]] != 0;
-    const unsigned a = __ballot_sync(kFull, lo), c = __ballot_sync(kFull, hi);
-    const int first = lane / 8 * N;   // of the tile's steps
-    return (first < 32 ? a : c) >> (first & 31) & ((1u << N) - 1u);
+    if (t0 + lane < s.steps) r.lo = *p;
+    if (kGroups * N > 32 && t0 + 32 + lane < s.steps) r.hi = p[32 * s.sr[1]];
+    return r;
+}
+
+template <int N>
+__device__ __forceinline__ unsigned reset_bits(Resets r)
+{
+    const unsigned a = __ballot_sync(kFull, r.lo != 0);
+    const int first = (threadIdx.x & 31) / 8 * N;   // of the tile's steps
+    if constexpr (kGroups * N > 32) {
+        const unsigned c = __ballot_sync(kFull, r.hi != 0);
+        return (first < 32 ? a : c) >> (first & 31) & ((1u << N) - 1u);
+    }
+    return a >> first & ((1u << N) - 1u);
 }
 
 template <int N>
@@ -527,7 +542,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_fwd(ScanArgs s
     };
 #pragma unroll
     for (int k = 0; k < (CLUSTER ? AHEAD : ST); ++k) request(k);
-    unsigned resets = reset_bits<N>(s, me.b, me.t0);
+    Resets ahead = request_resets<N>(s, me.b, me.t0);
     joints.state = first_state(s.h0, s, me);
     joints.begin(dyn + (blockDim.x >> 5) * R::BYTES, me.strip, times, me.time, csize, me.rank);
 
@@ -556,6 +571,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_fwd(ScanArgs s
         copies_wait<CLUSTER ? AHEAD - 1 : AHEAD>();
         __syncwarp();
         if (CLUSTER) request(k + AHEAD);   // (the place was last read before this warp's last shuffles)
+        const unsigned resets = reset_bits<N>(ahead);
+        ahead = request_resets<N>(s, me.b, t - me.off + me.span);
         h.resets = resets;
         F2 A{1.0f, 1.0f}, H{0.0f, 0.0f};
         auto run = [&](auto any) {
@@ -606,7 +623,6 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_fwd(ScanArgs s
             __syncwarp();   // every lane has read the tile
             request(k + ST);
         }
-        resets = reset_bits<N>(s, me.b, t - me.off + me.span);
     };
     auto second = [&](int k, const Tile &h) {
         const long long t = me.t0 + k * me.span + me.off;
@@ -700,7 +716,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_bwd(ScanArgs s
     };
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) request(k);
-    unsigned resets = reset_bits<N>(s, me.b, me.t0);
+    Resets ahead = request_resets<N>(s, me.b, me.t0);
     joints.state = first_state(s.glast, s, me);
     joints.begin(dyn + (blockDim.x >> 5) * R::BYTES, me.strip, times, me.time, csize, me.rank);
 
@@ -710,6 +726,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_bwd(ScanArgs s
         copies_wait<CLUSTER ? AHEAD - 1 : AHEAD>();
         __syncwarp();
         if (CLUSTER) request(k + AHEAD);   // (the place was last read before this warp's last shuffles)
+        const unsigned resets = reset_bits<N>(ahead);
+        ahead = request_resets<N>(s, me.b, t - me.off + me.span);
         d.resets = resets;
         F2 A{1.0f, 1.0f}, H{0.0f, 0.0f};
         auto run = [&](auto any) {
@@ -751,7 +769,6 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_bwd(ScanArgs s
             }
         }
         joints.first(k, d.plain, A, H, resets != 0, own, d.before, d.all);
-        resets = reset_bits<N>(s, me.b, t - me.off + me.span);
     };
     auto second = [&](int k, const Tile &d) {
         const long long t = me.t0 + k * me.span + me.off;
