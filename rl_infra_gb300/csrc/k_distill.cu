@@ -9,9 +9,9 @@
 // Sums and normalisers are binary32; the gradient is rounded once.
 //
 // Work.  A row is split over a cluster of 1 to 8 CTAs.  Each CTA's loader warps copy their part of the
-// row into shared memory (cp.async, batches ahead), keep the running (m, s) of what has arrived, exchange (m, s) with the row's other CTAs through
-// distributed shared memory (one hardware barrier), and turn the part into the gradient on its way
-// out.  So the step reads the logits once and writes the gradient once, which is its bound (HBM); three CTAs
+// row into shared memory (cp.async), keep the running (m, s) of what has arrived, exchange it with the row's
+// other CTAs through distributed shared memory (one hardware barrier), and turn the part into the gradient
+// on its way out.  So the step reads the logits once and writes the gradient once, which is its bound (HBM); three CTAs
 // an SM are in different phases.  One more warp of each CTA handles the teacher's entries meanwhile; their q
 // is taken off the gradient by a second write to those places after the CTA's barrier.  Every access to
 // memory is 16 bytes on a 16-byte boundary but for a row's ends; a row that starts elsewhere (an odd
@@ -19,6 +19,9 @@
 // summed in the same order, and gives the same bits, wherever it lies.  (Clusters that stay for many rows and
 // load the next while they write this one were slower, 2.5 ms against 0.86 for 8192 rows of 131072: the
 // barrier between the CTAs then waits for the stores of the row before.)
+//
+// Measured (GB300): step 8192 x 131072 bf16 with 64 entries 855 us, 5.0 TB/s, 74% of the copy rate; backward
+// 2048 x 131072 bf16 87%; forward 32 x 1009 f32 3.4 us.
 #include "ops_internal.cuh"
 
 #include <algorithm>
@@ -32,11 +35,12 @@ namespace {
 
 constexpr int kMaxTop = 1024;
 constexpr int kMaxCluster = 8;
-// Loader warps of a CTA at most, CTAs an SM has registers for, and KB of a row that a CTA takes: 8, 3, 64 take 0.86 ms
-// for 8192 rows of 131072 bf16; 16 warps 1.28, two CTAs 1.06, 40 KB 1.17, 96 KB 1.51.
+// Loader warps of a CTA at most, CTAs an SM keeps registers for, and KB of a row that a CTA takes at most: 8, 3 and
+// 64 take 0.86 ms for 8192 rows of 131072 bf16; 16 warps and 2 CTAs 1.17, 2 CTAs 1.10, 34 KB (more and smaller CTAs
+// in larger clusters) 1.34.
 constexpr int kMaxWarps = 8, kCtasPerSm = 3, kPartKb = 64;
 constexpr int kUnroll = 4;       // pieces of 16 bytes a loader thread takes at a time
-constexpr int kAhead = 1;        // batches of them that are requested ahead (2: 1% slower; 4: 4%)
+constexpr int kAhead = 1;        // batches of them that are requested ahead (0.86 ms; 4: 0.90)
 constexpr float kInf = __builtin_huge_valf();
 
 struct RowSum {

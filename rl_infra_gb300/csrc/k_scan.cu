@@ -21,7 +21,12 @@
 // (A, H) to the others by asynchronous stores into their shared memory, which count down a barrier there
 // (no fence, so output stores in flight are not waited for), and only then finishes the round before:
 // the exchange runs beside the next round's first sweep.  (A remote store takes about 8 cycles of the
-// receiver: with one warp's stretch a message, 16 CTAs to 16, the exchange took 3.6 us a round.)
+// receiver: with one warp's stretch a message, 16 CTAs to 16, the exchange took 3.6 us a round.)  Where the
+// channels are many, or the steps few, one thread a channel (k_scan_few) takes fewer instructions.
+//
+// Measured (GB300): 64 x 1024 x 1024 f32 forward 121 us, 6.7 TB/s; 16 x 2048 x 2048 bf16 sigmoid gradient 174 us, 4.6 TB/s
+// (its instructions bound it); one sequence of 65537 x 1024 bf16 146 us, 2.8 TB/s (the joints); one step of
+// 64 x 2048 2.0 us.
 #include "ops_internal.cuh"
 
 #include <algorithm>
@@ -34,13 +39,13 @@ namespace gbper {
 
 namespace {
 
-// Steps of a lane in a tile and tiles in a ring, measured on 64 x 1024 x 1024 bf16 with sigmoid gates (forward,
-// gradient) and on one sequence of 65537 x 1024: 8 steps 83 and 183 us, 16 steps 99 and 199 (registers);
-// with a cluster, where the exchange is the larger part, 16 steps 141 us, 8 steps 149.  Rings of 2 tiles and
-// of 3 take the same time within 3%; in a cluster 3 (two under way, one arriving) 141 us, 4 165.
+// Measured on 64 x 1024 x 1024 bf16 with sigmoid gates, forward and gradient, and on one sequence of 65537 x 1024 (a
+// cluster), us.  Steps of a lane in a tile: 8 82 and 170, 16 86 and 198 (registers); with a cluster, where the
+// joints are the larger part, 16 141, 8 149.  Tiles in a ring: 2 82 and 170, 3 82 and 172; with a cluster 3 (two
+// under way, one arriving) 141, 4 165.
 constexpr int kLaneSteps = 8, kLaneStepsCluster16 = 16;
 constexpr int kRing = 2, kRingCluster = 3;
-constexpr int kCtasPerSm = 4;   // registers for 4 CTAs of 4 warps (128 each): 184 us against 248 at 3 and 332 at 5
+constexpr int kCtasPerSm = 4;   // what registers are kept for (CTAs of 4 warps): 4 82, 170, 141; 3 83, 188, 162; 5 89, 203, 147
 
 constexpr int kMaxCluster = 16;
 constexpr int kWarps = 4;     // of a CTA at most: strips side by side, times tiles one after the other
