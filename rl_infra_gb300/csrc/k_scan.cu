@@ -536,7 +536,6 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_fwd(ScanArgs s
     const R ring{dyn + (threadIdx.x >> 5) * R::BYTES};
     Joints<CLUSTER> joints;
     pdl_wait();
-    pdl_release();
     const T *a = static_cast<const T *>(s.a) + me.b * s.sa[0] + me.c0;
     const T *x = static_cast<const T *>(s.x) + me.b * s.sx[0] + me.c0;
     T *out = static_cast<T *>(s.out_h) + me.b * s.sh[0] + me.ch;
@@ -686,6 +685,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_fwd(ScanArgs s
             second(k, h);
         }
     }
+    // Not at the start: the next kernel's CTAs would take the few places that are free meanwhile, and lie unevenly on
+    // the SMs (both passes of 8 x 16384 x 1024 f32: 737 us, released at the start 881).
+    pdl_release();
     joints.end();
     if (me.time == 0) last_state(s.last, joints.state, s, me);
 }
@@ -704,7 +706,6 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_bwd(ScanArgs s
     const R ring{dyn + (threadIdx.x >> 5) * R::BYTES};
     Joints<CLUSTER> joints;
     pdl_wait();
-    pdl_release();
     const T *a = static_cast<const T *>(s.a) + me.b * s.sa[0] + me.c0;
     const T *gh = static_cast<const T *>(s.gh) + me.b * s.sgh[0] + me.c0;
     const T *h = static_cast<const T *>(s.h) + me.b * s.sh[0] + me.c0;
@@ -868,6 +869,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_bwd(ScanArgs s
             second(k, d);
         }
     }
+    pdl_release();   // (as in the forward pass, not at the start)
     joints.end();
     if (me.time == 0) last_state(s.gh0, joints.state, s, me);
 }
