@@ -86,7 +86,7 @@ def _given(out, name, shape, dtype, dev, like):
     """The output `name`: the caller's, checked, or a new one."""
     t = out.get(name) if out is not None else None
     if t is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)   # (new_empty takes twice as long)
     _arg(t, name, torch.Size(shape), dtype, dev)
     return t
 
