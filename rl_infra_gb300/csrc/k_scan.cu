@@ -24,9 +24,9 @@
 // receiver: with one warp's stretch a message, 16 CTAs to 16, the exchange took 3.6 us a round.)  Where the
 // channels are many, or the steps few, one thread a channel (k_scan_few) takes fewer instructions.
 //
-// Measured (GB300): 64 x 1024 x 1024 f32 forward 121 us, 6.7 TB/s; 16 x 2048 x 2048 bf16 sigmoid gradient 174 us, 4.6 TB/s
-// (its instructions bound it); one sequence of 65537 x 1024 bf16 146 us, 2.8 TB/s (the joints); one step of
-// 64 x 2048 2.0 us.
+// Measured (GB300): 64 x 1024 x 1024 f32 forward 121 us, 6.7 TB/s; both passes of 8 x 16384 x 1024 f32 742 us, 5.8 TB/s;
+// 16 x 2048 x 2048 bf16 sigmoid gradient 176 us, 4.6 TB/s (its instructions bound it); one sequence of 65537 x
+// 1024 bf16 146 us, 2.8 TB/s (the joints); one step of 64 x 2048 2.0 us.
 #include "ops_internal.cuh"
 
 #include <algorithm>
@@ -519,6 +519,10 @@ __device__ __forceinline__ bool settle(F2 &A, F2 &H, const Place<N> &me, bool wh
     return whole && fminf(fabsf(A.x), fabsf(A.y)) > 0.0f && fabsf(H.x) < kInf && fabsf(H.y) < kInf;
 }
 
+// (Neither kernel lets the next one begin before it ends: the next one's CTAs would take the few places that are free
+// meanwhile and lie unevenly on the SMs.  Both passes of 8 x 16384 x 1024 f32 take 742 us; with the release at the
+// kernels' end 786, at their start 881.)
+//
 // Each sweep is first written with products and sums alone: w h + v, and a reset's state of 0 by a select
 // where a warp has any.  That is right unless a weight is 0 (then the product A is, or may be) or a dropped
 // input is not finite (then H is not), or not every step exists; those lanes go the careful way.
@@ -685,9 +689,6 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_fwd(ScanArgs s
             second(k, h);
         }
     }
-    // Not at the start: the next kernel's CTAs would take the few places that are free meanwhile, and lie unevenly on
-    // the SMs (both passes of 8 x 16384 x 1024 f32: 737 us, released at the start 881).
-    pdl_release();
     joints.end();
     if (me.time == 0) last_state(s.last, joints.state, s, me);
 }
@@ -869,7 +870,6 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_bwd(ScanArgs s
             second(k, d);
         }
     }
-    pdl_release();   // (as in the forward pass, not at the start)
     joints.end();
     if (me.time == 0) last_state(s.gh0, joints.state, s, me);
 }
