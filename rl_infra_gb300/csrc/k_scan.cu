@@ -317,16 +317,20 @@ struct Joints {
     {
         const int lane = threadIdx.x & 31;
         if (__all_sync(kFull, plain)) {
-            // everything is finite: a drop is a product with 0, and which stretches drop is told by the resets
+            // Every lane's own numbers are finite, but what they join to need not be: a stretch that drops what
+            // comes in leaves it out, which a product with 0 would not do to an infinite sum; which stretches drop
+            // is told by the resets.
             const unsigned drops = __ballot_sync(kFull, resets);
-            if (resets) A = {0.0f, 0.0f};
 #pragma unroll
             for (int o = 8; o < 32; o <<= 1) {
                 const F2 a{__shfl_up_sync(kFull, A.x, o), __shfl_up_sync(kFull, A.y, o)};
                 const F2 h{__shfl_up_sync(kFull, H.x, o), __shfl_up_sync(kFull, H.y, o)};
-                if (lane >= o) {
+                // the groups that this lane's stretch takes in by now: its own, then the one before too
+                const unsigned own_groups = o == 8 ? 0xffu << (lane & 24) : (0xffu << (lane & 24)) | (0xffu << (lane & 24)) >> 8;
+                if (lane >= o && !(drops & own_groups)) {
                     H = fma2(A, h, H);
                     A = A * a;
+                    if (o == 8) A = {nonzero(A.x), nonzero(A.y)};   // (it may meet an infinite sum)
                 }
             }
             const bool earlier = (drops & ((1u << (lane & 24)) - 1u)) != 0u;

@@ -1,0 +1,113 @@
+"""The operators where finite inputs overflow on the way, where waits run out, on other streams, and under
+torch.autograd beyond the first derivative.  Bounds come from tests/ops_oracle.py or are derived beside
+each test; U is half an ulp of binary32, relative."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+from rl_infra_gb300 import build, capi, ops  # noqa: E402
+from tests import ops_oracle as oo  # noqa: E402
+
+TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build()
+    capi.load()
+
+
+def host(t):
+    return t.detach().to(torch.float64 if t.dtype.is_floating_point else torch.int64).cpu().numpy()
+
+
+def f32(t):
+    return t.detach().float().cpu().numpy()
+
+
+def rand(g, *shape, kind="f32"):
+    return torch.from_numpy(g.normal(size=shape).astype(np.float32)).cuda().to(TYPES[kind])
+
+
+# -- sums that overflow before a reset ---------------------------------------------------------
+
+# first large step, second, reset: on both sides of a lane's 8 (or 16) steps, the reset one group of lanes later or more
+OVERFLOWS = [(7, 8, 18), (3, 12, 20), (7, 8, 24), (0, 15, 31), (15, 16, 33), (15, 16, 36), (14, 47, 50), (7, 24, 31), (31, 32, 42)]
+
+
+def overflow_case(g, b, t, c, kind, decay):
+    """Sequence r holds a pattern at the front, in the middle or at the end; and the place from which each sequence
+    counts from 0 again."""
+    a = torch.full((b, t, c), decay, device="cuda").to(TYPES[kind])
+    x = rand(g, b, t, c, kind=kind)
+    resets = torch.zeros(b, t, dtype=torch.uint8, device="cuda")
+    low = torch.finfo(TYPES[kind]).min
+    at = []
+    for r in range(b):
+        first, then, reset = OVERFLOWS[r % len(OVERFLOWS)]
+        base = [0, t // 128 * 64, (t - 51) // 64 * 64][(r + r // len(OVERFLOWS)) % 3]
+        x[r, base + first] = low
+        x[r, base + then] = low
+        resets[r, base + reset] = 1
+        at.append(base + reset)
+    return a, x, resets, at
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("decay", [1.0, 0.99, 0.75, 2.0 ** -13])
+@pytest.mark.parametrize("b, t, c", [(27, 64, 8), (27, 200, 16), (27, 3000, 16), (54, 128, 1024), (3, 9000, 33)])
+def test_scan_a_reset_drops_a_state_that_overflowed(kind, decay, b, t, c):
+    """Finite inputs whose sum is infinite, and a reset after them: what follows counts from 0."""
+    g = np.random.default_rng(50)
+    a, x, resets, at = overflow_case(g, b, t, c, kind, decay)
+    for reverse in (False, True):
+        turn = (lambda z: z.flip(1)) if reverse else (lambda z: z)
+        got = ops.scan_forward(turn(a), turn(x), resets=turn(resets), reverse=reverse)
+        h = turn(got["h"])
+        for r in range(b):
+            part = slice(at[r], None)
+            want = oo.scan(host(a[r:r + 1, part]), host(x[r:r + 1, part]), None, host(resets[r:r + 1, part]))
+            oo.close(f32(h[r:r + 1, part]), want["h"], want["bh"], kind)
+            oo.close(f32(got["last"][r:r + 1]), want["last"], want["blast"])
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("b, t, c", [(27, 64, 8), (27, 200, 16), (27, 3000, 16), (54, 128, 1024), (3, 9000, 33)])
+def test_scan_a_reset_drops_a_gradient_that_overflowed(kind, sigmoid, b, t, c):
+    g = np.random.default_rng(51)
+    a, gh, resets, at = overflow_case(g, b, t, c, kind, 20.0 if sigmoid else 1.0)   # (a gate of 20: a weight next to 1)
+    # the gradient runs from the last step on
+    a, gh, resets = a.flip(1), gh.flip(1), resets.flip(1)
+    x, h = rand(g, b, t, c, kind=kind), rand(g, b, t, c, kind=kind)
+    if not sigmoid:
+        x = None
+    h0 = rand(g, b, c)
+    gate = ops.GATE_SIGMOID if sigmoid else ops.GATE_DECAY
+    for reverse in (False, True):
+        turn = (lambda z: None if z is None else z.flip(1)) if reverse else (lambda z: z)
+        got = ops.scan_backward(turn(a), turn(x), turn(h), turn(gh), h0=h0, resets=turn(resets), gate=gate, reverse=reverse)
+        for r in range(b):
+            part = slice(None, t - 1 - at[r])      # before the reset
+            cut = lambda z: None if z is None else host(z[r:r + 1, part])
+            want = oo.scan_backward(cut(a), cut(x), cut(h), cut(gh), host(h0[r:r + 1]), cut(resets), None, sigmoid)
+            for k in ("grad_a", "grad_x"):
+                oo.close(f32(turn(got[k])[r:r + 1, part]), want[k], want["b" + k], kind)
+            oo.close(f32(got["grad_h0"][r:r + 1]), want["grad_h0"], want["bgrad_h0"])
+
+
+def test_scan_an_infinite_sum_outlasts_underflow():
+    """16 steps that join to an infinite state, then 16 whose weights' product underflows: it stays infinite."""
+    a = torch.ones(2, 96, 8, device="cuda")
+    x = torch.zeros_like(a)
+    a[:, 16:32] = 1e-5
+    x[:, 3] = x[:, 12] = torch.finfo(torch.float32).max
+    h = ops.scan_forward(a, x)["h"]
+    assert torch.isfinite(h[:, :12]).all() and (h[:, 12:] == float("inf")).all()
