@@ -447,6 +447,10 @@ typedef struct {
     int64_t stride_a[2], stride_x[2], stride_h[2];       /* between sequences, between steps */
     int64_t stride_gh[2], stride_ga[2], stride_gx[2];    /* the gradients' (per_scan_backward) */
     int64_t stride_resets[2];
+    uint32_t *d_status;    /* device word or NULL: PER_DEVFLAG_TIMEOUT is set in it when a wait ran out */
+    uint32_t wait_limit_ms; /* limit of a wait between the parts of a sequence, 0 .. 10000 (0: 2000) */
+    uint32_t withhold;     /* 0.  To test the limit: the part, 1 .. 16, of each sequence split over parts
+                              that tells the others nothing */
 } per_scan_shape;
 
 /*
@@ -459,8 +463,9 @@ typedef struct {
  * state is kept in binary32; h is rounded to its type where it is stored.  Long sequences are
  * split over time where the channels alone do not fill the GPU; the joints multiply the decays of
  * a stretch, whose product must stay finite in binary32 (decays of magnitude at most 1 always
- * do).  (The parts of a sequence wait for one another with a limit; one that ran out would leave NaN in
- * the states.)  PER_SCAN_REVERSE runs t = T-1 .. 0 (discounted returns: a = gamma, x = reward, a reset at each
+ * do).  The parts of a split sequence wait for one another with a limit.  A wait that runs out sets
+ * PER_DEVFLAG_TIMEOUT in d_status; states that are then not known are NaN, and so is what follows from
+ * them.  PER_SCAN_REVERSE runs t = T-1 .. 0 (discounted returns: a = gamma, x = reward, a reset at each
  * episode's last step).
  *   d_a, d_x [B x T x C], d_h0 [B x C] float or NULL, d_resets [B x T] uint8 or NULL,
  *   d_h [B x T x C], d_last [B x C] float (NULL to skip): the state after the last step; it may be

@@ -87,7 +87,8 @@ class per_verify_shape(ctypes.Structure):
 class per_scan_shape(ctypes.Structure):
     _fields_ = [("steps", ctypes.c_uint64), ("batch", ctypes.c_uint32), ("channels", ctypes.c_uint32),
                 ("type", ctypes.c_uint32), ("flags", ctypes.c_uint32)] + [
-        ("stride_" + n, ctypes.c_int64 * 2) for n in ("a", "x", "h", "gh", "ga", "gx", "resets")]
+        ("stride_" + n, ctypes.c_int64 * 2) for n in ("a", "x", "h", "gh", "ga", "gx", "resets")] + [
+        ("d_status", ctypes.c_void_p), ("wait_limit_ms", ctypes.c_uint32), ("withhold", ctypes.c_uint32)]
 
 
 class PerError(RuntimeError):

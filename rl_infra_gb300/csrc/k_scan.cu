@@ -232,21 +232,21 @@ __device__ __forceinline__ bool mbar_try(unsigned bar, unsigned parity)
                  "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
-// Waits for the phase of the given parity to end; false when it has not after about two seconds.
-__device__ __noinline__ bool mbar_wait_long(unsigned bar, unsigned parity)
+// Waits for the phase of the given parity to end; false when it has not after `limit` ms.
+__device__ __noinline__ bool mbar_wait_long(unsigned bar, unsigned parity, unsigned limit)
 {
     unsigned long long began, now;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(began));
     for (int tries = 0; tries < 1 << 24; ++tries) {
         if (mbar_try(bar, parity)) return true;
         asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
-        if (now - began > 2000000000ull) return false;
+        if (now - began > limit * 1000000ull) return false;
     }
     return false;
 }
-__device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned parity)
+__device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned parity, unsigned limit)
 {
-    return mbar_try(bar, parity) || mbar_wait_long(bar, parity);
+    return mbar_try(bar, parity) || mbar_wait_long(bar, parity, limit);
 }
 __device__ __forceinline__ void store_async(unsigned to, uint4 v, unsigned bar)
 {
@@ -261,7 +261,8 @@ __device__ __forceinline__ unsigned in_cta(unsigned addr, unsigned rank)
 }
 
 // Rounds whose joints have places of their own.  A CTA sends round k + 4 after finishing round k + 2, so
-// after this CTA sent round k + 2, so after this CTA finished round k: nothing is overwritten unread.
+// after this CTA sent round k + 2, so after this CTA finished round k: nothing is overwritten unread.  A warp that
+// sends and has given up a wait does not know that, so it sends nothing more; the other CTAs then give up too.
 constexpr int kDepth = 4;
 
 __device__ __forceinline__ uint4 packed(const Stretch (&s)[2])
@@ -284,7 +285,7 @@ struct Joints {
     unsigned csize, rank;
     int times, time;            // tiles of a strip in a round of the CTA, and which is this warp's
     F2 state;                   // what comes into the round, alike in all groups and warps of the strip
-    bool lost = false;
+    bool lost = false, sends;   // sends: this warp tells the other CTAs of the stretches
 
     static __host__ __device__ size_t bytes(int times, unsigned csize)   // of a strip
     {
@@ -292,7 +293,7 @@ struct Joints {
     }
 
     // mem: strips x bytes(times, csize); the whole cluster calls
-    __device__ __forceinline__ void begin(unsigned char *mem, int strip, int times_, int time_, unsigned csize_, unsigned rank_)
+    __device__ __forceinline__ void begin(const ScanArgs &args, unsigned char *mem, int strip, int times_, int time_, unsigned csize_, unsigned rank_)
     {
         csize = csize_;
         rank = rank_;
@@ -300,6 +301,7 @@ struct Joints {
         time = time_;
         tiles = reinterpret_cast<uint4 *>(mem + strip * bytes(times, csize));
         if (!CLUSTER) return;
+        sends = time == times - 1 && rank + 1 != args.withhold;
         slots = tiles + kDepth * times * 8;
         bar = reinterpret_cast<unsigned long long *>(slots + kDepth * csize * 8);
         if (time == 0 && (threadIdx.x & 31) == 0) {
@@ -361,7 +363,7 @@ struct Joints {
         uint4 *mine = tiles + place * times * 8 + lane % 8;
         if (lane < 8) mine[time * 8] = packed(all);
         __syncthreads();
-        if (CLUSTER && time == times - 1) {   // the CTA's stretch, to four CTAs at a time
+        if (CLUSTER && sends) {   // the CTA's stretch, to four CTAs at a time
             Stretch sum[2], next[2];
             unpacked(mine[0], sum);
             for (int i = 1; i < times; ++i) {
@@ -375,7 +377,7 @@ struct Joints {
     }
 
     // the state that comes into this lane's steps; moves `state` on
-    __device__ __forceinline__ F2 second(int round, const Stretch (&before)[2], const Stretch (&all)[2])
+    __device__ __forceinline__ F2 second(const ScanArgs &args, int round, const Stretch (&before)[2], const Stretch (&all)[2])
     {
         const int lane = threadIdx.x & 31;
         F2 in = state;
@@ -385,9 +387,10 @@ struct Joints {
             const unsigned place = round % kDepth;
             if (CLUSTER) {
                 const unsigned b = smem_u32(&bar[place]);
-                if (!lost) lost = !mbar_wait(b, round / kDepth & 1);
-                if (__any_sync(kFull, lost)) {   // never seen: the states say so
+                if (!lost) lost = !mbar_wait(b, round / kDepth & 1, args.wait_ms);
+                if (__any_sync(kFull, lost)) {   // the status and the states say so
                     lost = true;
+                    sends = false;
                     in = state = {__int_as_float(0x7fffffff), __int_as_float(0x7fffffff)};
                 } else {
                     if (lane == 0 && time == 0) mbar_expect(b, csize * 128);   // for the round that uses it next
@@ -417,9 +420,16 @@ struct Joints {
     }
 
     // nothing of this CTA is read or written any more when the whole cluster has finished every round
-    __device__ __forceinline__ void end() const
+    __device__ __forceinline__ void end(const ScanArgs &args) const
     {
-        if (CLUSTER) cluster_sync_all();
+        if (!CLUSTER) return;
+        cluster_sync_all();
+        if (lost) {
+            if (args.status && (threadIdx.x & 31) == 0) atomicOr(args.status, PER_DEVFLAG_TIMEOUT);
+            // what the others sent and this CTA did not wait for is on its way at most: its memory stays until
+            // that has arrived
+            for (int i = 0; i < 20; ++i) __nanosleep(50000);
+        }
     }
 };
 
@@ -556,7 +566,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_fwd(ScanArgs s
     for (int k = 0; k < (CLUSTER ? AHEAD : ST); ++k) request(k);
     Resets ahead = request_resets<N>(s, me.b, me.t0);
     joints.state = first_state(s.h0, s, me);
-    joints.begin(dyn + (blockDim.x >> 5) * R::BYTES, me.strip, times, me.time, csize, me.rank);
+    joints.begin(s, dyn + (blockDim.x >> 5) * R::BYTES, me.strip, times, me.time, csize, me.rank);
 
     typedef Held<HOLD ? N : 1, HOLD ? N : 1> Tile;
     auto weights = [&](int k, int i, F2 &w, F2 &v) {
@@ -638,7 +648,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_fwd(ScanArgs s
     };
     auto second = [&](int k, const Tile &h) {
         const long long t = me.t0 + k * me.span + me.off;
-        F2 st = joints.second(k, h.before, h.all);
+        F2 st = joints.second(s, k, h.before, h.all);
         const long long stride = s.sh[1];
         T *o = out + t * stride;
         if (!me.live) {
@@ -693,7 +703,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_fwd(ScanArgs s
             second(k, h);
         }
     }
-    joints.end();
+    joints.end(s);
     if (me.time == 0) last_state(s.last, joints.state, s, me);
 }
 
@@ -729,7 +739,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_bwd(ScanArgs s
     for (int k = 0; k < AHEAD; ++k) request(k);
     Resets ahead = request_resets<N>(s, me.b, me.t0);
     joints.state = first_state(s.glast, s, me);
-    joints.begin(dyn + (blockDim.x >> 5) * R::BYTES, me.strip, times, me.time, csize, me.rank);
+    joints.begin(s, dyn + (blockDim.x >> 5) * R::BYTES, me.strip, times, me.time, csize, me.rank);
 
     typedef Held<HOLD ? N : 1, HOLD && SIG ? N : 1> Tile;
     auto first = [&](int k, Tile &d) {
@@ -783,7 +793,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_bwd(ScanArgs s
     };
     auto second = [&](int k, const Tile &d) {
         const long long t = me.t0 + k * me.span + me.off;
-        F2 c = joints.second(k, d.before, d.all);
+        F2 c = joints.second(s, k, d.before, d.all);
         const F2 start = c;
         const long long stride_a = s.sga[1], stride_x = s.sgx[1];
         T *oa = ga + t * stride_a, *ox = gx + t * stride_x;
@@ -874,7 +884,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_bwd(ScanArgs s
             second(k, d);
         }
     }
-    joints.end();
+    joints.end(s);
     if (me.time == 0) last_state(s.gh0, joints.state, s, me);
 }
 

@@ -109,8 +109,18 @@ per_status scan_check(const char *where, const per_scan_shape *sh, bool *empty)
     if ((uint64_t)sh->batch * sh->channels > 0x7fffffffull) return refuse(where, "batch x channels must be below 2^31");
     if (bad_type(sh->type)) return refuse(where, "unknown element type");
     if (sh->flags & ~(uint32_t)(PER_SCAN_SIGMOID | PER_SCAN_REVERSE)) return refuse(where, "unknown flags");
+    if (sh->wait_limit_ms > 10000) return refuse(where, "wait_limit_ms must be at most 10000");
+    if (sh->withhold > 16) return refuse(where, "withhold must be at most 16");
+    if (misaligned(sh->d_status, 4)) return refuse(where, "misaligned pointer");
     *empty = sh->batch == 0 || sh->channels == 0;
     return PER_OK;
+}
+
+void set_waits(ScanArgs &a, const per_scan_shape *sh)
+{
+    a.status = sh->d_status;
+    a.wait_ms = sh->wait_limit_ms ? sh->wait_limit_ms : 2000;
+    a.withhold = sh->withhold;
 }
 
 // Moves an array's start to the first step that the pass takes and turns its time axis.
@@ -242,6 +252,7 @@ per_status per_scan_forward(const per_scan_shape *shape, const void *d_a, const 
     a.steps = (long long)shape->steps;
     a.batch = shape->batch;
     a.channels = shape->channels;
+    set_waits(a, shape);
     return done(launch_scan_forward((int)shape->type, (shape->flags & PER_SCAN_SIGMOID) != 0, a,
                                     reinterpret_cast<cudaStream_t>(stream)), where);
 }
@@ -278,6 +289,7 @@ per_status per_scan_backward(const per_scan_shape *shape, const void *d_a, const
     a.steps = (long long)shape->steps;
     a.batch = shape->batch;
     a.channels = shape->channels;
+    set_waits(a, shape);
     return done(launch_scan_backward((int)shape->type, sig, a, reinterpret_cast<cudaStream_t>(stream)), where);
 }
 

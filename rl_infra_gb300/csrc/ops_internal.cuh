@@ -47,6 +47,9 @@ struct ScanArgs {
     long long sa[2], sx[2], sh[2], sgh[2], sga[2], sgx[2], sr[2];
     long long steps;
     unsigned batch, channels;
+    unsigned *status;
+    unsigned wait_ms;    // limit of a wait between CTAs
+    unsigned withhold;   // the rank, from 1, of the CTA in each cluster that sends nothing (0: none)
 };
 
 enum DistillPart { kDistillForward = 0, kDistillBackward = 1, kDistillStep = 2 };

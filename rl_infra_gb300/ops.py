@@ -32,7 +32,7 @@ _TYPES = {torch.float32: capi.PER_TYPE_F32, torch.float16: capi.PER_TYPE_F16,
 # the C structures per_distill_shape, per_verify_shape and per_scan_shape, packed
 _DISTILL = struct.Struct("@Q4I4qfI")
 _VERIFY = struct.Struct("@4I6q2I")
-_SCAN = struct.Struct("@Q4I14q")
+_SCAN = struct.Struct("@Q4I14qQ2I")
 assert _DISTILL.size == ctypes.sizeof(capi.per_distill_shape)
 assert _VERIFY.size == ctypes.sizeof(capi.per_verify_shape)
 assert _SCAN.size == ctypes.sizeof(capi.per_scan_shape)
@@ -307,10 +307,11 @@ def _resets_ptr(resets, shape, dev):
     return resets.data_ptr()
 
 
-def scan_forward(a, x, h0=None, resets=None, gate=GATE_DECAY, reverse=False, out=None, stream=None):
+def scan_forward(a, x, h0=None, resets=None, gate=GATE_DECAY, reverse=False, out=None, stream=None,
+                 status=None):
     """{"h" [B, T, C], "last" float [B, C]} of h_t = a_t h_{t-1} + x_t (or with a sigmoid gate); h0 float
-    [B, C], resets uint8 or bool [B, T].  reverse: from the last step to the first.  See
-    per_scan_forward."""
+    [B, C], resets uint8 or bool [B, T].  reverse: from the last step to the first.  status int32 [1]
+    takes PER_DEVFLAG_* bits.  See per_scan_forward."""
     code, dev = _lead(a, "a", 3)
     b, t, c = a.shape
     xp = _arg(x, "x", a.shape, a.dtype, dev)
@@ -320,7 +321,7 @@ def scan_forward(a, x, h0=None, resets=None, gate=GATE_DECAY, reverse=False, out
     flags = _gate_flags(gate, reverse)
     if _elsewhere(stream, dev):
         with _On(stream, dev, (a, x, h0, resets)):
-            return scan_forward(a, x, h0, resets, gate, reverse, out)
+            return scan_forward(a, x, h0, resets, gate, reverse, out, None, status)
     h = _given(out, "h", a.shape, a.dtype, dev, a)
     last = _given(out, "last", edge, torch.float32, dev, a)
     if out is not None:
@@ -328,7 +329,8 @@ def scan_forward(a, x, h0=None, resets=None, gate=GATE_DECAY, reverse=False, out
     sa, sx, sh = a.stride(), x.stride(), h.stride()
     sr = resets.stride() if rp is not None else _NO_STRIDE
     _check(_library().per_scan_forward(
-        _SCAN.pack(t, b, c, code, flags, sa[0], sa[1], sx[0], sx[1], sh[0], sh[1], 0, 0, 0, 0, 0, 0, sr[0], sr[1]),
+        _SCAN.pack(t, b, c, code, flags, sa[0], sa[1], sx[0], sx[1], sh[0], sh[1], 0, 0, 0, 0, 0, 0, sr[0], sr[1],
+                   _status_ptr(status, dev) or 0, 0, 0),
         a.data_ptr(), xp, hp, rp, h.data_ptr(), last.data_ptr(), _raw_stream(dev)), "scan_forward")
     return {"h": h, "last": last}
 
@@ -353,13 +355,13 @@ def scan_step(a, x, state, resets=None, gate=GATE_DECAY, out=None, stream=None):
         _whole(new, "state", a.shape, torch.float32, dev)
     _check(_library().per_scan_forward(
         _SCAN.pack(1, b, c, code, flags, a.stride(0), 0, x.stride(0), 0, h.stride(0), 0, 0, 0, 0, 0, 0, 0,
-                   resets.stride(0) if rp is not None else 0, 0),
+                   resets.stride(0) if rp is not None else 0, 0, 0, 0, 0),
         a.data_ptr(), xp, hp, rp, h.data_ptr(), new.data_ptr(), _raw_stream(dev)), "scan_step")
     return {"h": h, "state": new}
 
 
 def scan_backward(a, x, h, grad_h, h0=None, resets=None, grad_last=None, gate=GATE_DECAY, reverse=False, out=None,
-                  stream=None):
+                  stream=None, status=None):
     """{"grad_a", "grad_x" [B, T, C], "grad_h0" float [B, C]} of scan_forward (same arguments) from the h
     that it returned and the gradients of h and of last (None: 0).  x may be None where decays are
     given.  See per_scan_backward."""
@@ -378,7 +380,7 @@ def scan_backward(a, x, h, grad_h, h0=None, resets=None, grad_last=None, gate=GA
     flags = _gate_flags(gate, reverse)
     if _elsewhere(stream, dev):
         with _On(stream, dev, (a, x, h, grad_h, h0, resets, grad_last)):
-            return scan_backward(a, x, h, grad_h, h0, resets, grad_last, gate, reverse, out)
+            return scan_backward(a, x, h, grad_h, h0, resets, grad_last, gate, reverse, out, None, status)
     ga = _given(out, "grad_a", shape, dt, dev, a)
     gx = _given(out, "grad_x", shape, dt, dev, a)
     g0 = _given(out, "grad_h0", edge, torch.float32, dev, a)
@@ -388,7 +390,7 @@ def scan_backward(a, x, h, grad_h, h0=None, resets=None, grad_last=None, gate=GA
     sr = resets.stride() if rp is not None else _NO_STRIDE
     _check(_library().per_scan_backward(
         _SCAN.pack(t, b, c, code, flags, sa[0], sa[1], sx[0], sx[1], sh[0], sh[1], sg[0], sg[1], sga[0], sga[1],
-                   sgx[0], sgx[1], sr[0], sr[1]),
+                   sgx[0], sgx[1], sr[0], sr[1], _status_ptr(status, dev) or 0, 0, 0),
         a.data_ptr(), xp, yp, hp, rp, gp, lp, ga.data_ptr(), gx.data_ptr(), g0.data_ptr(), _raw_stream(dev)),
         "scan_backward")
     return {"grad_a": ga, "grad_x": gx, "grad_h0": g0}

@@ -104,10 +104,69 @@ def test_scan_a_reset_drops_a_gradient_that_overflowed(kind, sigmoid, b, t, c):
 
 
 def test_scan_an_infinite_sum_outlasts_underflow():
-    """16 steps that join to an infinite state, then 16 whose weights' product underflows: it stays infinite."""
+    """16 steps that join to an infinite state, then 16 whose weights' product underflows: no 0 times it."""
     a = torch.ones(2, 96, 8, device="cuda")
     x = torch.zeros_like(a)
     a[:, 16:32] = 1e-5
     x[:, 3] = x[:, 12] = torch.finfo(torch.float32).max
     h = ops.scan_forward(a, x)["h"]
-    assert torch.isfinite(h[:, :12]).all() and (h[:, 12:] == float("inf")).all()
+    assert torch.isfinite(h[:, :12]).all() and (h[:, 12:16] == float("inf")).all() and not torch.isnan(h).any()
+
+
+# -- waits that run out ------------------------------------------------------------------------
+
+def _scan_c(direction, a, x, h, gh, outs, status, **kw):
+    """The C call of a pass over contiguous [B, T, C] arrays."""
+    import ctypes
+    b, t, c = a.shape
+    st = (ctypes.c_int64 * 2)(t * c, c)
+    sh = capi.per_scan_shape(steps=t, batch=b, channels=c, type=capi.PER_TYPE_F32, d_status=status.data_ptr(), **kw)
+    for n in ("a", "x", "h", "gh", "ga", "gx"):
+        setattr(sh, "stride_" + n, st)
+    stream = torch.cuda.current_stream().cuda_stream
+    if direction == "forward":
+        s = capi.per_scan_forward(ctypes.byref(sh), a.data_ptr(), x.data_ptr(), None, None, outs[0].data_ptr(),
+                                  outs[1].data_ptr(), stream)
+    else:
+        s = capi.per_scan_backward(ctypes.byref(sh), a.data_ptr(), None, h.data_ptr(), None, None, gh.data_ptr(), None,
+                                   outs[0].data_ptr(), outs[2].data_ptr(), outs[1].data_ptr(), stream)
+    assert s == capi.PER_OK
+
+
+@pytest.mark.parametrize("direction", ["forward", "backward"])
+@pytest.mark.parametrize("withhold", [1, 2])
+@pytest.mark.parametrize("t", [700, 20000])
+def test_scan_a_wait_that_runs_out_is_reported(direction, withhold, t):
+    """One part of a sequence that is split over CTAs tells the others nothing: the call ends, the status says so, and
+    no state looks valid; the next call is right again."""
+    g = np.random.default_rng(55)
+    a, x, gh = torch.sigmoid(rand(g, 1, t, 16)), rand(g, 1, t, 16), rand(g, 1, t, 16)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    new = lambda: [torch.zeros_like(a), torch.zeros(1, 16, device="cuda"), torch.zeros_like(a)]
+    h = ops.scan_forward(a, x, status=status)["h"]
+    want, bad, got = new(), new(), new()
+    _scan_c(direction, a, x, h, gh, want, status)
+    assert status.item() == 0
+    _scan_c(direction, a, x, h, gh, bad, status, wait_limit_ms=20, withhold=withhold)
+    torch.cuda.synchronize()
+    assert status.item() == capi.PER_DEVFLAG_TIMEOUT
+    assert torch.isnan(bad[0]).all() and torch.isnan(bad[1]).all()
+    status.zero_()
+    _scan_c(direction, a, x, h, gh, got, status, wait_limit_ms=20)
+    assert status.item() == 0
+    for i in range(3):
+        assert torch.equal(got[i], want[i])
+
+
+def test_scan_status_of_the_binding():
+    g = np.random.default_rng(56)
+    a, x = torch.sigmoid(rand(g, 1, 5000, 16)), rand(g, 1, 5000, 16)
+    status = torch.full((1,), 8, dtype=torch.int32, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    h = ops.scan_forward(a, x, status=status, stream=s)["h"]
+    ops.scan_backward(a, x, h, x, status=status, stream=s)
+    s.synchronize()
+    assert status.item() == 8                 # bits are set, never cleared
+    with pytest.raises(TypeError):
+        ops.scan_forward(a, x, status=torch.zeros(1, device="cuda"))
