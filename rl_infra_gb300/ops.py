@@ -141,6 +141,26 @@ def _status_ptr(status, dev):
     return _whole(status, "status", torch.Size((1,)), torch.int32, dev)
 
 
+class _FirstOnly(torch.autograd.Function):
+    """A gradient tied to what it was computed from, whose own derivative is refused.  (torch's
+    once_differentiable lets it pass as a constant where the incoming gradient needs none itself.)"""
+
+    @staticmethod
+    def forward(ctx, grad, *of):
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("second derivatives of the operators in rl_infra_gb300.ops are not available")
+
+
+def _first_only(grad, *of):
+    """`grad`, where a graph of the backward pass is being made (create_graph=True) not as a constant."""
+    if grad is None or not torch.is_grad_enabled():
+        return grad
+    return _FirstOnly.apply(grad, *of)
+
+
 # -- distillation from a teacher's top logits --------------------------------------------------
 
 def _distill_args(logits, top_logits, top_idx, teacher_lse):
@@ -232,11 +252,12 @@ class _DistillLoss(torch.autograd.Function):
         logits, top_logits, top_idx, lse, teacher_lse = ctx.saved_tensors
         got = distill_backward(logits, top_logits, top_idx, lse, grad_loss.contiguous(), ctx.temperature,
                                teacher_lse)
-        return got["grad"], None, None, None, None
+        return _first_only(got["grad"], logits, grad_loss), None, None, None, None
 
 
 def distill_loss(logits, top_logits, top_idx, temperature=1.0, teacher_lse=None):
-    """The row losses [N] (float) as a function that torch.autograd can differentiate by the logits."""
+    """The row losses [N] (float) as a function that torch.autograd can differentiate by the logits, once (a
+    second derivative is refused)."""
     return _DistillLoss.apply(logits, top_logits, top_idx, temperature, teacher_lse)
 
 
@@ -410,9 +431,12 @@ class _GatedScan(torch.autograd.Function):
         if a.shape[-1] > 1 and grad_h.stride(-1) != 1:
             grad_h = grad_h.contiguous()
         got = scan_backward(a, x, h, grad_h, h0, resets, grad_last.contiguous(), ctx.gate, ctx.reverse)
-        return got["grad_a"], got["grad_x"], got["grad_h0"] if h0 is not None else None, None, None, None
+        of = [t for t in (a, x, h0, grad_h, grad_last) if t is not None]
+        return (_first_only(got["grad_a"], *of), _first_only(got["grad_x"], *of),
+                _first_only(got["grad_h0"], *of) if h0 is not None else None, None, None, None)
 
 
 def gated_scan(a, x, h0=None, resets=None, gate=GATE_DECAY, reverse=False):
-    """(h, last) as a function that torch.autograd can differentiate by a, x and h0."""
+    """(h, last) as a function that torch.autograd can differentiate by a, x and h0, once (a second
+    derivative is refused)."""
     return _GatedScan.apply(a, x, h0, resets, gate, reverse)

@@ -170,3 +170,36 @@ def test_scan_status_of_the_binding():
     assert status.item() == 8                 # bits are set, never cleared
     with pytest.raises(TypeError):
         ops.scan_forward(a, x, status=torch.zeros(1, device="cuda"))
+
+
+# -- torch.autograd ----------------------------------------------------------------------------
+
+def test_second_derivatives_are_refused():
+    """The gradients are constants to autograd: differentiating them again must not pass silently."""
+    g = np.random.default_rng(60)
+    x = rand(g, 3, 50).requires_grad_()
+    t, idx = x.detach().topk(4, dim=1)
+    grad, = torch.autograd.grad(ops.distill_loss(x, t, idx).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        (grad.square().sum() + x.square().sum()).backward()
+    a, v = rand(g, 2, 40, 8).requires_grad_(), rand(g, 2, 40, 8).requires_grad_()
+    for gate in (ops.GATE_DECAY, ops.GATE_SIGMOID):
+        h, last = ops.gated_scan(a, v, gate=gate)
+        grad, = torch.autograd.grad(h.square().sum() + last.sum(), v, create_graph=True)
+        with pytest.raises(RuntimeError):
+            (grad.square().sum() + v.square().sum()).backward()
+
+
+def test_a_graph_of_the_backward_pass_that_is_not_used_is_no_error():
+    g = np.random.default_rng(63)
+    a, v = rand(g, 2, 40, 8).requires_grad_(), rand(g, 2, 40, 8).requires_grad_()
+    want = torch.autograd.grad(ops.gated_scan(a, v)[0].sum(), (a, v))
+    got = torch.autograd.grad(ops.gated_scan(a, v)[0].sum(), (a, v), create_graph=True)
+    for w, o in zip(want, got):
+        assert torch.equal(w, o)
+    # a path that does not lead through the operator's gradient stays differentiable
+    x = rand(g, 3, 50).requires_grad_()
+    t, idx = x.detach().topk(4, dim=1)
+    z, = torch.autograd.grad(ops.distill_loss(x.detach() * 2, t, idx).sum() + x.square().sum(), x, create_graph=True)
+    z.sum().backward()
+    assert torch.equal(x.grad, torch.full_like(x, 2.0))
