@@ -92,20 +92,21 @@ def _given(out, name, shape, dtype, dev, like):
 
 
 class _On:
-    """Runs a call on `stream` where that is not the current stream (or device): outputs are
-    allocated for it, and the inputs' memory is held until the stream has passed the call."""
+    """Runs a call on `stream` where that is not the current stream (or device): new outputs are
+    allocated for it, and the memory of the inputs, the caller's outputs and the status is held until
+    the stream has passed the call."""
 
-    def __init__(self, stream, dev, inputs):
-        self.dev, self.inputs, self.guard = dev, inputs, None
-        self.stream = stream
+    def __init__(self, stream, dev, inputs, out, status):
+        self.stream = stream if stream is not None else torch.cuda.current_stream(dev)
+        self.tensors = [*inputs, *(out or {}).values(), status]
+        self.guard = None
 
     def __enter__(self):
-        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.dev)
-        self.guard = torch.cuda.stream(s)
+        self.guard = torch.cuda.stream(self.stream)
         self.guard.__enter__()
-        for t in self.inputs:
-            if t is not None:
-                t.record_stream(s)
+        for t in self.tensors:
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                t.record_stream(self.stream)
         return self
 
     def __exit__(self, *exc):
@@ -188,7 +189,7 @@ def distill_forward(logits, top_logits, top_idx, temperature=1.0, teacher_lse=No
     [N, K] (negative: left out); see per_distill_forward."""
     code, dev, n, v, tcode, k, tp, ip, lp = _distill_args(logits, top_logits, top_idx, teacher_lse)
     if _elsewhere(stream, dev):
-        with _On(stream, dev, (logits, top_logits, top_idx, teacher_lse)):
+        with _On(stream, dev, (logits, top_logits, top_idx, teacher_lse), out, status):
             return distill_forward(logits, top_logits, top_idx, temperature, teacher_lse, out, status)
     loss = _given(out, "loss", (n,), torch.float32, dev, logits)
     lse = _given(out, "lse", (n,), torch.float32, dev, logits)
@@ -208,7 +209,7 @@ def distill_backward(logits, top_logits, top_idx, lse, row_scale=None, temperatu
     ep = _whole(lse, "lse", torch.Size((n,)), torch.float32, dev)
     sp = _whole(row_scale, "row_scale", torch.Size((n,)), torch.float32, dev)
     if _elsewhere(stream, dev):
-        with _On(stream, dev, (logits, top_logits, top_idx, lse, row_scale, teacher_lse)):
+        with _On(stream, dev, (logits, top_logits, top_idx, lse, row_scale, teacher_lse), out, status):
             return distill_backward(logits, top_logits, top_idx, lse, row_scale, temperature, teacher_lse, out,
                                     status)
     grad = _given(out, "grad", (n, v), logits.dtype, dev, logits)
@@ -227,7 +228,7 @@ def distill_step(logits, top_logits, top_idx, row_scale=None, temperature=1.0, t
     code, dev, n, v, tcode, k, tp, ip, lp = _distill_args(logits, top_logits, top_idx, teacher_lse)
     sp = _whole(row_scale, "row_scale", torch.Size((n,)), torch.float32, dev)
     if _elsewhere(stream, dev):
-        with _On(stream, dev, (logits, top_logits, top_idx, row_scale, teacher_lse)):
+        with _On(stream, dev, (logits, top_logits, top_idx, row_scale, teacher_lse), out, status):
             return distill_step(logits, top_logits, top_idx, row_scale, temperature, teacher_lse, out, status)
     loss = _given(out, "loss", (n,), torch.float32, dev, logits)
     lse = _given(out, "lse", (n,), torch.float32, dev, logits)
@@ -288,7 +289,7 @@ def verify_draft(target_probs, draft_probs, draft_tokens, accept_u, sample_u, dr
         qp = _arg(draft_probs, "draft_probs", torch.Size((b, d, v)), target_probs.dtype, dev)
         q0, q1 = draft_probs.stride(0), draft_probs.stride(1)
     if _elsewhere(stream, dev):
-        with _On(stream, dev, (target_probs, draft_probs, draft_tokens, accept_u, sample_u, draft_lens)):
+        with _On(stream, dev, (target_probs, draft_probs, draft_tokens, accept_u, sample_u, draft_lens), out, status):
             return verify_draft(target_probs, draft_probs, draft_tokens, accept_u, sample_u, draft_lens, out, status)
     got = {"accepted": _given(out, "accepted", (b,), torch.int32, dev, target_probs),
            "tokens": _given(out, "tokens", (b, d1), torch.int32, dev, target_probs),
@@ -341,7 +342,7 @@ def scan_forward(a, x, h0=None, resets=None, gate=GATE_DECAY, reverse=False, out
     rp = _resets_ptr(resets, (b, t), dev)
     flags = _gate_flags(gate, reverse)
     if _elsewhere(stream, dev):
-        with _On(stream, dev, (a, x, h0, resets)):
+        with _On(stream, dev, (a, x, h0, resets), out, status):
             return scan_forward(a, x, h0, resets, gate, reverse, out, None, status)
     h = _given(out, "h", a.shape, a.dtype, dev, a)
     last = _given(out, "last", edge, torch.float32, dev, a)
@@ -368,7 +369,7 @@ def scan_step(a, x, state, resets=None, gate=GATE_DECAY, out=None, stream=None):
     rp = _resets_ptr(resets, (b,), dev)
     flags = _gate_flags(gate, False)
     if _elsewhere(stream, dev):
-        with _On(stream, dev, (a, x, state, resets)):
+        with _On(stream, dev, (a, x, state, resets), out, None):
             return scan_step(a, x, state, resets, gate, out)
     h = _given(out, "h", a.shape, a.dtype, dev, a)
     new = _given(out, "state", a.shape, torch.float32, dev, a)
@@ -400,7 +401,7 @@ def scan_backward(a, x, h, grad_h, h0=None, resets=None, grad_last=None, gate=GA
     rp = _resets_ptr(resets, (b, t), dev)
     flags = _gate_flags(gate, reverse)
     if _elsewhere(stream, dev):
-        with _On(stream, dev, (a, x, h, grad_h, h0, resets, grad_last)):
+        with _On(stream, dev, (a, x, h, grad_h, h0, resets, grad_last), out, status):
             return scan_backward(a, x, h, grad_h, h0, resets, grad_last, gate, reverse, out, None, status)
     ga = _given(out, "grad_a", shape, dt, dev, a)
     gx = _given(out, "grad_x", shape, dt, dev, a)

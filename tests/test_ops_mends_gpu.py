@@ -203,3 +203,47 @@ def test_a_graph_of_the_backward_pass_that_is_not_used_is_no_error():
     z, = torch.autograd.grad(ops.distill_loss(x.detach() * 2, t, idx).sum() + x.square().sum(), x, create_graph=True)
     z.sum().backward()
     assert torch.equal(x.grad, torch.full_like(x, 2.0))
+
+
+# -- other streams -----------------------------------------------------------------------------
+
+def _cases(g):
+    x = rand(g, 32, 40000)
+    t, idx = x.topk(4, dim=1)
+    a, v, h0 = torch.sigmoid(rand(g, 2, 3000, 256)), rand(g, 2, 3000, 256), rand(g, 2, 256)
+    p = torch.softmax(rand(g, 2000, 3, 64), -1)
+    tok, u, us = torch.zeros(2000, 2, device="cuda").int(), torch.rand(2000, 2, device="cuda"), torch.rand(2000, device="cuda")
+    lse = ops.distill_forward(x, t, idx)["lse"]
+    h = ops.scan_forward(a, v)["h"]
+    status = dict(status=torch.zeros(1, dtype=torch.int32, device="cuda"))
+    return {"distill_forward": ((x, t, idx), status), "distill_backward": ((x, t, idx, lse), status),
+            "distill_step": ((x, t, idx), status), "verify_draft": ((p, p[:, :2].contiguous(), tok, u, us), status),
+            "scan_forward": ((a, v), status), "scan_step": ((v[:, 0], v[:, 0], h0), {}), "scan_backward": ((a, v, h, v), status)}
+
+
+@pytest.mark.parametrize("name", ["distill_forward", "distill_backward", "distill_step", "verify_draft", "scan_forward", "scan_step",
+                                  "scan_backward"])
+def test_outputs_given_to_another_stream_are_held(name):
+    """The caller drops its own outputs and the status while the other stream has yet to write them: their memory is
+    not given out again before it has."""
+    args, kw = _cases(np.random.default_rng(70))[name]
+    call = getattr(ops, name)
+    want = call(*args, **kw)
+    out = {k: torch.empty_like(z) for k, z in want.items()}
+    kw = {k: z.clone() for k, z in kw.items()}
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)             # about 0.1 s
+    call(*args, **kw, out=out, stream=s)
+    mine = [*out.values(), *kw.values()]
+    held = {z.data_ptr(): z.untyped_storage().nbytes() for z in mine}
+    sizes = [z.shape for z in mine]
+    dtypes = [z.dtype for z in mine]
+    del out, mine, kw
+    again = [torch.empty(z, dtype=d, device="cuda") for z, d in zip(sizes, dtypes) for _ in range(4)]
+    assert not s.query(), "the other stream has already passed the call"
+    for z in again:
+        for at, n in held.items():
+            assert z.data_ptr() + z.untyped_storage().nbytes() <= at or z.data_ptr() >= at + n, "memory given out again"
+    s.synchronize()
