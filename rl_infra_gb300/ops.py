@@ -98,6 +98,8 @@ class _On:
 
     def __init__(self, stream, dev, inputs, out, status):
         self.stream = stream if stream is not None else torch.cuda.current_stream(dev)
+        if self.stream.device_index != dev:
+            raise ValueError(f"stream must be of cuda:{dev}, the tensors' device, got {self.stream}")
         self.tensors = [*inputs, *(out or {}).values(), status]
         self.guard = None
 

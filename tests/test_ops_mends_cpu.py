@@ -1,4 +1,5 @@
-"""What the operators' C calls refuse of the settings of their waits (nothing is enqueued, so no GPU is needed)."""
+"""What the operators' C calls refuse of the settings of their waits, and the binding of streams (nothing is
+enqueued, so no GPU is needed)."""
 from __future__ import annotations
 
 import ctypes
@@ -27,3 +28,14 @@ def test_scan_refuses_settings_of_its_waits(kw, said):
     assert capi.per_scan_backward(ctypes.byref(sh), ONE, ONE, ONE, None, None, ONE, None, ONE, ONE, None, None) == \
         capi.PER_ERR_INVALID_ARG
     assert said in capi.per_last_op_error()
+
+
+def test_binding_refuses_a_stream_of_another_device():
+    """(It ran on the current stream of the tensors' device instead.)"""
+    from rl_infra_gb300 import ops
+
+    class Stream:
+        device_index = 1
+
+    with pytest.raises(ValueError, match="stream must be of cuda:0"):
+        ops._On(Stream(), 0, (), None, None)
