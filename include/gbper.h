@@ -460,7 +460,8 @@ typedef struct {
  * h_{-1} is d_h0 (NULL: 0).  A step with d_resets[b, t] != 0 starts an episode: the state that comes into it counts
  * as 0, whatever it holds.  A weight of exactly 0 likewise drops what it multiplies, infinities and NaN
  * too (a gate of -inf drops the state, of +inf the input: padding can hold anything).  The
- * state is kept in binary32; h is rounded to its type where it is stored.  Long sequences are
+ * state is kept in binary32; h is rounded to its type where it is stored.  f and 1 - f are good to a relative
+ * 2^-21 where a is binary32, to 2^-21 + |a| 2^-24 where it is not; an f below 2^-126 counts as 0.  Long sequences are
  * split over time where the channels alone do not fill the GPU; the joints multiply the decays of
  * a stretch, whose product must stay finite in binary32 (decays of magnitude at most 1 always
  * do).  The parts of a split sequence wait for one another with a limit.  A wait that runs out sets

@@ -65,20 +65,39 @@ struct Gate {
     float w, v;   // the state's weight f and the input's 1 - f
 };
 
-// f = 1 / (1 + e), 1 - f = e f with e = exp(-a): neither loses digits to a subtraction.
-template <bool SIG>
+// exp(-a) of two gates, by powers of 2.  x = -a log2(e) is off by its rounding, a relative |a| 2^-24 of the power and
+// 2^-22 more of its own (4e-6 at a gate of 80).  For binary32 gates that is made up for: 2^x times 1 - (a + x ln 2), the
+// difference small and good to 2^-24 of itself by two fused steps over ln 2 in two parts.  (Not finite below
+// about -88, where it would be 0 or NaN as a weight and the careful way is taken.)  The 16-bit passes, which
+// their instructions bound and whose gates are rounded to 2^-9 or 2^-12 themselves, take 2^x.
+template <typename T>
+__device__ __forceinline__ F2 exp_minus(F2 a)
+{
+    const F2 x = a * F2{-kLog2e, -kLog2e};
+    F2 e{ex2(x.x), ex2(x.y)};
+    if constexpr (sizeof(T) == 4) {
+        constexpr float kLn2 = 0.693147182f, kLn2Rest = -1.90465421e-9f;
+        const F2 minus{-1.0f, -1.0f};
+        const F2 r = fma2(x, F2{-kLn2Rest, -kLn2Rest}, fma2(x, F2{-kLn2, -kLn2}, a * minus));
+        e = fma2(e, r, e);
+    }
+    return e;
+}
+
+// f = 1 / (1 + e), 1 - f = e f with e = exp(-a): neither loses digits to a subtraction.  (f below 2^-126 is 0.)
+template <typename T, bool SIG>
 __device__ __forceinline__ Gate gate(float a)
 {
     if (!SIG) return {a, 1.0f};
-    const float e = ex2(a * -kLog2e), f = rcp(1.0f + e);
+    const float e = sizeof(T) == 4 ? expf(-a) : ex2(a * -kLog2e), f = rcp(1.0f + e);
     return {f, f == 0.0f ? 1.0f : e * f};
 }
 
 // the same of two gates that are not 0
+template <typename T>
 __device__ __forceinline__ void gates(F2 a, F2 &w, F2 &v)
 {
-    const F2 x = a * F2{-kLog2e, -kLog2e};
-    const F2 e{ex2(x.x), ex2(x.y)};
+    const F2 e = exp_minus<T>(a);
     const F2 d = e + F2{1.0f, 1.0f};
     w = {rcp(d.x), rcp(d.y)};
     v = e * w;
@@ -576,7 +595,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_fwd(ScanArgs s
         v = ring.read(k, 1, i);
         if constexpr (SIG) {
             F2 c;
-            gates(w, w, c);
+            gates<T>(w, w, c);
             v = v * c;
         }
     };
@@ -585,7 +604,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_fwd(ScanArgs s
         w = 1.0f;
         v = 0.0f;
         if (!valid) return;
-        const Gate g = gate<SIG>(at(ring.read(k, 0, i), c));
+        const Gate g = gate<T, SIG>(at(ring.read(k, 0, i), c));
         v = at(ring.read(k, 1, i), c);
         v = SIG ? weigh(g.v, v, 0.0f) : v;
         w = reset ? 0.0f : g.w;
@@ -757,7 +776,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_bwd(ScanArgs s
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 F2 w = ring.read(k, 0, i), v;
-                if constexpr (SIG) gates(w, w, v);
+                if constexpr (SIG) gates<T>(w, w, v);
                 if constexpr (HOLD) d.w[i] = w;
                 if constexpr (HOLD && SIG) d.v[i] = v;
                 H = w * (H + ring.read(k, 1, i));
@@ -783,7 +802,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_bwd(ScanArgs s
 #pragma unroll 1
                 for (int i = 0; i < N; ++i) {
                     if (!((c ? me.second : me.live) && t + i < s.steps)) break;
-                    const float w = resets >> i & 1u ? 0.0f : gate<SIG>(at(ring.read(k, 0, i), c)).w;
+                    const float w = resets >> i & 1u ? 0.0f : gate<T, SIG>(at(ring.read(k, 0, i), c)).w;
                     drop = drop || w == 0.0f;
                     own[c].H = weigh(w, own[c].H + at(ring.read(k, 1, i), c), 0.0f);
                     own[c].A *= w;
@@ -813,7 +832,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_bwd(ScanArgs s
                         if constexpr (SIG) v = d.v[i];
                     } else {
                         w = ring.read(k, 0, i);
-                        if constexpr (SIG) gates(w, w, v);
+                        if constexpr (SIG) gates<T>(w, w, v);
                     }
                     if (reset) before = {0.0f, 0.0f};
                     if constexpr (SIG) {
@@ -848,7 +867,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_bwd(ScanArgs s
                 F2 da, dx;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const Gate f = gate<SIG>(at(rw, e));
+                    const Gate f = gate<T, SIG>(at(rw, e));
                     const float g = at(rg, e) + at(c, e), before = reset ? 0.0f : at(rb, e);
                     if (SIG) {
                         const float slope = f.w * f.v;
@@ -965,7 +984,7 @@ __global__ void __launch_bounds__(128) k_scan_few(ScanArgs s)
             C::unpack(rx[i], v);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                const Gate g = gate<SIG>(w[e]);
+                const Gate g = gate<T, SIG>(w[e]);
                 h[e] = weigh(reset[i] ? 0.0f : g.w, h[e], SIG ? weigh(g.v, v[e], 0.0f) : v[e]);
             }
             C::store(out + (t + i) * s.sh[1], h);
@@ -1027,7 +1046,7 @@ __global__ void __launch_bounds__(128) k_scan_few_bwd(ScanArgs s)
             }
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                const Gate f = gate<SIG>(w[e]);
+                const Gate f = gate<T, SIG>(w[e]);
                 const float gt = g[e] + c[e], bt = reset[i] ? 0.0f : before[e];
                 if (SIG) {
                     const float slope = f.w * f.v;

@@ -247,3 +247,35 @@ def test_outputs_given_to_another_stream_are_held(name):
         for at, n in held.items():
             assert z.data_ptr() + z.untyped_storage().nbytes() <= at or z.data_ptr() >= at + n, "memory given out again"
     s.synchronize()
+
+
+# -- what binary32 keeps -----------------------------------------------------------------------
+
+@pytest.mark.parametrize("t", [2, 64, 4096])
+def test_scan_gates_keep_their_digits(t):
+    """f and 1 - f of large gates, each read off a state, for one thread a channel and for tiles.  e = exp(-a) to
+    4 U (a power of 2 to 2^-22) and its last product (U), at most once in f as in 1 - f = e f; 1 + e rounded (U), its
+    reciprocal to 1 ulp (2 U) and e f rounded (U): 9 U."""
+    c = 512
+    a = torch.zeros(1, t, c, device="cuda")
+    a[0, 0::2] = 80.0                                # a new episode: the state is the input's weight times x
+    a[0, 1::2] = torch.linspace(-80, 80, c, device="cuda")
+    x = torch.zeros_like(a)
+    resets = torch.zeros(1, t, dtype=torch.uint8, device="cuda")
+    resets[0, 0::2] = 1
+    # 1 - f: a reset, then x = 1
+    ones = torch.ones_like(a)
+    v = ops.scan_forward(a.flip(1), ones, resets=torch.ones_like(resets), gate=ops.GATE_SIGMOID)["h"]
+    e = np.exp(-host(a.flip(1)))
+    np.testing.assert_allclose(host(v), e / (1 + e), rtol=9 * oo.U, atol=0)
+    # f: a state of 1 (a gate of -80 takes x whole), then x = 0
+    a[0, 0::2] = -80.0
+    x[0, 0::2] = 1.0
+    h = ops.scan_forward(a, x, resets=resets, gate=ops.GATE_SIGMOID)["h"]
+    assert (h[0, 0::2] == 1).all()
+    f = 1 / (1 + np.exp(-host(a[0, 1::2])))
+    np.testing.assert_allclose(host(h[0, 1::2]), f, rtol=9 * oo.U, atol=0)
+    # the gradient of x: 1 - f (a reset at each step, so that g = gh)
+    back = ops.scan_backward(a, x, h, ones, resets=torch.ones_like(resets), gate=ops.GATE_SIGMOID)
+    e = np.exp(-host(a))
+    np.testing.assert_allclose(host(back["grad_x"]), e / (1 + e), rtol=9 * oo.U, atol=0)
