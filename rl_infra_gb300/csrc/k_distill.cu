@@ -1,7 +1,7 @@
 // k_distill.cu -- the loss of a student's logits against a teacher's top logits, and its gradient.
 //
 // Mathematics.  With c = log2(e) / tau, a row's soft maximum is lse = m + tau ln s, m = max x, s =
-// sum 2^((x - m) c); (m, s) of two stretches join by rescaling each s to the larger m, so one pass
+// sum exp((x - m) / tau) = sum 2^((x - m) c); (m, s) of two stretches join by rescaling each s to the larger m, so one pass
 // over a row suffices, split over threads, warps and CTAs, joined in a fixed order.  The differences
 // are taken before they are scaled: x - m is exact where it matters and logits of the type's lowest
 // value do not overflow.  -inf contributes 0; NaN and +inf make s NaN.
@@ -47,14 +47,46 @@ struct RowSum {
     float m, s;
 };
 
+// log2(e) / tau in two parts: the nearest binary32 and what that leaves
+struct Scale {
+    float c, rest;
+};
+
 __device__ __forceinline__ float finite_or_zero(float m) { return m == -kInf ? 0.0f : m; }
 
-__device__ __forceinline__ RowSum join(RowSum a, RowSum b, float c)
+// exp(d / tau) of two differences (-inf gives 0, NaN stays).  The power of 2 is good to 2^-22; the rounding of its
+// argument takes a relative |d / tau| 2^-24 more (4e-6 at 60), which MORE makes up for by the first order of what
+// it left out.  The gradient of binary32 elements and the teacher's q have that.  Sums do not: with p the share of
+// a term, sum p |d / tau| = H(p) - ln s <= ln V, so a sum is off by at most ln V 2^-24 for it (and with it, forward
+// 2048 x 131072 f32 took 315 us against 267).  Nor have 16-bit gradients, rounded to 2^-9 or 2^-12 in the end.
+template <bool MORE>
+__device__ __forceinline__ F2 exps(F2 d, Scale k)
+{
+    const F2 minus_x = d * F2{-k.c, -k.c};
+    F2 v{ex2(-minus_x.x), ex2(-minus_x.y)};
+    if constexpr (MORE) {
+        constexpr float kLn2 = 0.693147182f;
+        F2 r = fma2(d, F2{k.rest, k.rest}, fma2(d, F2{k.c, k.c}, minus_x)) * F2{kLn2, kLn2};
+        // (infinite or NaN where x is -inf: the power is 0 then, and stays; a NaN in d is in v)
+        r.x = fminf(r.x, 1.0f);
+        r.y = fminf(r.y, 1.0f);
+        v = fma2(v, r, v);
+    }
+    return v;
+}
+
+template <bool MORE>
+__device__ __forceinline__ float exps(float d, Scale k)
+{
+    return exps<MORE>(F2{d, 0.0f}, k).x;
+}
+
+__device__ __forceinline__ RowSum join(RowSum a, RowSum b, Scale c)
 {
     RowSum r;
     r.m = fmaxf(a.m, b.m);
     const float e = finite_or_zero(r.m);
-    r.s = a.s * ex2((a.m - e) * c) + b.s * ex2((b.m - e) * c);
+    r.s = a.s * exps<false>(a.m - e, c) + b.s * exps<false>(b.m - e, c);
     return r;
 }
 
@@ -124,25 +156,24 @@ struct Running {
             return r;
         }
     }
-    __device__ __forceinline__ void add(const Pack<T> (&in)[kUnroll], float c)
+    __device__ __forceinline__ void add(const Pack<T> (&in)[kUnroll], Scale c)
     {
         const float b = largest(in);
         if (b > m) {
-            const float k = ex2((m - b) * c);   // 0 at first
+            const float k = exps<false>(m - b, c);   // 0 at first
             s0 = s0 * F2{k, k};
             s1 = s1 * F2{k, k};
             m = b;
         }
         const float r = -finite_or_zero(m);
-        const F2 ref{r, r}, cc{c, c};
+        const F2 ref{r, r};
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
             float f[P];
             in[i].unpack(f);
 #pragma unroll
             for (int e = 0; e < P; e += 2) {
-                const F2 x = (F2{f[e], f[e + 1]} + ref) * cc;
-                const F2 v{ex2(x.x), ex2(x.y)};
+                const F2 v = exps<false>(F2{f[e], f[e + 1]} + ref, c);
                 if (e & 2) s1 = s1 + v;
                 else s0 = s0 + v;
             }
@@ -227,12 +258,12 @@ struct Pieces {
 };
 
 // The join of n stretches: the largest maximum first, then the rescaled sums in their order.
-__device__ __forceinline__ RowSum gather(const RowSum *p, int n, float c)
+__device__ __forceinline__ RowSum gather(const RowSum *p, int n, Scale c)
 {
     RowSum r{-kInf, 0.0f};
     for (int i = 0; i < n; ++i) r.m = fmaxf(r.m, p[i].m);
     const float e = finite_or_zero(r.m);
-    for (int i = 0; i < n; ++i) r.s += p[i].s * ex2((p[i].m - e) * c);
+    for (int i = 0; i < n; ++i) r.s += p[i].s * exps<false>(p[i].m - e, c);
     return r;
 }
 
@@ -262,7 +293,7 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, kCtasPerSm) k_distill(Di
     const int K = (int)a.k;
     const unsigned rank = blockIdx.x % csize;   // also the CTA's rank in its cluster, where there is one
     const long long row = blockIdx.x / csize;
-    const float c = kLog2e / a.tau;
+    const Scale c{a.c, a.c_rest};
     const int loaders = (int)blockDim.x - 32, t = (int)threadIdx.x, lane = t & 31;
     pdl_wait();
     pdl_release();
@@ -302,19 +333,21 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, kCtasPerSm) k_distill(Di
             tm = fmaxf(tm, v);
         }
         for (int o = 16; o; o >>= 1) tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, o));
-        float L;
+        // log q = (t - e) - l: the difference from the largest first, so that what all entries share costs no digits
+        float e, l;
         if (a.teacher_lse) {
-            L = a.teacher_lse[row];
+            e = a.teacher_lse[row];
+            l = 0.0f;
         } else {
-            const float e = finite_or_zero(tm);
+            e = finite_or_zero(tm);
             float s = 0.0f;
-            for (int k = lane; k < K; k += 32) s += ex2((d[k] - e) * c);
+            for (int k = lane; k < K; k += 32) s += exps<true>(d[k] - e, c);
             for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            L = s == 0.0f ? 0.0f : e + a.tau * logf(s);
+            l = s == 0.0f ? 0.0f : a.tau * logf(s);
         }
         float S = 0.0f;
         for (int k = lane; k < K; k += 32) {
-            const float v = d[k] - L, w = at[k] >= 0 ? ex2(v * c) : 0.0f;
+            const float v = (d[k] - e) - l, w = at[k] >= 0 ? exps<true>(v, c) : 0.0f;
             d[k] = v;
             q[k] = w;
             S += w;
@@ -452,11 +485,12 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, kCtasPerSm) k_distill(Di
             cluster_sync_all();
             all = gather(sh.cluster, (int)csize, c);
         }
-        lse = all.s == 0.0f ? -kInf : finite_or_zero(all.m) + a.tau * logf(all.s);
+        const float m = finite_or_zero(all.m), l = a.tau * logf(all.s);
+        lse = all.s == 0.0f ? -kInf : m + l;
         if (rank == 0 && t >= loaders) {
             float loss = 0.0f;
             for (int k = lane; k < K; k += 32)
-                if (q[k] != 0.0f) loss += q[k] * (d[k] - (xk[k] - lse));
+                if (q[k] != 0.0f) loss += q[k] * (d[k] - ((xk[k] - m) - l));
             for (int o = 16; o; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
             if (lane == 0) {
                 a.loss[row] = sh.some && lse != -kInf ? a.tau * loss : 0.0f;
@@ -479,15 +513,14 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, kCtasPerSm) k_distill(Di
     const int misg = (int)(reinterpret_cast<uintptr_t>(out) % 16 / sizeof(T));
     if (t < loaders && j0 < j1) {
         const int o0 = (j0 + misg) / P, o1 = (j1 - 1 + misg) / P + 1, first = o0 + (t & ~31), step = loaders * kUnroll;
-        const F2 ref{-lse, -lse}, cc{c, c}, ff{f0, f0};
+        const F2 ref{-lse, -lse}, ff{f0, f0};
         Pieces<T> from(cells, j0, j1, o0 * P - misg);
         auto turn = [&](Pack<T> &in) {
             float f[P];
             in.unpack(f);
 #pragma unroll
             for (int e = 0; e < P; e += 2) {
-                const F2 x = (F2{f[e], f[e + 1]} + ref) * cc;
-                const F2 y = F2{ex2(x.x), ex2(x.y)} * ff;
+                const F2 y = exps<sizeof(T) == 4>(F2{f[e], f[e + 1]} + ref, c) * ff;
                 f[e] = y.x;
                 f[e + 1] = y.y;
             }
@@ -560,7 +593,7 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, kCtasPerSm) k_distill(Di
             if (!first) continue;
         }
         const float v = to_f32(cells[p]);
-        out[p] = from_f32<T>(f0 * ex2((v - lse) * c) - g * sum);
+        out[p] = from_f32<T>(f0 * exps<sizeof(T) == 4>(v - lse, c) - g * sum);
     }
 }
 

@@ -98,6 +98,9 @@ per_status distill(const char *where, DistillPart part, const per_distill_shape 
     a.top_type = (int)sh->top_type;
     a.idx64 = (sh->flags & PER_DISTILL_IDX64) != 0;
     a.tau = sh->temperature;
+    const double c = 1.4426950408889634 / (double)sh->temperature;
+    a.c = (float)c;
+    a.c_rest = (float)(c - (double)a.c);
     return done(launch_distill((int)sh->type, part, a, reinterpret_cast<cudaStream_t>(stream)), where);
 }
 

@@ -23,7 +23,7 @@ struct DistillArgs {
     unsigned vocab, k;
     int top_type;
     int idx64;
-    float tau;
+    float tau, c, c_rest;       // c + c_rest: log2(e) / tau
 };
 
 struct VerifyArgs {

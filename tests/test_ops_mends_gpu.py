@@ -279,3 +279,60 @@ def test_scan_gates_keep_their_digits(t):
     back = ops.scan_backward(a, x, h, ones, resets=torch.ones_like(resets), gate=ops.GATE_SIGMOID)
     e = np.exp(-host(a))
     np.testing.assert_allclose(host(back["grad_x"]), e / (1 + e), rtol=9 * oo.U, atol=0)
+
+
+@pytest.mark.parametrize("tau", [0.05, 0.25, 1.0, 3.0])
+@pytest.mark.parametrize("lead", [0, 1])
+def test_distill_probabilities_keep_their_digits(tau, lead):
+    """The gradient of f32 logits away from the teacher's one entry is tau p, with the normaliser given.  Logits and
+    normaliser are whole multiples of 2^-10, so their difference is exact.  The power of 2 is good to 2^-22 (4 U), its
+    argument's rounding is made up for, and each product and sum that follows rounds once: 9 U."""
+    g = np.random.default_rng(61)
+    n, v = 4, 30011
+    low = -60 * tau
+    x = torch.from_numpy(np.round(g.uniform(low, 0, size=(n, v)) * 1024).astype(np.float32) / 1024).cuda()
+    store = torch.zeros(n * v + lead, device="cuda")
+    xs = store[lead:].view(n, v)
+    xs.copy_(x)
+    lse = torch.full((n,), 0.5, device="cuda")
+    idx = torch.zeros(n, 1, dtype=torch.int32, device="cuda")
+    got = ops.distill_backward(xs, torch.zeros(n, 1, device="cuda"), idx, lse, temperature=tau)["grad"]
+    tau32 = float(np.float32(tau))
+    want = tau32 * np.exp((host(x) - 0.5) / tau32)
+    np.testing.assert_allclose(host(got)[:, 1:], want[:, 1:], rtol=9 * oo.U, atol=0)
+
+
+@pytest.mark.parametrize("tau", [0.25, 1.0, 3.0])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_distill_losses_do_not_lose_digits_to_a_common_offset(kind, tau):
+    """The loss does not change with what all logits of a row share.  Everything is a whole multiple of 2^-10 (bf16
+    students of 4), so differences from a row's largest are exact.  With y and z those of a teacher's entry and of the
+    student there, over tau: q is good to (12 + K) U relative, log q = y - ln S to (2 |y| + 2 ln S + 8 + K) U,
+    log p = z - ln s to (2 |z| + 2 ln s + 48) U (1009 terms in groups of about 32), their difference rounds once and so
+    do the products and the K sums."""
+    g = np.random.default_rng(62)
+    n, v, k = 32, 1009, 8
+    grid = lambda w, s: np.round(w * s) / s
+    if kind == "f32":
+        x = grid(g.normal(size=(n, v)) * tau, 1024) + 3000.0
+        t = grid(g.normal(size=(n, k)) * tau, 1024) - 2000.0
+    else:
+        x = grid(g.normal(size=(n, v)) * 4 * tau, 0.25) + 600.0
+        t = grid(g.normal(size=(n, k)) * tau, 1024) - 2000.0
+    idx = np.stack([g.permutation(v)[:k] for _ in range(n)])
+    dev = lambda z, kd="f32": torch.from_numpy(np.asarray(z, np.float32)).cuda().to(TYPES[kd])
+    xs, ts = dev(x, kind), dev(t)
+    assert (host(xs) == x).all() and (host(ts) == t).all()
+    at = torch.from_numpy(idx).int().cuda()
+    got = [ops.distill_forward(xs, ts, at, temperature=tau)["loss"], ops.distill_step(xs, ts, at, temperature=tau)["loss"]]
+    y = (t - t.max(1, keepdims=True)) / tau
+    z = (x - x.max(1, keepdims=True)) / tau
+    S, s = np.exp(y).sum(1, keepdims=True), np.exp(z).sum(1, keepdims=True)
+    z = np.take_along_axis(z, idx, 1)
+    q, lq, lp = np.exp(y) / S, y - np.log(S), z - np.log(s)
+    want = tau * tau * (q * (lq - lp)).sum(1)
+    d = np.abs(lq - lp)
+    off = q * ((13 + k) * d + 2 * np.abs(y) + 2 * np.log(S) + 2 * np.abs(z) + 2 * np.log(s) + 56 + k)
+    bound = oo.U * (tau * tau * off.sum(1) + (k + 4) * np.abs(want))
+    for loss in got:
+        assert (np.abs(host(loss) - want) <= bound).all()
