@@ -385,10 +385,10 @@ def scan_step(a, x, state, resets=None, gate=GATE_DECAY, out=None, stream=None):
 
 
 def scan_backward(a, x, h, grad_h, h0=None, resets=None, grad_last=None, gate=GATE_DECAY, reverse=False, out=None,
-                  stream=None, status=None):
+                  stream=None, status=None, skip=()):
     """{"grad_a", "grad_x" [B, T, C], "grad_h0" float [B, C]} of scan_forward (same arguments) from the h
-    that it returned and the gradients of h and of last (None: 0).  x may be None where decays are
-    given.  See per_scan_backward."""
+    that it returned and the gradients of h and of last (None: 0); without those named in `skip`, which
+    are not computed.  x may be None where decays are given.  See per_scan_backward."""
     code, dev = _lead(a, "a", 3)
     b, t, c = a.shape
     shape, dt = a.shape, a.dtype
@@ -396,6 +396,8 @@ def scan_backward(a, x, h, grad_h, h0=None, resets=None, grad_last=None, gate=GA
     if x is not None:
         xp, sx = _arg(x, "x", shape, dt, dev), x.stride()
     yp = _arg(h, "h", shape, dt, dev)
+    if grad_h is None:
+        grad_h = torch.zeros(c, dtype=dt, device=a.device).expand(shape)   # one row for all steps
     gp = _arg(grad_h, "grad_h", shape, dt, dev)
     edge = torch.Size((b, c))
     hp = _whole(h0, "h0", edge, torch.float32, dev)
@@ -404,39 +406,50 @@ def scan_backward(a, x, h, grad_h, h0=None, resets=None, grad_last=None, gate=GA
     flags = _gate_flags(gate, reverse)
     if _elsewhere(stream, dev):
         with _On(stream, dev, (a, x, h, grad_h, h0, resets, grad_last), out, status):
-            return scan_backward(a, x, h, grad_h, h0, resets, grad_last, gate, reverse, out, None, status)
-    ga = _given(out, "grad_a", shape, dt, dev, a)
-    gx = _given(out, "grad_x", shape, dt, dev, a)
-    g0 = _given(out, "grad_h0", edge, torch.float32, dev, a)
+            return scan_backward(a, x, h, grad_h, h0, resets, grad_last, gate, reverse, out, None, status, skip)
+    got = {}
+    for name, size, kind in (("grad_a", shape, dt), ("grad_x", shape, dt), ("grad_h0", edge, torch.float32)):
+        if name not in skip:
+            got[name] = _given(out, name, size, kind, dev, a)
+    ga, gx, g0 = got.get("grad_a"), got.get("grad_x"), got.get("grad_h0")
     if out is not None:
         _whole(g0, "grad_h0", edge, torch.float32, dev)
-    sa, sh, sg, sga, sgx = a.stride(), h.stride(), grad_h.stride(), ga.stride(), gx.stride()
+    sa, sh, sg = a.stride(), h.stride(), grad_h.stride()
+    sga = ga.stride() if ga is not None else _NO_STRIDE
+    sgx = gx.stride() if gx is not None else _NO_STRIDE
     sr = resets.stride() if rp is not None else _NO_STRIDE
     _check(_library().per_scan_backward(
         _SCAN.pack(t, b, c, code, flags, sa[0], sa[1], sx[0], sx[1], sh[0], sh[1], sg[0], sg[1], sga[0], sga[1],
                    sgx[0], sgx[1], sr[0], sr[1], _status_ptr(status, dev) or 0, 0, 0),
-        a.data_ptr(), xp, yp, hp, rp, gp, lp, ga.data_ptr(), gx.data_ptr(), g0.data_ptr(), _raw_stream(dev)),
-        "scan_backward")
-    return {"grad_a": ga, "grad_x": gx, "grad_h0": g0}
+        a.data_ptr(), xp, yp, hp, rp, gp, lp, *(None if z is None else z.data_ptr() for z in (ga, gx, g0)),
+        _raw_stream(dev)), "scan_backward")
+    return got
 
 
 class _GatedScan(torch.autograd.Function):
     @staticmethod
     def forward(ctx, a, x, h0, resets, gate, reverse):
         got = scan_forward(a, x, h0, resets, gate, reverse)
-        ctx.save_for_backward(a, x, got["h"], h0, resets)
+        # with given decays the gradient does not depend on x
+        ctx.save_for_backward(a, x if gate == GATE_SIGMOID else None, got["h"], h0, resets)
+        ctx.set_materialize_grads(False)
         ctx.gate, ctx.reverse = gate, reverse
         return got["h"], got["last"]
 
     @staticmethod
     def backward(ctx, grad_h, grad_last):
         a, x, h, h0, resets = ctx.saved_tensors
-        if a.shape[-1] > 1 and grad_h.stride(-1) != 1:
+        wanted = dict(zip(("grad_a", "grad_x", "grad_h0"), ctx.needs_input_grad))
+        if (grad_h is None and grad_last is None) or not any(wanted.values()):
+            return None, None, None, None, None, None
+        if grad_h is not None and a.shape[-1] > 1 and grad_h.stride(-1) != 1:
             grad_h = grad_h.contiguous()
-        got = scan_backward(a, x, h, grad_h, h0, resets, grad_last.contiguous(), ctx.gate, ctx.reverse)
+        if grad_last is not None:
+            grad_last = grad_last.contiguous()
+        got = scan_backward(a, x, h, grad_h, h0, resets, grad_last, ctx.gate, ctx.reverse,
+                            skip=[name for name, want in wanted.items() if not want])
         of = [t for t in (a, x, h0, grad_h, grad_last) if t is not None]
-        return (_first_only(got["grad_a"], *of), _first_only(got["grad_x"], *of),
-                _first_only(got["grad_h0"], *of) if h0 is not None else None, None, None, None)
+        return (*(_first_only(got.get(name), *of) for name in wanted), None, None, None)
 
 
 def gated_scan(a, x, h0=None, resets=None, gate=GATE_DECAY, reverse=False):

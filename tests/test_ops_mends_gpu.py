@@ -336,3 +336,56 @@ def test_distill_losses_do_not_lose_digits_to_a_common_offset(kind, tau):
     bound = oo.U * (tau * tau * off.sum(1) + (k + 4) * np.abs(want))
     for loss in got:
         assert (np.abs(host(loss) - want) <= bound).all()
+
+
+# -- what a gradient does not need -------------------------------------------------------------
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("t, c", [(1, 5), (300, 40), (9000, 24)])
+def test_gated_scan_gradients_of_one_output_or_input_alone(sigmoid, kind, t, c):
+    """They are those of the whole call with zeros in the other's place."""
+    g = np.random.default_rng(80)
+    gate = ops.GATE_SIGMOID if sigmoid else ops.GATE_DECAY
+    a = rand(g, 2, t, c, kind=kind)
+    a = (a if sigmoid else torch.sigmoid(a)).requires_grad_()
+    x, h0, gl = rand(g, 2, t, c, kind=kind).requires_grad_(), rand(g, 2, c).requires_grad_(), rand(g, 2, c)
+    h, last = ops.gated_scan(a, x, h0, gate=gate)
+    zero = torch.zeros_like(h)
+    want = ops.scan_backward(a.detach(), x.detach(), h.detach(), zero, h0=h0.detach(), grad_last=gl, gate=gate)
+    for wrt, names in (((a, x, h0), ("grad_a", "grad_x", "grad_h0")), ((x,), ("grad_x",)), ((a,), ("grad_a",)), ((h0,), ("grad_h0",))):
+        z = [y.detach().requires_grad_(any(y is w for w in wrt)) for y in (a, x, h0)]
+        _, last = ops.gated_scan(*z, gate=gate)
+        got = torch.autograd.grad(last, [y for y in z if y.requires_grad], gl)
+        for o, n in zip(got, names):
+            assert torch.equal(o, want[n])
+    h, last = ops.gated_scan(a, x, h0, gate=gate)
+    got = torch.autograd.grad(h, (a, x, h0), torch.ones_like(h))
+    want = ops.scan_backward(a.detach(), x.detach(), h.detach(), torch.ones_like(h), h0=h0.detach(), gate=gate)
+    for o, n in zip(got, ("grad_a", "grad_x", "grad_h0")):
+        assert torch.equal(o, want[n])
+    for skip in (("grad_a",), ("grad_x", "grad_h0"), ("grad_a", "grad_x", "grad_h0")):
+        got = ops.scan_backward(a.detach(), x.detach(), h.detach(), torch.ones_like(h), h0=h0.detach(), gate=gate, skip=skip)
+        assert set(got) == set(want) - set(skip)
+        for n in got:
+            assert torch.equal(got[n], want[n])
+
+
+def test_gated_scan_keeps_and_writes_only_what_is_needed():
+    """A loss on the last state by x alone, with given decays: the backward pass allocates the gradient of x and
+    little else, and x itself is not kept for it."""
+    g = np.random.default_rng(81)
+    a, x = torch.sigmoid(rand(g, 4, 2000, 256)), rand(g, 4, 2000, 256).requires_grad_()
+    array = x.numel() * 4
+    used = lambda: (torch.cuda.synchronize(), torch.cuda.memory_allocated())[1]
+    before = used()
+    _, last = ops.gated_scan(a, x * 1.0)              # (the product is dropped after the call)
+    assert used() - before < 1.25 * array             # h
+    loss = last.sum()
+    before = used()
+    torch.cuda.reset_peak_memory_stats()
+    grad, = torch.autograd.grad(loss, x)
+    # the operator's gradient, the product's behind it, and less than a quarter of an array besides
+    assert torch.cuda.max_memory_allocated() - before < 2.25 * array
+    want = ops.scan_backward(a, None, torch.zeros_like(a), torch.zeros_like(a), grad_last=torch.ones_like(last))
+    assert torch.equal(grad, want["grad_x"])
