@@ -334,8 +334,10 @@ def _resets_ptr(resets, shape, dev):
 def scan_forward(a, x, h0=None, resets=None, gate=GATE_DECAY, reverse=False, out=None, stream=None,
                  status=None):
     """{"h" [B, T, C], "last" float [B, C]} of h_t = a_t h_{t-1} + x_t (or with a sigmoid gate); h0 float
-    [B, C], resets uint8 or bool [B, T].  reverse: from the last step to the first.  status int32 [1]
-    takes PER_DEVFLAG_* bits.  See per_scan_forward."""
+    [B, C], resets uint8 or bool [B, T]: a step that drops the state coming into it, an episode's first
+    in the direction of the pass (a buffer's dones mark last steps: one step earlier, or as they are with
+    reverse).  reverse: from the last step to the first.  status int32 [1] takes PER_DEVFLAG_* bits.
+    See per_scan_forward."""
     code, dev = _lead(a, "a", 3)
     b, t, c = a.shape
     xp = _arg(x, "x", a.shape, a.dtype, dev)
@@ -454,5 +456,5 @@ class _GatedScan(torch.autograd.Function):
 
 def gated_scan(a, x, h0=None, resets=None, gate=GATE_DECAY, reverse=False):
     """(h, last) as a function that torch.autograd can differentiate by a, x and h0, once (a second
-    derivative is refused)."""
+    derivative is refused).  Arguments as scan_forward's: resets mark first steps."""
     return _GatedScan.apply(a, x, h0, resets, gate, reverse)

@@ -389,3 +389,28 @@ def test_gated_scan_keeps_and_writes_only_what_is_needed():
     assert torch.cuda.max_memory_allocated() - before < 2.25 * array
     want = ops.scan_backward(a, None, torch.zeros_like(a), torch.zeros_like(a), grad_last=torch.ones_like(last))
     assert torch.equal(grad, want["grad_x"])
+
+
+# -- episodes ----------------------------------------------------------------------------------
+
+def test_scan_resets_from_a_buffers_dones():
+    """Forwards, the step after a done starts anew; backwards (returns) the done step itself does."""
+    g = np.random.default_rng(90)
+    b, t, c = 3, 200, 8
+    a, x, h0 = rand(g, b, t, c), rand(g, b, t, c), rand(g, b, c)
+    dones = torch.from_numpy((g.random((b, t)) < 0.05).astype(np.uint8)).cuda()
+    starts = torch.zeros_like(dones)
+    starts[:, 1:] = dones[:, :-1]
+    got = ops.gated_scan(a, x, h0, resets=starts, gate=ops.GATE_SIGMOID)[0]
+    gamma = torch.full((b, t, 1), 0.9, device="cuda")
+    returns = ops.scan_forward(gamma, x[..., :1].contiguous(), resets=dones, reverse=True)["h"]
+    for r in range(b):
+        ends = [i + 1 for i in range(t) if dones[r, i]]
+        for first, end in zip([0] + ends, ends + [t]):
+            if first == end:
+                continue
+            part = (slice(r, r + 1), slice(first, end))
+            want = oo.scan(host(a[part]), host(x[part]), host(h0[r:r + 1]) if first == 0 else None, None, True)
+            oo.close(f32(got[part]), want["h"], want["bh"])
+            want = oo.scan(host(gamma[part]), host(x[part][..., :1]), None, None, False, True)
+            oo.close(f32(returns[part]), want["h"], want["bh"])
