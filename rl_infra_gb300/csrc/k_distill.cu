@@ -40,7 +40,7 @@ constexpr int kMaxCluster = 8;
 // in larger clusters) 1.34.
 constexpr int kMaxWarps = 8, kCtasPerSm = 3, kPartKb = 64;
 constexpr int kUnroll = 4;       // pieces of 16 bytes a loader thread takes at a time
-constexpr int kAhead = 1;        // batches of them that are requested ahead (0.86 ms; 4: 0.90)
+constexpr int kAhead = 1;        // batches of them under way at a time, the one that is waited for among them (0.86 ms; 4: 0.90)
 constexpr float kInf = __builtin_huge_valf();
 
 struct RowSum {
