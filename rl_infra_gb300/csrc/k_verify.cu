@@ -32,7 +32,8 @@ constexpr int kUnroll = 4;   // 16-byte loads of each row that a lane has in fli
 // 2^23 that round toward zero, whose low mantissa bits are the two whole numbers; the additions' bit
 // patterns are summed as they are, and the pattern of 2^23 is taken off by the count.  (A conversion of a
 // binary32 to 64 bits runs on the binary64 pipe, which bound the kernel: 56 us against 31 for 128
-// sequences of 131072.)  Exact while a thread sums at most 2^12 masses.
+// sequences of 131072.)  Exact while a thread sums fewer than 2^12 masses: each adds at most 2^20 to a 32-bit sum.
+static_assert(kMaxVocab / kThreads + 2 * 8 < 1u << 12, "a lane's masses: its share of a row and up to two pieces of 8");
 struct Units {
     unsigned hi = 0, lo = 0;
     // r = max(0, min(1, p - q)); NaN counts 0
@@ -277,8 +278,8 @@ cudaError_t launch_t(const VerifyArgs &a, const DeviceInfo &dev, cudaStream_t st
 {
     constexpr unsigned P = 16 / sizeof(T);
     const unsigned pieces = (a.vocab + P - 1) / P + 1;   // a row that starts off a boundary has one more
-    // CTAs for a sequence: at least 512 pieces each (two a lane), and no more than 8 an SM in all: each runs the
-    // accept tests again (512 sequences of 131072: 4 CTAs a sequence 100 us, 8 103, 2 124)
+    // CTAs for a sequence: more as long as each keeps at least 512 pieces (two a lane) and there are fewer than 8 an SM
+    // in all (so fewer than 16 after the last doubling): each runs the accept tests again (512 sequences of 131072: 4 CTAs a sequence 100 us, 8 103, 2 124)
     unsigned csize = 1;
     while (csize < kMaxCluster && pieces / csize > 1024 && (unsigned long long)a.batch * csize < 8ull * dev.sms) csize *= 2;
     return launch_clusters(k_verify<T>, a.batch * csize, kThreads, csize, 0, st, a, csize, (pieces + csize - 1) / csize);

@@ -58,7 +58,7 @@ per_status distill(const char *where, DistillPart part, const per_distill_shape 
 {
     if (!sh) return refuse(where, "shape is NULL");
     if (sh->rows > 0x7fffffffull) return refuse(where, "rows must be below 2^31");
-    if (sh->vocab == 0 || sh->vocab > (1u << 18)) return refuse(where, "vocab must be in 1 .. 2^18");
+    if (sh->vocab == 0 || sh->vocab > kMaxVocab) return refuse(where, "vocab must be in 1 .. 2^18");
     if (sh->top == 0 || sh->top > 1024) return refuse(where, "top must be in 1 .. 1024");
     if (bad_type(sh->type) || bad_type(sh->top_type)) return refuse(where, "unknown element type");
     if (sh->flags & ~(uint32_t)PER_DISTILL_IDX64) return refuse(where, "unknown flags");
@@ -198,7 +198,7 @@ per_status per_verify_draft(const per_verify_shape *shape, const void *d_p, cons
     if (!sh) return refuse(where, "shape is NULL");
     if (sh->batch > (1u << 20)) return refuse(where, "batch must be at most 2^20");
     if (sh->drafts > 1024) return refuse(where, "drafts must be at most 1024");
-    if (sh->vocab == 0 || sh->vocab > (1u << 18)) return refuse(where, "vocab must be in 1 .. 2^18");
+    if (sh->vocab == 0 || sh->vocab > kMaxVocab) return refuse(where, "vocab must be in 1 .. 2^18");
     if (bad_type(sh->type)) return refuse(where, "unknown element type");
     if ((sh->flags & ~(uint32_t)PER_VERIFY_TOKENS64) || sh->reserved) return refuse(where, "unknown flags");
     if (sh->batch == 0) return PER_OK;

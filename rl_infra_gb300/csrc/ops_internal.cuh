@@ -12,6 +12,8 @@
 
 namespace gbper {
 
+constexpr uint32_t kMaxVocab = 1u << 18;   // of a distillation and of a verification
+
 struct DistillArgs {
     const void *x, *top, *idx;
     const float *teacher_lse, *scale;
