@@ -414,3 +414,49 @@ def test_scan_resets_from_a_buffers_dones():
             oo.close(f32(got[part]), want["h"], want["bh"])
             want = oo.scan(host(gamma[part]), host(x[part][..., :1]), None, None, False, True)
             oo.close(f32(returns[part]), want["h"], want["bh"])
+
+
+# -- strides where a sequence is split over CTAs -----------------------------------------------
+
+def padded(t, pad, lead):
+    """The same values with `pad` elements behind each row of the last axis and `lead` before the first."""
+    rows, w = t.numel() // t.shape[-1], t.shape[-1] + pad
+    store = torch.full((lead + rows * w,), 7.0, device=t.device).to(t.dtype)
+    strides, s = [1], w
+    for n in reversed(t.shape[:-1]):
+        strides.insert(0, s)
+        s *= n
+    view = store.as_strided(t.shape, strides, lead)
+    view.copy_(t)
+    return view
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("b, c, pad, lead", [(1, 64, 8, 8), (1, 64, 1, 0), (1, 64, 0, 3), (2, 37, 3, 1)])
+def test_scan_strides_of_long_sequences(kind, sigmoid, reverse, b, c, pad, lead):
+    """Long sequences in rows inside wider rows and off 16 bytes, outputs too: nothing between the rows is written."""
+    g = np.random.default_rng(95)
+    t = 4500
+    a, x, gh, h0, gl = (rand(g, b, t, c, kind=kind) * 1.5 + 2 if i == 0 else rand(g, b, t, c, kind=kind) if i < 3 else rand(g, b, c)
+                        for i in range(5))
+    a = a.to(TYPES[kind]) if sigmoid else torch.sigmoid(a.float()).to(TYPES[kind])
+    resets = torch.from_numpy((g.random((b, t)) < 0.01).astype(np.uint8)).cuda()
+    gate = ops.GATE_SIGMOID if sigmoid else ops.GATE_DECAY
+    kw = dict(gate=gate, reverse=reverse)
+    got = ops.scan_forward(padded(a, pad, lead), padded(x, pad + 1, lead), h0, resets,
+                           out={"h": padded(torch.zeros_like(a), pad, lead)}, **kw)
+    want = oo.scan(host(a), host(x), host(h0), host(resets), sigmoid, reverse)
+    oo.close(f32(got["h"]), want["h"], want["bh"], kind)
+    oo.close(f32(got["last"]), want["last"], want["blast"])
+    back = ops.scan_backward(padded(a, pad, lead), padded(x, pad + 1, lead), got["h"], padded(gh, pad, lead + 1), h0, resets, gl,
+                             out={k: padded(torch.zeros_like(a), pad, lead) for k in ("grad_a", "grad_x")}, **kw)
+    ref = oo.scan_backward(host(a), host(x), host(got["h"]), host(gh), host(h0), host(resets), host(gl), sigmoid, reverse)
+    for k in ("grad_a", "grad_x"):
+        oo.close(f32(back[k]), ref[k], ref["b" + k], kind)
+    oo.close(f32(back["grad_h0"]), ref["grad_h0"], ref["bgrad_h0"])
+    if pad:
+        for z in (got["h"], back["grad_a"], back["grad_x"]):
+            between = z.as_strided((b * t - 1, pad), (c + pad, 1), lead + c)
+            assert (between == 7).all(), "written between the rows"
