@@ -54,14 +54,15 @@ struct Units {
 };
 
 // 16 bytes at any address that is a multiple of 2: two aligned loads, shifted together.  The caller makes
-// sure that both lie inside the row.
+// sure that both lie inside the row.  (Loads that memory keeps coherent: the read-only path is for what no kernel
+// writes while this one runs, and this one begins before its predecessor in the stream has ended.)
 __device__ __forceinline__ uint4 load_across(const unsigned char *p)
 {
     const unsigned off = (unsigned)(reinterpret_cast<uintptr_t>(p) & 15u);
     const uint4 *a = reinterpret_cast<const uint4 *>(p - off);
-    const uint4 lo = __ldg(a);
+    const uint4 lo = *a;
     if (off == 0) return lo;
-    const uint4 hi = __ldg(a + 1);
+    const uint4 hi = a[1];
     return shift_bytes(lo, hi, off);
 }
 
@@ -82,7 +83,7 @@ struct Row {
         const bool margin = j >= P && j + 2 * P <= (long long)vocab;
         b.raw = make_uint4(0, 0, 0, 0);
         if (inside && (!q || margin)) {
-            a.raw = __ldg(reinterpret_cast<const uint4 *>(p + j));
+            a.raw = *reinterpret_cast<const uint4 *>(p + j);
             if (q) b.raw = load_across(reinterpret_cast<const unsigned char *>(q + j));
         } else {
             float f[P], g[P];
