@@ -551,7 +551,7 @@ __device__ __forceinline__ bool settle(F2 &A, F2 &H, const Place<N> &me, bool wh
             return true;
         }
     }
-    return whole && fminf(fabsf(A.x), fabsf(A.y)) > 0.0f && fabsf(H.x) < kInf && fabsf(H.y) < kInf;
+    return whole && fabsf(A.x) > 0.0f && fabsf(A.y) > 0.0f && fabsf(H.x) < kInf && fabsf(H.y) < kInf;   // (and not NaN)
 }
 
 // (Neither kernel lets the next one begin before it ends: the next one's CTAs would take the few places that are free

@@ -460,3 +460,34 @@ def test_scan_strides_of_long_sequences(kind, sigmoid, reverse, b, c, pad, lead)
         for z in (got["h"], back["grad_a"], back["grad_x"]):
             between = z.as_strided((b * t - 1, pad), (c + pad, 1), lead + c)
             assert (between == 7).all(), "written between the rows"
+
+
+# -- closed gates next to resets ---------------------------------------------------------------
+
+def shut_case(g, b, t, c, kind, closed):
+    """Gates of -inf or -120 (the state is dropped) before a reset in the same lane's steps, and after one."""
+    a, x, h0 = rand(g, b, t, c, kind=kind), rand(g, b, t, c, kind=kind), rand(g, b, c)
+    resets = torch.zeros(b, t, dtype=torch.uint8, device="cuda")
+    for i in range(2, t - 3, 5):
+        a[:, i, i % c::7] = closed
+        resets[:, i + 1 + i // 5 % 2] = 1
+    return a, x, h0, resets
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("closed", [-float("inf"), -120.0])
+@pytest.mark.parametrize("b, t, c", [(2, 64, 16), (1, 3000, 40), (64, 100, 1024)])
+def test_scan_closed_gates_before_resets(kind, closed, b, t, c):
+    g = np.random.default_rng(100)
+    a, x, h0, resets = shut_case(g, b, t, c, kind, closed)
+    want = oo.scan(host(a), host(x), host(h0), host(resets), True)
+    got = ops.scan_forward(a, x, h0, resets, ops.GATE_SIGMOID)
+    oo.close(f32(got["h"]), want["h"], want["bh"], kind)
+    oo.close(f32(got["last"]), want["last"], want["blast"])
+    gh = rand(g, b, t, c, kind=kind)
+    back = ops.scan_backward(a, x, got["h"], gh, h0, resets, gate=ops.GATE_SIGMOID)
+    ref = oo.scan_backward(host(a), host(x), host(got["h"]), host(gh), host(h0), host(resets), None, True)
+    # (slopes below 2^-126 count as 0: they are e^-120 here, and 0)
+    for k in ("grad_a", "grad_x"):
+        oo.close(f32(back[k]), ref[k], ref["b" + k] + 1e-37, kind)
+    oo.close(f32(back["grad_h0"]), ref["grad_h0"], ref["bgrad_h0"])
