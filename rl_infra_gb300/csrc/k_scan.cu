@@ -537,21 +537,22 @@ struct Held {
     bool plain, any;   // any: a lane of the warp has resets
 };
 
-// Whether a lane's products and sums can be taken as they are.  A channel that does not exist passes its state
-// on.
+// Whether a lane's products and sums can be taken as they are: check is 0 then, A is neither 0 nor NaN, and H is
+// finite.  A channel that does not exist passes its state on.
 template <int N>
-__device__ __forceinline__ bool settle(F2 &A, F2 &H, const Place<N> &me, bool whole)
+__device__ __forceinline__ bool settle(F2 &A, F2 &H, F2 check, const Place<N> &me, bool whole)
 {
     if (!me.second) {
         A.y = 1.0f;
-        H.y = 0.0f;
+        H.y = check.y = 0.0f;
         if (!me.live) {
             A.x = 1.0f;
             H.x = 0.0f;
             return true;
         }
     }
-    return whole && fabsf(A.x) > 0.0f && fabsf(A.y) > 0.0f && fabsf(H.x) < kInf && fabsf(H.y) < kInf;   // (and not NaN)
+    return whole && fabsf(A.x) > 0.0f && fabsf(A.y) > 0.0f && fabsf(H.x) < kInf && fabsf(H.y) < kInf && check.x == 0.0f &&
+           check.y == 0.0f;
 }
 
 // (Neither kernel lets the next one begin before it ends: the next one's CTAs would take the few places that are free
@@ -618,11 +619,13 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_fwd(ScanArgs s
         ahead = request_resets<N>(s, me.b, t - me.off + me.span);
         h.resets = resets;
         F2 A{1.0f, 1.0f}, H{0.0f, 0.0f};
+        F2 check{0.0f, 0.0f};   // NaN once an input is not finite: its weight of 0 may have to drop it, and a reset hides it
         auto run = [&](auto any) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 F2 w, v;
                 weights(k, i, w, v);
+                if constexpr (SIG && any.value) check = fma2(v, F2{0.0f, 0.0f}, check);
                 if constexpr (HOLD) {
                     h.w[i] = w;
                     h.v[i] = v;
@@ -636,7 +639,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_fwd(ScanArgs s
         if (h.any) run(std::true_type());
         else run(std::false_type());
         Stretch own[2];
-        h.plain = settle(A, H, me, t + N <= s.steps);
+        h.plain = settle(A, H, check, me, t + N <= s.steps);
         if (!h.plain) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -788,7 +791,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_bwd(ScanArgs s
         if (d.any) run(std::true_type());
         else run(std::false_type());
         Stretch own[2];
-        d.plain = settle(A, H, me, t + N < s.steps);   // (row steps - 1 reads h0)
+        d.plain = settle(A, H, F2{0.0f, 0.0f}, me, t + N < s.steps);   // (row steps - 1 reads h0)
         if (d.plain) {
             const float nan = __int_as_float(0x7fffffff);
             own[0] = {resets && me.live ? nan : A.x, H.x};

@@ -491,3 +491,24 @@ def test_scan_closed_gates_before_resets(kind, closed, b, t, c):
     for k in ("grad_a", "grad_x"):
         oo.close(f32(back[k]), ref[k], ref["b" + k] + 1e-37, kind)
     oo.close(f32(back["grad_h0"]), ref["grad_h0"], ref["bgrad_h0"])
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("held", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("b, t, c", [(2, 64, 16), (1, 3000, 40), (64, 100, 1024)])
+def test_scan_dropped_inputs_before_resets(kind, held, b, t, c):
+    """A gate of +inf drops its step's input, whatever that holds, with a reset later in the same lane's steps too."""
+    g = np.random.default_rng(101)
+    a, x, h0, resets = shut_case(g, b, t, c, kind, float("inf"))
+    x = torch.where(torch.isinf(a), torch.full_like(x, held), x)
+    want = oo.scan(host(a), host(x), host(h0), host(resets), True)
+    got = ops.scan_forward(a, x, h0, resets, ops.GATE_SIGMOID)
+    assert np.isfinite(want["h"]).all()
+    oo.close(f32(got["h"]), want["h"], want["bh"], kind)
+    oo.close(f32(got["last"]), want["last"], want["blast"])
+    gh = rand(g, b, t, c, kind=kind)
+    back = ops.scan_backward(a, x, got["h"], gh, h0, resets, gate=ops.GATE_SIGMOID)
+    ref = oo.scan_backward(host(a), host(x), host(got["h"]), host(gh), host(h0), host(resets), None, True)
+    for k in ("grad_a", "grad_x"):
+        oo.close(f32(back[k]), ref[k], ref["b" + k], kind)
+    oo.close(f32(back["grad_h0"]), ref["grad_h0"], ref["bgrad_h0"])
