@@ -84,13 +84,23 @@ __device__ __forceinline__ F2 exp_minus(F2 a)
     return e;
 }
 
+// e f, at most 1 as 1 - f is.  (Its roundings can take it to 1 + 2^-23, and binary32's lowest value times that, a mask,
+// would be infinite; those of 16-bit types are far enough from there.)  NaN gives 0.
+__device__ __forceinline__ float at_most_1(float e, float f)
+{
+    float v;
+    asm("mul.rn.sat.f32 %0, %1, %2;" : "=f"(v) : "f"(e), "f"(f));
+    return v;
+}
+
 // f = 1 / (1 + e), 1 - f = e f with e = exp(-a): neither loses digits to a subtraction.  (f below 2^-126 is 0.)
 template <typename T, bool SIG>
 __device__ __forceinline__ Gate gate(float a)
 {
     if (!SIG) return {a, 1.0f};
     const float e = sizeof(T) == 4 ? expf(-a) : ex2(a * -kLog2e), f = rcp(1.0f + e);
-    return {f, f == 0.0f ? 1.0f : e * f};
+    const float v = f == 0.0f ? 1.0f : e * f;
+    return {f, sizeof(T) == 4 && v > 1.0f ? 1.0f : v};
 }
 
 // the same of two gates that are not 0
@@ -100,7 +110,8 @@ __device__ __forceinline__ void gates(F2 a, F2 &w, F2 &v)
     const F2 e = exp_minus<T>(a);
     const F2 d = e + F2{1.0f, 1.0f};
     w = {rcp(d.x), rcp(d.y)};
-    v = e * w;
+    if constexpr (sizeof(T) == 4) v = {at_most_1(e.x, w.x), at_most_1(e.y, w.y)};
+    else v = e * w;
 }
 
 // w h + more, a weight of 0 dropping whatever h holds

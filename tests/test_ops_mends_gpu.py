@@ -512,3 +512,18 @@ def test_scan_dropped_inputs_before_resets(kind, held, b, t, c):
     for k in ("grad_a", "grad_x"):
         oo.close(f32(back[k]), ref[k], ref["b" + k], kind)
     oo.close(f32(back["grad_h0"]), ref["grad_h0"], ref["bgrad_h0"])
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("t", [1, 64, 4096])
+def test_scan_lowest_inputs_do_not_overflow(kind, t):
+    """1 - f is at most 1: the type's lowest value times it is finite."""
+    c = 1024
+    low = torch.finfo(TYPES[kind]).min
+    a = torch.linspace(-85, -0.5, t * c, device="cuda").view(1, t, c).to(TYPES[kind])
+    x = torch.full_like(a, low)
+    ones = torch.ones(1, t, dtype=torch.uint8, device="cuda")
+    got = ops.scan_forward(a, x, resets=ones, gate=ops.GATE_SIGMOID)
+    assert torch.isfinite(got["h"].float()).all() and torch.isfinite(got["last"]).all()
+    back = ops.scan_backward(a, x, torch.zeros_like(a), x, resets=ones, gate=ops.GATE_SIGMOID)
+    assert torch.isfinite(back["grad_x"].float()).all()
