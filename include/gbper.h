@@ -368,8 +368,8 @@ typedef struct {
  * d_teacher_lse is given, d_teacher_lse[n]: the teacher's over its whole vocabulary (q then sums to
  * the share that the top K hold).  An entry with idx < 0 is left out, whatever its t; one with
  * idx >= V is left out and sets PER_DEVFLAG_BAD_INDEX.  Entries that name one place several times
- * each count.  A row with no entry of q > 0, or whose logits are all -inf, has nothing to learn from:
- * its loss and its gradient are 0.  A q > 0 where x is -inf gives a loss of +inf; NaN in x
+ * each count.  A row with no entry of q > 0, or whose logits are all -inf or at or below -2^100 (masked by the
+ * lowest value of their type), has nothing to learn from: its loss and its gradient are 0.  A q > 0 where x is -inf gives a loss of +inf; NaN in x
  * or in a kept t gives NaN in its row.  The loss is not weighted: it is the row's next TD error
  * (per_update_priorities).
  *   d_logits [N x V], d_top [N x K], d_idx [N x K], d_teacher_lse [N] float or NULL,

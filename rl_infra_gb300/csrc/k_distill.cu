@@ -42,6 +42,9 @@ constexpr int kMaxWarps = 8, kCtasPerSm = 3, kPartKb = 64;
 constexpr int kUnroll = 4;       // pieces of 16 bytes a loader thread takes at a time
 constexpr int kAhead = 1;        // batches of them under way at a time, the one that is waited for among them (0.86 ms; 4: 0.90)
 constexpr float kInf = __builtin_huge_valf();
+// A normaliser at or below this is of a row that a mask leaves nothing of: all its logits are -inf, or about the lowest value
+// of binary32 or bfloat16, where m + tau ln s is m and no p can be told from it.
+constexpr float kNothing = -0x1p100f;
 
 struct RowSum {
     float m, s;
@@ -493,7 +496,7 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, kCtasPerSm) k_distill(Di
                 if (q[k] != 0.0f) loss += q[k] * (d[k] - ((xk[k] - m) - l));
             for (int o = 16; o; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
             if (lane == 0) {
-                a.loss[row] = sh.some && lse != -kInf ? a.tau * loss : 0.0f;
+                a.loss[row] = sh.some && !(lse <= kNothing) ? a.tau * loss : 0.0f;
                 if (a.lse) a.lse[row] = lse;
             }
         }
@@ -503,7 +506,7 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, kCtasPerSm) k_distill(Di
     if (PART == kDistillForward) return;
 
     // ---- the gradient of this CTA's part --------------------------------------------------------
-    const bool live = sh.some && lse != -kInf;
+    const bool live = sh.some && !(lse <= kNothing);   // (NaN is)
     const float g = (a.scale ? a.scale[row] : 1.0f) * a.tau;
     // from lse in the step too: it gives the same bits as the forward and the backward call
     const float f0 = live ? g * sh.S : 0.0f;

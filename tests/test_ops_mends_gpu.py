@@ -527,3 +527,35 @@ def test_scan_lowest_inputs_do_not_overflow(kind, t):
     assert torch.isfinite(got["h"].float()).all() and torch.isfinite(got["last"]).all()
     back = ops.scan_backward(a, x, torch.zeros_like(a), x, resets=ones, gate=ops.GATE_SIGMOID)
     assert torch.isfinite(back["grad_x"].float()).all()
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("tau", [1.0, 0.3])
+@pytest.mark.parametrize("v", [4, 5000, 140001])
+def test_distill_rows_masked_by_the_lowest_value(kind, tau, v):
+    """A row of lowest values alone has nothing to learn from, as one of -inf; one value above the mask takes all; binary16's
+    lowest is a number like others.  Rows between stay as they are."""
+    g = np.random.default_rng(110)
+    low = torch.finfo(TYPES[kind]).min
+    x = rand(g, 6, v, kind=kind)
+    t, idx = rand(g, 6, 3), torch.from_numpy(np.stack([g.permutation(v)[:3] for _ in range(6)])).cuda()
+    x[1] = low
+    x[3] = low
+    x[3, ::2] = -float("inf")
+    x[4] = low
+    x[4, 1] = 2.0
+    idx[4] = torch.tensor([1, -1, -1])
+    step = ops.distill_step(x, t, idx, temperature=tau)
+    fwd = ops.distill_forward(x, t, idx, temperature=tau)
+    back = ops.distill_backward(x, t, idx, fwd["lse"], temperature=tau)
+    if kind != "f16":
+        for r in (1, 3):
+            for z in (step["loss"], fwd["loss"], step["grad"], back["grad"]):
+                assert (z[r] == 0).all()
+    rows = [0, 2, 4, 5] + ([1] if kind == "f16" else [])
+    tau32 = float(np.float32(tau))
+    want = oo.distill(host(x)[rows], host(t)[rows], host(idx)[rows], tau32)
+    for got in (step, fwd):
+        oo.close(f32(got["loss"])[rows], want["loss"], want["bloss"])
+    for got in (step, back):
+        oo.close(f32(got["grad"])[rows], want["grad"], want["bgrad"], kind)
