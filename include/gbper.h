@@ -335,8 +335,10 @@ per_status per_rank_order_noalloc(const float *d_raw, uint32_t n, uint32_t *d_or
  * per_last_op_error(), on the calling thread.  Strides count elements; the innermost axis of
  * every array is contiguous.  Input strides may be any value (0 repeats a row for all); rows of an
  * output must not overlap.  Pointers need the alignment of their element type only; rows whose
- * start and stride are multiples of 16 bytes move in 16-byte pieces.  Where d_status is given, a
- * call sets PER_DEVFLAG_* bits in it (it never clears them).
+ * start and stride are multiples of 16 bytes move in 16-byte pieces.  Others take longer on a GB300: a
+ * recurrence with one such array (an odd number of channels, a shifted view) 1.4 to 2.6 times, a
+ * verification of 512 rows of 131071 1.3 times.  Where d_status is given, a call sets PER_DEVFLAG_*
+ * bits in it (it never clears them).
  * ------------------------------------------------------------------------------------------- */
 
 /* per_last_op_error -- a description of the last failure of an operator on this thread ("" if none).
@@ -378,12 +380,16 @@ typedef struct {
  * NULL: 1), an importance weight over the batch's size or what an outer gradient brings:
  *     grad_nj = s_n tau (S_n p_nj - sum over k with idx_nk = j of q_nk),  S_n = sum_k q_nk.
  * per_distill_step -- loss, lse and gradient in one pass over the logits (read once, gradient
- * written once; a row stays in the shared memory of up to 8 CTAs).
+ * written once; a row stays in the shared memory of up to 8 CTAs: 1, 2, 4 or 8 so that a part takes at most
+ * 64 KB, or 8 of larger parts.  A vocabulary just past 2^15, 2^16 or 2^17 16-bit elements or half as many of 32 bits
+ * is in parts of half the size and takes 1.4 to 1.75 times as long per byte on a GB300; float rows of 2^18 take twice
+ * as long per byte as those of 2^17).
  * d_grad may be d_logits itself (same stride): the gradient then takes the logits' place.
  * The gradient is rounded once to its type.  Before that, with U = 2^-24 and y = (x - lse) / tau, a p is good to a
- * relative 9 U + |y| U (the rounding of x - lse) for float logits and 9 U + 2 |y| U for 16-bit ones, beside what
- * lse's own error brings (tau U (ln V + 32), and |lse| U).  Losses take their differences from the rows' largest entries, so that
- * what all logits of a row share costs them no digits.  Results do not depend on the launch's order.
+ * relative 9 U + |y| U (the rounding of x - lse) for float logits and 9 U + 2 |y| U for 16-bit ones, beside what lse's
+ * own error brings (tau U (ln V + 32), and |lse| U); a p below 2^-126 counts as 0.  Losses take their differences
+ * from the rows' largest entries, so that what all logits of a row share costs them no digits.  Results do not depend
+ * on the launch's order.
  */
 per_status per_distill_forward(const per_distill_shape *shape, const void *d_logits, const void *d_top,
                                const void *d_idx, const float *d_teacher_lse, float *d_loss,
@@ -463,14 +469,15 @@ typedef struct {
  * h_{-1} is d_h0 (NULL: 0).  A step with d_resets[b, t] != 0 starts an episode: the state that comes into it counts
  * as 0, whatever it holds.  A weight of exactly 0 likewise drops what it multiplies, infinities and NaN
  * too (a gate of -inf drops the state, of +inf the input: padding can hold anything).  The
- * state is kept in binary32; h is rounded to its type where it is stored.  f and 1 - f are good to a relative
- * 2^-21 where a is binary32, to 2^-21 + |a| 2^-24 where it is not; an f below 2^-126 counts as 0.  Long sequences are
- * split over time where the channels alone do not fill the GPU; the joints multiply the decays of
- * a stretch, whose product must stay finite in binary32 (decays of magnitude at most 1 always
- * do).  The parts of a split sequence wait for one another with a limit.  A wait that runs out sets
- * PER_DEVFLAG_TIMEOUT in d_status; states that are then not known are NaN, and so is what follows from
- * them.  PER_SCAN_REVERSE runs t = T-1 .. 0 (discounted returns: a = gamma, x = reward, a reset at each
- * episode's last step).
+ * state is kept in binary32; h is rounded to its type where it is stored.  f and 1 - f are good to a
+ * relative 2^-21 where a is binary32, to 2^-21 + |a| 2^-24 where it is not; an f or 1 - f below 2^-126 may
+ * count as 0.  Long sequences are split over time where the channels alone do not fill the GPU; the
+ * joints multiply the decays of a stretch, whose product must stay finite in binary32 (decays of
+ * magnitude at most 1 always do; a product below 2^-126 is known to 2^-149, so that a state of size s
+ * can be off by s 2^-149 behind it).  The parts of a split sequence wait for one another with a limit.
+ * A wait that runs out sets PER_DEVFLAG_TIMEOUT in d_status; states that are then not known are NaN,
+ * and so is what follows from them.  PER_SCAN_REVERSE runs t = T-1 .. 0 (discounted returns: a = gamma,
+ * x = reward, a reset at each episode's last step).
  *   d_a, d_x [B x T x C], d_h0 [B x C] float or NULL, d_resets [B x T] uint8 or NULL,
  *   d_h [B x T x C], d_last [B x C] float (NULL to skip): the state after the last step; it may be
  *   d_h0 itself.  T = 1 is the step of a model that is being served.  T = 0 copies h0 to last.

@@ -21,7 +21,7 @@
 // barrier between the CTAs then waits for the stores of the row before.)
 //
 // Measured (GB300): step 8192 x 131072 bf16 with 64 entries 855 us, 5.0 TB/s, 74% of the copy rate; backward
-// 2048 x 131072 bf16 87%; forward 32 x 1009 f32 3.4 us.
+// 2048 x 131072 bf16 87%, f32 89%; step of the latter 446 us, 71%; forward 32 x 1009 f32 3.4 us.
 #include "ops_internal.cuh"
 
 #include <algorithm>

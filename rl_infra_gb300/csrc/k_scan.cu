@@ -26,7 +26,7 @@
 //
 // Measured (GB300): 64 x 1024 x 1024 f32 forward 121 us, 6.7 TB/s; both passes of 8 x 16384 x 1024 f32 742 us, 5.8 TB/s;
 // 16 x 2048 x 2048 bf16 sigmoid gradient 176 us, 4.6 TB/s (its instructions bound it); one sequence of 65537 x
-// 1024 bf16 146 us, 2.8 TB/s (the joints); one step of 64 x 2048 2.0 us.
+// 1024 bf16 149 us, 2.7 TB/s (the joints); one step of 64 x 2048 2.0 us.
 #include "ops_internal.cuh"
 
 #include <algorithm>
