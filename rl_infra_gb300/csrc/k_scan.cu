@@ -46,6 +46,9 @@ namespace {
 constexpr int kLaneSteps = 8, kLaneStepsCluster16 = 16;
 constexpr int kRing = 2, kRingCluster = 3;
 constexpr int kCtasPerSm = 4;   // what registers are kept for (CTAs of 4 warps): 4 82, 170, 141; 3 83, 188, 162; 5 89, 203, 147
+// With a cluster the gradient's ring takes 78 to 111 KB a CTA, so that two fit and may have twice the registers (one sequence
+// of 65537 x 1023 binary32 with sigmoid gates 710 us, with those of four 804).
+constexpr int kCtasPerSmBack = 2;
 
 constexpr int kMaxCluster = 16;
 constexpr int kWarps = 4;     // of a CTA at most: strips side by side, times tiles one after the other
@@ -745,7 +748,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_fwd(ScanArgs s
 // The gradient, on arrays turned so that step 0 is the last one forward; s.h is shifted by one step, so
 // that row t holds the state before that step (row steps - 1 is h0).
 template <typename T, int N, bool SIG, bool WIDE, bool CLUSTER, int ST>
-__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) k_scan_bwd(ScanArgs s, unsigned ctiles, unsigned csize, int times)
+__global__ void __launch_bounds__(kWarps * 32, CLUSTER ? kCtasPerSmBack : kCtasPerSm) k_scan_bwd(ScanArgs s, unsigned ctiles, unsigned csize, int times)
 {
     extern __shared__ __align__(16) unsigned char dyn[];
     constexpr int NA = SIG ? 4 : 3;
