@@ -409,23 +409,22 @@ def scan_backward(a, x, h, grad_h, h0=None, resets=None, grad_last=None, gate=GA
     if _elsewhere(stream, dev):
         with _On(stream, dev, (a, x, h, grad_h, h0, resets, grad_last), out, status):
             return scan_backward(a, x, h, grad_h, h0, resets, grad_last, gate, reverse, out, None, status, skip)
-    got = {}
-    for name, size, kind in (("grad_a", shape, dt), ("grad_x", shape, dt), ("grad_h0", edge, torch.float32)):
-        if name not in skip:
-            got[name] = _given(out, name, size, kind, dev, a)
-    ga, gx, g0 = got.get("grad_a"), got.get("grad_x"), got.get("grad_h0")
+    ga = _given(out, "grad_a", shape, dt, dev, a) if "grad_a" not in skip else None
+    gx = _given(out, "grad_x", shape, dt, dev, a) if "grad_x" not in skip else None
+    g0 = _given(out, "grad_h0", edge, torch.float32, dev, a) if "grad_h0" not in skip else None
     if out is not None:
         _whole(g0, "grad_h0", edge, torch.float32, dev)
     sa, sh, sg = a.stride(), h.stride(), grad_h.stride()
-    sga = ga.stride() if ga is not None else _NO_STRIDE
-    sgx = gx.stride() if gx is not None else _NO_STRIDE
+    pa, sga = (ga.data_ptr(), ga.stride()) if ga is not None else (None, _NO_STRIDE)
+    px, sgx = (gx.data_ptr(), gx.stride()) if gx is not None else (None, _NO_STRIDE)
     sr = resets.stride() if rp is not None else _NO_STRIDE
     _check(_library().per_scan_backward(
         _SCAN.pack(t, b, c, code, flags, sa[0], sa[1], sx[0], sx[1], sh[0], sh[1], sg[0], sg[1], sga[0], sga[1],
                    sgx[0], sgx[1], sr[0], sr[1], _status_ptr(status, dev) or 0, 0, 0),
-        a.data_ptr(), xp, yp, hp, rp, gp, lp, *(None if z is None else z.data_ptr() for z in (ga, gx, g0)),
-        _raw_stream(dev)), "scan_backward")
-    return got
+        a.data_ptr(), xp, yp, hp, rp, gp, lp, pa, px, None if g0 is None else g0.data_ptr(), _raw_stream(dev)),
+        "scan_backward")
+    got = {"grad_a": ga, "grad_x": gx, "grad_h0": g0}
+    return {k: z for k, z in got.items() if z is not None} if skip else got
 
 
 class _GatedScan(torch.autograd.Function):
