@@ -280,7 +280,8 @@ cudaError_t launch_t(const VerifyArgs &a, const DeviceInfo &dev, cudaStream_t st
     constexpr unsigned P = 16 / sizeof(T);
     const unsigned pieces = (a.vocab + P - 1) / P + 1;   // a row that starts off a boundary has one more
     // CTAs for a sequence: more as long as each keeps at least 512 pieces (two a lane) and there are fewer than 8 an SM
-    // in all (so fewer than 16 after the last doubling): each runs the accept tests again (512 sequences of 131072: 4 CTAs a sequence 100 us, 8 103, 2 124)
+    // in all (so fewer than 16 after the last doubling): each runs the accept tests again (512 sequences of 131072:
+    // 4 CTAs a sequence 100 us, 8 103, 2 124)
     unsigned csize = 1;
     while (csize < kMaxCluster && pieces / csize > 1024 && (unsigned long long)a.batch * csize < 8ull * dev.sms) csize *= 2;
     return launch_clusters(k_verify<T>, a.batch * csize, kThreads, csize, 0, st, a, csize, (pieces + csize - 1) / csize);
