@@ -121,13 +121,19 @@ __device__ __forceinline__ void gates(F2 a, F2 &w, F2 &v)
 __device__ __forceinline__ float weigh(float w, float h, float more) { return w == 0.0f ? more : fmaf(w, h, more); }
 
 // A stretch of steps.  A is NaN where the stretch drops what comes in (a weight of exactly 0 in it), and is
-// never 0: a product that underflows is held at the smallest number, so that an infinite state times it
-// stays infinite.  (A weight of NaN makes H NaN too.)
+// never 0: a product that underflows is held at the smallest number of its sign, so that an infinite state times
+// it stays infinite.  (A weight of NaN makes H NaN too.)
 struct Stretch {
     float A, H;
 };
 
-__device__ __forceinline__ float nonzero(float a) { return a == 0.0f ? 1.4e-45f : a; }
+// (by its bits: copysignf takes the long sequence to 162 us, this to 151)
+__device__ __forceinline__ float nonzero(float a)
+{
+    int bits = __float_as_int(a);
+    if (a == 0.0f) bits |= 1;
+    return __int_as_float(bits);
+}
 
 __device__ __forceinline__ float apply(Stretch s, float h)
 {

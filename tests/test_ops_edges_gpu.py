@@ -559,3 +559,19 @@ def test_distill_rows_masked_by_the_lowest_value(kind, tau, v):
         oo.close(f32(got["loss"])[rows], want["loss"], want["bloss"])
     for got in (step, back):
         oo.close(f32(got["grad"])[rows], want["grad"], want["bgrad"], kind)
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("b, t, c", [(2, 96, 8), (1, 5000, 24), (40, 300, 256)])
+def test_scan_infinite_states_keep_their_sign(kind, b, t, c):
+    """Through decays of either sign, whose products underflow: the sign of the state is that of the product."""
+    g = np.random.default_rng(120)
+    a = (0.5 * torch.where(rand(g, b, t, c) > 0, 1.0, -1.0)).to(TYPES[kind])
+    x, h0 = rand(g, b, t, c, kind=kind), torch.full((b, c), float("inf"), device="cuda")
+    want = torch.cumprod(torch.sign(a.double()), 1) * float("inf")
+    got = ops.scan_forward(a, x, h0=h0)
+    assert torch.equal(got["h"].double(), want) and torch.equal(got["last"].double(), want[:, -1])
+    back = ops.scan_backward(a, None, torch.zeros_like(a), x, grad_last=h0)
+    ends = torch.cumprod(torch.sign(a.double()).flip(1), 1).flip(1) * float("inf")       # of w_t ... w_{T-1}
+    assert torch.equal(back["grad_h0"].double(), ends[:, 0])
+    assert torch.equal(back["grad_x"][:, :-1].double(), ends[:, 1:]) and torch.isinf(back["grad_x"][:, -1]).all()
