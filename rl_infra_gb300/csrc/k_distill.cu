@@ -493,10 +493,10 @@ __global__ void __launch_bounds__((kMaxWarps + 1) * 32, kCtasPerSm) k_distill(Di
         if (rank == 0 && t >= loaders) {
             float loss = 0.0f;
             for (int k = lane; k < K; k += 32)
-                if (q[k] != 0.0f) loss += q[k] * (d[k] - ((xk[k] - m) - l));
+                if (q[k] != 0.0f) loss += q[k] * a.tau * (d[k] - ((xk[k] - m) - l));   // (tau first: it may keep it finite)
             for (int o = 16; o; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
             if (lane == 0) {
-                a.loss[row] = sh.some && !(lse <= kNothing) ? a.tau * loss : 0.0f;
+                a.loss[row] = sh.some && !(lse <= kNothing) ? loss : 0.0f;
                 if (a.lse) a.lse[row] = lse;
             }
         }

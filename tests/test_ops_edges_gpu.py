@@ -575,3 +575,19 @@ def test_scan_infinite_states_keep_their_sign(kind, b, t, c):
     ends = torch.cumprod(torch.sign(a.double()).flip(1), 1).flip(1) * float("inf")       # of w_t ... w_{T-1}
     assert torch.equal(back["grad_h0"].double(), ends[:, 0])
     assert torch.equal(back["grad_x"][:, :-1].double(), ends[:, 1:]) and torch.isinf(back["grad_x"][:, -1]).all()
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("tau", [0.1, 0.5])
+def test_distill_losses_of_lowest_logits_are_finite(kind, tau):
+    """The teacher wants what the student masks by its type's lowest value: tau times that is finite, and so is the
+    loss (U is taken eight times: the difference, q, its sum and the products)."""
+    g = np.random.default_rng(130)
+    low = torch.finfo(TYPES[kind]).min
+    x = rand(g, 200, 64, kind=kind)
+    x[:, 5] = low
+    t, idx = rand(g, 200, 3), torch.full((200, 3), 5, dtype=torch.int32, device="cuda")
+    want = -float(np.float32(tau)) * low * np.ones(200)
+    for call in (ops.distill_forward, ops.distill_step):
+        got = call(x, t, idx, temperature=tau)["loss"]
+        np.testing.assert_allclose(host(got), want, rtol=8 * oo.U, atol=0)
