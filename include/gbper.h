@@ -336,7 +336,7 @@ per_status per_rank_order_noalloc(const float *d_raw, uint32_t n, uint32_t *d_or
  * every array is contiguous.  Input strides may be any value (0 repeats a row for all); rows of an
  * output must not overlap.  Pointers need the alignment of their element type only; rows whose
  * start and stride are multiples of 16 bytes move in 16-byte pieces.  Others take longer on a GB300: a
- * recurrence with one such array (an odd number of channels, a shifted view) 1.4 to 2.6 times, a
+ * recurrence with one such array (an odd number of channels, a shifted view) 1.4 to 2.4 times, a
  * verification of 512 rows of 131071 1.3 times.  Where d_status is given, a call sets PER_DEVFLAG_*
  * bits in it (it never clears them).
  * ------------------------------------------------------------------------------------------- */
