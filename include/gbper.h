@@ -498,6 +498,120 @@ per_status per_scan_backward(const per_scan_shape *shape, const void *d_a, const
                              const void *d_gh, const float *d_glast, void *d_ga, void *d_gx,
                              float *d_gh0, void *stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Drafted trees over a paged cache: what an actor's target needs around per_verify_draft.  Keys and
+ * values lie in pages of S slots; row b of a table names the pages of sequence b in order, so that its
+ * slot s is slot s mod S of page table[b, s / S].  A sequence's first `start` (or `len`) slots hold its
+ * context; a call's new tokens (the nodes of a tree, each one token) take the slots behind it in their order.
+ * Nothing beyond a sequence's own slots is read into a result: what stale slots hold, NaN too, does not
+ * matter.  A table entry outside [0, P), a slot behind the table's end, a negative start and a count that
+ * is out of range set PER_DEVFLAG_BAD_INDEX; what they name is left out (not written, not attended to).
+ * ------------------------------------------------------------------------------------------- */
+
+typedef struct {
+    uint32_t pages;        /* P, 0 .. 2^31 - 1 */
+    uint32_t page;         /* S, slots of a page, 1 .. 2^20 */
+    uint32_t width;        /* pages that a row of the table names; width S < 2^31 */
+    uint32_t heads;        /* Hkv, heads of keys and values, 1 .. 4096 */
+    uint32_t dim;          /* D, entries of a head, 1 .. 256 */
+    uint32_t type;         /* PER_TYPE_* of the cache and of all that goes in and out of it */
+    int64_t stride_table;                  /* between sequences */
+    int64_t stride_k[3], stride_v[3];      /* between pages, slots of a page, heads (any layout) */
+} per_cache;
+
+enum { PER_APPEND_INTERLEAVED = 1u };   /* per_append_shape.flags: entries 2 j and 2 j + 1 turn together, else j and j + rot / 2 */
+
+typedef struct {
+    per_cache cache;
+    uint32_t batch;        /* B, 0 .. 2^20 (0 is a no-op) */
+    uint32_t tokens;       /* N, new tokens a sequence has at most; B N < 2^31 (0 is a no-op) */
+    uint32_t q_heads;      /* Hq, heads of queries, 0 .. 4096 (0: no queries) */
+    uint32_t rot;          /* entries of a head that are rotated, even, 0 .. D */
+    int64_t stride_in[2][3];               /* of k and of v: between sequences, tokens, heads */
+    int64_t stride_q[3], stride_q_out[3];
+    int64_t stride_positions;              /* between sequences */
+    uint32_t flags;        /* PER_APPEND_* */
+    uint32_t reserved;     /* 0 */
+} per_append_shape;
+
+/*
+ * per_cache_append -- keys and values of new tokens into their slots, keys and queries rotated by their
+ * positions on the way.  Token i < d_counts[b] of sequence b goes to slot d_starts[b] + i.  With pos =
+ * d_positions[b, i] (NULL: d_starts[b] + i) and theta_j = pos d_inv_freq[j], for j < rot / 2,
+ *     x'_j = x_j cos theta_j - x_j* sin theta_j,    x'_j* = x_j* cos theta_j + x_j sin theta_j,
+ * where j* = j + rot / 2 (or the places are 2 j and 2 j + 1 with PER_APPEND_INTERLEAVED); entries from
+ * rot on, and values, are copied as they are.  The angle is reduced in 64-bit fixed point: theta is off by
+ * at most 2^-23 of a radian for any 32-bit position and |d_inv_freq| <= 1.  Sums are binary32, rounded once.
+ * Queries need no cache: they are rotated into d_q_out (which may be d_q itself, same strides);
+ * those of tokens i >= d_counts[b] come out as 0.  Nothing else is written: slots outside
+ * [start, start + count) keep what they hold.  Two tokens must not name one slot of one page.
+ *   d_k, d_v [B x N x Hkv x D], d_q, d_q_out [B x N x Hq x D] (NULL where Hq is 0), d_table [B x width]
+ *   int32, d_starts [B] int32, d_counts [B] int32 or NULL (N), d_positions [B x N] int32 or NULL,
+ *   d_inv_freq [rot / 2] float (NULL where rot is 0).
+ */
+per_status per_cache_append(const per_append_shape *shape, const void *d_k, const void *d_v, const void *d_q,
+                            void *d_k_cache, void *d_v_cache, void *d_q_out, const int32_t *d_table,
+                            const int32_t *d_starts, const int32_t *d_counts, const int32_t *d_positions,
+                            const float *d_inv_freq, uint32_t *d_status, void *stream);
+
+typedef struct {
+    per_cache cache;
+    uint32_t batch;        /* B, 0 .. 2^20 (0 is a no-op) */
+    uint32_t nodes;        /* N, nodes a sequence has at most, 0 .. 1024 (0 is a no-op) */
+    uint32_t q_heads;      /* Hq, a multiple of Hkv, at most 64 to each: query head h reads head h / (Hq / Hkv) */
+    float scale;           /* of the scores, finite */
+    int64_t stride_q[3], stride_out[3];    /* between sequences, nodes, heads */
+    int64_t stride_mask[2];                /* between sequences (0: one mask for all), between nodes */
+    uint64_t work_bytes;   /* of d_work */
+} per_attend_shape;
+
+/*
+ * per_tree_attention -- attention of the drafted nodes of each sequence over its context and over one
+ * another.  Node i < m = d_counts[b] of sequence b sees the d_lens[b] tokens of the context and those nodes j < m,
+ * in slots d_lens[b] + j, that its mask names (d_mask[b, i, j] != 0; NULL: j <= i, a chain).  Over what it sees,
+ *     out_i = sum_j p_ij v_j,   p_ij = exp(s_ij - lse_i),   s_ij = scale q_i . k_j,   lse_i = log sum_j exp s_ij.
+ * A node that sees nothing (or only scores of -inf) gives 0 and an lse of -inf, and so does a node
+ * i >= m.  What a node does not see takes no part, whatever it holds (infinities and NaN too).  N = 1
+ * is the step of plain decoding.  Products of 16-bit types are summed in binary32, scores and their
+ * sums are binary32, and p is rounded once to the type before its product with v (the sum of p is
+ * not); binary32 entries are taken as two parts whose products give 21 bits (an infinite entry then gives
+ * NaN).  Out is rounded once.
+ *   d_q, d_out [B x N x Hq x D], d_mask [B x N x N] bytes, d_lens, d_counts [B] int32 (counts NULL: N),
+ *   d_table [B x width] int32, d_lse [B x N x Hq] float (contiguous) or NULL, d_work: work_bytes of scratch
+ *   memory (16-byte aligned) that this call alone uses until it has run; per_tree_attention_work says
+ *   how much.
+ * Which CTA takes which part depends on the lengths alone, and parts are joined in their order: the same
+ * inputs give the same bits.
+ * per_tree_attention_work -- the bytes of d_work that a call of this shape needs on the current device.
+ */
+per_status per_tree_attention(const per_attend_shape *shape, const void *d_q, const void *d_k_cache,
+                              const void *d_v_cache, const int32_t *d_table, const int32_t *d_lens,
+                              const int32_t *d_counts, const uint8_t *d_mask, void *d_out, float *d_lse,
+                              void *d_work, uint32_t *d_status, void *stream);
+per_status per_tree_attention_work(const per_attend_shape *shape, uint64_t *bytes);
+
+typedef struct {
+    per_cache cache;
+    uint32_t batch;        /* B, 0 .. 2^20 (0 is a no-op) */
+    uint32_t nodes;        /* N, nodes of a tree, 0 .. 2^20 */
+    uint32_t most;         /* L, entries that a path has at most, 0 .. 1024 (0 is a no-op) */
+    uint32_t reserved;     /* 0 */
+    int64_t stride_path;   /* between sequences */
+} per_keep_shape;
+
+/*
+ * per_cache_keep -- the accepted path of each tree moved to where its sequence goes on: for j <
+ * d_kept[b], keys and values of slot d_lens[b] + d_path[b, j] go to slot d_lens[b] + j.  A path goes from node to
+ * later node: 0 <= path_0 < path_1 < ... < N.  The first entry that breaks this (or lies in a page
+ * that does not exist) ends the path: it and what follows stay, and PER_DEVFLAG_BAD_INDEX is set.  The caller
+ * then counts d_kept[b] more tokens of context.  A page must not lie in two rows of the table if a move
+ * writes to it.
+ *   d_table [B x width] int32, d_lens [B] int32, d_path [B x L] int32, d_kept [B] int32 (0 .. L).
+ */
+per_status per_cache_keep(const per_keep_shape *shape, void *d_k_cache, void *d_v_cache, const int32_t *d_table,
+                          const int32_t *d_lens, const int32_t *d_path, const int32_t *d_kept, uint32_t *d_status,
+                          void *stream);
+
 #ifdef __cplusplus
 }
 #endif

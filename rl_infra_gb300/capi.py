@@ -53,13 +53,15 @@ EXPORTS = ("per_create", "per_destroy", "per_add", "per_sample", "per_update_pri
            "per_total", "per_min", "per_size", "per_status_device", "per_last_error",
            "per_read_state", "per_nleaves", "per_rank_order_noalloc", "per_rank_refresh",
            "per_distill_forward", "per_distill_backward", "per_distill_step", "per_verify_draft",
-           "per_scan_forward", "per_scan_backward", "per_last_op_error")
+           "per_scan_forward", "per_scan_backward", "per_last_op_error",
+           "per_cache_append", "per_tree_attention", "per_tree_attention_work", "per_cache_keep")
 
 # element types, flags and shapes of the learner's and the actor's operators
 PER_TYPE_F32, PER_TYPE_F16, PER_TYPE_BF16 = 0, 1, 2
 PER_DISTILL_IDX64 = 1
 PER_VERIFY_TOKENS64 = 1
 PER_SCAN_SIGMOID, PER_SCAN_REVERSE = 1, 2
+PER_APPEND_INTERLEAVED = 1
 
 
 class per_config(ctypes.Structure):
@@ -89,6 +91,28 @@ class per_scan_shape(ctypes.Structure):
                 ("type", ctypes.c_uint32), ("flags", ctypes.c_uint32)] + [
         ("stride_" + n, ctypes.c_int64 * 2) for n in ("a", "x", "h", "gh", "ga", "gx", "resets")] + [
         ("d_status", ctypes.c_void_p), ("wait_limit_ms", ctypes.c_uint32), ("withhold", ctypes.c_uint32)]
+
+
+class per_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_uint32) for n in ("pages", "page", "width", "heads", "dim", "type")] + [
+        ("stride_table", ctypes.c_int64), ("stride_k", ctypes.c_int64 * 3), ("stride_v", ctypes.c_int64 * 3)]
+
+
+class per_append_shape(ctypes.Structure):
+    _fields_ = [("cache", per_cache)] + [(n, ctypes.c_uint32) for n in ("batch", "tokens", "q_heads", "rot")] + [
+        ("stride_in", ctypes.c_int64 * 3 * 2), ("stride_q", ctypes.c_int64 * 3), ("stride_q_out", ctypes.c_int64 * 3),
+        ("stride_positions", ctypes.c_int64), ("flags", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+class per_attend_shape(ctypes.Structure):
+    _fields_ = [("cache", per_cache)] + [(n, ctypes.c_uint32) for n in ("batch", "nodes", "q_heads")] + [
+        ("scale", ctypes.c_float), ("stride_q", ctypes.c_int64 * 3), ("stride_out", ctypes.c_int64 * 3),
+        ("stride_mask", ctypes.c_int64 * 2), ("work_bytes", ctypes.c_uint64)]
+
+
+class per_keep_shape(ctypes.Structure):
+    _fields_ = [("cache", per_cache)] + [(n, ctypes.c_uint32) for n in ("batch", "nodes", "most", "reserved")] + [
+        ("stride_path", ctypes.c_int64)]
 
 
 class PerError(RuntimeError):
@@ -160,6 +184,14 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         L.per_scan_forward.restype = st
         L.per_scan_backward.argtypes = [vp] * 12
         L.per_scan_backward.restype = st
+        L.per_cache_append.argtypes = [vp] * 14
+        L.per_cache_append.restype = st
+        L.per_tree_attention.argtypes = [vp] * 13
+        L.per_tree_attention.restype = st
+        L.per_tree_attention_work.argtypes = [vp, ctypes.POINTER(u64)]
+        L.per_tree_attention_work.restype = st
+        L.per_cache_keep.argtypes = [vp] * 9
+        L.per_cache_keep.restype = st
         L.per_last_op_error.argtypes = []
         L.per_last_op_error.restype = ctypes.c_char_p
         _lib = L
@@ -282,6 +314,28 @@ def per_scan_backward(shape, d_a, d_x, d_h, d_h0, d_resets, d_gh, d_glast, d_ga,
 
 
 # -- torch-facing convenience ---------------------------------------------------------------
+
+
+def per_cache_append(shape, d_k, d_v, d_q, d_k_cache, d_v_cache, d_q_out, d_table, d_starts, d_counts, d_positions,
+                     d_inv_freq, d_status, stream):
+    return load().per_cache_append(shape, d_k, d_v, d_q, d_k_cache, d_v_cache, d_q_out, d_table, d_starts, d_counts,
+                                   d_positions, d_inv_freq, d_status, stream)
+
+
+def per_tree_attention(shape, d_q, d_k_cache, d_v_cache, d_table, d_lens, d_counts, d_mask, d_out, d_lse, d_work,
+                       d_status, stream):
+    return load().per_tree_attention(shape, d_q, d_k_cache, d_v_cache, d_table, d_lens, d_counts, d_mask, d_out, d_lse,
+                                     d_work, d_status, stream)
+
+
+def per_tree_attention_work(shape):
+    v = ctypes.c_uint64()
+    s = load().per_tree_attention_work(shape, ctypes.byref(v))
+    return s, v.value
+
+
+def per_cache_keep(shape, d_k_cache, d_v_cache, d_table, d_lens, d_path, d_kept, d_status, stream):
+    return load().per_cache_keep(shape, d_k_cache, d_v_cache, d_table, d_lens, d_path, d_kept, d_status, stream)
 
 def _ptr(t, dtype, what, allow_none=False):
     if t is None:

@@ -5,6 +5,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdio>
+#include <utility>
 
 using namespace gbper;
 
@@ -138,6 +139,84 @@ void set_axis(P **p, const void *src, const int64_t stride[2], long long dst[2],
         dst[1] = -stride[1];
     }
     *p = reinterpret_cast<P *>(const_cast<char *>(c));
+}
+
+// ---- the paged cache ------------------------------------------------------------------------
+
+const char *cache_fault(const per_cache &c)
+{
+    if (c.pages > 0x7fffffffu) return "pages must be below 2^31";
+    if (c.page == 0 || c.page > (1u << 20)) return "page must be in 1 .. 2^20";
+    if ((uint64_t)c.width * c.page > 0x7fffffffull) return "width x page must be below 2^31";
+    if (c.heads == 0 || c.heads > 4096) return "heads must be in 1 .. 4096";
+    if (c.dim == 0 || c.dim > 256) return "dim must be in 1 .. 256";
+    if (bad_type(c.type)) return "unknown element type";
+    return nullptr;
+}
+
+bool on16(const void *p, const int64_t *stride, int n, unsigned e)
+{
+    if (misaligned(p, 16)) return false;
+    for (int i = 0; i < n; ++i)
+        if (stride[i] * (int64_t)e % 16 != 0) return false;
+    return true;
+}
+
+CacheArgs cache_args(const per_cache &c, void *k, void *v, const int32_t *table, uint32_t *status)
+{
+    CacheArgs a{};
+    a.k = k;
+    a.v = v;
+    a.table = table;
+    a.status = status;
+    for (int i = 0; i < 3; ++i) {
+        a.sk[i] = c.stride_k[i];
+        a.sv[i] = c.stride_v[i];
+    }
+    a.st = c.stride_table;
+    a.pages = c.pages;
+    a.width = c.width;
+    a.heads = c.heads;
+    a.dim = c.dim;
+    a.page.set(c.page);
+    const unsigned e = type_bytes(c.type);
+    a.vec = c.dim * e % 16 == 0 && on16(k, c.stride_k, 3, e) && on16(v, c.stride_v, 3, e);
+    return a;
+}
+
+// The rows of a cache that is written to must not overlap; its three outer axes may be nested in any order.
+bool overlaps3(const int64_t st[3], uint64_t n0, uint64_t n1, uint64_t n2, uint64_t inner)
+{
+    struct Axis {
+        uint64_t s, n;
+    } x[3] = {{0, n0}, {0, n1}, {0, n2}};
+    for (int i = 0; i < 3; ++i) x[i].s = st[i] < 0 ? 0 - (uint64_t)st[i] : (uint64_t)st[i];
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2 - i; ++j)
+            if (x[j].s > x[j + 1].s) std::swap(x[j], x[j + 1]);
+    uint64_t covered = inner;   // what lies below the axis, in elements
+    for (const Axis &a : x) {
+        if (a.n == 0) return false;
+        if (a.n == 1) continue;
+        if (a.s < covered) return true;
+        covered += a.s * (a.n - 1);
+    }
+    return false;
+}
+
+const char *attend_fault(const per_attend_shape *sh)
+{
+    if (!sh) return "shape is NULL";
+    if (const char *f = cache_fault(sh->cache)) return f;
+    if (sh->batch > (1u << 20)) return "batch must be at most 2^20";
+    if (sh->nodes > 1024) return "nodes must be at most 1024";
+    if (sh->q_heads == 0 || sh->q_heads % sh->cache.heads || sh->q_heads / sh->cache.heads > 64)
+        return "q_heads must be 1 .. 64 times heads";
+    // tiles of 32 keys, of which no sequence has fewer than one
+    if (((uint64_t)sh->cache.width * sh->cache.page / 32 + 1) * sh->batch * sh->cache.heads >> 45)
+        return "batch x width x page x heads must be below 2^50";
+    if (!std::isfinite(sh->scale) || !std::isfinite(sh->scale * 1.5f)) return "scale must be finite";
+    return nullptr;
 }
 
 }  // namespace
@@ -294,6 +373,169 @@ per_status per_scan_backward(const per_scan_shape *shape, const void *d_a, const
     a.channels = shape->channels;
     set_waits(a, shape);
     return done(launch_scan_backward((int)shape->type, sig, a, reinterpret_cast<cudaStream_t>(stream)), where);
+}
+
+per_status per_cache_append(const per_append_shape *shape, const void *d_k, const void *d_v, const void *d_q,
+                            void *d_k_cache, void *d_v_cache, void *d_q_out, const int32_t *d_table,
+                            const int32_t *d_starts, const int32_t *d_counts, const int32_t *d_positions,
+                            const float *d_inv_freq, uint32_t *d_status, void *stream)
+{
+    const char *where = "per_cache_append";
+    const per_append_shape *sh = shape;
+    if (!sh) return refuse(where, "shape is NULL");
+    const per_cache &c = sh->cache;
+    if (const char *f = cache_fault(c)) return refuse(where, f);
+    if (sh->batch > (1u << 20)) return refuse(where, "batch must be at most 2^20");
+    if ((uint64_t)sh->batch * sh->tokens > 0x7fffffffull) return refuse(where, "batch x tokens must be below 2^31");
+    if (sh->q_heads > 4096) return refuse(where, "q_heads must be at most 4096");
+    if (sh->rot > c.dim || sh->rot % 2) return refuse(where, "rot must be even and at most dim");
+    if ((sh->flags & ~(uint32_t)PER_APPEND_INTERLEAVED) || sh->reserved) return refuse(where, "unknown flags");
+    if (sh->batch == 0 || sh->tokens == 0) return PER_OK;
+    if (!d_k || !d_v || !d_starts) return refuse(where, "k, v and starts are required");
+    if (c.pages && (!d_k_cache || !d_v_cache)) return refuse(where, "the caches are required");
+    if (c.width && !d_table) return refuse(where, "table is required");
+    if (sh->q_heads && (!d_q || !d_q_out)) return refuse(where, "q and q_out are required");
+    if (sh->rot && !d_inv_freq) return refuse(where, "inv_freq is required");
+    const unsigned e = type_bytes(c.type);
+    if (misaligned(d_k, e) || misaligned(d_v, e) || misaligned(d_q, e) || misaligned(d_q_out, e) ||
+        misaligned(d_k_cache, e) || misaligned(d_v_cache, e) || misaligned(d_table, 4) || misaligned(d_starts, 4) ||
+        misaligned(d_counts, 4) || misaligned(d_positions, 4) || misaligned(d_inv_freq, 4) || misaligned(d_status, 4))
+        return refuse(where, "misaligned pointer");
+    if (overlaps3(c.stride_k, c.pages, c.page, c.heads, c.dim) || overlaps3(c.stride_v, c.pages, c.page, c.heads, c.dim))
+        return refuse(where, "rows of a cache overlap");
+    if (sh->q_heads && overlaps3(sh->stride_q_out, sh->batch, sh->tokens, sh->q_heads, c.dim))
+        return refuse(where, "rows of q_out overlap");
+    if (sh->q_heads && d_q == d_q_out)
+        for (int i = 0; i < 3; ++i)
+            if (sh->stride_q[i] != sh->stride_q_out[i]) return refuse(where, "q_out in the place of q needs its strides");
+    AppendArgs a{};
+    a.c = cache_args(c, d_k_cache, d_v_cache, d_table, d_status);
+    a.k = d_k;
+    a.v = d_v;
+    a.q = d_q;
+    a.q_out = d_q_out;
+    a.starts = d_starts;
+    a.counts = d_counts;
+    a.positions = d_positions;
+    a.inv_freq = d_inv_freq;
+    for (int i = 0; i < 3; ++i) {
+        a.si[0][i] = sh->stride_in[0][i];
+        a.si[1][i] = sh->stride_in[1][i];
+        a.sq[i] = sh->stride_q[i];
+        a.sqo[i] = sh->stride_q_out[i];
+    }
+    a.sp = sh->stride_positions;
+    a.batch = sh->batch;
+    a.tokens = sh->tokens;
+    a.q_heads = sh->q_heads;
+    a.rot = sh->rot;
+    a.interleaved = (sh->flags & PER_APPEND_INTERLEAVED) != 0;
+    // whole 16-byte pieces everywhere, and a rotation that begins and ends with one
+    a.c.vec = a.c.vec && on16(d_k, sh->stride_in[0], 3, e) && on16(d_v, sh->stride_in[1], 3, e) &&
+              (!sh->q_heads || (on16(d_q, sh->stride_q, 3, e) && on16(d_q_out, sh->stride_q_out, 3, e))) &&
+              sh->rot * e % (a.interleaved ? 16 : 32) == 0;
+    return done(launch_append((int)c.type, a, reinterpret_cast<cudaStream_t>(stream)), where);
+}
+
+per_status per_tree_attention_work(const per_attend_shape *shape, uint64_t *bytes)
+{
+    const char *where = "per_tree_attention_work";
+    if (const char *f = attend_fault(shape)) return refuse(where, f);
+    if (!bytes) return refuse(where, "bytes is NULL");
+    *bytes = 0;
+    if (shape->batch == 0 || shape->nodes == 0) return PER_OK;
+    AttendArgs a{};
+    a.c = cache_args(shape->cache, nullptr, nullptr, nullptr, nullptr);
+    a.batch = shape->batch;
+    a.nodes = shape->nodes;
+    a.q_heads = shape->q_heads;
+    unsigned long long n = 0;
+    const cudaError_t e = attend_work((int)shape->cache.type, a, &n);
+    *bytes = n;
+    return done(e, where);
+}
+
+per_status per_tree_attention(const per_attend_shape *shape, const void *d_q, const void *d_k_cache,
+                              const void *d_v_cache, const int32_t *d_table, const int32_t *d_lens,
+                              const int32_t *d_counts, const uint8_t *d_mask, void *d_out, float *d_lse,
+                              void *d_work, uint32_t *d_status, void *stream)
+{
+    const char *where = "per_tree_attention";
+    if (const char *f = attend_fault(shape)) return refuse(where, f);
+    const per_cache &c = shape->cache;
+    if (shape->batch == 0 || shape->nodes == 0) return PER_OK;
+    if (!d_q || !d_lens || !d_out) return refuse(where, "q, lens and out are required");
+    if (c.pages && (!d_k_cache || !d_v_cache)) return refuse(where, "the caches are required");
+    if (c.width && !d_table) return refuse(where, "table is required");
+    const unsigned e = type_bytes(c.type);
+    if (misaligned(d_q, e) || misaligned(d_k_cache, e) || misaligned(d_v_cache, e) || misaligned(d_out, e) ||
+        misaligned(d_table, 4) || misaligned(d_lens, 4) || misaligned(d_counts, 4) || misaligned(d_lse, 4) ||
+        misaligned(d_work, 16) || misaligned(d_status, 4))
+        return refuse(where, "misaligned pointer");
+    if (overlaps3(shape->stride_out, shape->batch, shape->nodes, shape->q_heads, c.dim))
+        return refuse(where, "rows of out overlap");
+    AttendArgs a{};
+    a.c = cache_args(c, const_cast<void *>(d_k_cache), const_cast<void *>(d_v_cache), d_table, d_status);
+    a.q = d_q;
+    a.lens = d_lens;
+    a.counts = d_counts;
+    a.mask = d_mask;
+    a.out = d_out;
+    a.lse = d_lse;
+    a.work = static_cast<float *>(d_work);
+    for (int i = 0; i < 3; ++i) {
+        a.sq[i] = shape->stride_q[i];
+        a.so[i] = shape->stride_out[i];
+    }
+    a.sm[0] = shape->stride_mask[0];
+    a.sm[1] = shape->stride_mask[1];
+    a.batch = shape->batch;
+    a.nodes = shape->nodes;
+    a.q_heads = shape->q_heads;
+    a.c2 = (float)((double)shape->scale * 1.4426950408889634);
+    a.qvec = c.dim * e % 16 == 0 && on16(d_q, shape->stride_q, 3, e);
+    a.opair = e == 2 && c.dim % 2 == 0 && !misaligned(d_out, 4) && shape->stride_out[0] % 2 == 0 &&
+              shape->stride_out[1] % 2 == 0 && shape->stride_out[2] % 2 == 0;
+    unsigned long long need = 0;
+    const cudaError_t err = attend_work((int)c.type, a, &need);
+    if (err != cudaSuccess) return done(err, where);
+    if (need > shape->work_bytes || (need && !d_work)) return refuse(where, "work is smaller than per_tree_attention_work says");
+    return done(launch_attend((int)c.type, a, reinterpret_cast<cudaStream_t>(stream)), where);
+}
+
+per_status per_cache_keep(const per_keep_shape *shape, void *d_k_cache, void *d_v_cache, const int32_t *d_table,
+                          const int32_t *d_lens, const int32_t *d_path, const int32_t *d_kept, uint32_t *d_status,
+                          void *stream)
+{
+    const char *where = "per_cache_keep";
+    const per_keep_shape *sh = shape;
+    if (!sh) return refuse(where, "shape is NULL");
+    const per_cache &c = sh->cache;
+    if (const char *f = cache_fault(c)) return refuse(where, f);
+    if (sh->batch > (1u << 20)) return refuse(where, "batch must be at most 2^20");
+    if (sh->nodes > (1u << 20)) return refuse(where, "nodes must be at most 2^20");
+    if (sh->most > 1024) return refuse(where, "most must be at most 1024");
+    if (sh->reserved) return refuse(where, "unknown flags");
+    if (sh->batch == 0 || sh->most == 0) return PER_OK;
+    if (!d_lens || !d_path || !d_kept) return refuse(where, "lens, path and kept are required");
+    if (c.pages && (!d_k_cache || !d_v_cache)) return refuse(where, "the caches are required");
+    if (c.width && !d_table) return refuse(where, "table is required");
+    const unsigned e = type_bytes(c.type);
+    if (misaligned(d_k_cache, e) || misaligned(d_v_cache, e) || misaligned(d_table, 4) || misaligned(d_lens, 4) ||
+        misaligned(d_path, 4) || misaligned(d_kept, 4) || misaligned(d_status, 4))
+        return refuse(where, "misaligned pointer");
+    if (overlaps3(c.stride_k, c.pages, c.page, c.heads, c.dim) || overlaps3(c.stride_v, c.pages, c.page, c.heads, c.dim))
+        return refuse(where, "rows of a cache overlap");
+    KeepArgs a{};
+    a.c = cache_args(c, d_k_cache, d_v_cache, d_table, d_status);
+    a.lens = d_lens;
+    a.path = d_path;
+    a.kept = d_kept;
+    a.sp = sh->stride_path;
+    a.batch = sh->batch;
+    a.nodes = sh->nodes;
+    a.most = sh->most;
+    return done(launch_keep((int)c.type, a, reinterpret_cast<cudaStream_t>(stream)), where);
 }
 
 }  // extern "C"

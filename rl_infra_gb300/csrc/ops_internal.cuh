@@ -54,12 +54,72 @@ struct ScanArgs {
     unsigned withhold;   // the rank, from 1, of the CTA in each cluster that sends nothing (0: none)
 };
 
+// n / d for n < 2^31 by one multiplication: (floor(n mul / 2^32) + n) >> shift
+struct FastDiv {
+    unsigned d, mul, shift;
+    __host__ void set(unsigned by)
+    {
+        d = by;
+        shift = 0;
+        while ((1ull << shift) < by) ++shift;
+        mul = (unsigned)((((1ull << shift) - by) << 32) / by + 1);
+    }
+    __device__ __forceinline__ unsigned div(unsigned n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
+
+// The paged cache of a call.  Sequence b's slot s: page table[b * st + s / S], slot s mod S of it.
+struct CacheArgs {
+    void *k, *v;
+    const int *table;
+    unsigned *status;
+    long long sk[3], sv[3], st;
+    unsigned pages, width, heads, dim;
+    FastDiv page;
+    int vec;                    // every head starts on 16 bytes and ends there
+};
+
+struct AppendArgs {
+    CacheArgs c;
+    const void *k, *v, *q;
+    void *q_out;
+    const int *starts, *counts, *positions;
+    const float *inv_freq;
+    long long si[2][3], sq[3], sqo[3], sp;
+    unsigned batch, tokens, q_heads, rot;
+    int interleaved;
+};
+
+struct AttendArgs {
+    CacheArgs c;
+    const void *q;
+    const int *lens, *counts;
+    const uint8_t *mask;
+    void *out;
+    float *lse;
+    float *work;
+    long long sq[3], so[3], sm[2];
+    unsigned batch, nodes, q_heads;
+    float c2;                   // scale log2(e)
+    int qvec, opair;            // queries move in 16-byte pieces; outputs of 16 bits in pairs
+};
+
+struct KeepArgs {
+    CacheArgs c;
+    const int *lens, *path, *kept;
+    long long sp;
+    unsigned batch, nodes, most;
+};
+
 enum DistillPart { kDistillForward = 0, kDistillBackward = 1, kDistillStep = 2 };
 
 cudaError_t launch_distill(int type, DistillPart part, const DistillArgs &a, cudaStream_t st);
 cudaError_t launch_verify(int type, const VerifyArgs &a, cudaStream_t st);
 cudaError_t launch_scan_forward(int type, bool sigmoid, const ScanArgs &a, cudaStream_t st);
 cudaError_t launch_scan_backward(int type, bool sigmoid, const ScanArgs &a, cudaStream_t st);
+cudaError_t launch_append(int type, const AppendArgs &a, cudaStream_t st);
+cudaError_t launch_keep(int type, const KeepArgs &a, cudaStream_t st);
+cudaError_t launch_attend(int type, const AttendArgs &a, cudaStream_t st);
+cudaError_t attend_work(int type, const AttendArgs &a, unsigned long long *bytes);
 
 // ---- element types ------------------------------------------------------------------------
 __device__ __forceinline__ float to_f32(float v) { return v; }

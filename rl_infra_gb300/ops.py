@@ -6,10 +6,13 @@
       probabilities, from given random numbers
   scan_forward / scan_backward / scan_step             a gated linear recurrence with episode
       resets, its gradient, its single step
+  cache_append / tree_attention / cache_keep           a paged cache of keys and values: new tokens
+      put into it (keys and queries rotated), attention of a tree of drafted tokens over it, the
+      accepted path of the tree kept; forward only
   distill_loss, gated_scan                             the same for torch.autograd
 
 Nothing here computes: arguments are checked and marshalled, outputs allocated, and each call
-enqueues one kernel of libgbper on the given (or current) stream without a synchronisation.
+enqueues one kernel of libgbper (tree_attention two) on the given (or current) stream without a synchronisation.
 include/gbper.h defines every operator; the innermost axis of every tensor must be contiguous, the
 outer ones may have any stride.  `out` takes a dict of preallocated outputs under the names that the
 call returns.
@@ -33,9 +36,16 @@ _TYPES = {torch.float32: capi.PER_TYPE_F32, torch.float16: capi.PER_TYPE_F16,
 _DISTILL = struct.Struct("@Q4I4qfI")
 _VERIFY = struct.Struct("@4I6q2I")
 _SCAN = struct.Struct("@Q4I14qQ2I")
+# per_append_shape, per_attend_shape and per_keep_shape, each with a per_cache in front
+_APPEND = struct.Struct("@6I7q4I13q2I")
+_ATTEND = struct.Struct("@6I7q3If8qQ")
+_KEEP = struct.Struct("@6I7q4Iq")
 assert _DISTILL.size == ctypes.sizeof(capi.per_distill_shape)
 assert _VERIFY.size == ctypes.sizeof(capi.per_verify_shape)
 assert _SCAN.size == ctypes.sizeof(capi.per_scan_shape)
+assert _APPEND.size == ctypes.sizeof(capi.per_append_shape)
+assert _ATTEND.size == ctypes.sizeof(capi.per_attend_shape)
+assert _KEEP.size == ctypes.sizeof(capi.per_keep_shape)
 
 
 def _bad(what, want, t):
@@ -457,3 +467,174 @@ def gated_scan(a, x, h0=None, resets=None, gate=GATE_DECAY, reverse=False):
     """(h, last) as a function that torch.autograd can differentiate by a, x and h0, once (a second
     derivative is refused).  Arguments as scan_forward's: resets mark first steps."""
     return _GatedScan.apply(a, x, h0, resets, gate, reverse)
+
+
+# -- drafted trees over a paged cache ----------------------------------------------------------
+
+_NO_STRIDES = (0, 0, 0)
+_ENDLESS = 1 << 20
+
+
+def _serving(*tensors):
+    """These operators have no gradient: a tensor that asks for one is refused, not passed as a constant."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise RuntimeError("the cache's operators have no gradient: call them under torch.no_grad()")
+
+
+def _cache(k_cache, v_cache, block_table, batch, dev, code):
+    """The head of a shape, and the table's pointer."""
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise _bad("k_cache", "of 4 axes", k_cache)
+    if _TYPES.get(k_cache.dtype) != code:
+        raise _bad("k_cache", "of the dtype of what it is used with", k_cache)
+    kp = _arg(k_cache, "k_cache", k_cache.shape, k_cache.dtype, dev)
+    vp = _arg(v_cache, "v_cache", k_cache.shape, k_cache.dtype, dev)
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise _bad("block_table", "of 2 axes", block_table)
+    width = block_table.shape[1]
+    tp = _arg(block_table, "block_table", torch.Size((batch, width)), torch.int32, dev)
+    pages, page, heads, dim = k_cache.shape
+    return (pages, page, width, heads, dim, code, block_table.stride(0), *k_cache.stride()[:3],
+            *v_cache.stride()[:3]), kp, vp, tp
+
+
+def cache_append(k, v, k_cache, v_cache, block_table, starts, q=None, positions=None, counts=None, inv_freq=None,
+                 interleaved=False, out=None, status=None, stream=None):
+    """Puts k, v [B, N, Hkv, D] into the slots from starts [B] on of k_cache, v_cache [pages, slots, Hkv, D] (any
+    strides), whose pages block_table [B, width] names; token i < counts[b] (None: N) of sequence b goes to slot
+    starts[b] + i.  Keys and q [B, N, Hq, D] are rotated by positions [B, N] (None: their slots) times inv_freq
+    [rot / 2] (float; None: not at all) in their first rot entries: halves against one another, or neighbours
+    (interleaved).  Returns {"q": the rotated queries} ({} without q; out={"q": q} rotates in place).
+    See per_cache_append."""
+    code, dev = _lead(k, "k", 4)
+    b, n, heads, dim = k.shape
+    vp = _arg(v, "v", k.shape, k.dtype, dev)
+    head, kp, cp, tp = _cache(k_cache, v_cache, block_table, b, dev, code)
+    if head[3] != heads or head[4] != dim:
+        raise _bad("k_cache", f"of shape (pages, slots, {heads}, {dim})", k_cache)
+    edge = torch.Size((b,))
+    sp = _whole(starts, "starts", edge, torch.int32, dev)
+    if sp is None:
+        raise TypeError("starts is required")
+    np_ = _whole(counts, "counts", edge, torch.int32, dev)
+    pp = None if positions is None else _arg(positions, "positions", torch.Size((b, n)), torch.int32, dev)
+    fp, rot = None, 0
+    if inv_freq is not None:
+        if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+            raise _bad("inv_freq", "of 1 axis", inv_freq)
+        fp, rot = _whole(inv_freq, "inv_freq", inv_freq.shape, torch.float32, dev), 2 * inv_freq.shape[0]
+    hq, qp = 0, None
+    if q is not None:
+        if not isinstance(q, torch.Tensor) or q.dim() != 4:
+            raise _bad("q", "of 4 axes", q)
+        hq = q.shape[2]
+        qp = _arg(q, "q", torch.Size((b, n, hq, dim)), k.dtype, dev)
+    _serving(k, v, q, k_cache, v_cache, inv_freq)
+    if _elsewhere(stream, dev):
+        with _On(stream, dev, (k, v, k_cache, v_cache, block_table, starts, q, positions, counts, inv_freq), out, status):
+            return cache_append(k, v, k_cache, v_cache, block_table, starts, q, positions, counts, inv_freq,
+                                interleaved, out, status)
+    turned, op, sq, so = None, None, _NO_STRIDES, _NO_STRIDES
+    if q is not None:
+        turned = _given(out, "q", q.shape, q.dtype, dev, q)
+        op, sq, so = turned.data_ptr(), q.stride()[:3], turned.stride()[:3]
+    _check(_library().per_cache_append(
+        _APPEND.pack(*head, b, n, hq, rot, *k.stride()[:3], *v.stride()[:3], *sq, *so,
+                     positions.stride(0) if pp is not None else 0,
+                     capi.PER_APPEND_INTERLEAVED if interleaved else 0, 0),
+        k.data_ptr(), vp, qp, kp, cp, op, tp, sp, np_, pp, fp, _status_ptr(status, dev), _raw_stream(dev)),
+        "cache_append")
+    return {} if q is None else {"q": turned}
+
+
+def tree_attention(q, k_cache, v_cache, block_table, lens, mask=None, counts=None, scale=None, out=None, work=None,
+                   status=None, stream=None):
+    """{"out" [B, N, Hq, D], "lse" float [B, N, Hq]}: attention of the nodes q [B, N, Hq, D] over the lens [B] tokens of
+    context in the cache and over the nodes behind them (counts [B], None: N) that mask [N, N] or [B, N, N]
+    (bool or uint8; node i sees node j; None: a chain, j <= i) names.  scale None: D ** -0.5.  work: a uint8
+    tensor of scratch memory for a program that keeps one for each stream (tree_attention_work says how large; by
+    default one is allocated).  See per_tree_attention."""
+    code, dev = _lead(q, "q", 4)
+    b, n, hq, dim = q.shape
+    head, kp, vp, tp = _cache(k_cache, v_cache, block_table, b, dev, code)
+    if head[4] != dim:
+        raise _bad("k_cache", f"of shape (pages, slots, heads, {dim})", k_cache)
+    edge = torch.Size((b,))
+    lp = _whole(lens, "lens", edge, torch.int32, dev)
+    if lp is None:
+        raise TypeError("lens is required")
+    np_ = _whole(counts, "counts", edge, torch.int32, dev)
+    mp, sm = None, _NO_STRIDE
+    if mask is not None:
+        if not isinstance(mask, torch.Tensor) or mask.dtype not in (torch.bool, torch.uint8):
+            raise _bad("mask", "of dtype bool or uint8", mask)
+        each = mask.dim() == 3
+        mp = _arg(mask, "mask", torch.Size((b, n, n) if each else (n, n)), mask.dtype, dev)
+        sm = mask.stride()[:2] if each else (0, mask.stride(0))
+    _serving(q, k_cache, v_cache)
+    if _elsewhere(stream, dev):
+        with _On(stream, dev, (q, k_cache, v_cache, block_table, lens, mask, counts, work), out, status):
+            return tree_attention(q, k_cache, v_cache, block_table, lens, mask, counts, scale, out, work, status)
+    got = {"out": _given(out, "out", q.shape, q.dtype, dev, q),
+           "lse": _given(out, "lse", (b, n, hq), torch.float32, dev, q)}
+    if out is not None and not got["lse"].is_contiguous():
+        raise _bad("lse", "contiguous", got["lse"])
+    lib = _library()
+    shape = (*head, b, n, hq, dim ** -0.5 if scale is None else scale, *q.stride()[:3], *got["out"].stride()[:3], *sm)
+    if work is None:
+        size = _work_bytes(lib, _ATTEND.pack(*shape, 0), "tree_attention")
+        work = torch.empty(size, dtype=torch.uint8, device=q.device)
+    elif not isinstance(work, torch.Tensor) or work.dtype is not torch.uint8 or work.get_device() != dev or \
+            not work.is_contiguous():
+        raise _bad("work", f"contiguous, of dtype uint8, on cuda:{dev}", work)
+    _check(lib.per_tree_attention(
+        _ATTEND.pack(*shape, work.numel()), q.data_ptr(), kp, vp, tp, lp, np_, mp, got["out"].data_ptr(),
+        got["lse"].data_ptr(), work.data_ptr(), _status_ptr(status, dev), _raw_stream(dev)), "tree_attention")
+    return got
+
+
+def _work_bytes(lib, shape, name):
+    size = ctypes.c_uint64()
+    _check(lib.per_tree_attention_work(shape, ctypes.byref(size)), name)
+    return size.value
+
+
+def tree_attention_work(q, k_cache, block_table):
+    """Bytes of scratch memory that tree_attention needs for these shapes on the current device."""
+    code, dev = _lead(q, "q", 4)
+    b, n, hq, dim = q.shape
+    head = _cache(k_cache, k_cache, block_table, b, dev, code)[0]
+    with torch.cuda.device(dev):
+        return _work_bytes(_library(), _ATTEND.pack(*head, b, n, hq, 1.0, *_NO_STRIDES, *_NO_STRIDES, *_NO_STRIDE, 0),
+                           "tree_attention_work")
+
+
+def cache_keep(k_cache, v_cache, block_table, lens, path, kept, nodes=None, status=None, stream=None):
+    """Moves the accepted path of each tree to where its sequence goes on: for j < kept[b], slot lens[b] +
+    path[b, j] of the caches goes to slot lens[b] + j.  path [B, L] names ever later nodes (below nodes, where
+    that is given); an entry that does not ends the path and sets PER_DEVFLAG_BAD_INDEX in status.  See
+    per_cache_keep."""
+    if not isinstance(k_cache, torch.Tensor) or not k_cache.is_cuda:
+        raise _bad("k_cache", "on a CUDA device", k_cache)
+    code, dev = _TYPES.get(k_cache.dtype), k_cache.get_device()
+    if code is None:
+        raise _bad("k_cache", "of dtype float32, float16 or bfloat16", k_cache)
+    if not isinstance(path, torch.Tensor) or path.dim() != 2:
+        raise _bad("path", "of 2 axes", path)
+    b, most = path.shape
+    head, kp, vp, tp = _cache(k_cache, v_cache, block_table, b, dev, code)
+    edge = torch.Size((b,))
+    pp = _arg(path, "path", path.shape, torch.int32, dev)
+    lp = _whole(lens, "lens", edge, torch.int32, dev)
+    np_ = _whole(kept, "kept", edge, torch.int32, dev)
+    if lp is None or np_ is None:
+        raise TypeError("lens and kept are required")
+    _serving(k_cache, v_cache)
+    if _elsewhere(stream, dev):
+        with _On(stream, dev, (k_cache, v_cache, block_table, lens, path, kept), None, status):
+            return cache_keep(k_cache, v_cache, block_table, lens, path, kept, nodes, status)
+    _check(_library().per_cache_keep(
+        _KEEP.pack(*head, b, _ENDLESS if nodes is None else nodes, most, 0, path.stride(0)), kp, vp, tp, lp, pp, np_,
+        _status_ptr(status, dev), _raw_stream(dev)), "cache_keep")
