@@ -1,0 +1,359 @@
+// attend.cuh -- what the kernels of tree attention share: how the work is cut, how tiles of the paged cache
+// come into shared memory, where results go.
+//
+// The cut.  All tiles of all sequences and heads of keys lie in a row, which is cut into equal parts, one for
+// each CTA that the GPU holds at once (a team of CTAs, where the rows of a head of keys need several).  A part that
+// begins or ends inside a sequence leaves its sums in scratch memory, and a second kernel joins them in their
+// order.  So one long sequence fills the GPU, and ragged ones leave no SM idle.
+#pragma once
+
+#include <cuda.h>
+
+#include "ops_internal.cuh"
+
+namespace gbper {
+namespace attend {
+
+typedef unsigned long long u64;
+constexpr int kRecord = 8;             // ints of a CTA's record for the joining kernel
+constexpr unsigned kWaitMs = 2000;     // limit of a wait
+
+// ---- how the work is cut -----------------------------------------------------------------------
+struct Span {              // a sequence
+    int len, total, count; // context, context and nodes, nodes; in the table's range
+    bool bad;
+};
+
+__device__ __forceinline__ Span span(const AttendArgs &a, unsigned b)
+{
+    const long long room = (long long)a.c.width * a.c.page.d;
+    const int len = a.lens[b], count = a.counts ? a.counts[b] : (int)a.nodes;
+    Span s;
+    s.bad = len < 0 || count < 0 || (unsigned)count > a.nodes || (long long)len + count > room;
+    s.count = min(max(count, 0), (int)a.nodes);
+    s.len = (int)min((long long)max(len, 0), room);
+    s.total = (int)min((long long)s.len + s.count, room);
+    return s;
+}
+
+template <int KT>
+__device__ __forceinline__ unsigned tiles_of(const Span &s)
+{
+    return s.count == 0 ? 1u : max(1u, ((unsigned)s.total + KT - 1) / KT);   // a sequence without nodes has zeros to write
+}
+
+// (all < 2^45, checked on the host)
+__device__ __forceinline__ u64 part_start(u64 t, u64 all, unsigned teams) { return t * all / teams; }
+
+// A team's stretches, one sequence and head after another.
+template <int KT>
+struct Walk {
+    u64 pos, end, at, all;   // at: the sequence's first tile
+    unsigned teams, b, n_tiles, h, tile0, tile1;
+    Span s;
+
+    // All NT threads of the CTA; `scan` holds NT / 32 words.  False: the team has nothing to do.
+    template <int NT>
+    __device__ __forceinline__ bool begin(const AttendArgs &a, unsigned team, unsigned max_teams, u64 *scan)
+    {
+        const unsigned t = threadIdx.x, lane = t & 31u, warp = t >> 5;
+        const unsigned per = (a.batch + NT - 1) / NT;
+        const unsigned b0 = min(t * per, a.batch), b1 = min(b0 + per, a.batch);
+        u64 mine = 0;
+        for (unsigned i = b0; i < b1; ++i) mine += tiles_of<KT>(span(a, i));
+        u64 upto = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const u64 o = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += o;
+        }
+        if (lane == 31) scan[warp] = upto;
+        __syncthreads();
+        u64 before = upto - mine;
+        all = 0;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) {
+            if (w < (int)warp) before += scan[w];
+            all += scan[w];
+        }
+        all *= a.c.heads;
+        before *= a.c.heads;                                   // tiles in front of this thread's sequences
+        teams = (unsigned)min((u64)max_teams, all);            // every team has a tile
+        pos = team < teams ? part_start(team, all, teams) : all;
+        end = team < teams ? part_start(team + 1, all, teams) : all;
+        if (pos >= end) return false;
+        __syncthreads();
+        if (pos >= before && pos < before + mine * a.c.heads) {   // one thread's
+            unsigned i = b0;
+            u64 x = before;
+            for (;; ++i) {
+                const u64 n = (u64)tiles_of<KT>(span(a, i)) * a.c.heads;
+                if (pos < x + n) break;
+                x += n;
+            }
+            scan[0] = i;
+            scan[1] = x;
+        }
+        __syncthreads();
+        b = (unsigned)scan[0];
+        at = scan[1];
+        s = span(a, b);
+        n_tiles = tiles_of<KT>(s);
+        return true;
+    }
+
+    __device__ __forceinline__ bool next(const AttendArgs &a)
+    {
+        if (pos >= end) return false;
+        if (pos >= at + (u64)n_tiles * a.c.heads) {
+            at += (u64)n_tiles * a.c.heads;
+            ++b;
+            s = span(a, b);
+            n_tiles = tiles_of<KT>(s);
+        }
+        h = (unsigned)((pos - at) / n_tiles);
+        tile0 = (unsigned)(pos - at - (u64)h * n_tiles);
+        tile1 = (unsigned)min((u64)n_tiles, tile0 + (end - pos));
+        pos += tile1 - tile0;
+        return true;
+    }
+
+    __device__ __forceinline__ bool part() const { return tile0 != 0 || tile1 < n_tiles; }
+
+    // the record of a CTA that begins what others end
+    __device__ __forceinline__ void note(int *record, unsigned team) const
+    {
+        const u64 last = at + (u64)(h + 1) * n_tiles - 1;      // the tile that ends it
+        const unsigned last_team = (unsigned)(((last + 1) * teams + all - 1) / all) - 1;
+        record[0] = (int)b;
+        record[1] = (int)h;
+        record[2] = s.count;
+        record[3] = (int)(last_team - team + 1);               // parts
+    }
+};
+
+// whether node n of sequence b sees the key; `there` is known
+__device__ __forceinline__ bool sees(const AttendArgs &a, unsigned b, const Span &s, int n, unsigned key)
+{
+    if ((int)key < s.len) return true;
+    const unsigned j = key - (unsigned)s.len;
+    if (j >= (unsigned)s.count) return false;
+    if (!a.mask) return (int)j <= n;
+    return a.mask[b * a.sm[0] + n * a.sm[1] + j] != 0;
+}
+
+// zeros for the rows [row0, row0 + m) of nodes that are not there
+template <typename T>
+__device__ __forceinline__ void absent_rows(const AttendArgs &a, const FastDiv &by_group, unsigned b, unsigned h,
+                                            unsigned live, unsigned row0, unsigned m, unsigned t, unsigned threads)
+{
+    const unsigned rows = a.nodes * by_group.d, dim = a.c.dim;
+    const unsigned z0 = max(row0, live), z1 = min(row0 + m, rows);
+    if (z0 >= z1) return;
+    for (unsigned u = t; u < (z1 - z0) * dim; u += threads) {
+        const unsigned r = z0 + u / dim, d = u % dim, node = by_group.div(r), head = h * by_group.d + r - node * by_group.d;
+        static_cast<T *>(a.out)[b * a.so[0] + node * a.so[1] + head * a.so[2] + d] = from_f32<T>(0.0f);
+        if (d == 0 && a.lse) a.lse[((size_t)b * a.nodes + node) * a.q_heads + head] = -INFINITY;
+    }
+}
+
+template <typename T> __device__ __forceinline__ unsigned pack2(float x, float y);
+template <> __device__ __forceinline__ unsigned pack2<__nv_bfloat16>(float x, float y)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const unsigned *>(&h);
+}
+template <> __device__ __forceinline__ unsigned pack2<__half>(float x, float y)
+{
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const unsigned *>(&h);
+}
+template <> __device__ __forceinline__ unsigned pack2<float>(float, float) { return 0; }
+
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
+__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f; }
+
+// Where rows of a CTA's stretch go: to the result or, of a part, to its slot in scratch memory.
+template <typename T>
+struct RowOut {
+    const AttendArgs &a;
+    const FastDiv &by_group;
+    unsigned b, h, live, row0, m;
+    bool part;
+    float *slot;
+
+    // entries d and d + 1 of row r of the tile, its maximum and sum
+    __device__ __forceinline__ void put(unsigned r, unsigned d, float x, float y, float top, float sum) const
+    {
+        const unsigned dim = a.c.dim;
+        if (row0 + r >= live) return;
+        if (part) {
+            float *to = slot + r * dim + d;
+            if (d < dim) to[0] = x;
+            if (d + 1 < dim) to[1] = y;
+            if (d == 0) {
+                slot[m * dim + 2 * r] = top;
+                slot[m * dim + 2 * r + 1] = sum;
+            }
+            return;
+        }
+        const unsigned n = by_group.div(row0 + r), head = h * by_group.d + row0 + r - n * by_group.d;
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        T *to = static_cast<T *>(a.out) + b * a.so[0] + n * a.so[1] + head * a.so[2] + d;
+        if (sizeof(T) == 2 && a.opair) {
+            if (d < dim) *reinterpret_cast<unsigned *>(to) = pack2<T>(x * inv, y * inv);
+        } else {
+            if (d < dim) to[0] = from_f32<T>(x * inv);
+            if (d + 1 < dim) to[1] = from_f32<T>(y * inv);
+        }
+        if (d == 0 && a.lse) a.lse[((size_t)b * a.nodes + n) * a.q_heads + head] = lse_of(top, sum);
+    }
+};
+
+// ---- barriers and copies -------------------------------------------------------------------------
+__device__ __forceinline__ unsigned smem_u32(const void *p) { return (unsigned)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void bar_init(unsigned bar, unsigned count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_expect(unsigned bar, unsigned bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(unsigned bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool bar_try(unsigned bar, unsigned parity)
+{
+    unsigned ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+// Waits for the phase of the given parity to end; false when it has not after kWaitMs, or another wait of the CTA gave up.
+__device__ __noinline__ bool bar_wait_long(unsigned bar, unsigned parity, volatile unsigned *dead)
+{
+    u64 began, now;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(began));
+    for (int tries = 0; tries < 1 << 24; ++tries) {
+        if (bar_try(bar, parity)) return true;
+        if (*dead) return false;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+        if (now - began > kWaitMs * 1000000ull) break;
+    }
+    *dead = 1;
+    return false;
+}
+__device__ __forceinline__ bool bar_wait(unsigned bar, unsigned parity, volatile unsigned *dead)
+{
+    return bar_try(bar, parity) || bar_wait_long(bar, parity, dead);
+}
+
+// The cache as the copy engine sees it: entries, and slots, heads and pages in the order of their strides.
+struct CacheMaps {
+    CUtensorMap k, v;
+    unsigned char k_at[4], v_at[4];    // the axis (1 .. 3) of slot, head and page
+};
+
+__device__ __forceinline__ void load_box(unsigned dst, const CUtensorMap *map, const unsigned char *at, unsigned bar, int d, int slot,
+                                         int head, int page)
+{
+    const int c1 = at[0] == 1 ? slot : at[1] == 1 ? head : page;
+    const int c2 = at[0] == 2 ? slot : at[1] == 2 ? head : page;
+    const int c3 = at[0] == 3 ? slot : at[1] == 3 ? head : page;
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+                 ::"r"(dst), "l"(map), "r"(d), "r"(c1), "r"(c2), "r"(c3), "r"(bar) : "memory");
+}
+
+// What one warp asks for, tile after tile: boxes of 128 bytes by `1 << shift` slots of a page (a power of 2 that
+// divides the page), so that a row's 16-byte pieces lie turned by its number modulo 8.  What lies outside the tensor
+// (entries past the head's, a page that does not exist) comes as zeros.
+template <int KT>
+struct Loader {
+    static constexpr int EN = (KT + 31) / 32;
+    unsigned shift;            // log2 of the rows of a box
+    int page[EN], slot[EN];    // of this lane's boxes of the tile that is looked up
+
+    __device__ __forceinline__ void look_up(const AttendArgs &a, unsigned b, const Span &s, unsigned tile)
+    {
+        const unsigned lane = threadIdx.x & 31u;
+#pragma unroll
+        for (int e = 0; e < EN; ++e) {
+            const unsigned i = lane + 32 * e, key = tile * KT + (i << shift);
+            page[e] = -1;
+            slot[e] = 0;
+            if ((i << shift) < KT && key < (unsigned)s.total) {
+                const unsigned pg = a.c.page.div(key);
+                slot[e] = (int)(key - pg * a.c.page.d);
+                page[e] = a.c.table[b * a.c.st + pg];
+            }
+        }
+    }
+
+    // which boxes have no page: a bit for each in `bad`
+    __device__ __forceinline__ void judge(const AttendArgs &a, const Span &s, unsigned tile, unsigned *bad, bool tell)
+    {
+        const unsigned lane = threadIdx.x & 31u;
+        bool any = false;
+#pragma unroll
+        for (int e = 0; e < EN; ++e) {
+            const unsigned i = lane + 32 * e;
+            const bool wanted = (i << shift) < KT && tile * KT + (i << shift) < (unsigned)s.total;
+            const bool wrong = wanted && (unsigned)page[e] >= a.c.pages;
+            const unsigned bits = __ballot_sync(0xffffffffu, wrong);
+            if (lane == 0) bad[e] = bits;
+            any |= wrong;
+            if (wrong || !wanted) page[e] = (int)a.c.pages;
+        }
+        if (any && tell && a.c.status) atomicOr(a.c.status, PER_DEVFLAG_BAD_INDEX);
+    }
+
+    // one array's tile to `to`: [half][KT][128 bytes].  The bytes are expected by the barrier already.
+    __device__ __forceinline__ void request(const CUtensorMap *map, const unsigned char *at, unsigned h, unsigned to, unsigned halves,
+                                            unsigned per_half, unsigned bar)
+    {
+        const unsigned lane = threadIdx.x & 31u;
+#pragma unroll
+        for (int e = 0; e < EN; ++e) {
+            const unsigned i = lane + 32 * e;
+            if ((i << shift) >= KT) continue;
+            for (unsigned half = 0; half < halves; ++half)
+                load_box(to + half * KT * 128 + (i << shift) * 128, map, at, bar, half * per_half, slot[e], h, page[e]);
+        }
+    }
+};
+
+// ---- host --------------------------------------------------------------------------------------
+struct Plan {
+    unsigned m, row_tiles, teams, grid;
+    bool parts;             // a sequence can lie in several CTAs
+    u64 bytes;
+};
+
+inline Plan plan_of(const AttendArgs &a, unsigned m, unsigned kt, unsigned ctas)
+{
+    Plan p;
+    const u64 rows = (u64)a.nodes * (a.q_heads / a.c.heads);   // at most 2^16
+    p.m = m;
+    p.row_tiles = (unsigned)((rows + m - 1) / m);
+    p.teams = ctas > p.row_tiles ? ctas / p.row_tiles : 1;
+    const u64 most = ((u64)a.c.width * a.c.page.d + kt - 1) / kt;   // tiles of a sequence
+    const u64 tiles = (most ? most : 1) * a.batch * a.c.heads;
+    if (p.teams > tiles) p.teams = (unsigned)tiles;
+    p.grid = p.teams * p.row_tiles;
+    p.parts = most > 1 && p.teams > 1;
+    p.bytes = p.parts ? (u64)p.grid * (kRecord * 4 + 2ull * m * (a.c.dim + 2) * 4) : 0;
+    return p;
+}
+
+// The kernels that take their tiles from the copy engine (k_attend_rows.cu).  *taken false: the call is not theirs.
+cudaError_t attend_rows(int type, const AttendArgs &a, const DeviceInfo &dev, cudaStream_t st, u64 *bytes, bool *taken);
+// The maps of a call's cache; false where the copy engine cannot take it.  kt: keys of a tile.
+bool make_maps(int type, const AttendArgs &a, unsigned kt, CacheMaps *maps, unsigned *shift);   // k_attend.cu
+// joins what several CTAs hold (k_attend.cu)
+cudaError_t join_parts(int type, const AttendArgs &a, const Plan &p, const FastDiv &by_group, cudaStream_t st);
+
+}  // namespace attend
+}  // namespace gbper

@@ -1,0 +1,241 @@
+// attend_mma.cuh -- warp-wide matrix instructions of tree attention's kernels with few rows.
+#pragma once
+
+#include "attend.cuh"
+
+#include <cstring>
+
+namespace gbper {
+namespace attend {
+
+__device__ __forceinline__ void ldsm4(unsigned *r, unsigned at)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(unsigned *r, unsigned at)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+template <typename T> __device__ __forceinline__ void mma16(float *c, const unsigned *a, unsigned b0, unsigned b1);
+template <> __device__ __forceinline__ void mma16<__nv_bfloat16>(float *c, const unsigned *a, unsigned b0, unsigned b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <> __device__ __forceinline__ void mma16<__half>(float *c, const unsigned *a, unsigned b0, unsigned b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma8(float *c, const unsigned *a, unsigned b0, unsigned b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// x = hi + lo: hi rounded to 11 bits, the rest rounded to 11 more (both cut where rounding would reach infinity or
+// pass a NaN).  The instruction reads the upper 19 bits of each word.
+__device__ __forceinline__ void split(float x, unsigned &hi, unsigned &lo)
+{
+    const unsigned b = __float_as_uint(x), half = (b & 0x7fffffffu) < 0x7f7ff000u ? 0x1000u : 0u;
+    hi = (b + half) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi)) + half;
+}
+
+// Where piece c (16 bytes) of row r lies in a tile as the copy engine lays it: halves of 128 bytes of a head,
+// [half][rows][128], each row's pieces turned by its number modulo 8.
+__device__ __forceinline__ unsigned piece(unsigned rows, unsigned r, unsigned c)
+{
+    return (c >> 3) * rows * 128 + r * 128 + (((c & 7u) ^ (r & 7u)) << 4);
+}
+
+// piece c of a row of dim entries at src, entry by entry; zeros past the end and where there is no row
+template <typename T>
+__device__ __forceinline__ uint4 entries(const T *src, unsigned c, unsigned dim, bool some)
+{
+    constexpr int N = 16 / (int)sizeof(T);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (!some) return v;
+    T e[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) e[i] = c * N + i < dim ? src[c * N + i] : from_f32<T>(0.0f);
+    memcpy(&v, e, 16);
+    return v;
+}
+
+// sc = q k for 16 rows from r0 of the m rows at qs, and KW keys from key0 of the kt at ks; `steps` of the instruction
+// along a head.  A binary32 step takes two pieces four apart: column c of the instruction is entry 2 c
+// mod 4 of piece c / 2 * 4, column c + 4 the entry behind it, so that 16 lanes read 16 different banks twice.
+template <typename T, int DP, int KW>
+__device__ __forceinline__ void scores(float (*sc)[4], const unsigned char *qs, unsigned m, unsigned r0, const unsigned char *ks,
+                                       unsigned kt, unsigned key0, unsigned steps)
+{
+    const unsigned lane = threadIdx.x & 31u, g = lane >> 2, q4 = lane & 3u;
+#pragma unroll
+    for (int i = 0; i < KW / 8; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.0f;
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+            if (k >= (int)steps) break;
+            unsigned qa[4];
+            ldsm4(qa, smem_u32(qs + piece(m, r0 + (lane & 15u), k * 2 + (lane >> 4))));
+#pragma unroll
+            for (int i = 0; i < KW / 16; ++i) {
+                unsigned kb[4];   // keys 0-7 and 8-15, entries 0-7 and 8-15 of each
+                ldsm4(kb, smem_u32(ks + piece(kt, key0 + i * 16 + (lane & 7u) + ((lane >> 4) << 3), k * 2 + ((lane >> 3) & 1u))));
+                mma16<T>(sc[2 * i], qa, kb[0], kb[1]);
+                mma16<T>(sc[2 * i + 1], qa, kb[2], kb[3]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < DP / 8; ++k) {
+            if (k >= (int)steps) break;
+            unsigned ah[4], al[4];
+            const unsigned c = (k >> 2) * 8 + (k & 3) + (q4 >> 1) * 4, in = (q4 & 1u) * 8;
+            const float2 x = *reinterpret_cast<const float2 *>(qs + piece(m, r0 + g, c) + in);
+            const float2 y = *reinterpret_cast<const float2 *>(qs + piece(m, r0 + g + 8, c) + in);
+            split(x.x, ah[0], al[0]);
+            split(y.x, ah[1], al[1]);
+            split(x.y, ah[2], al[2]);
+            split(y.y, ah[3], al[3]);
+#pragma unroll
+            for (int i = 0; i < KW / 8; ++i) {
+                const float2 z = *reinterpret_cast<const float2 *>(ks + piece(kt, key0 + i * 8 + g, c) + in);
+                unsigned h0, l0, h1, l1;
+                split(z.x, h0, l0);
+                split(z.y, h1, l1);
+                mma8(sc[i], al, h0, h1);
+                mma8(sc[i], ah, l0, l1);
+                mma8(sc[i], ah, h0, h1);
+            }
+        }
+    }
+}
+
+// o += p v for the same rows and keys (p where the scores were).  binary32: key 2 c is column c of the instruction,
+// 2 c + 1 column c + 4: the scores lie so already.
+template <typename T, int DP, int KW>
+__device__ __forceinline__ void values(float (*o)[4], const float (*p)[4], const unsigned char *vs, unsigned kt, unsigned key0,
+                                       unsigned steps)
+{
+    const unsigned lane = threadIdx.x & 31u, g = lane >> 2, q4 = lane & 3u;
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int k = 0; k < KW / 16; ++k) {
+            const unsigned pa[4] = {pack2<T>(p[2 * k][0], p[2 * k][1]), pack2<T>(p[2 * k][2], p[2 * k][3]),
+                                    pack2<T>(p[2 * k + 1][0], p[2 * k + 1][1]), pack2<T>(p[2 * k + 1][2], p[2 * k + 1][3])};
+#pragma unroll
+            for (int i = 0; i < DP / 16; ++i) {
+                if (i >= (int)steps) break;
+                unsigned vb[4];   // keys 0-7 and 8-15 of entries 0-7, then of entries 8-15
+                ldsm4t(vb, smem_u32(vs + piece(kt, key0 + k * 16 + (lane & 15u), i * 2 + (lane >> 4))));
+                mma16<T>(o[2 * i], pa, vb[0], vb[1]);
+                mma16<T>(o[2 * i + 1], pa, vb[2], vb[3]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < KW / 8; ++k) {
+            unsigned ph[4], pl[4];
+            split(p[k][0], ph[0], pl[0]);
+            split(p[k][2], ph[1], pl[1]);
+            split(p[k][1], ph[2], pl[2]);
+            split(p[k][3], ph[3], pl[3]);
+#pragma unroll
+            for (int i = 0; i < DP / 8; ++i) {
+                if (i >= (int)steps) break;
+                const unsigned r = key0 + k * 8 + q4 * 2, c = i * 2 + (g >> 2), in = (g & 3u) * 4;
+                const float x = *reinterpret_cast<const float *>(vs + piece(kt, r, c) + in);
+                const float y = *reinterpret_cast<const float *>(vs + piece(kt, r + 1, c) + in);
+                unsigned h0, l0, h1, l1;
+                split(x, h0, l0);
+                split(y, h1, l1);
+                mma8(o[i], pl, h0, h1);
+                mma8(o[i], ph, l0, l1);
+                mma8(o[i], ph, h0, h1);
+            }
+        }
+    }
+}
+
+// The softmax's step for a warp's scores sc (in log2 already), in place: maxima and sums of rows g and g + 8 carried on, o
+// brought to the new maxima.  A thread's sums are its own columns' alone.
+template <int DP, int KW>
+__device__ __forceinline__ void soften(float (*sc)[4], float *top, float *sum, float (*o)[4])
+{
+    float keep[2], base[2], up[2] = {top[0], top[1]};
+#pragma unroll
+    for (int i = 0; i < KW / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) up[e >> 1] = fmaxf(up[e >> 1], sc[i][e]);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        up[e] = fmaxf(up[e], __shfl_xor_sync(0xffffffffu, up[e], 1));
+        up[e] = fmaxf(up[e], __shfl_xor_sync(0xffffffffu, up[e], 2));
+        base[e] = up[e] == -INFINITY ? 0.0f : up[e];      // nothing seen yet: every p is 2^-inf = 0
+        keep[e] = ex2(top[e] - base[e]);
+        top[e] = up[e];
+        sum[e] *= keep[e];
+    }
+#pragma unroll
+    for (int i = 0; i < KW / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            sc[i][e] = ex2(sc[i][e] - base[e >> 1]);
+            sum[e >> 1] += sc[i][e];
+        }
+    if (__any_sync(0xffffffffu, keep[0] != 1.0f || keep[1] != 1.0f)) {   // most tiles raise no maximum
+#pragma unroll
+        for (int i = 0; i < DP / 8; ++i) {
+            o[i][0] *= keep[0];
+            o[i][1] *= keep[0];
+            o[i][2] *= keep[1];
+            o[i][3] *= keep[1];
+        }
+    }
+}
+
+// What was taken out of the values of key `key`, for the rows that see it (rare: nothing here is fast).
+template <typename T, int DP>
+__device__ __forceinline__ void give_back(const AttendArgs &a, unsigned b, const Span &s, const int *node, unsigned key, const T *v,
+                                          float (*o)[4])
+{
+    const unsigned q4 = threadIdx.x & 3u;
+    const bool see[2] = {node[0] >= 0 && sees(a, b, s, node[0], key), node[1] >= 0 && sees(a, b, s, node[1], key)};
+#pragma unroll
+    for (int i = 0; i < DP / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const unsigned d = i * 8 + q4 * 2 + (e & 1);
+            if (d >= a.c.dim || !see[e >> 1]) continue;
+            const float x = to_f32(v[d]);
+            if (!finite(x)) o[i][e] += x;
+        }
+}
+
+// Takes what is not finite out of 16 bytes; whether there was any.
+template <typename T>
+__device__ __forceinline__ bool take_out(uint4 *at)
+{
+    Pack<T> p;
+    p.raw = *at;
+    float f[Pack<T>::N];
+    p.unpack(f);
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < Pack<T>::N; ++i)
+        if (!finite(f[i])) {
+            f[i] = 0.0f;
+            any = true;
+        }
+    if (any) {
+        p.pack(f);
+        *at = p.raw;
+    }
+    return any;
+}
+
+}  // namespace attend
+}  // namespace gbper
