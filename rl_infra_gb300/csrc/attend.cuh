@@ -233,7 +233,7 @@ __device__ __forceinline__ bool bar_try(unsigned bar, unsigned parity)
     return ok != 0;
 }
 // Waits for the phase of the given parity to end; false when it has not after kWaitMs, or another wait of the CTA gave up.
-__device__ __noinline__ bool bar_wait_long(unsigned bar, unsigned parity, volatile unsigned *dead)
+static __device__ __noinline__ bool bar_wait_long(unsigned bar, unsigned parity, volatile unsigned *dead)
 {
     u64 began, now;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(began));
@@ -348,8 +348,10 @@ inline Plan plan_of(const AttendArgs &a, unsigned m, unsigned kt, unsigned ctas)
     return p;
 }
 
-// The kernels that take their tiles from the copy engine (k_attend_rows.cu).  *taken false: the call is not theirs.
-cudaError_t attend_rows(int type, const AttendArgs &a, const DeviceInfo &dev, cudaStream_t st, u64 *bytes, bool *taken);
+// The kernels that take their tiles from the copy engine (attend_rows.cuh).  *taken false: the call is not theirs.
+cudaError_t attend_rows_f32(const AttendArgs &a, const DeviceInfo &dev, cudaStream_t st, u64 *bytes, bool *taken);
+cudaError_t attend_rows_f16(const AttendArgs &a, const DeviceInfo &dev, cudaStream_t st, u64 *bytes, bool *taken);
+cudaError_t attend_rows_bf16(const AttendArgs &a, const DeviceInfo &dev, cudaStream_t st, u64 *bytes, bool *taken);
 // The maps of a call's cache; false where the copy engine cannot take it.  kt: keys of a tile.
 bool make_maps(int type, const AttendArgs &a, unsigned kt, CacheMaps *maps, unsigned *shift);   // k_attend.cu
 // joins what several CTAs hold (k_attend.cu)

@@ -1,0 +1,343 @@
+// attend_rows.cuh -- attention over a paged cache for few rows: one warp asks the copy engine for tiles of keys
+// and values, four warps work on them.
+//
+// The rows of a head of keys (its query heads times the nodes) share every key that is read, so that HBM bounds
+// the kernel while they are few.  A CTA takes 16, 32 or 64 rows.  Its four warps share the rows where there are
+// many, the keys of a tile where there are few, and then join through shared memory at the end of a
+// stretch.  Tiles of 32 KB (64 KB of large heads) lie in a ring of barriers: a warp that is done with one
+// never waits for the others, and the copies of the next stretch begin while this one is joined.
+#pragma once
+
+#include "attend_mma.cuh"
+
+#include <algorithm>
+#include <atomic>
+
+namespace gbper {
+namespace attend {
+namespace {
+
+constexpr int kWarps = 4;                  // of them that compute
+constexpr int kThreads = kWarps * 32 + 32;
+
+template <typename T, int DP, int WR>
+struct Cfg {
+    static constexpr int ES = (int)sizeof(T);
+    static constexpr int WK = kWarps / WR;                        // warps along the keys
+    static constexpr int M = 16 * WR;                             // rows of a CTA
+    static constexpr int KT = DP * ES >= 1024 ? 32 : DP * ES >= 256 ? 64 : 128;
+    static constexpr int KW = KT / WK;                            // keys of a warp
+    static constexpr int PER_HALF = 128 / ES;
+    static constexpr int STAGE = 2 * KT * DP * ES;
+    static constexpr int JOIN = WK == 4 ? 2 * 16 * DP * 4 : WK == 2 ? M * DP * 4 : 0;   // what the warps hand over
+    static constexpr int AREA = M * DP * ES > JOIN ? M * DP * ES : JOIN;                // the queries lie there before
+    static constexpr int TAIL = 1024;
+    static constexpr int HALF_SM = 228 * 1024 / 2 - 1024;
+    static constexpr int WHOLE_SM = 227 * 1024;
+    static constexpr int PER_SM = (HALF_SM - AREA - TAIL) / STAGE >= 3 ? 2 : 1;
+    static constexpr int FIT = ((PER_SM == 2 ? HALF_SM : WHOLE_SM) - AREA - TAIL) / STAGE;
+    static constexpr int ST = FIT > 6 ? 6 : FIT;
+    static constexpr int SMEM = ST * STAGE + AREA + TAIL;
+    static_assert(ST >= 2, "fits");
+    static_assert(ES == 4 || KW % 16 == 0, "whole steps of the matrix instruction");
+};
+
+struct Tail {
+    u64 full[6], empty[6];
+    u64 scan[kThreads / 32];
+    unsigned bad[6][4];
+    float ml[2][16][2];        // maxima and sums that the warps hand over
+    unsigned dead;
+};
+static_assert(sizeof(Tail) <= 1024, "");
+
+__device__ __forceinline__ void warps_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool warps_or(bool x)
+{
+    unsigned r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r) : "r"((unsigned)x) : "memory");
+    return r != 0;
+}
+
+template <typename T, int DP, int WR>
+__global__ void __launch_bounds__(kThreads, Cfg<T, DP, WR>::PER_SM)
+k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row_tiles, unsigned max_teams, FastDiv by_group, unsigned shift)
+{
+    using C = Cfg<T, DP, WR>;
+    constexpr int KT = C::KT, KW = C::KW, WK = C::WK, M = C::M, ST = C::ST, ES = C::ES;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    unsigned char *area = smem + ST * C::STAGE;
+    Tail &tail = *reinterpret_cast<Tail *>(area + C::AREA);
+    volatile unsigned *dead = &tail.dead;
+    const unsigned t = threadIdx.x, lane = t & 31u, warp = t >> 5;
+    const unsigned cta = blockIdx.x, team = cta / row_tiles, rt = cta - team * row_tiles;
+    const unsigned group = by_group.d, row0 = rt * M, dim = a.c.dim;
+    const unsigned halves = (dim * ES + 127) / 128;
+    const unsigned full = smem_u32(tail.full), empty = smem_u32(tail.empty);
+
+    if (t == 0) {
+        for (int i = 0; i < ST; ++i) {
+            bar_init(full + 8 * i, 1);
+            bar_init(empty + 8 * i, kWarps);
+        }
+        tail.dead = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    pdl_wait();
+    pdl_release();
+    int *record = reinterpret_cast<int *>(a.work) + (size_t)cta * kRecord;
+    if (a.work && t == 0) record[3] = 0;
+    Walk<KT> w;
+    if (!w.template begin<kThreads>(a, team, max_teams, tail.scan)) return;
+    unsigned st = 0, phase = 0;
+
+    if (warp == kWarps) {   // the warp that asks for tiles
+        Loader<KT> load;
+        load.shift = shift;
+        unsigned asked = 0;
+        bool ok = true;
+        while (ok && w.next(a)) {
+            if (row0 >= (unsigned)w.s.count * group) continue;
+            load.look_up(a, w.b, w.s, w.tile0);
+            for (unsigned tile = w.tile0; tile < w.tile1; ++tile) {
+                if (asked >= (unsigned)ST) ok = __all_sync(0xffffffffu, bar_wait(empty + 8 * st, phase ^ 1, dead));
+                if (!ok) break;
+                const unsigned ks = smem_u32(smem + st * C::STAGE), bar = full + 8 * st;
+                load.judge(a, w.s, tile, tail.bad[st], rt == 0 && w.h == 0);
+                __syncwarp();
+                if (lane == 0) bar_expect(bar, halves * KT * 128 * 2);
+                __syncwarp();
+                load.request(&maps.k, maps.k_at, w.h, ks, halves, C::PER_HALF, bar);
+                load.request(&maps.v, maps.v_at, w.h, ks + KT * DP * ES, halves, C::PER_HALF, bar);
+                ++asked;
+                if (++st == ST) {
+                    st = 0;
+                    phase ^= 1;
+                }
+                if (tile + 1 < w.tile1) load.look_up(a, w.b, w.s, tile + 1);
+            }
+        }
+        if (!ok) {          // given up: the copies under way must land before the CTA ends
+            for (unsigned i = asked > (unsigned)ST ? asked - ST : 0; i < asked; ++i) {
+                unsigned none = 0;
+                bar_wait(full + 8 * (i % ST), i / ST & 1, &none);
+            }
+        }
+    } else {
+        const unsigned g = lane >> 2, q4 = lane & 3u;                // row and column pair of a fragment
+        const unsigned wr = warp / WK, wk = warp - wr * WK, key0 = wk * KW;
+        const unsigned steps = ES == 2 ? (dim + 15) / 16 : (dim + 31) / 32 * 4;   // of the matrix instruction along a head
+        const unsigned slot_floats = M * (dim + 2);
+        float *slots = a.work + (size_t)gridDim.x * kRecord + (size_t)cta * 2 * slot_floats;
+        bool ok = true;
+        while (ok && w.next(a)) {
+            const Span &s = w.s;
+            const unsigned b = w.b, h = w.h;
+            if (w.tile0 == 0 && s.bad && rt == 0 && h == 0 && t == 0 && a.c.status) atomicOr(a.c.status, PER_DEVFLAG_BAD_INDEX);
+            const unsigned live = (unsigned)s.count * group;         // rows of nodes that are there
+            if (w.tile0 == 0) absent_rows<T>(a, by_group, b, h, live, row0, M, t, kWarps * 32);
+            if (w.tile0 == 0 && w.tile1 < w.n_tiles && t == 0) w.note(record, team);
+            if (row0 >= live) continue;
+
+            // the queries, zero where there is none
+            warps_sync();
+            {
+                constexpr unsigned CH = DP * ES / 16;
+                const T *q = static_cast<const T *>(a.q) + b * a.sq[0];
+                for (unsigned u = t; u < M * CH; u += kWarps * 32) {
+                    const unsigned r = u / CH, c = u % CH;
+                    const bool some = row0 + r < live;
+                    const unsigned node = by_group.div(row0 + r), head = h * group + row0 + r - node * group;
+                    const T *src = some ? q + node * a.sq[1] + head * a.sq[2] : q;
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (!a.qvec) v = entries<T>(src, c, dim, some);
+                    else if (some && c * 16 < dim * ES) v = *reinterpret_cast<const uint4 *>(src + c * (16 / ES));
+                    *reinterpret_cast<uint4 *>(area + piece(M, r, c)) = v;
+                }
+            }
+            float o[DP / 8][4];
+#pragma unroll
+            for (int i = 0; i < DP / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+            float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.0f, 0.0f};
+            int node[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const unsigned r = row0 + wr * 16 + g + e * 8;
+                node[e] = r < live ? (int)by_group.div(r) : -1;      // -1: no such row
+            }
+            warps_sync();
+
+            for (unsigned tile = w.tile0; tile < w.tile1; ++tile) {
+                ok = __all_sync(0xffffffffu, bar_wait(full + 8 * st, phase, dead));
+                if (!ok) break;
+                unsigned char *ks = smem + st * C::STAGE, *vs = ks + KT * DP * ES;
+                const bool tail_in = (tile + 1) * KT > (unsigned)s.len;   // nodes, or the end
+                unsigned wrong = 0;
+#pragma unroll
+                for (int e = 0; e < Loader<KT>::EN; ++e) wrong |= tail.bad[st][e];
+
+                // what stale slots hold is taken out of the values, and what is not finite in a node's: it must
+                // reach only the rows that see it
+                bool odd = false;
+                if (tail_in) {
+                    for (unsigned u = t; u < KT * halves * 8; u += kWarps * 32) {
+                        const unsigned r = u % KT, key = tile * KT + r;
+                        uint4 *at = reinterpret_cast<uint4 *>(vs + piece(KT, r, u / KT));
+                        if (key >= (unsigned)s.total) *at = make_uint4(0, 0, 0, 0);
+                        else if (key >= (unsigned)s.len) odd |= take_out<T>(at);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the next copy comes after these stores
+                    odd = warps_or(odd);
+                }
+
+                float sc[KW / 8][4];
+                scores<T, DP, KW>(sc, area, M, wr * 16, ks, KT, key0, steps);
+#pragma unroll
+                for (int i = 0; i < KW / 8; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[i][e] *= a.c2;
+                if (tail_in || wrong) {
+#pragma unroll
+                    for (int i = 0; i < KW / 8; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const unsigned r = key0 + i * 8 + q4 * 2 + (e & 1), box = r >> shift;
+                            const bool there = !((tail.bad[st][box >> 5] >> (box & 31u)) & 1u);
+                            if (!there || node[e >> 1] < 0 || !sees(a, b, s, node[e >> 1], tile * KT + r)) sc[i][e] = -INFINITY;
+                        }
+                }
+                soften<DP, KW>(sc, top, sum, o);
+                values<T, DP, KW>(o, sc, vs, KT, key0, steps);
+                if (odd)
+                    for (unsigned r = key0; r < key0 + KW; ++r) {
+                        const unsigned key = tile * KT + r, box = r >> shift;
+                        if ((int)key < s.len || key >= (unsigned)s.total || ((tail.bad[st][box >> 5] >> (box & 31u)) & 1u)) continue;
+                        const unsigned pg = a.c.page.div(key);
+                        give_back<T, DP>(a, b, s, node, key,
+                                         static_cast<const T *>(a.c.v) + a.c.table[b * a.c.st + pg] * a.c.sv[0] +
+                                             (key - pg * a.c.page.d) * a.c.sv[1] + h * a.c.sv[2], o);
+                    }
+                __syncwarp();
+                if (lane == 0) bar_arrive(empty + 8 * st);
+                if (++st == ST) {
+                    st = 0;
+                    phase ^= 1;
+                }
+            }
+            if (!ok) break;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
+                sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
+            }
+
+            // the warps that share rows join, two by two: the upper ones hand their sums to the lower ones
+            if constexpr (WK > 1) {
+                auto hand = [&](unsigned i) {
+                    float *to = reinterpret_cast<float *>(area) + i * 16 * DP;
+#pragma unroll
+                    for (int k = 0; k < DP / 8; ++k)
+                        *reinterpret_cast<float4 *>(to + (k * 32 + lane) * 4) = make_float4(o[k][0], o[k][1], o[k][2], o[k][3]);
+                    if (q4 == 0) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            tail.ml[i][g + e * 8][0] = top[e];
+                            tail.ml[i][g + e * 8][1] = sum[e];
+                        }
+                    }
+                };
+                auto take = [&](unsigned i) {
+                    const float *from = reinterpret_cast<const float *>(area) + i * 16 * DP;
+                    float mine[2], other[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float m = tail.ml[i][g + e * 8][0], l = tail.ml[i][g + e * 8][1];
+                        const float up = fmaxf(top[e], m), base = up == -INFINITY ? 0.0f : up;
+                        mine[e] = ex2(top[e] - base);
+                        other[e] = ex2(m - base);
+                        sum[e] = sum[e] * mine[e] + l * other[e];
+                        top[e] = up;
+                    }
+#pragma unroll
+                    for (int k = 0; k < DP / 8; ++k) {
+                        const float4 x = *reinterpret_cast<const float4 *>(from + (k * 32 + lane) * 4);
+                        o[k][0] = o[k][0] * mine[0] + x.x * other[0];
+                        o[k][1] = o[k][1] * mine[0] + x.y * other[0];
+                        o[k][2] = o[k][2] * mine[1] + x.z * other[1];
+                        o[k][3] = o[k][3] * mine[1] + x.w * other[1];
+                    }
+                };
+                warps_sync();                                        // the queries are done with
+                if constexpr (WK == 4) {
+                    if (wk >= 2) hand(wk - 2);
+                    warps_sync();
+                    if (wk < 2) take(wk);
+                    warps_sync();
+                }
+                if (wk == 1) hand(wr);
+                warps_sync();
+                if (wk == 0) take(wr);
+            }
+            if (wk == 0) {
+                const RowOut<T> out{a, by_group, b, h, live, row0, M, w.part(), slots + (w.tile0 != 0 ? 0 : slot_floats)};
+#pragma unroll
+                for (int i = 0; i < DP / 8; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        out.put(wr * 16 + g + e * 8, i * 8 + q4 * 2, o[i][2 * e], o[i][2 * e + 1], top[e], sum[e]);
+            }
+        }
+        if (!ok && lane == 0 && a.c.status) atomicOr(a.c.status, PER_DEVFLAG_TIMEOUT);
+    }
+    __syncthreads();   // nobody leaves before the copies have landed
+}
+
+template <typename T, int DP, int WR>
+cudaError_t rows(AttendArgs a, int type, const DeviceInfo &dev, cudaStream_t st, u64 *bytes, bool *taken)
+{
+    using C = Cfg<T, DP, WR>;
+    const Plan p = plan_of(a, C::M, C::KT, (unsigned)dev.sms * C::PER_SM);
+    if (bytes) {
+        *bytes = std::max(*bytes, p.bytes);
+        return cudaSuccess;
+    }
+    CacheMaps maps;
+    unsigned shift;
+    *taken = make_maps(type, a, C::KT, &maps, &shift);
+    if (!*taken) return cudaSuccess;
+    static std::atomic<bool> done[64];   // (two threads may both set the attribute, to the same value)
+    if (!done[dev.device].load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(k_attend_rows<T, DP, WR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (e != cudaSuccess) return e;
+        done[dev.device].store(true, std::memory_order_release);
+    }
+    if (!p.parts) a.work = nullptr;
+    FastDiv by_group;
+    by_group.set(a.q_heads / a.c.heads);
+    const cudaError_t e = launch_clusters(k_attend_rows<T, DP, WR>, p.grid, kThreads, 1, C::SMEM, st, maps, a, p.row_tiles, p.teams,
+                                          by_group, shift);
+    return e != cudaSuccess || !p.parts ? e : join_parts(type, a, p, by_group, st);
+}
+
+template <typename T, int DP>
+cudaError_t rows_d(const AttendArgs &a, int type, const DeviceInfo &dev, cudaStream_t st, u64 *bytes, bool *taken)
+{
+    const unsigned n = a.nodes * (a.q_heads / a.c.heads);
+    if (n <= 16) return rows<T, DP, 1>(a, type, dev, st, bytes, taken);
+    if (n <= 32) return rows<T, DP, 2>(a, type, dev, st, bytes, taken);
+    return rows<T, DP, 4>(a, type, dev, st, bytes, taken);
+}
+
+template <typename T>
+cudaError_t rows_t(const AttendArgs &a, int type, const DeviceInfo &dev, cudaStream_t st, u64 *bytes, bool *taken)
+{
+    if (a.c.dim <= 64) return rows_d<T, 64>(a, type, dev, st, bytes, taken);
+    if (a.c.dim <= 128) return rows_d<T, 128>(a, type, dev, st, bytes, taken);
+    return rows_d<T, 256>(a, type, dev, st, bytes, taken);
+}
+
+}  // namespace
+}  // namespace attend
+}  // namespace gbper

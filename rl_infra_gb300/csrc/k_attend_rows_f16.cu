@@ -1,0 +1,13 @@
+// k_attend_rows_f16.cu -- attend_rows.cuh for caches of binary16 (a file for each type: they compile side by side).
+#include "attend_rows.cuh"
+
+namespace gbper {
+namespace attend {
+
+cudaError_t attend_rows_f16(const AttendArgs &a, const DeviceInfo &dev, cudaStream_t st, u64 *bytes, bool *taken)
+{
+    return rows_t<__half>(a, PER_TYPE_F16, dev, st, bytes, taken);
+}
+
+}  // namespace attend
+}  // namespace gbper
