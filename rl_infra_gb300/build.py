@@ -15,7 +15,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libgbper.so")
 SOURCES = ["per_api.cu", "k_tree.cu", "k_sample.cu", "k_rank.cu", "k_flat.cu",
-           "ops_api.cu", "k_distill.cu", "k_verify.cu", "k_scan.cu", "k_cache.cu", "k_attend.cu",
+           "ops_api.cu", "k_distill.cu", "k_verify.cu", "k_scan.cu", "k_cache.cu", "k_attend.cu", "k_attend_wide.cu",
            "k_attend_rows_f32.cu", "k_attend_rows_f16.cu", "k_attend_rows_bf16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -251,6 +251,17 @@ __device__ __forceinline__ bool bar_wait(unsigned bar, unsigned parity, volatile
     return bar_try(bar, parity) || bar_wait_long(bar, parity, dead);
 }
 
+// A barrier of the warps that `bar` counts, whose wait ends with the others' (a warp that gave up never comes to it).
+struct Meeting {
+    unsigned bar, phase;
+    __device__ __forceinline__ bool operator()(volatile unsigned *dead)
+    {
+        __syncwarp();
+        if ((threadIdx.x & 31u) == 0) bar_arrive(bar);
+        return __all_sync(0xffffffffu, bar_wait(bar, phase++ & 1, dead));
+    }
+};
+
 // The cache as the copy engine sees it: entries, and slots, heads and pages in the order of their strides.
 struct CacheMaps {
     CUtensorMap k, v;
@@ -348,7 +359,9 @@ inline Plan plan_of(const AttendArgs &a, unsigned m, unsigned kt, unsigned ctas)
     return p;
 }
 
-// The kernels that take their tiles from the copy engine (attend_rows.cuh).  *taken false: the call is not theirs.
+// The kernels that take their tiles from the copy engine (k_attend_wide.cu: 16-bit types, heads of up to 128, scale > 0;
+// attend_rows.cuh: all).  *taken false: the call is not theirs.
+cudaError_t attend_wide(int type, const AttendArgs &a, const DeviceInfo &dev, cudaStream_t st, u64 *bytes, bool *taken);
 cudaError_t attend_rows_f32(const AttendArgs &a, const DeviceInfo &dev, cudaStream_t st, u64 *bytes, bool *taken);
 cudaError_t attend_rows_f16(const AttendArgs &a, const DeviceInfo &dev, cudaStream_t st, u64 *bytes, bool *taken);
 cudaError_t attend_rows_bf16(const AttendArgs &a, const DeviceInfo &dev, cudaStream_t st, u64 *bytes, bool *taken);

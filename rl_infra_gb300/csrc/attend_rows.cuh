@@ -43,22 +43,13 @@ struct Cfg {
 };
 
 struct Tail {
-    u64 full[6], empty[6];
+    u64 full[6], empty[6], meet;
     u64 scan[kThreads / 32];
     unsigned bad[6][4];
     float ml[2][16][2];        // maxima and sums that the warps hand over
-    unsigned dead;
+    unsigned dead, odd;        // odd: the number of the last tile that something was taken out of
 };
 static_assert(sizeof(Tail) <= 1024, "");
-
-__device__ __forceinline__ void warps_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool warps_or(bool x)
-{
-    unsigned r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(r) : "r"((unsigned)x) : "memory");
-    return r != 0;
-}
 
 template <typename T, int DP, int WR>
 __global__ void __launch_bounds__(kThreads, Cfg<T, DP, WR>::PER_SM)
@@ -81,7 +72,9 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
             bar_init(full + 8 * i, 1);
             bar_init(empty + 8 * i, kWarps);
         }
+        bar_init(smem_u32(&tail.meet), kWarps);
         tail.dead = 0;
+        tail.odd = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
@@ -131,6 +124,8 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
         const unsigned steps = ES == 2 ? (dim + 15) / 16 : (dim + 31) / 32 * 4;   // of the matrix instruction along a head
         const unsigned slot_floats = M * (dim + 2);
         float *slots = a.work + (size_t)gridDim.x * kRecord + (size_t)cta * 2 * slot_floats;
+        Meeting meet{smem_u32(&tail.meet), 0};
+        unsigned tiles_done = 0;
         bool ok = true;
         while (ok && w.next(a)) {
             const Span &s = w.s;
@@ -142,7 +137,7 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
             if (row0 >= live) continue;
 
             // the queries, zero where there is none
-            warps_sync();
+            if (!(ok = meet(dead))) break;
             {
                 constexpr unsigned CH = DP * ES / 16;
                 const T *q = static_cast<const T *>(a.q) + b * a.sq[0];
@@ -167,7 +162,7 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                 const unsigned r = row0 + wr * 16 + g + e * 8;
                 node[e] = r < live ? (int)by_group.div(r) : -1;      // -1: no such row
             }
-            warps_sync();
+            if (!(ok = meet(dead))) break;
 
             for (unsigned tile = w.tile0; tile < w.tile1; ++tile) {
                 ok = __all_sync(0xffffffffu, bar_wait(full + 8 * st, phase, dead));
@@ -181,6 +176,7 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                 // what stale slots hold is taken out of the values, and what is not finite in a node's: it must
                 // reach only the rows that see it
                 bool odd = false;
+                ++tiles_done;
                 if (tail_in) {
                     for (unsigned u = t; u < KT * halves * 8; u += kWarps * 32) {
                         const unsigned r = u % KT, key = tile * KT + r;
@@ -189,7 +185,9 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                         else if (key >= (unsigned)s.len) odd |= take_out<T>(at);
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the next copy comes after these stores
-                    odd = warps_or(odd);
+                    if (odd) tail.odd = tiles_done;
+                    if (!(ok = meet(dead))) break;
+                    odd = *(volatile unsigned *)&tail.odd == tiles_done;
                 }
 
                 float sc[KW / 8][4];
@@ -269,15 +267,15 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                         o[k][3] = o[k][3] * mine[1] + x.w * other[1];
                     }
                 };
-                warps_sync();                                        // the queries are done with
+                if (!(ok = meet(dead))) break;                       // the queries are done with
                 if constexpr (WK == 4) {
                     if (wk >= 2) hand(wk - 2);
-                    warps_sync();
+                    if (!(ok = meet(dead))) break;
                     if (wk < 2) take(wk);
-                    warps_sync();
+                    if (!(ok = meet(dead))) break;
                 }
                 if (wk == 1) hand(wr);
-                warps_sync();
+                if (!(ok = meet(dead))) break;
                 if (wk == 0) take(wr);
             }
             if (wk == 0) {

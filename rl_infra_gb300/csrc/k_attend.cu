@@ -18,6 +18,7 @@ namespace attend {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr unsigned kFew = 32;    // rows of a head of keys that the warp-wide instruction takes
 
 template <typename T, int DP>
 struct Cfg {
@@ -309,6 +310,11 @@ cudaError_t attend(int type, const AttendArgs &a, cudaStream_t st, u64 *bytes)
     if (e != cudaSuccess) return e;
     if (bytes) *bytes = 0;
     bool taken = false;
+    const unsigned rows = a.nodes * (a.q_heads / a.c.heads);
+    if (type != PER_TYPE_F32 && a.c.dim <= 128 && rows > kFew && (bytes || a.c2 > 0.0f)) {
+        e = attend_wide(type, a, dev, st, bytes, &taken);
+        if (e != cudaSuccess || (taken && !bytes)) return e;
+    }
     e = type == PER_TYPE_F32 ? attend_rows_f32(a, dev, st, bytes, &taken)
         : type == PER_TYPE_F16 ? attend_rows_f16(a, dev, st, bytes, &taken) : attend_rows_bf16(a, dev, st, bytes, &taken);
     if (e != cudaSuccess || (taken && !bytes)) return e;

@@ -1,0 +1,530 @@
+// k_attend_wide.cu -- attention over a paged cache for many rows: the products on the tensor cores' own
+// instruction, with scores, p and outputs in tensor memory.
+//
+// A head of keys with many rows (query heads times nodes) is bound by its products, which the warp-wide
+// instruction makes at a quarter of the rate.  Here one thread issues them on tiles of 128 rows by 128 keys;
+// another warp asks the copy engine for keys and values (a ring of tiles, keys and values in turn); two groups of
+// four warps take the softmax, a thread a row.  Each group has its scores and its output in tensor memory:
+//     up to 128 rows:  both groups take the same rows and every other tile of keys, and join at the end;
+//     more:            each group takes 128 of up to 256 rows, and both every tile.
+// While one group turns scores into p (written over them, rounded to the type), the other's products run.
+//
+// The maximum that p refers to is raised only where a row's rises by more than 2^8 (exact all the same: p and
+// its sums keep their relative precision, and stay below 2^8 x 2^31): outputs in tensor memory are then
+// scaled, which is rare.
+#include "attend_mma.cuh"
+
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
+namespace gbper {
+namespace attend {
+namespace {
+
+constexpr int kGroups = 2, kThreads = kGroups * 128 + 64;   // and a warp for the copies, one for the products
+constexpr int KT = 128;                                      // keys of a tile, and rows of a group
+constexpr float kRise = 8.0f;
+constexpr int kColumns = 512;                                // of tensor memory: two of scores, two of outputs, 128 each
+
+template <int DP, bool PAIR>
+struct Cfg {
+    static constexpr int TILE = KT * DP * 2;                 // bytes of a tile of keys or of values
+    static constexpr int QB = (PAIR ? 2 : 1) * TILE;
+    static constexpr int TAIL = 3072;
+    static constexpr int FIT = (227 * 1024 - QB - TAIL) / TILE;
+    static constexpr int ST = FIT > 10 ? 10 : FIT;
+    static constexpr int SMEM = ST * TILE + QB + TAIL;
+    static constexpr int M = PAIR ? 256 : 128;
+    static_assert(ST >= 5, "the keys of the next tile come before this one's values are free");
+};
+
+struct Tail {
+    u64 full[10], empty[10], q_ready, s_full[2], p_ready[2], o_full[2], meet, last;
+    u64 scan[kThreads / 32];
+    unsigned bad[10][4];
+    float ml[2][128][2];
+    unsigned dead, odd, tmem;
+};
+static_assert(sizeof(Tail) <= 3072, "");
+
+// ---- the tensor cores' instructions ---------------------------------------------------------------
+// Operands of 128-byte rows, 16-byte pieces turned modulo 8; groups of 8 rows 1024 bytes apart.  `lead`: bytes
+// between blocks of 64 entries where those run across the product's columns (values).
+__device__ __forceinline__ u64 operand(unsigned at, unsigned lead)
+{
+    return (u64)((at & 0x3ffffu) >> 4) | (u64)(lead >> 4) << 16 | (u64)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+// 128 rows by n columns, binary32 sums; b_wide: the second operand's entries run along its columns
+template <typename T>
+__host__ __device__ constexpr unsigned product(unsigned n, bool b_wide)
+{
+    return 1u << 4 | (std::is_same<T, __nv_bfloat16>::value ? 1u << 7 | 1u << 10 : 0u) | (b_wide ? 1u << 16 : 0u) | (n >> 3) << 17 | (128u >> 4) << 24;
+}
+__device__ __forceinline__ void multiply(unsigned d, u64 a, u64 b, unsigned how, unsigned add)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(how), "r"(add) : "memory");
+}
+__device__ __forceinline__ void multiply_t(unsigned d, unsigned a, u64 b, unsigned how, unsigned add)   // a in tensor memory
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(how), "r"(add) : "memory");
+}
+// arrives when all products issued before are done
+__device__ __forceinline__ void commit(unsigned bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// (names what was loaded, so that nothing that reads it is moved before the wait)
+#define KEEP32(v) "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), \
+    "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), \
+    "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), \
+    "+r"(v[30]), "+r"(v[31])
+__device__ __forceinline__ void loaded32(unsigned *v) { asm volatile("" : KEEP32(v)::"memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+#define REGS32(v) "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), \
+    "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), \
+    "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), \
+    "=r"(v[30]), "=r"(v[31])
+#define ARGS32(v) "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), \
+    "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), \
+    "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+
+// 32 columns of a warp's 32 lanes, a thread a lane
+__device__ __forceinline__ void get32(unsigned *v, unsigned at)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
+                 "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];" : REGS32(v) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void put32(unsigned at, const unsigned *v)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+                 "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::ARGS32(v), "r"(at) : "memory");
+}
+
+// bit k of word[k / 32]: row of node n sees key first + k
+__device__ __forceinline__ void seen(const AttendArgs &a, unsigned b, const Span &s, int n, unsigned first, const unsigned *bad,
+                                     unsigned shift, unsigned *word)
+{
+#pragma unroll
+    for (int w = 0; w < KT / 32; ++w) {
+        unsigned bits = 0;
+        for (int k = 0; k < 32; ++k) {
+            const unsigned r = w * 32 + k, box = r >> shift;
+            if (n >= 0 && !((bad[box >> 5] >> (box & 31u)) & 1u) && sees(a, b, s, n, first + r)) bits |= 1u << k;
+        }
+        word[w] = bits;
+    }
+}
+
+template <typename T, int DP, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1)
+k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row_tiles, unsigned max_teams, FastDiv by_group, unsigned shift,
+              int ovec)
+{
+    using C = Cfg<DP, PAIR>;
+    constexpr int ST = C::ST, M = C::M, TILE = C::TILE;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    unsigned char *qs = smem + ST * TILE;
+    Tail &tail = *reinterpret_cast<Tail *>(qs + C::QB);
+    volatile unsigned *dead = &tail.dead;
+    const unsigned t = threadIdx.x, lane = t & 31u, warp = t >> 5;
+    const unsigned cta = blockIdx.x, team = cta / row_tiles, rt = cta - team * row_tiles;
+    const unsigned group = by_group.d, row0 = rt * M, dim = a.c.dim, halves = (dim + 63) / 64;
+    const unsigned full = smem_u32(tail.full), empty = smem_u32(tail.empty), q_ready = smem_u32(&tail.q_ready);
+    const unsigned s_full = smem_u32(tail.s_full), p_ready = smem_u32(tail.p_ready), o_full = smem_u32(tail.o_full);
+
+    if (t == 0) {
+        for (int i = 0; i < ST; ++i) {
+            bar_init(full + 8 * i, 1);
+            bar_init(empty + 8 * i, 1);
+        }
+        bar_init(q_ready, kGroups * 4);
+        for (int i = 0; i < 2; ++i) {
+            bar_init(s_full + 8 * i, 1);
+            bar_init(p_ready + 8 * i, 4);
+            bar_init(o_full + 8 * i, 1);
+        }
+        bar_init(smem_u32(&tail.meet), kGroups * 4);
+        bar_init(smem_u32(&tail.last), 1);
+        tail.dead = 0;
+        tail.odd = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    pdl_wait();
+    pdl_release();
+    int *record = reinterpret_cast<int *>(a.work) + (size_t)cta * kRecord;
+    if (a.work && t == 0) record[3] = 0;
+    Walk<KT> w;
+    if (!w.template begin<kThreads>(a, team, max_teams, tail.scan)) return;
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tail.tmem)), "r"(kColumns) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const unsigned tmem = tail.tmem;
+    // scores of group g (p over them) at column 128 g, outputs at 256 + 128 g
+    unsigned base = 0;         // tiles asked for before this stretch: keys and values in turn
+    unsigned stretch = 0;      // stretches before this one
+
+    if (warp == 8) {           // the warp that asks for tiles
+        Loader<KT> load;
+        load.shift = shift;
+        unsigned asked = 0;
+        bool ok = true;
+        while (ok && w.next(a)) {
+            if (row0 >= (unsigned)w.s.count * group) continue;
+            load.look_up(a, w.b, w.s, w.tile0);
+            for (unsigned tile = w.tile0; ok && tile < w.tile1; ++tile) {
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    const unsigned slot = asked % ST, bar = full + 8 * slot;
+                    if (asked >= (unsigned)ST) ok = __all_sync(0xffffffffu, bar_wait(empty + 8 * slot, (asked / ST - 1) & 1, dead));
+                    if (!ok) break;
+                    load.judge(a, w.s, tile, tail.bad[slot], kv == 0 && rt == 0 && w.h == 0);
+                    __syncwarp();
+                    if (lane == 0) bar_expect(bar, halves * KT * 128);
+                    __syncwarp();
+                    if (kv == 0) load.request(&maps.k, maps.k_at, w.h, smem_u32(smem + slot * TILE), halves, 64, bar);
+                    else load.request(&maps.v, maps.v_at, w.h, smem_u32(smem + slot * TILE), halves, 64, bar);
+                    ++asked;
+                }
+                if (tile + 1 < w.tile1) load.look_up(a, w.b, w.s, tile + 1);
+            }
+        }
+        if (!ok) {             // given up: the copies under way must land before the CTA ends
+            for (unsigned i = asked > (unsigned)ST ? asked - ST : 0; i < asked; ++i) {
+                unsigned none = 0;
+                bar_wait(full + 8 * (i % ST), i / ST & 1, &none);
+            }
+        }
+    } else if (warp == 9) {    // the thread that issues the products
+        // chosen by elect.sync: under `lane == 0` the compiler does not know that one thread is left, and the operands'
+        // addresses, which the instruction takes from registers of the whole warp, came out wrong
+        unsigned one;
+        asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+        if (one) {
+            const unsigned ksteps = (dim + 15) / 16, q_at = smem_u32(qs);
+            unsigned ready[2] = {0, 0};   // phases of p_ready
+            bool ok = true;
+            auto keys_times = [&](unsigned i) {     // step i's scores
+                const unsigned g = i & 1, n = base + 2 * (PAIR ? i >> 1 : i), slot = n % ST;
+                if (!(ok = bar_wait(full + 8 * slot, n / ST & 1, dead))) return;
+                fence_after();
+                const unsigned qa = q_at + (PAIR ? g * TILE : 0), ka = smem_u32(smem + slot * TILE);
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+                    if (k < (int)ksteps)
+                        multiply(tmem + 128 * g, operand(qa + (k >> 2) * KT * 128 + (k & 3) * 32, 0),
+                                 operand(ka + (k >> 2) * KT * 128 + (k & 3) * 32, 0), product<T>(KT, false), k > 0);
+                commit(s_full + 8 * g);
+                if (!PAIR || g == 1) commit(empty + 8 * slot);
+            };
+            while (ok && w.next(a)) {
+                if (row0 >= (unsigned)w.s.count * group) continue;
+                const unsigned tiles = w.tile1 - w.tile0, steps = PAIR ? 2 * tiles : tiles;
+                if (!(ok = bar_wait(q_ready, stretch & 1, dead))) break;
+                fence_after();
+                keys_times(0);
+                if (ok && steps > 1) keys_times(1);
+                for (unsigned i = 0; ok && i < steps; ++i) {
+                    const unsigned g = i & 1, n = base + 2 * (PAIR ? i >> 1 : i) + 1, slot = n % ST;
+                    if (!(ok = bar_wait(p_ready + 8 * g, ready[g] & 1, dead))) break;
+                    ++ready[g];
+                    if (!(ok = bar_wait(full + 8 * slot, n / ST & 1, dead))) break;
+                    fence_after();
+                    const unsigned va = smem_u32(smem + slot * TILE);
+#pragma unroll
+                    for (int k = 0; k < KT / 16; ++k)   // 16 keys: two groups of 8 rows
+                        multiply_t(tmem + 256 + 128 * g, tmem + 128 * g + k * 8, operand(va + k * 2048, KT * 128), product<T>(DP, true),
+                                   i > 1 || k > 0);
+                    if (!PAIR || g == 1) commit(empty + 8 * slot);
+                    if (i + 2 < steps) keys_times(i + 2);
+                    else commit(o_full + 8 * g);
+                }
+                base += 2 * tiles;
+                ++stretch;
+            }
+            if (!ok) {         // given up: nothing may run on when tensor memory is freed
+                unsigned none = 0;
+                commit(smem_u32(&tail.last));
+                bar_wait(smem_u32(&tail.last), 0, &none);
+                if (a.c.status) atomicOr(a.c.status, PER_DEVFLAG_TIMEOUT);
+            }
+        }
+        __syncwarp();
+    } else {                   // the softmax: a thread a row
+        const unsigned g = warp >> 2, r = t & 127u, lanes = (warp & 3u) << 21;   // this warp's lanes of tensor memory
+        const unsigned my_s = tmem + 128 * g + lanes, my_o = tmem + 256 + 128 * g + lanes;
+        const unsigned my_row = row0 + (PAIR ? g * 128 : 0) + r;
+        const unsigned slot_floats = M * (dim + 2);
+        float *slots = a.work + (size_t)gridDim.x * kRecord + (size_t)cta * 2 * slot_floats;
+        unsigned phase = 0;    // steps of this group
+        unsigned outs = 0;     // phases of o_full
+        Meeting meet{smem_u32(&tail.meet), 0};
+        bool ok = true;
+        while (ok && w.next(a)) {
+            const Span &s = w.s;
+            const unsigned b = w.b, h = w.h, live = (unsigned)s.count * group;
+            if (w.tile0 == 0 && s.bad && rt == 0 && h == 0 && t == 0 && a.c.status) atomicOr(a.c.status, PER_DEVFLAG_BAD_INDEX);
+            if (w.tile0 == 0) absent_rows<T>(a, by_group, b, h, live, row0, M, t, kGroups * 128);
+            if (w.tile0 == 0 && w.tile1 < w.n_tiles && t == 0) w.note(record, team);
+            if (row0 >= live) continue;
+            {                  // the queries, zero where there is none
+                constexpr unsigned CH = DP / 8;
+                const T *q = static_cast<const T *>(a.q) + b * a.sq[0];
+                for (unsigned u = t; u < M * CH; u += kGroups * 128) {
+                    const unsigned x = u / CH, c = u % CH;
+                    const bool some = row0 + x < live;
+                    const unsigned node = by_group.div(row0 + x), head = h * group + row0 + x - node * group;
+                    const T *src = some ? q + node * a.sq[1] + head * a.sq[2] : q;
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (!a.qvec) v = entries<T>(src, c, dim, some);
+                    else if (some && c * 8 < dim) v = *reinterpret_cast<const uint4 *>(src + c * 8);
+                    *reinterpret_cast<uint4 *>(qs + (x >> 7) * TILE + piece(KT, x & 127u, c)) = v;
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) bar_arrive(q_ready);
+            }
+            const int node = my_row < live ? (int)by_group.div(my_row) : -1;
+            const unsigned tiles = w.tile1 - w.tile0;
+            float top = -INFINITY, l = 0.0f;      // what p refers to (in log2), and the sum of p
+            bool raw_none = true;                 // nothing seen yet
+            float ref = 0.0f;                     // top as a score
+            for (unsigned j = PAIR ? 0 : g; j < tiles; j += PAIR ? 1 : 2) {
+                const unsigned tile = w.tile0 + j, n = base + 2 * j + 1, slot = n % ST;
+                ok = __all_sync(0xffffffffu, bar_wait(s_full + 8 * g, phase & 1, dead) && bar_wait(full + 8 * slot, n / ST & 1, dead));
+                if (!ok) break;
+                ++phase;
+                fence_after();
+                unsigned v[KT];
+#pragma unroll
+                for (int i = 0; i < KT / 32; ++i) get32(v + 32 * i, my_s + 32 * i);
+                const bool tail_in = (tile + 1) * KT > (unsigned)s.len;   // nodes, or the end
+                if (tail_in && (!PAIR || g == 0)) {
+                    // what stale slots hold is taken out of the values, and what is not finite in a node's: it must
+                    // reach only the rows that see it
+                    bool odd = false;
+                    unsigned char *vs = smem + slot * TILE;
+                    for (unsigned u = r; u < KT * halves * 8; u += 128) {
+                        const unsigned x = u % KT, key = tile * KT + x;
+                        uint4 *at = reinterpret_cast<uint4 *>(vs + piece(KT, x, u / KT));
+                        if (key >= (unsigned)s.total) *at = make_uint4(0, 0, 0, 0);
+                        else if (key >= (unsigned)s.len) odd |= take_out<T>(at);
+                    }
+                    if (odd) tail.odd = 1;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                wait_ld();
+#pragma unroll
+                for (int i = 0; i < KT / 32; ++i) loaded32(v + 32 * i);
+                float *sc = reinterpret_cast<float *>(v);
+                unsigned wrong = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) wrong |= tail.bad[slot][e];
+                if (tail_in || wrong) {
+                    unsigned word[KT / 32];
+                    seen(a, b, s, node, tile * KT, tail.bad[slot], shift, word);
+#pragma unroll
+                    for (int k = 0; k < KT; ++k)
+                        if (!(word[k / 32] >> (k % 32) & 1u)) sc[k] = -INFINITY;
+                }
+                float up[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int k = 0; k < KT; ++k) up[k & 3] = fmaxf(up[k & 3], sc[k]);
+                const float most = fmaxf(fmaxf(up[0], up[1]), fmaxf(up[2], up[3]));
+                const bool rise = most > -INFINITY && (raw_none || (most - ref) * a.c2 > kRise);
+                if (__any_sync(0xffffffffu, rise)) {
+                    const float now = rise ? most * a.c2 : top;
+                    const float keep = rise ? (raw_none ? 0.0f : ex2(top - now)) : 1.0f;
+                    if (rise) {
+                        ref = most;
+                        top = now;
+                        raw_none = false;
+                    }
+                    l *= keep;
+                    if (j >= 2 || (PAIR && j >= 1)) {   // there are outputs
+#pragma unroll
+                        for (int i = 0; i < DP / 32; ++i) {
+                            unsigned x[32];
+                            get32(x, my_o + 32 * i);
+                            wait_ld();
+                            loaded32(x);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * keep);
+                            put32(my_o + 32 * i, x);
+                        }
+                    }
+                }
+                const float off = raw_none ? 0.0f : top;
+                float add[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int i = 0; i < KT / 64; ++i) {
+                    unsigned p[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const float x = ex2(fmaf(sc[64 * i + 2 * k], a.c2, -off)), y = ex2(fmaf(sc[64 * i + 2 * k + 1], a.c2, -off));
+                        add[(2 * k) & 3] += x;
+                        add[(2 * k + 1) & 3] += y;
+                        p[k] = pack2<T>(x, y);
+                    }
+                    put32(my_s + 32 * i, p);
+                }
+                l += (add[0] + add[1]) + (add[2] + add[3]);
+                wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(p_ready + 8 * g);
+            }
+            if (!ok) break;
+            const bool has = PAIR || g < tiles;
+            if (has) ok = __all_sync(0xffffffffu, bar_wait(o_full + 8 * g, outs & 1, dead));
+            if (!ok) break;
+            if (has) ++outs;
+            tail.ml[g][r][0] = raw_none ? -INFINITY : top;
+            tail.ml[g][r][1] = l;
+            if (!(ok = meet(dead))) break;
+            fence_after();
+            const bool odd = *(volatile unsigned *)&tail.odd != 0;
+
+            // a group's rows, or (of rows that both have) half of the entries
+            const RowOut<T> out{a, by_group, b, h, live, row0, (unsigned)M, w.part(), slots + (w.tile0 != 0 ? 0 : slot_floats)};
+            const unsigned row_in = (PAIR ? g * 128 : 0) + r;
+            float f0 = 1.0f, f1 = 0.0f, m = tail.ml[g][r][0], sum = l;
+            const bool both = !PAIR && tiles > 1;
+            if (both) {
+                const float m0 = tail.ml[0][r][0], m1 = tail.ml[1][r][0];
+                m = fmaxf(m0, m1);
+                const float mb = m == -INFINITY ? 0.0f : m;
+                f0 = ex2(m0 - mb);
+                f1 = ex2(m1 - mb);
+                sum = tail.ml[0][r][1] * f0 + tail.ml[1][r][1] * f1;
+            } else if (!PAIR) {
+                m = tail.ml[0][r][0];
+                sum = tail.ml[0][r][1];
+            }
+            const unsigned o_at = PAIR ? my_o : tmem + 256 + lanes;
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const bool real = my_row < live;
+            const unsigned n_at = by_group.div(my_row), head_at = h * group + my_row - n_at * group;
+            T *to = static_cast<T *>(a.out) + b * a.so[0] + n_at * a.so[1] + head_at * a.so[2];
+            constexpr int HALF = DP / 32 / (PAIR ? 1 : 2);                // blocks of 32 entries a thread takes
+#pragma unroll 1
+            for (int i = 0; i < HALF; ++i) {
+                const int c = (PAIR ? 0 : g * HALF) + i;
+                unsigned x[32];
+                get32(x, o_at + 32 * c);
+                if (both) {
+                    unsigned y[32];
+                    get32(y, o_at + 128 + 32 * c);
+                    wait_ld();
+                    loaded32(x);
+                    loaded32(y);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f0 + __uint_as_float(y[k]) * f1);
+                } else {
+                    wait_ld();
+                    loaded32(x);
+                }
+                float *o = reinterpret_cast<float *>(x);
+                if (odd && real) {   // what was taken out of the values, for the rows that see it (rare: nothing here is fast)
+                    const unsigned first = max(w.tile0 * KT, (unsigned)s.len), end = min(w.tile1 * KT, (unsigned)s.total);
+                    for (unsigned key = first; key < end; ++key) {
+                        const unsigned pg = a.c.page.div(key);
+                        const int e = a.c.table[b * a.c.st + pg];
+                        if ((unsigned)e >= a.c.pages || !sees(a, b, s, node, key)) continue;
+                        const T *src = static_cast<const T *>(a.c.v) + e * a.c.sv[0] + (key - pg * a.c.page.d) * a.c.sv[1] + h * a.c.sv[2];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            const float z = c * 32 + k < (int)dim ? to_f32(src[c * 32 + k]) : 0.0f;
+                            if (!finite(z)) o[k] += z;
+                        }
+                    }
+                }
+                if (real && ovec && !out.part) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (c * 32 + k * 8 < (int)dim) {
+                            uint4 z;
+                            z.x = pack2<T>(o[8 * k] * inv, o[8 * k + 1] * inv);
+                            z.y = pack2<T>(o[8 * k + 2] * inv, o[8 * k + 3] * inv);
+                            z.z = pack2<T>(o[8 * k + 4] * inv, o[8 * k + 5] * inv);
+                            z.w = pack2<T>(o[8 * k + 6] * inv, o[8 * k + 7] * inv);
+                            *reinterpret_cast<uint4 *>(to + c * 32 + k * 8) = z;
+                        }
+                    if (c == 0 && a.lse) a.lse[((size_t)b * a.nodes + n_at) * a.q_heads + head_at] = lse_of(m, sum);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) out.put(row_in, c * 32 + 2 * k, o[2 * k], o[2 * k + 1], m, sum);
+                }
+            }
+            fence_before();
+            if (!(ok = meet(dead))) break;   // outputs, sums and the flag are read
+            if (t == 0) tail.odd = 0;
+            base += 2 * tiles;
+        }
+    }
+    fence_before();
+    __syncthreads();             // nobody leaves before copies and products are done
+    if (warp == 9) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kColumns));
+    }
+}
+
+template <typename T, int DP, bool PAIR>
+cudaError_t wide(AttendArgs a, int type, const DeviceInfo &dev, cudaStream_t st, u64 *bytes, bool *taken)
+{
+    using C = Cfg<DP, PAIR>;
+    const Plan p = plan_of(a, C::M, KT, (unsigned)dev.sms);
+    if (bytes) {
+        *bytes = std::max(*bytes, p.bytes);
+        return cudaSuccess;
+    }
+    CacheMaps maps;
+    unsigned shift;
+    *taken = make_maps(type, a, KT, &maps, &shift);
+    if (!*taken) return cudaSuccess;
+    static std::atomic<bool> done[64];   // (two threads may both set the attribute, to the same value)
+    if (!done[dev.device].load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(k_attend_wide<T, DP, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (e != cudaSuccess) return e;
+        done[dev.device].store(true, std::memory_order_release);
+    }
+    if (!p.parts) a.work = nullptr;
+    FastDiv by_group;
+    by_group.set(a.q_heads / a.c.heads);
+    const bool ovec = a.c.dim % 8 == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.so[0] % 8 == 0 && a.so[1] % 8 == 0 && a.so[2] % 8 == 0;
+    const cudaError_t e = launch_clusters(k_attend_wide<T, DP, PAIR>, p.grid, kThreads, 1, C::SMEM, st, maps, a, p.row_tiles, p.teams,
+                                          by_group, shift, (int)ovec);
+    return e != cudaSuccess || !p.parts ? e : join_parts(type, a, p, by_group, st);
+}
+
+template <typename T>
+cudaError_t wide_t(const AttendArgs &a, int type, const DeviceInfo &dev, cudaStream_t st, u64 *bytes, bool *taken)
+{
+    const bool pair = a.nodes * (a.q_heads / a.c.heads) > 128;
+    if (a.c.dim <= 64)
+        return pair ? wide<T, 64, true>(a, type, dev, st, bytes, taken) : wide<T, 64, false>(a, type, dev, st, bytes, taken);
+    return pair ? wide<T, 128, true>(a, type, dev, st, bytes, taken) : wide<T, 128, false>(a, type, dev, st, bytes, taken);
+}
+
+}  // namespace
+
+cudaError_t attend_wide(int type, const AttendArgs &a, const DeviceInfo &dev, cudaStream_t st, u64 *bytes, bool *taken)
+{
+    if (type == PER_TYPE_F16) return wide_t<__half>(a, type, dev, st, bytes, taken);
+    return wide_t<__nv_bfloat16>(a, type, dev, st, bytes, taken);
+}
+
+}  // namespace attend
+}  // namespace gbper

@@ -1,0 +1,157 @@
+"""Attention over a paged cache where a head of keys has many rows: the kernel on the tensor cores' own
+instruction, and the one with few rows at its borders."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+from rl_infra_gb300 import build, capi, ops  # noqa: E402
+from tests import cache_oracle as co  # noqa: E402
+from tests.test_cache_gpu import INF, NAN, TYPES, attend_case, cache, check_attend, fill, host, i32, rand, tree  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build()
+    capi.load()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("n, g", [(33, 1), (8, 8), (64, 2), (43, 3), (64, 3), (32, 8), (129, 2), (64, 8), (20, 25)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens", [[0, 100], [127, 300], [1]])
+def test_rows(kind, n, g, d, lens):
+    """Every number of row tiles and of key tiles in a part, odd and even."""
+    attend_case(31, kind, len(lens), n, 1, g, d, 16, lens, masks="tree")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("d", [8, 40, 72, 80, 104, 120, 192, 33])
+@pytest.mark.parametrize("n, page", [(35, 64), (70, 24)])
+def test_odd_heads(kind, d, n, page):
+    attend_case(32, kind, 2, n, 2, 2, d, page, [200, 33], masks="each")
+
+
+@pytest.mark.parametrize("page", [1, 2, 5, 12, 48, 128, 256, 300])
+@pytest.mark.parametrize("n, g", [(5, 2), (40, 1), (100, 2)])
+def test_pages(page, n, g):
+    attend_case(33, "bf16", 2, n, 2, g, 128, page, [340, 129], masks="tree")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("n, g", [(40, 1), (40, 6)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_long_sequence(kind, n, g, d):
+    attend_case(34, kind, 1, n, 1, g, d, 64, [20000], masks="tree")
+
+
+@pytest.mark.parametrize("n, g", [(40, 1), (40, 5)])
+def test_ragged(n, g):
+    r = np.random.default_rng(35)
+    lens, counts = r.integers(0, 700, 21), r.integers(0, n + 1, 21)
+    lens[3], counts[3], counts[4], lens[5], counts[6] = 0, 0, 0, 0, 1
+    attend_case(35, "bf16", 21, n, 2, g, 64, 16, lens, counts, "each")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("scale", [3.0, 0.0, -1.0])
+def test_maxima_that_rise(kind, scale):
+    """Scores that grow along the sequence, so that each tile raises the maximum; and scales that are not positive."""
+    r = np.random.default_rng(36)
+    kc, vc, table = cache(r, 1, 700, 16, 1, 64, kind)
+    fill(r, kc, vc, table, [700], kind)
+    tab = table.cpu().numpy()
+    for s in range(700):
+        p, x = co.place(tab[0], s, 16, kc.shape[0])
+        kc[p, x] *= 0.002 * s
+    q = rand(r, 1, 50, 4, 64, kind=kind)
+    got = ops.tree_attention(q, kc, vc, table, i32([650]), scale=scale)
+    check_attend(got, co.attend(host(q), host(kc), host(vc), tab, [650], scale=scale, kind=kind), kind)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("d, n, g", [(64, 40, 1), (128, 20, 3), (128, 100, 2), (64, 60, 5), (128, 20, 2), (256, 40, 1)])
+def test_masked_places_take_no_part(kind, d, n, g):
+    r = np.random.default_rng(37)
+    lens = [200, 0, 126]
+    kc, vc, table = cache(r, 3, 320, 16, 1, d, kind)
+    fill(r, kc, vc, table, [x + n for x in lens], kind)
+    mask = np.stack([tree(r, n) for _ in range(3)])
+    mask[:, :, 2] = False                      # nobody sees node 2
+    mask[1, 4] = False                         # this row of the sequence without context sees nothing
+    mask[:, :, 5] &= np.arange(n)[None] % 2 == 1
+    tab = table.cpu().numpy()
+    low = torch.finfo(TYPES[kind]).min
+    for i, ln in enumerate(lens):
+        p, s = co.place(tab[i], ln + 2, 16, kc.shape[0])
+        kc[p, s], vc[p, s] = torch.tensor([NAN, INF, -INF, low] * (d // 4), device="cuda"), NAN
+        vc[p, s, :, 1::2] = INF
+        p, s = co.place(tab[i], ln + 5, 16, kc.shape[0])
+        vc[p, s, :, 3], vc[p, s, :, 4], vc[p, s, :, 5] = INF, NAN, low / 4
+    q = rand(r, 3, n, g, d, kind=kind)
+    got = ops.tree_attention(q, kc, vc, table, i32(lens), mask=torch.from_numpy(mask).cuda())
+    want = co.attend(host(q), host(kc), host(vc), tab, lens, mask, kind=kind)
+    assert np.isnan(want["out"]).any() and np.isinf(want["out"]).any() and np.isinf(want["lse"]).any()
+    check_attend(got, want, kind)
+    # what is not finite was one call's: the next one, without it, has none
+    for i, ln in enumerate(lens):
+        p, s = co.place(tab[i], ln + 5, 16, kc.shape[0])
+        vc[p, s] = 1.0
+    assert torch.isfinite(ops.tree_attention(q, kc, vc, table, i32(lens), mask=torch.from_numpy(mask).cuda())["out"]).all()
+
+
+@pytest.mark.parametrize("n, g", [(40, 1), (40, 6), (6, 2)])
+def test_bad_pages(n, g):
+    r = np.random.default_rng(38)
+    kc, vc, table = cache(r, 2, 400, 16, 1, 64, "bf16")
+    fill(r, kc, vc, table, [400, 400], "bf16")
+    table[0, 1], table[0, 9], table[1, 0], table[1, 20] = -1, 1 << 30, -(1 << 31), kc.shape[0]
+    q = rand(r, 2, n, g, 64, kind="bf16")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = ops.tree_attention(q, kc, vc, table, i32([330, 300]), status=status)
+    check_attend(got, co.attend(host(q), host(kc), host(vc), table.cpu().numpy(), [330, 300], kind="bf16"), "bf16")
+    assert status.item() == capi.PER_DEVFLAG_BAD_INDEX
+
+
+def test_layouts_and_outputs():
+    """Heads before slots; a cache that is part of a larger one; outputs and queries with gaps; nothing beside the
+    rows is written."""
+    r = np.random.default_rng(39)
+    b, n, hkv, g, d, page = 2, 40, 2, 3, 64, 16
+    kc, vc, table = cache(r, b, 400, page, hkv, d, "bf16")
+    fill(r, kc, vc, table, [390, 200], "bf16")
+    q = rand(r, b, n, hkv * g, d, kind="bf16")
+    lens = i32([350, 160])
+    want = ops.tree_attention(q, kc, vc, table, lens)
+    k2 = kc.transpose(1, 2).contiguous().transpose(1, 2)                       # [pages, heads, slots, D]
+    both = torch.stack([kc, vc], 1).contiguous()                               # [pages, 2, slots, heads, D]
+    wide = torch.nn.functional.pad(q, (0, 24))[..., :d]
+    store = torch.full((b, n, hkv * g, d + 8), 3.0, dtype=torch.bfloat16, device="cuda")
+    odd = torch.full((b, n, hkv * g, d + 1), 3.0, dtype=torch.bfloat16, device="cuda")
+    for kk, vv, qq, out in ((k2, vc, q, None), (both[:, 0], both[:, 1], wide, store[..., :d]), (kc, vc, q, odd[..., :d])):
+        got = ops.tree_attention(qq, kk, vv, table, lens, out=None if out is None else {"out": out})
+        assert torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"])
+    assert (store[..., d:] == 3).all() and (odd[..., d:] == 3).all()
+
+
+def test_many_calls_at_once():
+    """Calls of every kernel under way on two streams give what they give alone."""
+    r = np.random.default_rng(40)
+    kc, vc, table = cache(r, 6, 900, 16, 2, 128, "bf16")
+    fill(r, kc, vc, table, [900] * 6, "bf16")
+    lens = i32([850, 100, 0, 613, 127, 128])
+    qs = [rand(r, 6, n, 2 * g, 128, kind="bf16") for n, g in ((1, 4), (8, 4), (40, 1), (40, 4))]
+    want = [ops.tree_attention(q, kc, vc, table, lens) for q in qs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[ops.tree_attention(q, kc, vc, table, lens, stream=s) for q in qs] for _ in range(10) for s in streams]
+    torch.cuda.synchronize()
+    for row in got:
+        for x, y in zip(row, want):
+            assert torch.equal(x["out"], y["out"]) and torch.equal(x["lse"], y["lse"])
