@@ -4,7 +4,9 @@
 // The cut.  All tiles of all sequences and heads of keys lie in a row, which is cut into equal parts, one for
 // each CTA that the GPU holds at once (a team of CTAs, where the rows of a head of keys need several).  A part that
 // begins or ends inside a sequence leaves its sums in scratch memory, and a second kernel joins them in their
-// order.  So one long sequence fills the GPU, and ragged ones leave no SM idle.
+// order.  So one long sequence fills the GPU, and ragged ones leave no SM idle.  Each sequence and head counts
+// kBegin tiles more than it has, for its queries, its nodes and its output: without them short sequences that lie
+// side by side became one CTA's (16 trees of which one has no context: 257 us, 126 without that one).
 #pragma once
 
 #include <cuda.h>
@@ -17,6 +19,7 @@ namespace attend {
 typedef unsigned long long u64;
 constexpr int kRecord = 8;             // ints of a CTA's record for the joining kernel
 constexpr unsigned kWaitMs = 2000;     // limit of a wait
+constexpr unsigned kBegin = 2;         // tiles that a sequence's begin and end are worth
 
 // ---- how the work is cut -----------------------------------------------------------------------
 struct Span {              // a sequence
@@ -48,7 +51,7 @@ __device__ __forceinline__ u64 part_start(u64 t, u64 all, unsigned teams) { retu
 // A team's stretches, one sequence and head after another.
 template <int KT>
 struct Walk {
-    u64 pos, end, at, all;   // at: the sequence's first tile
+    u64 pos, end, at, all;   // in tiles, kBegin before each sequence's and head's; at: where the sequence begins
     unsigned teams, b, n_tiles, h, tile0, tile1;
     Span s;
 
@@ -60,7 +63,7 @@ struct Walk {
         const unsigned per = (a.batch + NT - 1) / NT;
         const unsigned b0 = min(t * per, a.batch), b1 = min(b0 + per, a.batch);
         u64 mine = 0;
-        for (unsigned i = b0; i < b1; ++i) mine += tiles_of<KT>(span(a, i));
+        for (unsigned i = b0; i < b1; ++i) mine += tiles_of<KT>(span(a, i)) + kBegin;
         u64 upto = mine;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
@@ -87,7 +90,7 @@ struct Walk {
             unsigned i = b0;
             u64 x = before;
             for (;; ++i) {
-                const u64 n = (u64)tiles_of<KT>(span(a, i)) * a.c.heads;
+                const u64 n = (u64)(tiles_of<KT>(span(a, i)) + kBegin) * a.c.heads;
                 if (pos < x + n) break;
                 x += n;
             }
@@ -104,17 +107,21 @@ struct Walk {
 
     __device__ __forceinline__ bool next(const AttendArgs &a)
     {
-        if (pos >= end) return false;
-        if (pos >= at + (u64)n_tiles * a.c.heads) {
-            at += (u64)n_tiles * a.c.heads;
-            ++b;
-            s = span(a, b);
-            n_tiles = tiles_of<KT>(s);
-        }
-        h = (unsigned)((pos - at) / n_tiles);
-        tile0 = (unsigned)(pos - at - (u64)h * n_tiles);
-        tile1 = (unsigned)min((u64)n_tiles, tile0 + (end - pos));
-        pos += tile1 - tile0;
+        do {
+            if (pos >= end) return false;
+            if (pos >= at + (u64)(n_tiles + kBegin) * a.c.heads) {
+                at += (u64)(n_tiles + kBegin) * a.c.heads;
+                ++b;
+                s = span(a, b);
+                n_tiles = tiles_of<KT>(s);
+            }
+            const unsigned size = n_tiles + kBegin;
+            h = (unsigned)((pos - at) / size);
+            const unsigned x0 = (unsigned)(pos - at - (u64)h * size), x1 = (unsigned)min((u64)size, x0 + (end - pos));
+            tile0 = x0 > kBegin ? x0 - kBegin : 0;
+            tile1 = x1 > kBegin ? x1 - kBegin : 0;
+            pos += x1 - x0;
+        } while (tile0 == tile1);
         return true;
     }
 
@@ -123,7 +130,7 @@ struct Walk {
     // the record of a CTA that begins what others end
     __device__ __forceinline__ void note(int *record, unsigned team) const
     {
-        const u64 last = at + (u64)(h + 1) * n_tiles - 1;      // the tile that ends it
+        const u64 last = at + (u64)(h + 1) * (n_tiles + kBegin) - 1;   // the tile that ends it
         const unsigned last_team = (unsigned)(((last + 1) * teams + all - 1) / all) - 1;
         record[0] = (int)b;
         record[1] = (int)h;
@@ -351,7 +358,7 @@ inline Plan plan_of(const AttendArgs &a, unsigned m, unsigned kt, unsigned ctas)
     p.row_tiles = (unsigned)((rows + m - 1) / m);
     p.teams = ctas > p.row_tiles ? ctas / p.row_tiles : 1;
     const u64 most = ((u64)a.c.width * a.c.page.d + kt - 1) / kt;   // tiles of a sequence
-    const u64 tiles = (most ? most : 1) * a.batch * a.c.heads;
+    const u64 tiles = ((most ? most : 1) + kBegin) * a.batch * a.c.heads;
     if (p.teams > tiles) p.teams = (unsigned)tiles;
     p.grid = p.teams * p.row_tiles;
     p.parts = most > 1 && p.teams > 1;

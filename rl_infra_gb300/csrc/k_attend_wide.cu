@@ -107,18 +107,31 @@ __device__ __forceinline__ void put32(unsigned at, const unsigned *v)
                  "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::ARGS32(v), "r"(at) : "memory");
 }
 
-// bit k of word[k / 32]: row of node n sees key first + k
+// bit k of word[k / 32]: the row of node n sees key first + k
 __device__ __forceinline__ void seen(const AttendArgs &a, unsigned b, const Span &s, int n, unsigned first, const unsigned *bad,
-                                     unsigned shift, unsigned *word)
+                                     bool wrong, unsigned shift, unsigned *word)
 {
+    const int end = a.mask || n < 0 ? s.count : min(s.count, n + 1);   // nodes from 0 to here
+    const uint8_t *mask = a.mask ? a.mask + b * a.sm[0] + (long long)max(n, 0) * a.sm[1] : nullptr;
 #pragma unroll
     for (int w = 0; w < KT / 32; ++w) {
-        unsigned bits = 0;
-        for (int k = 0; k < 32; ++k) {
-            const unsigned r = w * 32 + k, box = r >> shift;
-            if (n >= 0 && !((bad[box >> 5] >> (box & 31u)) & 1u) && sees(a, b, s, n, first + r)) bits |= 1u << k;
+        const int j0 = (int)(first + 32 * w) - s.len;                  // the node at the word's first bit; < 0: context
+        const int below = min(max(-j0, 0), 32), upto = min(max(end - j0, 0), 32);
+        unsigned bits = upto == 32 ? ~0u : (1u << upto) - 1;           // context and nodes up to `end`
+        const unsigned context = below == 32 ? ~0u : (1u << below) - 1;
+        if (mask && (bits & ~context)) {
+            unsigned see = 0;
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+                if ((bits & ~context) >> k & 1u) see |= mask[j0 + k] != 0 ? 1u << k : 0u;
+            bits &= context | see;
         }
-        word[w] = bits;
+        if (wrong)
+            for (int k = 0; k < 32; ++k) {
+                const unsigned box = (w * 32 + k) >> shift;
+                if ((bad[box >> 5] >> (box & 31u)) & 1u) bits &= ~(1u << k);
+            }
+        word[w] = n < 0 ? 0 : bits;
     }
 }
 
@@ -333,7 +346,7 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                 for (int e = 0; e < 4; ++e) wrong |= tail.bad[slot][e];
                 if (tail_in || wrong) {
                     unsigned word[KT / 32];
-                    seen(a, b, s, node, tile * KT, tail.bad[slot], shift, word);
+                    seen(a, b, s, node, tile * KT, tail.bad[slot], wrong != 0, shift, word);
 #pragma unroll
                     for (int k = 0; k < KT; ++k)
                         if (!(word[k / 32] >> (k % 32) & 1u)) sc[k] = -INFINITY;

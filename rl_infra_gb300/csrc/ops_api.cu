@@ -212,8 +212,8 @@ const char *attend_fault(const per_attend_shape *sh)
     if (sh->nodes > 1024) return "nodes must be at most 1024";
     if (sh->q_heads == 0 || sh->q_heads % sh->cache.heads || sh->q_heads / sh->cache.heads > 64)
         return "q_heads must be 1 .. 64 times heads";
-    // tiles of 32 keys, of which no sequence has fewer than one
-    if (((uint64_t)sh->cache.width * sh->cache.page / 32 + 1) * sh->batch * sh->cache.heads >> 45)
+    // tiles of 32 keys, and what each sequence counts beside them
+    if (((uint64_t)sh->cache.width * sh->cache.page / 32 + 3) * sh->batch * sh->cache.heads >> 45)
         return "batch x width x page x heads must be below 2^50";
     if (!std::isfinite(sh->scale) || !std::isfinite(sh->scale * 1.5f)) return "scale must be finite";
     return nullptr;
