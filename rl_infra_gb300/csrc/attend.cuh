@@ -45,14 +45,18 @@ __device__ __forceinline__ unsigned tiles_of(const Span &s)
     return s.count == 0 ? 1u : max(1u, ((unsigned)s.total + KT - 1) / KT);   // a sequence without nodes has zeros to write
 }
 
-// (all < 2^45, checked on the host)
-__device__ __forceinline__ u64 part_start(u64 t, u64 all, unsigned teams) { return t * all / teams; }
+// x / y by 32 bits where they are enough (a division of 64 bits takes some hundred cycles)
+__device__ __forceinline__ u64 divide(u64 x, u64 y)
+{
+    return (x | y) >> 32 ? x / y : (u64)((unsigned)x / (unsigned)y);
+}
 
 // A team's stretches, one sequence and head after another.
 template <int KT>
 struct Walk {
-    u64 pos, end, at, all;   // in tiles, kBegin before each sequence's and head's; at: where the sequence begins
-    unsigned teams, b, n_tiles, h, tile0, tile1;
+    u64 pos, end, at;        // in tiles, kBegin before each sequence's and head's; at: where the sequence begins
+    u64 size, more;          // tiles of a team; the first `more` teams have one more
+    unsigned b, n_tiles, h, tile0, tile1;
     Span s;
 
     // All NT threads of the CTA; `scan` holds NT / 32 words.  False: the team has nothing to do.
@@ -72,8 +76,7 @@ struct Walk {
         }
         if (lane == 31) scan[warp] = upto;
         __syncthreads();
-        u64 before = upto - mine;
-        all = 0;
+        u64 before = upto - mine, all = 0;
 #pragma unroll
         for (int w = 0; w < NT / 32; ++w) {
             if (w < (int)warp) before += scan[w];
@@ -81,9 +84,10 @@ struct Walk {
         }
         all *= a.c.heads;
         before *= a.c.heads;                                   // tiles in front of this thread's sequences
-        teams = (unsigned)min((u64)max_teams, all);            // every team has a tile
-        pos = team < teams ? part_start(team, all, teams) : all;
-        end = team < teams ? part_start(team + 1, all, teams) : all;
+        size = divide(all, max_teams);
+        more = all - size * max_teams;
+        pos = team * size + min((u64)team, more);
+        end = pos + size + (team < more);
         if (pos >= end) return false;
         __syncthreads();
         if (pos >= before && pos < before + mine * a.c.heads) {   // one thread's
@@ -115,9 +119,9 @@ struct Walk {
                 s = span(a, b);
                 n_tiles = tiles_of<KT>(s);
             }
-            const unsigned size = n_tiles + kBegin;
-            h = (unsigned)((pos - at) / size);
-            const unsigned x0 = (unsigned)(pos - at - (u64)h * size), x1 = (unsigned)min((u64)size, x0 + (end - pos));
+            const unsigned whole = n_tiles + kBegin;
+            h = (unsigned)divide(pos - at, whole);
+            const unsigned x0 = (unsigned)(pos - at - (u64)h * whole), x1 = (unsigned)min((u64)whole, x0 + (end - pos));
             tile0 = x0 > kBegin ? x0 - kBegin : 0;
             tile1 = x1 > kBegin ? x1 - kBegin : 0;
             pos += x1 - x0;
@@ -131,11 +135,12 @@ struct Walk {
     __device__ __forceinline__ void note(int *record, unsigned team) const
     {
         const u64 last = at + (u64)(h + 1) * (n_tiles + kBegin) - 1;   // the tile that ends it
-        const unsigned last_team = (unsigned)(((last + 1) * teams + all - 1) / all) - 1;
+        const u64 border = more * (size + 1);
+        const u64 last_team = last < border ? divide(last, size + 1) : more + divide(last - border, size);
         record[0] = (int)b;
         record[1] = (int)h;
         record[2] = s.count;
-        record[3] = (int)(last_team - team + 1);               // parts
+        record[3] = (int)((unsigned)last_team - team + 1);     // parts
     }
 };
 
@@ -189,15 +194,21 @@ struct RowOut {
     bool part;
     float *slot;
 
-    // entries d and d + 1 of row r of the tile, its maximum and sum
-    __device__ __forceinline__ void put(unsigned r, unsigned d, float x, float y, float top, float sum) const
+    // entries d to d + 7 (d a multiple of 8) of row r of the tile, its maximum and sum
+    __device__ __forceinline__ void put8(unsigned r, unsigned d, const float *x, float top, float sum) const
     {
         const unsigned dim = a.c.dim;
-        if (row0 + r >= live) return;
+        if (row0 + r >= live || d >= dim) return;
         if (part) {
             float *to = slot + r * dim + d;
-            if (d < dim) to[0] = x;
-            if (d + 1 < dim) to[1] = y;
+            if (dim % 8 == 0) {
+                *reinterpret_cast<float4 *>(to) = make_float4(x[0], x[1], x[2], x[3]);
+                *reinterpret_cast<float4 *>(to + 4) = make_float4(x[4], x[5], x[6], x[7]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (d + e < dim) to[e] = x[e];
+            }
             if (d == 0) {
                 slot[m * dim + 2 * r] = top;
                 slot[m * dim + 2 * r + 1] = sum;
@@ -207,15 +218,31 @@ struct RowOut {
         const unsigned n = by_group.div(row0 + r), head = h * by_group.d + row0 + r - n * by_group.d;
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         T *to = static_cast<T *>(a.out) + b * a.so[0] + n * a.so[1] + head * a.so[2] + d;
-        if (sizeof(T) == 2 && a.opair) {
-            if (d < dim) *reinterpret_cast<unsigned *>(to) = pack2<T>(x * inv, y * inv);
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = x[e] * inv;
+        if (a.ovec) {
+#pragma unroll
+            for (int e = 0; e < 8; e += Pack<T>::N) {
+                Pack<T> p;
+                p.pack(y + e);
+                *reinterpret_cast<uint4 *>(to + e) = p.raw;
+            }
         } else {
-            if (d < dim) to[0] = from_f32<T>(x * inv);
-            if (d + 1 < dim) to[1] = from_f32<T>(y * inv);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (d + e < dim) to[e] = from_f32<T>(y[e]);
         }
         if (d == 0 && a.lse) a.lse[((size_t)b * a.nodes + n) * a.q_heads + head] = lse_of(top, sum);
     }
 };
+
+// A row's entries in binary32 on their way out: eights of columns c of row r in shared memory, pieces of 16 bytes turned
+// by the row so that a fragment's rows lie in different banks.
+__device__ __forceinline__ unsigned out_at(unsigned width, unsigned r, unsigned col)
+{
+    return r * width + ((((col >> 2) ^ (r & 7u)) << 2) | (col & 3u));
+}
 
 // ---- barriers and copies -------------------------------------------------------------------------
 __device__ __forceinline__ unsigned smem_u32(const void *p) { return (unsigned)__cvta_generic_to_shared(p); }

@@ -46,7 +46,7 @@ struct Tail {
     u64 full[6], empty[6], meet;
     u64 scan[kThreads / 32];
     unsigned bad[6][4];
-    float ml[2][16][2];        // maxima and sums that the warps hand over
+    float ml[64][2];           // maxima and sums that the warps hand over
     unsigned dead, odd;        // odd: the number of the last tile that something was taken out of
 };
 static_assert(sizeof(Tail) <= 1024, "");
@@ -133,8 +133,10 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
             if (w.tile0 == 0 && s.bad && rt == 0 && h == 0 && t == 0 && a.c.status) atomicOr(a.c.status, PER_DEVFLAG_BAD_INDEX);
             const unsigned live = (unsigned)s.count * group;         // rows of nodes that are there
             if (w.tile0 == 0) absent_rows<T>(a, by_group, b, h, live, row0, M, t, kWarps * 32);
-            if (w.tile0 == 0 && w.tile1 < w.n_tiles && t == 0) w.note(record, team);
-            if (row0 >= live) continue;
+            if (row0 >= live) {
+                if (w.tile0 == 0 && w.tile1 < w.n_tiles && t == 0) w.note(record, team);
+                continue;
+            }
 
             // the queries, zero where there is none
             if (!(ok = meet(dead))) break;
@@ -231,27 +233,35 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                 sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
             }
 
-            // the warps that share rows join, two by two: the upper ones hand their sums to the lower ones
+            // the warps that share rows join: the upper two hand their sums to the lower two; what is left lies in one
+            // or two areas of [row][entry], and all warps write it out
+            constexpr int AREAS = WK == 4 ? 2 : 1;
+            constexpr int WIDE = WK == 1 && ES == 2 ? DP / 2 : DP;        // entries that an area holds at once
+            float *sums = reinterpret_cast<float *>(area);
+            if (!(ok = meet(dead))) break;                              // the queries are done with
+            if (w.tile0 == 0 && w.tile1 < w.n_tiles && t == 0) w.note(record, team);
             if constexpr (WK > 1) {
-                auto hand = [&](unsigned i) {
-                    float *to = reinterpret_cast<float *>(area) + i * 16 * DP;
+                const unsigned i = WK == 4 ? wk & 1u : wr;              // the area that a pair shares
+                if (wk >= WK / 2) {
+                    float *to = sums + i * 16 * DP;
 #pragma unroll
                     for (int k = 0; k < DP / 8; ++k)
                         *reinterpret_cast<float4 *>(to + (k * 32 + lane) * 4) = make_float4(o[k][0], o[k][1], o[k][2], o[k][3]);
                     if (q4 == 0) {
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            tail.ml[i][g + e * 8][0] = top[e];
-                            tail.ml[i][g + e * 8][1] = sum[e];
+                            tail.ml[i * 16 + g + e * 8][0] = top[e];
+                            tail.ml[i * 16 + g + e * 8][1] = sum[e];
                         }
                     }
-                };
-                auto take = [&](unsigned i) {
-                    const float *from = reinterpret_cast<const float *>(area) + i * 16 * DP;
+                }
+                if (!(ok = meet(dead))) break;
+                if (wk < WK / 2) {
+                    const float *from = sums + i * 16 * DP;
                     float mine[2], other[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float m = tail.ml[i][g + e * 8][0], l = tail.ml[i][g + e * 8][1];
+                        const float m = tail.ml[i * 16 + g + e * 8][0], l = tail.ml[i * 16 + g + e * 8][1];
                         const float up = fmaxf(top[e], m), base = up == -INFINITY ? 0.0f : up;
                         mine[e] = ex2(top[e] - base);
                         other[e] = ex2(m - base);
@@ -266,25 +276,54 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                         o[k][2] = o[k][2] * mine[1] + x.z * other[1];
                         o[k][3] = o[k][3] * mine[1] + x.w * other[1];
                     }
-                };
-                if (!(ok = meet(dead))) break;                       // the queries are done with
-                if constexpr (WK == 4) {
-                    if (wk >= 2) hand(wk - 2);
-                    if (!(ok = meet(dead))) break;
-                    if (wk < 2) take(wk);
-                    if (!(ok = meet(dead))) break;
+                    __syncwarp();
                 }
-                if (wk == 1) hand(wr);
-                if (!(ok = meet(dead))) break;
-                if (wk == 0) take(wr);
             }
-            if (wk == 0) {
-                const RowOut<T> out{a, by_group, b, h, live, row0, M, w.part(), slots + (w.tile0 != 0 ? 0 : slot_floats)};
+            const RowOut<T> out{a, by_group, b, h, live, row0, M, w.part(), slots + (w.tile0 != 0 ? 0 : slot_floats)};
 #pragma unroll
-                for (int i = 0; i < DP / 8; ++i)
+            for (int d0 = 0; d0 < DP; d0 += WIDE) {
+                if (d0 > 0 && !(ok = meet(dead))) break;
+                if (wk < WK / 2 || WK == 1) {
+                    const unsigned i = WK == 4 ? wk * 16 : wr * 16;         // the first row of this warp's in the areas
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        out.put(wr * 16 + g + e * 8, i * 8 + q4 * 2, o[i][2 * e], o[i][2 * e + 1], top[e], sum[e]);
+                    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                        for (int k = d0 / 8; k < (d0 + WIDE) / 8; ++k)
+                            *reinterpret_cast<float2 *>(sums + out_at(WIDE, i + g + e * 8, k * 8 - d0 + q4 * 2)) =
+                                make_float2(o[k][2 * e], o[k][2 * e + 1]);
+                        if (q4 == 0) {
+                            tail.ml[i + g + e * 8][0] = top[e];
+                            tail.ml[i + g + e * 8][1] = sum[e];
+                        }
+                    }
+                }
+                if (!(ok = meet(dead))) break;
+                for (unsigned u = t; u < M * (WIDE / 8); u += kWarps * 32) {
+                    const unsigned r = u / (WIDE / 8), c = u % (WIDE / 8) * 8;
+                    if (row0 + r >= live || d0 + c >= dim) continue;
+                    float m = tail.ml[r][0], l = tail.ml[r][1], f[2] = {1.0f, 0.0f};
+                    if (AREAS == 2) {
+                        const float m1 = tail.ml[16 + r][0], up = fmaxf(m, m1), base = up == -INFINITY ? 0.0f : up;
+                        f[0] = ex2(m - base);
+                        f[1] = ex2(m1 - base);
+                        l = l * f[0] + tail.ml[16 + r][1] * f[1];
+                        m = up;
+                    }
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; e += 4) {
+                        const float4 y = *reinterpret_cast<const float4 *>(sums + out_at(WIDE, r, c + e));
+                        x[e] = y.x, x[e + 1] = y.y, x[e + 2] = y.z, x[e + 3] = y.w;
+                        if (AREAS == 2) {
+                            const float4 z = *reinterpret_cast<const float4 *>(sums + out_at(WIDE, 16 + r, c + e));
+                            x[e] = x[e] * f[0] + z.x * f[1];
+                            x[e + 1] = x[e + 1] * f[0] + z.y * f[1];
+                            x[e + 2] = x[e + 2] * f[0] + z.z * f[1];
+                            x[e + 3] = x[e + 3] * f[0] + z.w * f[1];
+                        }
+                    }
+                    out.put8(r, d0 + c, x, m, l);
+                }
             }
         }
         if (!ok && lane == 0 && a.c.status) atomicOr(a.c.status, PER_DEVFLAG_TIMEOUT);

@@ -28,6 +28,7 @@ struct Cfg {
     static constexpr int CH = DP * ES / 16;                 // pieces of a row
     static constexpr int TILE = KT * DP * ES;
     static constexpr int SMEM = 2 * TILE + M * DP * ES + KT * 16 + 64;
+    static_assert(KT * 16 >= M * 8 && DP * ES >= 64, "what goes out fits where queries and places were");
     static constexpr int PER_SM = 227 * 1024 / (SMEM + 1024) < 3 ? 227 * 1024 / (SMEM + 1024) : 3;
 };
 
@@ -159,12 +160,31 @@ __global__ void __launch_bounds__(kThreads) k_attend_any(AttendArgs a, unsigned 
             sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
             sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
         }
+        // out, by way of the queries' place, 16 columns at a time
         const RowOut<T> out{a, by_group, b, h, live, row0, M, w.part(), slots + (w.tile0 != 0 ? 0 : slot_floats)};
+        float *sums = reinterpret_cast<float *>(qs);                  // [M][16]
+        float *ml = reinterpret_cast<float *>(info);                  // [M][2]
 #pragma unroll
-        for (int i = 0; i < DP / 8; ++i)
+        for (int d0 = 0; d0 < DP; d0 += 16) {
+            __syncthreads();
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-                out.put(warp * 16 + g + e * 8, i * 8 + q4 * 2, o[i][2 * e], o[i][2 * e + 1], top[e], sum[e]);
+            for (int e = 0; e < 2; ++e) {
+                const unsigned r = warp * 16 + g + e * 8;
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    *reinterpret_cast<float2 *>(sums + r * 16 + k * 8 + q4 * 2) = make_float2(o[d0 / 8 + k][2 * e], o[d0 / 8 + k][2 * e + 1]);
+                if (q4 == 0) {
+                    ml[2 * r] = top[e];
+                    ml[2 * r + 1] = sum[e];
+                }
+            }
+            __syncthreads();
+            const unsigned r = t / 2, c = t % 2 * 8;                  // 128 threads, 64 rows of two eights
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = sums[r * 16 + c + e];
+            out.put8(r, d0 + c, x, ml[2 * r], ml[2 * r + 1]);
+        }
     }
 }
 

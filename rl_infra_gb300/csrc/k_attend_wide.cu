@@ -137,8 +137,7 @@ __device__ __forceinline__ void seen(const AttendArgs &a, unsigned b, const Span
 
 template <typename T, int DP, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
-k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row_tiles, unsigned max_teams, FastDiv by_group, unsigned shift,
-              int ovec)
+k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row_tiles, unsigned max_teams, FastDiv by_group, unsigned shift)
 {
     using C = Cfg<DP, PAIR>;
     constexpr int ST = C::ST, M = C::M, TILE = C::TILE;
@@ -426,10 +425,7 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                 sum = tail.ml[0][r][1];
             }
             const unsigned o_at = PAIR ? my_o : tmem + 256 + lanes;
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
             const bool real = my_row < live;
-            const unsigned n_at = by_group.div(my_row), head_at = h * group + my_row - n_at * group;
-            T *to = static_cast<T *>(a.out) + b * a.so[0] + n_at * a.so[1] + head_at * a.so[2];
             constexpr int HALF = DP / 32 / (PAIR ? 1 : 2);                // blocks of 32 entries a thread takes
 #pragma unroll 1
             for (int i = 0; i < HALF; ++i) {
@@ -463,22 +459,8 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                         }
                     }
                 }
-                if (real && ovec && !out.part) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (c * 32 + k * 8 < (int)dim) {
-                            uint4 z;
-                            z.x = pack2<T>(o[8 * k] * inv, o[8 * k + 1] * inv);
-                            z.y = pack2<T>(o[8 * k + 2] * inv, o[8 * k + 3] * inv);
-                            z.z = pack2<T>(o[8 * k + 4] * inv, o[8 * k + 5] * inv);
-                            z.w = pack2<T>(o[8 * k + 6] * inv, o[8 * k + 7] * inv);
-                            *reinterpret_cast<uint4 *>(to + c * 32 + k * 8) = z;
-                        }
-                    if (c == 0 && a.lse) a.lse[((size_t)b * a.nodes + n_at) * a.q_heads + head_at] = lse_of(m, sum);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) out.put(row_in, c * 32 + 2 * k, o[2 * k], o[2 * k + 1], m, sum);
-                }
+                for (int k = 0; k < 4; ++k) out.put8(row_in, c * 32 + k * 8, o + 8 * k, m, sum);
             }
             fence_before();
             if (!(ok = meet(dead))) break;   // outputs, sums and the flag are read
@@ -516,9 +498,8 @@ cudaError_t wide(AttendArgs a, int type, const DeviceInfo &dev, cudaStream_t st,
     if (!p.parts) a.work = nullptr;
     FastDiv by_group;
     by_group.set(a.q_heads / a.c.heads);
-    const bool ovec = a.c.dim % 8 == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.so[0] % 8 == 0 && a.so[1] % 8 == 0 && a.so[2] % 8 == 0;
     const cudaError_t e = launch_clusters(k_attend_wide<T, DP, PAIR>, p.grid, kThreads, 1, C::SMEM, st, maps, a, p.row_tiles, p.teams,
-                                          by_group, shift, (int)ovec);
+                                          by_group, shift);
     return e != cudaSuccess || !p.parts ? e : join_parts(type, a, p, by_group, st);
 }
 

@@ -494,8 +494,7 @@ per_status per_tree_attention(const per_attend_shape *shape, const void *d_q, co
     a.q_heads = shape->q_heads;
     a.c2 = (float)((double)shape->scale * 1.4426950408889634);
     a.qvec = c.dim * e % 16 == 0 && on16(d_q, shape->stride_q, 3, e);
-    a.opair = e == 2 && c.dim % 2 == 0 && !misaligned(d_out, 4) && shape->stride_out[0] % 2 == 0 &&
-              shape->stride_out[1] % 2 == 0 && shape->stride_out[2] % 2 == 0;
+    a.ovec = c.dim % 8 == 0 && on16(d_out, shape->stride_out, 3, e);
     unsigned long long need = 0;
     const cudaError_t err = attend_work((int)c.type, a, &need);
     if (err != cudaSuccess) return done(err, where);

@@ -100,7 +100,7 @@ struct AttendArgs {
     long long sq[3], so[3], sm[2];
     unsigned batch, nodes, q_heads;
     float c2;                   // scale log2(e)
-    int qvec, opair;            // queries move in 16-byte pieces; outputs of 16 bits in pairs
+    int qvec, ovec;             // queries, outputs move in 16-byte pieces (outputs eight entries at a time)
 };
 
 struct KeepArgs {
