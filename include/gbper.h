@@ -582,13 +582,15 @@ typedef struct {
  *   how much.
  * Which CTA takes which part depends on the lengths alone, and parts are joined in their order: the same
  * inputs give the same bits.
- * per_tree_attention_work -- the bytes of d_work that a call of this shape needs on the current device.
+ * per_tree_attention_work -- the bytes of d_work that a call of this shape with these caches needs on the current
+ * device (which kernel takes it depends on where they lie; nothing is read).
  */
 per_status per_tree_attention(const per_attend_shape *shape, const void *d_q, const void *d_k_cache,
                               const void *d_v_cache, const int32_t *d_table, const int32_t *d_lens,
                               const int32_t *d_counts, const uint8_t *d_mask, void *d_out, float *d_lse,
                               void *d_work, uint32_t *d_status, void *stream);
-per_status per_tree_attention_work(const per_attend_shape *shape, uint64_t *bytes);
+per_status per_tree_attention_work(const per_attend_shape *shape, const void *d_k_cache, const void *d_v_cache,
+                                   uint64_t *bytes);
 
 typedef struct {
     per_cache cache;

@@ -188,7 +188,7 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         L.per_cache_append.restype = st
         L.per_tree_attention.argtypes = [vp] * 13
         L.per_tree_attention.restype = st
-        L.per_tree_attention_work.argtypes = [vp, ctypes.POINTER(u64)]
+        L.per_tree_attention_work.argtypes = [vp, vp, vp, ctypes.POINTER(u64)]
         L.per_tree_attention_work.restype = st
         L.per_cache_keep.argtypes = [vp] * 9
         L.per_cache_keep.restype = st
@@ -328,9 +328,9 @@ def per_tree_attention(shape, d_q, d_k_cache, d_v_cache, d_table, d_lens, d_coun
                                      d_work, d_status, stream)
 
 
-def per_tree_attention_work(shape):
+def per_tree_attention_work(shape, d_k_cache, d_v_cache):
     v = ctypes.c_uint64()
-    s = load().per_tree_attention_work(shape, ctypes.byref(v))
+    s = load().per_tree_attention_work(shape, d_k_cache, d_v_cache, ctypes.byref(v))
     return s, v.value
 
 

@@ -109,6 +109,17 @@ struct Walk {
         return true;
     }
 
+    // One sequence and head for the whole cluster, its tiles shared among `parts` CTAs.
+    __device__ __forceinline__ void one(const AttendArgs &a, unsigned seq, unsigned head, unsigned rank, unsigned parts)
+    {
+        b = seq;
+        h = head;
+        s = span(a, b);
+        n_tiles = tiles_of<KT>(s);
+        tile0 = (unsigned)((u64)rank * n_tiles / parts);
+        tile1 = (unsigned)((u64)(rank + 1) * n_tiles / parts);
+    }
+
     __device__ __forceinline__ bool next(const AttendArgs &a)
     {
         do {
@@ -373,11 +384,15 @@ struct Loader {
 // ---- host --------------------------------------------------------------------------------------
 struct Plan {
     unsigned m, row_tiles, teams, grid;
-    bool parts;             // a sequence can lie in several CTAs
+    unsigned share;         // > 0: CTAs (a cluster) that share a sequence's head and rows; 0: the tiles are cut as above
+    bool parts;             // a sequence can lie in several CTAs, which the second kernel joins
     u64 bytes;
 };
 
-inline Plan plan_of(const AttendArgs &a, unsigned m, unsigned kt, unsigned ctas)
+// `shares`: the kernel can take a sequence's head whole; `clusters`: it can join through the shared memory of a cluster's CTAs.  Where sequences are short that is
+// quicker than the cut (one kernel, no scratch memory): by tiles that a CTA works through one after another, a
+// begin counting 3, the second kernel 8.  The lengths are not known here; the table's width stands for them.
+inline Plan plan_of(const AttendArgs &a, unsigned m, unsigned kt, unsigned ctas, bool shares, bool clusters)
 {
     Plan p;
     const u64 rows = (u64)a.nodes * (a.q_heads / a.c.heads);   // at most 2^16
@@ -388,18 +403,34 @@ inline Plan plan_of(const AttendArgs &a, unsigned m, unsigned kt, unsigned ctas)
     const u64 tiles = ((most ? most : 1) + kBegin) * a.batch * a.c.heads;
     if (p.teams > tiles) p.teams = (unsigned)tiles;
     p.grid = p.teams * p.row_tiles;
+    p.share = 0;
     p.parts = most > 1 && p.teams > 1;
+    if (p.parts && shares) {
+        const u64 units = (u64)a.batch * a.c.heads * p.row_tiles;
+        u64 least = (units * (most + kBegin) + ctas - 1) / ctas + 3 + 8;
+        for (unsigned n = 1; n <= (clusters ? 8u : 1u); n *= 2) {
+            const u64 cost = (units * n + ctas - 1) / ctas * ((most + n - 1) / n + 3);
+            if (cost < least && units * n < 1u << 20) {
+                least = cost;
+                p.share = n;
+            }
+        }
+        if (p.share) {
+            p.grid = (unsigned)units * p.share;
+            p.parts = false;
+        }
+    }
     p.bytes = p.parts ? (u64)p.grid * (kRecord * 4 + 2ull * m * (a.c.dim + 2) * 4) : 0;
     return p;
 }
 
 // The kernels that take their tiles from the copy engine (k_attend_wide.cu: 16-bit types, heads of up to 128, scale > 0;
-// attend_rows.cuh: all).  *taken false: the call is not theirs.
-cudaError_t attend_wide(int type, const AttendArgs &a, const DeviceInfo &dev, cudaStream_t st, u64 *bytes, bool *taken);
-cudaError_t attend_rows_f32(const AttendArgs &a, const DeviceInfo &dev, cudaStream_t st, u64 *bytes, bool *taken);
-cudaError_t attend_rows_f16(const AttendArgs &a, const DeviceInfo &dev, cudaStream_t st, u64 *bytes, bool *taken);
-cudaError_t attend_rows_bf16(const AttendArgs &a, const DeviceInfo &dev, cudaStream_t st, u64 *bytes, bool *taken);
-// The maps of a call's cache; false where the copy engine cannot take it.  kt: keys of a tile.
+// attend_rows.cuh: all).
+cudaError_t attend_wide(int type, const AttendArgs &a, const DeviceInfo &dev, cudaStream_t st, u64 *bytes);
+cudaError_t attend_rows_f32(const AttendArgs &a, const DeviceInfo &dev, cudaStream_t st, u64 *bytes);
+cudaError_t attend_rows_f16(const AttendArgs &a, const DeviceInfo &dev, cudaStream_t st, u64 *bytes);
+cudaError_t attend_rows_bf16(const AttendArgs &a, const DeviceInfo &dev, cudaStream_t st, u64 *bytes);
+// The maps of a call's cache, whose layout is known to be right.  kt: keys of a tile.
 bool make_maps(int type, const AttendArgs &a, unsigned kt, CacheMaps *maps, unsigned *shift);   // k_attend.cu
 // joins what several CTAs hold (k_attend.cu)
 cudaError_t join_parts(int type, const AttendArgs &a, const Plan &p, const FastDiv &by_group, cudaStream_t st);

@@ -51,9 +51,24 @@ struct Tail {
 };
 static_assert(sizeof(Tail) <= 1024, "");
 
+// two and four words at the same place of the shared memory of the cluster's CTA `rank`
+__device__ __forceinline__ float2 far2(const float *p, unsigned rank)
+{
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(cluster_smem_addr(p, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 far4(const float *p, unsigned rank)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(cluster_smem_addr(p, rank)) : "memory");
+    return v;
+}
+
 template <typename T, int DP, int WR>
 __global__ void __launch_bounds__(kThreads, Cfg<T, DP, WR>::PER_SM)
-k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row_tiles, unsigned max_teams, FastDiv by_group, unsigned shift)
+k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row_tiles, unsigned max_teams, FastDiv by_group, unsigned shift, unsigned share)
 {
     using C = Cfg<T, DP, WR>;
     constexpr int KT = C::KT, KW = C::KW, WK = C::WK, M = C::M, ST = C::ST, ES = C::ES;
@@ -62,7 +77,8 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
     Tail &tail = *reinterpret_cast<Tail *>(area + C::AREA);
     volatile unsigned *dead = &tail.dead;
     const unsigned t = threadIdx.x, lane = t & 31u, warp = t >> 5;
-    const unsigned cta = blockIdx.x, team = cta / row_tiles, rt = cta - team * row_tiles;
+    const unsigned cta = blockIdx.x, unit = share ? cta / share : cta, team = unit / row_tiles, rt = unit - team * row_tiles;
+    const unsigned rank = share ? cta - unit * share : 0;         // in a cluster that shares a sequence's head and rows
     const unsigned group = by_group.d, row0 = rt * M, dim = a.c.dim;
     const unsigned halves = (dim * ES + 127) / 128;
     const unsigned full = smem_u32(tail.full), empty = smem_u32(tail.empty);
@@ -83,7 +99,14 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
     int *record = reinterpret_cast<int *>(a.work) + (size_t)cta * kRecord;
     if (a.work && t == 0) record[3] = 0;
     Walk<KT> w;
-    if (!w.template begin<kThreads>(a, team, max_teams, tail.scan)) return;
+    if (share) {
+        __syncthreads();
+        w.one(a, team / a.c.heads, team % a.c.heads, rank, share);
+    } else if (!w.template begin<kThreads>(a, team, max_teams, tail.scan)) {
+        return;
+    }
+    unsigned turns = 0;
+    auto next = [&] { return share ? turns++ == 0 : w.next(a); };
     unsigned st = 0, phase = 0;
 
     if (warp == kWarps) {   // the warp that asks for tiles
@@ -91,7 +114,7 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
         load.shift = shift;
         unsigned asked = 0;
         bool ok = true;
-        while (ok && w.next(a)) {
+        while (ok && next()) {
             if (row0 >= (unsigned)w.s.count * group) continue;
             load.look_up(a, w.b, w.s, w.tile0);
             for (unsigned tile = w.tile0; tile < w.tile1; ++tile) {
@@ -127,14 +150,15 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
         Meeting meet{smem_u32(&tail.meet), 0};
         unsigned tiles_done = 0;
         bool ok = true;
-        while (ok && w.next(a)) {
+        while (ok && next()) {
             const Span &s = w.s;
             const unsigned b = w.b, h = w.h;
-            if (w.tile0 == 0 && s.bad && rt == 0 && h == 0 && t == 0 && a.c.status) atomicOr(a.c.status, PER_DEVFLAG_BAD_INDEX);
+            const bool begins = w.tile0 == 0 && rank == 0;
+            if (begins && s.bad && rt == 0 && h == 0 && t == 0 && a.c.status) atomicOr(a.c.status, PER_DEVFLAG_BAD_INDEX);
             const unsigned live = (unsigned)s.count * group;         // rows of nodes that are there
-            if (w.tile0 == 0) absent_rows<T>(a, by_group, b, h, live, row0, M, t, kWarps * 32);
+            if (begins) absent_rows<T>(a, by_group, b, h, live, row0, M, t, kWarps * 32);
             if (row0 >= live) {
-                if (w.tile0 == 0 && w.tile1 < w.n_tiles && t == 0) w.note(record, team);
+                if (!share && begins && w.tile1 < w.n_tiles && t == 0) w.note(record, team);
                 continue;
             }
 
@@ -239,7 +263,7 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
             constexpr int WIDE = WK == 1 && ES == 2 ? DP / 2 : DP;        // entries that an area holds at once
             float *sums = reinterpret_cast<float *>(area);
             if (!(ok = meet(dead))) break;                              // the queries are done with
-            if (w.tile0 == 0 && w.tile1 < w.n_tiles && t == 0) w.note(record, team);
+            if (!share && begins && w.tile1 < w.n_tiles && t == 0) w.note(record, team);
             if constexpr (WK > 1) {
                 const unsigned i = WK == 4 ? wk & 1u : wr;              // the area that a pair shares
                 if (wk >= WK / 2) {
@@ -279,7 +303,7 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                     __syncwarp();
                 }
             }
-            const RowOut<T> out{a, by_group, b, h, live, row0, M, w.part(), slots + (w.tile0 != 0 ? 0 : slot_floats)};
+            const RowOut<T> out{a, by_group, b, h, live, row0, M, !share && w.part(), slots + (w.tile0 != 0 ? 0 : slot_floats)};
 #pragma unroll
             for (int d0 = 0; d0 < DP; d0 += WIDE) {
                 if (d0 > 0 && !(ok = meet(dead))) break;
@@ -297,6 +321,7 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                         }
                     }
                 }
+                if (share > 1) break;                                   // the cluster goes on below
                 if (!(ok = meet(dead))) break;
                 for (unsigned u = t; u < M * (WIDE / 8); u += kWarps * 32) {
                     const unsigned r = u / (WIDE / 8), c = u % (WIDE / 8) * 8;
@@ -329,21 +354,52 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
         if (!ok && lane == 0 && a.c.status) atomicOr(a.c.status, PER_DEVFLAG_TIMEOUT);
     }
     __syncthreads();   // nobody leaves before the copies have landed
+    if constexpr (WK > 1) {
+        if (share > 1) {   // each CTA joins a part of the rows from all of them
+            cluster_sync_all();
+            const unsigned live = (unsigned)w.s.count * group;
+            if (warp < kWarps && row0 < live) {
+                constexpr unsigned AREAS = WK == 4 ? 2 : 1;
+                const RowOut<T> out{a, by_group, w.b, w.h, live, row0, M, false, nullptr};
+                const float *sums = reinterpret_cast<const float *>(area);
+                for (unsigned u = rank * kWarps * 32 + t; u < M * (DP / 8); u += share * kWarps * 32) {
+                    const unsigned r = u / (DP / 8), c = u % (DP / 8) * 8;
+                    if (row0 + r >= live || c >= dim) continue;
+                    float m = -INFINITY, l = 0.0f, x[8] = {};
+                    for (unsigned i = 0; i < share; ++i)
+#pragma unroll
+                        for (unsigned k = 0; k < AREAS; ++k) m = fmaxf(m, far2(&tail.ml[k * 16 + r][0], i).x);
+                    const float base = m == -INFINITY ? 0.0f : m;
+                    for (unsigned i = 0; i < share; ++i)
+#pragma unroll
+                        for (unsigned k = 0; k < AREAS; ++k) {
+                            const float2 z = far2(&tail.ml[k * 16 + r][0], i);
+                            const float f = ex2(z.x - base);
+                            l += f * z.y;
+                            const float4 p = far4(sums + out_at(DP, k * 16 + r, c), i), q = far4(sums + out_at(DP, k * 16 + r, c + 4), i);
+                            x[0] += f * p.x, x[1] += f * p.y, x[2] += f * p.z, x[3] += f * p.w;
+                            x[4] += f * q.x, x[5] += f * q.y, x[6] += f * q.z, x[7] += f * q.w;
+                        }
+                    out.put8(r, c, x, m, l);
+                }
+            }
+            cluster_sync_all();   // nobody leaves before its sums are read
+        }
+    }
 }
 
 template <typename T, int DP, int WR>
-cudaError_t rows(AttendArgs a, int type, const DeviceInfo &dev, cudaStream_t st, u64 *bytes, bool *taken)
+cudaError_t rows(AttendArgs a, int type, const DeviceInfo &dev, cudaStream_t st, u64 *bytes)
 {
     using C = Cfg<T, DP, WR>;
-    const Plan p = plan_of(a, C::M, C::KT, (unsigned)dev.sms * C::PER_SM);
+    const Plan p = plan_of(a, C::M, C::KT, (unsigned)dev.sms * C::PER_SM, true, C::WK > 1);
     if (bytes) {
-        *bytes = std::max(*bytes, p.bytes);
+        *bytes = p.parts ? p.bytes : 0;
         return cudaSuccess;
     }
     CacheMaps maps;
     unsigned shift;
-    *taken = make_maps(type, a, C::KT, &maps, &shift);
-    if (!*taken) return cudaSuccess;
+    if (!make_maps(type, a, C::KT, &maps, &shift)) return cudaErrorInvalidValue;
     static std::atomic<bool> done[64];   // (two threads may both set the attribute, to the same value)
     if (!done[dev.device].load(std::memory_order_acquire)) {
         const cudaError_t e = cudaFuncSetAttribute(k_attend_rows<T, DP, WR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
@@ -353,26 +409,26 @@ cudaError_t rows(AttendArgs a, int type, const DeviceInfo &dev, cudaStream_t st,
     if (!p.parts) a.work = nullptr;
     FastDiv by_group;
     by_group.set(a.q_heads / a.c.heads);
-    const cudaError_t e = launch_clusters(k_attend_rows<T, DP, WR>, p.grid, kThreads, 1, C::SMEM, st, maps, a, p.row_tiles, p.teams,
-                                          by_group, shift);
+    const cudaError_t e = launch_clusters(k_attend_rows<T, DP, WR>, p.grid, kThreads, std::max(p.share, 1u), C::SMEM, st, maps, a,
+                                          p.row_tiles, p.teams, by_group, shift, p.share);
     return e != cudaSuccess || !p.parts ? e : join_parts(type, a, p, by_group, st);
 }
 
 template <typename T, int DP>
-cudaError_t rows_d(const AttendArgs &a, int type, const DeviceInfo &dev, cudaStream_t st, u64 *bytes, bool *taken)
+cudaError_t rows_d(const AttendArgs &a, int type, const DeviceInfo &dev, cudaStream_t st, u64 *bytes)
 {
     const unsigned n = a.nodes * (a.q_heads / a.c.heads);
-    if (n <= 16) return rows<T, DP, 1>(a, type, dev, st, bytes, taken);
-    if (n <= 32) return rows<T, DP, 2>(a, type, dev, st, bytes, taken);
-    return rows<T, DP, 4>(a, type, dev, st, bytes, taken);
+    if (n <= 16) return rows<T, DP, 1>(a, type, dev, st, bytes);
+    if (n <= 32) return rows<T, DP, 2>(a, type, dev, st, bytes);
+    return rows<T, DP, 4>(a, type, dev, st, bytes);
 }
 
 template <typename T>
-cudaError_t rows_t(const AttendArgs &a, int type, const DeviceInfo &dev, cudaStream_t st, u64 *bytes, bool *taken)
+cudaError_t rows_t(const AttendArgs &a, int type, const DeviceInfo &dev, cudaStream_t st, u64 *bytes)
 {
-    if (a.c.dim <= 64) return rows_d<T, 64>(a, type, dev, st, bytes, taken);
-    if (a.c.dim <= 128) return rows_d<T, 128>(a, type, dev, st, bytes, taken);
-    return rows_d<T, 256>(a, type, dev, st, bytes, taken);
+    if (a.c.dim <= 64) return rows_d<T, 64>(a, type, dev, st, bytes);
+    if (a.c.dim <= 128) return rows_d<T, 128>(a, type, dev, st, bytes);
+    return rows_d<T, 256>(a, type, dev, st, bytes);
 }
 
 }  // namespace

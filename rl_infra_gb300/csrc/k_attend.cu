@@ -188,48 +188,62 @@ __global__ void __launch_bounds__(kThreads) k_attend_any(AttendArgs a, unsigned 
     }
 }
 
-// Joins the parts of what lies in several CTAs: each CTA that begins such a stretch left a record.  A warp
-// takes a row, a lane every 32nd entry.
+// Joins the parts of what lies in several CTAs: each CTA that begins such a stretch left a record.  A warp takes
+// per_warp rows one after another; its lanes work out 32 parts' weights at once, then take eight entries each.
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_attend_join(AttendArgs a, unsigned row_tiles, unsigned m_rows, FastDiv by_group)
+__global__ void __launch_bounds__(kThreads) k_attend_join(AttendArgs a, unsigned row_tiles, unsigned m_rows, FastDiv by_group, unsigned per_warp)
 {
     const unsigned cta = blockIdx.x, team = cta / row_tiles, rt = cta - team * row_tiles;
     pdl_wait();
     pdl_release();
-    const int *record = reinterpret_cast<const int *>(a.work) + (size_t)cta * kRecord;
-    const int parts = record[3];
+    const int4 record = *(reinterpret_cast<const int4 *>(a.work) + (size_t)cta * (kRecord / 4));
+    const int parts = record.w;
     if (parts == 0) return;
-    const unsigned b = (unsigned)record[0], h = (unsigned)record[1], count = (unsigned)record[2];
+    const unsigned b = (unsigned)record.x, h = (unsigned)record.y, count = (unsigned)record.z;
     const unsigned group = by_group.d, live = count * group, dim = a.c.dim, slot_floats = m_rows * (dim + 2);
-    const unsigned r = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31u, row = rt * m_rows + r;
-    if (r >= m_rows || row >= live) return;
+    const unsigned lane = threadIdx.x & 31u;
     const float *slots = a.work + (size_t)gridDim.x * kRecord;
     auto slot = [&](int i) {   // the first part lies in its CTA's second slot, the others in their first
         return slots + ((size_t)((team + i) * row_tiles + rt) * 2 + (i == 0)) * slot_floats;
     };
-    float m = -INFINITY;
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, slot(i)[m_rows * dim + 2 * r]);
+    const RowOut<T> out{a, by_group, b, h, live, rt * m_rows, m_rows, false, nullptr};
+    const unsigned r0 = (blockIdx.y * 4 + (threadIdx.x >> 5)) * per_warp;
+    for (unsigned r = r0; r < r0 + per_warp && r < m_rows && rt * m_rows + r < live; ++r) {
+        float m = -INFINITY;
+        for (int i = lane; i < parts; i += 32) m = fmaxf(m, slot(i)[m_rows * dim + 2 * r]);
 #pragma unroll
-    for (int d = 16; d; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const float base = m == -INFINITY ? 0.0f : m;
-    constexpr int E = 8;       // 32 lanes x 8 entries
-    float acc[E] = {}, l = 0.0f;
-#pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
-        const float *p = slot(i);
-        const float f = ex2(p[m_rows * dim + 2 * r] - base);
-        l += f * p[m_rows * dim + 2 * r + 1];
+        for (int d = 16; d; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        const float base = m == -INFINITY ? 0.0f : m;
+        float x[8] = {}, l = 0.0f;              // a lane's eight entries
+        for (int i0 = 0; i0 < parts; i0 += 32) {
+            float f = 0.0f;
+            if (i0 + (int)lane < parts) {
+                const float2 z = *reinterpret_cast<const float2 *>(slot(i0 + lane) + m_rows * dim + 2 * r);
+                f = ex2(z.x - base);
+                l += f * z.y;
+            }
+            const int n = min(32, parts - i0);
+#pragma unroll 8
+            for (int i = 0; i < n; ++i) {
+                const float w = __shfl_sync(0xffffffffu, f, i);
+                const float *p = slot(i0 + i) + r * dim + lane * 8;
+                if (lane * 8 >= dim) continue;
+                if (dim % 8 == 0) {
+                    const float4 y = *reinterpret_cast<const float4 *>(p), z = *reinterpret_cast<const float4 *>(p + 4);
+                    x[0] += w * y.x, x[1] += w * y.y, x[2] += w * y.z, x[3] += w * y.w;
+                    x[4] += w * z.x, x[5] += w * z.y, x[6] += w * z.z, x[7] += w * z.w;
+                } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (e * 32 + lane < dim) acc[e] += f * p[r * dim + e * 32 + lane];
+                    for (int e = 0; e < 8; ++e)
+                        if (lane * 8 + e < dim) x[e] += w * p[e];
+                }
+            }
+        }
+#pragma unroll
+        for (int d = 16; d; d /= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
+        out.put8(r, lane * 8, x, m, l);
     }
-    const unsigned node = by_group.div(row), head = h * group + row - node * group;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    T *to = static_cast<T *>(a.out) + b * a.so[0] + node * a.so[1] + head * a.so[2];
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        if (e * 32 + lane < dim) to[e * 32 + lane] = from_f32<T>(acc[e] * inv);
-    if (lane == 0 && a.lse) a.lse[((size_t)b * a.nodes + node) * a.q_heads + head] = lse_of(m, l);
 }
 
 // ---- the copy engine's maps ----------------------------------------------------------------------
@@ -253,21 +267,27 @@ Encode encoder()
     return reinterpret_cast<Encode>(f);
 }
 
-// One array, its axes in the order of their strides: each a multiple of the one before and past all that it covers.
-bool make_map(int type, const AttendArgs &a, const void *base, const long long st[3], unsigned rows, CUtensorMap *map, unsigned char *at)
+// One array as the copy engine sees it, its axes in the order of their strides.  False: it does not take it (each stride
+// must be a multiple of the one before and past all that this covers).
+struct Layout {
+    cuuint64_t size[4], stride[3];
+    int slot_axis;
+    unsigned char at[3];
+};
+
+bool layout_of(const AttendArgs &a, const long long st[3], unsigned es, Layout *l)
 {
-    const Encode encode = encoder();
-    if (!encode) return false;
-    const unsigned es = type == PER_TYPE_F32 ? 4 : 2;
     const u64 dims[3] = {a.c.page.d, a.c.heads, a.c.pages};   // slot, head, page
     const long long strides[3] = {st[1], st[2], st[0]};
     int order[3] = {0, 1, 2};
-    std::sort(order, order + 3, [&](int x, int y) {
+    auto before = [&](int x, int y) {
         if ((dims[x] == 1) != (dims[y] == 1)) return dims[y] == 1;   // axes of one place last
         return dims[x] == 1 || strides[x] == strides[y] ? x < y : strides[x] < strides[y];
-    });
-    cuuint64_t size[4] = {a.c.dim, 1, 1, 1}, stride[3];
-    cuuint32_t box[4] = {128 / es, 1, 1, 1}, one[4] = {1, 1, 1, 1};
+    };
+    if (before(order[1], order[0])) std::swap(order[0], order[1]);
+    if (before(order[2], order[1])) std::swap(order[1], order[2]);
+    if (before(order[1], order[0])) std::swap(order[0], order[1]);
+    l->size[0] = a.c.dim;
     u64 unit = 16, covered = (u64)a.c.dim * es;
     for (int i = 0; i < 3; ++i) {
         const int x = order[i];
@@ -278,16 +298,28 @@ bool make_map(int type, const AttendArgs &a, const void *base, const long long s
             if (s < covered || s % unit) return false;
         }
         if (s >= 1ull << 40) return false;
-        size[i + 1] = dims[x];
-        stride[i] = s;
-        if (x == 0) box[i + 1] = rows;
-        at[x] = (unsigned char)(i + 1);
+        l->size[i + 1] = dims[x];
+        l->stride[i] = s;
+        if (x == 0) l->slot_axis = i + 1;
+        l->at[x] = (unsigned char)(i + 1);
         covered += s * (dims[x] - 1);
         unit = s;
     }
+    return true;
+}
+
+bool make_map(int type, const AttendArgs &a, const void *base, const long long st[3], unsigned rows, CUtensorMap *map, unsigned char *at)
+{
+    const Encode encode = encoder();
+    const unsigned es = type == PER_TYPE_F32 ? 4 : 2;
+    Layout l;
+    if (!encode || !layout_of(a, st, es, &l)) return false;
+    cuuint32_t box[4] = {128 / es, 1, 1, 1}, one[4] = {1, 1, 1, 1};
+    box[l.slot_axis] = rows;
+    for (int i = 0; i < 3; ++i) at[i] = l.at[i];
     const CUtensorMapDataType kind = type == PER_TYPE_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                      : type == PER_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    return encode(map, kind, 4, const_cast<void *>(base), size, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    return encode(map, kind, 4, const_cast<void *>(base), l.size, l.stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -295,9 +327,9 @@ template <typename T, int DP>
 cudaError_t attend_any(AttendArgs a, int type, const DeviceInfo &dev, cudaStream_t st, u64 *bytes)
 {
     using C = Cfg<T, DP>;
-    const Plan p = plan_of(a, C::M, C::KT, (unsigned)dev.sms * C::PER_SM);
+    const Plan p = plan_of(a, C::M, C::KT, (unsigned)dev.sms * C::PER_SM, false, false);
     if (bytes) {
-        *bytes = std::max(*bytes, p.bytes);
+        *bytes = p.parts ? p.bytes : 0;
         return cudaSuccess;
     }
     static std::atomic<bool> done[64];   // (two threads may both set the attribute, to the same value)
@@ -321,23 +353,20 @@ cudaError_t attend_any_t(const AttendArgs &a, int type, const DeviceInfo &dev, c
     return attend_any<T, 256>(a, type, dev, st, bytes);
 }
 
-// Launches, or (bytes given) says what scratch memory the call needs: the most of the kernels that may take it, since
-// that depends on where its arrays lie.
+// Launches, or (bytes given) says what scratch memory the call needs.
 cudaError_t attend(int type, const AttendArgs &a, cudaStream_t st, u64 *bytes)
 {
     DeviceInfo dev;
-    cudaError_t e = device_info(&dev);
+    const cudaError_t e = device_info(&dev);
     if (e != cudaSuccess) return e;
     if (bytes) *bytes = 0;
-    bool taken = false;
-    const unsigned rows = a.nodes * (a.q_heads / a.c.heads);
-    if (type != PER_TYPE_F32 && a.c.dim <= 128 && rows > kFew && (bytes || a.c2 > 0.0f)) {
-        e = attend_wide(type, a, dev, st, bytes, &taken);
-        if (e != cudaSuccess || (taken && !bytes)) return e;
+    const unsigned es = type == PER_TYPE_F32 ? 4 : 2;
+    Layout l;
+    if (a.c.vec && a.c.pages && a.c.width && encoder() && layout_of(a, a.c.sk, es, &l) && layout_of(a, a.c.sv, es, &l)) {
+        if (type == PER_TYPE_F32) return attend_rows_f32(a, dev, st, bytes);
+        if (a.c.dim <= 128 && a.nodes * (a.q_heads / a.c.heads) > kFew && a.c2 > 0.0f) return attend_wide(type, a, dev, st, bytes);
+        return type == PER_TYPE_F16 ? attend_rows_f16(a, dev, st, bytes) : attend_rows_bf16(a, dev, st, bytes);
     }
-    e = type == PER_TYPE_F32 ? attend_rows_f32(a, dev, st, bytes, &taken)
-        : type == PER_TYPE_F16 ? attend_rows_f16(a, dev, st, bytes, &taken) : attend_rows_bf16(a, dev, st, bytes, &taken);
-    if (e != cudaSuccess || (taken && !bytes)) return e;
     if (type == PER_TYPE_F32) return attend_any_t<float>(a, type, dev, st, bytes);
     if (type == PER_TYPE_F16) return attend_any_t<__half>(a, type, dev, st, bytes);
     return attend_any_t<__nv_bfloat16>(a, type, dev, st, bytes);
@@ -347,7 +376,6 @@ cudaError_t attend(int type, const AttendArgs &a, cudaStream_t st, u64 *bytes)
 
 bool make_maps(int type, const AttendArgs &a, unsigned kt, CacheMaps *maps, unsigned *shift)
 {
-    if (!a.c.vec || a.c.pages == 0 || a.c.width == 0) return false;
     unsigned s = 0;                // rows of a box: a power of 2 that divides the page
     while ((2u << s) <= kt && a.c.page.d % (2u << s) == 0) ++s;
     *shift = s;
@@ -357,7 +385,8 @@ bool make_maps(int type, const AttendArgs &a, unsigned kt, CacheMaps *maps, unsi
 cudaError_t join_parts(int type, const AttendArgs &a, const Plan &p, const FastDiv &by_group, cudaStream_t st)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.grid, (p.m + 3) / 4);
+    const unsigned per_warp = p.m > 32 ? 4 : 1;   // (many CTAs of one row a warp took longer to come and go than to work)
+    cfg.gridDim = dim3(p.grid, (p.m + 4 * per_warp - 1) / (4 * per_warp));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -365,9 +394,9 @@ cudaError_t join_parts(int type, const AttendArgs &a, const Plan &p, const FastD
     attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (type == PER_TYPE_F32) return cudaLaunchKernelEx(&cfg, k_attend_join<float>, a, p.row_tiles, p.m, by_group);
-    if (type == PER_TYPE_F16) return cudaLaunchKernelEx(&cfg, k_attend_join<__half>, a, p.row_tiles, p.m, by_group);
-    return cudaLaunchKernelEx(&cfg, k_attend_join<__nv_bfloat16>, a, p.row_tiles, p.m, by_group);
+    if (type == PER_TYPE_F32) return cudaLaunchKernelEx(&cfg, k_attend_join<float>, a, p.row_tiles, p.m, by_group, per_warp);
+    if (type == PER_TYPE_F16) return cudaLaunchKernelEx(&cfg, k_attend_join<__half>, a, p.row_tiles, p.m, by_group, per_warp);
+    return cudaLaunchKernelEx(&cfg, k_attend_join<__nv_bfloat16>, a, p.row_tiles, p.m, by_group, per_warp);
 }
 
 }  // namespace attend

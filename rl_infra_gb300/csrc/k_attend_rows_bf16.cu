@@ -4,9 +4,9 @@
 namespace gbper {
 namespace attend {
 
-cudaError_t attend_rows_bf16(const AttendArgs &a, const DeviceInfo &dev, cudaStream_t st, u64 *bytes, bool *taken)
+cudaError_t attend_rows_bf16(const AttendArgs &a, const DeviceInfo &dev, cudaStream_t st, u64 *bytes)
 {
-    return rows_t<__nv_bfloat16>(a, PER_TYPE_BF16, dev, st, bytes, taken);
+    return rows_t<__nv_bfloat16>(a, PER_TYPE_BF16, dev, st, bytes);
 }
 
 }  // namespace attend

@@ -477,18 +477,17 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
 }
 
 template <typename T, int DP, bool PAIR>
-cudaError_t wide(AttendArgs a, int type, const DeviceInfo &dev, cudaStream_t st, u64 *bytes, bool *taken)
+cudaError_t wide(AttendArgs a, int type, const DeviceInfo &dev, cudaStream_t st, u64 *bytes)
 {
     using C = Cfg<DP, PAIR>;
-    const Plan p = plan_of(a, C::M, KT, (unsigned)dev.sms);
+    const Plan p = plan_of(a, C::M, KT, (unsigned)dev.sms, false, false);
     if (bytes) {
-        *bytes = std::max(*bytes, p.bytes);
+        *bytes = p.parts ? p.bytes : 0;
         return cudaSuccess;
     }
     CacheMaps maps;
     unsigned shift;
-    *taken = make_maps(type, a, KT, &maps, &shift);
-    if (!*taken) return cudaSuccess;
+    if (!make_maps(type, a, KT, &maps, &shift)) return cudaErrorInvalidValue;
     static std::atomic<bool> done[64];   // (two threads may both set the attribute, to the same value)
     if (!done[dev.device].load(std::memory_order_acquire)) {
         const cudaError_t e = cudaFuncSetAttribute(k_attend_wide<T, DP, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
@@ -504,20 +503,20 @@ cudaError_t wide(AttendArgs a, int type, const DeviceInfo &dev, cudaStream_t st,
 }
 
 template <typename T>
-cudaError_t wide_t(const AttendArgs &a, int type, const DeviceInfo &dev, cudaStream_t st, u64 *bytes, bool *taken)
+cudaError_t wide_t(const AttendArgs &a, int type, const DeviceInfo &dev, cudaStream_t st, u64 *bytes)
 {
     const bool pair = a.nodes * (a.q_heads / a.c.heads) > 128;
     if (a.c.dim <= 64)
-        return pair ? wide<T, 64, true>(a, type, dev, st, bytes, taken) : wide<T, 64, false>(a, type, dev, st, bytes, taken);
-    return pair ? wide<T, 128, true>(a, type, dev, st, bytes, taken) : wide<T, 128, false>(a, type, dev, st, bytes, taken);
+        return pair ? wide<T, 64, true>(a, type, dev, st, bytes) : wide<T, 64, false>(a, type, dev, st, bytes);
+    return pair ? wide<T, 128, true>(a, type, dev, st, bytes) : wide<T, 128, false>(a, type, dev, st, bytes);
 }
 
 }  // namespace
 
-cudaError_t attend_wide(int type, const AttendArgs &a, const DeviceInfo &dev, cudaStream_t st, u64 *bytes, bool *taken)
+cudaError_t attend_wide(int type, const AttendArgs &a, const DeviceInfo &dev, cudaStream_t st, u64 *bytes)
 {
-    if (type == PER_TYPE_F16) return wide_t<__half>(a, type, dev, st, bytes, taken);
-    return wide_t<__nv_bfloat16>(a, type, dev, st, bytes, taken);
+    if (type == PER_TYPE_F16) return wide_t<__half>(a, type, dev, st, bytes);
+    return wide_t<__nv_bfloat16>(a, type, dev, st, bytes);
 }
 
 }  // namespace attend

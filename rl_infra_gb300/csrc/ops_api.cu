@@ -437,7 +437,8 @@ per_status per_cache_append(const per_append_shape *shape, const void *d_k, cons
     return done(launch_append((int)c.type, a, reinterpret_cast<cudaStream_t>(stream)), where);
 }
 
-per_status per_tree_attention_work(const per_attend_shape *shape, uint64_t *bytes)
+per_status per_tree_attention_work(const per_attend_shape *shape, const void *d_k_cache, const void *d_v_cache,
+                                   uint64_t *bytes)
 {
     const char *where = "per_tree_attention_work";
     if (const char *f = attend_fault(shape)) return refuse(where, f);
@@ -445,10 +446,11 @@ per_status per_tree_attention_work(const per_attend_shape *shape, uint64_t *byte
     *bytes = 0;
     if (shape->batch == 0 || shape->nodes == 0) return PER_OK;
     AttendArgs a{};
-    a.c = cache_args(shape->cache, nullptr, nullptr, nullptr, nullptr);
+    a.c = cache_args(shape->cache, const_cast<void *>(d_k_cache), const_cast<void *>(d_v_cache), nullptr, nullptr);
     a.batch = shape->batch;
     a.nodes = shape->nodes;
     a.q_heads = shape->q_heads;
+    a.c2 = (float)((double)shape->scale * 1.4426950408889634);
     unsigned long long n = 0;
     const cudaError_t e = attend_work((int)shape->cache.type, a, &n);
     *bytes = n;

@@ -584,31 +584,32 @@ def tree_attention(q, k_cache, v_cache, block_table, lens, mask=None, counts=Non
     lib = _library()
     shape = (*head, b, n, hq, dim ** -0.5 if scale is None else scale, *q.stride()[:3], *got["out"].stride()[:3], *sm)
     if work is None:
-        size = _work_bytes(lib, _ATTEND.pack(*shape, 0), "tree_attention")
-        work = torch.empty(size, dtype=torch.uint8, device=q.device)
+        size = _work_bytes(lib, _ATTEND.pack(*shape, 0), kp, vp)
+        work = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
     elif not isinstance(work, torch.Tensor) or work.dtype is not torch.uint8 or work.get_device() != dev or \
             not work.is_contiguous():
         raise _bad("work", f"contiguous, of dtype uint8, on cuda:{dev}", work)
     _check(lib.per_tree_attention(
-        _ATTEND.pack(*shape, work.numel()), q.data_ptr(), kp, vp, tp, lp, np_, mp, got["out"].data_ptr(),
-        got["lse"].data_ptr(), work.data_ptr(), _status_ptr(status, dev), _raw_stream(dev)), "tree_attention")
+        _ATTEND.pack(*shape, work.numel() if work is not None else 0), q.data_ptr(), kp, vp, tp, lp, np_, mp,
+        got["out"].data_ptr(), got["lse"].data_ptr(), work.data_ptr() if work is not None else None,
+        _status_ptr(status, dev), _raw_stream(dev)), "tree_attention")
     return got
 
 
-def _work_bytes(lib, shape, name):
+def _work_bytes(lib, shape, kp, vp):
     size = ctypes.c_uint64()
-    _check(lib.per_tree_attention_work(shape, ctypes.byref(size)), name)
+    _check(lib.per_tree_attention_work(shape, kp, vp, ctypes.byref(size)), "tree_attention_work")
     return size.value
 
 
-def tree_attention_work(q, k_cache, block_table):
-    """Bytes of scratch memory that tree_attention needs for these shapes on the current device."""
+def tree_attention_work(q, k_cache, v_cache, block_table, scale=None):
+    """Bytes of scratch memory that tree_attention needs for such arrays on their device (0: none)."""
     code, dev = _lead(q, "q", 4)
     b, n, hq, dim = q.shape
-    head = _cache(k_cache, k_cache, block_table, b, dev, code)[0]
+    head, kp, vp, _ = _cache(k_cache, v_cache, block_table, b, dev, code)
     with torch.cuda.device(dev):
-        return _work_bytes(_library(), _ATTEND.pack(*head, b, n, hq, 1.0, *_NO_STRIDES, *_NO_STRIDES, *_NO_STRIDE, 0),
-                           "tree_attention_work")
+        return _work_bytes(_library(), _ATTEND.pack(*head, b, n, hq, dim ** -0.5 if scale is None else scale, *_NO_STRIDES,
+                                                    *_NO_STRIDES, *_NO_STRIDE, 0), kp, vp)
 
 
 def cache_keep(k_cache, v_cache, block_table, lens, path, kept, nodes=None, status=None, stream=None):

@@ -497,12 +497,13 @@ def test_captured_and_replayed():
 
 def test_another_stream_and_given_outputs():
     r = np.random.default_rng(21)
-    kc, vc, table = cache(r, 2, 300, 16, 1, 64, "f16")
-    fill(r, kc, vc, table, [300, 300], "f16")
-    q, lens = rand(r, 2, 4, 4, 64, kind="f16"), i32([280, 5])
+    kc, vc, table = cache(r, 2, 9000, 16, 1, 64, "f16")
+    fill(r, kc, vc, table, [9000, 300], "f16")
+    q, lens = rand(r, 2, 4, 4, 64, kind="f16"), i32([8980, 5])
     want = ops.tree_attention(q, kc, vc, table, lens)
     side = torch.cuda.Stream()
-    work = torch.empty(ops.tree_attention_work(q, kc, table), dtype=torch.uint8, device="cuda")
+    work = torch.empty(ops.tree_attention_work(q, kc, vc, table), dtype=torch.uint8, device="cuda")
+    assert work.numel() and not ops.tree_attention_work(q, kc, vc, table[:, :1])
     out = {"out": torch.empty_like(q), "lse": torch.empty(2, 4, 4, device="cuda")}
     side.wait_stream(torch.cuda.current_stream())
     got = ops.tree_attention(q, kc, vc, table, lens, out=out, work=work, stream=side)

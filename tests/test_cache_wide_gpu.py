@@ -155,3 +155,26 @@ def test_many_calls_at_once():
     for row in got:
         for x, y in zip(row, want):
             assert torch.equal(x["out"], y["out"]) and torch.equal(x["lse"], y["lse"])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("n, g", [(1, 4), (4, 8), (16, 4), (40, 6)])
+@pytest.mark.parametrize("b", [1, 3, 40, 150])
+def test_room_for_more(kind, n, g, b):
+    """Short sequences of every number of tiles, in a table just wide enough and in one with room for long ones: other
+    cuts of the work, the same results to the last roundings."""
+    r = np.random.default_rng(41)
+    lens, counts = r.integers(0, 500, b), r.integers(0, n + 1, b)
+    lens[0], counts[0] = 499, n
+    kc, vc, table = cache(r, b, 500 + n, 16, 2, 64, kind)
+    fill(r, kc, vc, table, lens + counts, kind)
+    q = rand(r, b, n, 2 * g, 64, kind=kind)
+    wide = torch.nn.functional.pad(table, (0, 5000), value=-1)
+    one = ops.tree_attention(q, kc, vc, table, i32(lens), counts=i32(counts))
+    two = ops.tree_attention(q, kc, vc, wide, i32(lens), counts=i32(counts))
+    some = min(b, 4)
+    want = co.attend(host(q[:some]), host(kc), host(vc), table.cpu().numpy(), lens[:some], None, counts[:some], kind=kind)
+    for got in (one, two):
+        check_attend({k: t[:some] for k, t in got.items()}, want, kind)
+    torch.testing.assert_close(one["out"], two["out"], rtol=2e-2 if kind == "bf16" else 1e-4, atol=1e-2 if kind == "bf16" else 1e-5)
+    torch.testing.assert_close(one["lse"], two["lse"], rtol=1e-5, atol=1e-5)
