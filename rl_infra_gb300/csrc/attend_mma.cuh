@@ -65,7 +65,7 @@ __device__ __forceinline__ uint4 entries(const T *src, unsigned c, unsigned dim,
 }
 
 // sc = q k for 16 rows from r0 of the m rows at qs, and KW keys from key0 of the kt at ks; `steps` of the instruction
-// along a head.  A binary32 step takes two pieces four apart: column c of the instruction is entry 2 c
+// along a head.  binary32 queries lie in two parts, upper and lower.  A step of these takes two pieces four apart: column c of the instruction is entry 2 c
 // mod 4 of piece c / 2 * 4, column c + 4 the entry behind it, so that 16 lanes read 16 different banks twice.
 template <typename T, int DP, int KW>
 __device__ __forceinline__ void scores(float (*sc)[4], const unsigned char *qs, unsigned m, unsigned r0, const unsigned char *ks,
@@ -94,12 +94,13 @@ __device__ __forceinline__ void scores(float (*sc)[4], const unsigned char *qs, 
             if (k >= (int)steps) break;
             unsigned ah[4], al[4];
             const unsigned c = (k >> 2) * 8 + (k & 3) + (q4 >> 1) * 4, in = (q4 & 1u) * 8;
-            const float2 x = *reinterpret_cast<const float2 *>(qs + piece(m, r0 + g, c) + in);
-            const float2 y = *reinterpret_cast<const float2 *>(qs + piece(m, r0 + g + 8, c) + in);
-            split(x.x, ah[0], al[0]);
-            split(y.x, ah[1], al[1]);
-            split(x.y, ah[2], al[2]);
-            split(y.y, ah[3], al[3]);
+            const unsigned low = m * DP * 4;   // the lower parts lie behind the upper ones
+            const uint2 x = *reinterpret_cast<const uint2 *>(qs + piece(m, r0 + g, c) + in);
+            const uint2 y = *reinterpret_cast<const uint2 *>(qs + piece(m, r0 + g + 8, c) + in);
+            const uint2 xl = *reinterpret_cast<const uint2 *>(qs + low + piece(m, r0 + g, c) + in);
+            const uint2 yl = *reinterpret_cast<const uint2 *>(qs + low + piece(m, r0 + g + 8, c) + in);
+            ah[0] = x.x, ah[1] = y.x, ah[2] = x.y, ah[3] = y.y;
+            al[0] = xl.x, al[1] = yl.x, al[2] = xl.y, al[3] = yl.y;
 #pragma unroll
             for (int i = 0; i < KW / 8; ++i) {
                 const float2 z = *reinterpret_cast<const float2 *>(ks + piece(kt, key0 + i * 8 + g, c) + in);

@@ -25,16 +25,17 @@ struct Cfg {
     static constexpr int ES = (int)sizeof(T);
     static constexpr int WK = kWarps / WR;                        // warps along the keys
     static constexpr int M = 16 * WR;                             // rows of a CTA
-    static constexpr int KT = DP * ES >= 1024 ? 32 : DP * ES >= 256 ? 64 : 128;
+    static constexpr int KT = ES == 4 ? (DP >= 128 ? 32 : 64) : DP >= 128 ? 64 : 128;
     static constexpr int KW = KT / WK;                            // keys of a warp
     static constexpr int PER_HALF = 128 / ES;
     static constexpr int STAGE = 2 * KT * DP * ES;
     static constexpr int JOIN = WK == 4 ? 2 * 16 * DP * 4 : WK == 2 ? M * DP * 4 : 0;   // what the warps hand over
-    static constexpr int AREA = M * DP * ES > JOIN ? M * DP * ES : JOIN;                // the queries lie there before
+    static constexpr int QB = M * DP * ES * (ES == 4 ? 2 : 1);                          // the queries lie there before
+    static constexpr int AREA = QB > JOIN ? QB : JOIN;
     static constexpr int TAIL = 1024;
     static constexpr int HALF_SM = 228 * 1024 / 2 - 1024;
     static constexpr int WHOLE_SM = 227 * 1024;
-    static constexpr int PER_SM = (HALF_SM - AREA - TAIL) / STAGE >= 3 ? 2 : 1;
+    static constexpr int PER_SM = (HALF_SM - AREA - TAIL) / STAGE >= (ES == 4 ? 2 : 3) ? 2 : 1;
     static constexpr int FIT = ((PER_SM == 2 ? HALF_SM : WHOLE_SM) - AREA - TAIL) / STAGE;
     static constexpr int ST = FIT > 6 ? 6 : FIT;
     static constexpr int SMEM = ST * STAGE + AREA + TAIL;
@@ -175,6 +176,14 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                     uint4 v = make_uint4(0, 0, 0, 0);
                     if (!a.qvec) v = entries<T>(src, c, dim, some);
                     else if (some && c * 16 < dim * ES) v = *reinterpret_cast<const uint4 *>(src + c * (16 / ES));
+                    if constexpr (ES == 4) {   // both parts of each
+                        uint4 lo;
+                        split(__uint_as_float(v.x), v.x, lo.x);
+                        split(__uint_as_float(v.y), v.y, lo.y);
+                        split(__uint_as_float(v.z), v.z, lo.z);
+                        split(__uint_as_float(v.w), v.w, lo.w);
+                        *reinterpret_cast<uint4 *>(area + M * DP * ES + piece(M, r, c)) = lo;
+                    }
                     *reinterpret_cast<uint4 *>(area + piece(M, r, c)) = v;
                 }
             }
@@ -266,7 +275,7 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
             if (!share && begins && w.tile1 < w.n_tiles && t == 0) w.note(record, team);
             if constexpr (WK > 1) {
                 const unsigned i = WK == 4 ? wk & 1u : wr;              // the area that a pair shares
-                if (wk >= WK / 2) {
+                if (wk >= (unsigned)WK / 2) {
                     float *to = sums + i * 16 * DP;
 #pragma unroll
                     for (int k = 0; k < DP / 8; ++k)
@@ -280,7 +289,7 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                     }
                 }
                 if (!(ok = meet(dead))) break;
-                if (wk < WK / 2) {
+                if (wk < (unsigned)WK / 2) {
                     const float *from = sums + i * 16 * DP;
                     float mine[2], other[2];
 #pragma unroll
@@ -307,7 +316,7 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
 #pragma unroll
             for (int d0 = 0; d0 < DP; d0 += WIDE) {
                 if (d0 > 0 && !(ok = meet(dead))) break;
-                if (wk < WK / 2 || WK == 1) {
+                if (WK == 1 || wk < (unsigned)WK / 2) {
                     const unsigned i = WK == 4 ? wk * 16 : wr * 16;         // the first row of this warp's in the areas
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -419,8 +428,10 @@ cudaError_t rows_d(const AttendArgs &a, int type, const DeviceInfo &dev, cudaStr
 {
     const unsigned n = a.nodes * (a.q_heads / a.c.heads);
     if (n <= 16) return rows<T, DP, 1>(a, type, dev, st, bytes);
-    if (n <= 32) return rows<T, DP, 2>(a, type, dev, st, bytes);
-    return rows<T, DP, 4>(a, type, dev, st, bytes);
+    if constexpr (DP * sizeof(T) < 1024) {   // (64 rows of 1024 bytes in two parts leave no room for tiles)
+        if (n > 32) return rows<T, DP, 4>(a, type, dev, st, bytes);
+    }
+    return rows<T, DP, 2>(a, type, dev, st, bytes);
 }
 
 template <typename T>

@@ -27,7 +27,8 @@ struct Cfg {
     static constexpr int M = 64;                            // rows of a CTA
     static constexpr int CH = DP * ES / 16;                 // pieces of a row
     static constexpr int TILE = KT * DP * ES;
-    static constexpr int SMEM = 2 * TILE + M * DP * ES + KT * 16 + 64;
+    static constexpr int QB = M * DP * ES * (ES == 4 ? 2 : 1);   // binary32: both parts of each
+    static constexpr int SMEM = 2 * TILE + QB + KT * 16 + 64;
     static_assert(KT * 16 >= M * 8 && DP * ES >= 64, "what goes out fits where queries and places were");
     static constexpr int PER_SM = 227 * 1024 / (SMEM + 1024) < 3 ? 227 * 1024 / (SMEM + 1024) : 3;
 };
@@ -39,7 +40,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_any(AttendArgs a, unsigned 
     constexpr int KT = C::KT, M = C::M, ES = C::ES;
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char *ks = smem, *vs = smem + C::TILE, *qs = smem + 2 * C::TILE;
-    longlong2 *info = reinterpret_cast<longlong2 *>(qs + M * DP * ES);   // [KT] element offsets of keys and values
+    longlong2 *info = reinterpret_cast<longlong2 *>(qs + C::QB);   // [KT] element offsets of keys and values
     unsigned *valid = reinterpret_cast<unsigned *>(info + KT);           // [2] bits: the key is there
     u64 *scan = reinterpret_cast<u64 *>(valid + 2);                      // [4]
     const unsigned t = threadIdx.x, lane = t & 31u, warp = t >> 5;
@@ -74,7 +75,16 @@ __global__ void __launch_bounds__(kThreads) k_attend_any(AttendArgs a, unsigned 
                 const bool some = row0 + r < live;
                 const unsigned node = by_group.div(row0 + r), head = h * group + row0 + r - node * group;
                 const T *src = some ? q + node * a.sq[1] + head * a.sq[2] : q;
-                *reinterpret_cast<uint4 *>(qs + piece(M, r, c)) = entries<T>(src, c, dim, some);
+                uint4 v = entries<T>(src, c, dim, some);
+                if constexpr (ES == 4) {
+                    uint4 lo;
+                    split(__uint_as_float(v.x), v.x, lo.x);
+                    split(__uint_as_float(v.y), v.y, lo.y);
+                    split(__uint_as_float(v.z), v.z, lo.z);
+                    split(__uint_as_float(v.w), v.w, lo.w);
+                    *reinterpret_cast<uint4 *>(qs + M * DP * ES + piece(M, r, c)) = lo;
+                }
+                *reinterpret_cast<uint4 *>(qs + piece(M, r, c)) = v;
             }
         }
         float o[DP / 8][4];

@@ -80,31 +80,44 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 // (names what was loaded, so that nothing that reads it is moved before the wait)
-#define KEEP32(v) "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), \
-    "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), \
-    "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), \
-    "+r"(v[30]), "+r"(v[31])
-__device__ __forceinline__ void loaded32(unsigned *v) { asm volatile("" : KEEP32(v)::"memory"); }
+#define KEEP32(v) "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), \
+    "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), \
+    "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), \
+    "+f"(v[30]), "+f"(v[31])
+__device__ __forceinline__ void loaded32(float *v) { asm volatile("" : KEEP32(v)::"memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-#define REGS32(v) "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), \
-    "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), \
-    "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), \
-    "=r"(v[30]), "=r"(v[31])
-#define ARGS32(v) "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), \
-    "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), \
-    "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-
+#define REGS32(v) "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), \
+    "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), \
+    "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), \
+    "=f"(v[30]), "=f"(v[31])
 // 32 columns of a warp's 32 lanes, a thread a lane
-__device__ __forceinline__ void get32(unsigned *v, unsigned at)
+__device__ __forceinline__ void get32(float *v, unsigned at)
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
                  "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];" : REGS32(v) : "r"(at) : "memory");
 }
-__device__ __forceinline__ void put32(unsigned at, const unsigned *v)
+#define ARGS32(v) "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]), \
+    "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), \
+    "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
+__device__ __forceinline__ void put32(unsigned at, const float *v)
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
                  "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::ARGS32(v), "r"(at) : "memory");
+}
+__device__ __forceinline__ void put16(unsigned at, const unsigned *v)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]),
+                 "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(at) : "memory");
+}
+
+// the scores of 64 keys that are not seen
+__device__ __forceinline__ void hide(float *sc, const unsigned *word)
+{
+#pragma unroll
+    for (int k = 0; k < 64; ++k)
+        if (!(word[k / 32] >> (k % 32) & 1u)) sc[k] = -INFINITY;
 }
 
 // bit k of word[k / 32]: the row of node n sees key first + k
@@ -183,7 +196,7 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
     __syncthreads();
     fence_after();
     const unsigned tmem = tail.tmem;
-    // scores of group g (p over them) at column 128 g, outputs at 256 + 128 g
+    // scores of group g at column 128 g (p over the upper half of them), outputs at 256 + 128 g
     unsigned base = 0;         // tiles asked for before this stretch: keys and values in turn
     unsigned stretch = 0;      // stretches before this one
 
@@ -256,7 +269,7 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                     const unsigned va = smem_u32(smem + slot * TILE);
 #pragma unroll
                     for (int k = 0; k < KT / 16; ++k)   // 16 keys: two groups of 8 rows
-                        multiply_t(tmem + 256 + 128 * g, tmem + 128 * g + k * 8, operand(va + k * 2048, KT * 128), product<T>(DP, true),
+                        multiply_t(tmem + 256 + 128 * g, tmem + 128 * g + 64 + k * 8, operand(va + k * 2048, KT * 128), product<T>(DP, true),
                                    i > 1 || k > 0);
                     if (!PAIR || g == 1) commit(empty + 8 * slot);
                     if (i + 2 < steps) keys_times(i + 2);
@@ -318,9 +331,6 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                 if (!ok) break;
                 ++phase;
                 fence_after();
-                unsigned v[KT];
-#pragma unroll
-                for (int i = 0; i < KT / 32; ++i) get32(v + 32 * i, my_s + 32 * i);
                 const bool tail_in = (tile + 1) * KT > (unsigned)s.len;   // nodes, or the end
                 if (tail_in && (!PAIR || g == 0)) {
                     // what stale slots hold is taken out of the values, and what is not finite in a node's: it must
@@ -336,24 +346,29 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                     if (odd) tail.odd = 1;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
-                wait_ld();
-#pragma unroll
-                for (int i = 0; i < KT / 32; ++i) loaded32(v + 32 * i);
-                float *sc = reinterpret_cast<float *>(v);
-                unsigned wrong = 0;
+                unsigned wrong = 0, word[KT / 32] = {};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) wrong |= tail.bad[slot][e];
-                if (tail_in || wrong) {
-                    unsigned word[KT / 32];
-                    seen(a, b, s, node, tile * KT, tail.bad[slot], wrong != 0, shift, word);
+                const bool masked = tail_in || wrong;
+                if (masked) seen(a, b, s, node, tile * KT, tail.bad[slot], wrong != 0, shift, word);
+                // Half of the scores at a time: all 128 of a row do not fit the registers beside the rest, and tensor
+                // memory is read at no cost to speak of.  The upper half stays for what follows.
+                float sc[64], most = -INFINITY;
 #pragma unroll
-                    for (int k = 0; k < KT; ++k)
-                        if (!(word[k / 32] >> (k % 32) & 1u)) sc[k] = -INFINITY;
+                for (int half = 0; half < 2; ++half) {
+                    get32(sc, my_s + 64 * half);
+                    get32(sc + 32, my_s + 64 * half + 32);
+                    wait_ld();
+                    loaded32(sc);
+                    loaded32(sc + 32);
+                    if (masked) hide(sc, word + 2 * half);
+                    float up[4] = {most, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int k = 0; k < 64; k += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) up[e] = fmaxf(up[e], fmaxf(sc[k + e], sc[k + 4 + e]));
+                    most = fmaxf(fmaxf(up[0], up[1]), fmaxf(up[2], up[3]));
                 }
-                float up[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int k = 0; k < KT; ++k) up[k & 3] = fmaxf(up[k & 3], sc[k]);
-                const float most = fmaxf(fmaxf(up[0], up[1]), fmaxf(up[2], up[3]));
                 const bool rise = most > -INFINITY && (raw_none || (most - ref) * a.c2 > kRise);
                 if (__any_sync(0xffffffffu, rise)) {
                     const float now = rise ? most * a.c2 : top;
@@ -367,31 +382,44 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                     if (j >= 2 || (PAIR && j >= 1)) {   // there are outputs
 #pragma unroll
                         for (int i = 0; i < DP / 32; ++i) {
-                            unsigned x[32];
+                            float x[32];
                             get32(x, my_o + 32 * i);
                             wait_ld();
                             loaded32(x);
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * keep);
+                            for (int k = 0; k < 32; ++k) x[k] *= keep;
                             put32(my_o + 32 * i, x);
                         }
                     }
                 }
                 const float off = raw_none ? 0.0f : top;
-                float add[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                const F2 c2 = {a.c2, a.c2}, less = {-off, -off};
+                F2 add[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
 #pragma unroll
-                for (int i = 0; i < KT / 64; ++i) {
-                    unsigned p[32];
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const float x = ex2(fmaf(sc[64 * i + 2 * k], a.c2, -off)), y = ex2(fmaf(sc[64 * i + 2 * k + 1], a.c2, -off));
-                        add[(2 * k) & 3] += x;
-                        add[(2 * k + 1) & 3] += y;
-                        p[k] = pack2<T>(x, y);
+                for (int half = 1; half >= 0; --half) {
+                    if (half == 0) {
+                        get32(sc, my_s);
+                        get32(sc + 32, my_s + 32);
+                        wait_ld();
+                        loaded32(sc);
+                        loaded32(sc + 32);
+                        if (masked) hide(sc, word);
                     }
-                    put32(my_s + 32 * i, p);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        unsigned p[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            F2 x = fma2(F2{sc[32 * i + 2 * k], sc[32 * i + 2 * k + 1]}, c2, less);
+                            x.x = ex2(x.x);
+                            x.y = ex2(x.y);
+                            add[k & 1] = add[k & 1] + x;
+                            p[k] = pack2<T>(x.x, x.y);
+                        }
+                        put16(my_s + 64 + 32 * half + 16 * i, p);
+                    }
                 }
-                l += (add[0] + add[1]) + (add[2] + add[3]);
+                l += (add[0].x + add[1].x) + (add[0].y + add[1].y);
                 wait_st();
                 fence_before();
                 __syncwarp();
@@ -430,21 +458,20 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
 #pragma unroll 1
             for (int i = 0; i < HALF; ++i) {
                 const int c = (PAIR ? 0 : g * HALF) + i;
-                unsigned x[32];
-                get32(x, o_at + 32 * c);
+                float o[32];
+                get32(o, o_at + 32 * c);
                 if (both) {
-                    unsigned y[32];
+                    float y[32];
                     get32(y, o_at + 128 + 32 * c);
                     wait_ld();
-                    loaded32(x);
+                    loaded32(o);
                     loaded32(y);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f0 + __uint_as_float(y[k]) * f1);
+                    for (int k = 0; k < 32; ++k) o[k] = o[k] * f0 + y[k] * f1;
                 } else {
                     wait_ld();
-                    loaded32(x);
+                    loaded32(o);
                 }
-                float *o = reinterpret_cast<float *>(x);
                 if (odd && real) {   // what was taken out of the values, for the rows that see it (rare: nothing here is fast)
                     const unsigned first = max(w.tile0 * KT, (unsigned)s.len), end = min(w.tile1 * KT, (unsigned)s.total);
                     for (unsigned key = first; key < end; ++key) {
