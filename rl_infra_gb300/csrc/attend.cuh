@@ -323,14 +323,26 @@ __device__ __forceinline__ void load_box(unsigned dst, const CUtensorMap *map, c
                  ::"r"(dst), "l"(map), "r"(d), "r"(c1), "r"(c2), "r"(c3), "r"(bar) : "memory");
 }
 
+// One thread of the warp.  (Under a choice like `lane == 0` the compiler does not know that one thread is left: it then
+// goes through the active lanes for instructions that take registers of the whole warp, and the addresses of the tensor
+// cores' operands came out wrong.)
+__device__ __forceinline__ bool chosen()
+{
+    unsigned one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+
 // What one warp asks for, tile after tile: boxes of 128 bytes by `1 << shift` slots of a page (a power of 2 that
 // divides the page), so that a row's 16-byte pieces lie turned by its number modulo 8.  What lies outside the tensor
-// (entries past the head's, a page that does not exist) comes as zeros.
+// (entries past the head's, a page that does not exist) comes as zeros.  The lanes look up the pages of a tile, one
+// thread asks for its boxes.
 template <int KT>
 struct Loader {
     static constexpr int EN = (KT + 31) / 32;
     unsigned shift;            // log2 of the rows of a box
-    int page[EN], slot[EN];    // of this lane's boxes of the tile that is looked up
+    int *boxes;                // [KT] their pages, in shared memory
+    int page[EN];              // of this lane's boxes of the tile that is looked up
 
     __device__ __forceinline__ void look_up(const AttendArgs &a, unsigned b, const Span &s, unsigned tile)
     {
@@ -338,45 +350,44 @@ struct Loader {
 #pragma unroll
         for (int e = 0; e < EN; ++e) {
             const unsigned i = lane + 32 * e, key = tile * KT + (i << shift);
-            page[e] = -1;
-            slot[e] = 0;
-            if ((i << shift) < KT && key < (unsigned)s.total) {
-                const unsigned pg = a.c.page.div(key);
-                slot[e] = (int)(key - pg * a.c.page.d);
-                page[e] = a.c.table[b * a.c.st + pg];
-            }
+            page[e] = (int)a.c.pages;
+            if ((i << shift) < KT && key < (unsigned)s.total) page[e] = a.c.table[b * a.c.st + a.c.page.div(key)];
         }
     }
 
-    // which boxes have no page: a bit for each in `bad`
-    __device__ __forceinline__ void judge(const AttendArgs &a, const Span &s, unsigned tile, unsigned *bad, bool tell)
+    // hands the boxes to the thread that asks; those without a page as bits of `bad`
+    __device__ __forceinline__ void hand(const AttendArgs &a, const Span &s, unsigned tile, unsigned *bad, bool tell)
     {
         const unsigned lane = threadIdx.x & 31u;
         bool any = false;
+        __syncwarp();          // the boxes of the tile before have been read
 #pragma unroll
         for (int e = 0; e < EN; ++e) {
             const unsigned i = lane + 32 * e;
-            const bool wanted = (i << shift) < KT && tile * KT + (i << shift) < (unsigned)s.total;
-            const bool wrong = wanted && (unsigned)page[e] >= a.c.pages;
+            const bool wrong = (unsigned)page[e] >= a.c.pages && (i << shift) < KT && tile * KT + (i << shift) < (unsigned)s.total;
             const unsigned bits = __ballot_sync(0xffffffffu, wrong);
             if (lane == 0) bad[e] = bits;
             any |= wrong;
-            if (wrong || !wanted) page[e] = (int)a.c.pages;
+            if ((i << shift) < KT) boxes[i] = wrong ? (int)a.c.pages : page[e];
         }
         if (any && tell && a.c.status) atomicOr(a.c.status, PER_DEVFLAG_BAD_INDEX);
+        __syncwarp();
     }
 
-    // one array's tile to `to`: [half][KT][128 bytes].  The bytes are expected by the barrier already.
-    __device__ __forceinline__ void request(const CUtensorMap *map, const unsigned char *at, unsigned h, unsigned to, unsigned halves,
-                                            unsigned per_half, unsigned bar)
+    // one array's tile to `to`: [half][KT][128 bytes].  By the thread that asks.
+    __device__ __forceinline__ void request(const AttendArgs &a, const CUtensorMap *map, const unsigned char *at, unsigned tile, unsigned h,
+                                            unsigned to, unsigned halves, unsigned per_half, unsigned bar) const
     {
-        const unsigned lane = threadIdx.x & 31u;
-#pragma unroll
-        for (int e = 0; e < EN; ++e) {
-            const unsigned i = lane + 32 * e;
-            if ((i << shift) >= KT) continue;
+        bar_expect(bar, halves * KT * 128);
+        unsigned slot = tile * KT - a.c.page.div(tile * KT) * a.c.page.d;   // boxes follow one another through a page
+#pragma unroll 1
+        for (unsigned i = 0; i << shift < KT; ++i) {
+            const int page = boxes[i];
+#pragma unroll 1
             for (unsigned half = 0; half < halves; ++half)
-                load_box(to + half * KT * 128 + (i << shift) * 128, map, at, bar, half * per_half, slot[e], h, page[e]);
+                load_box(to + half * KT * 128 + (i << shift) * 128, map, at, bar, half * per_half, (int)slot, h, page);
+            slot += 1u << shift;
+            if (slot == a.c.page.d) slot = 0;
         }
     }
 };

@@ -4,6 +4,7 @@
 #include "attend.cuh"
 
 #include <cstring>
+#include <type_traits>
 
 namespace gbper {
 namespace attend {
@@ -216,26 +217,44 @@ __device__ __forceinline__ void give_back(const AttendArgs &a, unsigned b, const
         }
 }
 
-// Takes what is not finite out of 16 bytes; whether there was any.
+// Takes what is not finite (all bits of the exponent set) out of 16 bytes; whether there was any.
 template <typename T>
 __device__ __forceinline__ bool take_out(uint4 *at)
 {
-    Pack<T> p;
-    p.raw = *at;
-    float f[Pack<T>::N];
-    p.unpack(f);
+    constexpr unsigned E = sizeof(T) == 4 ? 0x7f800000u : std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
+    const uint4 v = *at;
+    unsigned w[4] = {v.x, v.y, v.z, v.w};
     bool any = false;
 #pragma unroll
-    for (int i = 0; i < Pack<T>::N; ++i)
-        if (!finite(f[i])) {
-            f[i] = 0.0f;
-            any = true;
+    for (int i = 0; i < 4; ++i) {
+        unsigned gone = 0;
+        if (sizeof(T) == 4) {
+            if ((w[i] & E) == E) gone = ~0u;
+        } else {
+            if ((w[i] & E & 0xffffu) == (E & 0xffffu)) gone |= 0xffffu;
+            if ((w[i] & E & 0xffff0000u) == (E & 0xffff0000u)) gone |= 0xffff0000u;
         }
-    if (any) {
-        p.pack(f);
-        *at = p.raw;
+        any |= gone != 0;
+        w[i] &= ~gone;
     }
+    if (any) *at = make_uint4(w[0], w[1], w[2], w[3]);
     return any;
+}
+
+// The values of the sequence's end, in the tile at `vs` whose first key is `first`: zeros where there is no key, and what
+// is not finite in a node's taken out.  Whether there was any.
+template <typename T>
+__device__ __forceinline__ bool clean(unsigned char *vs, unsigned kt, unsigned first, const Span &s, unsigned pieces, unsigned t, unsigned threads)
+{
+    const unsigned r0 = (unsigned)s.len > first ? (unsigned)s.len - first : 0;
+    bool odd = false;
+    for (unsigned u = t; u < (kt - r0) * pieces; u += threads) {
+        const unsigned r = r0 + u / pieces, c = u % pieces;
+        uint4 *at = reinterpret_cast<uint4 *>(vs + piece(kt, r, c));
+        if (first + r >= (unsigned)s.total) *at = make_uint4(0, 0, 0, 0);
+        else odd |= take_out<T>(at);
+    }
+    return odd;
 }
 
 }  // namespace attend

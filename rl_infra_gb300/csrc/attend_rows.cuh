@@ -20,6 +20,17 @@ namespace {
 constexpr int kWarps = 4;                  // of them that compute
 constexpr int kThreads = kWarps * 32 + 32;
 
+// What lies behind the tiles and the queries: barriers, and what goes from warp to warp.
+template <int KT, int ML>
+struct Tail {
+    u64 full[12], empty[6], meet;   // full: keys, then values
+    u64 scan[kThreads / 32];
+    unsigned bad[6][KT / 32];
+    float ml[ML][2];           // maxima and sums that the warps hand over
+    int boxes[KT];
+    unsigned dead, odd;        // odd: the number of the last tile that something was taken out of
+};
+
 template <typename T, int DP, int WR>
 struct Cfg {
     static constexpr int ES = (int)sizeof(T);
@@ -32,7 +43,8 @@ struct Cfg {
     static constexpr int JOIN = WK == 4 ? 2 * 16 * DP * 4 : WK == 2 ? M * DP * 4 : 0;   // what the warps hand over
     static constexpr int QB = M * DP * ES * (ES == 4 ? 2 : 1);                          // the queries lie there before
     static constexpr int AREA = QB > JOIN ? QB : JOIN;
-    static constexpr int TAIL = 1024;
+    typedef Tail<KT, WK == 1 ? M : 32> End;
+    static constexpr int TAIL = ((int)sizeof(End) + 63) / 64 * 64;
     static constexpr int HALF_SM = 228 * 1024 / 2 - 1024;
     static constexpr int WHOLE_SM = 227 * 1024;
     static constexpr int PER_SM = (HALF_SM - AREA - TAIL) / STAGE >= (ES == 4 ? 2 : 3) ? 2 : 1;
@@ -42,15 +54,6 @@ struct Cfg {
     static_assert(ST >= 2, "fits");
     static_assert(ES == 4 || KW % 16 == 0, "whole steps of the matrix instruction");
 };
-
-struct Tail {
-    u64 full[6], empty[6], meet;
-    u64 scan[kThreads / 32];
-    unsigned bad[6][4];
-    float ml[64][2];           // maxima and sums that the warps hand over
-    unsigned dead, odd;        // odd: the number of the last tile that something was taken out of
-};
-static_assert(sizeof(Tail) <= 1024, "");
 
 // two and four words at the same place of the shared memory of the cluster's CTA `rank`
 __device__ __forceinline__ float2 far2(const float *p, unsigned rank)
@@ -75,7 +78,7 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
     constexpr int KT = C::KT, KW = C::KW, WK = C::WK, M = C::M, ST = C::ST, ES = C::ES;
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char *area = smem + ST * C::STAGE;
-    Tail &tail = *reinterpret_cast<Tail *>(area + C::AREA);
+    typename C::End &tail = *reinterpret_cast<typename C::End *>(area + C::AREA);
     volatile unsigned *dead = &tail.dead;
     const unsigned t = threadIdx.x, lane = t & 31u, warp = t >> 5;
     const unsigned cta = blockIdx.x, unit = share ? cta / share : cta, team = unit / row_tiles, rt = unit - team * row_tiles;
@@ -87,6 +90,7 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
     if (t == 0) {
         for (int i = 0; i < ST; ++i) {
             bar_init(full + 8 * i, 1);
+            bar_init(full + 8 * (ST + i), 1);
             bar_init(empty + 8 * i, kWarps);
         }
         bar_init(smem_u32(&tail.meet), kWarps);
@@ -113,8 +117,10 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
     if (warp == kWarps) {   // the warp that asks for tiles
         Loader<KT> load;
         load.shift = shift;
+        load.boxes = tail.boxes;
         unsigned asked = 0;
         bool ok = true;
+        const bool one = chosen();
         while (ok && next()) {
             if (row0 >= (unsigned)w.s.count * group) continue;
             load.look_up(a, w.b, w.s, w.tile0);
@@ -122,12 +128,11 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                 if (asked >= (unsigned)ST) ok = __all_sync(0xffffffffu, bar_wait(empty + 8 * st, phase ^ 1, dead));
                 if (!ok) break;
                 const unsigned ks = smem_u32(smem + st * C::STAGE), bar = full + 8 * st;
-                load.judge(a, w.s, tile, tail.bad[st], rt == 0 && w.h == 0);
-                __syncwarp();
-                if (lane == 0) bar_expect(bar, halves * KT * 128 * 2);
-                __syncwarp();
-                load.request(&maps.k, maps.k_at, w.h, ks, halves, C::PER_HALF, bar);
-                load.request(&maps.v, maps.v_at, w.h, ks + KT * DP * ES, halves, C::PER_HALF, bar);
+                load.hand(a, w.s, tile, tail.bad[st], rt == 0 && w.h == 0);
+                if (one) {
+                    load.request(a, &maps.k, maps.k_at, tile, w.h, ks, halves, C::PER_HALF, bar);
+                    load.request(a, &maps.v, maps.v_at, tile, w.h, ks + KT * DP * ES, halves, C::PER_HALF, bar + 8 * ST);
+                }
                 ++asked;
                 if (++st == ST) {
                     st = 0;
@@ -140,6 +145,7 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
             for (unsigned i = asked > (unsigned)ST ? asked - ST : 0; i < asked; ++i) {
                 unsigned none = 0;
                 bar_wait(full + 8 * (i % ST), i / ST & 1, &none);
+                bar_wait(full + 8 * (ST + i % ST), i / ST & 1, &none);
             }
         }
     } else {
@@ -213,12 +219,8 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                 bool odd = false;
                 ++tiles_done;
                 if (tail_in) {
-                    for (unsigned u = t; u < KT * halves * 8; u += kWarps * 32) {
-                        const unsigned r = u % KT, key = tile * KT + r;
-                        uint4 *at = reinterpret_cast<uint4 *>(vs + piece(KT, r, u / KT));
-                        if (key >= (unsigned)s.total) *at = make_uint4(0, 0, 0, 0);
-                        else if (key >= (unsigned)s.len) odd |= take_out<T>(at);
-                    }
+                    if (!(ok = __all_sync(0xffffffffu, bar_wait(full + 8 * (ST + st), phase, dead)))) break;
+                    odd = clean<T>(vs, KT, tile * KT, s, halves * 8, t, kWarps * 32);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the next copy comes after these stores
                     if (odd) tail.odd = tiles_done;
                     if (!(ok = meet(dead))) break;
@@ -242,6 +244,7 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                         }
                 }
                 soften<DP, KW>(sc, top, sum, o);
+                if (!tail_in && !(ok = __all_sync(0xffffffffu, bar_wait(full + 8 * (ST + st), phase, dead)))) break;
                 values<T, DP, KW>(o, sc, vs, KT, key0, steps);
                 if (odd)
                     for (unsigned r = key0; r < key0 + KW; ++r) {

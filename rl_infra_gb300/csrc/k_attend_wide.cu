@@ -43,6 +43,7 @@ struct Tail {
     u64 full[10], empty[10], q_ready, s_full[2], p_ready[2], o_full[2], meet, last;
     u64 scan[kThreads / 32];
     unsigned bad[10][4];
+    int boxes[KT];
     float ml[2][128][2];
     unsigned dead, odd, tmem;
 };
@@ -105,19 +106,21 @@ __device__ __forceinline__ void put32(unsigned at, const float *v)
     asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
                  "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::ARGS32(v), "r"(at) : "memory");
 }
-__device__ __forceinline__ void put16(unsigned at, const unsigned *v)
+#define WORDS32(v) "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), \
+    "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), \
+    "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+__device__ __forceinline__ void put32(unsigned at, const unsigned *v)
 {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(v[0]),
-                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]),
-                 "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(at) : "memory");
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+                 "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::WORDS32(v), "r"(at) : "memory");
 }
 
-// the scores of 64 keys that are not seen
-__device__ __forceinline__ void hide(float *sc, const unsigned *word)
+// the scores of 32 keys that are not seen
+__device__ __forceinline__ void hide(float *sc, unsigned word)
 {
 #pragma unroll
-    for (int k = 0; k < 64; ++k)
-        if (!(word[k / 32] >> (k % 32) & 1u)) sc[k] = -INFINITY;
+    for (int k = 0; k < 32; ++k)
+        if (!(word >> k & 1u)) sc[k] = -INFINITY;
 }
 
 // bit k of word[k / 32]: the row of node n sees key first + k
@@ -196,32 +199,33 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
     __syncthreads();
     fence_after();
     const unsigned tmem = tail.tmem;
-    // scores of group g at column 128 g (p over the upper half of them), outputs at 256 + 128 g
+    // scores of group g at column 128 g (p over them), outputs at 256 + 128 g
     unsigned base = 0;         // tiles asked for before this stretch: keys and values in turn
     unsigned stretch = 0;      // stretches before this one
 
     if (warp == 8) {           // the warp that asks for tiles
         Loader<KT> load;
         load.shift = shift;
+        load.boxes = tail.boxes;
         unsigned asked = 0;
         bool ok = true;
+        const bool one = chosen();
         while (ok && w.next(a)) {
             if (row0 >= (unsigned)w.s.count * group) continue;
             load.look_up(a, w.b, w.s, w.tile0);
-            for (unsigned tile = w.tile0; ok && tile < w.tile1; ++tile) {
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    const unsigned slot = asked % ST, bar = full + 8 * slot;
-                    if (asked >= (unsigned)ST) ok = __all_sync(0xffffffffu, bar_wait(empty + 8 * slot, (asked / ST - 1) & 1, dead));
-                    if (!ok) break;
-                    load.judge(a, w.s, tile, tail.bad[slot], kv == 0 && rt == 0 && w.h == 0);
-                    __syncwarp();
-                    if (lane == 0) bar_expect(bar, halves * KT * 128);
-                    __syncwarp();
-                    if (kv == 0) load.request(&maps.k, maps.k_at, w.h, smem_u32(smem + slot * TILE), halves, 64, bar);
-                    else load.request(&maps.v, maps.v_at, w.h, smem_u32(smem + slot * TILE), halves, 64, bar);
-                    ++asked;
+            for (unsigned tile = w.tile0; tile < w.tile1; ++tile) {
+                const unsigned k_slot = asked % ST, v_slot = (asked + 1) % ST;
+                // (bits of what has no page lie with the values, which are given up after the scores have been read)
+                if (asked + 1 >= (unsigned)ST)
+                    ok = __all_sync(0xffffffffu, bar_wait(empty + 8 * v_slot, ((asked + 1) / ST - 1) & 1, dead));
+                if (ok && asked >= (unsigned)ST) ok = __all_sync(0xffffffffu, bar_wait(empty + 8 * k_slot, (asked / ST - 1) & 1, dead));
+                if (!ok) break;
+                load.hand(a, w.s, tile, tail.bad[v_slot], rt == 0 && w.h == 0);
+                if (one) {
+                    load.request(a, &maps.k, maps.k_at, tile, w.h, smem_u32(smem + k_slot * TILE), halves, 64, full + 8 * k_slot);
+                    load.request(a, &maps.v, maps.v_at, tile, w.h, smem_u32(smem + v_slot * TILE), halves, 64, full + 8 * v_slot);
                 }
+                asked += 2;
                 if (tile + 1 < w.tile1) load.look_up(a, w.b, w.s, tile + 1);
             }
         }
@@ -232,11 +236,7 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
             }
         }
     } else if (warp == 9) {    // the thread that issues the products
-        // chosen by elect.sync: under `lane == 0` the compiler does not know that one thread is left, and the operands'
-        // addresses, which the instruction takes from registers of the whole warp, came out wrong
-        unsigned one;
-        asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
-        if (one) {
+        if (chosen()) {
             const unsigned ksteps = (dim + 15) / 16, q_at = smem_u32(qs);
             unsigned ready[2] = {0, 0};   // phases of p_ready
             bool ok = true;
@@ -269,7 +269,7 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                     const unsigned va = smem_u32(smem + slot * TILE);
 #pragma unroll
                     for (int k = 0; k < KT / 16; ++k)   // 16 keys: two groups of 8 rows
-                        multiply_t(tmem + 256 + 128 * g, tmem + 128 * g + 64 + k * 8, operand(va + k * 2048, KT * 128), product<T>(DP, true),
+                        multiply_t(tmem + 256 + 128 * g, tmem + 128 * g + k * 8, operand(va + k * 2048, KT * 128), product<T>(DP, true),
                                    i > 1 || k > 0);
                     if (!PAIR || g == 1) commit(empty + 8 * slot);
                     if (i + 2 < steps) keys_times(i + 2);
@@ -335,15 +335,7 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                 if (tail_in && (!PAIR || g == 0)) {
                     // what stale slots hold is taken out of the values, and what is not finite in a node's: it must
                     // reach only the rows that see it
-                    bool odd = false;
-                    unsigned char *vs = smem + slot * TILE;
-                    for (unsigned u = r; u < KT * halves * 8; u += 128) {
-                        const unsigned x = u % KT, key = tile * KT + x;
-                        uint4 *at = reinterpret_cast<uint4 *>(vs + piece(KT, x, u / KT));
-                        if (key >= (unsigned)s.total) *at = make_uint4(0, 0, 0, 0);
-                        else if (key >= (unsigned)s.len) odd |= take_out<T>(at);
-                    }
-                    if (odd) tail.odd = 1;
+                    if (clean<T>(smem + slot * TILE, KT, tile * KT, s, halves * 8, r, 128)) tail.odd = 1;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
                 unsigned wrong = 0, word[KT / 32] = {};
@@ -351,26 +343,39 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                 for (int e = 0; e < 4; ++e) wrong |= tail.bad[slot][e];
                 const bool masked = tail_in || wrong;
                 if (masked) seen(a, b, s, node, tile * KT, tail.bad[slot], wrong != 0, shift, word);
-                // Half of the scores at a time: all 128 of a row do not fit the registers beside the rest, and tensor
-                // memory is read at no cost to speak of.  The upper half stays for what follows.
-                float sc[64], most = -INFINITY;
+                // p against the maximum so far, a quarter of the row at a time, and the row's maximum on the way; once more
+                // where that has risen (the scores are still there: p is written when it stands)
+                unsigned p[KT / 2];
+                F2 add[2];
+                for (;;) {
+                    const float off = raw_none ? 0.0f : top;
+                    const F2 c2 = {a.c2, a.c2}, less = {-off, -off};
+                    float most = -INFINITY;
+                    add[0] = add[1] = F2{0.0f, 0.0f};
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    get32(sc, my_s + 64 * half);
-                    get32(sc + 32, my_s + 64 * half + 32);
-                    wait_ld();
-                    loaded32(sc);
-                    loaded32(sc + 32);
-                    if (masked) hide(sc, word + 2 * half);
-                    float up[4] = {most, -INFINITY, -INFINITY, -INFINITY};
+                    for (int i = 0; i < KT / 32; ++i) {
+                        float sc[32];
+                        get32(sc, my_s + 32 * i);
+                        wait_ld();
+                        loaded32(sc);
+                        if (masked) hide(sc, word[i]);
+                        float up[4] = {most, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int k = 0; k < 64; k += 8)
+                        for (int k = 0; k < 32; k += 8)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) up[e] = fmaxf(up[e], fmaxf(sc[k + e], sc[k + 4 + e]));
-                    most = fmaxf(fmaxf(up[0], up[1]), fmaxf(up[2], up[3]));
-                }
-                const bool rise = most > -INFINITY && (raw_none || (most - ref) * a.c2 > kRise);
-                if (__any_sync(0xffffffffu, rise)) {
+                            for (int e = 0; e < 4; ++e) up[e] = fmaxf(up[e], fmaxf(sc[k + e], sc[k + 4 + e]));
+                        most = fmaxf(fmaxf(up[0], up[1]), fmaxf(up[2], up[3]));
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            F2 x = fma2(F2{sc[2 * k], sc[2 * k + 1]}, c2, less);
+                            x.x = ex2(x.x);
+                            x.y = ex2(x.y);
+                            add[k & 1] = add[k & 1] + x;
+                            p[16 * i + k] = pack2<T>(x.x, x.y);
+                        }
+                    }
+                    const bool rise = most > -INFINITY && (raw_none || (most - ref) * a.c2 > kRise);
+                    if (!__any_sync(0xffffffffu, rise)) break;
                     const float now = rise ? most * a.c2 : top;
                     const float keep = rise ? (raw_none ? 0.0f : ex2(top - now)) : 1.0f;
                     if (rise) {
@@ -380,7 +385,7 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                     }
                     l *= keep;
                     if (j >= 2 || (PAIR && j >= 1)) {   // there are outputs
-#pragma unroll
+#pragma unroll 1
                         for (int i = 0; i < DP / 32; ++i) {
                             float x[32];
                             get32(x, my_o + 32 * i);
@@ -392,33 +397,8 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                         }
                     }
                 }
-                const float off = raw_none ? 0.0f : top;
-                const F2 c2 = {a.c2, a.c2}, less = {-off, -off};
-                F2 add[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
-#pragma unroll
-                for (int half = 1; half >= 0; --half) {
-                    if (half == 0) {
-                        get32(sc, my_s);
-                        get32(sc + 32, my_s + 32);
-                        wait_ld();
-                        loaded32(sc);
-                        loaded32(sc + 32);
-                        if (masked) hide(sc, word);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        unsigned p[16];
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            F2 x = fma2(F2{sc[32 * i + 2 * k], sc[32 * i + 2 * k + 1]}, c2, less);
-                            x.x = ex2(x.x);
-                            x.y = ex2(x.y);
-                            add[k & 1] = add[k & 1] + x;
-                            p[k] = pack2<T>(x.x, x.y);
-                        }
-                        put16(my_s + 64 + 32 * half + 16 * i, p);
-                    }
-                }
+                put32(my_s, p);
+                put32(my_s + 32, p + 32);
                 l += (add[0].x + add[1].x) + (add[0].y + add[1].y);
                 wait_st();
                 fence_before();
