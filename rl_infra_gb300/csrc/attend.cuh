@@ -341,7 +341,7 @@ template <int KT>
 struct Loader {
     static constexpr int EN = (KT + 31) / 32;
     unsigned shift;            // log2 of the rows of a box
-    int *boxes;                // [KT] their pages, in shared memory
+    int *boxes;                // [KT] their pages, in shared memory (16-byte aligned)
     int page[EN];              // of this lane's boxes of the tile that is looked up
 
     __device__ __forceinline__ void look_up(const AttendArgs &a, unsigned b, const Span &s, unsigned tile)
@@ -374,20 +374,28 @@ struct Loader {
         __syncwarp();
     }
 
-    // one array's tile to `to`: [half][KT][128 bytes].  By the thread that asks.
+    // one array's tile to `to`: [half][KT][128 bytes], at most HN halves.  By the thread that asks.  (Four boxes at a time,
+    // so that what one waits for does not keep the next.)
+    template <int HN>
     __device__ __forceinline__ void request(const AttendArgs &a, const CUtensorMap *map, const unsigned char *at, unsigned tile, unsigned h,
                                             unsigned to, unsigned halves, unsigned per_half, unsigned bar) const
     {
         bar_expect(bar, halves * KT * 128);
-        unsigned slot = tile * KT - a.c.page.div(tile * KT) * a.c.page.d;   // boxes follow one another through a page
-#pragma unroll 1
-        for (unsigned i = 0; i << shift < KT; ++i) {
-            const int page = boxes[i];
-#pragma unroll 1
-            for (unsigned half = 0; half < halves; ++half)
-                load_box(to + half * KT * 128 + (i << shift) * 128, map, at, bar, half * per_half, (int)slot, h, page);
-            slot += 1u << shift;
-            if (slot == a.c.page.d) slot = 0;
+        const unsigned rows = 1u << shift, size = a.c.page.d;
+        unsigned slot = tile * KT - a.c.page.div(tile * KT) * size;   // boxes follow one another through a page
+        for (unsigned r = 0; r < KT; r += 4 * rows) {
+            const int4 four = *reinterpret_cast<const int4 *>(boxes + (r >> shift));
+            const int page[4] = {four.x, four.y, four.z, four.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (e > 0 && r + e * rows >= KT) break;
+#pragma unroll
+                for (int half = 0; half < HN; ++half)
+                    if (half < (int)halves)
+                        load_box(to + half * KT * 128 + (r + e * rows) * 128, map, at, bar, half * per_half, (int)slot, h, page[e]);
+                slot += rows;
+                if (slot == size) slot = 0;
+            }
         }
     }
 };

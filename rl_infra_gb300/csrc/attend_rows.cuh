@@ -27,7 +27,7 @@ struct Tail {
     u64 scan[kThreads / 32];
     unsigned bad[6][KT / 32];
     float ml[ML][2];           // maxima and sums that the warps hand over
-    int boxes[KT];
+    alignas(16) int boxes[KT];
     unsigned dead, odd;        // odd: the number of the last tile that something was taken out of
 };
 
@@ -130,8 +130,8 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                 const unsigned ks = smem_u32(smem + st * C::STAGE), bar = full + 8 * st;
                 load.hand(a, w.s, tile, tail.bad[st], rt == 0 && w.h == 0);
                 if (one) {
-                    load.request(a, &maps.k, maps.k_at, tile, w.h, ks, halves, C::PER_HALF, bar);
-                    load.request(a, &maps.v, maps.v_at, tile, w.h, ks + KT * DP * ES, halves, C::PER_HALF, bar + 8 * ST);
+                    load.template request<DP * ES / 128>(a, &maps.k, maps.k_at, tile, w.h, ks, halves, C::PER_HALF, bar);
+                    load.template request<DP * ES / 128>(a, &maps.v, maps.v_at, tile, w.h, ks + KT * DP * ES, halves, C::PER_HALF, bar + 8 * ST);
                 }
                 ++asked;
                 if (++st == ST) {
@@ -172,25 +172,35 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
             // the queries, zero where there is none
             if (!(ok = meet(dead))) break;
             {
-                constexpr unsigned CH = DP * ES / 16;
+                // eight requests at a time, so that their latencies overlap
+                constexpr unsigned CH = DP * ES / 16, ALL = M * CH / (kWarps * 32), EACH = ALL < 8 ? ALL : 8;
                 const T *q = static_cast<const T *>(a.q) + b * a.sq[0];
-                for (unsigned u = t; u < M * CH; u += kWarps * 32) {
-                    const unsigned r = u / CH, c = u % CH;
-                    const bool some = row0 + r < live;
-                    const unsigned node = by_group.div(row0 + r), head = h * group + row0 + r - node * group;
-                    const T *src = some ? q + node * a.sq[1] + head * a.sq[2] : q;
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (!a.qvec) v = entries<T>(src, c, dim, some);
-                    else if (some && c * 16 < dim * ES) v = *reinterpret_cast<const uint4 *>(src + c * (16 / ES));
-                    if constexpr (ES == 4) {   // both parts of each
-                        uint4 lo;
-                        split(__uint_as_float(v.x), v.x, lo.x);
-                        split(__uint_as_float(v.y), v.y, lo.y);
-                        split(__uint_as_float(v.z), v.z, lo.z);
-                        split(__uint_as_float(v.w), v.w, lo.w);
-                        *reinterpret_cast<uint4 *>(area + M * DP * ES + piece(M, r, c)) = lo;
+#pragma unroll 1
+                for (unsigned u0 = 0; u0 < ALL; u0 += EACH) {
+                    uint4 v[EACH];
+#pragma unroll
+                    for (unsigned i = 0; i < EACH; ++i) {
+                        const unsigned u = t + (u0 + i) * kWarps * 32, r = u / CH, c = u % CH;
+                        const bool some = row0 + r < live;
+                        const unsigned node = by_group.div(row0 + r), head = h * group + row0 + r - node * group;
+                        const T *src = some ? q + node * a.sq[1] + head * a.sq[2] : q;
+                        v[i] = make_uint4(0, 0, 0, 0);
+                        if (!a.qvec) v[i] = entries<T>(src, c, dim, some);
+                        else if (some && c * 16 < dim * ES) v[i] = *reinterpret_cast<const uint4 *>(src + c * (16 / ES));
                     }
-                    *reinterpret_cast<uint4 *>(area + piece(M, r, c)) = v;
+#pragma unroll
+                    for (unsigned i = 0; i < EACH; ++i) {
+                        const unsigned u = t + (u0 + i) * kWarps * 32, r = u / CH, c = u % CH;
+                        if constexpr (ES == 4) {   // both parts of each
+                            uint4 lo;
+                            split(__uint_as_float(v[i].x), v[i].x, lo.x);
+                            split(__uint_as_float(v[i].y), v[i].y, lo.y);
+                            split(__uint_as_float(v[i].z), v[i].z, lo.z);
+                            split(__uint_as_float(v[i].w), v[i].w, lo.w);
+                            *reinterpret_cast<uint4 *>(area + M * DP * ES + piece(M, r, c)) = lo;
+                        }
+                        *reinterpret_cast<uint4 *>(area + piece(M, r, c)) = v[i];
+                    }
                 }
             }
             float o[DP / 8][4];

@@ -43,7 +43,7 @@ struct Tail {
     u64 full[10], empty[10], q_ready, s_full[2], p_ready[2], o_full[2], meet, last;
     u64 scan[kThreads / 32];
     unsigned bad[10][4];
-    int boxes[KT];
+    alignas(16) int boxes[KT];
     float ml[2][128][2];
     unsigned dead, odd, tmem;
 };
@@ -222,8 +222,8 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                 if (!ok) break;
                 load.hand(a, w.s, tile, tail.bad[v_slot], rt == 0 && w.h == 0);
                 if (one) {
-                    load.request(a, &maps.k, maps.k_at, tile, w.h, smem_u32(smem + k_slot * TILE), halves, 64, full + 8 * k_slot);
-                    load.request(a, &maps.v, maps.v_at, tile, w.h, smem_u32(smem + v_slot * TILE), halves, 64, full + 8 * v_slot);
+                    load.template request<DP / 64>(a, &maps.k, maps.k_at, tile, w.h, smem_u32(smem + k_slot * TILE), halves, 64, full + 8 * k_slot);
+                    load.template request<DP / 64>(a, &maps.v, maps.v_at, tile, w.h, smem_u32(smem + v_slot * TILE), halves, 64, full + 8 * v_slot);
                 }
                 asked += 2;
                 if (tile + 1 < w.tile1) load.look_up(a, w.b, w.s, tile + 1);
@@ -304,17 +304,27 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
             if (w.tile0 == 0 && w.tile1 < w.n_tiles && t == 0) w.note(record, team);
             if (row0 >= live) continue;
             {                  // the queries, zero where there is none
-                constexpr unsigned CH = DP / 8;
+                // eight requests at a time, so that their latencies overlap
+                constexpr unsigned CH = DP / 8, ALL = M * CH / (kGroups * 128), EACH = ALL < 8 ? ALL : 8;
                 const T *q = static_cast<const T *>(a.q) + b * a.sq[0];
-                for (unsigned u = t; u < M * CH; u += kGroups * 128) {
-                    const unsigned x = u / CH, c = u % CH;
-                    const bool some = row0 + x < live;
-                    const unsigned node = by_group.div(row0 + x), head = h * group + row0 + x - node * group;
-                    const T *src = some ? q + node * a.sq[1] + head * a.sq[2] : q;
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (!a.qvec) v = entries<T>(src, c, dim, some);
-                    else if (some && c * 8 < dim) v = *reinterpret_cast<const uint4 *>(src + c * 8);
-                    *reinterpret_cast<uint4 *>(qs + (x >> 7) * TILE + piece(KT, x & 127u, c)) = v;
+#pragma unroll 1
+                for (unsigned u0 = 0; u0 < ALL; u0 += EACH) {
+                    uint4 v[EACH];
+#pragma unroll
+                    for (unsigned i = 0; i < EACH; ++i) {
+                        const unsigned u = t + (u0 + i) * kGroups * 128, x = u / CH, c = u % CH;
+                        const bool some = row0 + x < live;
+                        const unsigned node = by_group.div(row0 + x), head = h * group + row0 + x - node * group;
+                        const T *src = some ? q + node * a.sq[1] + head * a.sq[2] : q;
+                        v[i] = make_uint4(0, 0, 0, 0);
+                        if (!a.qvec) v[i] = entries<T>(src, c, dim, some);
+                        else if (some && c * 8 < dim) v[i] = *reinterpret_cast<const uint4 *>(src + c * 8);
+                    }
+#pragma unroll
+                    for (unsigned i = 0; i < EACH; ++i) {
+                        const unsigned u = t + (u0 + i) * kGroups * 128, x = u / CH, c = u % CH;
+                        *reinterpret_cast<uint4 *>(qs + (x >> 7) * TILE + piece(KT, x & 127u, c)) = v[i];
+                    }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
