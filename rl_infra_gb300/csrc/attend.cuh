@@ -355,7 +355,7 @@ struct Loader {
         }
     }
 
-    // hands the boxes to the thread that asks; those without a page as bits of `bad`
+    // hands the boxes to the thread that asks; those without a page as bits of `bad` (null: another warp does)
     __device__ __forceinline__ void hand(const AttendArgs &a, const Span &s, unsigned tile, unsigned *bad, bool tell)
     {
         const unsigned lane = threadIdx.x & 31u;
@@ -366,11 +366,11 @@ struct Loader {
             const unsigned i = lane + 32 * e;
             const bool wrong = (unsigned)page[e] >= a.c.pages && (i << shift) < KT && tile * KT + (i << shift) < (unsigned)s.total;
             const unsigned bits = __ballot_sync(0xffffffffu, wrong);
-            if (lane == 0) bad[e] = bits;
+            if (bad && lane == 0) bad[e] = bits;
             any |= wrong;
             if ((i << shift) < KT) boxes[i] = wrong ? (int)a.c.pages : page[e];
         }
-        if (any && tell && a.c.status) atomicOr(a.c.status, PER_DEVFLAG_BAD_INDEX);
+        if (bad && any && tell && a.c.status) atomicOr(a.c.status, PER_DEVFLAG_BAD_INDEX);
         __syncwarp();
     }
 

@@ -18,16 +18,16 @@ namespace attend {
 namespace {
 
 constexpr int kWarps = 4;                  // of them that compute
-constexpr int kThreads = kWarps * 32 + 32;
+constexpr int kThreads = kWarps * 32 + 64;   // and a warp that asks for keys, one for values
 
 // What lies behind the tiles and the queries: barriers, and what goes from warp to warp.
-template <int KT, int ML>
+template <int KT, int ML, int ST>
 struct Tail {
-    u64 full[12], empty[6], meet;   // full: keys, then values
+    u64 full[2 * ST], empty[ST], meet;   // full: keys, then values
     u64 scan[kThreads / 32];
-    unsigned bad[6][KT / 32];
-    float ml[ML][2];           // maxima and sums that the warps hand over
-    alignas(16) int boxes[KT];
+    unsigned bad[ST][KT / 32];
+    alignas(8) float ml[ML][2];   // maxima and sums that the warps hand over
+    alignas(16) int boxes[2][KT];
     unsigned dead, odd;        // odd: the number of the last tile that something was taken out of
 };
 
@@ -43,15 +43,15 @@ struct Cfg {
     static constexpr int JOIN = WK == 4 ? 2 * 16 * DP * 4 : WK == 2 ? M * DP * 4 : 0;   // what the warps hand over
     static constexpr int QB = M * DP * ES * (ES == 4 ? 2 : 1);                          // the queries lie there before
     static constexpr int AREA = QB > JOIN ? QB : JOIN;
-    typedef Tail<KT, WK == 1 ? M : 32> End;
-    static constexpr int TAIL = ((int)sizeof(End) + 63) / 64 * 64;
+    static constexpr int TAIL = KT == 128 || WR == 4 ? 2048 : 1024;
     static constexpr int HALF_SM = 228 * 1024 / 2 - 1024;
     static constexpr int WHOLE_SM = 227 * 1024;
     static constexpr int PER_SM = (HALF_SM - AREA - TAIL) / STAGE >= (ES == 4 ? 2 : 3) ? 2 : 1;
     static constexpr int FIT = ((PER_SM == 2 ? HALF_SM : WHOLE_SM) - AREA - TAIL) / STAGE;
     static constexpr int ST = FIT > 6 ? 6 : FIT;
     static constexpr int SMEM = ST * STAGE + AREA + TAIL;
-    static_assert(ST >= 2, "fits");
+    typedef Tail<KT, WK == 1 ? M : 32, ST> End;
+    static_assert(ST >= 2 && sizeof(End) <= TAIL, "fits");
     static_assert(ES == 4 || KW % 16 == 0, "whole steps of the matrix instruction");
 };
 
@@ -114,10 +114,14 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
     auto next = [&] { return share ? turns++ == 0 : w.next(a); };
     unsigned st = 0, phase = 0;
 
-    if (warp == kWarps) {   // the warp that asks for tiles
+    if (warp >= kWarps) {   // the warps that ask for tiles: a box takes a thread some 150 cycles
+        const bool val = warp > kWarps;
+        const unsigned mine = full + (val ? 8 * ST : 0), at = val ? KT * DP * ES : 0;
+        const CUtensorMap *map = val ? &maps.v : &maps.k;
+        const unsigned char *axes = val ? maps.v_at : maps.k_at;
         Loader<KT> load;
         load.shift = shift;
-        load.boxes = tail.boxes;
+        load.boxes = tail.boxes[val];
         unsigned asked = 0;
         bool ok = true;
         const bool one = chosen();
@@ -127,12 +131,10 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
             for (unsigned tile = w.tile0; tile < w.tile1; ++tile) {
                 if (asked >= (unsigned)ST) ok = __all_sync(0xffffffffu, bar_wait(empty + 8 * st, phase ^ 1, dead));
                 if (!ok) break;
-                const unsigned ks = smem_u32(smem + st * C::STAGE), bar = full + 8 * st;
-                load.hand(a, w.s, tile, tail.bad[st], rt == 0 && w.h == 0);
-                if (one) {
-                    load.template request<DP * ES / 128>(a, &maps.k, maps.k_at, tile, w.h, ks, halves, C::PER_HALF, bar);
-                    load.template request<DP * ES / 128>(a, &maps.v, maps.v_at, tile, w.h, ks + KT * DP * ES, halves, C::PER_HALF, bar + 8 * ST);
-                }
+                load.hand(a, w.s, tile, val ? nullptr : tail.bad[st], rt == 0 && w.h == 0);
+                if (one)
+                    load.template request<DP * ES / 128>(a, map, axes, tile, w.h, smem_u32(smem + st * C::STAGE) + at, halves, C::PER_HALF,
+                                                         mine + 8 * st);
                 ++asked;
                 if (++st == ST) {
                     st = 0;
@@ -144,8 +146,7 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
         if (!ok) {          // given up: the copies under way must land before the CTA ends
             for (unsigned i = asked > (unsigned)ST ? asked - ST : 0; i < asked; ++i) {
                 unsigned none = 0;
-                bar_wait(full + 8 * (i % ST), i / ST & 1, &none);
-                bar_wait(full + 8 * (ST + i % ST), i / ST & 1, &none);
+                bar_wait(mine + 8 * (i % ST), i / ST & 1, &none);
             }
         }
     } else {

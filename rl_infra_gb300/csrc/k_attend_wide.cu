@@ -22,32 +22,32 @@ namespace gbper {
 namespace attend {
 namespace {
 
-constexpr int kGroups = 2, kThreads = kGroups * 128 + 64;   // and a warp for the copies, one for the products
+constexpr int kGroups = 2, kThreads = kGroups * 128 + 96;   // and two warps for the copies, one for the products
 constexpr int KT = 128;                                      // keys of a tile, and rows of a group
 constexpr float kRise = 8.0f;
 constexpr int kColumns = 512;                                // of tensor memory: two of scores, two of outputs, 128 each
+
+template <bool PAIR>
+struct Tail {
+    u64 full[10], empty[10], q_ready, s_full[2], p_ready[2], o_full[2], meet, last;
+    u64 scan[kThreads / 32];
+    unsigned bad[10][4];
+    alignas(16) int boxes[2][KT];
+    float ml[PAIR ? 1 : 256][2];   // maxima and sums, where both groups have the same rows
+    unsigned dead, odd, tmem;
+};
 
 template <int DP, bool PAIR>
 struct Cfg {
     static constexpr int TILE = KT * DP * 2;                 // bytes of a tile of keys or of values
     static constexpr int QB = (PAIR ? 2 : 1) * TILE;
-    static constexpr int TAIL = 3072;
+    static constexpr int TAIL = ((int)sizeof(Tail<PAIR>) + 63) / 64 * 64;
     static constexpr int FIT = (227 * 1024 - QB - TAIL) / TILE;
     static constexpr int ST = FIT > 10 ? 10 : FIT;
     static constexpr int SMEM = ST * TILE + QB + TAIL;
     static constexpr int M = PAIR ? 256 : 128;
     static_assert(ST >= 5, "the keys of the next tile come before this one's values are free");
 };
-
-struct Tail {
-    u64 full[10], empty[10], q_ready, s_full[2], p_ready[2], o_full[2], meet, last;
-    u64 scan[kThreads / 32];
-    unsigned bad[10][4];
-    alignas(16) int boxes[KT];
-    float ml[2][128][2];
-    unsigned dead, odd, tmem;
-};
-static_assert(sizeof(Tail) <= 3072, "");
 
 // ---- the tensor cores' instructions ---------------------------------------------------------------
 // Operands of 128-byte rows, 16-byte pieces turned modulo 8; groups of 8 rows 1024 bytes apart.  `lead`: bytes
@@ -159,7 +159,7 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
     constexpr int ST = C::ST, M = C::M, TILE = C::TILE;
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char *qs = smem + ST * TILE;
-    Tail &tail = *reinterpret_cast<Tail *>(qs + C::QB);
+    Tail<PAIR> &tail = *reinterpret_cast<Tail<PAIR> *>(qs + C::QB);
     volatile unsigned *dead = &tail.dead;
     const unsigned t = threadIdx.x, lane = t & 31u, warp = t >> 5;
     const unsigned cta = blockIdx.x, team = cta / row_tiles, rt = cta - team * row_tiles;
@@ -203,34 +203,32 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
     unsigned base = 0;         // tiles asked for before this stretch: keys and values in turn
     unsigned stretch = 0;      // stretches before this one
 
-    if (warp == 8) {           // the warp that asks for tiles
+    if (warp == 8 || warp == 10) {   // the warps that ask for tiles, one of keys, one of values
+        const unsigned val = warp == 10;
+        const CUtensorMap *map = val ? &maps.v : &maps.k;
+        const unsigned char *axes = val ? maps.v_at : maps.k_at;
         Loader<KT> load;
         load.shift = shift;
-        load.boxes = tail.boxes;
-        unsigned asked = 0;
+        load.boxes = tail.boxes[val];
+        unsigned asked = val;      // the next tile's number: keys even, values odd
         bool ok = true;
         const bool one = chosen();
         while (ok && w.next(a)) {
             if (row0 >= (unsigned)w.s.count * group) continue;
             load.look_up(a, w.b, w.s, w.tile0);
             for (unsigned tile = w.tile0; tile < w.tile1; ++tile) {
-                const unsigned k_slot = asked % ST, v_slot = (asked + 1) % ST;
-                // (bits of what has no page lie with the values, which are given up after the scores have been read)
-                if (asked + 1 >= (unsigned)ST)
-                    ok = __all_sync(0xffffffffu, bar_wait(empty + 8 * v_slot, ((asked + 1) / ST - 1) & 1, dead));
-                if (ok && asked >= (unsigned)ST) ok = __all_sync(0xffffffffu, bar_wait(empty + 8 * k_slot, (asked / ST - 1) & 1, dead));
+                const unsigned slot = asked % ST;
+                if (asked >= (unsigned)ST) ok = __all_sync(0xffffffffu, bar_wait(empty + 8 * slot, (asked / ST - 1) & 1, dead));
                 if (!ok) break;
-                load.hand(a, w.s, tile, tail.bad[v_slot], rt == 0 && w.h == 0);
-                if (one) {
-                    load.template request<DP / 64>(a, &maps.k, maps.k_at, tile, w.h, smem_u32(smem + k_slot * TILE), halves, 64, full + 8 * k_slot);
-                    load.template request<DP / 64>(a, &maps.v, maps.v_at, tile, w.h, smem_u32(smem + v_slot * TILE), halves, 64, full + 8 * v_slot);
-                }
+                // (bits of what has no page lie with the values, which are given up after the scores have been read)
+                load.hand(a, w.s, tile, val ? tail.bad[slot] : nullptr, rt == 0 && w.h == 0);
+                if (one) load.template request<DP / 64>(a, map, axes, tile, w.h, smem_u32(smem + slot * TILE), halves, 64, full + 8 * slot);
                 asked += 2;
                 if (tile + 1 < w.tile1) load.look_up(a, w.b, w.s, tile + 1);
             }
         }
         if (!ok) {             // given up: the copies under way must land before the CTA ends
-            for (unsigned i = asked > (unsigned)ST ? asked - ST : 0; i < asked; ++i) {
+            for (unsigned i = asked > (unsigned)ST + 1 ? asked - ST / 2 * 2 : val; i < asked; i += 2) {
                 unsigned none = 0;
                 bar_wait(full + 8 * (i % ST), i / ST & 1, &none);
             }
@@ -420,8 +418,11 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
             if (has) ok = __all_sync(0xffffffffu, bar_wait(o_full + 8 * g, outs & 1, dead));
             if (!ok) break;
             if (has) ++outs;
-            tail.ml[g][r][0] = raw_none ? -INFINITY : top;
-            tail.ml[g][r][1] = l;
+            const float mine = raw_none ? -INFINITY : top;
+            if constexpr (!PAIR) {
+                tail.ml[g * 128 + r][0] = mine;
+                tail.ml[g * 128 + r][1] = l;
+            }
             if (!(ok = meet(dead))) break;
             fence_after();
             const bool odd = *(volatile unsigned *)&tail.odd != 0;
@@ -429,18 +430,18 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
             // a group's rows, or (of rows that both have) half of the entries
             const RowOut<T> out{a, by_group, b, h, live, row0, (unsigned)M, w.part(), slots + (w.tile0 != 0 ? 0 : slot_floats)};
             const unsigned row_in = (PAIR ? g * 128 : 0) + r;
-            float f0 = 1.0f, f1 = 0.0f, m = tail.ml[g][r][0], sum = l;
+            float f0 = 1.0f, f1 = 0.0f, m = mine, sum = l;
             const bool both = !PAIR && tiles > 1;
-            if (both) {
-                const float m0 = tail.ml[0][r][0], m1 = tail.ml[1][r][0];
-                m = fmaxf(m0, m1);
-                const float mb = m == -INFINITY ? 0.0f : m;
-                f0 = ex2(m0 - mb);
-                f1 = ex2(m1 - mb);
-                sum = tail.ml[0][r][1] * f0 + tail.ml[1][r][1] * f1;
-            } else if (!PAIR) {
-                m = tail.ml[0][r][0];
-                sum = tail.ml[0][r][1];
+            if constexpr (!PAIR) {
+                m = tail.ml[r][0];
+                sum = tail.ml[r][1];
+                if (both) {
+                    const float m1 = tail.ml[128 + r][0], up = fmaxf(m, m1), least = up == -INFINITY ? 0.0f : up;
+                    f0 = ex2(m - least);
+                    f1 = ex2(m1 - least);
+                    sum = sum * f0 + tail.ml[128 + r][1] * f1;
+                    m = up;
+                }
             }
             const unsigned o_at = PAIR ? my_o : tmem + 256 + lanes;
             const bool real = my_row < live;
