@@ -198,11 +198,10 @@ __global__ void __launch_bounds__(kThreads) k_attend_any(AttendArgs a, unsigned 
     }
 }
 
-// Joins the parts of what lies in several CTAs: each CTA that begins such a stretch left a record.  A warp takes
-// per_warp rows one after another; its lanes work out 32 parts' weights at once, then take eight entries each.
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_attend_join(AttendArgs a, unsigned row_tiles, unsigned m_rows, FastDiv by_group, unsigned per_warp)
+// Joins the parts of what lies in several CTAs: each CTA that begins such a stretch left a record.  LR lanes take a row,
+// eight entries each; they work out the weights of LR parts at once.
+template <typename T, int LR>
+__global__ void __launch_bounds__(kThreads) k_attend_join(AttendArgs a, unsigned row_tiles, unsigned m_rows, FastDiv by_group)
 {
     const unsigned cta = blockIdx.x, team = cta / row_tiles, rt = cta - team * row_tiles;
     pdl_wait();
@@ -211,49 +210,50 @@ __global__ void __launch_bounds__(kThreads) k_attend_join(AttendArgs a, unsigned
     const int parts = record.w;
     if (parts == 0) return;
     const unsigned b = (unsigned)record.x, h = (unsigned)record.y, count = (unsigned)record.z;
-    const unsigned group = by_group.d, live = count * group, dim = a.c.dim, slot_floats = m_rows * (dim + 2);
-    const unsigned lane = threadIdx.x & 31u;
+    const unsigned live = count * by_group.d, dim = a.c.dim, slot_floats = m_rows * (dim + 2);
+    const unsigned lane = threadIdx.x & 31u, li = lane & (LR - 1);
+    const unsigned r = blockIdx.y * (kThreads / LR) + threadIdx.x / LR;
+    const bool real = r < m_rows && rt * m_rows + r < live;
+    if (!__any_sync(0xffffffffu, real)) return;
+    const unsigned row = real ? r : 0;
     const float *slots = a.work + (size_t)gridDim.x * kRecord;
     auto slot = [&](int i) {   // the first part lies in its CTA's second slot, the others in their first
         return slots + ((size_t)((team + i) * row_tiles + rt) * 2 + (i == 0)) * slot_floats;
     };
-    const RowOut<T> out{a, by_group, b, h, live, rt * m_rows, m_rows, false, nullptr};
-    const unsigned r0 = (blockIdx.y * 4 + (threadIdx.x >> 5)) * per_warp;
-    for (unsigned r = r0; r < r0 + per_warp && r < m_rows && rt * m_rows + r < live; ++r) {
-        float m = -INFINITY;
-        for (int i = lane; i < parts; i += 32) m = fmaxf(m, slot(i)[m_rows * dim + 2 * r]);
+    float m = -INFINITY;
+    for (int i = li; i < parts; i += LR) m = fmaxf(m, slot(i)[m_rows * dim + 2 * row]);
 #pragma unroll
-        for (int d = 16; d; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        const float base = m == -INFINITY ? 0.0f : m;
-        float x[8] = {}, l = 0.0f;              // a lane's eight entries
-        for (int i0 = 0; i0 < parts; i0 += 32) {
-            float f = 0.0f;
-            if (i0 + (int)lane < parts) {
-                const float2 z = *reinterpret_cast<const float2 *>(slot(i0 + lane) + m_rows * dim + 2 * r);
-                f = ex2(z.x - base);
-                l += f * z.y;
-            }
-            const int n = min(32, parts - i0);
+    for (int d = LR / 2; d; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const float base = m == -INFINITY ? 0.0f : m;
+    float x[8] = {}, l = 0.0f;
+    for (int i0 = 0; i0 < parts; i0 += LR) {
+        float f = 0.0f;
+        if (i0 + (int)li < parts) {
+            const float2 z = *reinterpret_cast<const float2 *>(slot(i0 + li) + m_rows * dim + 2 * row);
+            f = ex2(z.x - base);
+            l += f * z.y;
+        }
+        const int n = min(LR, parts - i0);
 #pragma unroll 8
-            for (int i = 0; i < n; ++i) {
-                const float w = __shfl_sync(0xffffffffu, f, i);
-                const float *p = slot(i0 + i) + r * dim + lane * 8;
-                if (lane * 8 >= dim) continue;
-                if (dim % 8 == 0) {
-                    const float4 y = *reinterpret_cast<const float4 *>(p), z = *reinterpret_cast<const float4 *>(p + 4);
-                    x[0] += w * y.x, x[1] += w * y.y, x[2] += w * y.z, x[3] += w * y.w;
-                    x[4] += w * z.x, x[5] += w * z.y, x[6] += w * z.z, x[7] += w * z.w;
-                } else {
+        for (int i = 0; i < n; ++i) {
+            const float w = __shfl_sync(0xffffffffu, f, i, LR);
+            const float *p = slot(i0 + i) + row * dim + li * 8;
+            if (li * 8 >= dim) continue;
+            if (dim % 8 == 0) {
+                const float4 y = *reinterpret_cast<const float4 *>(p), z = *reinterpret_cast<const float4 *>(p + 4);
+                x[0] += w * y.x, x[1] += w * y.y, x[2] += w * y.z, x[3] += w * y.w;
+                x[4] += w * z.x, x[5] += w * z.y, x[6] += w * z.z, x[7] += w * z.w;
+            } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (lane * 8 + e < dim) x[e] += w * p[e];
-                }
+                for (int e = 0; e < 8; ++e)
+                    if (li * 8 + e < dim) x[e] += w * p[e];
             }
         }
-#pragma unroll
-        for (int d = 16; d; d /= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
-        out.put8(r, lane * 8, x, m, l);
     }
+#pragma unroll
+    for (int d = LR / 2; d; d /= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
+    const RowOut<T> out{a, by_group, b, h, live, rt * m_rows, m_rows, false, nullptr};
+    if (real) out.put8(r, li * 8, x, m, l);
 }
 
 // ---- the copy engine's maps ----------------------------------------------------------------------
@@ -392,11 +392,13 @@ bool make_maps(int type, const AttendArgs &a, unsigned kt, CacheMaps *maps, unsi
     return make_map(type, a, a.c.k, a.c.sk, 1u << s, &maps->k, maps->k_at) && make_map(type, a, a.c.v, a.c.sv, 1u << s, &maps->v, maps->v_at);
 }
 
-cudaError_t join_parts(int type, const AttendArgs &a, const Plan &p, const FastDiv &by_group, cudaStream_t st)
+namespace {
+
+template <typename T, int LR>
+cudaError_t join(const AttendArgs &a, const Plan &p, const FastDiv &by_group, cudaStream_t st)
 {
     cudaLaunchConfig_t cfg = {};
-    const unsigned per_warp = p.m > 32 ? 4 : 1;   // (many CTAs of one row a warp took longer to come and go than to work)
-    cfg.gridDim = dim3(p.grid, (p.m + 4 * per_warp - 1) / (4 * per_warp));
+    cfg.gridDim = dim3(p.grid, (p.m + kThreads / LR - 1) / (kThreads / LR));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -404,9 +406,24 @@ cudaError_t join_parts(int type, const AttendArgs &a, const Plan &p, const FastD
     attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (type == PER_TYPE_F32) return cudaLaunchKernelEx(&cfg, k_attend_join<float>, a, p.row_tiles, p.m, by_group, per_warp);
-    if (type == PER_TYPE_F16) return cudaLaunchKernelEx(&cfg, k_attend_join<__half>, a, p.row_tiles, p.m, by_group, per_warp);
-    return cudaLaunchKernelEx(&cfg, k_attend_join<__nv_bfloat16>, a, p.row_tiles, p.m, by_group, per_warp);
+    return cudaLaunchKernelEx(&cfg, k_attend_join<T, LR>, a, p.row_tiles, p.m, by_group);
+}
+
+template <typename T>
+cudaError_t join_t(const AttendArgs &a, const Plan &p, const FastDiv &by_group, cudaStream_t st)
+{
+    if (a.c.dim <= 64) return join<T, 8>(a, p, by_group, st);
+    if (a.c.dim <= 128) return join<T, 16>(a, p, by_group, st);
+    return join<T, 32>(a, p, by_group, st);
+}
+
+}  // namespace
+
+cudaError_t join_parts(int type, const AttendArgs &a, const Plan &p, const FastDiv &by_group, cudaStream_t st)
+{
+    if (type == PER_TYPE_F32) return join_t<float>(a, p, by_group, st);
+    if (type == PER_TYPE_F16) return join_t<__half>(a, p, by_group, st);
+    return join_t<__nv_bfloat16>(a, p, by_group, st);
 }
 
 }  // namespace attend

@@ -333,24 +333,39 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
             float top = -INFINITY, l = 0.0f;      // what p refers to (in log2), and the sum of p
             bool raw_none = true;                 // nothing seen yet
             float ref = 0.0f;                     // top as a score
+            // before there is anything to wait for: whether the stretch has a page that does not exist (then, and at the
+            // sequence's end, a tile's values are waited for before its scores are used), and what the row sees of the
+            // first tile with nodes
+            bool holes = false;
+            {
+                const unsigned last = min(w.tile1 * KT, (unsigned)s.total);
+                if (w.tile0 * KT < last)
+                    for (unsigned pg = a.c.page.div(w.tile0 * KT) + lane, end = a.c.page.div(last - 1); pg <= end; pg += 32)
+                        holes |= (unsigned)a.c.table[b * a.c.st + pg] >= a.c.pages;
+                holes = __any_sync(0xffffffffu, holes);
+            }
+            unsigned word[KT / 32] = {}, known = (unsigned)s.len / KT;
+            if (known >= w.tile0 && known < w.tile1 && (PAIR || (known - w.tile0 & 1u) == g))
+                seen(a, b, s, node, known * KT, nullptr, false, shift, word);
             for (unsigned j = PAIR ? 0 : g; j < tiles; j += PAIR ? 1 : 2) {
                 const unsigned tile = w.tile0 + j, n = base + 2 * j + 1, slot = n % ST;
-                ok = __all_sync(0xffffffffu, bar_wait(s_full + 8 * g, phase & 1, dead) && bar_wait(full + 8 * slot, n / ST & 1, dead));
-                if (!ok) break;
+                const bool tail_in = (tile + 1) * KT > (unsigned)s.len;   // nodes, or the end
+                ok = bar_wait(s_full + 8 * g, phase & 1, dead);
+                if (ok && (tail_in || holes)) ok = bar_wait(full + 8 * slot, n / ST & 1, dead);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 ++phase;
                 fence_after();
-                const bool tail_in = (tile + 1) * KT > (unsigned)s.len;   // nodes, or the end
                 if (tail_in && (!PAIR || g == 0)) {
                     // what stale slots hold is taken out of the values, and what is not finite in a node's: it must
                     // reach only the rows that see it
                     if (clean<T>(smem + slot * TILE, KT, tile * KT, s, halves * 8, r, 128)) tail.odd = 1;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
-                unsigned wrong = 0, word[KT / 32] = {};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) wrong |= tail.bad[slot][e];
-                const bool masked = tail_in || wrong;
-                if (masked) seen(a, b, s, node, tile * KT, tail.bad[slot], wrong != 0, shift, word);
+                const bool masked = tail_in || holes;
+                if (masked && (tile != known || holes)) {
+                    seen(a, b, s, node, tile * KT, tail.bad[slot], holes, shift, word);
+                    known = ~0u;
+                }
                 // p against the maximum so far, a quarter of the row at a time, and the row's maximum on the way; once more
                 // where that has risen (the scores are still there: p is written when it stands)
                 unsigned p[KT / 2];
@@ -360,12 +375,14 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                     const F2 c2 = {a.c2, a.c2}, less = {-off, -off};
                     float most = -INFINITY;
                     add[0] = add[1] = F2{0.0f, 0.0f};
+                    float two[2][32];         // a quarter that is worked on, and the next one on its way
+                    get32(two[0], my_s);
 #pragma unroll
                     for (int i = 0; i < KT / 32; ++i) {
-                        float sc[32];
-                        get32(sc, my_s + 32 * i);
+                        float *sc = two[i & 1];
                         wait_ld();
                         loaded32(sc);
+                        if (i + 1 < KT / 32) get32(two[(i + 1) & 1], my_s + 32 * (i + 1));
                         if (masked) hide(sc, word[i]);
                         float up[4] = {most, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
