@@ -5,7 +5,7 @@
 // each CTA that the GPU holds at once (a team of CTAs, where the rows of a head of keys need several).  A part that
 // begins or ends inside a sequence leaves its sums in scratch memory, and a second kernel joins them in their
 // order.  So one long sequence fills the GPU, and ragged ones leave no SM idle.  Each sequence and head counts
-// kBegin tiles more than it has, for its queries, its nodes and its output: without them short sequences that lie
+// BEGIN tiles more than it has, for its queries, its nodes and its output: without them short sequences that lie
 // side by side became one CTA's (16 trees of which one has no context: 257 us, 126 without that one).
 #pragma once
 
@@ -19,7 +19,6 @@ namespace attend {
 typedef unsigned long long u64;
 constexpr int kRecord = 8;             // ints of a CTA's record for the joining kernel
 constexpr unsigned kWaitMs = 2000;     // limit of a wait
-constexpr unsigned kBegin = 2;         // tiles that a sequence's begin and end are worth
 
 // ---- how the work is cut -----------------------------------------------------------------------
 struct Span {              // a sequence
@@ -52,9 +51,9 @@ __device__ __forceinline__ u64 divide(u64 x, u64 y)
 }
 
 // A team's stretches, one sequence and head after another.
-template <int KT>
+template <int KT, unsigned BEGIN>
 struct Walk {
-    u64 pos, end, at;        // in tiles, kBegin before each sequence's and head's; at: where the sequence begins
+    u64 pos, end, at;        // in tiles, BEGIN before each sequence's and head's; at: where the sequence begins
     u64 size, more;          // tiles of a team; the first `more` teams have one more
     unsigned b, n_tiles, h, tile0, tile1;
     Span s;
@@ -67,7 +66,7 @@ struct Walk {
         const unsigned per = (a.batch + NT - 1) / NT;
         const unsigned b0 = min(t * per, a.batch), b1 = min(b0 + per, a.batch);
         u64 mine = 0;
-        for (unsigned i = b0; i < b1; ++i) mine += tiles_of<KT>(span(a, i)) + kBegin;
+        for (unsigned i = b0; i < b1; ++i) mine += tiles_of<KT>(span(a, i)) + BEGIN;
         u64 upto = mine;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
@@ -94,7 +93,7 @@ struct Walk {
             unsigned i = b0;
             u64 x = before;
             for (;; ++i) {
-                const u64 n = (u64)(tiles_of<KT>(span(a, i)) + kBegin) * a.c.heads;
+                const u64 n = (u64)(tiles_of<KT>(span(a, i)) + BEGIN) * a.c.heads;
                 if (pos < x + n) break;
                 x += n;
             }
@@ -124,17 +123,17 @@ struct Walk {
     {
         do {
             if (pos >= end) return false;
-            if (pos >= at + (u64)(n_tiles + kBegin) * a.c.heads) {
-                at += (u64)(n_tiles + kBegin) * a.c.heads;
+            if (pos >= at + (u64)(n_tiles + BEGIN) * a.c.heads) {
+                at += (u64)(n_tiles + BEGIN) * a.c.heads;
                 ++b;
                 s = span(a, b);
                 n_tiles = tiles_of<KT>(s);
             }
-            const unsigned whole = n_tiles + kBegin;
+            const unsigned whole = n_tiles + BEGIN;
             h = (unsigned)divide(pos - at, whole);
             const unsigned x0 = (unsigned)(pos - at - (u64)h * whole), x1 = (unsigned)min((u64)whole, x0 + (end - pos));
-            tile0 = x0 > kBegin ? x0 - kBegin : 0;
-            tile1 = x1 > kBegin ? x1 - kBegin : 0;
+            tile0 = x0 > BEGIN ? x0 - BEGIN : 0;
+            tile1 = x1 > BEGIN ? x1 - BEGIN : 0;
             pos += x1 - x0;
         } while (tile0 == tile1);
         return true;
@@ -145,7 +144,7 @@ struct Walk {
     // the record of a CTA that begins what others end
     __device__ __forceinline__ void note(int *record, unsigned team) const
     {
-        const u64 last = at + (u64)(h + 1) * (n_tiles + kBegin) - 1;   // the tile that ends it
+        const u64 last = at + (u64)(h + 1) * (n_tiles + BEGIN) - 1;   // the tile that ends it
         const u64 border = more * (size + 1);
         const u64 last_team = last < border ? divide(last, size + 1) : more + divide(last - border, size);
         record[0] = (int)b;
@@ -410,8 +409,8 @@ struct Plan {
 
 // `shares`: the kernel can take a sequence's head whole; `clusters`: it can join through the shared memory of a cluster's CTAs.  Where sequences are short that is
 // quicker than the cut (one kernel, no scratch memory): by tiles that a CTA works through one after another, a
-// begin counting 3, the second kernel 8.  The lengths are not known here; the table's width stands for them.
-inline Plan plan_of(const AttendArgs &a, unsigned m, unsigned kt, unsigned ctas, bool shares, bool clusters)
+// begin counting `begin`, the second kernel 8.  The lengths are not known here; the table's width stands for them.
+inline Plan plan_of(const AttendArgs &a, unsigned m, unsigned kt, unsigned ctas, unsigned begin, bool shares, bool clusters)
 {
     Plan p;
     const u64 rows = (u64)a.nodes * (a.q_heads / a.c.heads);   // at most 2^16
@@ -419,16 +418,16 @@ inline Plan plan_of(const AttendArgs &a, unsigned m, unsigned kt, unsigned ctas,
     p.row_tiles = (unsigned)((rows + m - 1) / m);
     p.teams = ctas > p.row_tiles ? ctas / p.row_tiles : 1;
     const u64 most = ((u64)a.c.width * a.c.page.d + kt - 1) / kt;   // tiles of a sequence
-    const u64 tiles = ((most ? most : 1) + kBegin) * a.batch * a.c.heads;
+    const u64 tiles = ((most ? most : 1) + begin) * a.batch * a.c.heads;
     if (p.teams > tiles) p.teams = (unsigned)tiles;
     p.grid = p.teams * p.row_tiles;
     p.share = 0;
     p.parts = most > 1 && p.teams > 1;
     if (p.parts && shares) {
         const u64 units = (u64)a.batch * a.c.heads * p.row_tiles;
-        u64 least = (units * (most + kBegin) + ctas - 1) / ctas + 3 + 8;
+        u64 least = (units * (most + begin) + ctas - 1) / ctas + 3 + 8;
         for (unsigned n = 1; n <= (clusters ? 8u : 1u); n *= 2) {
-            const u64 cost = (units * n + ctas - 1) / ctas * ((most + n - 1) / n + 3);
+            const u64 cost = (units * n + ctas - 1) / ctas * ((most + n - 1) / n + begin);
             if (cost < least && units * n < 1u << 20) {
                 least = cost;
                 p.share = n;

@@ -90,6 +90,13 @@ __device__ __forceinline__ void scores(float (*sc)[4], const unsigned char *qs, 
             }
         }
     } else {
+        // a sum for each kind of product and half of the steps, so that none waits for the one before it (and because the
+        // instruction cuts its sums instead of rounding them: the shorter, the nearer)
+        float low_q[KW / 8][4], low_k[KW / 8][4], odd[KW / 8][4];
+#pragma unroll
+        for (int i = 0; i < KW / 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) low_q[i][e] = low_k[i][e] = odd[i][e] = 0.0f;
 #pragma unroll
         for (int k = 0; k < DP / 8; ++k) {
             if (k >= (int)steps) break;
@@ -108,11 +115,15 @@ __device__ __forceinline__ void scores(float (*sc)[4], const unsigned char *qs, 
                 unsigned h0, l0, h1, l1;
                 split(z.x, h0, l0);
                 split(z.y, h1, l1);
-                mma8(sc[i], al, h0, h1);
-                mma8(sc[i], ah, l0, l1);
-                mma8(sc[i], ah, h0, h1);
+                mma8(low_q[i], al, h0, h1);
+                mma8(low_k[i], ah, l0, l1);
+                mma8(k & 1 ? odd[i] : sc[i], ah, h0, h1);
             }
         }
+#pragma unroll
+        for (int i = 0; i < KW / 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[i][e] = (sc[i][e] + odd[i][e]) + (low_q[i][e] + low_k[i][e]);
     }
 }
 
@@ -145,18 +156,30 @@ __device__ __forceinline__ void values(float (*o)[4], const float (*p)[4], const
             split(p[k][2], ph[1], pl[1]);
             split(p[k][1], ph[2], pl[2]);
             split(p[k][3], ph[3], pl[3]);
+            constexpr int TOGETHER = 4;   // products whose sums are different ones, so that none waits for the one before it
 #pragma unroll
-            for (int i = 0; i < DP / 8; ++i) {
-                if (i >= (int)steps) break;
-                const unsigned r = key0 + k * 8 + q4 * 2, c = i * 2 + (g >> 2), in = (g & 3u) * 4;
-                const float x = *reinterpret_cast<const float *>(vs + piece(kt, r, c) + in);
-                const float y = *reinterpret_cast<const float *>(vs + piece(kt, r + 1, c) + in);
-                unsigned h0, l0, h1, l1;
-                split(x, h0, l0);
-                split(y, h1, l1);
-                mma8(o[i], pl, h0, h1);
-                mma8(o[i], ph, l0, l1);
-                mma8(o[i], ph, h0, h1);
+            for (int i0 = 0; i0 < DP / 8; i0 += TOGETHER) {
+                if (i0 >= (int)steps) break;
+                unsigned h0[TOGETHER], l0[TOGETHER], h1[TOGETHER], l1[TOGETHER];
+#pragma unroll
+                for (int j = 0; j < TOGETHER; ++j) {
+                    const unsigned r = key0 + k * 8 + q4 * 2, c = (i0 + j) * 2 + (g >> 2), in = (g & 3u) * 4;
+                    split(*reinterpret_cast<const float *>(vs + piece(kt, r, c) + in), h0[j], l0[j]);
+                    split(*reinterpret_cast<const float *>(vs + piece(kt, r + 1, c) + in), h1[j], l1[j]);
+                }
+                float part[TOGETHER][4];      // eight keys' sum, added to the others' with rounding
+#pragma unroll
+                for (int j = 0; j < TOGETHER; ++j) part[j][0] = part[j][1] = part[j][2] = part[j][3] = 0.0f;
+#pragma unroll
+                for (int j = 0; j < TOGETHER; ++j) mma8(part[j], pl, h0[j], h1[j]);
+#pragma unroll
+                for (int j = 0; j < TOGETHER; ++j) mma8(part[j], ph, l0[j], l1[j]);
+#pragma unroll
+                for (int j = 0; j < TOGETHER; ++j) mma8(part[j], ph, h0[j], h1[j]);
+#pragma unroll
+                for (int j = 0; j < TOGETHER; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[i0 + j][e] += part[j][e];
             }
         }
     }

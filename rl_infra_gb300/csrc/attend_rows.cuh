@@ -17,6 +17,7 @@ namespace gbper {
 namespace attend {
 namespace {
 
+constexpr unsigned kBegin = 3;             // tiles that a sequence's begin and end are worth
 constexpr int kWarps = 4;                  // of them that compute
 constexpr int kThreads = kWarps * 32 + 64;   // and a warp that asks for keys, one for values
 
@@ -103,7 +104,7 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
     pdl_release();
     int *record = reinterpret_cast<int *>(a.work) + (size_t)cta * kRecord;
     if (a.work && t == 0) record[3] = 0;
-    Walk<KT> w;
+    Walk<KT, kBegin> w;
     if (share) {
         __syncthreads();
         w.one(a, team / a.c.heads, team % a.c.heads, rank, share);
@@ -415,7 +416,7 @@ template <typename T, int DP, int WR>
 cudaError_t rows(AttendArgs a, int type, const DeviceInfo &dev, cudaStream_t st, u64 *bytes)
 {
     using C = Cfg<T, DP, WR>;
-    const Plan p = plan_of(a, C::M, C::KT, (unsigned)dev.sms * C::PER_SM, true, C::WK > 1);
+    const Plan p = plan_of(a, C::M, C::KT, (unsigned)dev.sms * C::PER_SM, kBegin, true, C::WK > 1);
     if (bytes) {
         *bytes = p.parts ? p.bytes : 0;
         return cudaSuccess;

@@ -18,6 +18,7 @@ namespace attend {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr unsigned kBegin = 2;   // tiles that a sequence's begin and end are worth
 constexpr unsigned kFew = 32;    // rows of a head of keys that the warp-wide instruction takes
 
 template <typename T, int DP>
@@ -55,7 +56,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_any(AttendArgs a, unsigned 
     pdl_wait();
     pdl_release();
     if (a.work && t == 0) record[3] = 0;
-    Walk<KT> w;
+    Walk<KT, kBegin> w;
     if (!w.template begin<kThreads>(a, team, max_teams, scan)) return;
     while (w.next(a)) {
         const Span &s = w.s;
@@ -337,7 +338,7 @@ template <typename T, int DP>
 cudaError_t attend_any(AttendArgs a, int type, const DeviceInfo &dev, cudaStream_t st, u64 *bytes)
 {
     using C = Cfg<T, DP>;
-    const Plan p = plan_of(a, C::M, C::KT, (unsigned)dev.sms * C::PER_SM, false, false);
+    const Plan p = plan_of(a, C::M, C::KT, (unsigned)dev.sms * C::PER_SM, kBegin, false, false);
     if (bytes) {
         *bytes = p.parts ? p.bytes : 0;
         return cudaSuccess;

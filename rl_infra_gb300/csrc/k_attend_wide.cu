@@ -23,6 +23,7 @@ namespace attend {
 namespace {
 
 constexpr int kGroups = 2, kThreads = kGroups * 128 + 96;   // and two warps for the copies, one for the products
+constexpr unsigned kBegin = 6;                               // tiles that a sequence's begin and end are worth
 constexpr int KT = 128;                                      // keys of a tile, and rows of a group
 constexpr float kRise = 8.0f;
 constexpr int kColumns = 512;                                // of tensor memory: two of scores, two of outputs, 128 each
@@ -189,7 +190,7 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
     pdl_release();
     int *record = reinterpret_cast<int *>(a.work) + (size_t)cta * kRecord;
     if (a.work && t == 0) record[3] = 0;
-    Walk<KT> w;
+    Walk<KT, kBegin> w;
     if (!w.template begin<kThreads>(a, team, max_teams, tail.scan)) return;
     if (warp == 9) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tail.tmem)), "r"(kColumns) : "memory");
@@ -515,7 +516,7 @@ template <typename T, int DP, bool PAIR>
 cudaError_t wide(AttendArgs a, int type, const DeviceInfo &dev, cudaStream_t st, u64 *bytes)
 {
     using C = Cfg<DP, PAIR>;
-    const Plan p = plan_of(a, C::M, KT, (unsigned)dev.sms, false, false);
+    const Plan p = plan_of(a, C::M, KT, (unsigned)dev.sms, kBegin, false, false);
     if (bytes) {
         *bytes = p.parts ? p.bytes : 0;
         return cudaSuccess;
