@@ -65,12 +65,13 @@ __device__ __forceinline__ uint4 entries(const T *src, unsigned c, unsigned dim,
     return v;
 }
 
-// sc = q k for 16 rows from r0 of the m rows at qs, and KW keys from key0 of the kt at ks; `steps` of the instruction
-// along a head.  binary32 queries lie in two parts, upper and lower.  A step of these takes two pieces four apart: column c of the instruction is entry 2 c
+// sc = q k for 16 rows from r0 of the m rows at qs, and KW keys from key0 of the kt at ks; `halves` of 128 bytes of a head
+// (what lies past its entries is zero), four steps of the instruction each: without a branch between them, so that what
+// one waits for does not keep the next.  binary32 queries lie in two parts, upper and lower.  A step of these takes two pieces four apart: column c of the instruction is entry 2 c
 // mod 4 of piece c / 2 * 4, column c + 4 the entry behind it, so that 16 lanes read 16 different banks twice.
 template <typename T, int DP, int KW>
 __device__ __forceinline__ void scores(float (*sc)[4], const unsigned char *qs, unsigned m, unsigned r0, const unsigned char *ks,
-                                       unsigned kt, unsigned key0, unsigned steps)
+                                       unsigned kt, unsigned key0, unsigned halves)
 {
     const unsigned lane = threadIdx.x & 31u, g = lane >> 2, q4 = lane & 3u;
 #pragma unroll
@@ -78,7 +79,7 @@ __device__ __forceinline__ void scores(float (*sc)[4], const unsigned char *qs, 
     if constexpr (sizeof(T) == 2) {
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k) {
-            if (k >= (int)steps) break;
+            if (k % 4 == 0 && k / 4 >= (int)halves) break;
             unsigned qa[4];
             ldsm4(qa, smem_u32(qs + piece(m, r0 + (lane & 15u), k * 2 + (lane >> 4))));
 #pragma unroll
@@ -99,7 +100,7 @@ __device__ __forceinline__ void scores(float (*sc)[4], const unsigned char *qs, 
             for (int e = 0; e < 4; ++e) low_q[i][e] = low_k[i][e] = odd[i][e] = 0.0f;
 #pragma unroll
         for (int k = 0; k < DP / 8; ++k) {
-            if (k >= (int)steps) break;
+            if (k % 4 == 0 && k / 4 >= (int)halves) break;
             unsigned ah[4], al[4];
             const unsigned c = (k >> 2) * 8 + (k & 3) + (q4 >> 1) * 4, in = (q4 & 1u) * 8;
             const unsigned low = m * DP * 4;   // the lower parts lie behind the upper ones
@@ -131,7 +132,7 @@ __device__ __forceinline__ void scores(float (*sc)[4], const unsigned char *qs, 
 // 2 c + 1 column c + 4: the scores lie so already.
 template <typename T, int DP, int KW>
 __device__ __forceinline__ void values(float (*o)[4], const float (*p)[4], const unsigned char *vs, unsigned kt, unsigned key0,
-                                       unsigned steps)
+                                       unsigned halves)
 {
     const unsigned lane = threadIdx.x & 31u, g = lane >> 2, q4 = lane & 3u;
     if constexpr (sizeof(T) == 2) {
@@ -141,7 +142,7 @@ __device__ __forceinline__ void values(float (*o)[4], const float (*p)[4], const
                                     pack2<T>(p[2 * k + 1][0], p[2 * k + 1][1]), pack2<T>(p[2 * k + 1][2], p[2 * k + 1][3])};
 #pragma unroll
             for (int i = 0; i < DP / 16; ++i) {
-                if (i >= (int)steps) break;
+                if (i % 4 == 0 && i / 4 >= (int)halves) break;
                 unsigned vb[4];   // keys 0-7 and 8-15 of entries 0-7, then of entries 8-15
                 ldsm4t(vb, smem_u32(vs + piece(kt, key0 + k * 16 + (lane & 15u), i * 2 + (lane >> 4))));
                 mma16<T>(o[2 * i], pa, vb[0], vb[1]);
@@ -159,7 +160,7 @@ __device__ __forceinline__ void values(float (*o)[4], const float (*p)[4], const
             constexpr int TOGETHER = 4;   // products whose sums are different ones, so that none waits for the one before it
 #pragma unroll
             for (int i0 = 0; i0 < DP / 8; i0 += TOGETHER) {
-                if (i0 >= (int)steps) break;
+                if (i0 / 4 >= (int)halves) break;
                 unsigned h0[TOGETHER], l0[TOGETHER], h1[TOGETHER], l1[TOGETHER];
 #pragma unroll
                 for (int j = 0; j < TOGETHER; ++j) {

@@ -153,7 +153,6 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
     } else {
         const unsigned g = lane >> 2, q4 = lane & 3u;                // row and column pair of a fragment
         const unsigned wr = warp / WK, wk = warp - wr * WK, key0 = wk * KW;
-        const unsigned steps = ES == 2 ? (dim + 15) / 16 : (dim + 31) / 32 * 4;   // of the matrix instruction along a head
         const unsigned slot_floats = M * (dim + 2);
         float *slots = a.work + (size_t)gridDim.x * kRecord + (size_t)cta * 2 * slot_floats;
         Meeting meet{smem_u32(&tail.meet), 0};
@@ -240,7 +239,7 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                 }
 
                 float sc[KW / 8][4];
-                scores<T, DP, KW>(sc, area, M, wr * 16, ks, KT, key0, steps);
+                scores<T, DP, KW>(sc, area, M, wr * 16, ks, KT, key0, halves);
 #pragma unroll
                 for (int i = 0; i < KW / 8; ++i)
 #pragma unroll
@@ -257,7 +256,7 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                 }
                 soften<DP, KW>(sc, top, sum, o);
                 if (!tail_in && !(ok = __all_sync(0xffffffffu, bar_wait(full + 8 * (ST + st), phase, dead)))) break;
-                values<T, DP, KW>(o, sc, vs, KT, key0, steps);
+                values<T, DP, KW>(o, sc, vs, KT, key0, halves);
                 if (odd)
                     for (unsigned r = key0; r < key0 + KW; ++r) {
                         const unsigned key = tile * KT + r, box = r >> shift;

@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_any(AttendArgs a, unsigned 
     const unsigned g = lane >> 2, q4 = lane & 3u;                  // row and column pair of a fragment
     const unsigned cta = blockIdx.x, team = cta / row_tiles, rt = cta - team * row_tiles;
     const unsigned group = by_group.d, row0 = rt * M, dim = a.c.dim;
-    const unsigned steps = ES == 2 ? (dim + 15) / 16 : (dim + 31) / 32 * 4;   // of the matrix instruction along a head
+    const unsigned halves = (dim * ES + 127) / 128;
     const unsigned slot_floats = M * (dim + 2);
     int *record = reinterpret_cast<int *>(a.work) + (size_t)cta * kRecord;
     float *slots = a.work + (size_t)gridDim.x * kRecord + (size_t)cta * 2 * slot_floats;
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_any(AttendArgs a, unsigned 
             }
 
             float sc[KT / 8][4];
-            scores<T, DP, KT>(sc, qs, M, warp * 16, ks, KT, 0, steps);
+            scores<T, DP, KT>(sc, qs, M, warp * 16, ks, KT, 0, halves);
 #pragma unroll
             for (int i = 0; i < KT / 8; ++i)
 #pragma unroll
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_any(AttendArgs a, unsigned 
                     }
             }
             soften<DP, KT>(sc, top, sum, o);
-            values<T, DP, KT>(o, sc, vs, KT, 0, steps);
+            values<T, DP, KT>(o, sc, vs, KT, 0, halves);
             if (odd)
                 for (unsigned r = 0; r < KT; ++r) {
                     const unsigned key = tile * KT + r;
