@@ -511,7 +511,7 @@ per_status per_scan_backward(const per_scan_shape *shape, const void *d_a, const
 typedef struct {
     uint32_t pages;        /* P, 0 .. 2^31 - 1 */
     uint32_t page;         /* S, slots of a page, 1 .. 2^20 */
-    uint32_t width;        /* pages that a row of the table names; width S < 2^31 */
+    uint32_t width;        /* pages that a row of the table names; width S at most 2^30 */
     uint32_t heads;        /* Hkv, heads of keys and values, 1 .. 4096 */
     uint32_t dim;          /* D, entries of a head, 1 .. 256 */
     uint32_t type;         /* PER_TYPE_* of the cache and of all that goes in and out of it */

@@ -159,7 +159,7 @@ __device__ __forceinline__ bool sees(const AttendArgs &a, unsigned b, const Span
 {
     if ((int)key < s.len) return true;
     const unsigned j = key - (unsigned)s.len;
-    if (j >= (unsigned)s.count) return false;
+    if (j >= (unsigned)(s.total - s.len)) return false;   // no node, or one behind the table's end
     if (!a.mask) return (int)j <= n;
     return a.mask[b * a.sm[0] + n * a.sm[1] + j] != 0;
 }

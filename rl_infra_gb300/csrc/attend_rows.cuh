@@ -235,7 +235,7 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the next copy comes after these stores
                     if (odd) tail.odd = tiles_done;
                     if (!(ok = meet(dead))) break;
-                    odd = *(volatile unsigned *)&tail.odd == tiles_done;
+                    odd = *(volatile unsigned *)&tail.odd >= tiles_done;   // (a warp ahead may have written the next tile's)
                 }
 
                 float sc[KW / 8][4];

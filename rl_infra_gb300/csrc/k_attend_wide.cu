@@ -128,7 +128,8 @@ __device__ __forceinline__ void hide(float *sc, unsigned word)
 __device__ __forceinline__ void seen(const AttendArgs &a, unsigned b, const Span &s, int n, unsigned first, const unsigned *bad,
                                      bool wrong, unsigned shift, unsigned *word)
 {
-    const int end = a.mask || n < 0 ? s.count : min(s.count, n + 1);   // nodes from 0 to here
+    const int there = s.total - s.len;                                 // nodes that the table has a place for
+    const int end = a.mask || n < 0 ? there : min(there, n + 1);       // those that may be seen: from 0 to here
     const uint8_t *mask = a.mask ? a.mask + b * a.sm[0] + (long long)max(n, 0) * a.sm[1] : nullptr;
 #pragma unroll
     for (int w = 0; w < KT / 32; ++w) {

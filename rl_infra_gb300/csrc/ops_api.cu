@@ -147,7 +147,7 @@ const char *cache_fault(const per_cache &c)
 {
     if (c.pages > 0x7fffffffu) return "pages must be below 2^31";
     if (c.page == 0 || c.page > (1u << 20)) return "page must be in 1 .. 2^20";
-    if ((uint64_t)c.width * c.page > 0x7fffffffull) return "width x page must be below 2^31";
+    if ((uint64_t)c.width * c.page > 1ull << 30) return "width x page must be at most 2^30";
     if (c.heads == 0 || c.heads > 4096) return "heads must be in 1 .. 4096";
     if (c.dim == 0 || c.dim > 256) return "dim must be in 1 .. 256";
     if (bad_type(c.type)) return "unknown element type";

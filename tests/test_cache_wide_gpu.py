@@ -178,3 +178,19 @@ def test_room_for_more(kind, n, g, b):
         check_attend({k: t[:some] for k, t in got.items()}, want, kind)
     torch.testing.assert_close(one["out"], two["out"], rtol=2e-2 if kind == "bf16" else 1e-4, atol=1e-2 if kind == "bf16" else 1e-5)
     torch.testing.assert_close(one["lse"], two["lse"], rtol=1e-5, atol=1e-5)
+
+
+@pytest.mark.parametrize("kind, n, g", [("f32", 4, 2), ("bf16", 4, 2), ("f16", 40, 2), ("bf16", 100, 3)])
+@pytest.mark.parametrize("masked", [False, True])
+def test_nodes_behind_the_tables_end(kind, n, g, masked):
+    """Nodes that the table has no slot for are seen by nobody; they themselves see what is there."""
+    r = np.random.default_rng(42)
+    kc, vc, table = cache(r, 2, 112, 16, 1, 64, kind)
+    fill(r, kc, vc, table, [112, 112], kind)
+    lens = [112 - n // 2, 112]
+    q = rand(r, 2, n, g, 64, kind=kind)
+    mask = np.ones((n, n), bool) if masked else None
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = ops.tree_attention(q, kc, vc, table, i32(lens), mask=torch.from_numpy(mask).cuda() if masked else None, status=status)
+    check_attend(got, co.attend(host(q), host(kc), host(vc), table.cpu().numpy(), lens, mask, kind=kind), kind)
+    assert status.item() == capi.PER_DEVFLAG_BAD_INDEX
