@@ -172,9 +172,16 @@ __device__ __forceinline__ void absent_rows(const AttendArgs &a, const FastDiv &
     const unsigned rows = a.nodes * by_group.d, dim = a.c.dim;
     const unsigned z0 = max(row0, live), z1 = min(row0 + m, rows);
     if (z0 >= z1) return;
-    for (unsigned u = t; u < (z1 - z0) * dim; u += threads) {
-        const unsigned r = z0 + u / dim, d = u % dim, node = by_group.div(r), head = h * by_group.d + r - node * by_group.d;
-        static_cast<T *>(a.out)[b * a.so[0] + node * a.so[1] + head * a.so[2] + d] = from_f32<T>(0.0f);
+    const unsigned eights = (dim + 7) / 8;
+    for (unsigned u = t; u < (z1 - z0) * eights; u += threads) {
+        const unsigned r = z0 + u / eights, d = u % eights * 8, node = by_group.div(r), head = h * by_group.d + r - node * by_group.d;
+        T *to = static_cast<T *>(a.out) + b * a.so[0] + node * a.so[1] + head * a.so[2] + d;
+        if (a.ovec) {
+#pragma unroll
+            for (int e = 0; e < 8; e += 16 / (int)sizeof(T)) *reinterpret_cast<uint4 *>(to + e) = make_uint4(0, 0, 0, 0);
+        } else {
+            for (unsigned e = 0; e < 8 && d + e < dim; ++e) to[e] = from_f32<T>(0.0f);
+        }
         if (d == 0 && a.lse) a.lse[((size_t)b * a.nodes + node) * a.q_heads + head] = -INFINITY;
     }
 }

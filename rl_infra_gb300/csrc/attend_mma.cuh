@@ -186,6 +186,41 @@ __device__ __forceinline__ void values(float (*o)[4], const float (*p)[4], const
     }
 }
 
+// Hides the scores of a warp's keys that its rows' nodes (node < 0: no such row) do not see: first is the tile's first key,
+// there(r) whether its key r has a page.  Every mask byte is asked for (places outside the tree clamped), so that none
+// waits behind a branch for the one before it.
+template <int KW, typename There>
+__device__ __forceinline__ void hide(float (*sc)[4], const AttendArgs &a, unsigned b, const Span &s, const int *node, unsigned first,
+                                     unsigned key0, There there)
+{
+    const unsigned q4 = threadIdx.x & 3u;
+    const int nodes = s.total - s.len;                     // that the table has a place for
+    const bool bytes = a.mask && nodes > 0;
+    unsigned see[2] = {~0u, ~0u};                          // of the thread's columns, by node
+    static_assert(KW / 4 <= 32, "");
+    if (bytes) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint8_t *row = a.mask + b * a.sm[0] + (long long)max(node[e], 0) * a.sm[1];
+            see[e] = 0;
+#pragma unroll
+            for (int i = 0; i < KW / 4; ++i) {
+                const int j = (int)(first + key0 + (i >> 1) * 8 + q4 * 2 + (i & 1)) - s.len;
+                see[e] |= row[min(max(j, 0), nodes - 1)] != 0 ? 1u << i : 0u;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < KW / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const unsigned r = key0 + i * 8 + q4 * 2 + (e & 1);
+            const int j = (int)(first + r) - s.len, n = node[e >> 1];
+            const bool tree = bytes ? (see[e >> 1] >> (2 * i + (e & 1))) & 1u : j <= n;
+            if (n < 0 || !(j < 0 || (j < nodes && tree)) || !there(r)) sc[i][e] = -INFINITY;
+        }
+}
+
 // The softmax's step for a warp's scores sc (in log2 already), in place: maxima and sums of rows g and g + 8 carried on, o
 // brought to the new maxima.  A thread's sums are its own columns' alone.
 template <int DP, int KW>

@@ -244,16 +244,10 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                 for (int i = 0; i < KW / 8; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sc[i][e] *= a.c2;
-                if (tail_in || wrong) {
-#pragma unroll
-                    for (int i = 0; i < KW / 8; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const unsigned r = key0 + i * 8 + q4 * 2 + (e & 1), box = r >> shift;
-                            const bool there = !((tail.bad[st][box >> 5] >> (box & 31u)) & 1u);
-                            if (!there || node[e >> 1] < 0 || !sees(a, b, s, node[e >> 1], tile * KT + r)) sc[i][e] = -INFINITY;
-                        }
-                }
+                if (tail_in || wrong)
+                    hide<KW>(sc, a, b, s, node, tile * KT, key0, [&](unsigned r) {
+                        return !wrong || !((tail.bad[st][r >> shift >> 5] >> (r >> shift & 31u)) & 1u);
+                    });
                 soften<DP, KW>(sc, top, sum, o);
                 if (!tail_in && !(ok = __all_sync(0xffffffffu, bar_wait(full + 8 * (ST + st), phase, dead)))) break;
                 values<T, DP, KW>(o, sc, vs, KT, key0, halves);
@@ -442,7 +436,9 @@ cudaError_t rows_d(const AttendArgs &a, int type, const DeviceInfo &dev, cudaStr
 {
     const unsigned n = a.nodes * (a.q_heads / a.c.heads);
     if (n <= 16) return rows<T, DP, 1>(a, type, dev, st, bytes);
-    if constexpr (DP * sizeof(T) < 1024) {   // (64 rows of 1024 bytes in two parts leave no room for tiles)
+    // binary32 rows lie in two parts: with 64 of them one CTA fills an SM, and its four warps wait for one another's
+    // products; with 32 there are two CTAs (136 rows of 96 entries: 930 us against 460)
+    if constexpr (sizeof(T) == 2) {
         if (n > 32) return rows<T, DP, 4>(a, type, dev, st, bytes);
     }
     return rows<T, DP, 2>(a, type, dev, st, bytes);

@@ -147,16 +147,8 @@ __global__ void __launch_bounds__(kThreads) k_attend_any(AttendArgs a, unsigned 
             for (int i = 0; i < KT / 8; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sc[i][e] *= a.c2;
-            if (masked) {
-#pragma unroll
-                for (int i = 0; i < KT / 8; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const unsigned r = i * 8 + q4 * 2 + (e & 1);
-                        const bool there = ((r < 32 ? there0 : there1) >> (r & 31u)) & 1u;
-                        if (!there || node[e >> 1] < 0 || !sees(a, b, s, node[e >> 1], tile * KT + r)) sc[i][e] = -INFINITY;
-                    }
-            }
+            if (masked)
+                hide<KT>(sc, a, b, s, node, tile * KT, 0, [&](unsigned r) { return ((r < 32 ? there0 : there1) >> (r & 31u) & 1u) != 0; });
             soften<DP, KT>(sc, top, sum, o);
             values<T, DP, KT>(o, sc, vs, KT, 0, halves);
             if (odd)
