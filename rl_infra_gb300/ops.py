@@ -473,6 +473,7 @@ def gated_scan(a, x, h0=None, resets=None, gate=GATE_DECAY, reverse=False):
 
 _NO_STRIDES = (0, 0, 0)
 _ENDLESS = 1 << 20
+_WORK = {}             # scratch memory by shape and alignment (a number that the library works out)
 
 
 def _serving(*tensors):
@@ -577,21 +578,35 @@ def tree_attention(q, k_cache, v_cache, block_table, lens, mask=None, counts=Non
     if _elsewhere(stream, dev):
         with _On(stream, dev, (q, k_cache, v_cache, block_table, lens, mask, counts, work), out, status):
             return tree_attention(q, k_cache, v_cache, block_table, lens, mask, counts, scale, out, work, status)
-    got = {"out": _given(out, "out", q.shape, q.dtype, dev, q),
-           "lse": _given(out, "lse", (b, n, hq), torch.float32, dev, q)}
-    if out is not None and not got["lse"].is_contiguous():
-        raise _bad("lse", "contiguous", got["lse"])
+    if out is None:
+        place = q.device
+        got = {"out": torch.empty(q.shape, dtype=q.dtype, device=place),
+               "lse": torch.empty((b, n, hq), dtype=torch.float32, device=place)}
+    else:
+        got = {"out": _given(out, "out", q.shape, q.dtype, dev, q),
+               "lse": _given(out, "lse", (b, n, hq), torch.float32, dev, q)}
+        if not got["lse"].is_contiguous():
+            raise _bad("lse", "contiguous", got["lse"])
     lib = _library()
     shape = (*head, b, n, hq, dim ** -0.5 if scale is None else scale, *q.stride()[:3], *got["out"].stride()[:3], *sm)
+    packed = _ATTEND.pack(*shape, 0)
     if work is None:
-        size = _work_bytes(lib, _ATTEND.pack(*shape, 0), kp, vp)
-        work = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
+        key = (packed, kp & 15, vp & 15, dev)       # all that the size depends on
+        size = _WORK.get(key)
+        if size is None:
+            if len(_WORK) >= 4096:
+                _WORK.clear()
+            size = _WORK[key] = _work_bytes(lib, packed, kp, vp)
+        if size:
+            work = torch.empty(size, dtype=torch.uint8, device=q.device)
     elif not isinstance(work, torch.Tensor) or work.dtype is not torch.uint8 or work.get_device() != dev or \
             not work.is_contiguous():
         raise _bad("work", f"contiguous, of dtype uint8, on cuda:{dev}", work)
+    wp = None
+    if work is not None:
+        packed, wp = _ATTEND.pack(*shape, work.numel()), work.data_ptr()
     _check(lib.per_tree_attention(
-        _ATTEND.pack(*shape, work.numel() if work is not None else 0), q.data_ptr(), kp, vp, tp, lp, np_, mp,
-        got["out"].data_ptr(), got["lse"].data_ptr(), work.data_ptr() if work is not None else None,
+        packed, q.data_ptr(), kp, vp, tp, lp, np_, mp, got["out"].data_ptr(), got["lse"].data_ptr(), wp,
         _status_ptr(status, dev), _raw_stream(dev)), "tree_attention")
     return got
 

@@ -194,3 +194,37 @@ def test_nodes_behind_the_tables_end(kind, n, g, masked):
     got = ops.tree_attention(q, kc, vc, table, i32(lens), mask=torch.from_numpy(mask).cuda() if masked else None, status=status)
     check_attend(got, co.attend(host(q), host(kc), host(vc), table.cpu().numpy(), lens, mask, kind=kind), kind)
     assert status.item() == capi.PER_DEVFLAG_BAD_INDEX
+
+
+@pytest.mark.parametrize("kind, n, g, d", [("bf16", 1024, 2, 64), ("f32", 300, 1, 32), ("f16", 1024, 1, 256)])
+def test_the_most_nodes(kind, n, g, d):
+    attend_case(43, kind, 1, n, 1, g, d, 64, [100], masks="tree" if n < 1024 else None)
+
+
+def test_a_first_call_can_be_captured():
+    """In a new process, whose first call of each kernel is under capture."""
+    code = """
+import torch
+from rl_infra_gb300 import ops
+kc = torch.randn(40, 16, 2, 64, device="cuda", dtype=torch.bfloat16)
+vc, table = torch.randn_like(kc), torch.arange(40, device="cuda", dtype=torch.int32)[None]
+lens = torch.tensor([500], device="cuda", dtype=torch.int32)
+qs = [torch.randn(1, n, 2 * g, 64, device="cuda", dtype=torch.bfloat16) for n, g in ((1, 4), (9, 2), (60, 2))]
+new = torch.randn(1, 60, 2, 64, device="cuda", dtype=torch.bfloat16)
+side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph, stream=side):
+    ops.cache_append(new, new, kc, vc, table, lens)
+    got = [ops.tree_attention(q, kc, vc, table, lens) for q in qs]
+    ops.cache_keep(kc, vc, table, lens, lens[None], torch.zeros_like(lens))
+graph.replay()
+torch.cuda.synchronize()
+for q, x in zip(qs, got):
+    assert torch.equal(x["out"], ops.tree_attention(q, kc, vc, table, lens)["out"])
+"""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=120)
+    assert done.returncode == 0, done.stderr[-2000:]
