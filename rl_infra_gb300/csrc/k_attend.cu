@@ -19,7 +19,9 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr unsigned kBegin = 2;   // tiles that a sequence's begin and end are worth
-constexpr unsigned kFew = 32;    // rows of a head of keys that the warp-wide instruction takes
+// Rows of a head of keys that the warp-wide instruction takes: it is quicker to begin, the tensor cores' own one to go on
+// (16 trees, up to 4000 tokens: 48 rows 64.6 us against 79.7 warp-wide; 16 of 8000, 32 rows 83 us warp-wide against 108).
+constexpr unsigned kFew = 32;
 
 template <typename T, int DP>
 struct Cfg {
