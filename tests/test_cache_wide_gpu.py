@@ -228,3 +228,21 @@ for q, x in zip(qs, got):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=120)
     assert done.returncode == 0, done.stderr[-2000:]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("n, g", [(40, 1), (40, 5)])
+def test_scores_of_minus_infinity(kind, n, g):
+    """Whole tiles of keys that score -inf, first, in between and last; then nothing else."""
+    r = np.random.default_rng(44)
+    kc, vc, table = cache(r, 1, 700, 16, 1, 64, kind)
+    fill(r, kc, vc, table, [700], kind)
+    tab = table.cpu().numpy()
+    for s in [*range(0, 260), *range(400, 520), *range(530, 640, 3)]:
+        kc[co.place(tab[0], s, 16, kc.shape[0])] = -INF
+    q = rand(r, 1, n, g, 64, kind=kind).abs()
+    got = ops.tree_attention(q, kc, vc, table, i32([650]))
+    check_attend(got, co.attend(host(q), host(kc), host(vc), tab, [650], kind=kind), kind)
+    kc.fill_(-INF)
+    got = ops.tree_attention(q, kc, vc, table, i32([650]))
+    assert (got["out"] == 0).all() and (got["lse"] == -INF).all()
