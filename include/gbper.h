@@ -575,8 +575,8 @@ typedef struct {
  * i >= m.  What a node does not see takes no part, whatever it holds (infinities and NaN too).  N = 1
  * is the step of plain decoding.  Products of 16-bit types are summed in binary32, scores and their
  * sums are binary32, and p is rounded once to the type before its product with v (the sum of p is
- * not); binary32 entries are taken as two parts whose products give 21 bits (an infinite entry then gives
- * NaN).  Out is rounded once.
+ * not; as float16, a p below 2^-25 of its row's largest is off by up to 2^-36 of that).  binary32 entries are
+ * taken as two parts whose products give 21 bits (an infinite entry then gives NaN).  Out is rounded once.
  *   d_q, d_out [B x N x Hq x D] (not the same memory), d_mask [B x N x N] bytes, d_lens, d_counts [B] int32 (counts NULL: N),
  *   d_table [B x width] int32, d_lse [B x N x Hq] float (contiguous) or NULL, d_work: work_bytes of scratch
  *   memory (16-byte aligned) that this call alone uses until it has run; per_tree_attention_work says

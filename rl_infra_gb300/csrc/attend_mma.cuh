@@ -221,9 +221,20 @@ __device__ __forceinline__ void hide(float (*sc)[4], const AttendArgs &a, unsign
         }
 }
 
+// What a row's p and sum refer to, for its maximum so far (in log2).  p goes into a product as T: a float16 holds 11 bits down
+// to 2^-14 and nothing below 2^-25, so that under one key far above the others theirs would be lost from the product, though
+// not from the sum (8000 keys 18 nats below one whose value is 0: 0.5% off).  Referred to 2^-15 of the maximum, p uses the
+// type's upper end too: 11 bits down to 2^-29 of the maximum, off by at most 2^-40 of it below.  (From 2^22 on the
+// difference would be rounded.  bfloat16 and binary32 have the range: their p is at most 1.)
+template <typename T>
+__device__ __forceinline__ float below(float top)
+{
+    return std::is_same<T, __half>::value && fabsf(top) < 4194304.0f ? top - 15.0f : top;
+}
+
 // The softmax's step for a warp's scores sc (in log2 already), in place: maxima and sums of rows g and g + 8 carried on, o
-// brought to the new maxima.  A thread's sums are its own columns' alone.
-template <int DP, int KW>
+// brought to the new maxima (p, sums and o refer to below(top)).  A thread's sums are its own columns' alone.
+template <typename T, int DP, int KW>
 __device__ __forceinline__ void soften(float (*sc)[4], float *top, float *sum, float (*o)[4])
 {
     float keep[2], base[2], up[2] = {top[0], top[1]};
@@ -235,8 +246,8 @@ __device__ __forceinline__ void soften(float (*sc)[4], float *top, float *sum, f
     for (int e = 0; e < 2; ++e) {
         up[e] = fmaxf(up[e], __shfl_xor_sync(0xffffffffu, up[e], 1));
         up[e] = fmaxf(up[e], __shfl_xor_sync(0xffffffffu, up[e], 2));
-        base[e] = up[e] == -INFINITY ? 0.0f : up[e];      // nothing seen yet: every p is 2^-inf = 0
-        keep[e] = ex2(top[e] - base[e]);
+        base[e] = up[e] == -INFINITY ? 0.0f : below<T>(up[e]);      // nothing seen yet: every p is 2^-inf = 0
+        keep[e] = ex2(below<T>(top[e]) - base[e]);
         top[e] = up[e];
         sum[e] *= keep[e];
     }

@@ -254,7 +254,7 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                     hide<KW>(sc, a, b, s, node, tile * KT, key0, [&](unsigned r) {
                         return !wrong || !((tail.bad[st][r >> shift >> 5] >> (r >> shift & 31u)) & 1u);
                     });
-                soften<DP, KW>(sc, top, sum, o);
+                soften<T, DP, KW>(sc, top, sum, o);
                 if (!tail_in && !(ok = __all_sync(0xffffffffu, bar_wait(full + 8 * (ST + st), phase, dead)))) break;
                 values<T, DP, KW>(o, sc, vs, KT, key0, halves);
                 if (odd)
@@ -278,6 +278,7 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
             for (int e = 0; e < 2; ++e) {
                 sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
                 sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
+                top[e] = below<T>(top[e]);      // from here on what the sums refer to
             }
 
             // the warps that share rows join: the upper two hand their sums to the lower two; what is left lies in one

@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_any(AttendArgs a, unsigned 
                 for (int e = 0; e < 4; ++e) sc[i][e] *= a.c2;
             if (masked)
                 hide<KT>(sc, a, b, s, node, tile * KT, 0, [&](unsigned r) { return ((r < 32 ? there0 : there1) >> (r & 31u) & 1u) != 0; });
-            soften<DP, KT>(sc, top, sum, o);
+            soften<T, DP, KT>(sc, top, sum, o);
             values<T, DP, KT>(o, sc, vs, KT, 0, halves);
             if (odd)
                 for (unsigned r = 0; r < KT; ++r) {
@@ -164,6 +164,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_any(AttendArgs a, unsigned 
         for (int e = 0; e < 2; ++e) {
             sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
             sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
+            top[e] = below<T>(top[e]);      // from here on what the sums refer to
         }
         // out, by way of the queries' place, 16 columns at a time
         const RowOut<T> out{a, by_group, b, h, live, row0, M, w.part(), slots + (w.tile0 != 0 ? 0 : slot_floats)};

@@ -9,15 +9,15 @@
 //     more:            each group takes 128 of up to 256 rows, and both every tile.
 // While one group turns scores into p (written over them, rounded to the type), the other's products run.
 //
-// The maximum that p refers to is raised only where a row's rises by more than 2^8 (exact all the same: p and
-// its sums keep their relative precision, and stay below 2^8 x 2^31): outputs in tensor memory are then
+// The maximum that p refers to is raised only where a row's rises by more than 2^8 (float16: 2^4; exact all the same: p and
+// its sums keep their relative precision, and stay below 2^16 x 2^31): outputs in tensor memory are then
 // scaled, which is rare.  So p is worked out in one pass over the scores, which also finds their maximum; where that
 // has risen, the pass is made again.
 //
 // Measured (GB300): 32 trees of 64 nodes, 64 query heads on 8, up to 6000 tokens, bf16 294 us, 901 TFLOP/s (a chain of
 // the softmax, 1250 cycles a tile of 128 x 128, and two products of 512 each, while the other group does the same; the
-// tensor cores are busy half of the time); 16 trees of 24 nodes, 96 rows a head of 64 entries, up to 8000 tokens, f16 57 us,
-// 3.35 TB/s.  With the warp-wide instruction 1611 and 236 us.
+// tensor cores are busy half of the time); 16 trees of 24 nodes, 96 rows a head of 64 entries, up to 8000 tokens, f16 59 us,
+// 3.26 TB/s.  With the warp-wide instruction 1611 and 236 us.
 //
 // What was tried and not kept: registers dealt anew between the warps (setmaxnreg; the compiler then spilled 2.4 KB a
 // thread: 2309 us); outputs by way of shared memory, mask bytes asked for without branches, a warp without rows that skips
@@ -35,7 +35,12 @@ namespace {
 constexpr int kGroups = 2, kThreads = kGroups * 128 + 96;   // and two warps for the copies, one for the products
 constexpr unsigned kBegin = 6;                               // tiles that a sequence's begin and end are worth
 constexpr int KT = 128;                                      // keys of a tile, and rows of a group
-constexpr float kRise = 8.0f;
+// What a row's maximum may rise above the one that p refers to, in log2, and what p = 2^(s - top + kUp) has there: a float16
+// uses its upper end too (p below 2^15.8, with top's own rounding), for what `below` in attend_mma.cuh says: 11 bits down
+// to 2^-25.5 of the maximum, off by at most 2^-36.5 of it below.  Each rise costs a second pass over a tile's scores: with 2
+// and 13 there were so many that 32 trees of 64 nodes took 371 us, with 4 284 us, as with 8.
+template <typename T> constexpr float kRise = std::is_same<T, __half>::value ? 4.0f : 8.0f;
+template <typename T> constexpr float kUp = std::is_same<T, __half>::value ? 11.5f : 0.0f;
 constexpr int kColumns = 512;                                // of tensor memory: two of scores, two of outputs, 128 each
 
 template <bool PAIR>
@@ -383,7 +388,7 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                 unsigned p[KT / 2];
                 F2 add[2];
                 for (;;) {
-                    const float off = raw_none ? 0.0f : top;
+                    const float off = raw_none ? 0.0f : top - kUp<T>;
                     const F2 c2 = {a.c2, a.c2}, less = {-off, -off};
                     float most = -INFINITY;
                     add[0] = add[1] = F2{0.0f, 0.0f};
@@ -411,7 +416,7 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                             p[16 * i + k] = pack2<T>(x.x, x.y);
                         }
                     }
-                    const bool rise = most > -INFINITY && (raw_none || (most - ref) * a.c2 > kRise);
+                    const bool rise = most > -INFINITY && (raw_none || (most - ref) * a.c2 > kRise<T>);
                     if (!__any_sync(0xffffffffu, rise)) break;
                     const float now = rise ? most * a.c2 : top;
                     const float keep = rise ? (raw_none ? 0.0f : ex2(top - now)) : 1.0f;
@@ -447,7 +452,7 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
             if (has) ok = __all_sync(0xffffffffu, bar_wait(o_full + 8 * g, outs & 1, dead));
             if (!ok) break;
             if (has) ++outs;
-            const float mine = raw_none ? -INFINITY : top;
+            const float mine = raw_none ? -INFINITY : top - kUp<T>;
             if constexpr (!PAIR) {
                 tail.ml[g * 128 + r][0] = mine;
                 tail.ml[g * 128 + r][1] = l;

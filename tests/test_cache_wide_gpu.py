@@ -246,3 +246,36 @@ def test_scores_of_minus_infinity(kind, n, g):
     kc.fill_(-INF)
     got = ops.tree_attention(q, kc, vc, table, i32([650]))
     assert (got["out"] == 0).all() and (got["lse"] == -INF).all()
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("n, g, d", [(1, 4, 64), (6, 4, 64), (12, 4, 128), (40, 1, 64), (20, 5, 128), (40, 4, 64), (40, 5, 128), (3, 2, 256),
+                                     (9, 5, 33)])
+@pytest.mark.parametrize("nats, ctx", [(14, 8000), (16, 8000), (17.5, 8000), (18, 30000), (19, 8000)])
+def test_one_key_far_above_the_others(kind, n, g, d, nats, ctx):
+    """A key that takes nearly all of the mass and whose value is 0, first or last: the output is what the many others
+    have left, each of them w = exp(-nats) of the maximum.  All scores are exact, so that out is sum(v) over
+    exp(nats) + the others: off by out's rounding and p's (half a step each), and 2^-12 for the references and sums.  A
+    float16 below 2^-14 is off by 2^-25: p is w 2^15 where a head of keys has few rows, and at least w 2^11.5 on the tensor
+    cores' own instruction."""
+    r = np.random.default_rng(45)
+    kc, vc, table = cache(r, 1, ctx + n, 16, 1, d, kind)
+    kc.zero_()
+    vc.copy_((rand(r, *vc.shape, kind="f32").abs() * 100 + 1).to(TYPES[kind]))
+    q = torch.zeros(1, n, g, d, dtype=TYPES[kind], device="cuda")
+    q[..., 0] = 1
+    tab = table.cpu().numpy()
+    mask = torch.zeros(n, n, dtype=torch.bool, device="cuda")
+    for at in (0, ctx - 1):
+        top = co.place(tab[0], at, 16, kc.shape[0])
+        keep = kc[top].clone(), vc[top].clone()
+        kc[top[0], top[1], 0, 0], vc[top] = nats, 0
+        got = ops.tree_attention(q, kc, vc, table, i32([ctx]), mask=mask, scale=1.0)
+        values = host(vc[table[0].long()].reshape(-1, d)[:ctx])
+        want = values.sum(0) / (np.exp(nats) + ctx - 1)
+        half = torch.finfo(TYPES[kind]).eps / 2
+        err = np.abs(host(got["out"]) - want) / want
+        rounds = half if kind == "bf16" else max(half, 2.0 ** -25 / (np.exp(-nats) * 2 ** (11.5 if n * g > 32 and d <= 128 else 15)))
+        assert err.max() <= half + rounds + 2.0 ** -12, err.max()
+        np.testing.assert_allclose(host(got["lse"]), np.log(np.exp(nats) + ctx - 1), rtol=1e-5)
+        kc[top], vc[top] = keep
