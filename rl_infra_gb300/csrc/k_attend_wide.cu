@@ -16,8 +16,8 @@
 //
 // Measured (GB300): 32 trees of 64 nodes, 64 query heads on 8, up to 6000 tokens, bf16 294 us, 901 TFLOP/s (a chain of
 // the softmax, 1250 cycles a tile of 128 x 128, and two products of 512 each, while the other group does the same; the
-// tensor cores are busy half of the time); 16 trees of 24 nodes, 96 rows a head of 64 entries, up to 8000 tokens, f16 59 us,
-// 3.26 TB/s.  With the warp-wide instruction 1611 and 236 us.
+// tensor cores are busy half of the time); 16 trees of 24 nodes, 96 rows a head of 64 entries, up to 8000 tokens, f16 57 us,
+// 3.36 TB/s.  With the warp-wide instruction 1611 and 236 us.
 //
 // What was tried and not kept: registers dealt anew between the warps (setmaxnreg; the compiler then spilled 2.4 KB a
 // thread: 2309 us); outputs by way of shared memory, mask bytes asked for without branches, a warp without rows that skips
@@ -36,7 +36,7 @@ constexpr int kGroups = 2, kThreads = kGroups * 128 + 96;   // and two warps for
 constexpr unsigned kBegin = 6;                               // tiles that a sequence's begin and end are worth
 constexpr int KT = 128;                                      // keys of a tile, and rows of a group
 // What a row's maximum may rise above the one that p refers to, in log2, and what p = 2^(s - top + kUp) has there: a float16
-// uses its upper end too (p below 2^15.8, with top's own rounding), for what `below` in attend_mma.cuh says: 11 bits down
+// uses its upper end too (p up to 2^15.5), for what `below` in attend_mma.cuh says: 11 bits down
 // to 2^-25.5 of the maximum, off by at most 2^-36.5 of it below.  Each rise costs a second pass over a tile's scores: with 2
 // and 13 there were so many that 32 trees of 64 nodes took 371 us, with 4 284 us, as with 8.
 template <typename T> constexpr float kRise = std::is_same<T, __half>::value ? 4.0f : 8.0f;
@@ -129,6 +129,24 @@ __device__ __forceinline__ void put32(unsigned at, const unsigned *v)
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
                  "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::WORDS32(v), "r"(at) : "memory");
+}
+
+// A reference past kFar in log2 cannot stay one: its own rounding would be a power of two or more in p = 2^(s c2 - top) (at
+// 2^31 as much as binary32 holds).  What such a row refers to is taken off its scores themselves, in tensor memory.
+constexpr float kFar = 4194304.0f;
+__device__ __forceinline__ void take_off(unsigned my_s, float shift)
+{
+#pragma unroll 1
+    for (unsigned i = 0; i < KT / 32; ++i) {
+        float sc[32];
+        get32(sc, my_s + 32 * i);
+        wait_ld();
+        loaded32(sc);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) sc[k] -= shift;
+        put32(my_s + 32 * i, sc);
+    }
+    wait_st();
 }
 
 // the scores of 32 keys that are not seen
@@ -347,9 +365,8 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
             }
             const int node = my_row < live ? (int)by_group.div(my_row) : -1;
             const unsigned tiles = w.tile1 - w.tile0;
-            float top = -INFINITY, l = 0.0f;      // what p refers to (in log2), and the sum of p
-            bool raw_none = true;                 // nothing seen yet
-            float ref = 0.0f;                     // top as a score
+            float top = -INFINITY, l = 0.0f;      // what p refers to (in log2; -inf: nothing seen yet), and the sum of p
+            float taken = 0.0f;                   // what is taken off the row's scores
             // before there is anything to wait for: whether the stretch has a page that does not exist (then, and at the
             // sequence's end, a tile's values are waited for before its scores are used), and what the row sees of the
             // first tile with nodes
@@ -379,16 +396,19 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
                 const bool masked = tail_in || holes;
-                if (masked && (tile != known || holes)) {
-                    seen(a, b, s, node, tile * KT, tail.bad[slot], holes, shift, word);
-                    known = ~0u;
+                if (masked) {
+                    if (tile != known || holes) {
+                        seen(a, b, s, node, tile * KT, tail.bad[slot], holes, shift, word);
+                        known = ~0u;
+                    }
+                    if (__any_sync(0xffffffffu, taken != 0.0f)) take_off(my_s, taken);
                 }
                 // p against the maximum so far, a quarter of the row at a time, and the row's maximum on the way; once more
                 // where that has risen (the scores are still there: p is written when it stands)
                 unsigned p[KT / 2];
                 F2 add[2];
                 for (;;) {
-                    const float off = raw_none ? 0.0f : top - kUp<T>;
+                    const float off = top == -INFINITY ? 0.0f : top - kUp<T>;
                     const F2 c2 = {a.c2, a.c2}, less = {-off, -off};
                     float most = -INFINITY;
                     add[0] = add[1] = F2{0.0f, 0.0f};
@@ -416,15 +436,21 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                             p[16 * i + k] = pack2<T>(x.x, x.y);
                         }
                     }
-                    const bool rise = most > -INFINITY && (raw_none || (most - ref) * a.c2 > kRise<T>);
+                    // (NaN, no rise, where nothing is seen even now)
+                    const bool rise = fmaf(most, a.c2, -top) > kRise<T>;
                     if (!__any_sync(0xffffffffu, rise)) break;
-                    const float now = rise ? most * a.c2 : top;
-                    const float keep = rise ? (raw_none ? 0.0f : ex2(top - now)) : 1.0f;
-                    if (rise) {
-                        ref = most;
-                        top = now;
-                        raw_none = false;
+                    const float now = most * a.c2;
+                    float keep = rise ? ex2(top - now) : 1.0f;
+                    const bool far = rise && !(fabsf(now) < kFar);
+                    if (__any_sync(0xffffffffu, far)) {
+                        holes = true;             // (the tiles to come take the way with the branches)
+                        take_off(my_s, far ? most : 0.0f);
+                        if (far) {
+                            keep = ex2(fmaf(-most, a.c2, top));
+                            taken += most;
+                        }
                     }
+                    if (rise) top = far ? 0.0f : now;
                     l *= keep;
                     if (j >= 2 || (PAIR && j >= 1)) {   // there are outputs
 #pragma unroll 1
@@ -452,7 +478,7 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
             if (has) ok = __all_sync(0xffffffffu, bar_wait(o_full + 8 * g, outs & 1, dead));
             if (!ok) break;
             if (has) ++outs;
-            const float mine = raw_none ? -INFINITY : top - kUp<T>;
+            const float mine = fmaf(taken, a.c2, top) - kUp<T>;
             if constexpr (!PAIR) {
                 tail.ml[g * 128 + r][0] = mine;
                 tail.ml[g * 128 + r][1] = l;

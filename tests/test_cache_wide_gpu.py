@@ -13,6 +13,7 @@ if not torch.cuda.is_available():  # pragma: no cover
 
 from rl_infra_gb300 import build, capi, ops  # noqa: E402
 from tests import cache_oracle as co  # noqa: E402
+from tests.ops_oracle import TINY  # noqa: E402
 from tests.test_cache_gpu import INF, NAN, TYPES, attend_case, cache, check_attend, fill, host, i32, rand, tree  # noqa: E402
 
 
@@ -279,3 +280,72 @@ def test_one_key_far_above_the_others(kind, n, g, d, nats, ctx):
         assert err.max() <= half + rounds + 2.0 ** -12, err.max()
         np.testing.assert_allclose(host(got["lse"]), np.log(np.exp(nats) + ctx - 1), rtol=1e-5)
         kc[top], vc[top] = keep
+
+
+@pytest.mark.parametrize("kind, big", [("bf16", 6e4), ("bf16", 1e9), ("bf16", 1e18), ("f16", 6e4), ("f16", 2e3)])
+@pytest.mark.parametrize("n, g, d", [(3, 4, 64), (40, 1, 64), (40, 1, 128), (40, 5, 128), (70, 2, 64)])
+@pytest.mark.parametrize("steps", [(1.0, 1.0, 1.0), (1e-6, 1.0, 3.0), (1.0, 1e-3, 1e-7)])
+def test_large_scores(kind, big, n, g, d, steps):
+    """Scores of up to 2^30 and past it, in stretches of keys of different size (references that go far at once, later,
+    or twice): a row whose first score is ahead of the second by far more than binary32's noise gives that key's value,
+    off by half a step of the type for its p (2^x for any x, over a sum that is not rounded) and half a step for out."""
+    r = np.random.default_rng(46)
+    half = torch.finfo(TYPES[kind]).eps / 2
+    ctx = 900
+    kc, vc, table = cache(r, 1, ctx + n, 16, 1, d, kind)
+    fill(r, kc, vc, table, [ctx + n], kind)
+    kc.copy_((r.uniform() + rand(r, *kc.shape, kind="f32").clamp(-4, 4)) * big / 5)
+    tab = table.cpu().numpy()
+    for s in range(ctx + n):
+        p, x = co.place(tab[0], s, 16, kc.shape[0])
+        kc[p, x] *= steps[min(s // 300, 2)] / max(steps)
+    q = (rand(r, 1, n, g, d, kind="f32").clamp(-4, 4) * big / 5).to(TYPES[kind])
+    got = ops.tree_attention(q, kc, vc, table, i32([ctx]))
+    keys, values = (host(t[table[0].long()].reshape(-1, d)) for t in (kc, vc))
+    out, lse, sure = host(got["out"]), host(got["lse"]), 0
+    assert np.isfinite(out).all() and np.isfinite(lse).all()
+    for i in range(n):
+        x, y = keys[:ctx + i + 1], values[:ctx + i + 1]
+        for h in range(g):
+            s = x @ host(q)[0, i, h] * d ** -0.5
+            noise = 2.0 ** -23 * (d + 8) * (np.abs(x) @ np.abs(host(q)[0, i, h])).max() * d ** -0.5
+            first, second = np.argmax(s), np.partition(s, -2)[-2]
+            assert abs(lse[0, i, h] - s[first]) <= noise + 8
+            if s[first] - second > 2 * noise + 30:
+                sure += 1
+                np.testing.assert_allclose(out[0, i, h], y[first], rtol=2.01 * half, atol=TINY[kind])
+    assert sure > n * g // 2
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("n, g, d", [(40, 1, 64), (20, 4, 128), (40, 5, 64), (40, 4, 128)])
+@pytest.mark.parametrize("far", [1, -1])
+@pytest.mark.parametrize("ctx", [700, 80])
+def test_scores_far_from_zero(kind, n, g, d, far, ctx):
+    """Scores of far 2^23 + j and small j, which binary32 holds, as 2^30 + 128 j times a scale of 2^-7: a softmax of j alone.
+    p and out are off by half a step of the type each, 2^-12 for sums (no j is 16 below the maximum).  A sequence of more than
+    one tile is joined from parts whose references, in log2, are binary32: steps of 1 there, each off by up to a half, so that a
+    part's weight is off by a factor f of 2^-0.5 to 2^0.5, and sum(w f v) / sum(w f) from its value without f by up to
+    max(f) / min(f) = 2 times the weighted mean of |v - value|."""
+    r = np.random.default_rng(47)
+    kc, vc, table = cache(r, 1, ctx + n, 16, 1, d, kind)
+    vc.copy_(rand(r, *vc.shape, kind="f32").abs() + 1)
+    kc.zero_()
+    j = torch.from_numpy(r.integers(0, 8, kc.shape[:3]).astype(np.float32)).cuda()
+    tab = table.cpu().numpy()
+    for s in range(ctx):                       # maxima that rise from tile to tile
+        p, x = co.place(tab[0], s, 16, kc.shape[0])
+        j[p, x] += s // 90
+    kc[..., 0], kc[..., 1] = 2.0 ** 15, j
+    q = torch.zeros(1, n, g, d, dtype=TYPES[kind], device="cuda")
+    q[..., 0], q[..., 1] = far * 2.0 ** 15, 128
+    mask = torch.zeros(n, n, dtype=torch.bool, device="cuda")
+    got = ops.tree_attention(q, kc, vc, table, i32([ctx]), mask=mask, scale=2.0 ** -7)
+    line = lambda t: host(t[table[0].long()]).reshape(-1, *t.shape[3:])[:ctx]
+    p = np.exp(line(j) - line(j).max())
+    want = p / p.sum() @ line(vc)
+    half = torch.finfo(TYPES[kind]).eps / 2
+    joins = 2 * (p / p.sum() @ np.abs(line(vc) - want)) / want if ctx + n > 128 else 0
+    err = np.abs(host(got["out"]) - want) / want
+    assert (err <= 2 * half + 2.0 ** -12 + joins).all(), err.max()
+    np.testing.assert_allclose(host(got["lse"]), far * 2.0 ** 23 + np.log(p.sum()) + line(j).max(), atol=2)
