@@ -564,6 +564,10 @@ typedef struct {
     int64_t stride_q[3], stride_out[3];    /* between sequences, nodes, heads */
     int64_t stride_mask[2];                /* between sequences (0: one mask for all), between nodes */
     uint64_t work_bytes;   /* of d_work */
+    uint32_t wait_limit_ms; /* limit of a wait inside the kernel, 0 .. 10000 (0: 2000) */
+    uint32_t withhold;     /* 0.  To test the limit: the barrier, 1 .. 8, that waits for an arrival which never comes: of keys, of
+                              values, of a tile's release, of the warps among one another; with many rows also of queries, of
+                              scores, of p, of outputs (a kernel that has no such barrier runs as with 0) */
 } per_attend_shape;
 
 /*
@@ -585,8 +589,8 @@ typedef struct {
  * Which CTA takes which part depends on the lengths alone, and parts are joined in their order: the same
  * inputs give the same bits.  A value that is not finite gives NaN or infinity in the rows that see it.  Caches whose
  * heads begin on 16 bytes and whose axes lie in one another (each stride a multiple of the next smaller one) are copied by
- * tiles; others entry by entry, several times slower.  Waits inside the kernel have a limit of two seconds, after
- * which PER_DEVFLAG_TIMEOUT is set and results are not valid.
+ * tiles; others entry by entry, several times slower.  Waits inside the kernel have a limit, after which the kernel waits
+ * for its copies and products under way (with the same limit for each), sets PER_DEVFLAG_TIMEOUT and ends; results are not valid.
  * per_tree_attention_work -- the bytes of d_work that a call of this shape with these caches needs on the current
  * device (which kernel takes it depends on where they lie; nothing is read).
  */

@@ -107,7 +107,8 @@ class per_append_shape(ctypes.Structure):
 class per_attend_shape(ctypes.Structure):
     _fields_ = [("cache", per_cache)] + [(n, ctypes.c_uint32) for n in ("batch", "nodes", "q_heads")] + [
         ("scale", ctypes.c_float), ("stride_q", ctypes.c_int64 * 3), ("stride_out", ctypes.c_int64 * 3),
-        ("stride_mask", ctypes.c_int64 * 2), ("work_bytes", ctypes.c_uint64)]
+        ("stride_mask", ctypes.c_int64 * 2), ("work_bytes", ctypes.c_uint64), ("wait_limit_ms", ctypes.c_uint32),
+        ("withhold", ctypes.c_uint32)]
 
 
 class per_keep_shape(ctypes.Structure):

@@ -18,7 +18,8 @@ namespace attend {
 
 typedef unsigned long long u64;
 constexpr int kRecord = 8;             // ints of a CTA's record for the joining kernel
-constexpr unsigned kWaitMs = 2000;     // limit of a wait
+// barriers by the numbers of AttendArgs::withhold: one that waits for an arrival more than come, to test what follows
+enum Barrier { kKeys = 1, kValues, kRelease, kMeet, kQueries, kScores, kP, kOutputs };
 
 // ---- how the work is cut -----------------------------------------------------------------------
 struct Span {              // a sequence
@@ -283,18 +284,19 @@ __device__ __forceinline__ bool bar_try(unsigned bar, unsigned parity)
                  "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
-// Waits for the phase of the given parity to end; false when it has not after kWaitMs, or another wait of the CTA gave up.
+// Waits for the phase of the given parity to end; false when it has not after dead[1] milliseconds, or another wait of the CTA
+// gave up (dead[0]).
 static __device__ __noinline__ bool bar_wait_long(unsigned bar, unsigned parity, volatile unsigned *dead)
 {
     u64 began, now;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(began));
     for (int tries = 0; tries < 1 << 24; ++tries) {
         if (bar_try(bar, parity)) return true;
-        if (*dead) return false;
+        if (dead[0]) return false;
         asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
-        if (now - began > kWaitMs * 1000000ull) break;
+        if (now - began > dead[1] * 1000000ull) break;
     }
-    *dead = 1;
+    dead[0] = 1;
     return false;
 }
 __device__ __forceinline__ bool bar_wait(unsigned bar, unsigned parity, volatile unsigned *dead)

@@ -35,7 +35,7 @@ struct Tail {
     unsigned bad[ST][KT / 32];
     alignas(8) float ml[ML][2];   // maxima and sums that the warps hand over
     alignas(16) int boxes[2][KT];
-    unsigned dead, odd;        // odd: the number of the last tile that something was taken out of
+    unsigned dead[2], odd;     // whether a wait gave up, and their limit; odd: the number of the last tile that something was taken out of
 };
 
 template <typename T, int DP, int WR>
@@ -86,7 +86,7 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char *area = smem + ST * C::STAGE;
     typename C::End &tail = *reinterpret_cast<typename C::End *>(area + C::AREA);
-    volatile unsigned *dead = &tail.dead;
+    volatile unsigned *dead = tail.dead;
     const unsigned t = threadIdx.x, lane = t & 31u, warp = t >> 5;
     const unsigned cta = blockIdx.x, unit = share ? cta / share : cta, team = unit / row_tiles, rt = unit - team * row_tiles;
     const unsigned rank = share ? cta - unit * share : 0;         // in a cluster that shares a sequence's head and rows
@@ -96,12 +96,13 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
 
     if (t == 0) {
         for (int i = 0; i < ST; ++i) {
-            bar_init(full + 8 * i, 1);
-            bar_init(full + 8 * (ST + i), 1);
-            bar_init(empty + 8 * i, kWarps);
+            bar_init(full + 8 * i, 1 + (a.withhold == kKeys));
+            bar_init(full + 8 * (ST + i), 1 + (a.withhold == kValues));
+            bar_init(empty + 8 * i, kWarps + (a.withhold == kRelease));
         }
-        bar_init(smem_u32(&tail.meet), kWarps);
-        tail.dead = 0;
+        bar_init(smem_u32(&tail.meet), kWarps + (a.withhold == kMeet));
+        tail.dead[0] = 0;
+        tail.dead[1] = a.wait_ms;
         tail.odd = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -152,8 +153,8 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
         }
         if (!ok) {          // given up: the copies under way must land before the CTA ends
             for (unsigned i = asked > (unsigned)ST ? asked - ST : 0; i < asked; ++i) {
-                unsigned none = 0;
-                bar_wait(mine + 8 * (i % ST), i / ST & 1, &none);
+                unsigned none[2] = {0, a.wait_ms};
+                bar_wait(mine + 8 * (i % ST), i / ST & 1, none);
             }
         }
     } else {

@@ -50,7 +50,7 @@ struct Tail {
     unsigned bad[10][4];
     alignas(16) int boxes[2][KT];
     float ml[PAIR ? 1 : 256][2];   // maxima and sums, where both groups have the same rows
-    unsigned dead, odd, tmem;
+    unsigned dead[2], odd, tmem;   // whether a wait gave up, and their limit
 };
 
 template <int DP, bool PAIR>
@@ -195,7 +195,7 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char *qs = smem + ST * TILE;
     Tail<PAIR> &tail = *reinterpret_cast<Tail<PAIR> *>(qs + C::QB);
-    volatile unsigned *dead = &tail.dead;
+    volatile unsigned *dead = tail.dead;
     const unsigned t = threadIdx.x, lane = t & 31u, warp = t >> 5;
     const unsigned cta = blockIdx.x, team = cta / row_tiles, rt = cta - team * row_tiles;
     const unsigned group = by_group.d, row0 = rt * M, dim = a.c.dim, halves = (dim + 63) / 64;
@@ -204,18 +204,19 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
 
     if (t == 0) {
         for (int i = 0; i < ST; ++i) {
-            bar_init(full + 8 * i, 1);
-            bar_init(empty + 8 * i, 1);
+            bar_init(full + 8 * i, 1 + (a.withhold == (i % 2 ? kValues : kKeys)));   // (of the first round; ST may be odd)
+            bar_init(empty + 8 * i, 1 + (a.withhold == kRelease));
         }
-        bar_init(q_ready, kGroups * 4);
+        bar_init(q_ready, kGroups * 4 + (a.withhold == kQueries));
         for (int i = 0; i < 2; ++i) {
-            bar_init(s_full + 8 * i, 1);
-            bar_init(p_ready + 8 * i, 4);
-            bar_init(o_full + 8 * i, 1);
+            bar_init(s_full + 8 * i, 1 + (a.withhold == kScores));
+            bar_init(p_ready + 8 * i, 4 + (a.withhold == kP));
+            bar_init(o_full + 8 * i, 1 + (a.withhold == kOutputs));
         }
-        bar_init(smem_u32(&tail.meet), kGroups * 4);
+        bar_init(smem_u32(&tail.meet), kGroups * 4 + (a.withhold == kMeet));
         bar_init(smem_u32(&tail.last), 1);
-        tail.dead = 0;
+        tail.dead[0] = 0;
+        tail.dead[1] = a.wait_ms;
         tail.odd = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -264,8 +265,8 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
         }
         if (!ok) {             // given up: the copies under way must land before the CTA ends
             for (unsigned i = asked > (unsigned)ST + 1 ? asked - ST / 2 * 2 : val; i < asked; i += 2) {
-                unsigned none = 0;
-                bar_wait(full + 8 * (i % ST), i / ST & 1, &none);
+                unsigned none[2] = {0, a.wait_ms};
+                bar_wait(full + 8 * (i % ST), i / ST & 1, none);
             }
         }
     } else if (warp == 9) {    // the thread that issues the products
@@ -312,9 +313,9 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                 ++stretch;
             }
             if (!ok) {         // given up: nothing may run on when tensor memory is freed
-                unsigned none = 0;
+                unsigned none[2] = {0, a.wait_ms};
                 commit(smem_u32(&tail.last));
-                bar_wait(smem_u32(&tail.last), 0, &none);
+                bar_wait(smem_u32(&tail.last), 0, none);
                 if (a.c.status) atomicOr(a.c.status, PER_DEVFLAG_TIMEOUT);
             }
         }

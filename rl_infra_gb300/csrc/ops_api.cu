@@ -216,6 +216,8 @@ const char *attend_fault(const per_attend_shape *sh)
     if (((uint64_t)sh->cache.width * sh->cache.page / 32 + 3) * sh->batch * sh->cache.heads >> 45)
         return "batch x width x page x heads must be below 2^50";
     if (!std::isfinite(sh->scale) || !std::isfinite(sh->scale * 1.5f)) return "scale must be finite";
+    if (sh->wait_limit_ms > 10000) return "wait_limit_ms must be at most 10000";
+    if (sh->withhold > 8) return "withhold must be at most 8";
     return nullptr;
 }
 
@@ -496,6 +498,8 @@ per_status per_tree_attention(const per_attend_shape *shape, const void *d_q, co
     a.q_heads = shape->q_heads;
     a.c2 = (float)((double)shape->scale * 1.4426950408889634);
     a.qvec = c.dim * e % 16 == 0 && on16(d_q, shape->stride_q, 3, e);
+    a.wait_ms = shape->wait_limit_ms ? shape->wait_limit_ms : 2000;
+    a.withhold = shape->withhold;
     a.ovec = c.dim % 8 == 0 && on16(d_out, shape->stride_out, 3, e);
     unsigned long long need = 0;
     const cudaError_t err = attend_work((int)c.type, a, &need);

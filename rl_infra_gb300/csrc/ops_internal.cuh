@@ -101,6 +101,8 @@ struct AttendArgs {
     unsigned batch, nodes, q_heads;
     float c2;                   // scale log2(e)
     int qvec, ovec;             // queries, outputs move in 16-byte pieces (outputs eight entries at a time)
+    unsigned wait_ms;           // limit of a wait
+    unsigned withhold;          // the barrier, from 1, that expects an arrival more than come (0: none)
 };
 
 struct KeepArgs {

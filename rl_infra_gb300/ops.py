@@ -38,7 +38,7 @@ _VERIFY = struct.Struct("@4I6q2I")
 _SCAN = struct.Struct("@Q4I14qQ2I")
 # per_append_shape, per_attend_shape and per_keep_shape, each with a per_cache in front
 _APPEND = struct.Struct("@6I7q4I13q2I")
-_ATTEND = struct.Struct("@6I7q3If8qQ")
+_ATTEND = struct.Struct("@6I7q3If8qQ2I")
 _KEEP = struct.Struct("@6I7q4Iq")
 assert _DISTILL.size == ctypes.sizeof(capi.per_distill_shape)
 assert _VERIFY.size == ctypes.sizeof(capi.per_verify_shape)
@@ -589,7 +589,7 @@ def tree_attention(q, k_cache, v_cache, block_table, lens, mask=None, counts=Non
             raise _bad("lse", "contiguous", got["lse"])
     lib = _library()
     shape = (*head, b, n, hq, dim ** -0.5 if scale is None else scale, *q.stride()[:3], *got["out"].stride()[:3], *sm)
-    packed = _ATTEND.pack(*shape, 0)
+    packed = _ATTEND.pack(*shape, 0, 0, 0)
     if work is None:
         key = (packed, kp & 15, vp & 15, dev)       # all that the size depends on
         size = _WORK.get(key)
@@ -604,7 +604,7 @@ def tree_attention(q, k_cache, v_cache, block_table, lens, mask=None, counts=Non
         raise _bad("work", f"contiguous, of dtype uint8, on cuda:{dev}", work)
     wp = None
     if work is not None:
-        packed, wp = _ATTEND.pack(*shape, work.numel()), work.data_ptr()
+        packed, wp = _ATTEND.pack(*shape, work.numel(), 0, 0), work.data_ptr()
     _check(lib.per_tree_attention(
         packed, q.data_ptr(), kp, vp, tp, lp, np_, mp, got["out"].data_ptr(), got["lse"].data_ptr(), wp,
         _status_ptr(status, dev), _raw_stream(dev)), "tree_attention")
@@ -624,7 +624,7 @@ def tree_attention_work(q, k_cache, v_cache, block_table, scale=None):
     head, kp, vp, _ = _cache(k_cache, v_cache, block_table, b, dev, code)
     with torch.cuda.device(dev):
         return _work_bytes(_library(), _ATTEND.pack(*head, b, n, hq, dim ** -0.5 if scale is None else scale, *_NO_STRIDES,
-                                                    *_NO_STRIDES, *_NO_STRIDE, 0), kp, vp)
+                                                    *_NO_STRIDES, *_NO_STRIDE, 0, 0, 0), kp, vp)
 
 
 def cache_keep(k_cache, v_cache, block_table, lens, path, kept, nodes=None, status=None, stream=None):

@@ -188,3 +188,11 @@ def test_keep_against_a_list():
     got = co.keep(kc, kc, table, [4], path, [4])
     moved = line[:4] + [line[4 + x] for x in path[0]] + line[8:]
     assert [got["k"][table[0, s // 3], s % 3, 0, 0] for s in range(12)] == moved and not got["flag"]
+
+
+@pytest.mark.parametrize("kw, said", [(dict(wait_limit_ms=10001), "wait_limit_ms"), (dict(withhold=9), "withhold")])
+def test_attention_refuses_limits(kw, said):
+    assert _attend({}, {}, **kw) == capi.PER_ERR_INVALID_ARG
+    assert said in capi.per_last_op_error()
+    s = capi.per_attend_shape(cache=_cache(), batch=2, nodes=3, q_heads=4, scale=1.0, **kw)
+    assert capi.per_tree_attention_work(ctypes.byref(s), None, None)[0] == capi.PER_ERR_INVALID_ARG
