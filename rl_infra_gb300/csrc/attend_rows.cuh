@@ -35,6 +35,7 @@ struct Tail {
     unsigned bad[ST][KT / 32];
     alignas(8) float ml[ML][2];   // maxima and sums that the warps hand over
     alignas(16) int boxes[2][KT];
+    unsigned asked[2];         // tiles that the warps have asked for in all
     unsigned dead[2], odd;     // whether a wait gave up, and their limit; odd: the number of the last tile that something was taken out of
 };
 
@@ -151,12 +152,7 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                 if (tile + 1 < w.tile1) load.look_up(a, w.b, w.s, tile + 1);
             }
         }
-        if (!ok) {          // given up: the copies under way must land before the CTA ends
-            for (unsigned i = asked > (unsigned)ST ? asked - ST : 0; i < asked; ++i) {
-                unsigned none[2] = {0, a.wait_ms};
-                bar_wait(mine + 8 * (i % ST), i / ST & 1, none);
-            }
-        }
+        if (lane == 0) tail.asked[val] = asked;
     } else {
         const unsigned g = lane >> 2, q4 = lane & 3u;                // row and column pair of a fragment
         const unsigned wr = warp / WK, wk = warp - wr * WK, key0 = wk * KW;
@@ -378,7 +374,17 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
         }
         if (!ok && lane == 0 && a.c.status) atomicOr(a.c.status, PER_DEVFLAG_TIMEOUT);
     }
-    __syncthreads();   // nobody leaves before the copies have landed
+    __syncthreads();
+    if (tail.dead[0]) {   // a wait gave up, be it the last one: nobody leaves before the copies under way have landed
+        if (warp >= kWarps) {
+            const unsigned asked = tail.asked[warp - kWarps], mine = full + (warp - kWarps) * 8 * ST;
+            for (unsigned i = asked > (unsigned)ST ? asked - ST : 0; i < asked; ++i) {
+                unsigned none[2] = {0, a.wait_ms};
+                bar_wait(mine + 8 * (i % ST), i / ST & 1, none);
+            }
+        }
+        __syncthreads();
+    }
     if constexpr (WK > 1) {
         if (share > 1) {   // each CTA joins a part of the rows from all of them
             cluster_sync_all();

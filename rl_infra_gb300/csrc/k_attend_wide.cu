@@ -50,6 +50,7 @@ struct Tail {
     unsigned bad[10][4];
     alignas(16) int boxes[2][KT];
     float ml[PAIR ? 1 : 256][2];   // maxima and sums, where both groups have the same rows
+    unsigned asked[2];             // the numbers of the next tiles that the warps would have asked for
     unsigned dead[2], odd, tmem;   // whether a wait gave up, and their limit
 };
 
@@ -263,12 +264,7 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                 if (tile + 1 < w.tile1) load.look_up(a, w.b, w.s, tile + 1);
             }
         }
-        if (!ok) {             // given up: the copies under way must land before the CTA ends
-            for (unsigned i = asked > (unsigned)ST + 1 ? asked - ST / 2 * 2 : val; i < asked; i += 2) {
-                unsigned none[2] = {0, a.wait_ms};
-                bar_wait(full + 8 * (i % ST), i / ST & 1, none);
-            }
-        }
+        if (lane == 0) tail.asked[val] = asked;
     } else if (warp == 9) {    // the thread that issues the products
         if (chosen()) {
             const unsigned ksteps = (dim + 15) / 16, q_at = smem_u32(qs);
@@ -548,7 +544,17 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
         }
     }
     fence_before();
-    __syncthreads();             // nobody leaves before copies and products are done
+    __syncthreads();
+    if (tail.dead[0]) {          // a wait gave up, be it the last one: nobody leaves before the copies under way have landed
+        if (warp == 8 || warp == 10) {
+            const unsigned val = warp == 10, asked = tail.asked[val];
+            for (unsigned i = asked > (unsigned)ST + 1 ? asked - (ST + 1) / 2 * 2 : val; i < asked; i += 2) {
+                unsigned none[2] = {0, a.wait_ms};
+                bar_wait(full + 8 * (i % ST), i / ST & 1, none);
+            }
+        }
+        __syncthreads();
+    }
     if (warp == 9) {
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kColumns));
