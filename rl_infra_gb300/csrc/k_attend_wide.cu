@@ -308,12 +308,6 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                 base += 2 * tiles;
                 ++stretch;
             }
-            if (!ok) {         // given up: nothing may run on when tensor memory is freed
-                unsigned none[2] = {0, a.wait_ms};
-                commit(smem_u32(&tail.last));
-                bar_wait(smem_u32(&tail.last), 0, none);
-                if (a.c.status) atomicOr(a.c.status, PER_DEVFLAG_TIMEOUT);
-            }
         }
         __syncwarp();
     } else {                   // the softmax: a thread a row
@@ -545,7 +539,14 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
     }
     fence_before();
     __syncthreads();
-    if (tail.dead[0]) {          // a wait gave up, be it the last one: nobody leaves before the copies under way have landed
+    if (tail.dead[0]) {          // a wait gave up, be it the last one: nobody leaves, and tensor memory stays, before the copies
+        if (t == 0 && a.c.status) atomicOr(a.c.status, PER_DEVFLAG_TIMEOUT);   // and products under way are done
+        if (warp == 9 && chosen()) {   // the thread that issued them
+            unsigned none[2] = {0, a.wait_ms};
+            commit(smem_u32(&tail.last));
+            bar_wait(smem_u32(&tail.last), 0, none);
+        }
+        __syncwarp();
         if (warp == 8 || warp == 10) {
             const unsigned val = warp == 10, asked = tail.asked[val];
             for (unsigned i = asked > (unsigned)ST + 1 ? asked - (ST + 1) / 2 * 2 : val; i < asked; i += 2) {

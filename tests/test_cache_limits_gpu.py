@@ -85,3 +85,20 @@ def test_few_rows_release(kind, n, g):
 
 def test_any_layout_has_no_waits():
     runs_out("bf16", 1, 3, 2, 2, 33, 7, 500, KEYS, ends=False)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("withhold", [KEYS, VALUES, MEET, QUERIES, SCORES, P, OUTPUTS])
+@pytest.mark.parametrize("b, n, hkv, g, d, page, ctx", [
+    (1, 40, 1, 1, 64, 16, 60),             # one tile
+    (2, 20, 2, 4, 64, 16, 700), (40, 20, 2, 4, 128, 16, 3000),      # rows that both groups share
+    (2, 40, 1, 6, 128, 64, 500), (24, 40, 2, 4, 64, 16, 3000),      # rows of each group's own
+])
+def test_many_rows(kind, withhold, b, n, hkv, g, d, page, ctx):
+    runs_out(kind, b, n, hkv, g, d, page, ctx, withhold)
+
+
+@pytest.mark.parametrize("n, g, d", [(20, 4, 128), (40, 4, 128), (40, 4, 64)])
+def test_many_rows_release(n, g, d):
+    runs_out("bf16", 40, n, 2, g, d, 16, 3000, RELEASE)
+    runs_out("bf16", 1, n, 2, g, d, 16, 40, RELEASE, ends=False)
