@@ -112,7 +112,7 @@ struct TokenInfo {
 template <typename T, int N>
 __global__ void __launch_bounds__(kThreads) k_append(AppendArgs a, AppendPlan p)
 {
-    extern __shared__ char smem_raw[];
+    extern __shared__ __align__(16) unsigned char smem_raw[];
     TokenInfo *info = reinterpret_cast<TokenInfo *>(smem_raw);
     float2 *turn = reinterpret_cast<float2 *>(info + p.group);   // [group][rot / 2]
     const unsigned t = threadIdx.x, half = a.rot / 2;
@@ -280,7 +280,7 @@ struct Move {
 template <typename T, int N>
 __global__ void __launch_bounds__(kThreads) k_keep(KeepArgs a, unsigned splits, unsigned columns, FastDiv by_head)
 {
-    extern __shared__ char smem_raw[];
+    extern __shared__ __align__(16) unsigned char smem_raw[];
     Move *move = reinterpret_cast<Move *>(smem_raw);
     __shared__ unsigned ends;      // the first entry that is not moved
     const unsigned t = threadIdx.x, b = blockIdx.x / splits, part = blockIdx.x - b * splits;

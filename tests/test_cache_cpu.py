@@ -196,3 +196,16 @@ def test_attention_refuses_limits(kw, said):
     assert said in capi.per_last_op_error()
     s = capi.per_attend_shape(cache=_cache(), batch=2, nodes=3, q_heads=4, scale=1.0, **kw)
     assert capi.per_tree_attention_work(ctypes.byref(s), None, None)[0] == capi.PER_ERR_INVALID_ARG
+
+
+def test_shared_memory_that_is_cast_asks_for_its_alignment():
+    """Dynamic shared memory of bytes lies where the compiler likes unless it asks: what casts it to wider words must."""
+    import re
+    from pathlib import Path
+    seen = 0
+    for f in sorted(Path(build.CSRC).glob("*.cu*")):
+        for line in re.findall(r"extern __shared__.*", f.read_text()):
+            if re.search(r"\bchar\b", line):
+                seen += 1
+                assert re.search(r"__align__\((16|\d{3,4})\)", line), f"{f.name}: {line}"
+    assert seen
