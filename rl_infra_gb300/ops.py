@@ -23,6 +23,7 @@ import ctypes
 import struct
 
 import torch
+from torch.autograd import forward_ad
 
 from . import capi
 from .capi import PerError
@@ -477,11 +478,16 @@ _WORK = {}             # scratch memory by shape and alignment (a number that th
 
 
 def _serving(*tensors):
-    """These operators have no gradient: a tensor that asks for one is refused, not passed as a constant."""
+    """These operators have no gradient: a tensor that asks for one is refused, not passed as a constant (and so is one
+    that carries a tangent, which torch.no_grad() does not take from it)."""
     if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and t.requires_grad:
                 raise RuntimeError("the cache's operators have no gradient: call them under torch.no_grad()")
+    if forward_ad._current_level >= 0:
+        for t in tensors:
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+                raise RuntimeError("the cache's operators have no gradient: unpack dual tensors before them")
 
 
 def _cache(k_cache, v_cache, block_table, batch, dev, code):

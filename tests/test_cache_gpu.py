@@ -573,3 +573,24 @@ def test_refusals():
         ops.tree_attention(q.clone().requires_grad_(), kc, vc, table, lens)
     with torch.no_grad():
         ops.tree_attention(q.clone().requires_grad_(), kc, vc, table, lens)
+
+
+def test_dual_tensors_are_refused():
+    """A tensor with a tangent of forward-mode differentiation does not pass as a constant, under no_grad neither."""
+    import torch.autograd.forward_ad as fw
+    kc = torch.zeros(4, 16, 1, 32, device="cuda")
+    vc, table, lens = kc.clone(), i32([[1, 2]]), i32([3])
+    q, one = torch.ones(1, 2, 1, 32, device="cuda"), torch.ones(1, 2, 1, 32, device="cuda")
+    inv = torch.ones(4, device="cuda")
+    with fw.dual_level():
+        dual = lambda t: fw.make_dual(t, torch.ones_like(t))
+        for call in (lambda: ops.tree_attention(dual(q), kc, vc, table, lens), lambda: ops.tree_attention(q, kc, dual(vc), table, lens),
+                     lambda: ops.cache_append(dual(one), one, kc, vc, table, lens), lambda: ops.cache_append(one, one, kc, vc, table, lens, q=dual(q)),
+                     lambda: ops.cache_append(one, one, kc, vc, table, lens, inv_freq=dual(inv)),
+                     lambda: ops.cache_keep(dual(kc), vc, table, lens, i32([[0]]), i32([1]))):
+            for grad in (True, False):
+                with torch.set_grad_enabled(grad), pytest.raises(RuntimeError, match="no gradient"):
+                    call()
+        assert (ops.tree_attention(q, kc, vc, table, lens)["out"] == 0).all()
+    assert (kc == 0).all()
+    ops.tree_attention(q, kc, vc, table, lens)
