@@ -580,7 +580,7 @@ typedef struct {
  * is the step of plain decoding.  Products of 16-bit types are summed in binary32, scores and their
  * sums are binary32, and p is rounded once to the type before its product with v (the sum of p is
  * not; as float16, a p below 2^-25 of its row's largest is off by up to 2^-36 of that).  binary32 entries are
- * taken as two parts whose products give 21 bits (an infinite entry then gives NaN).  Out is rounded once.
+ * taken as two parts whose products give 21 bits.  Out is rounded once.
  * Scores may be as large as binary32 holds (times log2(e)); what is past that is infinite.
  *   d_q, d_out [B x N x Hq x D] (not the same memory), d_mask [B x N x N] bytes, d_lens, d_counts [B] int32 (counts NULL: N),
  *   d_table [B x width] int32, d_lse [B x N x Hq] float (contiguous) or NULL, d_work: work_bytes of scratch

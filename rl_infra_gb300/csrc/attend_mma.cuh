@@ -221,6 +221,36 @@ __device__ __forceinline__ void hide(float (*sc)[4], const AttendArgs &a, unsign
         }
 }
 
+// binary32 scores of keys that are seen and came out NaN, once more in plain sums: an infinite entry has no two parts (its rest
+// is inf - inf), and its score may well be -inf.  row: of the rows that share a head of keys, the thread's first (rare: nothing
+// here is fast).
+template <int KW>
+__device__ __forceinline__ void once_more(float (*sc)[4], const AttendArgs &a, unsigned b, unsigned h, unsigned group, const int *node,
+                                          unsigned row, const unsigned char *ks, unsigned kt, unsigned key0)
+{
+    float all = 0.0f;
+#pragma unroll
+    for (int i = 0; i < KW / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) all += sc[i][e];
+    if (!__any_sync(0xffffffffu, all != all)) return;
+    const unsigned q4 = threadIdx.x & 3u;
+#pragma unroll
+    for (int i = 0; i < KW / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int n = node[e >> 1];
+            if (sc[i][e] == sc[i][e] || n < 0) continue;
+            const unsigned r = key0 + i * 8 + q4 * 2 + (e & 1), head = (h - (unsigned)n) * group + row + (e >> 1) * 8;
+            const float *q = static_cast<const float *>(a.q) + b * a.sq[0] + n * a.sq[1] + head * a.sq[2];
+            float s = 0.0f;
+#pragma unroll 1
+            for (unsigned d = 0; d < a.c.dim; ++d)
+                s = fmaf(q[d], *reinterpret_cast<const float *>(ks + piece(kt, r, d >> 2) + (d & 3u) * 4), s);
+            sc[i][e] = s * a.c2;
+        }
+}
+
 // What a row's p and sum refer to, for its maximum so far (in log2).  p goes into a product as T: a float16 holds 11 bits down
 // to 2^-14 and nothing below 2^-25, so that under one key far above the others theirs would be lost from the product, though
 // not from the sum (8000 keys 18 nats below one whose value is 0: 0.5% off).  Referred to 2^-15 of the maximum, p uses the

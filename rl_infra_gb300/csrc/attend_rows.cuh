@@ -251,6 +251,7 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                     hide<KW>(sc, a, b, s, node, tile * KT, key0, [&](unsigned r) {
                         return !wrong || !((tail.bad[st][r >> shift >> 5] >> (r >> shift & 31u)) & 1u);
                     });
+                if constexpr (ES == 4) once_more<KW>(sc, a, b, h, group, node, row0 + wr * 16 + g, ks, KT, key0);
                 soften<T, DP, KW>(sc, top, sum, o);
                 if (!tail_in && !(ok = __all_sync(0xffffffffu, bar_wait(full + 8 * (ST + st), phase, dead)))) break;
                 values<T, DP, KW>(o, sc, vs, KT, key0, halves);

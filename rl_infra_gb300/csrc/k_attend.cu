@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_any(AttendArgs a, unsigned 
                 for (int e = 0; e < 4; ++e) sc[i][e] *= a.c2;
             if (masked)
                 hide<KT>(sc, a, b, s, node, tile * KT, 0, [&](unsigned r) { return ((r < 32 ? there0 : there1) >> (r & 31u) & 1u) != 0; });
+            if constexpr (ES == 4) once_more<KT>(sc, a, b, h, group, node, row0 + warp * 16 + g, ks, KT, 0);
             soften<T, DP, KT>(sc, top, sum, o);
             values<T, DP, KT>(o, sc, vs, KT, 0, halves);
             if (odd)

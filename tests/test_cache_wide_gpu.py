@@ -13,7 +13,7 @@ if not torch.cuda.is_available():  # pragma: no cover
 
 from rl_infra_gb300 import build, capi, ops  # noqa: E402
 from tests import cache_oracle as co  # noqa: E402
-from tests.ops_oracle import TINY  # noqa: E402
+from tests.ops_oracle import TINY, close  # noqa: E402
 from tests.test_cache_gpu import INF, NAN, TYPES, attend_case, cache, check_attend, fill, host, i32, rand, tree  # noqa: E402
 
 
@@ -349,3 +349,47 @@ def test_scores_far_from_zero(kind, n, g, d, far, ctx):
     err = np.abs(host(got["out"]) - want) / want
     assert (err <= 2 * half + 2.0 ** -12 + joins).all(), err.max()
     np.testing.assert_allclose(host(got["lse"]), far * 2.0 ** 23 + np.log(p.sum()) + line(j).max(), atol=2)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("n, g, d, page", [(1, 4, 64, 16), (2, 3, 128, 16), (7, 2, 96, 8), (9, 2, 256, 16), (20, 2, 80, 16), (12, 8, 128, 16),
+                                           (5, 2, 33, 7), (40, 2, 130, 3)])
+def test_infinite_entries(kind, n, g, d, page):
+    """Keys with infinite entries score -inf, inf or NaN by their signs and the query's, in every type; so do queries with
+    infinite entries.  Where nothing scores inf or NaN, a row gives what the other keys give."""
+    r = np.random.default_rng(48)
+    ctx = 300
+    kc, vc, table = cache(r, 1, ctx + n, page, 1, d, kind)
+    fill(r, kc, vc, table, [ctx + n], kind)
+    tab = table.cpu().numpy()
+    q = rand(r, 1, n, g, d, kind=kind)
+    q[..., :3] = q[..., :3].abs() + 0.01
+    q[0, n - 1, 0, 1] = -1.0                   # this row scores inf somewhere
+    gone = [0, 5, 6, 77, 130, 131, 200, ctx - 1, ctx]      # the last is node 0's
+    for s in gone:
+        kc[co.place(tab[0], s, page, kc.shape[0])][..., 1] = -INF
+    kc[co.place(tab[0], 6, page, kc.shape[0])][..., 2] = -INF
+    kc[co.place(tab[0], 200, page, kc.shape[0])][..., 0] = -INF
+    got = {name: host(t) for name, t in ops.tree_attention(q, kc, vc, table, i32([ctx])).items()}
+    assert np.isnan(got["out"][0, n - 1, 0]).all() and np.isnan(got["lse"][0, n - 1, 0])
+    # the same without those keys: pages of one slot, and node 0 seen by nobody
+    left = np.setdiff1d(np.arange(ctx + n), gone[:-1])
+    line = [host(t[table[0].long()]).reshape(-1, 1, 1, d)[left] for t in (kc, vc)]
+    line[0][~np.isfinite(line[0])] = 0
+    mask = np.tri(n, dtype=bool)
+    mask[:, 0] = False
+    qs = host(q)
+    qs[0, n - 1, 0] = 0
+    want = co.attend(qs, *line, np.arange(len(left))[None], [ctx - len(gone) + 1], mask, kind=kind)
+    for name in ("out", "lse"):
+        got[name][0, n - 1, 0] = want[name][0, n - 1, 0]
+    close(got["out"], want["out"], want["bout"], kind)
+    close(got["lse"], want["lse"], want["blse"])
+    # an infinite query: every score of its row is inf, -inf or NaN
+    fill(r, kc, vc, table, [ctx + n], kind)
+    q = rand(r, 1, n, g, d, kind=kind).abs()
+    kc.abs_().neg_()
+    q[0, 0, 0, 0] = INF
+    got = ops.tree_attention(q, kc, vc, table, i32([ctx]))
+    assert (got["out"][0, 0, 0] == 0).all() and got["lse"][0, 0, 0] == -INF
+    assert torch.isfinite(got["out"]).all() and torch.isfinite(got["lse"].flatten()[1:]).all()
