@@ -506,7 +506,9 @@ per_status per_scan_backward(const per_scan_shape *shape, const void *d_a, const
  * context; a call's new tokens (the nodes of a tree, each one token) take the slots behind it in their order.
  * Nothing beyond a sequence's own slots is read into a result: what stale slots hold, NaN too, does not
  * matter.  A table entry outside [0, P), a slot behind the table's end, a negative start and a count that
- * is out of range set PER_DEVFLAG_BAD_INDEX; what they name is left out (not written, not attended to).
+ * is out of range set PER_DEVFLAG_BAD_INDEX; what they name is left out (not written, not attended to; a negative d_lens
+ * counts as no context in per_tree_attention).  What is written to, keys and values, must not overlap (one and the same
+ * memory is refused; attention may read both from one).
  * ------------------------------------------------------------------------------------------- */
 
 typedef struct {

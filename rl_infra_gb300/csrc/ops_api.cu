@@ -410,6 +410,7 @@ per_status per_cache_append(const per_append_shape *shape, const void *d_k, cons
     if (sh->q_heads && d_q == d_q_out)
         for (int i = 0; i < 3; ++i)
             if (sh->stride_q[i] != sh->stride_q_out[i]) return refuse(where, "q_out in the place of q needs its strides");
+    if (c.pages && d_k_cache == d_v_cache) return refuse(where, "keys and values in the same memory");
     AppendArgs a{};
     a.c = cache_args(c, d_k_cache, d_v_cache, d_table, d_status);
     a.k = d_k;
@@ -531,6 +532,7 @@ per_status per_cache_keep(const per_keep_shape *shape, void *d_k_cache, void *d_
         return refuse(where, "misaligned pointer");
     if (overlaps3(c.stride_k, c.pages, c.page, c.heads, c.dim) || overlaps3(c.stride_v, c.pages, c.page, c.heads, c.dim))
         return refuse(where, "rows of a cache overlap");
+    if (c.pages && d_k_cache == d_v_cache) return refuse(where, "keys and values in the same memory");
     KeepArgs a{};
     a.c = cache_args(c, d_k_cache, d_v_cache, d_table, d_status);
     a.lens = d_lens;

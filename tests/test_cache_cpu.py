@@ -209,3 +209,10 @@ def test_shared_memory_that_is_cast_asks_for_its_alignment():
                 seen += 1
                 assert re.search(r"__align__\((16|\d{3,4})\)", line), f"{f.name}: {line}"
     assert seen
+
+
+def test_one_memory_for_keys_and_values_is_refused():
+    """append and keep write both, from different threads; attention reads them and may have one for both."""
+    for call, name in ((_append, "per_cache_append"), (_keep, "per_cache_keep")):
+        assert call() == capi.PER_ERR_INVALID_ARG
+        assert "same memory" in capi.per_last_op_error() and capi.per_last_op_error().startswith(name)
