@@ -581,7 +581,8 @@ typedef struct {
  * i >= m.  What a node does not see takes no part, whatever it holds (infinities and NaN too).  N = 1
  * is the step of plain decoding.  Products of 16-bit types are summed in binary32, scores and their
  * sums are binary32, and p is rounded once to the type before its product with v (the sum of p is
- * not; as float16, a p below 2^-25 of its row's largest is off by up to 2^-36 of that).  binary32 entries are
+ * not; as float16, a p below 2^-25 of its row's largest is off by up to 2^-36 of that), or, with up to 16 rows (nodes times
+ * query heads) to a head of keys on 16-byte boundaries, taken in two rounded parts.  binary32 entries are
  * taken as two parts whose products give 21 bits.  Out is rounded once.
  * Scores may be as large as binary32 holds (times log2(e)); what is past that is infinite.
  *   d_q, d_out [B x N x Hq x D] (not the same memory), d_mask [B x N x N] bytes, d_lens, d_counts [B] int32 (counts NULL: N),

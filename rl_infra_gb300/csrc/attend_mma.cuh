@@ -128,9 +128,12 @@ __device__ __forceinline__ void scores(float (*sc)[4], const unsigned char *qs, 
     }
 }
 
-// o += p v for the same rows and keys (p where the scores were).  binary32: key 2 c is column c of the instruction,
+// o += p v for the same rows and keys (p where the scores were).  TWO: 16-bit p in two parts, itself rounded and the rest rounded,
+// so that what is lost of it is 2^-16 (float16 2^-22) and not a half step of the type.  Taken where it costs nothing, with one
+// fragment of rows (64 sequences of up to 5000, one token, 153 us with it and without; one token over 1023 9.3 and 9.1); with
+// two, the products no longer hide behind the copies (262145 tokens, 32 rows a head: 178 us and 171).  binary32: key 2 c is column c of the instruction,
 // 2 c + 1 column c + 4: the scores lie so already.
-template <typename T, int DP, int KW>
+template <typename T, int DP, int KW, bool TWO>
 __device__ __forceinline__ void values(float (*o)[4], const float (*p)[4], const unsigned char *vs, unsigned kt, unsigned key0,
                                        unsigned halves)
 {
@@ -140,11 +143,23 @@ __device__ __forceinline__ void values(float (*o)[4], const float (*p)[4], const
         for (int k = 0; k < KW / 16; ++k) {
             const unsigned pa[4] = {pack2<T>(p[2 * k][0], p[2 * k][1]), pack2<T>(p[2 * k][2], p[2 * k][3]),
                                     pack2<T>(p[2 * k + 1][0], p[2 * k + 1][1]), pack2<T>(p[2 * k + 1][2], p[2 * k + 1][3])};
+            unsigned pl[4];       // what is left of p
+            if constexpr (TWO) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 hi = unpack2<T>(pa[j]);
+                    pl[j] = pack2<T>(p[2 * k + (j >> 1)][(j & 1) * 2] - hi.x, p[2 * k + (j >> 1)][(j & 1) * 2 + 1] - hi.y);
+                }
+            }
 #pragma unroll
             for (int i = 0; i < DP / 16; ++i) {
                 if (i % 4 == 0 && i / 4 >= (int)halves) break;
                 unsigned vb[4];   // keys 0-7 and 8-15 of entries 0-7, then of entries 8-15
                 ldsm4t(vb, smem_u32(vs + piece(kt, key0 + k * 16 + (lane & 15u), i * 2 + (lane >> 4))));
+                if constexpr (TWO) {
+                    mma16<T>(o[2 * i], pl, vb[0], vb[1]);
+                    mma16<T>(o[2 * i + 1], pl, vb[2], vb[3]);
+                }
                 mma16<T>(o[2 * i], pa, vb[0], vb[1]);
                 mma16<T>(o[2 * i + 1], pa, vb[2], vb[3]);
             }

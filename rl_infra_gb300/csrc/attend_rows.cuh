@@ -254,7 +254,7 @@ k_attend_rows(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
                 if constexpr (ES == 4) once_more<KW>(sc, a, b, h, group, node, row0 + wr * 16 + g, ks, KT, key0);
                 soften<T, DP, KW>(sc, top, sum, o);
                 if (!tail_in && !(ok = __all_sync(0xffffffffu, bar_wait(full + 8 * (ST + st), phase, dead)))) break;
-                values<T, DP, KW>(o, sc, vs, KT, key0, halves);
+                values<T, DP, KW, WR == 1>(o, sc, vs, KT, key0, halves);
                 if (odd)
                     for (unsigned r = key0; r < key0 + KW; ++r) {
                         const unsigned key = tile * KT + r, box = r >> shift;

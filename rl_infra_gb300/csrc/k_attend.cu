@@ -4,7 +4,8 @@
 // Mathematics.  A pass over the keys with the running maximum m and sum l of a softmax: for each tile,
 // s = scale q k, m' = max(m, max s), p = 2^(s - m'), l = l 2^(m - m') + sum p, o = o 2^(m - m') + p v (scores in units of
 // log2).  Parts of a sequence join the same way.  Scores, sums and outputs are binary32; p is rounded
-// to the type of v for the matrix instruction, whose products are exact.  binary32 operands are split into two parts of
+// to the type of v for the matrix instruction, whose products are exact (where few rows share a head of keys, taken in two
+// parts: `values` in attend_mma.cuh).  binary32 operands are split into two parts of
 // 11 bits, and the product of the two lower parts is dropped.
 //
 // The kernel here takes any strides and alignment: 64 rows a CTA, 16 a warp, entries copied one by one.
@@ -153,7 +154,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_any(AttendArgs a, unsigned 
                 hide<KT>(sc, a, b, s, node, tile * KT, 0, [&](unsigned r) { return ((r < 32 ? there0 : there1) >> (r & 31u) & 1u) != 0; });
             if constexpr (ES == 4) once_more<KT>(sc, a, b, h, group, node, row0 + warp * 16 + g, ks, KT, 0);
             soften<T, DP, KT>(sc, top, sum, o);
-            values<T, DP, KT>(o, sc, vs, KT, 0, halves);
+            values<T, DP, KT, false>(o, sc, vs, KT, 0, halves);
             if (odd)
                 for (unsigned r = 0; r < KT; ++r) {
                     const unsigned key = tile * KT + r;

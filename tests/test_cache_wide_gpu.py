@@ -393,3 +393,19 @@ def test_infinite_entries(kind, n, g, d, page):
     got = ops.tree_attention(q, kc, vc, table, i32([ctx]))
     assert (got["out"][0, 0, 0] == 0).all() and got["lse"][0, 0, 0] == -INF
     assert torch.isfinite(got["out"]).all() and torch.isfinite(got["lse"].flatten()[1:]).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("b, n, g, d, page, ctx", [(3, 1, 4, 128, 16, 1000), (1, 4, 4, 64, 16, 9000), (2, 3, 1, 256, 8, 700), (1, 16, 1, 40, 16, 130)])
+def test_few_rows_keep_p_in_two_parts(kind, b, n, g, d, page, ctx):
+    """Up to 16 rows: out is off by its own rounding, binary32's and what two roundings leave of p (half a step squared)."""
+    r = np.random.default_rng(49)
+    kc, vc, table = cache(r, b, ctx + n, page, 2, d, kind)
+    fill(r, kc, vc, table, [ctx + n] * b, kind)
+    q, lens = rand(r, b, n, 2 * g, d, kind=kind), np.full(b, ctx)
+    got = ops.tree_attention(q, kc, vc, table, i32(lens))
+    args = host(q), host(kc)
+    tab = table.cpu().numpy()
+    want = co.attend(*args, host(vc), tab, lens, kind="f32")
+    size = co.attend(*args, np.abs(host(vc)), tab, lens, kind="f32")["out"]
+    close(host(got["out"]), want["out"], want["bout"] + size * (torch.finfo(TYPES[kind]).eps / 2) ** 2, kind)
