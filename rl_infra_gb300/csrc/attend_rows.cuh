@@ -7,11 +7,12 @@
 // stretch.  Tiles of 32 KB (64 KB of large heads) lie in a ring of barriers: a warp that is done with one
 // never waits for the others, and the copies of the next stretch begin while this one is joined.
 //
-// Measured (GB300): 64 sequences of up to 5000 tokens, 32 query heads on 8 of 128 entries, bf16, pages of 16 150 us,
-// 6.15 TB/s (92% of the copy rate); one of 262145 tokens, 8 nodes, 32 rows a head 176 us (91%); one token over 1023
-// 9.3 us.  binary32 is bound by its products, three for one at half the rate: 5 trees of 13 nodes, up to 3001 tokens,
-// 12 heads of 80 entries 60 us (23%).  Pages that hold no 16 slots in a row come as smaller boxes, of which the copy
-// engine takes one in about 64 cycles.
+// Measured (GB300): 64 sequences of up to 5000 tokens, 32 query heads on 8 of 128 entries, bf16, pages of 16 151 us,
+// 6.12 TB/s (92% of the copy rate); one of 262145 tokens, 8 nodes, 32 rows a head 176 us (91%); one token over 1023
+// 9.3 us.  binary32: 5 trees of 13 nodes, up to 3001 tokens, 12 heads of 80 entries 49 us (29%), the first ones decoding 491 us
+// (60%).  Its products, three for one, are not the limit (42 TFLOP/s of them in the former): a warp has 8 keys of a tile, so
+// that operands are read from shared memory for three products at a time, in one short chain.  Pages that hold no 16
+// slots in a row come as smaller boxes, of which the copy engine takes one in about 64 cycles.
 #pragma once
 
 #include "attend_mma.cuh"

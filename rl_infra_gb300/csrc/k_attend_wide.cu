@@ -14,14 +14,15 @@
 // scaled, which is rare.  So p is worked out in one pass over the scores, which also finds their maximum; where that
 // has risen, the pass is made again.
 //
-// Measured (GB300): 32 trees of 64 nodes, 64 query heads on 8, up to 6000 tokens, bf16 294 us, 901 TFLOP/s (a chain of
+// Measured (GB300): 32 trees of 64 nodes, 64 query heads on 8, up to 6000 tokens, bf16 288 us, 920 TFLOP/s (a chain of
 // the softmax, 1250 cycles a tile of 128 x 128, and two products of 512 each, while the other group does the same; the
 // tensor cores are busy half of the time); 16 trees of 24 nodes, 96 rows a head of 64 entries, up to 8000 tokens, f16 57 us,
 // 3.36 TB/s.  With the warp-wide instruction 1611 and 236 us.
 //
 // What was tried and not kept: registers dealt anew between the warps (setmaxnreg; the compiler then spilled 2.4 KB a
 // thread: 2309 us); outputs by way of shared memory, mask bytes asked for without branches, a warp without rows that skips
-// its softmax (297 to 312 us against 286 each: the loop's registers are full, and it spills).
+// its softmax (297 to 312 us of GPU time, at 286 without each: the loop's registers are full, and it spills); a second way
+// through the loop for scores past kFar, as a call or in place (304 and 317 us, at 284 without).
 #include "attend_mma.cuh"
 
 #include <algorithm>

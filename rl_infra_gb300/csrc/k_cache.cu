@@ -12,11 +12,12 @@
 // angle to 2^-64 pos, in integers: no binary64, of which an SM retires a warp's instruction in 16 cycles.
 //
 // Measured (GB300): four prompts of 8191 tokens, 32 + 8 + 8 heads of 128 entries, bf16 117 us, 6.0 TB/s (90% of the copy
-// rate); 64 trees of 24 nodes, f16 10.3 us; one token 3.0 us.
+// rate); 64 trees of 24 nodes, f16 12.7 us from HBM, 10.3 from L2 (floor 5.3: the heads are asked for only when places and
+// angles stand); one token 3.0 us.
 //
 // Keep.  A thread owns 16 bytes of a head and moves them along the path.  Since path_j >= j grows, a slot
 // is read before or in the same batch of loads as anything is written to it.  1024 paths of up to 12 nodes, 8 heads of
-// 128 binary32 entries 13.5 us (109 MB); 64 of up to 6, bf16 2.5 us.
+// 128 binary32 entries 19.2 us from HBM (109 MB, 85% of the copy rate; 13.3 us from L2); 64 of up to 6, bf16 2.4 us.
 #include "ops_internal.cuh"
 
 #include <algorithm>
