@@ -584,7 +584,8 @@ typedef struct {
  * not; as float16, a p below 2^-25 of its row's largest is off by up to 2^-36 of that), or, with up to 16 rows (nodes times
  * query heads) to a head of keys on 16-byte boundaries, taken in two rounded parts.  binary32 entries are
  * taken as two parts whose products give 21 bits.  Out is rounded once.
- * Scores may be as large as binary32 holds (times log2(e)); what is past that is infinite.
+ * Scores may be as large as binary32 holds (times log2(e)); what is past that is infinite.  Sums of p v are divided by the sum
+ * of p at the end: they, with p of up to 2^8, must be within binary32 (|v| below 2^120 over the number of keys, say).
  *   d_q, d_out [B x N x Hq x D] (not the same memory), d_mask [B x N x N] bytes, d_lens, d_counts [B] int32 (counts NULL: N),
  *   d_table [B x width] int32, d_lse [B x N x Hq] float (contiguous) or NULL, d_work: work_bytes of scratch
  *   memory (16-byte aligned) that this call alone uses until it has run; per_tree_attention_work says
