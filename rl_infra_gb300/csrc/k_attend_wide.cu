@@ -133,8 +133,9 @@ __device__ __forceinline__ void put32(unsigned at, const unsigned *v)
                  "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::WORDS32(v), "r"(at) : "memory");
 }
 
-// A reference past kFar in log2 cannot stay one: its own rounding would be a power of two or more in p = 2^(s c2 - top) (at
-// 2^31 as much as binary32 holds).  What such a row refers to is taken off its scores themselves, in tensor memory.
+// A reference past kFar in log2 cannot stay one: p = 2^(s c2 - top) carries its rounding, up to a quarter there (what float16's
+// range has room for) and 128 at 2^31, as much as binary32 holds.  What such a row refers to is taken off its scores
+// themselves, in tensor memory.
 constexpr float kFar = 4194304.0f;
 __device__ __forceinline__ void take_off(unsigned my_s, float shift)
 {
@@ -206,7 +207,7 @@ k_attend_wide(const __grid_constant__ CacheMaps maps, AttendArgs a, unsigned row
 
     if (t == 0) {
         for (int i = 0; i < ST; ++i) {
-            bar_init(full + 8 * i, 1 + (a.withhold == (i % 2 ? kValues : kKeys)));   // (of the first round; ST may be odd)
+            bar_init(full + 8 * i, 1 + (a.withhold == (i % 2 ? kValues : kKeys)));   // (of its first turn; ST may be odd)
             bar_init(empty + 8 * i, 1 + (a.withhold == kRelease));
         }
         bar_init(q_ready, kGroups * 4 + (a.withhold == kQueries));
